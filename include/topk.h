@@ -245,7 +245,8 @@ const char* topk_status_str(int status);
  * `unsorted` field at the end of topk_options_t; 0.3.0 (300) added
  * `wait_limit_ns`, `inject_wait_timeout` and `recall` after it, `shortfalls`
  * at the end of topk_stats_t, topk_last_status, topk_autotune and topk_tuning
- * (cost_ratio = 0 meaning "measured").
+ * (cost_ratio = 0 meaning "measured"); 0.4.0 (400) added the operators
+ * around the selection at the end of this header.
  * Fill the struct with topk_options_init from the same version's library. */
 int topk_version(void);
 
@@ -322,6 +323,106 @@ int topk_prof_filter(const void* x, int dtype, int64_t rows, int64_t n, int glob
  */
 int topk_select_noalloc(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int largest,
                         double eps, void* out_vals, int64_t* out_idx, int global, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the selection: what a sparse autoencoder's training step
+ * runs before and after topk_select_global (or topk_select, which keeps k
+ * features a row) -- the encoder, the reconstruction from the selected
+ * activations, their gradients, and the gradient norm with clipping.
+ *
+ *   - All tensors of one call have one dtype (F32 or BF16).  Matrices are
+ *     row-major with unit stride along a row; ld* is the distance between
+ *     rows in elements (at least the row's length).  Outputs without an ld
+ *     are contiguous.  No alignment is needed beyond the element's own (rows
+ *     that start on 16-byte boundaries are read faster).
+ *   - Products, sums, activations and norms are formed in f32 or wider; each
+ *     result is rounded once, to nearest even.  Results do not depend on the
+ *     order in which blocks run: the same call gives the same bits.
+ *   - Outputs marked "nullable" are not computed when null.
+ *   - Extents are below 2^31 (EUNSUPPORTED beyond).  Scratch memory comes from
+ *     a per-(device, stream) block of these operators, grown on demand.
+ * ------------------------------------------------------------------------ */
+
+/* z, max(z, 0), z Phi(z) with the normal distribution function Phi, z / (1 + e^-z). */
+typedef enum { TOPK_ACT_NONE = 0, TOPK_ACT_RELU = 1, TOPK_ACT_GELU = 2, TOPK_ACT_SILU = 3 } topk_act_t;
+
+/*
+ * y = act(x w^T + bias) + residual: x is rows x inner, w is outer x inner, y
+ * rows x outer.  bias (outer values) and residual (rows x outer) are nullable;
+ * residual may be y itself.  pre (nullable): x w^T + bias, kept for
+ * topk_linear_backward.  rows == 0 is a no-op.
+ */
+int topk_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* residual,
+                int64_t ldr, int dtype, int64_t rows, int64_t inner, int64_t outer, int act, void* y, int64_t ldy,
+                void* pre, int64_t ldp, void* stream);
+
+/*
+ * Gradients of topk_linear from dy (rows x outer), with dz = dy act'(pre):
+ * dx = dz w, dw = dz^T x, dbias = the column sums of dz (each nullable; the
+ * residual's gradient is dy itself).  pre is read unless act is NONE; for RELU
+ * the layer's own output serves when it had no residual (the signs agree).
+ * BF16: dz is rounded to BF16 once before the two products (dbias sums it
+ * unrounded).  x is needed for dw only and w for dx only.
+ */
+int topk_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                         const void* pre, int64_t ldp, int dtype, int64_t rows, int64_t inner, int64_t outer, int act,
+                         void* dx, void* dw, void* dbias, void* stream);
+
+/*
+ * A selection's places, as the entry points below take them: `idx` as
+ * topk_select_global writes it (per_row == 0: `count` flat positions r*n + c)
+ * or as topk_select does (per_row != 0: `count` row-local positions for each
+ * row), in any order.  A position out of range (the -1 of a relaxed recall's
+ * shortfall) holds no place: it adds nothing, and its gradient is 0.  A place
+ * listed twice counts twice.
+ */
+
+/*
+ * Gradients of topk_linear when only selected outputs carry one: dvals[s] at
+ * place s, vals[s] the selected output.  With dz_s = dvals[s] act'(vals[s])
+ * (act NONE or RELU): dx[r] = sum of dz_s w[c_s] over the places of row r
+ * (rows x inner), dw[c] = sum of dz_s x[r_s] over those of column c (outer x
+ * inner), dbias[c] = sum of dz_s; each nullable.
+ */
+int topk_linear_backward_selected(const void* dvals, const void* vals, const int64_t* idx, int64_t count, int per_row,
+                                  const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype, int64_t rows,
+                                  int64_t inner, int64_t outer, int act, void* dx, void* dw, void* dbias, void* stream);
+
+/*
+ * Reconstruction from a selection out of rows x n activations: y[r] = bias +
+ * the sum of vals[s] w[c_s] over the places of row r.  w is n x d (one row a
+ * feature), y rows x d; bias (d values) is nullable.
+ */
+int topk_decode(const void* vals, const int64_t* idx, int64_t count, int per_row, const void* w, int64_t ldw,
+                const void* bias, int dtype, int64_t rows, int64_t n, int64_t d, void* y, void* stream);
+
+/*
+ * Gradients of topk_decode from dy (rows x d): dvals[s] = dy[r_s] . w[c_s],
+ * dw[c] = the sum of vals[s] dy[r_s] over the places of column c (n x d, zero
+ * for features that were not selected), dbias = the column sums of dy; each
+ * nullable.
+ */
+int topk_decode_backward(const void* dy, int64_t lddy, const void* vals, const int64_t* idx, int64_t count, int per_row,
+                         const void* w, int64_t ldw, int dtype, int64_t rows, int64_t n, int64_t d, void* dvals,
+                         void* dw, void* dbias, void* stream);
+
+/*
+ * The norm of `num` tensors taken as one vector, *norm = sqrt(sum of squares)
+ * (f32, on the device; any finite input whose norm is below the f32 range's
+ * end gives a finite norm).  grads, counts and dtypes are HOST arrays: device
+ * pointers, elements (0 allowed) and dtypes (which may differ) of each tensor.
+ */
+int topk_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t num, float* norm,
+                   void* stream);
+
+/*
+ * The same norm, and out[i] = grads[i] * min(1, max_norm / (*norm + 1e-6)).
+ * out[i] == grads[i] clips in place; otherwise the two do not overlap.  A norm
+ * that is not finite carries over to the results as the formula says.
+ * EINVAL: max_norm < 0 or NaN.
+ */
+int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* counts, const int* dtypes,
+                        int64_t num, double max_norm, float* norm, void* stream);
 
 #ifdef __cplusplus
 }

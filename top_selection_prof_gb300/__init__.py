@@ -8,6 +8,9 @@ inputs must be CUDA tensors and the library must be built.
     import top_selection_prof_gb300 as tk
     vals, idx = tk.select(x, k)                  # per row, x: (rows, n) or (n,)
     vals, idx = tk.select_global(acts, K)        # BatchTopK: over the flattened tensor
+
+Around the selection, a sparse autoencoder's step (operators.py): linear, decode, their gradients, and the
+gradient norm with clipping.
 """
 from __future__ import annotations
 
@@ -19,7 +22,8 @@ from ._lib import (PATH_NAMES, TOPK_BF16, TOPK_F32, TOPK_PATH_AUTO, TOPK_PATH_DI
 
 __all__ = ["select", "select_global", "select_ex", "plan", "prof_sample", "prof_filter", "index_bits",
            "options", "TopkError", "TOPK_PATH_AUTO", "TOPK_PATH_DIRECT", "TOPK_PATH_PROFK", "TOPK_PATH_EXACT",
-           "TOPK_RULE_EXACT", "TOPK_RULE_ALG1"]
+           "TOPK_RULE_EXACT", "TOPK_RULE_ALG1", "linear", "linear_backward", "linear_backward_selected", "decode",
+           "decode_backward", "grad_norm", "clip_grad_norm", "clip_grad_norm_"]
 
 
 def _torch():
@@ -167,3 +171,7 @@ def prof_filter(x, tau, M: int, global_: bool = False, largest: bool = True, str
                                          counts.data_ptr(), _stream_ptr(x2, stream))
     _lib.check(rc, "topk_prof_filter")
     return buf, counts
+
+
+from .operators import (clip_grad_norm, clip_grad_norm_, decode, decode_backward, grad_norm, linear,  # noqa: E402
+                        linear_backward, linear_backward_selected)

@@ -11,12 +11,15 @@ TOPK_F32, TOPK_BF16 = 0, 1
 TOPK_OK, TOPK_EINVAL, TOPK_ENOMEM, TOPK_ECUDA, TOPK_EUNSUPPORTED, TOPK_ETIMEOUT = 0, -1, -2, -3, -4, -5
 TOPK_RULE_EXACT, TOPK_RULE_ALG1 = 0, 1
 TOPK_PATH_AUTO, TOPK_PATH_DIRECT, TOPK_PATH_PROFK, TOPK_PATH_EXACT = 0, 1, 2, 3
+TOPK_ACT_NONE, TOPK_ACT_RELU, TOPK_ACT_GELU, TOPK_ACT_SILU = 0, 1, 2, 3
 PATH_NAMES = {TOPK_PATH_DIRECT: "direct", TOPK_PATH_PROFK: "profk", TOPK_PATH_EXACT: "exact"}
 
 # Every symbol include/topk.h declares.
 EXPORTS = ("topk_options_init", "topk_select", "topk_select_global", "topk_select_ex", "topk_plan",
            "topk_status_str", "topk_version", "topk_index_bits", "topk_prof_sample", "topk_prof_filter",
-           "topk_select_noalloc", "topk_last_status", "topk_autotune", "topk_tuning")
+           "topk_select_noalloc", "topk_last_status", "topk_autotune", "topk_tuning", "topk_linear",
+           "topk_linear_backward", "topk_linear_backward_selected", "topk_decode", "topk_decode_backward",
+           "topk_grad_norm", "topk_clip_grad_norm")
 
 
 class TopkOptions(ctypes.Structure):
@@ -85,6 +88,19 @@ def get():
         lib.topk_prof_sample.restype = c_int
         lib.topk_prof_filter.argtypes = [vp, c_int, i64, i64, c_int, c_int, vp, i64, vp, vp, vp]
         lib.topk_prof_filter.restype = c_int
+        ptrs = ctypes.POINTER(vp)
+        lib.topk_linear.argtypes = [vp, i64, vp, i64, vp, vp, i64, c_int, i64, i64, i64, c_int, vp, i64, vp, i64, vp]
+        lib.topk_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, c_int, i64, i64, i64, c_int, vp, vp,
+                                             vp, vp]
+        lib.topk_linear_backward_selected.argtypes = [vp, vp, vp, i64, c_int, vp, i64, vp, i64, c_int, i64, i64, i64,
+                                                      c_int, vp, vp, vp, vp]
+        lib.topk_decode.argtypes = [vp, vp, i64, c_int, vp, i64, vp, c_int, i64, i64, i64, vp, vp]
+        lib.topk_decode_backward.argtypes = [vp, i64, vp, vp, i64, c_int, vp, i64, c_int, i64, i64, i64, vp, vp, vp, vp]
+        lib.topk_grad_norm.argtypes = [ptrs, ctypes.POINTER(i64), ctypes.POINTER(c_int), i64, vp, vp]
+        lib.topk_clip_grad_norm.argtypes = [ptrs, ptrs, ctypes.POINTER(i64), ctypes.POINTER(c_int), i64, c_double, vp,
+                                            vp]
+        for name in EXPORTS[-7:]:
+            getattr(lib, name).restype = c_int
         _lib = lib
     return _lib
 

@@ -1,0 +1,296 @@
+// C entries of the operators around the selection (declared in include/topk.h):
+// argument checks, the per-(device, stream) scratch block and the launches.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <map>
+#include <mutex>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "../../include/topk.h"
+#include "common.cuh"
+#include "engine.h"
+#include "ops.h"
+
+namespace tk {
+
+int ops_sm_count() {
+  static int sms[64] = {};
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if (!sms[dev]) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    sms[dev] = v;
+  }
+  return sms[dev];
+}
+
+namespace {
+
+// Scratch blocks of the operators, apart from the selection's (which keeps
+// words at zero between calls).  Grown with stream-ordered allocation, the old
+// block released in stream order, never shrunk.
+struct Block {
+  void* ptr = nullptr;
+  size_t bytes = 0;
+};
+std::mutex g_mu;
+std::map<std::pair<int, cudaStream_t>, Block> g_blocks;
+
+cudaError_t block_of(cudaStream_t st, size_t bytes, void** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_mu);
+  Block& b = g_blocks[std::make_pair(dev, st)];
+  if (b.bytes < bytes) {
+    const size_t grow = (bytes + bytes / 4 + 0xFFFFF) & ~size_t(0xFFFFF);
+    void* p = nullptr;
+    e = cudaMallocAsync(&p, grow, st);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+    if (b.ptr) cudaFreeAsync(b.ptr, st);
+    b.ptr = p;
+    b.bytes = grow;
+  }
+  *out = b.ptr;
+  return cudaSuccess;
+}
+
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return TOPK_OK;
+  return e == cudaErrorMemoryAllocation ? TOPK_ENOMEM : TOPK_ECUDA;
+}
+
+// No exception leaves a C entry: the library's own containers can only run out of host memory.
+template <typename F>
+int guarded(F f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return TOPK_ENOMEM;
+  }
+}
+
+bool known_dtype(int dtype) { return dtype == TOPK_F32 || dtype == TOPK_BF16; }
+bool known_act(int act) { return act >= TOPK_ACT_NONE && act <= TOPK_ACT_SILU; }
+constexpr int64_t kMaxExtent = INT32_MAX;
+size_t value_bytes(int dtype) { return dtype == TOPK_F32 ? 4 : 2; }
+
+int linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* residual, int64_t ldr,
+           int dtype, int64_t rows, int64_t inner, int64_t outer, int act, void* y, int64_t ldy, void* pre, int64_t ldp,
+           cudaStream_t st) {
+  if (!known_dtype(dtype) || !known_act(act) || rows < 0 || inner < 1 || outer < 1) return TOPK_EINVAL;
+  if (rows == 0) return TOPK_OK;
+  if (!x || !w || !y || ldx < inner || ldw < inner || ldy < outer) return TOPK_EINVAL;
+  if ((residual && ldr < outer) || (pre && ldp < outer)) return TOPK_EINVAL;
+  if (rows > kMaxExtent || inner > kMaxExtent || outer > kMaxExtent) return TOPK_EUNSUPPORTED;
+  const Product g{{x, ldx, true}, {w, ldw, true}, rows, outer, inner, dtype, bias, residual, ldr, act, y, ldy, pre, ldp};
+  void* base = nullptr;
+  cudaError_t e = block_of(st, product_scratch_bytes(g), &base);
+  if (e != cudaSuccess) return status_of(e);
+  Scratch sc(base);
+  return status_of(launch_product(g, sc, nullptr, st));
+}
+
+int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre,
+                    int64_t ldp, int dtype, int64_t rows, int64_t inner, int64_t outer, int act, void* dx, void* dw,
+                    void* dbias, cudaStream_t st) {
+  if (!known_dtype(dtype) || !known_act(act) || rows < 0 || inner < 1 || outer < 1) return TOPK_EINVAL;
+  if (!dx && !dw && !dbias) return TOPK_OK;
+  if (rows > kMaxExtent || inner > kMaxExtent || outer > kMaxExtent) return TOPK_EUNSUPPORTED;
+  if (rows == 0) {  // sums over no rows
+    cudaError_t e = cudaSuccess;
+    if (dw) e = cudaMemsetAsync(dw, 0, value_bytes(dtype) * static_cast<size_t>(inner * outer), st);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, value_bytes(dtype) * static_cast<size_t>(outer), st);
+    return status_of(e);
+  }
+  if (!dy || lddy < outer || (dw && (!x || ldx < inner)) || (dx && (!w || ldw < inner))) return TOPK_EINVAL;
+  if (act != TOPK_ACT_NONE && (!pre || ldp < outer)) return TOPK_EINVAL;
+  SlopeSums s{dy, lddy, pre, ldp, dtype, rows, outer, act, nullptr, dbias, nullptr};
+  const bool make_dz = act != TOPK_ACT_NONE && (dx || dw);
+  Product gx{{dy, lddy, true}, {w, ldw, false}, rows, inner, outer, dtype, nullptr, nullptr, 0, kActNone, dx, inner, nullptr, 0};
+  Product gw{{dy, lddy, false}, {x, ldx, false}, outer, inner, rows, dtype, nullptr, nullptr, 0, kActNone, dw, inner, nullptr, 0};
+  auto lay = [&](Scratch& sc) {
+    if (make_dz) {
+      s.dz = sc.take<char>(static_cast<int64_t>(value_bytes(dtype)) * rows * outer);
+      gx.a = Operand{s.dz, outer, true};
+      gw.a = Operand{s.dz, outer, false};
+    }
+    if (dbias) s.part = sc.take<float>(slope_sums_parts(rows, outer) * outer);
+  };
+  Scratch plan;
+  lay(plan);
+  const size_t px = dx ? product_scratch_bytes(gx) : 0, pw = dw ? product_scratch_bytes(gw) : 0;
+  void* base = nullptr;
+  cudaError_t e = block_of(st, plan.used() + (px > pw ? px : pw), &base);
+  if (e != cudaSuccess) return status_of(e);
+  Scratch sc(base);
+  lay(sc);
+  if (make_dz || dbias) e = launch_slope_sums(s, st);
+  if (e == cudaSuccess && dx) {
+    Scratch own = sc;
+    e = launch_product(gx, own, nullptr, st);
+  }
+  if (e == cudaSuccess && dw) {
+    Scratch own = sc;
+    e = launch_product(gw, own, nullptr, st);
+  }
+  return status_of(e);
+}
+
+// Checks the places of a selection; TOPK_OK or the error.
+int check_places(const int64_t* idx, int64_t count, int per_row, int dtype, int64_t rows, int64_t n, int64_t d) {
+  if (!known_dtype(dtype) || rows < 0 || n < 1 || d < 1 || count < 0) return TOPK_EINVAL;
+  if (rows > kMaxExtent || n > kMaxExtent || d > kMaxExtent) return TOPK_EUNSUPPORTED;
+  if (per_row && count > 0 && rows > kMaxExtent / count) return TOPK_EUNSUPPORTED;
+  if (count > kMaxExtent) return TOPK_EUNSUPPORTED;
+  const int64_t total = per_row ? rows * count : count;
+  if (total > 0 && !idx) return TOPK_EINVAL;
+  return TOPK_OK;
+}
+
+// Runs the sums by column and by row that are asked for (either null) on one scratch block, one after the other.
+int run_sums(const ColumnSums* cols, const RowSums* rws, const SlopeSums* sums_in, cudaStream_t st) {
+  SlopeSums sums{};
+  size_t bytes = cols ? column_sums_scratch_bytes(*cols) : 0;
+  if (rws) {
+    const size_t b = row_sums_scratch_bytes(*rws);
+    bytes = b > bytes ? b : bytes;
+  }
+  if (sums_in) {
+    sums = *sums_in;
+    Scratch sc;
+    sc.take<float>(slope_sums_parts(sums.rows, sums.n) * sums.n);
+    bytes = sc.used() > bytes ? sc.used() : bytes;
+  }
+  void* base = nullptr;
+  cudaError_t e = block_of(st, bytes, &base);
+  if (e == cudaSuccess && cols) {
+    Scratch sc(base);
+    e = launch_column_sums(*cols, sc, st);
+  }
+  if (e == cudaSuccess && rws) {
+    Scratch sc(base);
+    e = launch_row_sums(*rws, sc, st);
+  }
+  if (e == cudaSuccess && sums_in) {
+    Scratch sc(base);
+    sums.part = sc.take<float>(slope_sums_parts(sums.rows, sums.n) * sums.n);
+    e = launch_slope_sums(sums, st);
+  }
+  return status_of(e);
+}
+
+int clip(const void* const* grads, void* const* out, const int64_t* counts, const int* dtypes, int64_t num, bool scale,
+         double max_norm, float* norm, cudaStream_t st) {
+  if (num < 0 || !norm || (num > 0 && (!grads || !counts || !dtypes || (scale && !out)))) return TOPK_EINVAL;
+  if (scale && !(max_norm >= 0.0)) return TOPK_EINVAL;
+  std::vector<ClipTensor> list(static_cast<size_t>(num));
+  for (int64_t i = 0; i < num; ++i) {
+    if (counts[i] < 0 || !known_dtype(dtypes[i]) || (counts[i] > 0 && (!grads[i] || (scale && !out[i])))) return TOPK_EINVAL;
+    if (counts[i] > (int64_t(1) << 44)) return TOPK_EUNSUPPORTED;
+    list[static_cast<size_t>(i)] = ClipTensor{grads[i], scale ? out[i] : nullptr, counts[i], dtypes[i]};
+  }
+  void* base = nullptr;
+  const cudaError_t e = block_of(st, clip_scratch_bytes(), &base);
+  if (e != cudaSuccess) return status_of(e);
+  Scratch sc(base);
+  return status_of(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, sc, st));
+}
+
+}  // namespace
+}  // namespace tk
+
+using namespace tk;
+
+extern "C" {
+
+int topk_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* residual,
+                int64_t ldr, int dtype, int64_t rows, int64_t inner, int64_t outer, int act, void* y, int64_t ldy,
+                void* pre, int64_t ldp, void* stream) {
+  return guarded([&] {
+    return linear(x, ldx, w, ldw, bias, residual, ldr, dtype, rows, inner, outer, act, y, ldy, pre, ldp,
+                  static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                         const void* pre, int64_t ldp, int dtype, int64_t rows, int64_t inner, int64_t outer, int act,
+                         void* dx, void* dw, void* dbias, void* stream) {
+  return guarded([&] {
+    return linear_backward(dy, lddy, x, ldx, w, ldw, pre, ldp, dtype, rows, inner, outer, act, dx, dw, dbias,
+                           static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_linear_backward_selected(const void* dvals, const void* vals, const int64_t* idx, int64_t count, int per_row,
+                                  const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype, int64_t rows,
+                                  int64_t inner, int64_t outer, int act, void* dx, void* dw, void* dbias, void* stream) {
+  return guarded([&]() -> int {
+    if (int e = check_places(idx, count, per_row, dtype, rows, outer, inner)) return e;
+    if (act != TOPK_ACT_NONE && act != TOPK_ACT_RELU) return TOPK_EINVAL;
+    const Places p{idx, count, per_row != 0, rows, outer, per_row ? rows * count : count};
+    if (p.total > 0 && (!dvals || (act == TOPK_ACT_RELU && !vals))) return TOPK_EINVAL;
+    if ((dw && rows > 0 && (!x || ldx < inner)) || (dx && (!w || ldw < inner))) return TOPK_EINVAL;
+    const Coef coef{dvals, act == TOPK_ACT_RELU ? vals : nullptr};
+    const ColumnSums c{p, coef, dtype, x, ldx, inner, nullptr, 0, dw, dbias, nullptr};
+    const RowSums r{p, coef, dtype, w, ldw, inner, nullptr, dx};
+    return run_sums(dw || dbias ? &c : nullptr, dx && rows > 0 ? &r : nullptr, nullptr, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_decode(const void* vals, const int64_t* idx, int64_t count, int per_row, const void* w, int64_t ldw,
+                const void* bias, int dtype, int64_t rows, int64_t n, int64_t d, void* y, void* stream) {
+  return guarded([&]() -> int {
+    if (int e = check_places(idx, count, per_row, dtype, rows, n, d)) return e;
+    if (rows == 0) return TOPK_OK;
+    const Places p{idx, count, per_row != 0, rows, n, per_row ? rows * count : count};
+    if (!y || !w || ldw < d || (p.total > 0 && !vals)) return TOPK_EINVAL;
+    const RowSums r{p, Coef{vals, nullptr}, dtype, w, ldw, d, bias, y};
+    return run_sums(nullptr, &r, nullptr, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_decode_backward(const void* dy, int64_t lddy, const void* vals, const int64_t* idx, int64_t count, int per_row,
+                         const void* w, int64_t ldw, int dtype, int64_t rows, int64_t n, int64_t d, void* dvals,
+                         void* dw, void* dbias, void* stream) {
+  return guarded([&]() -> int {
+    if (int e = check_places(idx, count, per_row, dtype, rows, n, d)) return e;
+    const Places p{idx, count, per_row != 0, rows, n, per_row ? rows * count : count};
+    if (rows > 0 && (dvals || dw || dbias) && (!dy || lddy < d)) return TOPK_EINVAL;
+    if (p.total > 0 && ((dw && !vals) || (dvals && (!w || ldw < d)))) return TOPK_EINVAL;
+    if (rows == 0) {  // sums over no rows
+      cudaStream_t st = static_cast<cudaStream_t>(stream);
+      cudaError_t e = cudaSuccess;
+      if (dw) e = cudaMemsetAsync(dw, 0, value_bytes(dtype) * static_cast<size_t>(n * d), st);
+      if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, value_bytes(dtype) * static_cast<size_t>(d), st);
+      if (e == cudaSuccess && dvals && p.total > 0)
+        e = cudaMemsetAsync(dvals, 0, value_bytes(dtype) * static_cast<size_t>(p.total), st);
+      return status_of(e);
+    }
+    const ColumnSums c{p, Coef{vals, nullptr}, dtype, dy, lddy, d, w, ldw, dw, nullptr, dvals};
+    const SlopeSums s{dy, lddy, nullptr, 0, dtype, rows, d, kActNone, nullptr, dbias, nullptr};
+    return run_sums(dw || dvals ? &c : nullptr, nullptr, dbias ? &s : nullptr, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t num, float* norm,
+                   void* stream) {
+  return guarded([&] {
+    return clip(grads, nullptr, counts, dtypes, num, false, 0.0, norm, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* counts, const int* dtypes,
+                        int64_t num, double max_norm, float* norm, void* stream) {
+  return guarded([&] {
+    return clip(grads, out, counts, dtypes, num, true, max_norm, norm, static_cast<cudaStream_t>(stream));
+  });
+}
+
+}  // extern "C"

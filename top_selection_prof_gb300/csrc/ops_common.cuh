@@ -1,0 +1,109 @@
+// Device helpers of the operators around the selection: conversions between
+// the storage types and f32, vector loads, activations.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace tk {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Rounded to nearest even (the one rounding of each result).
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// VEC consecutive values as f32: one 16-byte access when VEC values fill 16
+// bytes (p then 16-byte aligned), one value when VEC == 1.
+template <typename T, int VEC>
+struct Vec {
+  static_assert(VEC == 1 || VEC * sizeof(T) == 16, "one value or 16 bytes");
+  float v[VEC];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 1) {
+      v[0] = to_f32(*p);
+    } else {
+      set(*reinterpret_cast<const uint4*>(p));
+    }
+  }
+  __device__ __forceinline__ void load_nc(const T* p) {
+    if constexpr (VEC == 1) {
+      v[0] = to_f32(__ldg(p));
+    } else {
+      set(__ldg(reinterpret_cast<const uint4*>(p)));
+    }
+  }
+  __device__ __forceinline__ void set(uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        v[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+      }
+    }
+  }
+  __device__ __forceinline__ uint4 pack() const {
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC == 1) {
+      *p = from_f32<T>(v[0]);
+    } else {
+      *reinterpret_cast<uint4*>(p) = pack();
+    }
+  }
+};
+
+// act(z) and act'(z).  relu(NaN) = NaN and relu'(NaN) = 0.  gelu is the exact
+// form z Phi(z), with Phi(z) = (1 + erf(z / sqrt 2)) / 2; silu is z / (1 + e^-z),
+// which is 0 at -inf (the quotient alone would be -inf / inf).
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678118654752f)); }
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;
+    case kActGelu: return z == -INFINITY ? 0.0f : z * normal_cdf(z);
+    case kActSilu: return z == -INFINITY ? 0.0f : z / (1.0f + expf(-z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
+    case kActGelu: return fabsf(z) > 16.0f ? (z > 0.0f ? 1.0f : 0.0f)
+                                            : normal_cdf(z) + z * expf(-0.5f * z * z) * 0.3989422804014327f;
+    case kActSilu: {
+      if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;  // (the formula meets inf x 0 beyond)
+      const float s = 1.0f / (1.0f + expf(-z));
+      return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+  }
+}
+
+}  // namespace tk

@@ -980,7 +980,8 @@ const char* topk_status_str(int status) {
 
 // 0.2.0: topk_options_t gained `unsorted` (a caller built against 0.1 passes a shorter struct).
 // 0.3.0: topk_options_t gained `wait_limit_ns` and `inject_wait_timeout`; topk_last_status.
-int topk_version(void) { return 300; }
+// 0.4.0: the operators around the selection (ops_api.cu).
+int topk_version(void) { return 400; }
 
 #ifdef TK_PHASE_TIMING
 int topk_debug_phase_ns(unsigned long long* out) { return tk::debug_phase_ns(out); }

@@ -1,0 +1,284 @@
+"""The operators around the selection (include/topk.h): a sparse autoencoder's step with BatchTopK.
+
+    acts = tk.linear(x, w_enc, b_enc, act="relu")                 # (rows, n)
+    vals, idx = tk.select_global(acts, K)                         # or tk.select(acts, k): k features a row
+    y = tk.decode(vals, idx, w_dec, rows, bias=b_dec)             # (rows, d)
+    dvals, dw_dec, db_dec = tk.decode_backward(dy, vals, idx, w_dec)
+    dx, dw_enc, db_enc = tk.linear_backward_selected(dvals, vals, idx, x, w_enc, act="relu")
+    norm = tk.clip_grad_norm_([dw_enc, db_enc, dw_dec, db_dec], 1.0)
+
+As for the selection, every step runs in the library's CUDA kernels; this
+module checks tensors, allocates outputs and passes pointers and the stream.
+Inputs are float32 or bfloat16 CUDA tensors, all of one dtype and device in a
+call; matrices may be strided by row, with their last dimension contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import TOPK_ACT_GELU, TOPK_ACT_NONE, TOPK_ACT_RELU, TOPK_ACT_SILU, TOPK_BF16, TOPK_F32
+
+_ACTS = {"none": TOPK_ACT_NONE, "relu": TOPK_ACT_RELU, "gelu": TOPK_ACT_GELU, "silu": TOPK_ACT_SILU}
+_CODES = {torch.float32: TOPK_F32, torch.bfloat16: TOPK_BF16}
+
+
+def _act(act: str) -> int:
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(_ACTS), act)) from None
+
+
+def _first(t):
+    """dtype code of the tensor that the call's others are checked against."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("input must be a CUDA tensor (the engine has no CPU path)")
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise TypeError("operators take float32 or bfloat16 tensors, got %s" % t.dtype) from None
+
+
+def _like(t, ref, name):
+    if not isinstance(t, torch.Tensor) or t.dtype != ref.dtype or t.device != ref.device:
+        raise TypeError("%s must be a %s tensor on %s" % (name, ref.dtype, ref.device))
+
+
+def _matrix(t, rows, cols, name):
+    """Distance between the rows of t, which must be (rows, cols) with contiguous rows that do not overlap."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must have shape (%d, %d), got %s" % (name, rows, cols, tuple(t.shape)))
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    if rows <= 1:
+        return cols
+    if s0 < cols:
+        raise ValueError("the rows of %s must not overlap" % name)
+    return s0
+
+
+def _vector(t, ref, n, name):
+    _like(t, ref, name)
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d values" % (name, n))
+    return t.data_ptr()
+
+
+def _call(name, device, stream, tensors, *args):
+    """lib.<name>(*args, stream); with a stream of the caller's, the call's tensors are kept until it has run."""
+    fn = getattr(_lib.get(), name)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc:
+        _lib.check(rc, name)
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, save_pre: bool = False, out=None, stream=None):
+    """act(x w^T + bias) + residual, with x (rows, inner) and w (outer, inner).
+
+    save_pre=True returns (y, pre) with pre = x w^T + bias, for linear_backward.  out: where y is written
+    (it may be the residual)."""
+    code = _first(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (rows, inner)")
+    rows, inner = x.shape
+    _like(w, x, "w")
+    outer = w.shape[0]
+    ldx, ldw = _matrix(x, rows, inner, "x"), _matrix(w, outer, inner, "w")
+    pb = None if bias is None else _vector(bias, x, outer, "bias")
+    ldr = 0
+    if residual is not None:
+        _like(residual, x, "residual")
+        ldr = _matrix(residual, rows, outer, "residual")
+    if out is None:
+        out, ldy = torch.empty((rows, outer), dtype=x.dtype, device=x.device), outer
+    else:
+        _like(out, x, "out")
+        ldy = _matrix(out, rows, outer, "out")
+    pre = torch.empty((rows, outer), dtype=x.dtype, device=x.device) if save_pre else None
+    _call("topk_linear", x.device, stream, (x, w, bias, residual, out, pre), x.data_ptr(), ldx, w.data_ptr(), ldw, pb,
+          None if residual is None else residual.data_ptr(), ldr, code, rows, inner, outer, _act(act), out.data_ptr(),
+          ldy, pre.data_ptr() if save_pre else None, outer)
+    return (out, pre) if save_pre else out
+
+
+def linear_backward(dy, x, w, pre=None, act: str = "none", need=(True, True, True), stream=None):
+    """(dx, dw, dbias) of linear from dy (rows, outer); None where `need` is false.
+
+    pre: what linear kept with save_pre (needed unless act is "none"; with "relu" and no residual, its output serves)."""
+    code = _first(dy)
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D (rows, outer)")
+    rows, outer = dy.shape
+    _like(x, dy, "x")
+    _like(w, dy, "w")
+    if w.dim() != 2:
+        raise ValueError("w must be 2-D (outer, inner)")
+    inner = w.shape[1]
+    lddy, ldx, ldw = _matrix(dy, rows, outer, "dy"), _matrix(x, rows, inner, "x"), _matrix(w, outer, inner, "w")
+    a, ldp = _act(act), 0
+    if a != TOPK_ACT_NONE:
+        if pre is None:
+            raise ValueError("act %r needs pre" % act)
+        _like(pre, dy, "pre")
+        ldp = _matrix(pre, rows, outer, "pre")
+    else:
+        pre = None
+    dx = torch.empty((rows, inner), dtype=dy.dtype, device=dy.device) if need[0] else None
+    dw = torch.empty((outer, inner), dtype=dy.dtype, device=dy.device) if need[1] else None
+    db = torch.empty((outer,), dtype=dy.dtype, device=dy.device) if need[2] else None
+    _call("topk_linear_backward", dy.device, stream, (dy, x, w, pre, dx, dw, db), dy.data_ptr(), lddy, x.data_ptr(), ldx,
+          w.data_ptr(), ldw, None if pre is None else pre.data_ptr(), ldp, code, rows, inner, outer, a,
+          None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+          None if db is None else db.data_ptr())
+    return dx, dw, db
+
+
+def _places(idx, rows, ref):
+    """(count, per_row) of a selection's positions: 1-D flat ones, or (rows, k) row-local ones."""
+    if not isinstance(idx, torch.Tensor) or idx.dtype != torch.int64 or idx.device != ref.device:
+        raise TypeError("idx must be an int64 tensor on %s" % ref.device)
+    if not idx.is_contiguous():
+        raise ValueError("idx must be contiguous")
+    if idx.dim() == 1:
+        return idx.shape[0], 0
+    if idx.dim() != 2 or idx.shape[0] != rows:
+        raise ValueError("idx must be 1-D (flat positions) or (rows, k) with %d rows" % rows)
+    return idx.shape[1], 1
+
+
+def _of_places(t, idx, ref, name):
+    _like(t, ref, name)
+    if t.shape != idx.shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with idx's shape %s" % (name, tuple(idx.shape)))
+    return t.data_ptr()
+
+
+def linear_backward_selected(dvals, vals, idx, x, w, act: str = "relu", need=(True, True, True), stream=None):
+    """(dx, dw, dbias) of linear when only the selected outputs carry a gradient.
+
+    dvals, vals: gradient and value at each selected place; idx: flat positions (1-D, from select_global) or
+    row-local ones ((rows, k), from select); act: "relu" or "none".  None where `need` is false."""
+    code = _first(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (rows, inner)")
+    rows, inner = x.shape
+    _like(w, x, "w")
+    outer = w.shape[0]
+    ldx, ldw = _matrix(x, rows, inner, "x"), _matrix(w, outer, inner, "w")
+    count, per_row = _places(idx, rows, x)
+    pd, pv = _of_places(dvals, idx, x, "dvals"), _of_places(vals, idx, x, "vals")
+    dx = torch.empty((rows, inner), dtype=x.dtype, device=x.device) if need[0] else None
+    dw = torch.empty((outer, inner), dtype=x.dtype, device=x.device) if need[1] else None
+    db = torch.empty((outer,), dtype=x.dtype, device=x.device) if need[2] else None
+    _call("topk_linear_backward_selected", x.device, stream, (dvals, vals, idx, x, w, dx, dw, db), pd, pv,
+          idx.data_ptr(), count, per_row, x.data_ptr(), ldx, w.data_ptr(), ldw, code, rows, inner, outer, _act(act),
+          None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+          None if db is None else db.data_ptr())
+    return dx, dw, db
+
+
+def decode(vals, idx, w, rows: int, bias=None, stream=None):
+    """Reconstruction (rows, d): y[r] = bias + sum of vals_s w[c_s] over row r's selected places; w is (n, d)."""
+    code = _first(w)
+    if w.dim() != 2:
+        raise ValueError("w must be 2-D (n, d)")
+    n, d = w.shape
+    ldw = _matrix(w, n, d, "w")
+    count, per_row = _places(idx, rows, w)
+    pv = _of_places(vals, idx, w, "vals")
+    pb = None if bias is None else _vector(bias, w, d, "bias")
+    y = torch.empty((rows, d), dtype=w.dtype, device=w.device)
+    _call("topk_decode", w.device, stream, (vals, idx, w, bias, y), pv, idx.data_ptr(), count, per_row, w.data_ptr(), ldw,
+          pb, code, rows, n, d, y.data_ptr())
+    return y
+
+
+def decode_backward(dy, vals, idx, w, need=(True, True, True), stream=None):
+    """(dvals, dw, dbias) of decode from dy (rows, d); None where `need` is false."""
+    code = _first(dy)
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D (rows, d)")
+    rows, d = dy.shape
+    _like(w, dy, "w")
+    n = w.shape[0]
+    lddy, ldw = _matrix(dy, rows, d, "dy"), _matrix(w, n, d, "w")
+    count, per_row = _places(idx, rows, dy)
+    pv = _of_places(vals, idx, dy, "vals")
+    dv = torch.empty_like(vals) if need[0] else None
+    dw = torch.empty((n, d), dtype=dy.dtype, device=dy.device) if need[1] else None
+    db = torch.empty((d,), dtype=dy.dtype, device=dy.device) if need[2] else None
+    _call("topk_decode_backward", dy.device, stream, (dy, vals, idx, w, dv, dw, db), dy.data_ptr(), lddy, pv,
+          idx.data_ptr(), count, per_row, w.data_ptr(), ldw, code, rows, n, d, None if dv is None else dv.data_ptr(),
+          None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr())
+    return dv, dw, db
+
+
+def _table(tensors, name):
+    """(pointers, counts, dtypes) of contiguous tensors on one device, as the host arrays the library reads."""
+    num = len(tensors)
+    ptrs, counts, codes = (ctypes.c_void_p * num)(), (ctypes.c_int64 * num)(), (ctypes.c_int * num)()
+    device = tensors[0].device if num else None
+    for i, t in enumerate(tensors):
+        codes[i] = _first(t)
+        if t.device != device:
+            raise TypeError("%s must lie on one device" % name)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        ptrs[i] = t.data_ptr()
+        counts[i] = t.numel()
+    return ptrs, counts, codes
+
+
+def _norm(tensors, max_norm, out, stream):
+    """out None: in place (max_norm None: the norm alone)."""
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("needs at least one tensor")
+    ptrs, counts, codes = _table(tensors, "tensors")
+    device = tensors[0].device
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    if max_norm is None:
+        _call("topk_grad_norm", device, stream, (*tensors, norm), ptrs, counts, codes, len(tensors), norm.data_ptr())
+        return norm
+    if out is None:
+        outs, out = ptrs, ()
+    else:
+        out = list(out)
+        outs, out_counts, out_codes = _table(out, "out")
+        if out_counts[:] != counts[:] or out_codes[:] != codes[:] or (out and out[0].device != device):
+            raise ValueError("out must match the tensors' sizes, dtypes and device")
+    _call("topk_clip_grad_norm", device, stream, (*tensors, *out, norm), ptrs, outs, counts, codes, len(tensors),
+          float(max_norm), norm.data_ptr())
+    return norm
+
+
+def grad_norm(tensors, stream=None):
+    """The norm of the tensors taken as one vector: a float32 scalar on their device."""
+    return _norm(tensors, None, None, stream)
+
+
+def clip_grad_norm(tensors, max_norm: float, out, stream=None):
+    """Writes tensors * min(1, max_norm / (norm + 1e-6)) to the tensors of `out`; returns the norm before that."""
+    if out is None:
+        raise ValueError("out must be a list of tensors (clip_grad_norm_ works in place)")
+    return _norm(tensors, max_norm, out, stream)
+
+
+def clip_grad_norm_(tensors, max_norm: float, stream=None):
+    """clip_grad_norm in place."""
+    return _norm(tensors, max_norm, None, stream)
