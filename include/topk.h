@@ -203,7 +203,9 @@ int topk_plan(int64_t n, int64_t k, double eps, const topk_options_t* opt, topk_
  * only.  The short-row direct path (rows of at most 32768 elements, k <= 1024)
  * keeps a status word only when topk_select_ex is given `stats`; otherwise
  * this returns TOPK_OK for it.  Calls without any selection on `stream`
- * return TOPK_OK.
+ * return TOPK_OK.  TOPK_ETIMEOUT is also returned, once, when a bounded device
+ * wait of topk_linear or topk_linear_backward gave up on this stream since the
+ * last call of this function.
  */
 int topk_last_status(void* stream);
 

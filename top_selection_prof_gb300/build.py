@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libtopk_gb300.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["topk_api.cu", "kernels_sample.cu", "kernels_filter.cu", "kernels_fallback.cu", "kernels_select.cu",
-           "kernels_rows.cu", "params.cpp", "topk_noalloc.cu", "ops_api.cu", "kernels_linear.cu", "kernels_places.cu",
+           "kernels_rows.cu", "params.cpp", "topk_noalloc.cu", "ops_api.cu", "kernels_linear.cu", "kernels_mma.cu", "kernels_places.cu",
            "kernels_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -194,10 +194,10 @@ cudaError_t launch_slope_sums(const SlopeSums& s, cudaStream_t st) {
   return s.dtype == kF32 ? launch_slope_sums_t<float>(s, st) : launch_slope_sums_t<__nv_bfloat16>(s, st);
 }
 
-size_t product_scratch_bytes(const Product&) { return 0; }
+size_t product_scratch_bytes(const Product& g) { return g.dtype == kF32 ? 0 : mma_scratch_bytes(g); }
 
-cudaError_t launch_product(const Product& g, Scratch&, int*, cudaStream_t st) {
-  return g.dtype == kF32 ? launch_simt<float>(g, st) : launch_simt<__nv_bfloat16>(g, st);
+cudaError_t launch_product(const Product& g, Scratch& sc, int* status, cudaStream_t st) {
+  return g.dtype == kF32 ? launch_simt<float>(g, st) : launch_mma(g, sc, status, st);
 }
 
 }  // namespace tk

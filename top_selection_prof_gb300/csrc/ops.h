@@ -28,6 +28,10 @@ class Scratch {
   size_t used_ = 0;
 };
 
+// Status of the operators' device waits on `st` since it was last asked (the
+// stream must have been synchronised): kDevOk or kDevTimeout.
+cudaError_t ops_take_status(cudaStream_t st, int* status);
+
 // SMs of the current device.
 int ops_sm_count();
 
@@ -58,6 +62,9 @@ struct Product {
 };
 cudaError_t launch_product(const Product& g, Scratch& sc, int* status, cudaStream_t st);
 size_t product_scratch_bytes(const Product& g);
+// The same for BF16 on the tensor cores (kernels_mma.cu).  `status` is set when a wait runs out.
+cudaError_t launch_mma(const Product& g, Scratch& sc, int* status, cudaStream_t st);
+size_t mma_scratch_bytes(const Product& g);
 
 // dz = dy * act'(pre) (act != none; dz contiguous) and the column sums of dz
 // into dbias (nullable).  With act == none only the sums are formed, from dy.

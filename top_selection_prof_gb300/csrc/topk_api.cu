@@ -28,6 +28,7 @@
 #include "../../include/topk.h"
 #include "common.cuh"
 #include "engine.h"
+#include "ops.h"
 
 namespace tk {
 namespace {
@@ -959,6 +960,9 @@ int topk_last_status(void* stream) {
     if (it != g_last_status.end()) word = it->second;
   }
   TK_TRY(cudaStreamSynchronize(st));
+  int ostat = kDevOk;
+  TK_TRY(ops_take_status(st, &ostat));
+  if (ostat != kDevOk) return TOPK_ETIMEOUT;
   if (!word) return TOPK_OK;
   int dstat = 0;
   TK_TRY(cudaMemcpy(&dstat, word, sizeof(int), cudaMemcpyDeviceToHost));
