@@ -83,25 +83,29 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 }
 // Arrivals on a barrier of any CTA of the cluster (bar: its shared::cluster address).
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                "selp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
 // Waits for phase `parity`, at most kWaitLimitNs; false when it gave up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  if (bar_try(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!bar_try(bar, parity))
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  return true;
+  uint64_t t0 = 0;
+  for (;;) {
+    // (the timer is slow to read: only once in many tries)
+    for (int i = 0; i < 256; ++i)
+      if (bar_try(bar, parity)) return true;
+    const uint64_t t = globaltimer_ns();
+    if (!t0) t0 = t;
+    if (t - t0 > kWaitLimitNs) return false;
+  }
 }
 template <int CTAS>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
