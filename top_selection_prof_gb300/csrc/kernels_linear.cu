@@ -196,8 +196,8 @@ cudaError_t launch_slope_sums(const SlopeSums& s, cudaStream_t st) {
 
 size_t product_scratch_bytes(const Product& g) { return g.dtype == kF32 ? 0 : mma_scratch_bytes(g); }
 
-cudaError_t launch_product(const Product& g, Scratch& sc, int* status, cudaStream_t st) {
-  return g.dtype == kF32 ? launch_simt<float>(g, st) : launch_mma(g, sc, status, st);
+cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
+  return g.dtype == kF32 ? launch_simt<float>(g, st) : launch_mma(g, sc, words, st);
 }
 
 }  // namespace tk

@@ -1,16 +1,22 @@
 // Matrix products c = act(a b^T + bias) + residual on the tensor cores
 // (tcgen05.mma, bf16 operands, f32 accumulators in tensor memory).
 //
-// A persistent grid of CTAs (alone, or in pairs that share one product) takes
-// work units (tile of c, part of k) in turn.  In each CTA one thread brings
-// the operands' slices into a ring of shared-memory stages by TMA (128-byte
-// swizzle, zeros outside the matrices), one thread of the (leading) CTA
-// issues the products from them, and eight warps read finished accumulators
-// from tensor memory, apply bias, activation and residual in f32, round once
-// and store.  Tensor memory holds two accumulators, so that a tile's results
-// are written while the next tile is multiplied.  When there are too few
-// tiles for the GPU, k is cut into parts whose f32 sums go to scratch; a
-// second kernel adds them in their order and applies the same epilogue.
+// A persistent grid of CTA pairs takes 256 x 256 tiles of c in turn, each pair
+// sharing one product (cta_group::2: each CTA holds half of a's rows and half
+// of b's).  In each CTA one thread brings the operands' slices into a ring of
+// shared-memory stages by TMA (128-byte swizzle, zeros outside the matrices),
+// one thread of the leading CTA issues the products from them, and eight warps
+// read finished accumulators from tensor memory, apply bias, activation and
+// residual in f32, round once and store.  Tensor memory holds two
+// accumulators, so that a tile's results are written while the next tile is
+// multiplied.
+//
+// The last tiles rarely fill the pairs evenly.  Where it pays, the stages of
+// the tiles past the last whole wave (all of them when there is no whole wave)
+// are dealt to the pairs in equal runs, whatever tile they fall in: a run that
+// covers part of a tile's k leaves its f32 sums in scratch, and of the warps
+// that do so for the same rows and columns the last one (by a ticket) adds the
+// parts in order of k and writes the result.  Nothing waits for another run.
 //
 // Every wait has a limit, after which the status word is set and the kernel
 // winds up.
@@ -30,25 +36,39 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kStageBytesOut = 4096;   // staging of one epilogue warp: 32 rows x 128 bytes
 
-template <int CTAS, int BN>
-struct Shape {
-  static constexpr int kRowsB = BN / CTAS;  // rows of b that one CTA brings in
-  static constexpr int kBytesA = kTileM * kDeepK * 2, kBytesB = kRowsB * kDeepK * 2;
-  static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr int kOffStaging = kStages * kStage;
-  static constexpr int kOffBias = kOffStaging + kEpiWarps * kStageBytesOut;
-  static constexpr int kOffBars = kOffBias + 2 * BN * 4;
-  static constexpr int kSmem = kOffBars + (2 * kStages + 4) * 8 + 16;
-  static constexpr int kTmemCols = 2 * BN;
+constexpr int kTileN = 256;            // columns of c in a pair's tile (and of tensor memory in an accumulator)
+constexpr int kPairM = 2 * kTileM;     // its rows
+constexpr int kRowsB = kTileN / 2;     // rows of b that one CTA brings in
+constexpr int kBytesA = kTileM * kDeepK * 2, kBytesB = kRowsB * kDeepK * 2;
+constexpr int kStage = kBytesA + kBytesB;
+constexpr int kStages = 6;
+constexpr int kOffStaging = kStages * kStage;
+constexpr int kOffBias = kOffStaging + kEpiWarps * kStageBytesOut;
+constexpr int kOffBars = kOffBias + 2 * kTileN * 4;
+constexpr int kSmem = kOffBars + (2 * kStages + 4) * 8 + 16;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+// How the stages of all tiles are dealt to `pairs` pairs: `waves` whole tiles
+// to each, then the stages of the remaining `shared_tiles` in equal runs.
+struct Deal {
+  int tiles_m, tiles_n;
+  int k_blocks;       // stages of a tile
+  int pairs;
+  int waves;
+  int shared_tiles;   // 0: every pair's tiles are whole (the last wave may be short)
+  int run, longer;    // stages of a run; the first `longer` pairs' runs have one more
+  __device__ __forceinline__ int run_start(int pair) const { return pair * run + min(pair, longer); }
+  // The pair whose run holds a stage (counted over the shared tiles).
+  __device__ __forceinline__ int run_of(int stage) const {
+    const int head = longer * (run + 1);
+    return stage < head ? stage / (run + 1) : longer + (stage - head) / run;
+  }
 };
 
 struct MmaParams {
   CUtensorMap a, b, c, pre;
   int64_t m, n;
-  int k_blocks;            // stages along k
-  int splits, k_per_split; // parts of k, stages of each
-  int tiles_m, tiles_n;
+  Deal deal;
   bool a_k, b_k;           // operand order: k contiguous
   uint32_t idesc;
   const __nv_bfloat16* bias;
@@ -56,11 +76,12 @@ struct MmaParams {
   int64_t ldr;
   int act;
   bool tma_c, tma_pre;     // stores by TMA (else by plain stores)
-  void* c_ptr;
+  __nv_bfloat16* c_ptr;
   int64_t ldc;
-  void* pre_ptr;
+  __nv_bfloat16* pre_ptr;  // nullable
   int64_t ldp;
-  bool want_pre;
+  float* part;             // sums of parts of k: 2 slots a pair, each kPairM x kTileN
+  unsigned* ticket;        // 2 kEpiWarps a shared tile, zero between launches
   int* status;
 };
 
@@ -107,14 +128,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (t - t0 > kWaitLimitNs) return false;
   }
 }
-template <int CTAS>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (CTAS == 2)
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-  else
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+               "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
@@ -124,42 +140,22 @@ __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.com
 __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
-  if constexpr (CTAS == 2)
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
-  else
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
 }
-template <int CTAS>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  if constexpr (CTAS == 2) {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  } else {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  }
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
-template <int CTAS>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
-  if constexpr (CTAS == 2)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(uint32_t(add)) : "memory");
-  else
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(uint32_t(add)) : "memory");
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(uint32_t(add)) : "memory");
 }
-// Arrives on `bar` (at the same place in each CTA) when the products issued so far are done.
-template <int CTAS>
+// Arrives on `bar` (at the same place in both CTAs) when the products issued so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  if constexpr (CTAS == 2)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(bar), "h"(uint16_t(3)) : "memory");
-  else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               ::"r"(bar), "h"(uint16_t(3)) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -196,25 +192,53 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-struct Unit {
-  int m, n, split;  // tile and part of k
+// A pair's next piece of work: stages [kb0, kb1) of a tile.
+struct Work {
+  int m, n;
+  int kb0, kb1;
+  int slot;   // where its sums go when it covers only part of k; -1: a whole tile
+  int shared; // the tile's number among the shared ones
 };
-// Tiles in strips of kStrip tile rows, down the strip first: CTAs that run at
+// Tiles in strips of kStrip tile rows, down the strip first: pairs that run at
 // the same time share rows of b and keep a strip of a in L2.
 constexpr int kStrip = 16;
-__device__ __forceinline__ Unit unit_of(int u, const MmaParams& p) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  Unit r;
-  r.split = u / tiles;
-  const int t = u - r.split * tiles;
-  const int strip = t / (kStrip * p.tiles_n);
+__device__ __forceinline__ void tile_at(const Deal& d, int t, int* m, int* n) {
+  const int strip = t / (kStrip * d.tiles_n);
   const int first = strip * kStrip;
-  const int tall = min(kStrip, p.tiles_m - first);
-  const int in = t - strip * kStrip * p.tiles_n;
-  r.m = first + in % tall;
-  r.n = in / tall;
-  return r;
+  const int tall = min(kStrip, d.tiles_m - first);
+  const int in = t - strip * kStrip * d.tiles_n;
+  *m = first + in % tall;
+  *n = in / tall;
 }
+struct Worker {
+  int pair, wave;
+  int at, end;  // the pair's run of stages, counted over the shared tiles
+  __device__ __forceinline__ Worker(const Deal& d, int pair_) : pair(pair_), wave(0) {
+    at = d.shared_tiles ? d.run_start(pair) : 0;
+    end = d.shared_tiles ? d.run_start(pair + 1) : 0;
+  }
+  __device__ __forceinline__ bool next(const Deal& d, Work* w) {
+    const int64_t tile = int64_t(wave) * d.pairs + pair;
+    if (wave < d.waves && tile < int64_t(d.tiles_m) * d.tiles_n) {
+      ++wave;
+      tile_at(d, static_cast<int>(tile), &w->m, &w->n);
+      w->kb0 = 0;
+      w->kb1 = d.k_blocks;
+      w->slot = -1;
+      return true;
+    }
+    if (at >= end) return false;
+    const int t = at / d.k_blocks;
+    w->kb0 = at - t * d.k_blocks;
+    w->kb1 = min(d.k_blocks, w->kb0 + (end - at));
+    // a run begins at most one tile in its middle (slot 2 pair) and leaves at most one tile from its start (2 pair + 1)
+    w->slot = w->kb0 > 0 ? 2 * pair : w->kb1 < d.k_blocks ? 2 * pair + 1 : -1;
+    w->shared = t;
+    tile_at(d, d.waves * d.pairs + t, &w->m, &w->n);
+    at += w->kb1 - w->kb0;
+    return true;
+  }
+};
 
 // ---- the epilogue's tile chunk: 32 rows x 128 bytes in a warp's staging ---------------
 // 16-byte piece `q` (0..7) of row `row`, at its place in the 128-byte swizzle.
@@ -260,15 +284,15 @@ __device__ __forceinline__ void stage_residual(uint32_t staging, const __nv_bflo
     }
   }
 }
-// 64 values of the lane's row, rounded to bf16, into staging.
-__device__ __forceinline__ void stage_bf16(uint32_t staging, int lane, const float* v) {
+// 32 values of the lane's row, rounded to bf16, into half `h` of the staging's row.
+__device__ __forceinline__ void stage_bf16(uint32_t staging, int lane, int h, const float* v) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 4; ++q) {
     Vec<__nv_bfloat16, 8> o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.v[i] = v[q * 8 + i];
     const uint4 u = o.pack();
-    st_shared16(piece(staging, lane, q), u.x, u.y, u.z, u.w);
+    st_shared16(piece(staging, lane, 4 * h + q), u.x, u.y, u.z, u.w);
   }
 }
 template <int N>
@@ -286,81 +310,91 @@ __device__ __forceinline__ void apply_act(float* v, int act) {
   }
 }
 
-// PARTIAL: f32 sums of one part of k (no epilogue) to scratch; else bf16 results.
-template <int CTAS, int BN, bool PARTIAL>
-__global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant__ MmaParams p) {
-  using S = Shape<CTAS, BN>;
+// The pairs whose runs meet shared tile t, [first, first + parts).
+__device__ __forceinline__ void runs_of_tile(const Deal& d, int t, int* first, int* parts) {
+  *first = d.run_of(t * d.k_blocks);
+  *parts = d.run_of(t * d.k_blocks + d.k_blocks - 1) + 1 - *first;
+}
+// The warp has read its accumulator (bar: the leading CTA's barrier counts both CTAs' warps).
+__device__ __forceinline__ void free_accumulator(int lane, uint32_t bar) {
+  fence_before();
+  __syncwarp();
+  if (lane == 0) bar_arrive(map_to_rank(bar, 0));
+}
+
+__global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant__ MmaParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_addr(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  const uint32_t bars = base + S::kOffBars;
+  const uint32_t rank = cluster_rank();
+  const uint32_t bars = base + kOffBars;
   auto full = [&](int s) { return bars + s * 8; };
-  auto empty = [&](int s) { return bars + (S::kStages + s) * 8; };
-  auto acc_full = [&](int b) { return bars + (2 * S::kStages + b) * 8; };
-  auto acc_empty = [&](int b) { return bars + (2 * S::kStages + 2 + b) * 8; };
-  const uint32_t tmem_word = bars + (2 * S::kStages + 4) * 8;
+  auto empty = [&](int s) { return bars + (kStages + s) * 8; };
+  auto acc_full = [&](int b) { return bars + (2 * kStages + b) * 8; };
+  auto acc_empty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };
+  const uint32_t tmem_word = bars + (2 * kStages + 4) * 8;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      bar_init(full(s), CTAS);  // each CTA's loads
-      bar_init(empty(s), 1);    // the products that read the stage
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(full(s), 2);   // each CTA's loads
+      bar_init(empty(s), 1);  // the products that read the stage
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(acc_full(b), 1);
-      bar_init(acc_empty(b), CTAS * kEpiWarps);
+      bar_init(acc_empty(b), 2 * kEpiWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) tmem_alloc<CTAS>(tmem_word, S::kTmemCols);
+  if (warp == 2) tmem_alloc(tmem_word, 2 * kTileN);
   fence_before();
   __syncthreads();
-  if constexpr (CTAS == 2) cluster_sync();
+  cluster_sync();
   fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_word) : "memory");
+  // what comes before this grid is not needed until here
+  grid_dependency_wait();
+  grid_launch_dependents();
 
-  const int units = p.tiles_m * p.tiles_n * p.splits;
-  const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+  Worker worker(p.deal, blockIdx.x / 2);
+  Work w;
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {  // loads
       int stage = 0;
       uint32_t phase = 0;
-      for (int u = first; u < units && ok; u += step) {
-        const Unit w = unit_of(u, p);
-        const int m0 = (w.m * CTAS + static_cast<int>(rank)) * kTileM;
-        const int n0 = w.n * BN + static_cast<int>(rank) * S::kRowsB;
-        const int kb0 = w.split * p.k_per_split, kb1 = min(p.k_blocks, kb0 + p.k_per_split);
-        for (int kb = kb0; kb < kb1; ++kb) {
+      while (ok && worker.next(p.deal, &w)) {
+        const int m0 = w.m * kPairM + static_cast<int>(rank) * kTileM;
+        const int n0 = w.n * kTileN + static_cast<int>(rank) * kRowsB;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!(ok = bar_wait(empty(stage), phase ^ 1))) break;
-          const uint32_t sa = base + stage * S::kStage, sb = sa + S::kBytesA;
-          const uint32_t bar = CTAS == 2 ? map_to_rank(full(stage), 0) : full(stage);
-          bar_expect(bar, S::kStage);
+          const uint32_t sa = base + stage * kStage, sb = sa + kBytesA;
+          const uint32_t bar = map_to_rank(full(stage), 0);
+          bar_expect(bar, kStage);
           const int k0 = kb * kDeepK;
           if (p.a_k) {
-            tma_load<CTAS>(sa, &p.a, k0, m0, bar);
+            tma_load(sa, &p.a, k0, m0, bar);
           } else {
-            tma_load<CTAS>(sa, &p.a, m0, k0, bar);
-            tma_load<CTAS>(sa + 8192, &p.a, m0 + 64, k0, bar);
+            tma_load(sa, &p.a, m0, k0, bar);
+            tma_load(sa + 8192, &p.a, m0 + 64, k0, bar);
           }
           if (p.b_k) {
-            tma_load<CTAS>(sb, &p.b, k0, n0, bar);
+            tma_load(sb, &p.b, k0, n0, bar);
           } else {
-#pragma unroll
-            for (int i = 0; i < S::kRowsB / 64; ++i) tma_load<CTAS>(sb + i * 8192, &p.b, n0 + i * 64, k0, bar);
+            tma_load(sb, &p.b, n0, k0, bar);
+            tma_load(sb + 8192, &p.b, n0 + 64, k0, bar);
           }
-          if (++stage == S::kStages) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
       // every stage has been read before this CTA ends
-      for (int s = 0; s < S::kStages && ok; ++s) {
+      for (int s = 0; s < kStages && ok; ++s) {
         ok = bar_wait(empty(stage), phase ^ 1);
-        if (++stage == S::kStages) {
+        if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
@@ -371,129 +405,178 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant_
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       const uint32_t step_a = (p.a_k ? 32 : 2048) >> 4, step_b = (p.b_k ? 32 : 2048) >> 4;
-      for (int u = first; u < units && ok; u += step) {
-        const Unit w = unit_of(u, p);
-        const int kb0 = w.split * p.k_per_split, kb1 = min(p.k_blocks, kb0 + p.k_per_split);
+      while (ok && worker.next(p.deal, &w)) {
         if (!(ok = bar_wait(acc_empty(buf), acc_phase ^ 1))) break;
         fence_after();
-        const uint32_t d = tmem + buf * BN;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t d = tmem + buf * kTileN;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!(ok = bar_wait(full(stage), phase))) break;
           fence_after();
-          const uint32_t sa = base + stage * S::kStage, sb = sa + S::kBytesA;
+          const uint32_t sa = base + stage * kStage, sb = sa + kBytesA;
           const uint64_t da = operand_desc(sa, 8192), db = operand_desc(sb, 8192);
 #pragma unroll
           for (int i = 0; i < kDeepK / 16; ++i)
-            mma<CTAS>(d, da + i * step_a, db + i * step_b, p.idesc, kb > kb0 || i > 0);
-          mma_commit<CTAS>(empty(stage));
-          if (++stage == S::kStages) {
+            mma(d, da + i * step_a, db + i * step_b, p.idesc, kb > w.kb0 || i > 0);
+          mma_commit(empty(stage));
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        mma_commit<CTAS>(acc_full(buf));
+        mma_commit(acc_full(buf));
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1;
       }
     }
   } else if (warp >= 4) {  // results
     const int e = warp - 4, quad = e % 4, half = e / 4;
-    const uint32_t staging = base + S::kOffStaging + e * kStageBytesOut;
-    float* bias_smem = reinterpret_cast<float*>(smem + S::kOffBias);
-    constexpr int kChunk = PARTIAL ? 32 : 64;  // columns of 128 bytes
-    constexpr int kHalf = BN / 2;
+    const uint32_t staging = base + kOffStaging + e * kStageBytesOut;
+    float* bias_smem = reinterpret_cast<float*>(smem + kOffBias);
+    constexpr int kChunk = 64, kHalf = kTileN / 2;
     int buf = 0;
     uint32_t acc_phase = 0;
-    for (int u = first; u < units; u += step) {
-      const Unit w = unit_of(u, p);
-      const int64_t row0 = int64_t(w.m * CTAS + static_cast<int>(rank)) * kTileM + quad * 32;
-      const int64_t n0 = int64_t(w.n) * BN;
-      if constexpr (!PARTIAL) {
-        if (p.bias) {
-          for (int i = threadIdx.x - 128; i < BN; i += 32 * kEpiWarps)
-            bias_smem[buf * BN + i] = n0 + i < p.n ? to_f32(p.bias[n0 + i]) : 0.0f;
-        }
+    while (worker.next(p.deal, &w)) {
+      const int64_t row0 = int64_t(w.m) * kPairM + rank * kTileM + quad * 32;
+      const int64_t n0 = int64_t(w.n) * kTileN;
+      if (p.bias) {
+        for (int i = threadIdx.x - 128; i < kTileN; i += 32 * kEpiWarps)
+          bias_smem[buf * kTileN + i] = n0 + i < p.n ? to_f32(p.bias[n0 + i]) : 0.0f;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
       }
       // (a warp that gave up goes on without waiting, so that the others' barriers are still met)
       if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
       fence_after();
+      const uint32_t acc = tmem + buf * kTileN + half * kHalf + (uint32_t(quad * 32) << 16);
+      if (row0 >= p.m || n0 + half * kHalf >= p.n) {  // nothing of the warp's part lies in c
+        free_accumulator(lane, acc_empty(buf));
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1;
+        continue;
+      }
+      // a warp's part of a slot: four columns of each of its 32 rows together
+      const int64_t region = (int64_t(rank) * kEpiWarps + e) * (32 * kHalf) + lane * 4;
+      int first = 0, parts = 0;  // pairs whose runs make up a shared tile
+      if (w.slot >= 0) {
+        float* dst = p.part + int64_t(w.slot) * (kPairM * kTileN) + region;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kHalf; c0 += kChunk) {
-        float v[kChunk];
-        const uint32_t from = tmem + buf * BN + half * kHalf + c0 + (uint32_t(quad * 32) << 16);
+        for (int c0 = 0; c0 < kHalf; c0 += 32) {
+          float v[32];
+          tmem_load32(acc + c0, v);
+          tmem_wait_load();
 #pragma unroll
-        for (int i = 0; i < kChunk; i += 32) tmem_load32(from + i, v + i);
-        tmem_wait_load();
-        if (c0 + kChunk == kHalf) {  // the accumulator is free
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(CTAS == 2 ? map_to_rank(acc_empty(buf), 0) : acc_empty(buf));
+          for (int i = 0; i < 8; ++i)
+            __stcg(reinterpret_cast<float4*>(dst + (c0 / 4 + i) * 128), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
-        const int64_t col0 = n0 + half * kHalf + c0;
-        if (lane == 0) store_wait_read();  // the staging's last store has been read
+        free_accumulator(lane, acc_empty(buf));
+        __threadfence();
+        runs_of_tile(p.deal, w.shared, &first, &parts);
         __syncwarp();
-        if constexpr (PARTIAL) {
+        unsigned seen = 0;  // (counts up to parts - 1 and then back to 0 for the next launch)
+        if (lane == 0) seen = atomicInc(&p.ticket[(w.shared * 2 + static_cast<int>(rank)) * kEpiWarps + e], parts - 1);
+        seen = __shfl_sync(~0u, seen, 0);
+        __threadfence();
+        if (static_cast<int>(seen) != parts - 1) first = -1;
+      }
+      // 32 columns' sums (and the bias): from the accumulator, or from the parts, two parts' loads in flight
+      auto fetch = [&](int c, float* v) {
+        if (w.slot < 0) {
+          tmem_load32(acc + c, v);
+          tmem_wait_load();
+        } else {
+          const int k0 = w.shared * p.deal.k_blocks;
+          auto part_of = [&](int pair) {
+            const int slot = 2 * pair + (p.deal.run_start(pair) > k0 ? 0 : 1);
+            return reinterpret_cast<const float4*>(p.part + int64_t(slot) * (kPairM * kTileN) + region) + c / 4 * 32;
+          };
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            st_shared16(piece(staging, lane, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll 1
+          for (int o = 0; o < parts; o += 2) {
+            const bool two = o + 1 < parts;
+            const float4* s0 = part_of(first + o);
+            const float4* s1 = part_of(first + o + (two ? 1 : 0));
+            float4 t0[8], t1[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              t0[i] = __ldcg(s0 + i * 32);
+              t1[i] = __ldcg(s1 + i * 32);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a[4] = {t0[i].x, t0[i].y, t0[i].z, t0[i].w}, b[4] = {t1[i].x, t1[i].y, t1[i].z, t1[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[4 * i + j] = (v[4 * i + j] + a[j]) + (two ? b[j] : 0.0f);
+            }
+          }
+        }
+        if (p.bias) {
+          const float4* b = reinterpret_cast<const float4*>(bias_smem + buf * kTileN + half * kHalf + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 t = b[i];
+            v[4 * i] += t.x;
+            v[4 * i + 1] += t.y;
+            v[4 * i + 2] += t.z;
+            v[4 * i + 3] += t.w;
+          }
+        }
+      };
+#pragma unroll 1
+      for (int c0 = 0; c0 < kHalf && first >= 0; c0 += kChunk) {
+        const int64_t col0 = n0 + half * kHalf + c0;
+        const bool inside = col0 < p.n && row0 < p.m;
+        if (p.pre_ptr) {
+          if (lane == 0) store_wait_read();  // the staging's last store has been read
+          __syncwarp();
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            fetch(c0 + 32 * h, v);
+            stage_bf16(staging, lane, h, v);
+          }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && col0 < p.n && row0 < p.m) {
-            tma_store(&p.c, static_cast<int>(col0), static_cast<int>(row0), w.split, staging);
-            store_commit();
-          }
-        } else {
-          if (p.bias) {
-            const float4* b = reinterpret_cast<const float4*>(bias_smem + buf * BN + half * kHalf + c0);
-#pragma unroll
-            for (int i = 0; i < kChunk / 4; ++i) {
-              const float4 t = b[i];
-              v[4 * i] += t.x;
-              v[4 * i + 1] += t.y;
-              v[4 * i + 2] += t.z;
-              v[4 * i + 3] += t.w;
+          if (p.tma_pre) {
+            if (lane == 0 && inside) {
+              tma_store(&p.pre, static_cast<int>(col0), static_cast<int>(row0), 0, staging);
+              store_commit();
             }
+          } else {
+            store_plain(staging, p.pre_ptr, p.ldp, row0, p.m, col0, p.n, lane);
           }
-          if (p.want_pre) {
-            stage_bf16(staging, lane, v);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (p.tma_pre) {
-              if (lane == 0 && col0 < p.n && row0 < p.m) {
-                tma_store(&p.pre, static_cast<int>(col0), static_cast<int>(row0), 0, staging);
-                store_commit();
-                store_wait_read();
-              }
-            } else {
-              store_plain(staging, static_cast<__nv_bfloat16*>(p.pre_ptr), p.ldp, row0, p.m, col0, p.n, lane);
-            }
-            __syncwarp();
-          }
-          apply_act<kChunk>(v, p.act);
+        }
+        if (lane == 0) store_wait_read();
+        __syncwarp();
+        if (p.residual) {
+          stage_residual(staging, p.residual, p.ldr, row0, p.m, col0, p.n, lane);
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float v[32];
+          fetch(c0 + 32 * h, v);
+          if (w.slot < 0 && c0 + 32 * h + 32 == kHalf) free_accumulator(lane, acc_empty(buf));
+          apply_act<32>(v, p.act);
           if (p.residual) {
-            stage_residual(staging, p.residual, p.ldr, row0, p.m, col0, p.n, lane);
-            __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
               Vec<__nv_bfloat16, 8> r;
-              r.set(ld_shared16(piece(staging, lane, q)));
+              r.set(ld_shared16(piece(staging, lane, 4 * h + q)));
 #pragma unroll
               for (int i = 0; i < 8; ++i) v[q * 8 + i] += r.v[i];
             }
           }
-          stage_bf16(staging, lane, v);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (p.tma_c) {
-            if (lane == 0 && col0 < p.n && row0 < p.m) {
-              tma_store(&p.c, static_cast<int>(col0), static_cast<int>(row0), 0, staging);
-              store_commit();
-            }
-          } else {
-            store_plain(staging, static_cast<__nv_bfloat16*>(p.c_ptr), p.ldc, row0, p.m, col0, p.n, lane);
+          stage_bf16(staging, lane, h, v);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (p.tma_c) {
+          if (lane == 0 && inside) {
+            tma_store(&p.c, static_cast<int>(col0), static_cast<int>(row0), 0, staging);
+            store_commit();
           }
+        } else {
+          store_plain(staging, p.c_ptr, p.ldc, row0, p.m, col0, p.n, lane);
         }
       }
       buf ^= 1;
@@ -505,40 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant_
   __syncwarp();
   fence_before();
   __syncthreads();
-  if constexpr (CTAS == 2) cluster_sync();
+  cluster_sync();
   fence_after();
-  if (warp == 2) tmem_free<CTAS>(tmem, S::kTmemCols);
-}
-
-// Adds the parts of k in their order, and the epilogue.
-__global__ void __launch_bounds__(256) join_parts_kernel(const float* part, int64_t stride, int64_t ld, int splits, int64_t m,
-                                                         int64_t n, const __nv_bfloat16* bias,
-                                                         const __nv_bfloat16* residual, int64_t ldr, int act,
-                                                         __nv_bfloat16* c, int64_t ldc, __nv_bfloat16* pre, int64_t ldp) {
-  const int64_t quads = (n + 3) / 4;
-  const int64_t at = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (at >= m * quads) return;
-  const int64_t i = at / quads, j = (at - i * quads) * 4;
-  float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float* src = part + i * ld + j;
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 t = __ldcg(reinterpret_cast<const float4*>(src + s * stride));
-    z.x += t.x;
-    z.y += t.y;
-    z.z += t.z;
-    z.w += t.w;
-  }
-  const float zs[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (j + e >= n) break;
-    float v = zs[e] + (bias ? to_f32(bias[j + e]) : 0.0f);
-    if (pre) pre[i * ldp + j + e] = from_f32<__nv_bfloat16>(v);
-    v = act_value(v, act);
-    if (residual) v += to_f32(residual[i * ldr + j + e]);
-    c[i * ldc + j + e] = from_f32<__nv_bfloat16>(v);
-  }
+  if (warp == 2) tmem_free(tmem, 2 * kTileN);
 }
 
 // Copies an operand whose rows TMA cannot address to rows of `ld` values (a multiple of 8).
@@ -567,115 +619,80 @@ EncodeFn encode_fn() {
 }
 
 // A matrix of rows x cols values, rows ld apart, `planes` of them `plane` rows apart; boxes of box_cols x box_rows.
-bool encode(CUtensorMap* map, bool f32, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t planes, int64_t plane,
+bool encode(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t planes, int64_t plane,
             int box_cols, int box_rows) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
-  const int size = f32 ? 4 : 2;
+  constexpr int size = 2;
   const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
   const cuuint64_t strides[2] = {cuuint64_t(ld) * size, cuuint64_t(plane) * ld * size};
   const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(p),
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(p),
             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr double kStageUs = 0.30;  // a stage of a tile, as timed
+
 bool tma_rows(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 
 struct MmaPlan {
-  int shape;  // 0: pair, 256 x 256; 1: pair, 256 x 128; 2: one CTA, 128 x 128
-  int tiles_m, tiles_n, k_blocks, splits, k_per_split;
-  int64_t part_ld, part_rows;
+  Deal deal;
   __nv_bfloat16* copy_a;
   __nv_bfloat16* copy_b;
   int64_t ld_a, ld_b;
   float* part;
 };
-constexpr int kShapeCtas[3] = {2, 2, 1}, kShapeN[3] = {256, 128, 128};
 
 int64_t operand_rows(const Operand& o, int64_t i, int64_t k) { return o.k_inner ? i : k; }
 int64_t operand_cols(const Operand& o, int64_t i, int64_t k) { return o.k_inner ? k : i; }
 
-MmaPlan plan_mma(const Product& g, Scratch& sc) {
-  MmaPlan q{};
-  q.k_blocks = static_cast<int>((g.k + kDeepK - 1) / kDeepK);
-  q.shape = 0;
-  q.splits = 1;
-  const int sms = ops_sm_count();
-  double best = 1e30;
-  for (int shape = 0; shape < 3; ++shape) {
-    const int64_t tm = (g.m + kTileM * kShapeCtas[shape] - 1) / (kTileM * kShapeCtas[shape]);
-    const int64_t tn = (g.n + kShapeN[shape] - 1) / kShapeN[shape];
-    const int64_t slots = sms / kShapeCtas[shape];
-    const double per_block = shape == 0 ? 512 : shape == 1 ? 320 : 400;  // cycles a stage
-    if (tm * tn > INT32_MAX / 64) continue;
-    for (int s = 1; s <= 16 && s <= q.k_blocks; ++s) {
-      const int64_t kp = (q.k_blocks + s - 1) / s;
-      if ((q.k_blocks + kp - 1) / kp != s) continue;
-      const double waves = static_cast<double>((tm * tn * s + slots - 1) / slots);
-      const double join = s == 1 ? 0 : 5000.0 + 8.0 * s * g.m * g.n / 2500.0;
-      const double t = waves * (kp * per_block + 700.0) + join;
-      if (t < best) {
-        best = t;
-        q.shape = shape;
-        q.splits = s;
-        q.k_per_split = static_cast<int>(kp);
-        q.tiles_m = static_cast<int>(tm);
-        q.tiles_n = static_cast<int>(tn);
-      }
-    }
+// False when there are more tiles than a launch counts.
+bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
+  *q = MmaPlan{};
+  Deal& d = q->deal;
+  const int64_t tm = (g.m + kPairM - 1) / kPairM, tn = (g.n + kTileN - 1) / kTileN;
+  if (tm > INT32_MAX / 4 / tn) return false;
+  const int64_t tiles = tm * tn;
+  d.tiles_m = static_cast<int>(tm);
+  d.tiles_n = static_cast<int>(tn);
+  d.k_blocks = static_cast<int>((g.k + kDeepK - 1) / kDeepK);
+  const int slots = ops_sm_count() / 2 > 0 ? ops_sm_count() / 2 : 1;
+  d.pairs = static_cast<int>(tiles < slots ? tiles : slots);
+  d.waves = static_cast<int>((tiles + d.pairs - 1) / d.pairs);
+  d.shared_tiles = 0;
+  // Equal runs pay when the stages they save outweigh the parts' way through scratch.  Measured: 4096 x 12288 x 512
+  // (32 tiles of 192 stages) 60.7 -> 45.4 us, 12288 x 4096 x 512 (96 of 64) 48.0 -> 46.6; 300 x 4096 x 1000 (8 of 64)
+  // 23.9 -> 25.1, 4096 x 1024 x 8192 (512 of 16) 44.5 -> 53.4, 2000 x 16384 x 4096 (128 of 256, where all SMs at once
+  // draw the power limit) 158 -> 179.
+  const int64_t rest_waves = tiles / slots > 1 ? tiles / slots - 1 : 0;
+  const int64_t shared = tiles - rest_waves * slots;
+  const double whole = static_cast<double>((tiles + slots - 1) / slots - rest_waves) * d.k_blocks;
+  const double even = static_cast<double>(shared) * d.k_blocks / slots;
+  const double parts = static_cast<double>(slots) / shared;
+  const double join = 15.0 + 0.5 * parts + 0.1 * static_cast<double>(tiles) * d.k_blocks / slots;
+  if (tiles % slots != 0 && (whole - even) * kStageUs > join && shared * d.k_blocks >= 2 * slots && shared * d.k_blocks <= INT32_MAX &&
+      shared * 2 * kEpiWarps <= kOpsWords - 64) {
+    d.pairs = slots;
+    d.waves = static_cast<int>(rest_waves);
+    d.shared_tiles = static_cast<int>(shared);
+    d.run = static_cast<int>(shared * d.k_blocks / slots);
+    d.longer = static_cast<int>(shared * d.k_blocks % slots);
+    q->part = sc.take<float>(int64_t(2) * slots * kPairM * kTileN);
   }
   const bool ta = tma_rows(g.a.p, g.a.ld), tb = tma_rows(g.b.p, g.b.ld);
-  q.ld_a = g.a.ld;
-  q.ld_b = g.b.ld;
+  q->ld_a = g.a.ld;
+  q->ld_b = g.b.ld;
   if (!ta) {
-    q.ld_a = (operand_cols(g.a, g.m, g.k) + 7) / 8 * 8;
-    q.copy_a = sc.take<__nv_bfloat16>(q.ld_a * operand_rows(g.a, g.m, g.k));
+    q->ld_a = (operand_cols(g.a, g.m, g.k) + 7) / 8 * 8;
+    q->copy_a = sc.take<__nv_bfloat16>(q->ld_a * operand_rows(g.a, g.m, g.k));
   }
   if (!tb) {
-    q.ld_b = (operand_cols(g.b, g.n, g.k) + 7) / 8 * 8;
-    q.copy_b = sc.take<__nv_bfloat16>(q.ld_b * operand_rows(g.b, g.n, g.k));
+    q->ld_b = (operand_cols(g.b, g.n, g.k) + 7) / 8 * 8;
+    q->copy_b = sc.take<__nv_bfloat16>(q->ld_b * operand_rows(g.b, g.n, g.k));
   }
-  if (q.splits > 1) {
-    q.part_ld = (g.n + 3) / 4 * 4;
-    q.part_rows = g.m;
-    q.part = sc.take<float>(q.part_ld * q.part_rows * q.splits);
-  }
-  return q;
-}
-
-template <int CTAS, int BN, bool PARTIAL>
-cudaError_t launch_shape(const MmaParams& p, cudaStream_t st) {
-  using S = Shape<CTAS, BN>;
-  static_assert(S::kSmem <= 232448, "shared memory of one CTA");
-  auto kernel = mma_kernel<CTAS, BN, PARTIAL>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return e;
-  const int units = p.tiles_m * p.tiles_n * p.splits;
-  const int slots = ops_sm_count() / CTAS;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((units < slots ? units : slots) * CTAS));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CTAS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-template <bool PARTIAL>
-cudaError_t launch_any(int shape, const MmaParams& p, cudaStream_t st) {
-  switch (shape) {
-    case 0: return launch_shape<2, 256, PARTIAL>(p, st);
-    case 1: return launch_shape<2, 128, PARTIAL>(p, st);
-    default: return launch_shape<1, 128, PARTIAL>(p, st);
-  }
+  return true;
 }
 
 cudaError_t align_rows(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_t ld, cudaStream_t st) {
@@ -690,13 +707,14 @@ cudaError_t align_rows(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* ds
 
 size_t mma_scratch_bytes(const Product& g) {
   Scratch sc;
-  plan_mma(g, sc);
+  MmaPlan q;
+  plan_mma(g, sc, &q);
   return sc.used();
 }
 
-cudaError_t launch_mma(const Product& g, Scratch& sc, int* status, cudaStream_t st) {
-  const MmaPlan q = plan_mma(g, sc);
-  if (!q.tiles_m) return cudaErrorInvalidValue;  // more tiles than a launch counts
+cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
+  MmaPlan q;
+  if (!plan_mma(g, sc, &q)) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   if (q.copy_a) e = align_rows(g.a, g.m, g.k, q.copy_a, q.ld_a, st);
   if (e == cudaSuccess && q.copy_b) e = align_rows(g.b, g.n, g.k, q.copy_b, q.ld_b, st);
@@ -704,54 +722,37 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* status, cudaStream_t 
   MmaParams p{};
   p.m = g.m;
   p.n = g.n;
-  p.k_blocks = q.k_blocks;
-  p.splits = q.splits;
-  p.k_per_split = q.k_per_split;
-  p.tiles_m = q.tiles_m;
-  p.tiles_n = q.tiles_n;
+  p.deal = q.deal;
   p.a_k = g.a.k_inner;
   p.b_k = g.b.k_inner;
-  const int ctas = kShapeCtas[q.shape], bn = kShapeN[q.shape];
   // f32 accumulators, bf16 operands, their order, and the product's size
   p.idesc = (1u << 4) | (1u << 7) | (1u << 10) | (p.a_k ? 0u : 1u << 15) | (p.b_k ? 0u : 1u << 16) |
-            (static_cast<uint32_t>(bn / 8) << 17) | (static_cast<uint32_t>(kTileM * ctas / 16) << 24);
+            (static_cast<uint32_t>(kTileN / 8) << 17) | (static_cast<uint32_t>(kPairM / 16) << 24);
   const void* a = q.copy_a ? q.copy_a : g.a.p;
   const void* b = q.copy_b ? q.copy_b : g.b.p;
-  bool ok = p.a_k ? encode(&p.a, false, a, g.k, g.m, q.ld_a, 0, 0, kDeepK, kTileM)
-                  : encode(&p.a, false, a, g.m, g.k, q.ld_a, 0, 0, 64, kDeepK);
-  ok = ok && (p.b_k ? encode(&p.b, false, b, g.k, g.n, q.ld_b, 0, 0, kDeepK, bn / ctas)
-                    : encode(&p.b, false, b, g.n, g.k, q.ld_b, 0, 0, 64, kDeepK));
-  p.status = status;
-  if (q.splits > 1) {
-    ok = ok && encode(&p.c, true, q.part, q.part_ld, q.part_rows, q.part_ld, q.splits, q.part_rows, 32, 32);
-    if (!ok) return cudaErrorInvalidValue;
-    p.tma_c = true;
-    e = launch_any<true>(q.shape, p, st);
-    if (e != cudaSuccess) return e;
-    const int64_t quads = (g.n + 3) / 4;
-    const int64_t blocks = (g.m * quads + 255) / 256;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    join_parts_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
-        q.part, q.part_ld * q.part_rows, q.part_ld, q.splits, g.m, g.n, static_cast<const __nv_bfloat16*>(g.bias),
-        static_cast<const __nv_bfloat16*>(g.residual), g.ldr, g.act, static_cast<__nv_bfloat16*>(g.c), g.ldc,
-        static_cast<__nv_bfloat16*>(g.pre), g.ldp);
-    return cudaGetLastError();
-  }
+  bool ok = p.a_k ? encode(&p.a, a, g.k, g.m, q.ld_a, 0, 0, kDeepK, kTileM)
+                  : encode(&p.a, a, g.m, g.k, q.ld_a, 0, 0, 64, kDeepK);
+  ok = ok && (p.b_k ? encode(&p.b, b, g.k, g.n, q.ld_b, 0, 0, kDeepK, kRowsB)
+                    : encode(&p.b, b, g.n, g.k, q.ld_b, 0, 0, 64, kDeepK));
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
   p.residual = static_cast<const __nv_bfloat16*>(g.residual);
   p.ldr = g.ldr;
   p.act = g.act;
-  p.c_ptr = g.c;
+  p.c_ptr = static_cast<__nv_bfloat16*>(g.c);
   p.ldc = g.ldc;
-  p.pre_ptr = g.pre;
+  p.pre_ptr = static_cast<__nv_bfloat16*>(g.pre);
   p.ldp = g.ldp;
-  p.want_pre = g.pre != nullptr;
+  p.part = q.part;
+  p.ticket = reinterpret_cast<unsigned*>(words) + 64;
+  p.status = words;
   p.tma_c = tma_rows(g.c, g.ldc);
   p.tma_pre = g.pre && tma_rows(g.pre, g.ldp);
-  if (p.tma_c) ok = ok && encode(&p.c, false, g.c, g.n, g.m, g.ldc, 1, g.m, 64, 32);
-  if (p.tma_pre) ok = ok && encode(&p.pre, false, g.pre, g.n, g.m, g.ldp, 1, g.m, 64, 32);
+  if (p.tma_c) ok = ok && encode(&p.c, g.c, g.n, g.m, g.ldc, 1, g.m, 64, 32);
+  if (p.tma_pre) ok = ok && encode(&p.pre, g.pre, g.n, g.m, g.ldp, 1, g.m, 64, 32);
   if (!ok) return cudaErrorInvalidValue;
-  return launch_any<false>(q.shape, p, st);
+  e = cudaFuncSetAttribute(mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_after(mma_kernel, static_cast<unsigned>(2 * q.deal.pairs), kThreads, kSmem, st, p);
 }
 
 }  // namespace tk

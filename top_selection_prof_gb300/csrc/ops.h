@@ -32,6 +32,11 @@ class Scratch {
 // stream must have been synchronised): kDevOk or kDevTimeout.
 cudaError_t ops_take_status(cudaStream_t st, int* status);
 
+// Words that each (device, stream) keeps for the operators, zero at first: [0]
+// the status that a kernel sets when a wait runs out, [64..] tickets that every
+// kernel leaves at zero.
+constexpr int64_t kOpsWords = 16384;
+
 // SMs of the current device.
 int ops_sm_count();
 
@@ -60,10 +65,11 @@ struct Product {
   void* pre;             // nullable
   int64_t ldp;
 };
-cudaError_t launch_product(const Product& g, Scratch& sc, int* status, cudaStream_t st);
+// words: the stream's kOpsWords.
+cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st);
 size_t product_scratch_bytes(const Product& g);
-// The same for BF16 on the tensor cores (kernels_mma.cu).  `status` is set when a wait runs out.
-cudaError_t launch_mma(const Product& g, Scratch& sc, int* status, cudaStream_t st);
+// The same for BF16 on the tensor cores (kernels_mma.cu).
+cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, cudaStream_t st);
 size_t mma_scratch_bytes(const Product& g);
 
 // dz = dy * act'(pre) (act != none; dz contiguous) and the column sums of dz

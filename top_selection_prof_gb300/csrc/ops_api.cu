@@ -35,12 +35,12 @@ namespace {
 struct Block {
   void* ptr = nullptr;
   size_t bytes = 0;
-  int* status = nullptr;  // set by a kernel whose wait ran out; kept until it is asked for
+  int* words = nullptr;  // kOpsWords
 };
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Block> g_blocks;
 
-cudaError_t block_of(cudaStream_t st, size_t bytes, void** out, int** status = nullptr) {
+cudaError_t block_of(cudaStream_t st, size_t bytes, void** out, int** words = nullptr) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -58,18 +58,18 @@ cudaError_t block_of(cudaStream_t st, size_t bytes, void** out, int** status = n
     b.ptr = p;
     b.bytes = grow;
   }
-  if (status && !b.status) {
+  if (words && !b.words) {
     int* w = nullptr;
-    e = cudaMallocAsync(&w, 256, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(w, 0, 256, st);
+    e = cudaMallocAsync(&w, sizeof(int) * kOpsWords, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(w, 0, sizeof(int) * kOpsWords, st);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return e;
     }
-    b.status = w;
+    b.words = w;
   }
   *out = b.ptr;
-  if (status) *status = b.status;
+  if (words) *words = b.words;
   return cudaSuccess;
 }
 
@@ -103,11 +103,11 @@ int linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* b
   if (rows > kMaxExtent || inner > kMaxExtent || outer > kMaxExtent) return TOPK_EUNSUPPORTED;
   const Product g{{x, ldx, true}, {w, ldw, true}, rows, outer, inner, dtype, bias, residual, ldr, act, y, ldy, pre, ldp};
   void* base = nullptr;
-  int* word = nullptr;
-  cudaError_t e = block_of(st, product_scratch_bytes(g), &base, &word);
+  int* words = nullptr;
+  cudaError_t e = block_of(st, product_scratch_bytes(g), &base, &words);
   if (e != cudaSuccess) return status_of(e);
   Scratch sc(base);
-  return status_of(launch_product(g, sc, word, st));
+  return status_of(launch_product(g, sc, words, st));
 }
 
 int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre,
@@ -140,19 +140,19 @@ int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, co
   lay(plan);
   const size_t px = dx ? product_scratch_bytes(gx) : 0, pw = dw ? product_scratch_bytes(gw) : 0;
   void* base = nullptr;
-  int* word = nullptr;
-  cudaError_t e = block_of(st, plan.used() + (px > pw ? px : pw), &base, &word);
+  int* words = nullptr;
+  cudaError_t e = block_of(st, plan.used() + (px > pw ? px : pw), &base, &words);
   if (e != cudaSuccess) return status_of(e);
   Scratch sc(base);
   lay(sc);
   if (make_dz || dbias) e = launch_slope_sums(s, st);
   if (e == cudaSuccess && dx) {
     Scratch own = sc;
-    e = launch_product(gx, own, word, st);
+    e = launch_product(gx, own, words, st);
   }
   if (e == cudaSuccess && dw) {
     Scratch own = sc;
-    e = launch_product(gw, own, word, st);
+    e = launch_product(gw, own, words, st);
   }
   return status_of(e);
 }
@@ -226,7 +226,7 @@ cudaError_t ops_take_status(cudaStream_t st, int* status) {
   {
     std::lock_guard<std::mutex> lock(g_mu);
     const auto it = g_blocks.find(std::make_pair(dev, st));
-    if (it != g_blocks.end()) word = it->second.status;
+    if (it != g_blocks.end()) word = it->second.words;
   }
   *status = kDevOk;
   if (!word) return cudaSuccess;

@@ -80,6 +80,23 @@ struct Vec {
   }
 };
 
+// Launches a kernel that calls grid_dependency_wait() before it touches memory:
+// it may start, and set itself up, while the grid before it in the stream ends.
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // act(z) and act'(z).  relu(NaN) = NaN and relu'(NaN) = 0.  gelu is the exact
 // form z Phi(z), with Phi(z) = (1 + erf(z / sqrt 2)) / 2; silu is z / (1 + e^-z),
 // which is 0 at -inf (the quotient alone would be -inf / inf).
