@@ -127,76 +127,261 @@ cudaError_t launch_simt(const Product& g, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// dz = dy act'(pre) and its column sums.  A block takes 64 columns x
-// kSumRows rows (8 rows of threads); a column's partial sums go to part[block
-// row][column] and are added in that order by the second kernel.
+// Products of few rows: y = act(x w^T + bias) + residual for at most kFewRows
+// rows of x, one pass over w at memory speed.  A warp takes kFewCols rows of w
+// (or a KS-th of their length), 16 bytes of each a lane and step, and keeps
+// kFewCols x R sums; the lanes' sums are added by exchanging halves.
 // ---------------------------------------------------------------------------
-constexpr int kSumCols = 64, kSumThreads = 256, kSumRows = 256;
+constexpr int kFewRows = 8, kFewCols = 4, kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
 template <typename T>
-__global__ void __launch_bounds__(kSumThreads) slope_sums_kernel(const SlopeSums s) {
+struct FewParams {
+  const T* x;
+  const T* w;
+  int64_t ldx, ldw, rows, n, k, k_run;  // k_run: length of one KS-th
+  const T* bias;
+  const T* residual;
+  int64_t ldr;
+  int act;
+  T* y;
+  int64_t ldy;
+  T* pre;
+  int64_t ldp;
+};
+
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T> p, int ks) {
+  constexpr int kSums = kFewCols * R;
+  __shared__ float sums[kFewWarps][kSums];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int groups = kFewWarps / ks, group = warp / ks, part = warp % ks;
+  const int64_t n0 = (int64_t(blockIdx.x) * groups + group) * kFewCols;
+  float acc[kSums] = {};
+  const T* wp[kFewCols];
+#pragma unroll
+  for (int c = 0; c < kFewCols; ++c) wp[c] = p.w + min(n0 + c, p.n - 1) * p.ldw;
+  const T* xp[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) xp[r] = p.x + min(int64_t(r), p.rows - 1) * p.ldx;
+  const int64_t k1 = min(p.k, (part + 1) * p.k_run);
+#pragma unroll 2
+  for (int64_t k = part * p.k_run + lane * VEC; k < k1; k += 32 * VEC) {
+    Vec<T, VEC> wv[kFewCols];
+#pragma unroll
+    for (int c = 0; c < kFewCols; ++c) wv[c].load_nc(wp[c] + k);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Vec<T, VEC> xv;
+      xv.load_nc(xp[r] + k);
+#pragma unroll
+      for (int c = 0; c < kFewCols; ++c)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[c * R + r] = fmaf(wv[c].v[v], xv.v[v], acc[c * R + r]);
+    }
+  }
+  // halves exchanged until a lane holds one sum: sum i in the lanes whose high bits say i
+  int o = 16;
+#pragma unroll
+  for (int h = kSums / 2; h >= 1; h /= 2) {
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const bool high = lane & o;
+      const float give = high ? acc[i] : acc[i + h];
+      acc[i] = (high ? acc[i + h] : acc[i]) + __shfl_xor_sync(~0u, give, o);
+    }
+    o /= 2;
+  }
+  for (; o; o /= 2) acc[0] += __shfl_xor_sync(~0u, acc[0], o);
+  constexpr int kLanes = 32 / kSums;  // lanes that hold the same sum
+  if (lane % kLanes == 0) sums[warp][lane / kLanes] = acc[0];
+  __syncthreads();
+  // each group's first lanes finish its sums, the parts in their order
+  if (part != 0 || lane >= kSums) return;
+  float z = 0.0f;
+  for (int q = 0; q < ks; ++q) z += sums[group * ks + q][lane];
+  const int64_t j = n0 + lane / R, i = lane % R;
+  if (j >= p.n || i >= p.rows) return;
+  z += p.bias ? to_f32(p.bias[j]) : 0.0f;
+  if (p.pre) p.pre[i * p.ldp + j] = from_f32<T>(z);
+  z = act_value(z, p.act);
+  if (p.residual) z += to_f32(p.residual[i * p.ldr + j]);
+  p.y[i * p.ldy + j] = from_f32<T>(z);
+}
+
+template <typename T, int VEC>
+cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
+  const int64_t per = kFewCols * (kFewWarps / ks);
+  const unsigned grid = static_cast<unsigned>((p.n + per - 1) / per);
+  if (p.rows <= 1) return launch_after(few_rows_kernel<T, VEC, 1>, grid, kFewThreads, 0, st, p, ks);
+  if (p.rows <= 2) return launch_after(few_rows_kernel<T, VEC, 2>, grid, kFewThreads, 0, st, p, ks);
+  if (p.rows <= 4) return launch_after(few_rows_kernel<T, VEC, 4>, grid, kFewThreads, 0, st, p, ks);
+  return launch_after(few_rows_kernel<T, VEC, 8>, grid, kFewThreads, 0, st, p, ks);
+}
+
+bool few_rows(const Product& g) { return g.m <= kFewRows && g.a.k_inner && g.b.k_inner; }
+
+template <typename T>
+cudaError_t launch_few(const Product& g, cudaStream_t st) {
+  constexpr int kVec = 16 / sizeof(T);
+  FewParams<T> p{static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p), g.a.ld, g.b.ld, g.m, g.n, g.k, 0,
+                 static_cast<const T*>(g.bias), static_cast<const T*>(g.residual), g.ldr, g.act, static_cast<T*>(g.c), g.ldc,
+                 static_cast<T*>(g.pre), g.ldp};
+  const bool vec = g.k % kVec == 0 && g.a.ld % kVec == 0 && g.b.ld % kVec == 0 &&
+                   (reinterpret_cast<uintptr_t>(g.a.p) | reinterpret_cast<uintptr_t>(g.b.p)) % 16 == 0;
+  const int64_t step = 32 * (vec ? kVec : 1);
+  // k in parts until there are 16 warps for every SM, each with a step at least
+  int ks = 1;
+  while (ks < kFewWarps && (g.n + kFewCols - 1) / kFewCols * ks < 16 * ops_sm_count() && g.k > 2 * ks * step) ks *= 2;
+  p.k_run = ((g.k + ks - 1) / ks + step - 1) / step * step;
+  return vec ? launch_few_v<T, kVec>(p, ks, st) : launch_few_v<T, 1>(p, ks, st);
+}
+
+// ---------------------------------------------------------------------------
+// dz = dy act'(pre) and its column sums.  A block takes 32 x VEC columns and
+// `rows_each` rows, a warp every eighth of them; a column's sums over the
+// block go to part[block row][column] and are added in that order by the
+// second kernel.
+// ---------------------------------------------------------------------------
+constexpr int kSumWarps = 8, kSumThreads = 32 * kSumWarps, kSumAhead = 4;
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kSumThreads) slope_sums_kernel(const SlopeSums s, int64_t rows_each) {
   const T* dy = static_cast<const T*>(s.dy);
   const T* pre = static_cast<const T*>(s.pre);
   T* dz = static_cast<T*>(s.dz);
-  __shared__ float sums[kSumThreads / kSumCols][kSumCols];
-  const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
-  const int64_t col_blocks = (s.n + kSumCols - 1) / kSumCols;
+  __shared__ float sums[kSumWarps][32 * VEC];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t col_blocks = (s.n + 32 * VEC - 1) / (32 * VEC);
   const int64_t rb = blockIdx.x / col_blocks;
-  const int64_t j = (blockIdx.x % col_blocks) * kSumCols + tx;
-  const int64_t r1 = min(s.rows, (rb + 1) * kSumRows);
-  float acc = 0.0f;
+  const int64_t j0 = (blockIdx.x % col_blocks) * (32 * VEC), j = j0 + lane * VEC;
+  const int64_t r1 = min(s.rows, (rb + 1) * rows_each);
+  float acc[VEC] = {};
   if (j < s.n) {
-    for (int64_t r = rb * kSumRows + ty; r < r1; r += kSumThreads / kSumCols) {
-      float v = to_f32(dy[r * s.lddy + j]);
-      if (s.act != kActNone) {
-        v *= act_slope(to_f32(pre[r * s.ldp + j]), s.act);
-        if (dz) dz[r * s.n + j] = from_f32<T>(v);
+    for (int64_t r = rb * rows_each + warp; r < r1; r += kSumWarps * kSumAhead) {
+      Raw<T, VEC> v[kSumAhead], z[kSumAhead];
+#pragma unroll
+      for (int a = 0; a < kSumAhead; ++a) {
+        const int64_t i = r + a * kSumWarps;
+        if (i < r1) {
+          v[a].load_nc(dy + i * s.lddy + j);
+          if constexpr (ACT != kActNone) z[a].load_nc(pre + i * s.ldp + j);
+        }
       }
-      acc += v;
+#pragma unroll
+      for (int a = 0; a < kSumAhead; ++a) {
+        const int64_t i = r + a * kSumWarps;
+        if (i >= r1) break;
+        Vec<T, VEC> t;
+        t.set_raw(v[a]);
+        if constexpr (ACT != kActNone) {
+          Vec<T, VEC> u;
+          u.set_raw(z[a]);
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) t.v[c] *= act_slope(u.v[c], ACT);
+          if (dz) t.store(dz + i * s.n + j);
+        }
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] += t.v[c];
+      }
     }
   }
-  sums[ty][tx] = acc;
+  if (!s.dbias) return;
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) sums[warp][lane * VEC + c] = acc[c];
   __syncthreads();
-  if (s.dbias && ty == 0 && j < s.n) {
+  for (int c = threadIdx.x; c < 32 * VEC; c += kSumThreads) {
+    if (j0 + c >= s.n) break;
     float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSumThreads / kSumCols; ++i) t += sums[i][tx];
-    s.part[rb * s.n + j] = t;
+    for (int w = 0; w < kSumWarps; ++w) t += sums[w][c];
+    s.part[rb * s.n + j0 + c] = t;
+  }
+}
+
+// A block adds 32 columns' parts, a warp every eighth of them.
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const float* part, int64_t parts, int64_t n, T* out) {
+  __shared__ float sums[kSumWarps][32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t j = int64_t(blockIdx.x) * 32 + lane;
+  float t = 0.0f;
+  if (j < n) {
+#pragma unroll 8
+    for (int64_t i = warp; i < parts; i += kSumWarps) t += __ldcg(part + i * n + j);
+  }
+  sums[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && j < n) {
+    t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSumWarps; ++w) t += sums[w][lane];
+    out[j] = from_f32<T>(t);
   }
 }
 
 template <typename T>
-__global__ void sum_parts_kernel(const float* part, int64_t parts, int64_t n, T* out) {
-  const int64_t j = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (j >= n) return;
-  float t = 0.0f;
-  for (int64_t i = 0; i < parts; ++i) t += part[i * n + j];
-  out[j] = from_f32<T>(t);
+bool slope_vectors(const SlopeSums& s) {
+  constexpr int kVec = 16 / sizeof(T);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(s.dy) | (s.act != kActNone ? reinterpret_cast<uintptr_t>(s.pre) : 0);
+  return at % 16 == 0 && s.lddy % kVec == 0 && s.n % kVec == 0 && (s.act == kActNone || s.ldp % kVec == 0);
+}
+
+// Rows of a block: sixteen blocks an SM where there are enough rows, so that the last ones cost little (with four an
+// SM a few blocks more than fit at once doubled the time).
+int64_t slope_rows_each(int64_t rows, int64_t n) {
+  const int64_t col_blocks = (n + 255) / 256;
+  const int64_t each = rows * col_blocks / (16 * ops_sm_count());
+  const int64_t least = kSumWarps * kSumAhead;
+  return each < least ? least : each > 512 ? 512 : (each + least - 1) / least * least;
+}
+
+template <typename T, int VEC>
+cudaError_t launch_slope_act(const SlopeSums& s, int64_t each, unsigned grid, cudaStream_t st) {
+  switch (s.act) {
+    case kActRelu: return launch_after(slope_sums_kernel<T, VEC, kActRelu>, grid, kSumThreads, 0, st, s, each);
+    case kActGelu: return launch_after(slope_sums_kernel<T, VEC, kActGelu>, grid, kSumThreads, 0, st, s, each);
+    case kActSilu: return launch_after(slope_sums_kernel<T, VEC, kActSilu>, grid, kSumThreads, 0, st, s, each);
+    default: return launch_after(slope_sums_kernel<T, VEC, kActNone>, grid, kSumThreads, 0, st, s, each);
+  }
 }
 
 template <typename T>
 cudaError_t launch_slope_sums_t(const SlopeSums& s, cudaStream_t st) {
-  const int64_t parts = slope_sums_parts(s.rows, s.n);
-  const int64_t blocks = parts * ((s.n + kSumCols - 1) / kSumCols);
+  constexpr int kVec = 16 / sizeof(T);
+  const int64_t each = slope_rows_each(s.rows, s.n), parts = slope_sums_parts(s.rows, s.n);
+  const bool vec = slope_vectors<T>(s);
+  const int64_t wide = 32 * (vec ? kVec : 1);
+  const int64_t blocks = parts * ((s.n + wide - 1) / wide);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  slope_sums_kernel<T><<<static_cast<unsigned>(blocks), kSumThreads, 0, st>>>(s);
-  if (s.dbias)
-    sum_parts_kernel<T><<<static_cast<unsigned>((s.n + 127) / 128), 128, 0, st>>>(s.part, parts, s.n,
-                                                                                  static_cast<T*>(s.dbias));
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(blocks);
+  cudaError_t e = vec ? launch_slope_act<T, kVec>(s, each, grid, st) : launch_slope_act<T, 1>(s, each, grid, st);
+  if (e == cudaSuccess && s.dbias)
+    e = launch_after(sum_parts_kernel<T>, static_cast<unsigned>((s.n + 31) / 32), kSumThreads, 0, st,
+                     static_cast<const float*>(s.part), parts, s.n, static_cast<T*>(s.dbias));
+  return e;
 }
 
 }  // namespace
 
-int64_t slope_sums_parts(int64_t rows, int64_t) { return (rows + kSumRows - 1) / kSumRows; }
+int64_t slope_sums_parts(int64_t rows, int64_t n) {
+  const int64_t each = slope_rows_each(rows, n);
+  return (rows + each - 1) / each;
+}
 
 cudaError_t launch_slope_sums(const SlopeSums& s, cudaStream_t st) {
   return s.dtype == kF32 ? launch_slope_sums_t<float>(s, st) : launch_slope_sums_t<__nv_bfloat16>(s, st);
 }
 
-size_t product_scratch_bytes(const Product& g) { return g.dtype == kF32 ? 0 : mma_scratch_bytes(g); }
+size_t product_scratch_bytes(const Product& g) { return g.dtype == kF32 || few_rows(g) ? 0 : mma_scratch_bytes(g); }
 
 cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
+  if (few_rows(g)) return g.dtype == kF32 ? launch_few<float>(g, st) : launch_few<__nv_bfloat16>(g, st);
   return g.dtype == kF32 ? launch_simt<float>(g, st) : launch_mma(g, sc, words, st);
 }
 

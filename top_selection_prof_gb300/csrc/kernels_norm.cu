@@ -1,14 +1,19 @@
 // The norm of many tensors taken as one vector, and their scaling to a largest
 // norm: n = sqrt(sum g^2), g <- g min(1, max_norm / (n + 1e-6)).
 //
-// The tensors are cut into chunks of kChunk values; the table of tensors goes
-// to the kernel as its parameter, so nothing is copied to the device.  A block
-// sums the squares of its chunks in f32 a thread at a time (at most
-// kChunk / kThreads squares in one f32 sum), adds those in f64 and writes one
-// partial sum; the last block adds all partial sums in their order.  Where the
-// f32 squares of a chunk overflow, or are so small that bits are lost, the
-// chunk is summed again in f64, so that the norm is exact to f32 for any
-// finite input.
+// The tensors' values are cut into chunks, dealt to the blocks in turn (all
+// blocks then read close to each other: one run a block took 45 us where this
+// takes 28); the table of tensors goes to the kernel as its parameter, so
+// nothing is copied to the device.  A thread sums a chunk's squares in f32 and
+// adds them in f64; the blocks' sums are added in their order.  Where the f32
+// squares overflow, or are so small that bits are lost, the chunk is summed
+// again in f64, so that the norm is exact to f32 for any finite input.
+//
+// Few values (at most kFewValues) take one launch: a cluster of blocks holds
+// them in registers, exchanges its sums through distributed shared memory and
+// writes them scaled.  More
+// take two: the sums, whose last block forms the norm, and the scaling, which
+// goes over the chunks from the last, so that it finds in L2 what was read last.
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -19,65 +24,129 @@ namespace tk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;        // values of a chunk
-constexpr int kTable = 640;         // tensors of one launch (the kernel parameter holds their table)
+constexpr int kAhead = 8;            // 16-byte loads of a thread in flight
+constexpr int kTable = 640;          // tensors of one launch (the kernel's parameter holds their table)
+constexpr int kFewTensors = 48;      // the smaller table of calls with few tensors
 constexpr int kMaxBlocks = 2048;
+constexpr int kCluster = 8;
+constexpr int kFewThreads = 512, kFewEach = 16;  // values of a thread, held in registers
+constexpr int64_t kFewValues = int64_t(kCluster) * kFewThreads * kFewEach;
 
+template <int N>
 struct TensorTable {
-  const void* in[kTable];
-  void* out[kTable];
-  int64_t count[kTable];
-  uint32_t first[kTable + 1];  // first chunk of each tensor
-  uint8_t f32[kTable];
+  const void* in[N];
+  void* out[N];
+  int64_t end[N];  // values up to and including the tensor, over the launch
+  uint8_t f32[N];
   int tensors;
+  int64_t chunk;   // values of a chunk (a multiple of 8)
 };
 struct NormScratch {
   double* part;       // per block of this launch
   double* carry;      // sum of the launches before it
-  unsigned* ticket;
   float* scale;
+  unsigned* ticket;   // zero between launches
 };
 
-__device__ __forceinline__ int tensor_of(const TensorTable& t, uint32_t chunk) {
+// Calls f(tensor, first value, count) for each tensor's part of values [v0, v1).
+template <int N, typename F>
+__device__ __forceinline__ void each_part(const TensorTable<N>& t, int64_t v0, int64_t v1, F f) {
   int lo = 0, hi = t.tensors - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (t.first[mid] <= chunk) lo = mid;
-    else hi = mid - 1;
+  while (lo < hi) {  // the first tensor that ends past v0
+    const int mid = (lo + hi) / 2;
+    if (t.end[mid] > v0) hi = mid;
+    else lo = mid + 1;
   }
-  return lo;
+  for (; lo < t.tensors && v0 < v1; ++lo) {
+    const int64_t first = lo ? t.end[lo - 1] : 0, end = min(t.end[lo], v1);
+    if (end > v0) f(lo, v0 - first, end - v0);
+    v0 = max(v0, end);
+  }
 }
 
-// Calls f(value) for this thread's values of [p, p + n): whole 16-byte vectors
-// between a head and a tail of single values.
-template <typename T, typename F>
-__device__ __forceinline__ void each_value(const T* p, int n, F f) {
+// Goes over the block's values of [p, p + n), from the end when BACKWARD: whole
+// 16-byte vectors (aligned to those of p) kAhead at a time through `vec(values,
+// place)`, single values at the ends through `one(value, place)`.
+template <typename T, bool BACKWARD, typename V, typename O>
+__device__ __forceinline__ void each_value(const T* p, int64_t n, V vec, O one) {
   constexpr int kVec = 16 / sizeof(T);
-  const int head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int(sizeof(T)));
-  const int vecs = (n - head) / kVec;
-  for (int i = threadIdx.x; i < head; i += kThreads) f(to_f32(p[i]));
-#pragma unroll 4
-  for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    Vec<T, kVec> v;
-    v.load(p + head + i * kVec);
+  const int64_t head = min(n, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int64_t(sizeof(T)));
+  const int64_t vecs = (n - head) / kVec;
+  for (int64_t i = threadIdx.x; i < head; i += kThreads) one(to_f32(p[i]), i);
+  const int64_t steps = vecs / (kThreads * kAhead);
+  const uint4* q = reinterpret_cast<const uint4*>(p + head) + threadIdx.x;
+  auto rest = [&] {  // less than a whole step, at the end
+    for (int64_t i = steps * (kThreads * kAhead) + threadIdx.x; i < vecs; i += kThreads) {
+      Vec<T, kVec> v;
+      v.set(q[i - threadIdx.x]);
+      vec(v, head + i * kVec);
+    }
+  };
+  if (BACKWARD) rest();
+#pragma unroll 1
+  for (int64_t s = 0; s < steps; ++s) {
+    const int64_t i0 = (BACKWARD ? steps - 1 - s : s) * (kThreads * kAhead);
+    uint4 raw[kAhead];
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) f(v.v[c]);
+    for (int a = 0; a < kAhead; ++a) raw[a] = q[i0 + a * kThreads];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      Vec<T, kVec> v;
+      v.set(raw[a]);
+      vec(v, head + (i0 + a * kThreads + threadIdx.x) * kVec);
+    }
   }
-  for (int i = head + vecs * kVec + threadIdx.x; i < n; i += kThreads) f(to_f32(p[i]));
+  if (!BACKWARD) rest();
+  for (int64_t i = head + vecs * kVec + threadIdx.x; i < n; i += kThreads) one(to_f32(p[i]), i);
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* p, int n) {
+__device__ __noinline__ double part_squares_wide(const T* p, int64_t n) {
+  constexpr int kVec = 16 / sizeof(T);
+  double wide = 0.0;
+  each_value<T, false>(
+      p, n,
+      [&](const Vec<T, kVec>& v, int64_t) {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) wide += static_cast<double>(v.v[c]) * v.v[c];
+      },
+      [&](float v, int64_t) { wide += static_cast<double>(v) * v; });
+  return wide;
+}
+
+template <typename T>
+__device__ __forceinline__ double part_squares(const T* p, int64_t n) {
+  constexpr int kVec = 16 / sizeof(T);
   float sum = 0.0f, most = 0.0f;
-  each_value(p, n, [&](float v) {
+  auto add = [&](float v) {
     sum = fmaf(v, v, sum);
     most = fmaxf(most, fabsf(v));
-  });
-  // squares between 2^-100 and 2^126 / n lose nothing; NaN and inf stay what they are
+  };
+  each_value<T, false>(
+      p, n,
+      [&](const Vec<T, kVec>& v, int64_t) {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) add(v.v[c]);
+      },
+      [&](float v, int64_t) { add(v); });
+  // f32 squares neither overflow nor lose bits between these; zeros, NaN and infinities stay what they are
   if (most == 0.0f || !(most < INFINITY) || (most > 1e-15f && most < 1e17f)) return static_cast<double>(sum);
-  double wide = 0.0;
-  each_value(p, n, [&](float v) { wide += static_cast<double>(v) * v; });
-  return wide;
+  return part_squares_wide(p, n);
+}
+
+template <int N>
+__device__ __forceinline__ double chunk_squares(const TensorTable<N>& t, int64_t chunk) {
+  const int64_t v0 = chunk * t.chunk, v1 = min(v0 + t.chunk, t.end[t.tensors - 1]);
+  double sum = 0.0;
+  each_part(t, v0, v1, [&](int i, int64_t at, int64_t n) {
+    sum += t.f32[i] ? part_squares(static_cast<const float*>(t.in[i]) + at, n)
+                    : part_squares(static_cast<const __nv_bfloat16*>(t.in[i]) + at, n);
+  });
+  return sum;
+}
+template <int N>
+__device__ __forceinline__ int64_t chunks_of(const TensorTable<N>& t) {
+  return t.tensors ? (t.end[t.tensors - 1] + t.chunk - 1) / t.chunk : 0;
 }
 
 __device__ __forceinline__ double block_sum(double v, double* shared) {
@@ -90,25 +159,56 @@ __device__ __forceinline__ double block_sum(double v, double* shared) {
   __syncthreads();
   return t;
 }
+__device__ __forceinline__ float scale_of(float norm, float max_norm) {
+  const float f = max_norm / (norm + 1e-6f);
+  return f > 1.0f ? 1.0f : f;  // (NaN stays NaN)
+}
 
-__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ TensorTable t, NormScratch s,
-                                                           bool first, bool finish, float max_norm, float* norm) {
+template <typename T>
+__device__ __forceinline__ void scale_part(const T* p, T* out, int64_t n, float f) {
+  constexpr int kVec = 16 / sizeof(T);
+  const bool apart = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0;
+  each_value<T, true>(
+      p, n,
+      [&](const Vec<T, kVec>& v, int64_t at) {
+        Vec<T, kVec> o;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) o.v[c] = v.v[c] * f;
+        if (apart) {
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) out[at + c] = from_f32<T>(o.v[c]);
+        } else {
+          __stcs(reinterpret_cast<uint4*>(out + at), o.pack());
+        }
+      },
+      [&](float v, int64_t at) { out[at] = from_f32<T>(v * f); });
+}
+template <int N>
+__device__ __forceinline__ void scale_chunk(const TensorTable<N>& t, int64_t chunk, float f) {
+  const int64_t v0 = chunk * t.chunk, v1 = min(v0 + t.chunk, t.end[t.tensors - 1]);
+  each_part(t, v0, v1, [&](int i, int64_t at, int64_t n) {
+    if (f == 1.0f && t.in[i] == t.out[i]) return;
+    if (t.f32[i])
+      scale_part(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, n, f);
+    else
+      scale_part(static_cast<const __nv_bfloat16*>(t.in[i]) + at, static_cast<__nv_bfloat16*>(t.out[i]) + at, n, f);
+  });
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 4) squares_kernel(const __grid_constant__ TensorTable<N> t, NormScratch s, bool first,
+                                                           bool finish, float max_norm, float* norm) {
   __shared__ double shared[kThreads / 32];
   __shared__ bool last;
+  grid_dependency_wait();
+  grid_launch_dependents();
   double sum = 0.0;
-  const uint32_t chunks = t.first[t.tensors];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const int64_t at = int64_t(c - t.first[i]) * kChunk;
-    const int n = static_cast<int>(min(int64_t(kChunk), t.count[i] - at));
-    sum += t.f32[i] ? chunk_squares(static_cast<const float*>(t.in[i]) + at, n)
-                    : chunk_squares(static_cast<const __nv_bfloat16*>(t.in[i]) + at, n);
-  }
+  for (int64_t c = blockIdx.x; c < chunks_of(t); c += gridDim.x) sum += chunk_squares(t, c);
   sum = block_sum(sum, shared);
   if (threadIdx.x == 0) {
     s.part[blockIdx.x] = sum;
     __threadfence();
-    last = atomicAdd(s.ticket, 1u) == gridDim.x - 1;
+    last = atomicInc(s.ticket, gridDim.x - 1) == gridDim.x - 1;  // (back to 0 for the next launch)
   }
   __syncthreads();
   if (!last) return;
@@ -119,46 +219,104 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
   if (threadIdx.x == 0) {
     if (!first) all += *s.carry;
     *s.carry = all;
-    *s.ticket = 0;
     if (finish) {
       const float n = static_cast<float>(sqrt(all));
       *norm = n;
-      const float f = max_norm / (n + 1e-6f);
-      *s.scale = f > 1.0f ? 1.0f : f;  // (NaN stays NaN)
+      *s.scale = scale_of(n, max_norm);
     }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_chunk(const T* p, T* out, int n, float f) {
-  constexpr int kVec = 16 / sizeof(T);
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p) & 15, b = reinterpret_cast<uintptr_t>(out) & 15;
-  const int head = a == b ? min(n, static_cast<int>((16 - a) & 15) / int(sizeof(T))) : n;
-  const int vecs = (n - head) / kVec;
-  for (int i = threadIdx.x; i < head; i += kThreads) out[i] = from_f32<T>(to_f32(p[i]) * f);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    Vec<T, kVec> v;
-    v.load(p + head + i * kVec);
-#pragma unroll
-    for (int c = 0; c < kVec; ++c) v.v[c] *= f;
-    v.store(out + head + i * kVec);
-  }
-  for (int i = head + vecs * kVec + threadIdx.x; i < n; i += kThreads) out[i] = from_f32<T>(to_f32(p[i]) * f);
+template <int N>
+__global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constant__ TensorTable<N> t, const float* scale) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const float f = *scale;
+  for (int64_t c = chunks_of(t) - 1 - blockIdx.x; c >= 0; c -= gridDim.x) scale_chunk(t, c, f);
 }
 
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ TensorTable t, const float* scale) {
-  const float f = *scale;
-  const uint32_t chunks = t.first[t.tensors];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    if (f == 1.0f && t.in[i] == t.out[i]) continue;
-    const int64_t at = int64_t(c - t.first[i]) * kChunk;
-    const int n = static_cast<int>(min(int64_t(kChunk), t.count[i] - at));
-    if (t.f32[i])
-      scale_chunk(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, n, f);
-    else
-      scale_chunk(static_cast<const __nv_bfloat16*>(t.in[i]) + at, static_cast<__nv_bfloat16*>(t.out[i]) + at, n, f);
+// Norm and scaling of few values by one cluster.  Values are dealt to threads
+// one at a time, whatever tensor they lie in, all loads of a thread in flight.
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kFewThreads)
+    clip_few_kernel(const __grid_constant__ TensorTable<kFewTensors> t, bool scale, float max_norm, float* norm) {
+  __shared__ double shared[kFewThreads / 32];
+  __shared__ double sums[kCluster];
+  __shared__ int64_t ends[kFewTensors];
+  __shared__ const void* ins[kFewTensors];
+  if (threadIdx.x < t.tensors) {
+    ends[threadIdx.x] = t.end[threadIdx.x];
+    ins[threadIdx.x] = t.in[threadIdx.x];
+  }
+  __syncthreads();
+  // (every block of the cluster has started before another writes to its memory)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int values = t.tensors ? static_cast<int>(t.end[t.tensors - 1]) : 0;
+  float v[kFewEach];
+  int where[kFewEach];  // tensor, or -1
+#pragma unroll
+  for (int e = 0; e < kFewEach; ++e) {
+    const int at = (e * kCluster + static_cast<int>(blockIdx.x)) * kFewThreads + static_cast<int>(threadIdx.x);
+    v[e] = 0.0f;
+    where[e] = -1;
+    if (at < values) {
+      int lo = 0, hi = t.tensors - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (ends[mid] > at) hi = mid;
+        else lo = mid + 1;
+      }
+      const int64_t i = at - (lo ? ends[lo - 1] : 0);
+      v[e] = t.f32[lo] ? static_cast<const float*>(ins[lo])[i] : to_f32(static_cast<const __nv_bfloat16*>(ins[lo])[i]);
+      where[e] = lo;
+    }
+  }
+  // in f32 over a warp, then f64; all in f64 where the squares leave f32 or lose bits (the card's f64 is slow)
+  float sum32 = 0.0f, most = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kFewEach; ++e) {
+    sum32 = fmaf(v[e], v[e], sum32);
+    most = fmaxf(most, fabsf(v[e]));
+  }
+  double sum;
+  if (__all_sync(~0u, most == 0.0f || !(most < INFINITY) || (most > 1e-15f && most < 1e17f))) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum32 += __shfl_xor_sync(~0u, sum32, o);
+    sum = static_cast<double>(sum32);
+  } else {
+    sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < kFewEach; ++e) sum += static_cast<double>(v[e]) * v[e];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  }
+  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x < kCluster) {  // this block's sum to every block of the cluster
+    sum = 0.0;
+    for (int w = 0; w < kFewThreads / 32; ++w) sum += shared[w];
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(&sums[blockIdx.x])), "r"(threadIdx.x));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(sum) : "memory");
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  double all = 0.0;
+#pragma unroll
+  for (int b = 0; b < kCluster; ++b) all += sums[b];
+  const float n = static_cast<float>(sqrt(all));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  if (!scale) return;
+  const float f = scale_of(n, max_norm);
+#pragma unroll
+  for (int e = 0; e < kFewEach; ++e) {
+    if (where[e] < 0) continue;
+    const int lo = where[e];
+    const int at = (e * kCluster + static_cast<int>(blockIdx.x)) * kFewThreads + static_cast<int>(threadIdx.x);
+    const int64_t i = at - (lo ? ends[lo - 1] : 0);
+    if (t.f32[lo]) static_cast<float*>(t.out[lo])[i] = v[e] * f;
+    else static_cast<__nv_bfloat16*>(t.out[lo])[i] = from_f32<__nv_bfloat16>(v[e] * f);
   }
 }
 
@@ -166,30 +324,72 @@ NormScratch take_norm(Scratch& sc) {
   NormScratch s;
   s.part = sc.take<double>(kMaxBlocks);
   s.carry = sc.take<double>(1);
-  s.ticket = sc.take<unsigned>(1);
   s.scale = sc.take<float>(1);
+  s.ticket = nullptr;
   return s;
 }
 
 // Fills the next launch's table from tensor `from` on; returns the tensor after its last.
-int64_t fill_table(TensorTable* t, const ClipTensor* list, int64_t num, int64_t from) {
+template <int N>
+int64_t fill_table(TensorTable<N>* t, const ClipTensor* list, int64_t num, int64_t from) {
   t->tensors = 0;
-  uint64_t chunks = 0;
-  int64_t i = from;
-  for (; i < num && t->tensors < kTable; ++i) {
-    const uint64_t c = static_cast<uint64_t>((list[i].count + kChunk - 1) / kChunk);
-    if (!c) continue;
-    if (chunks + c > 0xffffffffull) break;
+  int64_t values = 0, i = from;
+  for (; i < num && t->tensors < N; ++i) {
+    if (!list[i].count) continue;
     const int k = t->tensors++;
+    values += list[i].count;
     t->in[k] = list[i].in;
     t->out[k] = list[i].out;
-    t->count[k] = list[i].count;
+    t->end[k] = values;
     t->f32[k] = list[i].dtype == kF32;
-    t->first[k] = static_cast<uint32_t>(chunks);
-    chunks += c;
   }
-  t->first[t->tensors] = static_cast<uint32_t>(chunks);
   return i;
+}
+// Blocks for the table's chunks: as many as fit at once.
+template <int N>
+unsigned cut_chunks(TensorTable<N>* t, int64_t most) {
+  const int64_t values = t->tensors ? t->end[t->tensors - 1] : 0;
+  t->chunk = kThreads * kAhead * 8;
+  const int64_t blocks = (values + t->chunk - 1) / t->chunk;
+  return static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most);
+}
+
+template <int N>
+cudaError_t launch_many(const ClipTensor* list, int64_t num, bool scale, float max_norm, float* norm, const NormScratch& s,
+                        cudaStream_t st) {
+  // as many blocks as fit at once, so that they end near the same time
+  static int each = 0;
+  if (!each) {
+    int a = 0, b = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a, squares_kernel<N>, kThreads, 0);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, scale_kernel<N>, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    a = a < b ? a : b;
+    each = a < 1 ? 1 : a;
+  }
+  const int64_t fit = int64_t(each) * ops_sm_count(), most = fit < kMaxBlocks ? fit : kMaxBlocks;
+  TensorTable<N> t;
+  int64_t at = 0;
+  bool first = true;
+  int launches = 0;
+  do {
+    ++launches;
+    at = fill_table(&t, list, num, at);
+    const cudaError_t e = launch_after(squares_kernel<N>, cut_chunks(&t, most), kThreads, 0, st, t, s, first, at >= num, max_norm, norm);
+    if (e != cudaSuccess) return e;
+    first = false;
+  } while (at < num);
+  if (!scale) return cudaSuccess;
+  at = 0;
+  do {
+    if (launches > 1) at = fill_table(&t, list, num, at);
+    if (t.tensors) {
+      const unsigned blocks = cut_chunks(&t, most);
+      const cudaError_t e = launch_after(scale_kernel<N>, blocks, kThreads, 0, st, t, static_cast<const float*>(s.scale));
+      if (e != cudaSuccess) return e;
+    }
+  } while (launches > 1 && at < num);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -200,31 +400,22 @@ size_t clip_scratch_bytes() {
   return sc.used();
 }
 
-cudaError_t launch_clip(const ClipTensor* list, int64_t num, bool scale, float max_norm, float* norm, Scratch& sc,
+cudaError_t launch_clip(const ClipTensor* list, int64_t num, bool scale, float max_norm, float* norm, int* words, Scratch& sc,
                         cudaStream_t st) {
-  const NormScratch s = take_norm(sc);
-  cudaError_t e = cudaMemsetAsync(s.ticket, 0, sizeof(unsigned), st);
-  if (e != cudaSuccess) return e;
-  const int most = 4 * ops_sm_count() < kMaxBlocks ? 4 * ops_sm_count() : kMaxBlocks;
-  TensorTable t;
-  int64_t at = 0;
-  bool first = true;
-  do {
-    const int64_t next = fill_table(&t, list, num, at);
-    const uint32_t chunks = t.first[t.tensors];
-    const unsigned grid = chunks < 1 ? 1u : (chunks < static_cast<uint32_t>(most) ? chunks : static_cast<unsigned>(most));
-    squares_kernel<<<grid, kThreads, 0, st>>>(t, s, first, next >= num, max_norm, norm);
-    first = false;
-    if (next == at && next < num) return cudaErrorInvalidValue;
-    at = next;
-  } while (at < num);
-  for (at = 0; scale && at < num;) {
-    at = fill_table(&t, list, num, at);
-    const uint32_t chunks = t.first[t.tensors];
-    if (!chunks) continue;
-    scale_kernel<<<chunks < static_cast<uint32_t>(most) ? chunks : static_cast<unsigned>(most), kThreads, 0, st>>>(t, s.scale);
+  NormScratch s = take_norm(sc);
+  s.ticket = reinterpret_cast<unsigned*>(words) + 32;
+  int64_t values = 0, tensors = 0;
+  for (int64_t i = 0; i < num; ++i) {
+    values += list[i].count;
+    tensors += list[i].count > 0;
   }
-  return cudaGetLastError();
+  if (tensors <= kFewTensors && values <= kFewValues) {
+    TensorTable<kFewTensors> t;
+    fill_table(&t, list, num, 0);
+    return launch_after(clip_few_kernel, unsigned(kCluster), kFewThreads, 0, st, t, scale, max_norm, norm);
+  }
+  return tensors <= kFewTensors ? launch_many<kFewTensors>(list, num, scale, max_norm, norm, s, st)
+                                : launch_many<kTable>(list, num, scale, max_norm, norm, s, st);
 }
 
 }  // namespace tk

@@ -6,11 +6,11 @@
 // are grouped first: each place takes a rank in its group by an atomic
 // counter, groups take their bases from one running total, and the places are
 // written to their slots.  Ranks and bases differ from run to run; the order
-// in which a group is summed does not: its places are put in order of s where
-// they are summed (a group of at most kPiece), or by a bitmap of s over the
-// whole selection (a longer group, one block each).  A longer group is summed
-// in pieces of kPiece places, and the piece that ends last adds the pieces up
-// in their order.  So results do not depend on the order of the atomics.
+// in which a group is summed does not: a short group's places are put in
+// order of s where they are summed, a long group's by a block of its own
+// before that.  A long group is summed in pieces, and the piece that ends last
+// (by a ticket) adds the pieces up in their order.  So results do not depend
+// on the order of the atomics, and nothing waits for another block.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -19,54 +19,70 @@
 namespace tk {
 namespace {
 
-constexpr int kPiece = 64;       // places summed by one warp or block at a time
-constexpr int kBaseThreads = 256;
-constexpr int kSortThreads = 512;
-constexpr int64_t kBitmapBits = int64_t(1) << 20;  // places one bitmap of the sort covers (128 KB)
+constexpr int kRowPiece = 64, kColPiece = 32;  // places summed at a time; a group with more is long
+constexpr int kThreads = 256, kSortThreads = 512;
+constexpr int kSpan = 8;                       // groups next to each other that may share a task
+constexpr int kGroupsBlock = 256;              // groups of one block of the base kernel: their places lie together
+constexpr int kSortSmall = 512;               // places of a long group ordered by counting smaller ones
+constexpr int64_t kBitmapBits = int64_t(1) << 18;  // places that one bitmap of a longer group covers (with its counts 64 KB)
 constexpr uint32_t kNoPlace = 0xffffffffu;
 
 struct GroupHeader {
   unsigned total;   // places that lie in range
   unsigned pieces;  // pieces of long groups
   unsigned longs;   // long groups
+  unsigned tasks;   // warps' tasks of the sums by column
 };
 struct PieceRec {
   unsigned group, index, slot0, count;  // piece `index` of a group whose first slot is slot0; the group's places
+};
+// A grouped place.
+struct __align__(16) Entry {
+  uint32_t s, other;  // the place and its other coordinate
+  float coef;
+  uint32_t group;
+};
+// Columns [c0, c0 + columns) that one warp sums: none of them long, their
+// places, at most kColPiece, next to each other from `start` on.
+struct __align__(16) Task {
+  unsigned c0, columns, start, places;
 };
 // Groups of one call, in its scratch.
 struct Groups {
   GroupHeader* hdr;
   unsigned* count;    // per group
-  unsigned* ticket;   // per piece slot: pieces of the group that are done (counted at its first slot)
   unsigned* start;    // per group
-  uint32_t* rank;     // per place: its rank in its group as counted, or kNoPlace
-  uint2* order;       // grouped places (s, other coordinate)
-  uint2* sorted;      // long groups: the same in order of s
+  uint4* seen;        // per place: group, other coordinate, rank in the group as counted (kNoPlace: none), coefficient
+  Entry* order;       // the places by group
+  Entry* sorted;      // long groups in order of s
   PieceRec* pieces;
-  unsigned* longs;    // long groups
+  Task* tasks;        // sums by column (else null)
+  unsigned* longs;
+  unsigned* ticket;   // pieces of a long group (and tile of d) that are done, counted at its first slot; zero at first
   float* part;        // pieces x d sums
   float* part_bias;   // pieces sums of coefficients
-  int64_t zero_bytes; // hdr, count and ticket lie together and start at zero
-  int64_t n_groups, max_pieces, max_longs;
+  int64_t n_groups, max_pieces, max_longs, max_tasks, n_tickets;
 };
 
-Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int64_t d, bool bias) {
+Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int piece, int64_t d, int64_t d_tiles, bool bias, bool tasks) {
   Groups g{};
   g.n_groups = groups;
-  // a group in pieces has more than kPiece places, so at most 2 x places / kPiece pieces
-  g.max_longs = total / (kPiece + 1);
-  g.max_pieces = g.max_longs ? 2 * (total / kPiece) : 0;
-  const size_t z0 = sc.used();
+  // a long group has more than `piece` places, so at most 2 x places / piece pieces
+  g.max_longs = total / (piece + 1);
+  g.max_pieces = g.max_longs ? 2 * (total / piece) : 0;
+  g.n_tickets = g.max_pieces * d_tiles;
   g.hdr = sc.take<GroupHeader>(1);
   g.count = sc.take<unsigned>(groups);
-  g.ticket = sc.take<unsigned>(g.max_pieces);
-  g.zero_bytes = static_cast<int64_t>(sc.used() - z0);
   g.start = sc.take<unsigned>(groups);
-  g.rank = sc.take<uint32_t>(total);
-  g.order = sc.take<uint2>(total);
-  g.sorted = sc.take<uint2>(g.max_longs ? total : 0);
+  g.seen = sc.take<uint4>(total);
+  g.order = sc.take<Entry>(total);
+  g.sorted = sc.take<Entry>(g.max_longs ? total : 0);
   g.pieces = sc.take<PieceRec>(g.max_pieces);
+  // a span of groups that share no task has more than `piece` places
+  g.max_tasks = tasks ? (groups + kSpan - 1) / kSpan + (kSpan - 1) * (total / piece) : 0;
+  g.tasks = tasks ? sc.take<Task>(g.max_tasks) : nullptr;
   g.longs = sc.take<unsigned>(g.max_longs);
+  g.ticket = sc.take<unsigned>(g.n_tickets);
   g.part = sc.take<float>(g.max_pieces * d);
   g.part_bias = sc.take<float>(bias ? g.max_pieces : 0);
   return g;
@@ -76,11 +92,17 @@ Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int64_t d, bool b
 __device__ __forceinline__ bool locate(const Places& p, int64_t s, uint32_t* row, uint32_t* col) {
   const int64_t v = p.idx[s];
   if (p.per_row) {
-    *row = static_cast<uint32_t>(s / p.count);
+    *row = static_cast<uint32_t>(s) / static_cast<uint32_t>(p.count);
     *col = static_cast<uint32_t>(v);
     return v >= 0 && v < p.n;
   }
   if (v < 0) return false;
+  if (v <= 0xffffffffll) {
+    const uint32_t r = static_cast<uint32_t>(v) / static_cast<uint32_t>(p.n);
+    *row = r;
+    *col = static_cast<uint32_t>(v) - r * static_cast<uint32_t>(p.n);
+    return r < p.rows;
+  }
   const int64_t r = v / p.n;
   *row = static_cast<uint32_t>(r);
   *col = static_cast<uint32_t>(v - r * p.n);
@@ -96,165 +118,203 @@ __device__ __forceinline__ float coef_of(const Coef& c, int64_t s) {
 }
 
 // ---- grouping -----------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) zero_groups_kernel(const Groups g) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (i == 0) *g.hdr = GroupHeader{0, 0, 0, 0};
+  if (i < g.n_groups) g.count[i] = 0;
+  if (i < g.n_tickets) g.ticket[i] = 0;
+}
+
 template <bool BY_ROW, typename T>
-__global__ void count_places_kernel(const Places p, const Groups g, T* dots) {
-  const int64_t s = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+__global__ void __launch_bounds__(kThreads) count_places_kernel(const Places p, const Coef c, const Groups g, T* dots) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t s = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (s >= p.total) return;
   uint32_t row, col;
-  if (!locate(p, s, &row, &col)) {
-    g.rank[s] = kNoPlace;
+  const bool in = locate(p, s, &row, &col);
+  const float coef = coef_of<T>(c, s);
+  if (!in) {
+    g.seen[s] = make_uint4(0, 0, kNoPlace, 0);
     if (dots) dots[s] = from_f32<T>(0.0f);
     return;
   }
-  g.rank[s] = atomicAdd(&g.count[BY_ROW ? row : col], 1u);
+  const uint32_t group = BY_ROW ? row : col;
+  const uint32_t rank = atomicAdd(&g.count[group], 1u);
+  g.seen[s] = make_uint4(group, BY_ROW ? col : row, rank, __float_as_uint(coef));
 }
 
-// A base for every group, from a scan over the block's groups and one atomic
-// on the running total; the pieces and the list of long groups likewise.
-__global__ void __launch_bounds__(kBaseThreads) group_base_kernel(const Groups g) {
-  __shared__ unsigned warp_sum[kBaseThreads / 32];
-  __shared__ unsigned block_base;
-  const int64_t i = int64_t(blockIdx.x) * kBaseThreads + threadIdx.x;
-  const unsigned cnt = i < g.n_groups ? g.count[i] : 0u;
-  unsigned incl = cnt;
+// Inclusive sum over the block's threads; *total: of all.  (Two barriers.)
+template <int THREADS>
+__device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* total) {
+  __shared__ unsigned warp_sum[THREADS / 32];
+  unsigned incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned t = __shfl_up_sync(~0u, incl, o);
     if (static_cast<int>(threadIdx.x % 32) >= o) incl += t;
   }
+  __syncthreads();
   if (threadIdx.x % 32 == 31) warp_sum[threadIdx.x / 32] = incl;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    unsigned t = 0;
-    for (int w = 0; w < kBaseThreads / 32; ++w) {
-      const unsigned v = warp_sum[w];
-      warp_sum[w] = t;
-      t += v;
-    }
-    block_base = t ? atomicAdd(&g.hdr->total, t) : 0u;
+  unsigned before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const unsigned t = warp_sum[w];
+    if (w < static_cast<int>(threadIdx.x / 32)) before += t;
+    all += t;
   }
+  *total = all;
+  return before + incl;
+}
+
+// A base for every group, from a scan over the block's groups and one atomic
+// on the running total; the pieces and the list of long groups likewise.
+__global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g, unsigned piece) {
+  __shared__ unsigned block_base;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t i = int64_t(blockIdx.x) * kGroupsBlock + threadIdx.x;
+  const unsigned cnt = i < g.n_groups ? g.count[i] : 0u;
+  unsigned total;
+  const unsigned incl = block_scan<kGroupsBlock>(cnt, &total);
+  if (threadIdx.x == 0) block_base = total ? atomicAdd(&g.hdr->total, total) : 0u;
   __syncthreads();
+  const unsigned start = block_base + incl - cnt;
+  if (g.tasks) {
+    // as many groups next to each other (8, 4, 2 or 1, aligned) as hold at most `piece` places
+    const int lane = threadIdx.x % 32;
+    const unsigned s2 = cnt + __shfl_xor_sync(~0u, cnt, 1), s4 = s2 + __shfl_xor_sync(~0u, s2, 2);
+    const unsigned s8 = s4 + __shfl_xor_sync(~0u, s4, 4);
+    unsigned size = 1, places = cnt;
+    if (s8 <= piece) size = 8, places = s8;
+    else if (s4 <= piece) size = 4, places = s4;
+    else if (s2 <= piece) size = 2, places = s2;
+    const bool leads = lane % size == 0 && places <= piece && i < g.n_groups;
+    const unsigned who = __ballot_sync(~0u, leads);
+    unsigned slot = 0;
+    if (lane == 0 && who) slot = atomicAdd(&g.hdr->tasks, static_cast<unsigned>(__popc(who)));
+    slot = __shfl_sync(~0u, slot, 0) + __popc(who & lanemask_lt());
+    if (leads)
+      g.tasks[slot] = Task{static_cast<unsigned>(i), static_cast<unsigned>(min(int64_t(size), g.n_groups - i)), start, places};
+  }
   if (i >= g.n_groups) return;
-  g.start[i] = block_base + warp_sum[threadIdx.x / 32] + incl - cnt;
-  if (cnt > kPiece) {
-    const unsigned np = (cnt + kPiece - 1) / kPiece;
+  g.start[i] = start;
+  if (cnt > piece) {
+    const unsigned np = (cnt + piece - 1) / piece;
     const unsigned slot0 = atomicAdd(&g.hdr->pieces, np);
     for (unsigned q = 0; q < np; ++q) g.pieces[slot0 + q] = PieceRec{static_cast<unsigned>(i), q, slot0, cnt};
     g.longs[atomicAdd(&g.hdr->longs, 1u)] = static_cast<unsigned>(i);
   }
 }
 
-template <bool BY_ROW>
-__global__ void place_kernel(const Places p, const Groups g) {
-  const int64_t s = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (s >= p.total) return;
-  const uint32_t rank = g.rank[s];
-  if (rank == kNoPlace) return;
-  uint32_t row, col;
-  locate(p, s, &row, &col);
-  g.order[g.start[BY_ROW ? row : col] + rank] = make_uint2(static_cast<uint32_t>(s), BY_ROW ? col : row);
+__global__ void __launch_bounds__(kThreads) place_kernel(const Groups g, int64_t total) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t s = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (s >= total) return;
+  const uint4 v = g.seen[s];
+  if (v.z == kNoPlace) return;
+  g.order[g.start[v.x] + v.z] = Entry{static_cast<uint32_t>(s), v.y, __uint_as_float(v.w), v.x};
 }
 
-// Long groups in order of s: a bitmap of the places, kBitmapBits at a time;
-// each set bit's rank is the number of bits before it.
-template <bool BY_ROW>
-__global__ void __launch_bounds__(kSortThreads) sort_long_kernel(const Places p, const Groups g, int64_t words) {
-  extern __shared__ uint32_t bitmap[];
-  __shared__ unsigned warp_sum[kSortThreads / 32];
-  __shared__ unsigned window_total;
-  for (unsigned l = blockIdx.x; l < g.hdr->longs; l += gridDim.x) {
+// Long groups in order of s, a block each: the rank of a place is the number
+// of smaller s in its group, counted directly for up to kSortSmall places and
+// by a bitmap of s, kBitmapBits at a time, beyond.
+__global__ void __launch_bounds__(kSortThreads) sort_long_kernel(const Groups g, int64_t total, int words) {
+  extern __shared__ uint32_t sort_smem[];
+  uint32_t* bitmap = sort_smem;
+  uint32_t* before = sort_smem + words;  // set bits before each word
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const unsigned n_long = g.hdr->longs;
+  for (unsigned l = blockIdx.x; l < n_long; l += gridDim.x) {
     const unsigned group = g.longs[l];
-    const unsigned cnt = g.count[group], start = g.start[group];
-    unsigned done = 0;
-    for (int64_t s0 = 0; s0 < p.total && done < cnt; s0 += words * 32) {
-      for (int64_t i = threadIdx.x; i < words; i += kSortThreads) bitmap[i] = 0;
-      __syncthreads();
-      for (unsigned i = threadIdx.x; i < cnt; i += kSortThreads) {
-        const int64_t at = int64_t(g.order[start + i].x) - s0;
-        if (at >= 0 && at < words * 32) atomicOr(&bitmap[at >> 5], 1u << (at & 31));
-      }
-      __syncthreads();
-      // each thread's words, in a run; the bits before it by a scan over the block
-      const int64_t run = (words + kSortThreads - 1) / kSortThreads;
-      const int64_t w0 = threadIdx.x * run, w1 = min(words, w0 + run);
-      unsigned mine = 0;
-      for (int64_t w = w0; w < w1; ++w) mine += __popc(bitmap[w]);
-      unsigned incl = mine;
+    const int cnt = static_cast<int>(g.count[group]);
+    const Entry* src = g.order + g.start[group];
+    Entry* dst = g.sorted + g.start[group];
+    if (cnt <= kSortSmall) {
+      constexpr int kEach = kSortSmall / kSortThreads;
+      Entry e[kEach];
+      int rank[kEach] = {};
+      for (int i = threadIdx.x; i < (cnt + 3) / 4 * 4; i += kSortThreads) sort_smem[i] = i < cnt ? src[i].s : kNoPlace;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned t = __shfl_up_sync(~0u, incl, o);
-        if (static_cast<int>(threadIdx.x % 32) >= o) incl += t;
-      }
-      if (threadIdx.x % 32 == 31) warp_sum[threadIdx.x / 32] = incl;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        unsigned t = 0;
-        for (int w = 0; w < kSortThreads / 32; ++w) {
-          const unsigned v = warp_sum[w];
-          warp_sum[w] = t;
-          t += v;
-        }
-        window_total = t;
+      for (int q = 0; q < kEach; ++q) {
+        const int i = q * kSortThreads + threadIdx.x;
+        if (i < cnt) e[q] = src[i];
+        else e[q].s = 0;
       }
       __syncthreads();
-      unsigned at = start + done + warp_sum[threadIdx.x / 32] + incl - mine;
-      for (int64_t w = w0; w < w1; ++w) {
-        for (uint32_t b = bitmap[w]; b; b &= b - 1) {
-          const int64_t s = s0 + w * 32 + (__ffs(b) - 1);
-          uint32_t row, col;
-          locate(p, s, &row, &col);
-          g.sorted[at++] = make_uint2(static_cast<uint32_t>(s), BY_ROW ? col : row);
-        }
+      for (int j = 0; j < cnt; j += 4) {
+        const uint4 t = *reinterpret_cast<const uint4*>(sort_smem + j);
+#pragma unroll
+        for (int q = 0; q < kEach; ++q)
+          rank[q] += (t.x < e[q].s) + (t.y < e[q].s) + (t.z < e[q].s) + (t.w < e[q].s);
       }
-      done += window_total;
+#pragma unroll
+      for (int q = 0; q < kEach; ++q)
+        if (q * kSortThreads + static_cast<int>(threadIdx.x) < cnt) dst[rank[q]] = e[q];
+      __syncthreads();
+      continue;
+    }
+    unsigned done = 0;
+    for (int64_t s0 = 0; s0 < total && done < static_cast<unsigned>(cnt); s0 += int64_t(words) * 32) {
+      for (int i = threadIdx.x; i < words; i += kSortThreads) bitmap[i] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < cnt; i += kSortThreads) {
+        const int64_t at = int64_t(src[i].s) - s0;
+        if (at >= 0 && at < int64_t(words) * 32) atomicOr(&bitmap[at >> 5], 1u << (at & 31));
+      }
+      __syncthreads();
+      // a thread's words in a run; the bits before it by a scan over the block
+      const int run = (words + kSortThreads - 1) / kSortThreads;
+      const int w0 = min(words, static_cast<int>(threadIdx.x) * run), w1 = min(words, w0 + run);
+      unsigned bits = 0, held;
+      for (int w = w0; w < w1; ++w) bits += __popc(bitmap[w]);
+      unsigned at0 = block_scan<kSortThreads>(bits, &held) - bits;
+      for (int w = w0; w < w1; ++w) {
+        before[w] = at0;
+        at0 += __popc(bitmap[w]);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < cnt; i += kSortThreads) {
+        const Entry e = src[i];
+        const int64_t at = int64_t(e.s) - s0;
+        if (at >= 0 && at < int64_t(words) * 32)
+          dst[done + before[at >> 5] + __popc(bitmap[at >> 5] & ((1u << (at & 31)) - 1u))] = e;
+      }
+      done += held;
       __syncthreads();
     }
   }
 }
 
 template <bool BY_ROW, typename T>
-cudaError_t launch_grouping(const Places& p, const Groups& g, T* dots, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(g.hdr, 0, static_cast<size_t>(g.zero_bytes), st);
+cudaError_t launch_grouping(const Places& p, const Coef& c, const Groups& g, T* dots, cudaStream_t st) {
+  const int64_t zero = g.n_groups > g.n_tickets ? g.n_groups : g.n_tickets;
+  cudaError_t e = launch_after(zero_groups_kernel, static_cast<unsigned>((zero + kThreads - 1) / kThreads), kThreads, 0, st, g);
+  const unsigned blocks = static_cast<unsigned>((p.total + kThreads - 1) / kThreads);
+  if (e == cudaSuccess && blocks) e = launch_after(count_places_kernel<BY_ROW, T>, blocks, kThreads, 0, st, p, c, g, dots);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>((p.total + 255) / 256);
-  if (!blocks) return cudaSuccess;  // every group is empty
-  count_places_kernel<BY_ROW, T><<<blocks, 256, 0, st>>>(p, g, dots);
-  group_base_kernel<<<static_cast<unsigned>((g.n_groups + kBaseThreads - 1) / kBaseThreads), kBaseThreads, 0, st>>>(g);
-  place_kernel<BY_ROW><<<blocks, 256, 0, st>>>(p, g);
-  if (g.max_longs) {
-    const int64_t bits = p.total < kBitmapBits ? p.total : kBitmapBits;
-    const int64_t words = (bits + 31) / 32;
-    e = cudaFuncSetAttribute(sort_long_kernel<BY_ROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kBitmapBits / 8));
-    if (e != cudaSuccess) return e;
-    const int64_t most = 4 * ops_sm_count();
-    const unsigned grid = static_cast<unsigned>(g.max_longs < most ? g.max_longs : most);
-    sort_long_kernel<BY_ROW><<<grid, kSortThreads, static_cast<size_t>(words) * 4, st>>>(p, g, words);
-  }
-  return cudaGetLastError();
+  e = launch_after(group_base_kernel, static_cast<unsigned>((g.n_groups + kGroupsBlock - 1) / kGroupsBlock), kGroupsBlock, 0, st,
+                   g, static_cast<unsigned>(BY_ROW ? kRowPiece : kColPiece));
+  if (e != cudaSuccess || !blocks) return e;  // (no places: every group is empty)
+  e = launch_after(place_kernel, blocks, kThreads, 0, st, g, p.total);
+  if (e != cudaSuccess || !g.max_longs) return e;
+  const int64_t bits = p.total < kBitmapBits ? p.total : kBitmapBits;
+  int words = static_cast<int>((bits + 31) / 32);
+  if (words < kSortSmall) words = kSortSmall;
+  e = cudaFuncSetAttribute(sort_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBitmapBits / 4));
+  if (e != cudaSuccess) return e;
+  const int64_t most = 3 * ops_sm_count();
+  return launch_after(sort_long_kernel, static_cast<unsigned>(g.max_longs < most ? g.max_longs : most), kSortThreads,
+                      static_cast<size_t>(words) * 8, st, g, p.total, words);
 }
-
-// The places [first, first + cnt) of a group in order of s: entry i of out.
-// `threads` threads of which this is `t`; the caller synchronises after it.
-__device__ __forceinline__ void order_short(const uint2* src, int cnt, uint2* raw, int t, int threads) {
-  for (int i = t; i < cnt; i += threads) raw[i] = src[i];
-}
-__device__ __forceinline__ int rank_short(const uint2* raw, int cnt, int i) {
-  const uint32_t s = raw[i].x;
-  int rank = 0;
-  for (int j = 0; j < cnt; ++j) rank += raw[j].x < s;
-  return rank;
-}
-
-struct Entry {
-  uint32_t other;
-  float coef;
-};
 
 // ---- sums by row ------------------------------------------------------------------
-// A block takes one piece of a row: kRowTx threads across d (VEC values each),
-// kRowTy places at a time, whose sums are added in shared memory in order.
-constexpr int kRowTx = 64, kRowTy = 4, kRowThreads = kRowTx * kRowTy;
+constexpr int kRowAhead = 8;
 
 struct RowParams {
   RowSums r;
@@ -263,16 +323,154 @@ struct RowParams {
   int64_t d_tiles;
 };
 
+// Many rows: a warp takes one piece of a row and one tile of 32 x VEC values,
+// places in order one after the other, kRowAhead of them in flight.
+constexpr int kRowWarps = 4;
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kRowThreads) row_sums_kernel(const RowParams q) {
-  __shared__ uint2 raw[kPiece];
-  __shared__ Entry ent[kPiece];
-  __shared__ float sums[kRowTy - 1][kRowTx * VEC];
+__global__ void __launch_bounds__(kRowWarps * 32) row_sums_warp_kernel(const RowParams q) {
+  __shared__ Entry raw_all[kRowWarps][kRowPiece];
+  __shared__ uint2 ent_all[kRowWarps][kRowPiece + kRowAhead];  // other coordinate, coefficient
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const RowSums& r = q.r;
+  const Places& p = r.places;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  Entry* raw = raw_all[warp];
+  uint2* ent = ent_all[warp];
+  const int64_t wk = int64_t(blockIdx.x) * kRowWarps + warp;
+  const int64_t w = wk / q.d_tiles, tile = wk - w * q.d_tiles;
+  int64_t row;
+  unsigned n_pieces = 1, index = 0, slot0 = 0;
+  int cnt = 0;
+  if (p.per_row) {
+    row = w / q.pieces_per_row;
+    if (row >= p.rows) return;
+    index = static_cast<unsigned>(w - row * q.pieces_per_row);
+    n_pieces = static_cast<unsigned>(q.pieces_per_row);
+    slot0 = static_cast<unsigned>(row * q.pieces_per_row);
+    const int64_t at = int64_t(index) * kRowPiece;
+    const int listed = static_cast<int>(min(int64_t(kRowPiece), p.count - at));
+    for (int i0 = 0; i0 < listed; i0 += 32) {  // positions out of range are left out
+      const int64_t s = row * p.count + at + i0 + lane;
+      int64_t c = -1;
+      float f = 0.0f;
+      if (i0 + lane < listed) {
+        c = p.idx[s];
+        f = coef_of<T>(r.coef, s);
+      }
+      const bool held = c >= 0 && c < p.n;
+      const unsigned who = __ballot_sync(~0u, held);
+      if (held) ent[cnt + __popc(who & lanemask_lt())] = make_uint2(static_cast<uint32_t>(c), __float_as_uint(f));
+      cnt += __popc(who);
+    }
+  } else if (w < p.rows) {
+    row = w;
+    const unsigned c = q.g.count[row];
+    const unsigned start = q.g.start[row];
+    if (c > kRowPiece) return;
+    cnt = static_cast<int>(c);
+    Entry e[2];
+    int rank[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k * 32 + lane < cnt) raw[k * 32 + lane] = e[k] = q.g.order[start + k * 32 + lane];
+    __syncwarp();
+    for (int j = 0; j < cnt; ++j) {
+      const uint32_t s = raw[j].s;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) rank[k] += s < e[k].s;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k * 32 + lane < cnt) ent[rank[k]] = make_uint2(e[k].other, __float_as_uint(e[k].coef));
+  } else {
+    if (w - p.rows >= q.g.hdr->pieces) return;
+    const PieceRec rec = q.g.pieces[w - p.rows];
+    row = rec.group;
+    index = rec.index;
+    slot0 = rec.slot0;
+    n_pieces = (rec.count + kRowPiece - 1) / kRowPiece;
+    cnt = static_cast<int>(min(unsigned(kRowPiece), rec.count - index * kRowPiece));
+    for (int i = lane; i < cnt; i += 32) {
+      const Entry e = q.g.sorted[q.g.start[row] + index * kRowPiece + i];
+      ent[i] = make_uint2(e.other, __float_as_uint(e.coef));
+    }
+  }
+  __syncwarp();
+  const int64_t j = tile * (32 * VEC) + int64_t(lane) * VEC;
+  const bool in = j < r.d;
+  const T* wt = static_cast<const T*>(r.w) + j;
+  float acc[VEC] = {};
+  if (in) {
+    int i0 = 0;
+#pragma unroll 1
+    for (; i0 < cnt; i0 += kRowAhead) {
+      Raw<T, VEC> v[kRowAhead];
+#pragma unroll
+      for (int a = 0; a < kRowAhead; ++a)
+        if (i0 + a < cnt) v[a].load_nc(wt + int64_t(ent[i0 + a].x) * r.ldw);
+#pragma unroll
+      for (int a = 0; a < kRowAhead; ++a) {
+        if (i0 + a < cnt) {
+          Vec<T, VEC> u;
+          u.set_raw(v[a]);
+          const float f = __uint_as_float(ent[i0 + a].y);
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) acc[c] = fmaf(f, u.v[c], acc[c]);
+        }
+      }
+    }
+  }
+  if (n_pieces > 1) {
+    // this piece's sums, then the last piece of the row adds them all in order
+    if (in) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) q.g.part[int64_t(slot0 + index) * r.d + j + c] = acc[c];
+    }
+    __threadfence();
+    __syncwarp();
+    unsigned seen = 0;
+    if (lane == 0) seen = atomicAdd(&q.g.ticket[int64_t(slot0) * q.d_tiles + tile], 1u);
+    seen = __shfl_sync(~0u, seen, 0);
+    if (seen != n_pieces - 1) return;
+    __threadfence();
+    if (in) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) acc[c] = 0.0f;
+#pragma unroll 4
+      for (unsigned o = 0; o < n_pieces; ++o)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] += __ldcg(&q.g.part[int64_t(slot0 + o) * r.d + j + c]);
+    }
+  }
+  if (in) {
+    Vec<T, VEC> out;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) out.v[c] = 0.0f;
+    if (r.bias) out.load_nc(static_cast<const T*>(r.bias) + j);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) out.v[c] += acc[c];
+    out.store(static_cast<T*>(r.y) + row * r.d + j);
+  }
+}
+
+// Few rows: a block takes one piece of a row, kRowTx threads across d, the
+// others different places, whose sums are added in shared memory in order.
+constexpr int kRowTx = 16;
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) row_sums_kernel(const RowParams q) {
+  constexpr int TX = kRowTx;
+  constexpr int TY = kThreads / TX;
+  __shared__ Entry raw[kRowPiece];
+  __shared__ uint2 ent[kRowPiece];  // other coordinate, coefficient
+  __shared__ float sums[TY - 1][TX * VEC];
   __shared__ bool last;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const RowSums& r = q.r;
   const Places& p = r.places;
   const int64_t tile = blockIdx.x % q.d_tiles;
-  int64_t w = blockIdx.x / q.d_tiles;
+  const int64_t w = blockIdx.x / q.d_tiles;
   const int t = threadIdx.x;
   // which piece
   int64_t row;
@@ -283,13 +481,12 @@ __global__ void __launch_bounds__(kRowThreads) row_sums_kernel(const RowParams q
     index = static_cast<unsigned>(w % q.pieces_per_row);
     n_pieces = static_cast<unsigned>(q.pieces_per_row);
     slot0 = static_cast<unsigned>(row * q.pieces_per_row);
-    const int64_t at = int64_t(index) * kPiece;
-    cnt = static_cast<int>(min(int64_t(kPiece), p.count - at));
+    const int64_t at = int64_t(index) * kRowPiece;
+    cnt = static_cast<int>(min(int64_t(kRowPiece), p.count - at));
     if (t < cnt) {
       const int64_t s = row * p.count + at + t;
       const int64_t c = p.idx[s];
-      const bool ok = c >= 0 && c < p.n;
-      ent[t] = Entry{ok ? static_cast<uint32_t>(c) : kNoPlace, ok ? coef_of<T>(r.coef, s) : 0.0f};
+      ent[t] = make_uint2(c >= 0 && c < p.n ? static_cast<uint32_t>(c) : kNoPlace, __float_as_uint(coef_of<T>(r.coef, s)));
     }
   } else if (w < q.g.max_pieces) {
     if (w >= q.g.hdr->pieces) return;
@@ -297,36 +494,55 @@ __global__ void __launch_bounds__(kRowThreads) row_sums_kernel(const RowParams q
     row = rec.group;
     index = rec.index;
     slot0 = rec.slot0;
-    n_pieces = (rec.count + kPiece - 1) / kPiece;
-    cnt = static_cast<int>(min(unsigned(kPiece), rec.count - index * kPiece));
+    n_pieces = (rec.count + kRowPiece - 1) / kRowPiece;
+    cnt = static_cast<int>(min(unsigned(kRowPiece), rec.count - index * kRowPiece));
     if (t < cnt) {
-      const uint2 e = q.g.sorted[q.g.start[row] + index * kPiece + t];
-      ent[t] = Entry{e.y, coef_of<T>(r.coef, e.x)};
+      const Entry e = q.g.sorted[q.g.start[row] + index * kRowPiece + t];
+      ent[t] = make_uint2(e.other, __float_as_uint(e.coef));
     }
   } else {
     row = w - q.g.max_pieces;
     const unsigned c = q.g.count[row];
-    if (c > kPiece) return;
+    const unsigned start = q.g.start[row];
+    if (c > kRowPiece) return;
     cnt = static_cast<int>(c);
-    order_short(q.g.order + q.g.start[row], cnt, raw, t, kRowThreads);
+    Entry e;
+    if (t < cnt) raw[t] = e = q.g.order[start + t];
     __syncthreads();
-    if (t < cnt) ent[rank_short(raw, cnt, t)] = Entry{raw[t].y, coef_of<T>(r.coef, raw[t].x)};
+    if (t < cnt) {
+      int rank = 0;
+      for (int j = 0; j < cnt; ++j) rank += raw[j].s < e.s;
+      ent[rank] = make_uint2(e.other, __float_as_uint(e.coef));
+    }
   }
   __syncthreads();
-  const int tx = t % kRowTx, ty = t / kRowTx;
-  const int64_t j = tile * (kRowTx * VEC) + int64_t(tx) * VEC;
+  const int tx = t % TX, ty = t / TX;
+  const int64_t j = tile * (TX * VEC) + int64_t(tx) * VEC;
   const bool in = j < r.d;
   const T* wt = static_cast<const T*>(r.w) + j;
   float acc[VEC] = {};
   if (in) {
-#pragma unroll 4
-    for (int i = ty; i < cnt; i += kRowTy) {
-      const Entry e = ent[i];
-      if (e.other == kNoPlace) continue;
-      Vec<T, VEC> v;
-      v.load_nc(wt + int64_t(e.other) * r.ldw);
+    for (int i0 = ty; i0 < cnt; i0 += TY * kRowAhead) {
+      Raw<T, VEC> v[kRowAhead];
+      float f[kRowAhead];
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) acc[c] = fmaf(e.coef, v.v[c], acc[c]);
+      for (int a = 0; a < kRowAhead; ++a) {
+        f[a] = 0.0f;
+        v[a].clear();
+        const int i = i0 + a * TY;
+        const uint2 e = i < cnt ? ent[i] : make_uint2(kNoPlace, 0u);
+        if (e.x != kNoPlace) {
+          v[a].load_nc(wt + int64_t(e.x) * r.ldw);
+          f[a] = __uint_as_float(e.y);
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kRowAhead; ++a) {
+        Vec<T, VEC> u;
+        u.set_raw(v[a]);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] = fmaf(f[a], u.v[c], acc[c]);
+      }
     }
   }
   if (ty > 0) {
@@ -336,7 +552,7 @@ __global__ void __launch_bounds__(kRowThreads) row_sums_kernel(const RowParams q
   __syncthreads();
   if (ty == 0) {
 #pragma unroll
-    for (int o = 0; o < kRowTy - 1; ++o)
+    for (int o = 0; o < TY - 1; ++o)
 #pragma unroll
       for (int c = 0; c < VEC; ++c) acc[c] += sums[o][tx * VEC + c];
   }
@@ -382,24 +598,43 @@ bool row_vectors(const RowSums& r) {
   constexpr int kVec = 16 / sizeof(T);
   return r.d % kVec == 0 && r.ldw % kVec == 0 && aligned16(r.w) && aligned16(r.y) && (!r.bias || aligned16(r.bias));
 }
+int row_vec(const RowSums& r) {
+  if (r.dtype == kF32) return row_vectors<float>(r) ? 4 : 1;
+  return row_vectors<__nv_bfloat16>(r) ? 8 : 1;
+}
+// A warp a piece and tile when that gives every SM eight warps, else a block each (64 places of one row of 512 values:
+// 12.6 us by one block's 64 threads across d, 4.8 us by four blocks' 16).
+bool many_rows(const RowSums& r) {
+  const int64_t wide = 32 * row_vec(r);
+  return r.places.rows * ((r.d + wide - 1) / wide) >= 8 * ops_sm_count();
+}
 
 RowParams plan_rows(const RowSums& r, Scratch& sc) {
   RowParams q{};
   q.r = r;
-  const int vec = (r.dtype == kF32 ? row_vectors<float>(r) : row_vectors<__nv_bfloat16>(r)) ? (r.dtype == kF32 ? 4 : 8) : 1;
-  q.d_tiles = (r.d + kRowTx * vec - 1) / (kRowTx * vec);
+  const int64_t wide = int64_t(many_rows(r) ? 32 : kRowTx) * row_vec(r);
+  q.d_tiles = (r.d + wide - 1) / wide;
   if (r.places.per_row) {
-    q.pieces_per_row = r.places.count > kPiece ? (r.places.count + kPiece - 1) / kPiece : 1;
+    q.pieces_per_row = r.places.count > kRowPiece ? (r.places.count + kRowPiece - 1) / kRowPiece : 1;
     if (q.pieces_per_row > 1) {
-      q.g.ticket = sc.take<unsigned>(r.places.rows * q.pieces_per_row * q.d_tiles);
+      q.g.n_tickets = r.places.rows * q.pieces_per_row * q.d_tiles;
+      q.g.hdr = sc.take<GroupHeader>(1);
+      q.g.ticket = sc.take<unsigned>(q.g.n_tickets);
       q.g.part = sc.take<float>(r.places.rows * q.pieces_per_row * r.d);
     }
   } else {
-    q.g = plan_groups(sc, r.places.total, r.places.rows, r.d, false);
-    // one ticket a slot and tile of d
-    q.g.ticket = sc.take<unsigned>(q.g.max_pieces * q.d_tiles);
+    q.g = plan_groups(sc, r.places.total, r.places.rows, kRowPiece, r.d, q.d_tiles, false, false);
   }
   return q;
+}
+
+template <typename T, int VEC>
+cudaError_t launch_rows_v(const RowParams& q, int64_t work, cudaStream_t st) {
+  const bool many = many_rows(q.r);
+  const int64_t grid = many ? (work + kRowWarps - 1) / kRowWarps : work;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  if (many) return launch_after(row_sums_warp_kernel<T, VEC>, static_cast<unsigned>(grid), kRowWarps * 32, 0, st, q);
+  return launch_after(row_sums_kernel<T, VEC>, static_cast<unsigned>(grid), kThreads, 0, st, q);
 }
 
 template <typename T>
@@ -411,202 +646,276 @@ cudaError_t launch_rows_t(const RowParams& q, cudaStream_t st) {
   if (r.places.per_row) {
     work = r.places.rows * q.pieces_per_row;
     if (q.pieces_per_row > 1)
-      e = cudaMemsetAsync(q.g.ticket, 0, sizeof(unsigned) * static_cast<size_t>(work * q.d_tiles), st);
+      e = launch_after(zero_groups_kernel, static_cast<unsigned>((q.g.n_tickets + kThreads - 1) / kThreads), kThreads, 0, st, q.g);
   } else {
     work = q.g.max_pieces + r.places.rows;
-    e = launch_grouping<true, T>(r.places, q.g, static_cast<T*>(nullptr), st);
-    if (e == cudaSuccess && q.g.max_pieces)
-      e = cudaMemsetAsync(q.g.ticket, 0, sizeof(unsigned) * static_cast<size_t>(q.g.max_pieces * q.d_tiles), st);
+    e = launch_grouping<true, T>(r.places, r.coef, q.g, static_cast<T*>(nullptr), st);
   }
   if (e != cudaSuccess) return e;
   work *= q.d_tiles;
-  if (work > INT32_MAX) return cudaErrorInvalidValue;
-  if (row_vectors<T>(r))
-    row_sums_kernel<T, kVec><<<static_cast<unsigned>(work), kRowThreads, 0, st>>>(q);
-  else
-    row_sums_kernel<T, 1><<<static_cast<unsigned>(work), kRowThreads, 0, st>>>(q);
-  return cudaGetLastError();
+  return row_vectors<T>(r) ? launch_rows_v<T, kVec>(q, work, st) : launch_rows_v<T, 1>(q, work, st);
 }
 
 // ---- sums by column ---------------------------------------------------------------
-// A warp takes one piece of a column and goes over d in tiles of 32 x VEC x
-// kColChunks values: the column's row of w in registers, the rows of x of its
-// places streamed past it, kColAhead places' loads in flight.
-constexpr int kColWarps = 4, kColChunks = 2, kColAhead = 4;
+// A warp takes pieces of long columns and tasks of short ones, whose places
+// (one a lane) it puts in order by column and s and streams through: the rows
+// of x (and of w, for the dots) of AHEAD places in flight, sums of 32 x VEC x
+// CHUNKS values in registers, written where the column ends.  Longer rows take
+// several such tiles one after the other.  FULL: every tile is whole.
+constexpr int kColWarps = 4, kColBlocks = 5;
 
 struct ColParams {
   ColumnSums c;
   Groups g;
 };
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kColWarps * 32) column_sums_kernel(const ColParams q) {
-  __shared__ uint2 raw_all[kColWarps][kPiece];
-  __shared__ Entry ent_all[kColWarps][kPiece];
-  __shared__ uint32_t place_all[kColWarps][kPiece];
-  __shared__ float dots_all[kColWarps][kPiece];
-  const ColumnSums& c = q.c;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  uint2* raw = raw_all[warp];
-  Entry* ent = ent_all[warp];
-  uint32_t* place = place_all[warp];
-  float* dots = dots_all[warp];
-  const int64_t wk = int64_t(blockIdx.x) * kColWarps + warp;
-  int64_t col;
-  unsigned n_pieces = 1, index = 0, slot0 = 0;
-  int cnt;
-  if (wk < q.g.max_pieces) {
-    if (wk >= q.g.hdr->pieces) return;
-    const PieceRec rec = q.g.pieces[wk];
-    col = rec.group;
-    index = rec.index;
-    slot0 = rec.slot0;
-    n_pieces = (rec.count + kPiece - 1) / kPiece;
-    cnt = static_cast<int>(min(unsigned(kPiece), rec.count - index * kPiece));
-    for (int i = lane; i < cnt; i += 32) {
-      const uint2 e = q.g.sorted[q.g.start[col] + index * kPiece + i];
-      ent[i] = Entry{e.y, coef_of<T>(c.coef, e.x)};
-      place[i] = e.x;
-    }
-  } else {
-    col = wk - q.g.max_pieces;
-    if (col >= q.g.n_groups) return;
-    const unsigned n = q.g.count[col];
-    if (n > kPiece) return;
-    cnt = static_cast<int>(n);
-    order_short(q.g.order + q.g.start[col], cnt, raw, lane, 32);
-    __syncwarp();
-    for (int i = lane; i < cnt; i += 32) {
-      const int k = rank_short(raw, cnt, i);
-      ent[k] = Entry{raw[i].y, coef_of<T>(c.coef, raw[i].x)};
-      place[k] = raw[i].x;
-    }
-  }
-  for (int i = lane; i < cnt; i += 32) dots[i] = 0.0f;
-  __syncwarp();
-  const T* x = static_cast<const T*>(c.x);
-  const T* w = static_cast<const T*>(c.w);
-  T* dw = static_cast<T*>(c.dw);
-  const bool want_dots = c.dots != nullptr, want_dw = c.dw != nullptr;
-  constexpr int kSpan = 32 * VEC * kColChunks;
-  for (int64_t d0 = 0; d0 < c.d && (want_dots || want_dw); d0 += kSpan) {
-    int64_t j[kColChunks];
-    bool in[kColChunks];
-    Vec<T, VEC> wv[kColChunks];
-    float acc[kColChunks][VEC] = {};
+template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL, bool DOTS>
+struct ColumnStream {
+  static constexpr int kTile = 32 * VEC * CHUNKS;
+  const ColumnSums& c;
+  const Entry* ent;
+  float* dots;
+  float* part;  // where a piece's sums go (null: to dw)
+  int lane, total;
+  bool want_dw;
+  int64_t d0;
+  float acc[CHUNKS][VEC];
+
+  __device__ __forceinline__ int64_t at(int h) const { return d0 + (h * 32 + lane) * VEC; }
+  __device__ __forceinline__ bool in(int h) const { return FULL || at(h) < c.d; }
+  // The sums so far are column `col`'s.
+  __device__ __forceinline__ void flush(int64_t col) {
 #pragma unroll
-    for (int e = 0; e < kColChunks; ++e) {
-      j[e] = d0 + (e * 32 + lane) * VEC;
-      in[e] = j[e] < c.d;
+    for (int h = 0; h < CHUNKS; ++h) {
+      if (in(h)) {
+        if (part) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) wv[e].v[v] = 0.0f;
-      if (want_dots && cnt && in[e]) wv[e].load_nc(w + col * c.ldw + j[e]);
-    }
-    for (int i0 = 0; i0 < cnt; i0 += kColAhead) {
-      Vec<T, VEC> xv[kColAhead][kColChunks];
-#pragma unroll
-      for (int a = 0; a < kColAhead; ++a) {
-        const bool have = i0 + a < cnt;
-        const T* xr = x + int64_t(have ? ent[i0 + a].other : 0) * c.ldx;
-#pragma unroll
-        for (int e = 0; e < kColChunks; ++e) {
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) xv[a][e].v[v] = 0.0f;
-          if (have && in[e]) xv[a][e].load_nc(xr + j[e]);
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < kColAhead; ++a) {
-        if (i0 + a >= cnt) break;
-        const float f = ent[i0 + a].coef;
-        float dot = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kColChunks; ++e)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            acc[e][v] = fmaf(f, xv[a][e].v[v], acc[e][v]);
-            dot = fmaf(xv[a][e].v[v], wv[e].v[v], dot);
-          }
-        if (want_dots) {
-#pragma unroll
-          for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-          if (lane == 0) dots[i0 + a] += dot;
-        }
-      }
-    }
-    if (want_dw) {
-#pragma unroll
-      for (int e = 0; e < kColChunks; ++e) {
-        if (!in[e]) continue;
-        if (n_pieces > 1) {
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) q.g.part[int64_t(slot0 + index) * c.d + j[e] + v] = acc[e][v];
+          for (int v = 0; v < VEC; ++v) part[at(h) + v] = acc[h][v];
         } else {
           Vec<T, VEC> out;
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) out.v[v] = acc[e][v];
-          out.store(dw + col * c.d + j[e]);
+          for (int v = 0; v < VEC; ++v) out.v[v] = acc[h][v];
+          out.store_stream(static_cast<T*>(c.dw) + col * c.d + at(h));
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[h][v] = 0.0f;
+    }
+  }
+  // Places [i0, i0 + n), n <= AHEAD (WHOLE: n == AHEAD).
+  template <bool WHOLE>
+  __device__ __forceinline__ void batch(int i0, int n) {
+    Raw<T, VEC> xv[AHEAD][CHUNKS], wv[AHEAD][DOTS ? CHUNKS : 1];
+    const T* x = static_cast<const T*>(c.x) + at(0);
+    const T* w = static_cast<const T*>(c.w) + at(0);
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      if (WHOLE || a < n) {
+        const Entry e = ent[i0 + a];
+        const T* xr = x + int64_t(e.other) * c.ldx;
+        const T* wr = w + int64_t(e.group) * c.ldw;
+#pragma unroll
+        for (int h = 0; h < CHUNKS; ++h) {
+          if (in(h)) {
+            xv[a][h].load_nc(xr + h * 32 * VEC);
+            if constexpr (DOTS) wv[a][h].load_nc(wr + h * 32 * VEC);
+          }
         }
       }
     }
-  }
-  __syncwarp();
-  if (want_dots)
-    for (int i = lane; i < cnt; i += 32) static_cast<T*>(c.dots)[place[i]] = from_f32<T>(dots[i]);
-  float sum = 0.0f;
-  if (c.dbias) {
-    for (int i = 0; i < cnt; ++i) sum += ent[i].coef;
-    if (n_pieces == 1 && lane == 0) static_cast<T*>(c.dbias)[col] = from_f32<T>(sum);
-  }
-  if (n_pieces == 1) return;
-  if (c.dbias && lane == 0) q.g.part_bias[slot0 + index] = sum;
-  __threadfence();
-  __syncwarp();
-  unsigned seen = 0;
-  if (lane == 0) seen = atomicAdd(&q.g.ticket[slot0], 1u);
-  seen = __shfl_sync(~0u, seen, 0);
-  if (seen != n_pieces - 1) return;
-  __threadfence();
-  if (want_dw) {
-    for (int64_t j = int64_t(lane) * VEC; j < c.d; j += 32 * VEC) {
-      Vec<T, VEC> out;
+    float dot[AHEAD] = {};
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) out.v[v] = 0.0f;
-#pragma unroll 4
-      for (unsigned o = 0; o < n_pieces; ++o)
+    for (int a = 0; a < AHEAD; ++a) {
+      if (WHOLE || a < n) {
+        const float f = ent[i0 + a].coef;
+        const uint32_t group = ent[i0 + a].group;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) out.v[v] += __ldcg(&q.g.part[int64_t(slot0 + o) * c.d + j + v]);
-      out.store(dw + col * c.d + j);
+        for (int h = 0; h < CHUNKS; ++h) {
+          if (in(h)) {
+            Vec<T, VEC> t;
+            t.set_raw(xv[a][h]);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) acc[h][v] = fmaf(f, t.v[v], acc[h][v]);
+            if constexpr (DOTS) {
+              Vec<T, VEC> u;
+              u.set_raw(wv[a][h]);
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) dot[a] = fmaf(t.v[v], u.v[v], dot[a]);
+            }
+          }
+        }
+        // (the entry past the last has no group's number)
+        if (want_dw && ent[i0 + a + 1].group != group) flush(group);
+      }
+    }
+    if constexpr (DOTS) {
+      // AHEAD sums over the lanes, by exchanging halves until a lane holds one
+      int o = 16;
+#pragma unroll
+      for (int h = AHEAD / 2; h >= 1; h /= 2) {
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+          const bool high = lane & o;
+          const float give = high ? dot[i] : dot[i + h];
+          dot[i] = (high ? dot[i + h] : dot[i]) + __shfl_xor_sync(~0u, give, o);
+        }
+        o /= 2;
+      }
+#pragma unroll
+      for (int p = 16 / AHEAD; p; p /= 2) dot[0] += __shfl_xor_sync(~0u, dot[0], p);
+      constexpr int kLanes = 32 / AHEAD;
+      const int i = lane / kLanes;
+      if (lane % kLanes == 0 && i < n) dots[i0 + i] = (d0 ? dots[i0 + i] : 0.0f) + dot[0];
     }
   }
-  if (c.dbias && lane == 0) {
-    float t = 0.0f;
-    for (unsigned o = 0; o < n_pieces; ++o) t += __ldcg(&q.g.part_bias[slot0 + o]);
-    static_cast<T*>(c.dbias)[col] = from_f32<T>(t);
+  __device__ __forceinline__ void tile() {
+#pragma unroll
+    for (int h = 0; h < CHUNKS; ++h)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[h][v] = 0.0f;
+    int i0 = 0;
+#pragma unroll 1
+    for (; i0 + AHEAD <= total; i0 += AHEAD) batch<true>(i0, AHEAD);
+    if (i0 < total) batch<false>(i0, total - i0);
   }
+};
+
+// Adds a long column's pieces in their order (by the warp that ended last).
+template <typename T, int VEC>
+__device__ __noinline__ void join_pieces(const float* part, const float* part_bias, unsigned n_pieces, int64_t d, T* dw, T* dbias) {
+  const int lane = threadIdx.x % 32;
+  if (dw) {
+    constexpr int kHold = VEC == 1 ? 1 : 4;
+    for (int64_t j = int64_t(lane) * kHold; j < d; j += 32 * kHold) {
+      float out[kHold] = {};
+#pragma unroll 8
+      for (unsigned o = 0; o < n_pieces; ++o) {
+        Vec<float, kHold> t;
+        t.load(part + int64_t(o) * d + j);
+#pragma unroll
+        for (int v = 0; v < kHold; ++v) out[v] += t.v[v];
+      }
+#pragma unroll
+      for (int v = 0; v < kHold; ++v) dw[j + v] = from_f32<T>(out[v]);
+    }
+  }
+  if (dbias && lane == 0) {
+    float t = 0.0f;
+    for (unsigned o = 0; o < n_pieces; ++o) t += __ldcg(&part_bias[o]);
+    *dbias = from_f32<T>(t);
+  }
+}
+
+template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL, bool DOTS>
+__global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel(const ColParams q) {
+  __shared__ Entry ent_all[kColWarps][kColPiece + 1];
+  __shared__ float dots_all[kColWarps][kColPiece];
+  static_assert(kColPiece == 32, "a place a lane");
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const ColumnSums& c = q.c;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  Entry* ent = ent_all[warp];
+  float* dots = dots_all[warp];
+  T* dw = static_cast<T*>(c.dw);
+  T* dbias = static_cast<T*>(c.dbias);
+  using Stream = ColumnStream<T, VEC, CHUNKS, AHEAD, FULL, DOTS>;
+  Stream st{c, ent, dots, nullptr, lane, 0, dw != nullptr, 0, {}};
+  const unsigned pieces = q.g.hdr->pieces, work = pieces + q.g.hdr->tasks;
+  for (unsigned wk = blockIdx.x * kColWarps + warp; wk < work; wk += gridDim.x * kColWarps) {
+    unsigned n_pieces = 1, slot0 = 0, slot = 0, empty = 0;  // empty: columns of the task without a place
+    int64_t c0;
+    int total;
+    Entry e{kNoPlace, 0, 0.0f, kNoPlace};
+    int rank = lane;
+    __syncwarp();  // (the last piece of work has been read from shared memory)
+    if (wk < pieces) {
+      const PieceRec rec = q.g.pieces[wk];
+      c0 = rec.group;
+      slot0 = rec.slot0;
+      slot = slot0 + rec.index;
+      n_pieces = (rec.count + kColPiece - 1) / kColPiece;
+      total = static_cast<int>(min(unsigned(kColPiece), rec.count - rec.index * kColPiece));
+      if (lane < total) e = q.g.sorted[q.g.start[c0] + rec.index * kColPiece + lane];
+    } else {
+      const Task task = q.g.tasks[wk - pieces];
+      c0 = task.c0;
+      total = static_cast<int>(task.places);
+      const bool bare = lane < static_cast<int>(task.columns) && q.g.count[c0 + lane] == 0;
+      if (lane < total) e = q.g.order[task.start + lane];
+      empty = __ballot_sync(~0u, bare);
+      if (total > 1) {
+        // groups in 3 bits (their place in the task) above s: one number to compare
+        const uint64_t key = (uint64_t(e.group - static_cast<uint32_t>(c0)) << 32) | e.s;
+        rank = 0;
+        for (int i = 0; i < total; ++i) rank += __shfl_sync(~0u, key, i) < key;
+      }
+    }
+    if (lane < total) ent[rank] = e;
+    if (lane == 0) ent[total].group = kNoPlace;
+    __syncwarp();
+    st.total = total;
+    st.part = n_pieces > 1 ? q.g.part + int64_t(slot) * c.d : nullptr;
+    if (st.want_dw || DOTS) {
+      for (st.d0 = 0; st.d0 < c.d; st.d0 += Stream::kTile) {
+        st.tile();
+        if (st.want_dw)
+          for (unsigned b = empty; b; b &= b - 1) st.flush(c0 + __ffs(b) - 1);  // (the sums are zero again)
+      }
+    }
+    __syncwarp();
+    if (DOTS && lane < total) static_cast<T*>(c.dots)[ent[lane].s] = from_f32<T>(dots[lane]);
+    float sum = 0.0f;
+    if (dbias) {
+      for (unsigned b = empty; b; b &= b - 1)
+        if (lane == 0) dbias[c0 + __ffs(b) - 1] = from_f32<T>(0.0f);
+      for (int i = 0; i < total; ++i) {
+        sum += ent[i].coef;
+        if (n_pieces == 1 && ent[i + 1].group != ent[i].group) {
+          if (lane == 0) dbias[ent[i].group] = from_f32<T>(sum);
+          sum = 0.0f;
+        }
+      }
+    }
+    if (n_pieces == 1) continue;
+    if (dbias && lane == 0) q.g.part_bias[slot] = sum;
+    __threadfence();
+    __syncwarp();
+    unsigned seen = 0;
+    if (lane == 0) seen = atomicAdd(&q.g.ticket[slot0], 1u);
+    seen = __shfl_sync(~0u, seen, 0);
+    if (seen != n_pieces - 1) continue;
+    __threadfence();
+    join_pieces<T, VEC>(q.g.part + int64_t(slot0) * c.d, q.g.part_bias + slot0, n_pieces, c.d, dw ? dw + c0 * c.d : nullptr,
+                        dbias ? dbias + c0 : nullptr);
+  }
+}
+
+template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL>
+cudaError_t launch_columns_v(const ColParams& q, unsigned grid, cudaStream_t st) {
+  return q.c.dots ? launch_after(column_sums_kernel<T, VEC, CHUNKS, AHEAD, FULL, true>, grid, kColWarps * 32, 0, st, q)
+                  : launch_after(column_sums_kernel<T, VEC, CHUNKS, AHEAD, FULL, false>, grid, kColWarps * 32, 0, st, q);
 }
 
 template <typename T>
 cudaError_t launch_columns_t(const ColParams& q, cudaStream_t st) {
   const ColumnSums& c = q.c;
   constexpr int kVec = 16 / sizeof(T);
-  cudaError_t e = launch_grouping<false, T>(c.places, q.g, static_cast<T*>(c.dots), st);
+  cudaError_t e = launch_grouping<false, T>(c.places, c.coef, q.g, static_cast<T*>(c.dots), st);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (q.g.max_pieces + q.g.n_groups + kColWarps - 1) / kColWarps;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t blocks = (q.g.max_pieces + q.g.max_tasks + kColWarps - 1) / kColWarps, fit = kColBlocks * ops_sm_count();
   const bool vec = c.d % kVec == 0 && c.ldx % kVec == 0 && aligned16(c.x) && (!c.dots || (c.ldw % kVec == 0 && aligned16(c.w))) &&
                    (!c.dw || aligned16(c.dw));
-  if (vec)
-    column_sums_kernel<T, kVec><<<static_cast<unsigned>(blocks), kColWarps * 32, 0, st>>>(q);
-  else
-    column_sums_kernel<T, 1><<<static_cast<unsigned>(blocks), kColWarps * 32, 0, st>>>(q);
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(blocks < fit ? blocks : fit);
+  if (!vec) return launch_columns_v<T, 1, 8, 2, false>(q, grid, st);
+  return c.d % (64 * kVec) == 0 ? launch_columns_v<T, kVec, 2, 2, true>(q, grid, st)
+                                : launch_columns_v<T, kVec, 2, 2, false>(q, grid, st);
 }
 
 ColParams plan_columns(const ColumnSums& c, Scratch& sc) {
   ColParams q{};
   q.c = c;
-  q.g = plan_groups(sc, c.places.total, c.places.n, c.dw ? c.d : 0, c.dbias != nullptr);
+  q.g = plan_groups(sc, c.places.total, c.places.n, kColPiece, c.dw ? c.d : 0, 1, c.dbias != nullptr, true);
   return q;
 }
 

@@ -33,8 +33,8 @@ class Scratch {
 cudaError_t ops_take_status(cudaStream_t st, int* status);
 
 // Words that each (device, stream) keeps for the operators, zero at first: [0]
-// the status that a kernel sets when a wait runs out, [64..] tickets that every
-// kernel leaves at zero.
+// the status that a kernel sets when a wait runs out, [32] and [64..] tickets
+// that every kernel leaves at zero.
 constexpr int64_t kOpsWords = 16384;
 
 // SMs of the current device.
@@ -143,7 +143,7 @@ struct ClipTensor {
 };
 size_t clip_scratch_bytes();
 // scale == false: the norm alone.
-cudaError_t launch_clip(const ClipTensor* t, int64_t num, bool scale, float max_norm, float* norm, Scratch& sc,
-                        cudaStream_t st);
+cudaError_t launch_clip(const ClipTensor* t, int64_t num, bool scale, float max_norm, float* norm, int* words,
+                        Scratch& sc, cudaStream_t st);
 
 }  // namespace tk

@@ -211,10 +211,11 @@ int clip(const void* const* grads, void* const* out, const int64_t* counts, cons
     list[static_cast<size_t>(i)] = ClipTensor{grads[i], scale ? out[i] : nullptr, counts[i], dtypes[i]};
   }
   void* base = nullptr;
-  const cudaError_t e = block_of(st, clip_scratch_bytes(), &base);
+  int* words = nullptr;
+  const cudaError_t e = block_of(st, clip_scratch_bytes(), &base, &words);
   if (e != cudaSuccess) return status_of(e);
   Scratch sc(base);
-  return status_of(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, sc, st));
+  return status_of(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, words, sc, st));
 }
 
 }  // namespace

@@ -26,6 +26,20 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// VEC consecutive values as they are stored.
+template <typename T, int VEC>
+struct Raw {
+  uint4 u;
+  __device__ __forceinline__ void load_nc(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T u;
+  __device__ __forceinline__ void load_nc(const T* p) { u = __ldg(p); }
+  __device__ __forceinline__ void clear() { u = from_f32<T>(0.0f); }
+};
+
 // VEC consecutive values as f32: one 16-byte access when VEC values fill 16
 // bytes (p then 16-byte aligned), one value when VEC == 1.
 template <typename T, int VEC>
@@ -70,6 +84,15 @@ struct Vec {
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void set_raw(const Raw<T, VEC>& r) {
+    if constexpr (VEC == 1) v[0] = to_f32(r.u);
+    else set(r.u);
+  }
+  // (written once and not read again here)
+  __device__ __forceinline__ void store_stream(T* p) const {
+    if constexpr (VEC == 1) *p = from_f32<T>(v[0]);
+    else __stcs(reinterpret_cast<uint4*>(p), pack());
   }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (VEC == 1) {
