@@ -1,6 +1,7 @@
 // Matrix products with a fused epilogue, and the pass that prepares their
 // gradients: c = act(a b^T + bias) + residual for the linear layer, and the
 // plain products of its backward pass, over operands of either order.
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -10,9 +11,12 @@ namespace tk {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Products on the CUDA cores.  One block of 256 threads makes a 128 x 128 tile
-// of c from 16-deep slices in shared memory, 8 x 8 results a thread in
-// registers, every product and sum in f32.
+// f32 products on the CUDA cores: what runs in the tensor cores' place when an
+// operand holds an infinity or NaN (their three-part form has no such
+// values).  One block of 256 threads makes a 128 x 128 tile of c from 16-deep
+// slices in shared memory, 8 x 8 results a thread in registers, every product
+// and sum in f32.  It does nothing, at the cost of its launch, unless the
+// operands' split left this call's mark.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128, kDeep = 16, kSimtThreads = 256;
 constexpr int kTilePad = kTile + 4;
@@ -33,6 +37,8 @@ struct SimtParams {
   T* pre;
   int64_t ldp;
   int64_t tiles_n;
+  const int* mark;  // the product is made only where *mark == call (nullable)
+  int call;
 };
 
 // A kDeep x kTile slice of an operand into shared memory, as f32, zeros outside it.
@@ -61,6 +67,9 @@ __device__ __forceinline__ void load_slice(float (&dst)[kDeep][kTilePad], const 
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) simt_product_kernel(const SimtParams<T> p) {
   __shared__ float as[kDeep][kTilePad], bs[kDeep][kTilePad];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (p.mark && *p.mark != p.call) return;
   const int64_t m0 = (blockIdx.x / p.tiles_n) * kTile, n0 = (blockIdx.x % p.tiles_n) * kTile;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float acc[8][8] = {};
@@ -92,16 +101,18 @@ __global__ void __launch_bounds__(kSimtThreads) simt_product_kernel(const SimtPa
       if (j >= p.n) continue;
       float z = acc[r][c] + (p.bias ? to_f32(p.bias[j]) : 0.0f);
       if (p.pre) p.pre[i * p.ldp + j] = from_f32<T>(z);
-      z = act_value(z, p.act);
+      z = act_value<T>(z, p.act);
       if (p.residual) z += to_f32(p.residual[i * p.ldr + j]);
       p.c[i * p.ldc + j] = from_f32<T>(z);
     }
   }
 }
 
-template <typename T>
-cudaError_t launch_simt(const Product& g, cudaStream_t st) {
+cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStream_t st) {
+  using T = float;
   SimtParams<T> p;
+  p.mark = mark;
+  p.call = call;
   p.a = static_cast<const T*>(g.a.p);
   p.b = static_cast<const T*>(g.b.p);
   p.lda = g.a.ld;
@@ -122,8 +133,7 @@ cudaError_t launch_simt(const Product& g, cudaStream_t st) {
   p.tiles_n = (g.n + kTile - 1) / kTile;
   const int64_t tiles = p.tiles_n * ((g.m + kTile - 1) / kTile);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  simt_product_kernel<T><<<static_cast<unsigned>(tiles), kSimtThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_after(simt_product_kernel<T>, static_cast<unsigned>(tiles), kSimtThreads, 0, st, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -205,7 +215,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T
   if (j >= p.n || i >= p.rows) return;
   z += p.bias ? to_f32(p.bias[j]) : 0.0f;
   if (p.pre) p.pre[i * p.ldp + j] = from_f32<T>(z);
-  z = act_value(z, p.act);
+  z = act_value<T>(z, p.act);
   if (p.residual) z += to_f32(p.residual[i * p.ldr + j]);
   p.y[i * p.ldy + j] = from_f32<T>(z);
 }
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(kSumThreads) slope_sums_kernel(const SlopeSums
           Vec<T, VEC> u;
           u.set_raw(z[a]);
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) t.v[c] *= act_slope(u.v[c], ACT);
+          for (int c = 0; c < VEC; ++c) t.v[c] *= act_slope<T>(u.v[c], ACT);
           if (dz) t.store(dz + i * s.n + j);
         }
 #pragma unroll
@@ -378,11 +388,15 @@ cudaError_t launch_slope_sums(const SlopeSums& s, cudaStream_t st) {
   return s.dtype == kF32 ? launch_slope_sums_t<float>(s, st) : launch_slope_sums_t<__nv_bfloat16>(s, st);
 }
 
-size_t product_scratch_bytes(const Product& g) { return g.dtype == kF32 || few_rows(g) ? 0 : mma_scratch_bytes(g); }
+size_t product_scratch_bytes(const Product& g) { return few_rows(g) ? 0 : mma_scratch_bytes(g); }
 
 cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
   if (few_rows(g)) return g.dtype == kF32 ? launch_few<float>(g, st) : launch_few<__nv_bfloat16>(g, st);
-  return g.dtype == kF32 ? launch_simt<float>(g, st) : launch_mma(g, sc, words, st);
+  static std::atomic<int> calls{0};
+  const int call = g.dtype == kF32 ? 1 + (calls.fetch_add(1) & 0x3fffffff) : 0;
+  return launch_mma(g, sc, words, call, st);
 }
+
+cudaError_t launch_simt(const Product& g, const int* mark, int call, cudaStream_t st) { return launch_simt_t(g, mark, call, st); }
 
 }  // namespace tk

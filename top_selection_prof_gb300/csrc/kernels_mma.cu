@@ -18,6 +18,13 @@
 // that do so for the same rows and columns the last one (by a ticket) adds the
 // parts in order of k and writes the result.  Nothing waits for another run.
 //
+// F32 operands are taken apart into three bf16 parts each (8 + 8 + 8 bits, no
+// remainder), and the six products of parts whose orders add up to at most two
+// are summed, the smallest first: the dropped ones are below 2^-23 of a
+// product.  So a stage is one of six times as many; results are f32.  An
+// infinity would meet a zero part (NaN): where the split finds one, the
+// product is made on the CUDA cores and this kernel does nothing.
+//
 // Every wait has a limit, after which the status word is set and the kernel
 // winds up.
 #include <cstdint>
@@ -36,6 +43,12 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kStageBytesOut = 4096;   // staging of one epilogue warp: 32 rows x 128 bytes
 
+// f32: the tensor cores' sums are cut off, not rounded, so that a long sum
+// drifts (K = 4096 in one accumulator: 4.5e-6 of the result).  After kRoundDepth
+// stages of k (all six products of them) the sums go to f32 registers, which
+// are added to those before and kept in scratch: the drift stays that of
+// K = 512 (5e-7).
+constexpr int kRoundDepth = 8, kRoundStages = 6 * kRoundDepth;
 constexpr int kTileN = 256;            // columns of c in a pair's tile (and of tensor memory in an accumulator)
 constexpr int kPairM = 2 * kTileM;     // its rows
 constexpr int kRowsB = kTileN / 2;     // rows of b that one CTA brings in
@@ -53,6 +66,7 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 struct Deal {
   int tiles_m, tiles_n;
   int k_blocks;       // stages of a tile
+  int depth;          // those of one product of parts (k_blocks for bf16)
   int pairs;
   int waves;
   int shared_tiles;   // 0: every pair's tiles are whole (the last wave may be short)
@@ -71,17 +85,19 @@ struct MmaParams {
   Deal deal;
   bool a_k, b_k;           // operand order: k contiguous
   uint32_t idesc;
-  const __nv_bfloat16* bias;
-  const __nv_bfloat16* residual;
+  const void* bias;        // nullable
+  const void* residual;    // nullable
   int64_t ldr;
   int act;
   bool tma_c, tma_pre;     // stores by TMA (else by plain stores)
-  __nv_bfloat16* c_ptr;
+  void* c_ptr;
   int64_t ldc;
-  __nv_bfloat16* pre_ptr;  // nullable
+  void* pre_ptr;           // nullable
   int64_t ldp;
   float* part;             // sums of parts of k: 2 slots a pair, each kPairM x kTileN
   unsigned* ticket;        // 2 kEpiWarps a shared tile, zero between launches
+  const int* mark;         // f32: the kernel does nothing where *mark == call
+  int call;
   int* status;
 };
 
@@ -128,9 +144,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (t - t0 > kWaitLimitNs) return false;
   }
 }
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-               "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+               "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
@@ -217,6 +233,10 @@ struct Worker {
     at = d.shared_tiles ? d.run_start(pair) : 0;
     end = d.shared_tiles ? d.run_start(pair + 1) : 0;
   }
+  __device__ __forceinline__ void leave() {
+    wave = INT32_MAX;
+    at = end;
+  }
   __device__ __forceinline__ bool next(const Deal& d, Work* w) {
     const int64_t tile = int64_t(wave) * d.pairs + pair;
     if (wave < d.waves && tile < int64_t(d.tiles_m) * d.tiles_n) {
@@ -271,42 +291,58 @@ __device__ __forceinline__ void store_plain(uint32_t staging, T* dst, int64_t ld
   }
 }
 // A chunk of the residual into staging, zeros outside it (any alignment, rows read in order).
-__device__ __forceinline__ void stage_residual(uint32_t staging, const __nv_bfloat16* src, int64_t ld, int64_t row0,
-                                               int64_t rows, int64_t col0, int64_t cols, int lane) {
+template <typename T>
+__device__ __forceinline__ void stage_residual(uint32_t staging, const T* src, int64_t ld, int64_t row0, int64_t rows,
+                                               int64_t col0, int64_t cols, int lane) {
 #pragma unroll 8
   for (int r = 0; r < 32; ++r) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 4 / int(sizeof(T)); ++e) {
       const int c = e * 32 + lane;
-      uint16_t u = 0;
-      if (row0 + r < rows && col0 + c < cols) u = __bfloat16_as_ushort(src[(row0 + r) * ld + col0 + c]);
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(piece(staging, r, c / 8) + (c % 8) * 2), "h"(u) : "memory");
+      const uint32_t addr = piece(staging, r, c * int(sizeof(T)) / 16) + (c * sizeof(T)) % 16;
+      T v = from_f32<T>(0.0f);
+      if (row0 + r < rows && col0 + c < cols) v = src[(row0 + r) * ld + col0 + c];
+      if constexpr (sizeof(T) == 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(v)) : "memory");
+      else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
     }
   }
 }
-// 32 values of the lane's row, rounded to bf16, into half `h` of the staging's row.
-__device__ __forceinline__ void stage_bf16(uint32_t staging, int lane, int h, const float* v) {
+// 32 values of the lane's row, rounded to T, into staging: half `h` of its 128 bytes (bf16), or all (f32).
+template <typename T>
+__device__ __forceinline__ void stage_values(uint32_t staging, int lane, int h, const float* v) {
+  constexpr int kVec = 16 / sizeof(T), kPieces = 32 / kVec;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    Vec<__nv_bfloat16, 8> o;
+  for (int q = 0; q < kPieces; ++q) {
+    Vec<T, kVec> o;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.v[i] = v[q * 8 + i];
+    for (int i = 0; i < kVec; ++i) o.v[i] = v[q * kVec + i];
     const uint4 u = o.pack();
-    st_shared16(piece(staging, lane, 4 * h + q), u.x, u.y, u.z, u.w);
+    st_shared16(piece(staging, lane, kPieces * h + q), u.x, u.y, u.z, u.w);
   }
 }
-template <int N>
+template <typename T, int N>
 __device__ __forceinline__ void apply_act(float* v, int act) {
-  if (act == kActNone) return;
   if (act == kActRelu) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], kActRelu);
+    for (int i = 0; i < N; ++i) v[i] = relu(v[i]);
   } else if (act == kActGelu) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], kActGelu);
-  } else {
+    for (int i = 0; i < N; ++i) v[i] = act_value<T>(v[i], kActGelu);
+  } else if (act == kActSilu) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], kActSilu);
+    for (int i = 0; i < N; ++i) v[i] = act_value<T>(v[i], kActSilu);
+  }
+}
+__device__ __forceinline__ void add_bias32(float* v, const float* bias) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 t = reinterpret_cast<const float4*>(bias)[i];
+    v[4 * i] += t.x;
+    v[4 * i + 1] += t.y;
+    v[4 * i + 2] += t.z;
+    v[4 * i + 3] += t.w;
   }
 }
 
@@ -322,7 +358,10 @@ __device__ __forceinline__ void free_accumulator(int lane, uint32_t bar) {
   if (lane == 0) bar_arrive(map_to_rank(bar, 0));
 }
 
+template <typename T>
 __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant__ MmaParams p) {
+  const T* bias = static_cast<const T*>(p.bias);
+  const T* residual = static_cast<const T*>(p.residual);
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_addr(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -357,6 +396,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
   grid_launch_dependents();
 
   Worker worker(p.deal, blockIdx.x / 2);
+  if (sizeof(T) == 4 && *p.mark == p.call) worker.leave();
   Work w;
   bool ok = true;
 
@@ -372,18 +412,26 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
           const uint32_t sa = base + stage * kStage, sb = sa + kBytesA;
           const uint32_t bar = map_to_rank(full(stage), 0);
           bar_expect(bar, kStage);
-          const int k0 = kb * kDeepK;
+          int k0 = kb * kDeepK, part_a = 0, part_b = 0;
+          if constexpr (sizeof(T) == 4) {
+            // a round's products of parts one after the other: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
+            const int round = kb / kRoundStages, in = kb - round * kRoundStages;
+            const int deep = min(kRoundDepth, p.deal.depth - round * kRoundDepth), term = in / deep;
+            k0 = (round * kRoundDepth + in - term * deep) * kDeepK;
+            part_a = 0x001102 >> (4 * term) & 3;
+            part_b = 0x010120 >> (4 * term) & 3;
+          }
           if (p.a_k) {
-            tma_load(sa, &p.a, k0, m0, bar);
+            tma_load(sa, &p.a, k0, m0, part_a, bar);
           } else {
-            tma_load(sa, &p.a, m0, k0, bar);
-            tma_load(sa + 8192, &p.a, m0 + 64, k0, bar);
+            tma_load(sa, &p.a, m0, k0, part_a, bar);
+            tma_load(sa + 8192, &p.a, m0 + 64, k0, part_a, bar);
           }
           if (p.b_k) {
-            tma_load(sb, &p.b, k0, n0, bar);
+            tma_load(sb, &p.b, k0, n0, part_b, bar);
           } else {
-            tma_load(sb, &p.b, n0, k0, bar);
-            tma_load(sb + 8192, &p.b, n0 + 64, k0, bar);
+            tma_load(sb, &p.b, n0, k0, part_b, bar);
+            tma_load(sb + 8192, &p.b, n0 + 64, k0, part_b, bar);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -408,15 +456,26 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
       while (ok && worker.next(p.deal, &w)) {
         if (!(ok = bar_wait(acc_empty(buf), acc_phase ^ 1))) break;
         fence_after();
-        const uint32_t d = tmem + buf * kTileN;
+        uint32_t d = tmem + buf * kTileN;
+        bool fresh = true;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (sizeof(T) == 4 && kb != w.kb0 && kb % kRoundStages == 0) {  // the round's sums go out, the next begins
+            mma_commit(acc_full(buf));
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1;
+            if (!(ok = bar_wait(acc_empty(buf), acc_phase ^ 1))) break;
+            fence_after();
+            d = tmem + buf * kTileN;
+            fresh = true;
+          }
           if (!(ok = bar_wait(full(stage), phase))) break;
           fence_after();
           const uint32_t sa = base + stage * kStage, sb = sa + kBytesA;
           const uint64_t da = operand_desc(sa, 8192), db = operand_desc(sb, 8192);
 #pragma unroll
           for (int i = 0; i < kDeepK / 16; ++i)
-            mma(d, da + i * step_a, db + i * step_b, p.idesc, kb > w.kb0 || i > 0);
+            mma(d, da + i * step_a, db + i * step_b, p.idesc, !fresh || i > 0);
+          fresh = false;
           mma_commit(empty(stage));
           if (++stage == kStages) {
             stage = 0;
@@ -432,41 +491,67 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
     const int e = warp - 4, quad = e % 4, half = e / 4;
     const uint32_t staging = base + kOffStaging + e * kStageBytesOut;
     float* bias_smem = reinterpret_cast<float*>(smem + kOffBias);
-    constexpr int kChunk = 64, kHalf = kTileN / 2;
-    int buf = 0;
+    constexpr int kChunk = 128 / sizeof(T), kHalf = kTileN / 2;  // columns of the staging's 128 bytes
+    int buf = 0, bias_buf = 0;
     uint32_t acc_phase = 0;
-    while (worker.next(p.deal, &w)) {
+    for (; worker.next(p.deal, &w); bias_buf ^= 1) {
       const int64_t row0 = int64_t(w.m) * kPairM + rank * kTileM + quad * 32;
       const int64_t n0 = int64_t(w.n) * kTileN;
-      if (p.bias) {
+      if (bias) {
         for (int i = threadIdx.x - 128; i < kTileN; i += 32 * kEpiWarps)
-          bias_smem[buf * kTileN + i] = n0 + i < p.n ? to_f32(p.bias[n0 + i]) : 0.0f;
+          bias_smem[bias_buf * kTileN + i] = n0 + i < p.n ? to_f32(bias[n0 + i]) : 0.0f;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+      }
+      const bool lies = row0 < p.m && n0 + half * kHalf < p.n;  // else nothing of the warp's part lies in c
+      // a warp's part of a slot: four columns of each of its 32 rows together
+      const int64_t region = (int64_t(rank) * kEpiWarps + e) * (32 * kHalf) + lane * 4;
+      float* own = p.part + int64_t(w.slot >= 0 ? w.slot : 2 * p.deal.pairs + static_cast<int>(blockIdx.x / 2)) * (kPairM * kTileN) + region;
+      // this round's sums to the warp's own slot, onto those before
+      auto drain = [&](bool onto) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < kHalf; c0 += 32) {
+          float v[32];
+          tmem_load32(tmem + buf * kTileN + half * kHalf + c0 + (uint32_t(quad * 32) << 16), v);
+          float4* dst = reinterpret_cast<float4*>(own) + c0 / 4 * 32;
+          float4 t[8];
+          if (onto) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = __ldcg(dst + i * 32);
+          }
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 z = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (onto) z = make_float4(z.x + t[i].x, z.y + t[i].y, z.z + t[i].z, z.w + t[i].w);
+            __stcg(dst + i * 32, z);
+          }
+        }
+      };
+      bool held = false;  // the slot holds earlier rounds
+      if constexpr (sizeof(T) == 4) {
+        for (int kb = (w.kb0 / kRoundStages + 1) * kRoundStages; kb < w.kb1; kb += kRoundStages) {
+          if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
+          fence_after();
+          if (lies) drain(held);
+          free_accumulator(lane, acc_empty(buf));
+          buf ^= 1;
+          if (buf == 0) acc_phase ^= 1;
+          held = true;
+        }
       }
       // (a warp that gave up goes on without waiting, so that the others' barriers are still met)
       if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
       fence_after();
       const uint32_t acc = tmem + buf * kTileN + half * kHalf + (uint32_t(quad * 32) << 16);
-      if (row0 >= p.m || n0 + half * kHalf >= p.n) {  // nothing of the warp's part lies in c
+      if (!lies) {
         free_accumulator(lane, acc_empty(buf));
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1;
         continue;
       }
-      // a warp's part of a slot: four columns of each of its 32 rows together
-      const int64_t region = (int64_t(rank) * kEpiWarps + e) * (32 * kHalf) + lane * 4;
       int first = 0, parts = 0;  // pairs whose runs make up a shared tile
       if (w.slot >= 0) {
-        float* dst = p.part + int64_t(w.slot) * (kPairM * kTileN) + region;
-#pragma unroll 1
-        for (int c0 = 0; c0 < kHalf; c0 += 32) {
-          float v[32];
-          tmem_load32(acc + c0, v);
-          tmem_wait_load();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            __stcg(reinterpret_cast<float4*>(dst + (c0 / 4 + i) * 128), make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-        }
+        drain(held);
         free_accumulator(lane, acc_empty(buf));
         __threadfence();
         runs_of_tile(p.deal, w.shared, &first, &parts);
@@ -477,11 +562,23 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
         __threadfence();
         if (static_cast<int>(seen) != parts - 1) first = -1;
       }
+      const float* bias_own = bias_smem + bias_buf * kTileN + half * kHalf;
       // 32 columns' sums (and the bias): from the accumulator, or from the parts, two parts' loads in flight
       auto fetch = [&](int c, float* v) {
         if (w.slot < 0) {
           tmem_load32(acc + c, v);
           tmem_wait_load();
+          if (held) {
+            const float4* t = reinterpret_cast<const float4*>(own) + c / 4 * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 z = __ldcg(t + i * 32);
+              v[4 * i] += z.x;
+              v[4 * i + 1] += z.y;
+              v[4 * i + 2] += z.z;
+              v[4 * i + 3] += z.w;
+            }
+          }
         } else {
           const int k0 = w.shared * p.deal.k_blocks;
           auto part_of = [&](int pair) {
@@ -509,18 +606,43 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             }
           }
         }
-        if (p.bias) {
-          const float4* b = reinterpret_cast<const float4*>(bias_smem + buf * kTileN + half * kHalf + c);
+        if (bias) add_bias32(v, bias_own + c);
+      };
+      if (sizeof(T) == 2 && w.slot < 0 && !p.pre_ptr && !residual) {
+        // the usual case: 32 columns on their way from tensor memory while the 32 before them are finished
+        float v[2][32];
+        tmem_load32(acc, v[0]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 t = b[i];
-            v[4 * i] += t.x;
-            v[4 * i + 1] += t.y;
-            v[4 * i + 2] += t.z;
-            v[4 * i + 3] += t.w;
+        for (int s = 0; s < kHalf / 32; ++s) {
+          tmem_wait_load();
+          if (s + 1 < kHalf / 32) tmem_load32(acc + 32 * (s + 1), v[(s + 1) & 1]);
+          else free_accumulator(lane, acc_empty(buf));
+          float* z = v[s & 1];
+          if (bias) add_bias32(z, bias_own + 32 * s);
+          apply_act<T, 32>(z, p.act);
+          constexpr int kSteps = kChunk / 32;  // of a staged chunk
+          if (s % kSteps == 0) {
+            if (lane == 0) store_wait_read();  // the staging's last store has been read
+            __syncwarp();
+          }
+          stage_values<T>(staging, lane, s % kSteps, z);
+          if (s % kSteps == kSteps - 1) {
+            const int64_t col0 = n0 + half * kHalf + (s / kSteps) * kChunk;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (p.tma_c) {
+              if (lane == 0 && col0 < p.n) {
+                tma_store(&p.c, static_cast<int>(col0), static_cast<int>(row0), 0, staging);
+                store_commit();
+              }
+            } else {
+              store_plain(staging, static_cast<T*>(p.c_ptr), p.ldc, row0, p.m, col0, p.n, lane);
+              __syncwarp();
+            }
           }
         }
-      };
+        first = -1;
+      }
 #pragma unroll 1
       for (int c0 = 0; c0 < kHalf && first >= 0; c0 += kChunk) {
         const int64_t col0 = n0 + half * kHalf + c0;
@@ -529,10 +651,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
           if (lane == 0) store_wait_read();  // the staging's last store has been read
           __syncwarp();
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kChunk / 32; ++h) {
             float v[32];
             fetch(c0 + 32 * h, v);
-            stage_bf16(staging, lane, h, v);
+            stage_values<T>(staging, lane, h, v);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -542,31 +664,32 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
               store_commit();
             }
           } else {
-            store_plain(staging, p.pre_ptr, p.ldp, row0, p.m, col0, p.n, lane);
+            store_plain(staging, static_cast<T*>(p.pre_ptr), p.ldp, row0, p.m, col0, p.n, lane);
           }
         }
         if (lane == 0) store_wait_read();
         __syncwarp();
-        if (p.residual) {
-          stage_residual(staging, p.residual, p.ldr, row0, p.m, col0, p.n, lane);
+        if (residual) {
+          stage_residual(staging, residual, p.ldr, row0, p.m, col0, p.n, lane);
           __syncwarp();
         }
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kChunk / 32; ++h) {
           float v[32];
           fetch(c0 + 32 * h, v);
           if (w.slot < 0 && c0 + 32 * h + 32 == kHalf) free_accumulator(lane, acc_empty(buf));
-          apply_act<32>(v, p.act);
-          if (p.residual) {
+          apply_act<T, 32>(v, p.act);
+          if (residual) {
+            constexpr int kVec = 16 / sizeof(T), kPieces = 32 / kVec;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              Vec<__nv_bfloat16, 8> r;
-              r.set(ld_shared16(piece(staging, lane, 4 * h + q)));
+            for (int q = 0; q < kPieces; ++q) {
+              Vec<T, kVec> r;
+              r.set(ld_shared16(piece(staging, lane, kPieces * h + q)));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[q * 8 + i] += r.v[i];
+              for (int i = 0; i < kVec; ++i) v[q * kVec + i] += r.v[i];
             }
           }
-          stage_bf16(staging, lane, h, v);
+          stage_values<T>(staging, lane, h, v);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -576,7 +699,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             store_commit();
           }
         } else {
-          store_plain(staging, p.c_ptr, p.ldc, row0, p.m, col0, p.n, lane);
+          store_plain(staging, static_cast<T*>(p.c_ptr), p.ldc, row0, p.m, col0, p.n, lane);
         }
       }
       buf ^= 1;
@@ -596,9 +719,41 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
 // Copies an operand whose rows TMA cannot address to rows of `ld` values (a multiple of 8).
 __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* src, int64_t lds, int64_t rows, int64_t cols,
                                                          __nv_bfloat16* dst, int64_t ld) {
-  const int64_t per = (cols + 255) / 256;
-  const int64_t r = blockIdx.x / per, c = (blockIdx.x % per) * 256 + threadIdx.x;
-  if (r < rows && c < cols) dst[r * ld + c] = src[r * lds + c];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t per = (cols + 1023) / 1024;
+  const int64_t r = blockIdx.x / per, c0 = (blockIdx.x % per) * 1024 + threadIdx.x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t c = c0 + e * 256;
+    if (r < rows && c < cols) dst[r * ld + c] = src[r * lds + c];
+  }
+}
+
+// The three bf16 parts of an f32 operand, `plane` values apart, rows of `ld`
+// values.  A part is the leading 8 bits of what the parts before it left, so
+// the three hold all 24.  *other becomes `call` when a value is not finite.
+__global__ void __launch_bounds__(256) split_rows_kernel(const float* src, int64_t lds, int64_t rows, int64_t cols,
+                                                         __nv_bfloat16* dst, int64_t ld, int64_t plane, int* other, int call) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t per = (cols + 1023) / 1024;
+  const int64_t r = blockIdx.x / per, c0 = (blockIdx.x % per) * 1024 + threadIdx.x;
+  bool finite = true;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t c = c0 + e * 256;
+    if (r >= rows || c >= cols) continue;
+    float v = src[r * lds + c];
+    finite = finite && fabsf(v) < INFINITY;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+      dst[q * plane + r * ld + c] = __ushort_as_bfloat16(static_cast<unsigned short>(top >> 16));
+      v -= __uint_as_float(top);
+    }
+  }
+  if (!finite) *other = call;
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -619,29 +774,29 @@ EncodeFn encode_fn() {
 }
 
 // A matrix of rows x cols values, rows ld apart, `planes` of them `plane` rows apart; boxes of box_cols x box_rows.
-bool encode(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t planes, int64_t plane,
+bool encode(CUtensorMap* map, bool f32, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t planes, int64_t plane,
             int box_cols, int box_rows) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
-  constexpr int size = 2;
+  const int size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
   const cuuint64_t strides[2] = {cuuint64_t(ld) * size, cuuint64_t(plane) * ld * size};
   const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(p),
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p),
             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr double kStageUs = 0.30;  // a stage of a tile, as timed
 
-bool tma_rows(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+bool tma_rows(const void* p, int64_t ld, int size) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0; }
 
 struct MmaPlan {
   Deal deal;
   __nv_bfloat16* copy_a;
   __nv_bfloat16* copy_b;
-  int64_t ld_a, ld_b;
+  int64_t ld_a, ld_b;  // of the copies, or of the operands where they serve as they are
   float* part;
 };
 
@@ -657,7 +812,10 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
   const int64_t tiles = tm * tn;
   d.tiles_m = static_cast<int>(tm);
   d.tiles_n = static_cast<int>(tn);
-  d.k_blocks = static_cast<int>((g.k + kDeepK - 1) / kDeepK);
+  const bool f32 = g.dtype == kF32;
+  d.depth = static_cast<int>((g.k + kDeepK - 1) / kDeepK);
+  if (f32 && d.depth > INT32_MAX / 6) return false;
+  d.k_blocks = f32 ? 6 * d.depth : d.depth;
   const int slots = ops_sm_count() / 2 > 0 ? ops_sm_count() / 2 : 1;
   d.pairs = static_cast<int>(tiles < slots ? tiles : slots);
   d.waves = static_cast<int>((tiles + d.pairs - 1) / d.pairs);
@@ -679,28 +837,39 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
     d.shared_tiles = static_cast<int>(shared);
     d.run = static_cast<int>(shared * d.k_blocks / slots);
     d.longer = static_cast<int>(shared * d.k_blocks % slots);
-    q->part = sc.take<float>(int64_t(2) * slots * kPairM * kTileN);
   }
-  const bool ta = tma_rows(g.a.p, g.a.ld), tb = tma_rows(g.b.p, g.b.ld);
+  // two slots a pair for runs, one for the rounds of f32
+  if (d.shared_tiles || (f32 && d.depth > kRoundDepth)) q->part = sc.take<float>(int64_t(3) * d.pairs * kPairM * kTileN);
   q->ld_a = g.a.ld;
   q->ld_b = g.b.ld;
-  if (!ta) {
+  if (f32 || !tma_rows(g.a.p, g.a.ld, 2)) {
     q->ld_a = (operand_cols(g.a, g.m, g.k) + 7) / 8 * 8;
-    q->copy_a = sc.take<__nv_bfloat16>(q->ld_a * operand_rows(g.a, g.m, g.k));
+    q->copy_a = sc.take<__nv_bfloat16>((f32 ? 3 : 1) * q->ld_a * operand_rows(g.a, g.m, g.k));
   }
-  if (!tb) {
+  if (f32 || !tma_rows(g.b.p, g.b.ld, 2)) {
     q->ld_b = (operand_cols(g.b, g.n, g.k) + 7) / 8 * 8;
-    q->copy_b = sc.take<__nv_bfloat16>(q->ld_b * operand_rows(g.b, g.n, g.k));
+    q->copy_b = sc.take<__nv_bfloat16>((f32 ? 3 : 1) * q->ld_b * operand_rows(g.b, g.n, g.k));
   }
   return true;
 }
 
-cudaError_t align_rows(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_t ld, cudaStream_t st) {
+cudaError_t prepare_rows(const Operand& o, int64_t i, int64_t k, bool f32, __nv_bfloat16* dst, int64_t ld, int* other, int call,
+                         cudaStream_t st) {
   const int64_t rows = operand_rows(o, i, k), cols = operand_cols(o, i, k);
-  const int64_t blocks = rows * ((cols + 255) / 256);
+  const int64_t blocks = rows * ((cols + 1023) / 1024);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  align_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(o.p), o.ld, rows, cols, dst, ld);
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (f32)
+    return launch_after(split_rows_kernel, grid, 256, 0, st, static_cast<const float*>(o.p), o.ld, rows, cols, dst, ld, rows * ld,
+                        other, call);
+  return launch_after(align_rows_kernel, grid, 256, 0, st, static_cast<const __nv_bfloat16*>(o.p), o.ld, rows, cols, dst, ld);
+}
+
+template <typename T>
+cudaError_t launch_mma_t(const MmaParams& p, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_after(mma_kernel<T>, static_cast<unsigned>(2 * p.deal.pairs), kThreads, kSmem, st, p);
 }
 
 }  // namespace
@@ -712,12 +881,15 @@ size_t mma_scratch_bytes(const Product& g) {
   return sc.used();
 }
 
-cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
+cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cudaStream_t st) {
   MmaPlan q;
   if (!plan_mma(g, sc, &q)) return cudaErrorInvalidValue;
+  const bool f32 = g.dtype == kF32;
+  int* other = words + kOpsOther;
   cudaError_t e = cudaSuccess;
-  if (q.copy_a) e = align_rows(g.a, g.m, g.k, q.copy_a, q.ld_a, st);
-  if (e == cudaSuccess && q.copy_b) e = align_rows(g.b, g.n, g.k, q.copy_b, q.ld_b, st);
+  if (q.copy_a) e = prepare_rows(g.a, g.m, g.k, f32, q.copy_a, q.ld_a, other, call, st);
+  if (e == cudaSuccess && q.copy_b) e = prepare_rows(g.b, g.n, g.k, f32, q.copy_b, q.ld_b, other, call, st);
+  if (e == cudaSuccess && f32) e = launch_simt(g, other, call, st);
   if (e != cudaSuccess) return e;
   MmaParams p{};
   p.m = g.m;
@@ -730,29 +902,30 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, cudaStream_t s
             (static_cast<uint32_t>(kTileN / 8) << 17) | (static_cast<uint32_t>(kPairM / 16) << 24);
   const void* a = q.copy_a ? q.copy_a : g.a.p;
   const void* b = q.copy_b ? q.copy_b : g.b.p;
-  bool ok = p.a_k ? encode(&p.a, a, g.k, g.m, q.ld_a, 0, 0, kDeepK, kTileM)
-                  : encode(&p.a, a, g.m, g.k, q.ld_a, 0, 0, 64, kDeepK);
-  ok = ok && (p.b_k ? encode(&p.b, b, g.k, g.n, q.ld_b, 0, 0, kDeepK, kRowsB)
-                    : encode(&p.b, b, g.n, g.k, q.ld_b, 0, 0, 64, kDeepK));
-  p.bias = static_cast<const __nv_bfloat16*>(g.bias);
-  p.residual = static_cast<const __nv_bfloat16*>(g.residual);
+  const int64_t ra = operand_rows(g.a, g.m, g.k), rb = operand_rows(g.b, g.n, g.k);
+  const int parts = f32 ? 3 : 1;
+  bool ok = encode(&p.a, false, a, operand_cols(g.a, g.m, g.k), ra, q.ld_a, parts, ra, 64, p.a_k ? kTileM : kDeepK);
+  ok = ok && encode(&p.b, false, b, operand_cols(g.b, g.n, g.k), rb, q.ld_b, parts, rb, 64, p.b_k ? kRowsB : kDeepK);
+  p.bias = g.bias;
+  p.residual = g.residual;
   p.ldr = g.ldr;
   p.act = g.act;
-  p.c_ptr = static_cast<__nv_bfloat16*>(g.c);
+  p.c_ptr = g.c;
   p.ldc = g.ldc;
-  p.pre_ptr = static_cast<__nv_bfloat16*>(g.pre);
+  p.pre_ptr = g.pre;
   p.ldp = g.ldp;
+  p.mark = other;
+  p.call = call;
   p.part = q.part;
   p.ticket = reinterpret_cast<unsigned*>(words) + 64;
   p.status = words;
-  p.tma_c = tma_rows(g.c, g.ldc);
-  p.tma_pre = g.pre && tma_rows(g.pre, g.ldp);
-  if (p.tma_c) ok = ok && encode(&p.c, g.c, g.n, g.m, g.ldc, 1, g.m, 64, 32);
-  if (p.tma_pre) ok = ok && encode(&p.pre, g.pre, g.n, g.m, g.ldp, 1, g.m, 64, 32);
+  const int size = f32 ? 4 : 2;
+  p.tma_c = tma_rows(g.c, g.ldc, size);
+  p.tma_pre = g.pre && tma_rows(g.pre, g.ldp, size);
+  if (p.tma_c) ok = ok && encode(&p.c, f32, g.c, g.n, g.m, g.ldc, 1, g.m, 128 / size, 32);
+  if (p.tma_pre) ok = ok && encode(&p.pre, f32, g.pre, g.n, g.m, g.ldp, 1, g.m, 128 / size, 32);
   if (!ok) return cudaErrorInvalidValue;
-  e = cudaFuncSetAttribute(mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_after(mma_kernel, static_cast<unsigned>(2 * q.deal.pairs), kThreads, kSmem, st, p);
+  return f32 ? launch_mma_t<float>(p, st) : launch_mma_t<__nv_bfloat16>(p, st);
 }
 
 }  // namespace tk

@@ -34,8 +34,8 @@ cudaError_t ops_take_status(cudaStream_t st, int* status);
 
 // Words that each (device, stream) keeps for the operators, zero at first: [0]
 // the status that a kernel sets when a wait runs out, [32] and [64..] tickets
-// that every kernel leaves at zero.
-constexpr int64_t kOpsWords = 16384;
+// that every kernel leaves at zero, [kOpsOther] the last call that met a value that is not finite.
+constexpr int64_t kOpsWords = 16384, kOpsOther = 48;
 
 // SMs of the current device.
 int ops_sm_count();
@@ -68,8 +68,10 @@ struct Product {
 // words: the stream's kOpsWords.
 cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st);
 size_t product_scratch_bytes(const Product& g);
-// The same for BF16 on the tensor cores (kernels_mma.cu).
-cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, cudaStream_t st);
+// The same on the tensor cores (kernels_mma.cu).  F32: words[kOpsOther] becomes `call` when an operand holds a value that
+// is not finite; launch_simt, which makes the product when it finds that mark, then runs in their place.
+cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cudaStream_t st);
+cudaError_t launch_simt(const Product& g, const int* mark, int call, cudaStream_t st);
 size_t mma_scratch_bytes(const Product& g);
 
 // dz = dy * act'(pre) (act != none; dz contiguous) and the column sums of dz

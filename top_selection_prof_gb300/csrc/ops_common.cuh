@@ -120,26 +120,83 @@ cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, si
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// act(z) and act'(z).  relu(NaN) = NaN and relu'(NaN) = 0.  gelu is the exact
-// form z Phi(z), with Phi(z) = (1 + erf(z / sqrt 2)) / 2; silu is z / (1 + e^-z),
-// which is 0 at -inf (the quotient alone would be -inf / inf).
+// act(z) and act'(z), for results of type T.  relu(NaN) = NaN and relu'(NaN) =
+// 0.  gelu is the exact form z Phi(z), silu z / (1 + e^-z); both are 0 at -inf
+// (where their formulas meet inf x 0) and z at inf.
+//
+// f32 results take CUDA's erff and expf.  bf16 results, whose own rounding is
+// 2^-9, take the hardware's exponential and reciprocal (2^-22) and
+//   Phi(-a) = e^(-a^2/2) t (c1 + c2 t + ... + c6 t^5),  t = 1 / (1 + 0.31 a),  a >= 0,
+// the coefficients fitted (weighted least squares, reweighted towards the
+// largest error) to e^(a^2/2) Phi(-a) on [0, 14] with a relative error of at
+// most 4.8e-6: with erff the epilogue of 4096 x 512 x 65536 took 695 us where
+// the product takes 180.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Phi(-a) for 0 <= a <= 16, and e = e^(-a^2/2).
+__device__ __forceinline__ float fast_upper_tail(float a, float* e) {
+  const float t = fast_rcp(fmaf(0.31f, a, 1.0f));
+  *e = fast_exp2(a * a * -0.72134752f);
+  float s = fmaf(t, -0.07392814f, 0.18044704f);
+  s = fmaf(s, t, 0.015749037f);
+  s = fmaf(s, t, 0.13342702f);
+  s = fmaf(s, t, 0.12044213f);
+  s = fmaf(s, t, 0.12386061f);
+  return s * t * *e;
+}
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678118654752f)); }
+__device__ __forceinline__ float relu(float z) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
+  return y;
+}
+
+template <typename T>
 __device__ __forceinline__ float act_value(float z, int act) {
+  constexpr bool kFast = sizeof(T) == 2;
   switch (act) {
-    case kActRelu: return z < 0.0f ? 0.0f : z;
-    case kActGelu: return z == -INFINITY ? 0.0f : z * normal_cdf(z);
-    case kActSilu: return z == -INFINITY ? 0.0f : z / (1.0f + expf(-z));
+    case kActRelu: return relu(z);
+    case kActGelu:
+      if constexpr (kFast) {
+        float a = fabsf(z), e;
+        a = a > 16.0f ? 16.0f : a;  // (NaN stays)
+        const float low = (z < 0.0f ? -a : a) * fast_upper_tail(a, &e);
+        return z >= 0.0f ? z - low : low;
+      }
+      return z == -INFINITY ? 0.0f : z * normal_cdf(z);
+    case kActSilu:
+      if constexpr (kFast) {
+        const float c = z < -100.0f ? -100.0f : z;
+        return c * fast_rcp(1.0f + fast_exp2(c * -1.44269504f));
+      }
+      return z == -INFINITY ? 0.0f : z / (1.0f + expf(-z));
     default: return z;
   }
 }
+template <typename T>
 __device__ __forceinline__ float act_slope(float z, int act) {
+  constexpr bool kFast = sizeof(T) == 2;
   switch (act) {
     case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
-    case kActGelu: return fabsf(z) > 16.0f ? (z > 0.0f ? 1.0f : 0.0f)
-                                            : normal_cdf(z) + z * expf(-0.5f * z * z) * 0.3989422804014327f;
+    case kActGelu:
+      if (fabsf(z) > 16.0f) return z > 0.0f ? 1.0f : 0.0f;
+      if constexpr (kFast) {
+        float e;
+        const float q = fast_upper_tail(fabsf(z), &e);
+        return fmaf(z * e, 0.39894228f, z < 0.0f ? q : 1.0f - q);
+      }
+      return normal_cdf(z) + z * expf(-0.5f * z * z) * 0.3989422804014327f;
     case kActSilu: {
-      if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;  // (the formula meets inf x 0 beyond)
-      const float s = 1.0f / (1.0f + expf(-z));
+      if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;
+      const float s = kFast ? fast_rcp(1.0f + fast_exp2(z * -1.44269504f)) : 1.0f / (1.0f + expf(-z));
       return s * (1.0f + z * (1.0f - s));
     }
     default: return 1.0f;
