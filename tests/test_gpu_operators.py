@@ -137,6 +137,31 @@ def test_linear_is_exact_on_whole_numbers(tk, dtype, rows, inner, outer):
     same_bits(tk.linear(strided(x, 64, 0), strided(w, 32 if inner % 8 == 0 else 5, 0)), z, "apart")
 
 
+# More tiles than the GPU takes at once, over short and long inner extents: whole waves and a rest that does not fill one,
+# few tiles with many products each, and (short inner) columns of tiles that a pair of blocks goes down.
+MANY = [(300, 200, 20000), (600, 512, 13000), (1030, 72, 9001), (300, 520, 20000), (2100, 600, 2600), (500, 20000, 300),
+        (40, 9000, 700)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,inner,outer", MANY)
+def test_linear_over_many_tiles_is_exact_on_whole_numbers(tk, dtype, rows, inner, outer):
+    g = gen(inner)
+    x, w = ints((rows, inner), dtype, g), ints((outer, inner), dtype, g)
+    b, r, dy = ints((outer,), dtype, g, -9, 9), ints((rows, outer), dtype, g, -9, 9), ints((rows, outer), dtype, g)
+    xd, wd, bd, rd, dyd = (t.cuda() for t in (x, w, b, r, dy))
+    z = (xd.double() @ wd.double().T + bd.double()).cpu()
+    same_bits(tk.linear(xd, wd, bd, act="relu"), z.clamp(min=0), "relu")
+    y, pre = tk.linear(xd, wd, bd, act="relu", residual=rd, save_pre=True)
+    same_bits(pre, z, "pre")
+    same_bits(y, z.clamp(min=0) + r.double(), "residual")
+    same_bits(tk.linear(strided(x), strided(w, 1, 0), bd), z, "strided")
+    dx, dw, db = tk.linear_backward(dyd, xd, wd)
+    same_bits(dx, (dyd.double() @ wd.double()).cpu(), "dx")
+    same_bits(dw, (dyd.double().T @ xd.double()).cpu(), "dw")
+    same_bits(db, dy.double().sum(0), "dbias")
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,inner,outer", [(1, 512, 300), (7, 33, 129), (150, 700, 260)])
