@@ -294,19 +294,29 @@ __device__ __forceinline__ void store_plain(uint32_t staging, T* dst, int64_t ld
 template <typename T>
 __device__ __forceinline__ void stage_residual(uint32_t staging, const T* src, int64_t ld, int64_t row0, int64_t rows,
                                                int64_t col0, int64_t cols, int lane) {
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
+  constexpr int kEach = 4 / sizeof(T), kRows = 32 / kEach;  // loads of 32 values in flight
 #pragma unroll
-    for (int e = 0; e < 4 / int(sizeof(T)); ++e) {
-      const int c = e * 32 + lane;
-      const uint32_t addr = piece(staging, r, c * int(sizeof(T)) / 16) + (c * sizeof(T)) % 16;
-      T v = from_f32<T>(0.0f);
-      if (row0 + r < rows && col0 + c < cols) v = src[(row0 + r) * ld + col0 + c];
-      if constexpr (sizeof(T) == 2)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(v)) : "memory");
-      else
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-    }
+  for (int r0 = 0; r0 < 32; r0 += kRows) {
+    T v[kRows][kEach];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int c = e * 32 + lane;
+        v[r][e] = from_f32<T>(0.0f);
+        if (row0 + r0 + r < rows && col0 + c < cols) v[r][e] = src[(row0 + r0 + r) * ld + col0 + c];
+      }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int c = e * 32 + lane;
+        const uint32_t addr = piece(staging, r0 + r, c * int(sizeof(T)) / 16) + (c * sizeof(T)) % 16;
+        if constexpr (sizeof(T) == 2)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(v[r][e])) : "memory");
+        else
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v[r][e]) : "memory");
+      }
   }
 }
 // 32 values of the lane's row, rounded to T, into staging: half `h` of its 128 bytes (bf16), or all (f32).
@@ -750,28 +760,43 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* sr
   }
 }
 
-// The three bf16 parts of an f32 operand, `plane` values apart, rows of `ld`
+// The three bf16 parts of both f32 operands, `plane` values apart, rows of `ld`
 // values.  A part is the leading 8 bits of what the parts before it left, so
 // the three hold all 24.  *other becomes `call` when a value is not finite.
-__global__ void __launch_bounds__(256) split_rows_kernel(const float* src, int64_t lds, int64_t rows, int64_t cols,
-                                                         __nv_bfloat16* dst, int64_t ld, int64_t plane, int* other, int call) {
+struct Split {
+  const float* src;
+  int64_t lds, rows, cols;
+  __nv_bfloat16* dst;
+  int64_t ld, plane;
+  unsigned blocks;
+};
+constexpr int kSplitEach = 4;  // values of a thread, next to each other
+__global__ void __launch_bounds__(256) split_rows_kernel(const Split a, const Split b, int* other, int call) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t per = (cols + 1023) / 1024;
-  const int64_t r = blockIdx.x / per, c0 = (blockIdx.x % per) * 1024 + threadIdx.x;
+  const bool second = blockIdx.x >= a.blocks;
+  const Split& s = second ? b : a;
+  const int64_t per = (s.cols + kSplitEach - 1) / kSplitEach;
+  const int64_t at = int64_t(blockIdx.x - (second ? a.blocks : 0)) * 256 + threadIdx.x;
+  if (at >= s.rows * per) return;
+  const int64_t r = at / per, c = (at - r * per) * kSplitEach;
+  const float* src = s.src + r * s.lds + c;
+  float v[kSplitEach];
   bool finite = true;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int64_t c = c0 + e * 256;
-    if (r >= rows || c >= cols) continue;
-    float v = src[r * lds + c];
-    finite = finite && fabsf(v) < INFINITY;
+  for (int e = 0; e < kSplitEach; ++e) v[e] = c + e < s.cols ? src[e] : 0.0f;
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-      dst[q * plane + r * ld + c] = __ushort_as_bfloat16(static_cast<unsigned short>(top >> 16));
-      v -= __uint_as_float(top);
+  for (int e = 0; e < kSplitEach; ++e) finite = finite && fabsf(v[e]) < INFINITY;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    uint32_t top[kSplitEach];
+#pragma unroll
+    for (int e = 0; e < kSplitEach; ++e) {
+      top[e] = __float_as_uint(v[e]) & 0xffff0000u;
+      v[e] -= __uint_as_float(top[e]);
     }
+    // (rows of the parts hold a multiple of 8 values: the last store may go past cols, not past the row)
+    *reinterpret_cast<uint2*>(s.dst + q * s.plane + r * s.ld + c) = make_uint2((top[0] >> 16) | top[1], (top[2] >> 16) | top[3]);
   }
   if (!finite) *other = call;
 }
@@ -849,7 +874,7 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
   const double whole = static_cast<double>((tiles + slots - 1) / slots - rest_waves) * d.k_blocks;
   const double even = static_cast<double>(shared) * d.k_blocks / slots;
   const double parts = static_cast<double>(slots) / shared;
-  const double join = 15.0 + 0.5 * parts + 0.1 * static_cast<double>(tiles) * d.k_blocks / slots;
+  const double join = 12.0 + 0.5 * parts + 0.1 * static_cast<double>(tiles) * d.k_blocks / slots;
   if (tiles % slots != 0 && (whole - even) * kStageUs > join && shared * d.k_blocks >= 2 * slots && shared * d.k_blocks <= INT32_MAX &&
       shared * 2 * kEpiWarps <= kOpsWords - 64) {
     d.pairs = slots;
@@ -873,16 +898,19 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
   return true;
 }
 
-cudaError_t prepare_rows(const Operand& o, int64_t i, int64_t k, bool f32, __nv_bfloat16* dst, int64_t ld, int* other, int call,
-                         cudaStream_t st) {
+cudaError_t align_rows(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_t ld, cudaStream_t st) {
   const int64_t rows = operand_rows(o, i, k), cols = operand_cols(o, i, k);
   const int64_t blocks = rows * ((cols + 1023) / 1024);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
-  if (f32)
-    return launch_after(split_rows_kernel, grid, 256, 0, st, static_cast<const float*>(o.p), o.ld, rows, cols, dst, ld, rows * ld,
-                        other, call);
-  return launch_after(align_rows_kernel, grid, 256, 0, st, static_cast<const __nv_bfloat16*>(o.p), o.ld, rows, cols, dst, ld);
+  return launch_after(align_rows_kernel, static_cast<unsigned>(blocks), 256, 0, st, static_cast<const __nv_bfloat16*>(o.p), o.ld,
+                      rows, cols, dst, ld);
+}
+bool split_of(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_t ld, Split* s) {
+  const int64_t rows = operand_rows(o, i, k), cols = operand_cols(o, i, k);
+  const int64_t blocks = (rows * ((cols + kSplitEach - 1) / kSplitEach) + 255) / 256;
+  if (blocks > INT32_MAX / 2) return false;
+  *s = Split{static_cast<const float*>(o.p), o.ld, rows, cols, dst, ld, rows * ld, static_cast<unsigned>(blocks)};
+  return true;
 }
 
 template <typename T>
@@ -907,8 +935,14 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   const bool f32 = g.dtype == kF32;
   int* other = words + kOpsOther;
   cudaError_t e = cudaSuccess;
-  if (q.copy_a) e = prepare_rows(g.a, g.m, g.k, f32, q.copy_a, q.ld_a, other, call, st);
-  if (e == cudaSuccess && q.copy_b) e = prepare_rows(g.b, g.n, g.k, f32, q.copy_b, q.ld_b, other, call, st);
+  if (f32) {
+    Split a, b;
+    if (!split_of(g.a, g.m, g.k, q.copy_a, q.ld_a, &a) || !split_of(g.b, g.n, g.k, q.copy_b, q.ld_b, &b)) return cudaErrorInvalidValue;
+    e = launch_after(split_rows_kernel, a.blocks + b.blocks, 256, 0, st, a, b, other, call);
+  } else {
+    if (q.copy_a) e = align_rows(g.a, g.m, g.k, q.copy_a, q.ld_a, st);
+    if (e == cudaSuccess && q.copy_b) e = align_rows(g.b, g.n, g.k, q.copy_b, q.ld_b, st);
+  }
   if (e == cudaSuccess && f32) e = launch_simt(g, other, call, st);
   if (e != cudaSuccess) return e;
   MmaParams p{};
