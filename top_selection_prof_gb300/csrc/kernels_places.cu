@@ -32,20 +32,19 @@ struct GroupHeader {
   unsigned pieces;  // pieces of long groups
   unsigned longs;   // long groups
   unsigned tasks;   // warps' tasks of the sums by column
+  unsigned taken;   // items taken by the warps that sum them, after each warp's first
 };
-struct PieceRec {
-  unsigned group, index, slot0, count;  // piece `index` of a group whose first slot is slot0; the group's places
+// What one warp (or block) sums: a piece of a long group, or, by column, a few
+// short groups next to each other.
+struct __align__(16) Item {
+  unsigned group, columns, start, places;  // first group and how many (0: a piece); where their places lie
+  unsigned slot0, index, pieces, unused;   // piece `index` of a group in `pieces`, whose first slot is slot0
 };
 // A grouped place.
 struct __align__(16) Entry {
   uint32_t s, other;  // the place and its other coordinate
   float coef;
   uint32_t group;
-};
-// Columns [c0, c0 + columns) that one warp sums: none of them long, their
-// places, at most kColPiece, next to each other from `start` on.
-struct __align__(16) Task {
-  unsigned c0, columns, start, places;
 };
 // Groups of one call, in its scratch.
 struct Groups {
@@ -55,8 +54,8 @@ struct Groups {
   uint4* seen;        // per place: group, other coordinate, rank in the group as counted (kNoPlace: none), coefficient
   Entry* order;       // the places by group
   Entry* sorted;      // long groups in order of s
-  PieceRec* pieces;
-  Task* tasks;        // sums by column (else null)
+  Item* pieces;       // of long groups
+  Item* tasks;        // sums by column (else null): short groups that share a warp
   unsigned* longs;
   unsigned* ticket;   // pieces of a long group (and tile of d) that are done, counted at its first slot; zero at first
   float* part;        // pieces x d sums
@@ -77,10 +76,10 @@ Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int piece, int64_
   g.seen = sc.take<uint4>(total);
   g.order = sc.take<Entry>(total);
   g.sorted = sc.take<Entry>(g.max_longs ? total : 0);
-  g.pieces = sc.take<PieceRec>(g.max_pieces);
+  g.pieces = sc.take<Item>(g.max_pieces);
   // a span of groups that share no task has more than `piece` places
   g.max_tasks = tasks ? (groups + kSpan - 1) / kSpan + (kSpan - 1) * (total / piece) : 0;
-  g.tasks = tasks ? sc.take<Task>(g.max_tasks) : nullptr;
+  g.tasks = tasks ? sc.take<Item>(g.max_tasks) : nullptr;
   g.longs = sc.take<unsigned>(g.max_longs);
   g.ticket = sc.take<unsigned>(g.n_tickets);
   g.part = sc.take<float>(g.max_pieces * d);
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) zero_groups_kernel(const Groups g) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (i == 0) *g.hdr = GroupHeader{0, 0, 0, 0};
+  if (i == 0) *g.hdr = GroupHeader{0, 0, 0, 0, 0};
   if (i < g.n_groups) g.count[i] = 0;
   if (i < g.n_tickets) g.ticket[i] = 0;
 }
@@ -198,14 +197,16 @@ __global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g
     if (lane == 0 && who) slot = atomicAdd(&g.hdr->tasks, static_cast<unsigned>(__popc(who)));
     slot = __shfl_sync(~0u, slot, 0) + __popc(who & lanemask_lt());
     if (leads)
-      g.tasks[slot] = Task{static_cast<unsigned>(i), static_cast<unsigned>(min(int64_t(size), g.n_groups - i)), start, places};
+      g.tasks[slot] = Item{static_cast<unsigned>(i), static_cast<unsigned>(min(int64_t(size), g.n_groups - i)), start, places,
+                           0, 0, 1, 0};
   }
   if (i >= g.n_groups) return;
   g.start[i] = start;
   if (cnt > piece) {
     const unsigned np = (cnt + piece - 1) / piece;
     const unsigned slot0 = atomicAdd(&g.hdr->pieces, np);
-    for (unsigned q = 0; q < np; ++q) g.pieces[slot0 + q] = PieceRec{static_cast<unsigned>(i), q, slot0, cnt};
+    for (unsigned q = 0; q < np; ++q)
+      g.pieces[slot0 + q] = Item{static_cast<unsigned>(i), 0, start + q * piece, min(piece, cnt - q * piece), slot0, q, np, 0};
     g.longs[atomicAdd(&g.hdr->longs, 1u)] = static_cast<unsigned>(i);
   }
 }
@@ -385,14 +386,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) row_sums_warp_kernel(const Row
       if (k * 32 + lane < cnt) ent[rank[k]] = make_uint2(e[k].other, __float_as_uint(e[k].coef));
   } else {
     if (w - p.rows >= q.g.hdr->pieces) return;
-    const PieceRec rec = q.g.pieces[w - p.rows];
+    const Item rec = q.g.pieces[w - p.rows];
     row = rec.group;
     index = rec.index;
     slot0 = rec.slot0;
-    n_pieces = (rec.count + kRowPiece - 1) / kRowPiece;
-    cnt = static_cast<int>(min(unsigned(kRowPiece), rec.count - index * kRowPiece));
+    n_pieces = rec.pieces;
+    cnt = static_cast<int>(rec.places);
     for (int i = lane; i < cnt; i += 32) {
-      const Entry e = q.g.sorted[q.g.start[row] + index * kRowPiece + i];
+      const Entry e = q.g.sorted[rec.start + i];
       ent[i] = make_uint2(e.other, __float_as_uint(e.coef));
     }
   }
@@ -490,14 +491,14 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const RowParams q) {
     }
   } else if (w < q.g.max_pieces) {
     if (w >= q.g.hdr->pieces) return;
-    const PieceRec rec = q.g.pieces[w];
+    const Item rec = q.g.pieces[w];
     row = rec.group;
     index = rec.index;
     slot0 = rec.slot0;
-    n_pieces = (rec.count + kRowPiece - 1) / kRowPiece;
-    cnt = static_cast<int>(min(unsigned(kRowPiece), rec.count - index * kRowPiece));
+    n_pieces = rec.pieces;
+    cnt = static_cast<int>(rec.places);
     if (t < cnt) {
-      const Entry e = q.g.sorted[q.g.start[row] + index * kRowPiece + t];
+      const Entry e = q.g.sorted[rec.start + t];
       ent[t] = make_uint2(e.other, __float_as_uint(e.coef));
     }
   } else {
@@ -679,28 +680,41 @@ struct ColumnStream {
   int lane, total;
   bool want_dw;
   int64_t d0;
-  float acc[CHUNKS][VEC];
+  static constexpr int kPairs = VEC / 2;
+  Pair acc2[CHUNKS][kPairs ? kPairs : 1];  // sums, two a register pair
+  float acc1[CHUNKS];                      // (VEC == 1)
 
   __device__ __forceinline__ int64_t at(int h) const { return d0 + (h * 32 + lane) * VEC; }
   __device__ __forceinline__ bool in(int h) const { return FULL || at(h) < c.d; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int h = 0; h < CHUNKS; ++h) {
+      acc1[h] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) acc2[h][i] = Pair::of(0.0f, 0.0f);
+    }
+  }
   // The sums so far are column `col`'s.
   __device__ __forceinline__ void flush(int64_t col) {
 #pragma unroll
     for (int h = 0; h < CHUNKS; ++h) {
       if (in(h)) {
+        Vec<T, VEC> out;
+        if constexpr (VEC == 1) {
+          out.v[0] = acc1[h];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) acc2[h][i].get(&out.v[2 * i], &out.v[2 * i + 1]);
+        }
         if (part) {
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) part[at(h) + v] = acc[h][v];
+          for (int v = 0; v < VEC; ++v) part[at(h) + v] = out.v[v];
         } else {
-          Vec<T, VEC> out;
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) out.v[v] = acc[h][v];
           out.store_stream(static_cast<T*>(c.dw) + col * c.d + at(h));
         }
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[h][v] = 0.0f;
     }
+    clear();
   }
   // Places [i0, i0 + n), n <= AHEAD (WHOLE: n == AHEAD).
   template <bool WHOLE>
@@ -729,20 +743,29 @@ struct ColumnStream {
       if (WHOLE || a < n) {
         const float f = ent[i0 + a].coef;
         const uint32_t group = ent[i0 + a].group;
+        const Pair f2 = Pair::of(f, f);
+        Pair dot2 = Pair::of(0.0f, 0.0f);
 #pragma unroll
         for (int h = 0; h < CHUNKS; ++h) {
           if (in(h)) {
-            Vec<T, VEC> t;
-            t.set_raw(xv[a][h]);
+            if constexpr (VEC == 1) {
+              const float t = to_f32(xv[a][h].u);
+              acc1[h] = fmaf(f, t, acc1[h]);
+              if constexpr (DOTS) dot[a] = fmaf(t, to_f32(wv[a][h].u), dot[a]);
+            } else {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) acc[h][v] = fmaf(f, t.v[v], acc[h][v]);
-            if constexpr (DOTS) {
-              Vec<T, VEC> u;
-              u.set_raw(wv[a][h]);
-#pragma unroll
-              for (int v = 0; v < VEC; ++v) dot[a] = fmaf(t.v[v], u.v[v], dot[a]);
+              for (int i = 0; i < kPairs; ++i) {
+                const Pair t = xv[a][h].pair(i);
+                acc2[h][i].fma(f2, t);
+                if constexpr (DOTS) dot2.fma(t, wv[a][h].pair(i));
+              }
             }
           }
+        }
+        if constexpr (DOTS && VEC > 1) {
+          float lo, hi;
+          dot2.get(&lo, &hi);
+          dot[a] = lo + hi;
         }
         // (the entry past the last has no group's number)
         if (want_dw && ent[i0 + a + 1].group != group) flush(group);
@@ -769,10 +792,7 @@ struct ColumnStream {
     }
   }
   __device__ __forceinline__ void tile() {
-#pragma unroll
-    for (int h = 0; h < CHUNKS; ++h)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[h][v] = 0.0f;
+    clear();
     int i0 = 0;
 #pragma unroll 1
     for (; i0 + AHEAD <= total; i0 += AHEAD) batch<true>(i0, AHEAD);
@@ -809,6 +829,8 @@ __device__ __noinline__ void join_pieces(const float* part, const float* part_bi
 template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL, bool DOTS>
 __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel(const ColParams q) {
   __shared__ Entry ent_all[kColWarps][kColPiece + 1];
+  __shared__ Entry raw_all[kColWarps][kColPiece];  // the next item's places on their way
+  __shared__ Item item_all[kColWarps][2];          // and the records of the two next items
   __shared__ float dots_all[kColWarps][kColPiece];
   static_assert(kColPiece == 32, "a place a lane");
   grid_dependency_wait();
@@ -816,37 +838,56 @@ __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel
   const ColumnSums& c = q.c;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   Entry* ent = ent_all[warp];
+  Entry* raw = raw_all[warp];
+  Item* items = item_all[warp];
   float* dots = dots_all[warp];
   T* dw = static_cast<T*>(c.dw);
   T* dbias = static_cast<T*>(c.dbias);
   using Stream = ColumnStream<T, VEC, CHUNKS, AHEAD, FULL, DOTS>;
-  Stream st{c, ent, dots, nullptr, lane, 0, dw != nullptr, 0, {}};
-  const unsigned pieces = q.g.hdr->pieces, work = pieces + q.g.hdr->tasks;
-  for (unsigned wk = blockIdx.x * kColWarps + warp; wk < work; wk += gridDim.x * kColWarps) {
-    unsigned n_pieces = 1, slot0 = 0, slot = 0, empty = 0;  // empty: columns of the task without a place
-    int64_t c0;
-    int total;
+  Stream st{c, ent, dots, nullptr, lane, 0, dw != nullptr, 0};
+  const unsigned pieces = q.g.hdr->pieces, work = pieces + q.g.hdr->tasks, step = gridDim.x * kColWarps;
+  // Records and places are copied to shared memory ahead of their use: the record two items ahead, the places one.
+  auto fetch_item = [&](unsigned wk, int slot) {
+    if (wk < work && lane < 2) {
+      const Item* from = wk < pieces ? q.g.pieces + wk : q.g.tasks + (wk - pieces);
+      copy_async16(reinterpret_cast<uint4*>(items + slot) + lane, reinterpret_cast<const uint4*>(from) + lane);
+    }
+  };
+  auto fetch_places = [&](unsigned wk, int slot) {
+    if (wk < work && lane < static_cast<int>(items[slot].places))
+      copy_async16(raw + lane, (items[slot].columns ? q.g.order : q.g.sorted) + items[slot].start + lane);
+  };
+  // Each warp's first two items are its own; the others it takes from a counter, three ahead.
+  unsigned wk = blockIdx.x * kColWarps + warp, next = wk + step, after = 0;
+  auto take = [&] { return lane == 0 ? 2 * step + atomicAdd(&q.g.hdr->taken, 1u) : 0u; };
+  fetch_item(wk, 0);
+  fetch_item(next, 1);
+  after = take();
+  copy_async_wait();
+  __syncwarp();
+  fetch_places(wk, 0);
+  for (unsigned turn = 0; wk < work; turn ^= 1) {
+    copy_async_wait();
+    __syncwarp();
+    const Item item = items[turn];
+    const int64_t c0 = item.group;
+    const int total = static_cast<int>(item.places);
+    const unsigned n_pieces = item.pieces, slot = item.slot0 + item.index;
     Entry e{kNoPlace, 0, 0.0f, kNoPlace};
+    if (lane < total) e = raw[lane];
+    __syncwarp();
+    wk = next;
+    next = __shfl_sync(~0u, after, 0);
+    fetch_item(next, turn);
+    fetch_places(wk, turn ^ 1);
+    after = take();
     int rank = lane;
-    __syncwarp();  // (the last piece of work has been read from shared memory)
-    if (wk < pieces) {
-      const PieceRec rec = q.g.pieces[wk];
-      c0 = rec.group;
-      slot0 = rec.slot0;
-      slot = slot0 + rec.index;
-      n_pieces = (rec.count + kColPiece - 1) / kColPiece;
-      total = static_cast<int>(min(unsigned(kColPiece), rec.count - rec.index * kColPiece));
-      if (lane < total) e = q.g.sorted[q.g.start[c0] + rec.index * kColPiece + lane];
-    } else {
-      const Task task = q.g.tasks[wk - pieces];
-      c0 = task.c0;
-      total = static_cast<int>(task.places);
-      const bool bare = lane < static_cast<int>(task.columns) && q.g.count[c0 + lane] == 0;
-      if (lane < total) e = q.g.order[task.start + lane];
-      empty = __ballot_sync(~0u, bare);
+    unsigned empty = 0;  // columns of the item without a place
+    if (item.columns) {
+      empty = ~__reduce_or_sync(~0u, lane < total ? 1u << (e.group - item.group) : 0u) & ((1u << item.columns) - 1u);
       if (total > 1) {
-        // groups in 3 bits (their place in the task) above s: one number to compare
-        const uint64_t key = (uint64_t(e.group - static_cast<uint32_t>(c0)) << 32) | e.s;
+        // groups (their place in the item) above s: one number to compare
+        const uint64_t key = (uint64_t(e.group - item.group) << 32) | e.s;
         rank = 0;
         for (int i = 0; i < total; ++i) rank += __shfl_sync(~0u, key, i) < key;
       }
@@ -882,11 +923,11 @@ __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel
     __threadfence();
     __syncwarp();
     unsigned seen = 0;
-    if (lane == 0) seen = atomicAdd(&q.g.ticket[slot0], 1u);
+    if (lane == 0) seen = atomicAdd(&q.g.ticket[item.slot0], 1u);
     seen = __shfl_sync(~0u, seen, 0);
     if (seen != n_pieces - 1) continue;
     __threadfence();
-    join_pieces<T, VEC>(q.g.part + int64_t(slot0) * c.d, q.g.part_bias + slot0, n_pieces, c.d, dw ? dw + c0 * c.d : nullptr,
+    join_pieces<T, VEC>(q.g.part + int64_t(item.slot0) * c.d, q.g.part_bias + item.slot0, n_pieces, c.d, dw ? dw + c0 * c.d : nullptr,
                         dbias ? dbias + c0 : nullptr);
   }
 }

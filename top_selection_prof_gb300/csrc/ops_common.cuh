@@ -26,12 +26,37 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Two f32 side by side in a register pair, multiplied and added in one instruction.
+struct Pair {
+  uint64_t u;
+  __device__ __forceinline__ static Pair of(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.u) : "f"(a), "f"(b));
+    return p;
+  }
+  __device__ __forceinline__ void get(float* a, float* b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(u)); }
+  __device__ __forceinline__ void fma(Pair a, Pair b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(u) : "l"(a.u), "l"(b.u)); }
+};
+
+// 16 bytes from global to shared memory without passing through registers; the
+// thread's copies are in place after copy_async_wait().
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // VEC consecutive values as they are stored.
 template <typename T, int VEC>
 struct Raw {
   uint4 u;
   __device__ __forceinline__ void load_nc(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  // Values 2 i and 2 i + 1 as f32.
+  __device__ __forceinline__ Pair pair(int i) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 4) return Pair::of(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    return Pair::of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
 };
 template <typename T>
 struct Raw<T, 1> {
