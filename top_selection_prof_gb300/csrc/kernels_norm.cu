@@ -4,10 +4,11 @@
 // The tensors' values are cut into chunks, dealt to the blocks in turn (all
 // blocks then read close to each other: one run a block took 45 us where this
 // takes 28); the table of tensors goes to the kernel as its parameter, so
-// nothing is copied to the device.  A thread sums a chunk's squares in f32 and
-// adds them in f64; the blocks' sums are added in their order.  Where the f32
-// squares overflow, or are so small that bits are lost, the chunk is summed
-// again in f64, so that the norm is exact to f32 for any finite input.
+// nothing is copied to the device.  A thread sums a chunk's squares in f32
+// and adds the chunks' sums in two f32 (a sum and what its rounding lost: the
+// card's f64 is slow); the blocks' sums are added in f64 in their order.  Where
+// the f32 squares overflow, or are so small that bits are lost, the chunk is
+// summed again in f64, so that the norm is exact to f32 for any finite input.
 //
 // Few values (at most kFewValues) take one launch: a cluster of blocks holds
 // them in registers, exchanges its sums through distributed shared memory and
@@ -24,10 +25,13 @@ namespace tk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;            // 16-byte loads of a thread in flight
+constexpr int kAhead = 4;            // 16-byte loads of a thread in flight
 constexpr int kTable = 640;          // tensors of one launch (the kernel's parameter holds their table)
 constexpr int kFewTensors = 48;      // the smaller table of calls with few tensors
 constexpr int kMaxBlocks = 2048;
+// Bytes at the end of the tensors whose lines L2 is asked to keep from the sums to the scaling (67M bf16 values: 71.7 us
+// without, 69.6 with 48 MB, 67.9 with 64, 68.5 with 96).
+constexpr int64_t kKeepBytes = int64_t(64) << 20;
 constexpr int kCluster = 8;
 constexpr int kFewThreads = 512, kFewEach = 16;  // values of a thread, held in registers
 constexpr int64_t kFewValues = int64_t(kCluster) * kFewThreads * kFewEach;
@@ -40,6 +44,7 @@ struct TensorTable {
   uint8_t f32[N];
   int tensors;
   int64_t chunk;   // values of a chunk (a multiple of 8)
+  int64_t keep;    // chunks at the end whose lines L2 is asked to keep for the scaling
 };
 struct NormScratch {
   double* part;       // per block of this launch
@@ -64,11 +69,23 @@ __device__ __forceinline__ void each_part(const TensorTable<N>& t, int64_t v0, i
   }
 }
 
+// L2's policy for lines that are read again soon.
+__device__ __forceinline__ uint64_t l2_evict_last_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "l"(policy));
+  return v;
+}
 // Goes over the block's values of [p, p + n), from the end when BACKWARD: whole
 // 16-byte vectors (aligned to those of p) kAhead at a time through `vec(values,
 // place)`, single values at the ends through `one(value, place)`.
 template <typename T, bool BACKWARD, typename V, typename O>
-__device__ __forceinline__ void each_value(const T* p, int64_t n, V vec, O one) {
+__device__ __forceinline__ void each_value(const T* p, int64_t n, uint64_t policy, V vec, O one) {
   constexpr int kVec = 16 / sizeof(T);
   const int64_t head = min(n, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int64_t(sizeof(T)));
   const int64_t vecs = (n - head) / kVec;
@@ -78,7 +95,7 @@ __device__ __forceinline__ void each_value(const T* p, int64_t n, V vec, O one) 
   auto rest = [&] {  // less than a whole step, at the end
     for (int64_t i = steps * (kThreads * kAhead) + threadIdx.x; i < vecs; i += kThreads) {
       Vec<T, kVec> v;
-      v.set(q[i - threadIdx.x]);
+      v.set(load_hint(q + (i - threadIdx.x), policy));
       vec(v, head + i * kVec);
     }
   };
@@ -88,7 +105,7 @@ __device__ __forceinline__ void each_value(const T* p, int64_t n, V vec, O one) 
     const int64_t i0 = (BACKWARD ? steps - 1 - s : s) * (kThreads * kAhead);
     uint4 raw[kAhead];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) raw[a] = q[i0 + a * kThreads];
+    for (int a = 0; a < kAhead; ++a) raw[a] = load_hint(q + i0 + a * kThreads, policy);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       Vec<T, kVec> v;
@@ -101,11 +118,11 @@ __device__ __forceinline__ void each_value(const T* p, int64_t n, V vec, O one) 
 }
 
 template <typename T>
-__device__ __noinline__ double part_squares_wide(const T* p, int64_t n) {
+__device__ __noinline__ double part_squares_wide(const T* p, int64_t n, uint64_t policy) {
   constexpr int kVec = 16 / sizeof(T);
   double wide = 0.0;
   each_value<T, false>(
-      p, n,
+      p, n, policy,
       [&](const Vec<T, kVec>& v, int64_t) {
 #pragma unroll
         for (int c = 0; c < kVec; ++c) wide += static_cast<double>(v.v[c]) * v.v[c];
@@ -114,8 +131,22 @@ __device__ __noinline__ double part_squares_wide(const T* p, int64_t n) {
   return wide;
 }
 
+// A sum in two f32: the rounded sum, and what the roundings lost.
+struct TwoSum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {
+    const float s = hi + v, b = s - hi;
+    lo += (hi - (s - b)) + (v - b);
+    hi = s;
+  }
+};
+struct Squares {
+  TwoSum sum{0.0f, 0.0f};
+  double wide = 0.0;  // what f32 could not hold
+};
+
 template <typename T>
-__device__ __forceinline__ double part_squares(const T* p, int64_t n) {
+__device__ __forceinline__ void part_squares(const T* p, int64_t n, uint64_t policy, Squares* to) {
   constexpr int kVec = 16 / sizeof(T);
   float sum = 0.0f, most = 0.0f;
   auto add = [&](float v) {
@@ -123,26 +154,26 @@ __device__ __forceinline__ double part_squares(const T* p, int64_t n) {
     most = fmaxf(most, fabsf(v));
   };
   each_value<T, false>(
-      p, n,
+      p, n, policy,
       [&](const Vec<T, kVec>& v, int64_t) {
 #pragma unroll
         for (int c = 0; c < kVec; ++c) add(v.v[c]);
       },
       [&](float v, int64_t) { add(v); });
-  // f32 squares neither overflow nor lose bits between these; zeros, NaN and infinities stay what they are
-  if (most == 0.0f || !(most < INFINITY) || (most > 1e-15f && most < 1e17f)) return static_cast<double>(sum);
-  return part_squares_wide(p, n);
+  // f32 squares neither overflow nor lose bits between these (a block's sum of them stays below 2^127 for any tensor
+  // that fits the card); zeros stay what they are, NaN and infinities go on through f64
+  if (most == 0.0f && sum == 0.0f) return;
+  if (most > 1e-15f && most < 1e12f && sum < INFINITY) to->sum.add(sum);
+  else to->wide += part_squares_wide(p, n, policy);
 }
 
 template <int N>
-__device__ __forceinline__ double chunk_squares(const TensorTable<N>& t, int64_t chunk) {
+__device__ __forceinline__ void chunk_squares(const TensorTable<N>& t, int64_t chunk, uint64_t policy, Squares* to) {
   const int64_t v0 = chunk * t.chunk, v1 = min(v0 + t.chunk, t.end[t.tensors - 1]);
-  double sum = 0.0;
   each_part(t, v0, v1, [&](int i, int64_t at, int64_t n) {
-    sum += t.f32[i] ? part_squares(static_cast<const float*>(t.in[i]) + at, n)
-                    : part_squares(static_cast<const __nv_bfloat16*>(t.in[i]) + at, n);
+    if (t.f32[i]) part_squares(static_cast<const float*>(t.in[i]) + at, n, policy, to);
+    else part_squares(static_cast<const __nv_bfloat16*>(t.in[i]) + at, n, policy, to);
   });
-  return sum;
 }
 template <int N>
 __device__ __forceinline__ int64_t chunks_of(const TensorTable<N>& t) {
@@ -165,11 +196,11 @@ __device__ __forceinline__ float scale_of(float norm, float max_norm) {
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_part(const T* p, T* out, int64_t n, float f) {
+__device__ __forceinline__ void scale_part(const T* p, T* out, int64_t n, uint64_t policy, float f) {
   constexpr int kVec = 16 / sizeof(T);
   const bool apart = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0;
   each_value<T, true>(
-      p, n,
+      p, n, policy,
       [&](const Vec<T, kVec>& v, int64_t at) {
         Vec<T, kVec> o;
 #pragma unroll
@@ -184,27 +215,43 @@ __device__ __forceinline__ void scale_part(const T* p, T* out, int64_t n, float 
       [&](float v, int64_t at) { out[at] = from_f32<T>(v * f); });
 }
 template <int N>
-__device__ __forceinline__ void scale_chunk(const TensorTable<N>& t, int64_t chunk, float f) {
+__device__ __forceinline__ void scale_chunk(const TensorTable<N>& t, int64_t chunk, uint64_t policy, float f) {
   const int64_t v0 = chunk * t.chunk, v1 = min(v0 + t.chunk, t.end[t.tensors - 1]);
   each_part(t, v0, v1, [&](int i, int64_t at, int64_t n) {
     if (f == 1.0f && t.in[i] == t.out[i]) return;
     if (t.f32[i])
-      scale_part(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, n, f);
+      scale_part(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, n, policy, f);
     else
-      scale_part(static_cast<const __nv_bfloat16*>(t.in[i]) + at, static_cast<__nv_bfloat16*>(t.out[i]) + at, n, f);
+      scale_part(static_cast<const __nv_bfloat16*>(t.in[i]) + at, static_cast<__nv_bfloat16*>(t.out[i]) + at, n, policy, f);
   });
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 4) squares_kernel(const __grid_constant__ TensorTable<N> t, NormScratch s, bool first,
+__global__ void __launch_bounds__(kThreads, 8) squares_kernel(const __grid_constant__ TensorTable<N> t, NormScratch s, bool first,
                                                            bool finish, float max_norm, float* norm) {
   __shared__ double shared[kThreads / 32];
   __shared__ bool last;
   grid_dependency_wait();
   grid_launch_dependents();
+  Squares mine;
+  const uint64_t first_out = l2_evict_first_policy(), last_out = l2_evict_last_policy();
+  for (int64_t c = blockIdx.x; c < chunks_of(t); c += gridDim.x) chunk_squares(t, c, c < chunks_of(t) - t.keep ? first_out : last_out, &mine);
+  // the warps' sums in two f32, the block's in f64
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float hi = __shfl_xor_sync(~0u, mine.sum.hi, o), lo = __shfl_xor_sync(~0u, mine.sum.lo, o);
+    mine.sum.add(hi);
+    mine.sum.lo += lo;
+  }
   double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < chunks_of(t); c += gridDim.x) sum += chunk_squares(t, c);
-  sum = block_sum(sum, shared);
+  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = static_cast<double>(mine.sum.hi) + mine.sum.lo;
+  const bool any_wide = __syncthreads_or(mine.wide != 0.0);  // (NaN too)
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kThreads / 32; ++w) sum += shared[w];
+  if (any_wide) {
+    __syncthreads();
+    sum += block_sum(mine.wide, shared);
+  }
   if (threadIdx.x == 0) {
     s.part[blockIdx.x] = sum;
     __threadfence();
@@ -228,11 +275,12 @@ __global__ void __launch_bounds__(kThreads, 4) squares_kernel(const __grid_const
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constant__ TensorTable<N> t, const float* scale) {
+__global__ void __launch_bounds__(kThreads, 8) scale_kernel(const __grid_constant__ TensorTable<N> t, const float* scale) {
   grid_dependency_wait();
   grid_launch_dependents();
   const float f = *scale;
-  for (int64_t c = chunks_of(t) - 1 - blockIdx.x; c >= 0; c -= gridDim.x) scale_chunk(t, c, f);
+  const uint64_t policy = l2_evict_first_policy();
+  for (int64_t c = chunks_of(t) - 1 - blockIdx.x; c >= 0; c -= gridDim.x) scale_chunk(t, c, policy, f);
 }
 
 // Norm and scaling of few values by one cluster.  Values are dealt to threads
@@ -347,9 +395,12 @@ int64_t fill_table(TensorTable<N>* t, const ClipTensor* list, int64_t num, int64
 }
 // Blocks for the table's chunks: as many as fit at once.
 template <int N>
-unsigned cut_chunks(TensorTable<N>* t, int64_t most) {
+unsigned cut_chunks(TensorTable<N>* t, int64_t most, bool scale) {
   const int64_t values = t->tensors ? t->end[t->tensors - 1] : 0;
-  t->chunk = kThreads * kAhead * 8;
+  int64_t bytes = 0;
+  for (int i = 0; i < t->tensors; ++i) bytes += (t->end[i] - (i ? t->end[i - 1] : 0)) * (t->f32[i] ? 4 : 2);
+  t->chunk = kThreads * kAhead * 32;
+  t->keep = scale && bytes ? static_cast<int64_t>(static_cast<double>(kKeepBytes) / bytes * values / t->chunk) : 0;
   const int64_t blocks = (values + t->chunk - 1) / t->chunk;
   return static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
@@ -375,7 +426,7 @@ cudaError_t launch_many(const ClipTensor* list, int64_t num, bool scale, float m
   do {
     ++launches;
     at = fill_table(&t, list, num, at);
-    const cudaError_t e = launch_after(squares_kernel<N>, cut_chunks(&t, most), kThreads, 0, st, t, s, first, at >= num, max_norm, norm);
+    const cudaError_t e = launch_after(squares_kernel<N>, cut_chunks(&t, most, scale), kThreads, 0, st, t, s, first, at >= num, max_norm, norm);
     if (e != cudaSuccess) return e;
     first = false;
   } while (at < num);
@@ -384,7 +435,7 @@ cudaError_t launch_many(const ClipTensor* list, int64_t num, bool scale, float m
   do {
     if (launches > 1) at = fill_table(&t, list, num, at);
     if (t.tensors) {
-      const unsigned blocks = cut_chunks(&t, most);
+      const unsigned blocks = cut_chunks(&t, most, scale);
       const cudaError_t e = launch_after(scale_kernel<N>, blocks, kThreads, 0, st, t, static_cast<const float*>(s.scale));
       if (e != cudaSuccess) return e;
     }

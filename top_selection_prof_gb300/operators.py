@@ -36,20 +36,20 @@ def _first(t):
     """dtype code of the tensor that the call's others are checked against."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("input must be a CUDA tensor (the engine has no CPU path)")
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise TypeError("operators take float32 or bfloat16 tensors, got %s" % t.dtype) from None
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("operators take float32 or bfloat16 tensors, got %s" % t.dtype)
+    return code
 
 
-def _like(t, ref, name):
-    if not isinstance(t, torch.Tensor) or t.dtype != ref.dtype or t.device != ref.device:
-        raise TypeError("%s must be a %s tensor on %s" % (name, ref.dtype, ref.device))
+def _like(t, dtype, device, name):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
+        raise TypeError("%s must be a %s tensor on %s" % (name, dtype, device))
 
 
 def _matrix(t, rows, cols, name):
     """Distance between the rows of t, which must be (rows, cols) with contiguous rows that do not overlap."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError("%s must have shape (%d, %d), got %s" % (name, rows, cols, tuple(t.shape)))
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
@@ -61,24 +61,30 @@ def _matrix(t, rows, cols, name):
     return s0
 
 
-def _vector(t, ref, n, name):
-    _like(t, ref, name)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _vector(t, dtype, device, n, name):
+    _like(t, dtype, device, name)
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d values" % (name, n))
     return t.data_ptr()
 
 
+_FUNCTIONS = {}
+
+
 def _call(name, device, stream, tensors, *args):
     """lib.<name>(*args, stream); with a stream of the caller's, the call's tensors are kept until it has run."""
-    fn = getattr(_lib.get(), name)
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(_lib.get(), name)
+    index = device.index
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        raw = torch._C._cuda_getCurrentRawStream(index)
     else:
         raw = stream.cuda_stream
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -96,23 +102,23 @@ def linear(x, w, bias=None, act: str = "none", residual=None, save_pre: bool = F
     if x.dim() != 2:
         raise ValueError("x must be 2-D (rows, inner)")
     rows, inner = x.shape
-    _like(w, x, "w")
+    dtype, device = x.dtype, x.device
+    _like(w, dtype, device, "w")
     outer = w.shape[0]
     ldx, ldw = _matrix(x, rows, inner, "x"), _matrix(w, outer, inner, "w")
-    pb = None if bias is None else _vector(bias, x, outer, "bias")
-    ldr = 0
+    pb = None if bias is None else _vector(bias, dtype, device, outer, "bias")
+    pr, ldr = None, 0
     if residual is not None:
-        _like(residual, x, "residual")
-        ldr = _matrix(residual, rows, outer, "residual")
+        _like(residual, dtype, device, "residual")
+        pr, ldr = residual.data_ptr(), _matrix(residual, rows, outer, "residual")
     if out is None:
-        out, ldy = torch.empty((rows, outer), dtype=x.dtype, device=x.device), outer
+        out, ldy = torch.empty((rows, outer), dtype=dtype, device=device), outer
     else:
-        _like(out, x, "out")
+        _like(out, dtype, device, "out")
         ldy = _matrix(out, rows, outer, "out")
-    pre = torch.empty((rows, outer), dtype=x.dtype, device=x.device) if save_pre else None
-    _call("topk_linear", x.device, stream, (x, w, bias, residual, out, pre), x.data_ptr(), ldx, w.data_ptr(), ldw, pb,
-          None if residual is None else residual.data_ptr(), ldr, code, rows, inner, outer, _act(act), out.data_ptr(),
-          ldy, pre.data_ptr() if save_pre else None, outer)
+    pre = torch.empty((rows, outer), dtype=dtype, device=device) if save_pre else None
+    _call("topk_linear", device, stream, (x, w, bias, residual, out, pre), x.data_ptr(), ldx, w.data_ptr(), ldw, pb, pr,
+          ldr, code, rows, inner, outer, _act(act), out.data_ptr(), ldy, pre.data_ptr() if save_pre else None, outer)
     return (out, pre) if save_pre else out
 
 
@@ -124,8 +130,9 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", need=(True, True, Tru
     if dy.dim() != 2:
         raise ValueError("dy must be 2-D (rows, outer)")
     rows, outer = dy.shape
-    _like(x, dy, "x")
-    _like(w, dy, "w")
+    dtype, device = dy.dtype, dy.device
+    _like(x, dtype, device, "x")
+    _like(w, dtype, device, "w")
     if w.dim() != 2:
         raise ValueError("w must be 2-D (outer, inner)")
     inner = w.shape[1]
@@ -134,24 +141,24 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", need=(True, True, Tru
     if a != TOPK_ACT_NONE:
         if pre is None:
             raise ValueError("act %r needs pre" % act)
-        _like(pre, dy, "pre")
+        _like(pre, dtype, device, "pre")
         ldp = _matrix(pre, rows, outer, "pre")
     else:
         pre = None
-    dx = torch.empty((rows, inner), dtype=dy.dtype, device=dy.device) if need[0] else None
-    dw = torch.empty((outer, inner), dtype=dy.dtype, device=dy.device) if need[1] else None
-    db = torch.empty((outer,), dtype=dy.dtype, device=dy.device) if need[2] else None
-    _call("topk_linear_backward", dy.device, stream, (dy, x, w, pre, dx, dw, db), dy.data_ptr(), lddy, x.data_ptr(), ldx,
+    dx = torch.empty((rows, inner), dtype=dtype, device=device) if need[0] else None
+    dw = torch.empty((outer, inner), dtype=dtype, device=device) if need[1] else None
+    db = torch.empty((outer,), dtype=dtype, device=device) if need[2] else None
+    _call("topk_linear_backward", device, stream, (dy, x, w, pre, dx, dw, db), dy.data_ptr(), lddy, x.data_ptr(), ldx,
           w.data_ptr(), ldw, None if pre is None else pre.data_ptr(), ldp, code, rows, inner, outer, a,
           None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
           None if db is None else db.data_ptr())
     return dx, dw, db
 
 
-def _places(idx, rows, ref):
+def _places(idx, rows, device):
     """(count, per_row) of a selection's positions: 1-D flat ones, or (rows, k) row-local ones."""
-    if not isinstance(idx, torch.Tensor) or idx.dtype != torch.int64 or idx.device != ref.device:
-        raise TypeError("idx must be an int64 tensor on %s" % ref.device)
+    if not isinstance(idx, torch.Tensor) or idx.dtype is not torch.int64 or idx.device != device:
+        raise TypeError("idx must be an int64 tensor on %s" % device)
     if not idx.is_contiguous():
         raise ValueError("idx must be contiguous")
     if idx.dim() == 1:
@@ -161,8 +168,8 @@ def _places(idx, rows, ref):
     return idx.shape[1], 1
 
 
-def _of_places(t, idx, ref, name):
-    _like(t, ref, name)
+def _of_places(t, idx, dtype, device, name):
+    _like(t, dtype, device, name)
     if t.shape != idx.shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous with idx's shape %s" % (name, tuple(idx.shape)))
     return t.data_ptr()
@@ -177,15 +184,16 @@ def linear_backward_selected(dvals, vals, idx, x, w, act: str = "relu", need=(Tr
     if x.dim() != 2:
         raise ValueError("x must be 2-D (rows, inner)")
     rows, inner = x.shape
-    _like(w, x, "w")
+    dtype, device = x.dtype, x.device
+    _like(w, dtype, device, "w")
     outer = w.shape[0]
     ldx, ldw = _matrix(x, rows, inner, "x"), _matrix(w, outer, inner, "w")
-    count, per_row = _places(idx, rows, x)
-    pd, pv = _of_places(dvals, idx, x, "dvals"), _of_places(vals, idx, x, "vals")
-    dx = torch.empty((rows, inner), dtype=x.dtype, device=x.device) if need[0] else None
-    dw = torch.empty((outer, inner), dtype=x.dtype, device=x.device) if need[1] else None
-    db = torch.empty((outer,), dtype=x.dtype, device=x.device) if need[2] else None
-    _call("topk_linear_backward_selected", x.device, stream, (dvals, vals, idx, x, w, dx, dw, db), pd, pv,
+    count, per_row = _places(idx, rows, device)
+    pd, pv = _of_places(dvals, idx, dtype, device, "dvals"), _of_places(vals, idx, dtype, device, "vals")
+    dx = torch.empty((rows, inner), dtype=dtype, device=device) if need[0] else None
+    dw = torch.empty((outer, inner), dtype=dtype, device=device) if need[1] else None
+    db = torch.empty((outer,), dtype=dtype, device=device) if need[2] else None
+    _call("topk_linear_backward_selected", device, stream, (dvals, vals, idx, x, w, dx, dw, db), pd, pv,
           idx.data_ptr(), count, per_row, x.data_ptr(), ldx, w.data_ptr(), ldw, code, rows, inner, outer, _act(act),
           None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
           None if db is None else db.data_ptr())
@@ -198,12 +206,13 @@ def decode(vals, idx, w, rows: int, bias=None, stream=None):
     if w.dim() != 2:
         raise ValueError("w must be 2-D (n, d)")
     n, d = w.shape
+    dtype, device = w.dtype, w.device
     ldw = _matrix(w, n, d, "w")
-    count, per_row = _places(idx, rows, w)
-    pv = _of_places(vals, idx, w, "vals")
-    pb = None if bias is None else _vector(bias, w, d, "bias")
-    y = torch.empty((rows, d), dtype=w.dtype, device=w.device)
-    _call("topk_decode", w.device, stream, (vals, idx, w, bias, y), pv, idx.data_ptr(), count, per_row, w.data_ptr(), ldw,
+    count, per_row = _places(idx, rows, device)
+    pv = _of_places(vals, idx, dtype, device, "vals")
+    pb = None if bias is None else _vector(bias, dtype, device, d, "bias")
+    y = torch.empty((rows, d), dtype=dtype, device=device)
+    _call("topk_decode", device, stream, (vals, idx, w, bias, y), pv, idx.data_ptr(), count, per_row, w.data_ptr(), ldw,
           pb, code, rows, n, d, y.data_ptr())
     return y
 
@@ -214,34 +223,42 @@ def decode_backward(dy, vals, idx, w, need=(True, True, True), stream=None):
     if dy.dim() != 2:
         raise ValueError("dy must be 2-D (rows, d)")
     rows, d = dy.shape
-    _like(w, dy, "w")
+    dtype, device = dy.dtype, dy.device
+    _like(w, dtype, device, "w")
     n = w.shape[0]
     lddy, ldw = _matrix(dy, rows, d, "dy"), _matrix(w, n, d, "w")
-    count, per_row = _places(idx, rows, dy)
-    pv = _of_places(vals, idx, dy, "vals")
+    count, per_row = _places(idx, rows, device)
+    pv = _of_places(vals, idx, dtype, device, "vals")
     dv = torch.empty_like(vals) if need[0] else None
-    dw = torch.empty((n, d), dtype=dy.dtype, device=dy.device) if need[1] else None
-    db = torch.empty((d,), dtype=dy.dtype, device=dy.device) if need[2] else None
-    _call("topk_decode_backward", dy.device, stream, (dy, vals, idx, w, dv, dw, db), dy.data_ptr(), lddy, pv,
+    dw = torch.empty((n, d), dtype=dtype, device=device) if need[1] else None
+    db = torch.empty((d,), dtype=dtype, device=device) if need[2] else None
+    _call("topk_decode_backward", device, stream, (dy, vals, idx, w, dv, dw, db), dy.data_ptr(), lddy, pv,
           idx.data_ptr(), count, per_row, w.data_ptr(), ldw, code, rows, n, d, None if dv is None else dv.data_ptr(),
           None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr())
     return dv, dw, db
 
 
+_ARRAYS = {}
+
+
 def _table(tensors, name):
     """(pointers, counts, dtypes) of contiguous tensors on one device, as the host arrays the library reads."""
     num = len(tensors)
-    ptrs, counts, codes = (ctypes.c_void_p * num)(), (ctypes.c_int64 * num)(), (ctypes.c_int * num)()
-    device = tensors[0].device if num else None
-    for i, t in enumerate(tensors):
-        codes[i] = _first(t)
-        if t.device != device:
+    arrays = _ARRAYS.get(num)
+    if arrays is None:
+        arrays = _ARRAYS[num] = (ctypes.c_void_p * num, ctypes.c_int64 * num, ctypes.c_int * num)
+    where, codes, ptrs, counts = tensors[0].get_device() if num else -1, [], [], []
+    for t in tensors:
+        code = _CODES.get(t.dtype)
+        if code is None or t.get_device() != where or where < 0:
+            _first(t)
             raise TypeError("%s must lie on one device" % name)
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-        ptrs[i] = t.data_ptr()
-        counts[i] = t.numel()
-    return ptrs, counts, codes
+        codes.append(code)
+        ptrs.append(t.data_ptr())
+        counts.append(t.numel())
+    return arrays[0](*ptrs), arrays[1](*counts), arrays[2](*codes)
 
 
 def _norm(tensors, max_norm, out, stream):
