@@ -341,7 +341,8 @@ int topk_select_noalloc(const void* x, int dtype, int64_t rows, int64_t n, int64
  *     result is rounded once, to nearest even.  Results do not depend on the
  *     order in which blocks run: the same call gives the same bits.
  *   - Outputs marked "nullable" are not computed when null.
- *   - Extents are below 2^31 (EUNSUPPORTED beyond).  Scratch memory comes from
+ *   - Extents are below 2^31 and a selection's places below 2^29
+ *     (EUNSUPPORTED beyond).  Scratch memory comes from
  *     a per-(device, stream) block of these operators, grown on demand.
  * ------------------------------------------------------------------------ */
 

@@ -8,9 +8,10 @@
 // written to their slots.  Ranks and bases differ from run to run; the order
 // in which a group is summed does not: a short group's places are put in
 // order of s where they are summed, a long group's by a block of its own
-// before that.  A long group is summed in pieces, and the piece that ends last
-// (by a ticket) adds the pieces up in their order.  So results do not depend
-// on the order of the atomics, and nothing waits for another block.
+// before that.  A long group is summed in pieces, whose sums are added eight at a
+// time, level by level, by the warp of each eight that ends last (by a
+// ticket).  So results do not depend on the order of the atomics, and nothing
+// waits for another block.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -19,7 +20,8 @@
 namespace tk {
 namespace {
 
-constexpr int kRowPiece = 64, kColPiece = 32;  // places summed at a time; a group with more is long
+// Places summed at a time (most; a group with more is long): by a warp or block of a row, by a warp of columns.
+constexpr int kRowPiece = 64, kColPiece = 32;
 constexpr int kThreads = 256, kSortThreads = 512;
 constexpr int kSpan = 8;                       // groups next to each other that may share a task
 constexpr int kGroupsBlock = 256;              // groups of one block of the base kernel: their places lie together
@@ -58,14 +60,18 @@ struct Groups {
   Item* tasks;        // sums by column (else null): short groups that share a warp
   unsigned* longs;
   unsigned* ticket;   // pieces of a long group (and tile of d) that are done, counted at its first slot; zero at first
-  float* part;        // pieces x d sums
+  float* part;        // pieces x d sums, rows of part_ld
   float* part_bias;   // pieces sums of coefficients
   int64_t n_groups, max_pieces, max_longs, max_tasks, n_tickets;
+  int64_t part_ld;
+  int piece, share;   // most places of a piece, and of columns that share a warp
 };
 
 Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int piece, int64_t d, int64_t d_tiles, bool bias, bool tasks) {
   Groups g{};
   g.n_groups = groups;
+  g.piece = piece;
+  g.share = piece < 16 ? piece : 16;
   // a long group has more than `piece` places, so at most 2 x places / piece pieces
   g.max_longs = total / (piece + 1);
   g.max_pieces = g.max_longs ? 2 * (total / piece) : 0;
@@ -77,12 +83,13 @@ Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int piece, int64_
   g.order = sc.take<Entry>(total);
   g.sorted = sc.take<Entry>(g.max_longs ? total : 0);
   g.pieces = sc.take<Item>(g.max_pieces);
-  // a span of groups that share no task has more than `piece` places
-  g.max_tasks = tasks ? (groups + kSpan - 1) / kSpan + (kSpan - 1) * (total / piece) : 0;
+  // a span of groups that is no one task has more than `share` places
+  g.max_tasks = tasks ? (groups + kSpan - 1) / kSpan + (kSpan - 1) * (total / g.share) : 0;
   g.tasks = tasks ? sc.take<Item>(g.max_tasks) : nullptr;
   g.longs = sc.take<unsigned>(g.max_longs);
   g.ticket = sc.take<unsigned>(g.n_tickets);
-  g.part = sc.take<float>(g.max_pieces * d);
+  g.part_ld = (d + 3) / 4 * 4;
+  g.part = sc.take<float>(g.max_pieces * g.part_ld);
   g.part_bias = sc.take<float>(bias ? g.max_pieces : 0);
   return g;
 }
@@ -171,7 +178,8 @@ __device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* total) {
 
 // A base for every group, from a scan over the block's groups and one atomic
 // on the running total; the pieces and the list of long groups likewise.
-__global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g, unsigned piece) {
+__global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g) {
+  const unsigned piece = g.piece, share = g.share;
   __shared__ unsigned block_base;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -183,14 +191,14 @@ __global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g
   __syncthreads();
   const unsigned start = block_base + incl - cnt;
   if (g.tasks) {
-    // as many groups next to each other (8, 4, 2 or 1, aligned) as hold at most `piece` places
+    // as many groups next to each other (8, 4 or 2, aligned) as hold at most g.share places, or one
     const int lane = threadIdx.x % 32;
     const unsigned s2 = cnt + __shfl_xor_sync(~0u, cnt, 1), s4 = s2 + __shfl_xor_sync(~0u, s2, 2);
     const unsigned s8 = s4 + __shfl_xor_sync(~0u, s4, 4);
     unsigned size = 1, places = cnt;
-    if (s8 <= piece) size = 8, places = s8;
-    else if (s4 <= piece) size = 4, places = s4;
-    else if (s2 <= piece) size = 2, places = s2;
+    if (s8 <= share) size = 8, places = s8;
+    else if (s4 <= share) size = 4, places = s4;
+    else if (s2 <= share) size = 2, places = s2;
     const bool leads = lane % size == 0 && places <= piece && i < g.n_groups;
     const unsigned who = __ballot_sync(~0u, leads);
     unsigned slot = 0;
@@ -300,7 +308,7 @@ cudaError_t launch_grouping(const Places& p, const Coef& c, const Groups& g, T* 
   if (e == cudaSuccess && blocks) e = launch_after(count_places_kernel<BY_ROW, T>, blocks, kThreads, 0, st, p, c, g, dots);
   if (e != cudaSuccess) return e;
   e = launch_after(group_base_kernel, static_cast<unsigned>((g.n_groups + kGroupsBlock - 1) / kGroupsBlock), kGroupsBlock, 0, st,
-                   g, static_cast<unsigned>(BY_ROW ? kRowPiece : kColPiece));
+                   g);
   if (e != cudaSuccess || !blocks) return e;  // (no places: every group is empty)
   e = launch_after(place_kernel, blocks, kThreads, 0, st, g, p.total);
   if (e != cudaSuccess || !g.max_longs) return e;
@@ -317,6 +325,70 @@ cudaError_t launch_grouping(const Places& p, const Coef& c, const Groups& g, T* 
 // ---- sums by row ------------------------------------------------------------------
 constexpr int kRowAhead = 8;
 
+// Adds up a long group's pieces, a warp at a time: called by the warp that has
+// written piece `index` (of `pieces`, the first in slot `slot0`) to its slot,
+// with values [j0, j1) of each slot's row of ld.  The warp that ends last of each eight
+// adds them in their order into the first one's slot and goes on with the
+// eights of the next level; the last of all writes dst = sum (+ bias).
+constexpr unsigned kFan = 8;
+struct Join {
+  float* part;
+  float* part_bias;   // nullable: a value a slot, added up the same way
+  unsigned* ticket;   // of slot s and level l: [(s + l) * stride]; a level's eights lie eight slots apart or more
+  int64_t stride, ld, j0, j1;
+  unsigned slot0, index, pieces;
+};
+template <typename T>
+__device__ __noinline__ void join_pieces(const Join& q, T* dst, const T* bias, T* dbias) {
+  const int lane = threadIdx.x % 32;
+  unsigned at = q.index, left = q.pieces, apart = 1;  // the sums of this level lie `apart` slots apart
+  for (unsigned level = 0; left > 1; ++level) {
+    const unsigned group = at / kFan, members = min(kFan, left - group * kFan);
+    const unsigned slot = q.slot0 + group * kFan * apart;
+    if (members > 1) {
+      __threadfence();
+      __syncwarp();
+      unsigned seen = 0;
+      if (lane == 0) seen = atomicAdd(&q.ticket[int64_t(slot + level) * q.stride], 1u);
+      seen = __shfl_sync(~0u, seen, 0);
+      if (seen != members - 1) return;
+      __threadfence();
+      const bool top = left <= kFan;
+      // four values of each of the eight in flight (slots hold whole float4, j0 is one's first); more would cost the
+      // kernels that call this their registers, and so their warps: with eight values 43 -> 76 us
+      for (int64_t j = q.j0 + lane * 4; dst && j < q.j1; j += 128) {
+        Vec<float, 4> t[kFan];
+        float* src = q.part + int64_t(slot) * q.ld + j;
+#pragma unroll
+        for (unsigned m = 0; m < kFan; ++m)
+          if (m < members) t[m].load_cg(src + int64_t(m) * apart * q.ld);
+#pragma unroll
+        for (unsigned m = 1; m < kFan; ++m)
+          if (m < members) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) t[0].v[v] += t[m].v[v];
+          }
+        if (top) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (j + v < q.j1) dst[j + v] = from_f32<T>(t[0].v[v] + (bias ? to_f32(bias[j + v]) : 0.0f));
+        } else {
+          t[0].store(src);
+        }
+      }
+      if (q.part_bias && lane == 0) {
+        float sum = 0.0f;
+        for (unsigned m = 0; m < members; ++m) sum += __ldcg(&q.part_bias[slot + m * apart]);
+        if (top) *dbias = from_f32<T>(sum);
+        else q.part_bias[slot] = sum;
+      }
+    }
+    at = group;
+    left = (left + kFan - 1) / kFan;
+    apart *= kFan;
+  }
+}
+
 struct RowParams {
   RowSums r;
   Groups g;
@@ -324,13 +396,13 @@ struct RowParams {
   int64_t d_tiles;
 };
 
-// Many rows: a warp takes one piece of a row and one tile of 32 x VEC values,
-// places in order one after the other, kRowAhead of them in flight.
-constexpr int kRowWarps = 4;
-template <typename T, int VEC>
+// Many rows: a warp takes one piece of a row and one tile of 32 x VEC x CHUNKS
+// values, places in order one after the other, AHEAD of them in flight.
+constexpr int kRowWarps = 4, kRowChunks1 = 8;  // (chunks of rows that do not hold whole vectors)
+template <typename T, int VEC, int CHUNKS, int AHEAD>
 __global__ void __launch_bounds__(kRowWarps * 32) row_sums_warp_kernel(const RowParams q) {
   __shared__ Entry raw_all[kRowWarps][kRowPiece];
-  __shared__ uint2 ent_all[kRowWarps][kRowPiece + kRowAhead];  // other coordinate, coefficient
+  __shared__ uint2 ent_all[kRowWarps][kRowPiece];  // other coordinate, coefficient
   grid_dependency_wait();
   grid_launch_dependents();
   const RowSums& r = q.r;
@@ -398,61 +470,62 @@ __global__ void __launch_bounds__(kRowWarps * 32) row_sums_warp_kernel(const Row
     }
   }
   __syncwarp();
-  const int64_t j = tile * (32 * VEC) + int64_t(lane) * VEC;
-  const bool in = j < r.d;
+  const int64_t j0 = tile * (32 * VEC * CHUNKS), j = j0 + int64_t(lane) * VEC;
   const T* wt = static_cast<const T*>(r.w) + j;
-  float acc[VEC] = {};
-  if (in) {
-    int i0 = 0;
+  bool in[CHUNKS];
+  float acc[CHUNKS][VEC] = {};
+#pragma unroll
+  for (int h = 0; h < CHUNKS; ++h) in[h] = j + h * 32 * VEC < r.d;
 #pragma unroll 1
-    for (; i0 < cnt; i0 += kRowAhead) {
-      Raw<T, VEC> v[kRowAhead];
+  for (int i0 = 0; i0 < cnt; i0 += AHEAD) {
+    Raw<T, VEC> v[AHEAD][CHUNKS];
 #pragma unroll
-      for (int a = 0; a < kRowAhead; ++a)
-        if (i0 + a < cnt) v[a].load_nc(wt + int64_t(ent[i0 + a].x) * r.ldw);
+    for (int a = 0; a < AHEAD; ++a)
+      if (i0 + a < cnt) {
+        const T* row_w = wt + int64_t(ent[i0 + a].x) * r.ldw;
 #pragma unroll
-      for (int a = 0; a < kRowAhead; ++a) {
-        if (i0 + a < cnt) {
-          Vec<T, VEC> u;
-          u.set_raw(v[a]);
-          const float f = __uint_as_float(ent[i0 + a].y);
+        for (int h = 0; h < CHUNKS; ++h)
+          if (in[h]) v[a][h].load_nc(row_w + h * 32 * VEC);
+      }
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) acc[c] = fmaf(f, u.v[c], acc[c]);
-        }
+    for (int a = 0; a < AHEAD; ++a) {
+      if (i0 + a < cnt) {
+        const float f = __uint_as_float(ent[i0 + a].y);
+#pragma unroll
+        for (int h = 0; h < CHUNKS; ++h)
+          if (in[h]) {
+            Vec<T, VEC> u;
+            u.set_raw(v[a][h]);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) acc[h][c] = fmaf(f, u.v[c], acc[h][c]);
+          }
       }
     }
   }
+  T* y = static_cast<T*>(r.y) + row * r.d;
+  const T* bias = static_cast<const T*>(r.bias);
   if (n_pieces > 1) {
-    // this piece's sums, then the last piece of the row adds them all in order
-    if (in) {
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) q.g.part[int64_t(slot0 + index) * r.d + j + c] = acc[c];
-    }
-    __threadfence();
-    __syncwarp();
-    unsigned seen = 0;
-    if (lane == 0) seen = atomicAdd(&q.g.ticket[int64_t(slot0) * q.d_tiles + tile], 1u);
-    seen = __shfl_sync(~0u, seen, 0);
-    if (seen != n_pieces - 1) return;
-    __threadfence();
-    if (in) {
+    for (int h = 0; h < CHUNKS; ++h)
+      if (in[h]) {
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) acc[c] = 0.0f;
-#pragma unroll 4
-      for (unsigned o = 0; o < n_pieces; ++o)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[c] += __ldcg(&q.g.part[int64_t(slot0 + o) * r.d + j + c]);
-    }
+        for (int c = 0; c < VEC; ++c) q.g.part[int64_t(slot0 + index) * q.g.part_ld + j + h * 32 * VEC + c] = acc[h][c];
+      }
+    const Join join{q.g.part, nullptr, q.g.ticket + tile, q.d_tiles, q.g.part_ld, j0, min(r.d, j0 + 32 * VEC * CHUNKS), slot0, index, n_pieces};
+    join_pieces(join, y, bias, static_cast<T*>(nullptr));
+    return;
   }
-  if (in) {
-    Vec<T, VEC> out;
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) out.v[c] = 0.0f;
-    if (r.bias) out.load_nc(static_cast<const T*>(r.bias) + j);
+  for (int h = 0; h < CHUNKS; ++h)
+    if (in[h]) {
+      Vec<T, VEC> out;
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) out.v[c] += acc[c];
-    out.store(static_cast<T*>(r.y) + row * r.d + j);
-  }
+      for (int c = 0; c < VEC; ++c) out.v[c] = 0.0f;
+      if (bias) out.load_nc(bias + j + h * 32 * VEC);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) out.v[c] += acc[h][c];
+      out.store(y + j + h * 32 * VEC);
+    }
 }
 
 // Few rows: a block takes one piece of a row, kRowTx threads across d, the
@@ -465,7 +538,6 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const RowParams q) {
   __shared__ Entry raw[kRowPiece];
   __shared__ uint2 ent[kRowPiece];  // other coordinate, coefficient
   __shared__ float sums[TY - 1][TX * VEC];
-  __shared__ bool last;
   grid_dependency_wait();
   grid_launch_dependents();
   const RowSums& r = q.r;
@@ -558,25 +630,16 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const RowParams q) {
       for (int c = 0; c < VEC; ++c) acc[c] += sums[o][tx * VEC + c];
   }
   if (n_pieces > 1) {
-    // this piece's sums, then the last piece of the row adds them all in order
     if (ty == 0 && in) {
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) q.g.part[int64_t(slot0 + index) * r.d + j + c] = acc[c];
-      __threadfence();
+      for (int c = 0; c < VEC; ++c) q.g.part[int64_t(slot0 + index) * q.g.part_ld + j + c] = acc[c];
     }
-    __syncthreads();
-    if (t == 0) last = atomicAdd(&q.g.ticket[int64_t(slot0) * q.d_tiles + tile], 1u) == n_pieces - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    if (ty == 0 && in) {
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) acc[c] = 0.0f;
-#pragma unroll 4
-      for (unsigned o = 0; o < n_pieces; ++o)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[c] += __ldcg(&q.g.part[int64_t(slot0 + o) * r.d + j + c]);
-    }
+    if (t >= 32) return;
+    __syncwarp();
+    const int64_t j0 = tile * (TX * VEC);
+    const Join join{q.g.part, nullptr, q.g.ticket + tile, q.d_tiles, q.g.part_ld, j0, min(r.d, j0 + TX * VEC), slot0, index, n_pieces};
+    join_pieces(join, static_cast<T*>(r.y) + row * r.d, static_cast<const T*>(r.bias), static_cast<T*>(nullptr));
+    return;
   }
   if (ty == 0 && in) {
     Vec<T, VEC> out;
@@ -605,15 +668,16 @@ int row_vec(const RowSums& r) {
 }
 // A warp a piece and tile when that gives every SM eight warps, else a block each (64 places of one row of 512 values:
 // 12.6 us by one block's 64 threads across d, 4.8 us by four blocks' 16).
+int64_t many_wide(const RowSums& r) { return row_vec(r) == 1 ? 32 * kRowChunks1 : 32 * row_vec(r); }
 bool many_rows(const RowSums& r) {
-  const int64_t wide = 32 * row_vec(r);
+  const int64_t wide = many_wide(r);
   return r.places.rows * ((r.d + wide - 1) / wide) >= 8 * ops_sm_count();
 }
 
 RowParams plan_rows(const RowSums& r, Scratch& sc) {
   RowParams q{};
   q.r = r;
-  const int64_t wide = int64_t(many_rows(r) ? 32 : kRowTx) * row_vec(r);
+  const int64_t wide = many_rows(r) ? many_wide(r) : int64_t(kRowTx) * row_vec(r);
   q.d_tiles = (r.d + wide - 1) / wide;
   if (r.places.per_row) {
     q.pieces_per_row = r.places.count > kRowPiece ? (r.places.count + kRowPiece - 1) / kRowPiece : 1;
@@ -621,7 +685,8 @@ RowParams plan_rows(const RowSums& r, Scratch& sc) {
       q.g.n_tickets = r.places.rows * q.pieces_per_row * q.d_tiles;
       q.g.hdr = sc.take<GroupHeader>(1);
       q.g.ticket = sc.take<unsigned>(q.g.n_tickets);
-      q.g.part = sc.take<float>(r.places.rows * q.pieces_per_row * r.d);
+      q.g.part_ld = (r.d + 3) / 4 * 4;
+      q.g.part = sc.take<float>(r.places.rows * q.pieces_per_row * q.g.part_ld);
     }
   } else {
     q.g = plan_groups(sc, r.places.total, r.places.rows, kRowPiece, r.d, q.d_tiles, false, false);
@@ -634,7 +699,9 @@ cudaError_t launch_rows_v(const RowParams& q, int64_t work, cudaStream_t st) {
   const bool many = many_rows(q.r);
   const int64_t grid = many ? (work + kRowWarps - 1) / kRowWarps : work;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  if (many) return launch_after(row_sums_warp_kernel<T, VEC>, static_cast<unsigned>(grid), kRowWarps * 32, 0, st, q);
+  if (many)
+    return launch_after(row_sums_warp_kernel<T, VEC, VEC == 1 ? kRowChunks1 : 1, VEC == 1 ? 4 : 8>, static_cast<unsigned>(grid),
+                        kRowWarps * 32, 0, st, q);
   return launch_after(row_sums_kernel<T, VEC>, static_cast<unsigned>(grid), kThreads, 0, st, q);
 }
 
@@ -658,34 +725,51 @@ cudaError_t launch_rows_t(const RowParams& q, cudaStream_t st) {
 }
 
 // ---- sums by column ---------------------------------------------------------------
-// A warp takes pieces of long columns and tasks of short ones, whose places
-// (one a lane) it puts in order by column and s and streams through: the rows
-// of x (and of w, for the dots) of AHEAD places in flight, sums of 32 x VEC x
-// CHUNKS values in registers, written where the column ends.  Longer rows take
-// several such tiles one after the other.  FULL: every tile is whole.
-constexpr int kColWarps = 4, kColBlocks = 5;
+// A warp takes items from a counter: pieces of long columns, or short columns
+// next to each other, whose places (one a lane) it puts in order by column and
+// s and streams through.  The places' rows of x (and, where a column begins,
+// its row of w, for the dots) are copied to a ring of the warp's shared memory
+// a tile of 32 x VEC x CHUNKS values at a time, kSlots - 1 places ahead, each
+// lane the values that it will read itself; the sums stay in registers and are
+// written where the column ends.  (131072 places of 512 bf16 values, with the
+// dots: loads into registers two ahead leave a warp 0.7 us a place, 57 us in
+// all; bulk copies of whole rows 95 us, one taking an SM some 70 ns.)
+// FULL: every tile is whole.  VECOUT: dw takes whole vectors too; else x and w
+// are copies with rows of whole vectors, zeros past d.
+constexpr int kColWarps = 4;
 
 struct ColParams {
   ColumnSums c;
   Groups g;
+  bool padded;    // x and w go through copies with rows of pad_ld values
+  int64_t pad_ld;
+  void* pad_x;
+  void* pad_w;
 };
 
-template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL, bool DOTS>
+template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS, bool VECOUT>
 struct ColumnStream {
   static constexpr int kTile = 32 * VEC * CHUNKS;
+  static constexpr int kTileBytes = kTile * sizeof(T);
+  static constexpr int kSlots = DOTS ? 6 : 8;
+  static constexpr int kSlotBytes = kTileBytes * (DOTS ? 2 : 1);
+  static constexpr int kPairs = VEC / 2;
   const ColumnSums& c;
+  unsigned char* ring;  // kSlots x kSlotBytes
   const Entry* ent;
   float* dots;
   float* part;  // where a piece's sums go (null: to dw)
-  int lane, total;
+  int lane, total, tiles;
   bool want_dw;
-  int64_t d0;
-  static constexpr int kPairs = VEC / 2;
   Pair acc2[CHUNKS][kPairs ? kPairs : 1];  // sums, two a register pair
   float acc1[CHUNKS];                      // (VEC == 1)
+  Pair wv2[DOTS ? CHUNKS : 1][kPairs ? kPairs : 1];  // the column's row of w
+  float wv1[DOTS ? CHUNKS : 1];
 
-  __device__ __forceinline__ int64_t at(int h) const { return d0 + (h * 32 + lane) * VEC; }
-  __device__ __forceinline__ bool in(int h) const { return FULL || at(h) < c.d; }
+  // The lane's first value of chunk h of a tile, in the row and in a slot.
+  __device__ __forceinline__ int64_t at(int tile, int h) const { return int64_t(tile) * kTile + (h * 32 + lane) * VEC; }
+  __device__ __forceinline__ int slot_at(int h) const { return (h * 32 + lane) * VEC * int(sizeof(T)); }
+  __device__ __forceinline__ bool in(int tile, int h) const { return FULL || at(tile, h) < c.d; }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int h = 0; h < CHUNKS; ++h) {
@@ -694,11 +778,11 @@ struct ColumnStream {
       for (int i = 0; i < kPairs; ++i) acc2[h][i] = Pair::of(0.0f, 0.0f);
     }
   }
-  // The sums so far are column `col`'s.
-  __device__ __forceinline__ void flush(int64_t col) {
+  // The sums so far are a tile of column `col`.
+  __device__ __forceinline__ void flush(int64_t col, int tile) {
 #pragma unroll
     for (int h = 0; h < CHUNKS; ++h) {
-      if (in(h)) {
+      if (in(tile, h)) {
         Vec<T, VEC> out;
         if constexpr (VEC == 1) {
           out.v[0] = acc1[h];
@@ -708,126 +792,151 @@ struct ColumnStream {
         }
         if (part) {
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) part[at(h) + v] = out.v[v];
+          for (int v = 0; v < VEC; ++v)
+            if (VECOUT || at(tile, h) + v < c.d) part[at(tile, h) + v] = out.v[v];
+        } else if constexpr (VECOUT) {
+          out.store_stream(static_cast<T*>(c.dw) + col * c.d + at(tile, h));
         } else {
-          out.store_stream(static_cast<T*>(c.dw) + col * c.d + at(h));
+#pragma unroll
+          for (int v = 0; v < VEC; ++v)
+            if (at(tile, h) + v < c.d) static_cast<T*>(c.dw)[col * c.d + at(tile, h) + v] = from_f32<T>(out.v[v]);
         }
       }
     }
     clear();
   }
-  // Places [i0, i0 + n), n <= AHEAD (WHOLE: n == AHEAD).
-  template <bool WHOLE>
-  __device__ __forceinline__ void batch(int i0, int n) {
-    Raw<T, VEC> xv[AHEAD][CHUNKS], wv[AHEAD][DOTS ? CHUNKS : 1];
-    const T* x = static_cast<const T*>(c.x) + at(0);
-    const T* w = static_cast<const T*>(c.w) + at(0);
+  // Place f (tile by tile) on its way to its slot; a group of copies in any case.
+  __device__ __forceinline__ void issue(int f, int n) {
+    if (f < n) {
+      const int tile = tiles == 1 ? 0 : f / total, i = f - tile * total;
+      const Entry e = ent[i];
+      unsigned char* slot = ring + (f % kSlots) * kSlotBytes;
+      const T* xr = static_cast<const T*>(c.x) + int64_t(e.other) * c.ldx;
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      if (WHOLE || a < n) {
-        const Entry e = ent[i0 + a];
-        const T* xr = x + int64_t(e.other) * c.ldx;
-        const T* wr = w + int64_t(e.group) * c.ldw;
+      for (int h = 0; h < CHUNKS; ++h)
+        if (in(tile, h)) copy_async<VEC>(reinterpret_cast<T*>(slot + slot_at(h)), xr + at(tile, h));
+      if constexpr (DOTS) {
+        if (i == 0 || ent[i - 1].group != e.group) {
+          const T* wr = static_cast<const T*>(c.w) + int64_t(e.group) * c.ldw;
 #pragma unroll
-        for (int h = 0; h < CHUNKS; ++h) {
-          if (in(h)) {
-            xv[a][h].load_nc(xr + h * 32 * VEC);
-            if constexpr (DOTS) wv[a][h].load_nc(wr + h * 32 * VEC);
-          }
+          for (int h = 0; h < CHUNKS; ++h)
+            if (in(tile, h)) copy_async<VEC>(reinterpret_cast<T*>(slot + kTileBytes + slot_at(h)), wr + at(tile, h));
         }
       }
     }
-    float dot[AHEAD] = {};
+    copy_async_commit();
+  }
+  __device__ __forceinline__ Raw<T, VEC> read(const unsigned char* slot, int tile, int h) const {
+    Raw<T, VEC> r;
+    r.clear();
+    if (in(tile, h)) r.load(reinterpret_cast<const T*>(slot + slot_at(h)));
+    return r;
+  }
+  __device__ __forceinline__ void run() {
+    const int n = total * tiles;
+    clear();
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      if (WHOLE || a < n) {
-        const float f = ent[i0 + a].coef;
-        const uint32_t group = ent[i0 + a].group;
-        const Pair f2 = Pair::of(f, f);
-        Pair dot2 = Pair::of(0.0f, 0.0f);
+    for (int f = 0; f < kSlots - 1; ++f) issue(f, n);
+    int i = 0, tile = 0;
+    for (int f0 = 0; f0 < n; f0 += 4) {
+      float dot[4] = {};
 #pragma unroll
-        for (int h = 0; h < CHUNKS; ++h) {
-          if (in(h)) {
-            if constexpr (VEC == 1) {
-              const float t = to_f32(xv[a][h].u);
-              acc1[h] = fmaf(f, t, acc1[h]);
-              if constexpr (DOTS) dot[a] = fmaf(t, to_f32(wv[a][h].u), dot[a]);
-            } else {
+      for (int a = 0; a < 4; ++a) {
+        if (f0 + a < n) {
+          issue(f0 + a + kSlots - 1, n);
+          copy_async_wait_group<kSlots - 1>();
+          const unsigned char* slot = ring + ((f0 + a) % kSlots) * kSlotBytes;
+          const float coef = ent[i].coef;
+          const uint32_t group = ent[i].group;
+          const Pair f2 = Pair::of(coef, coef);
+          if constexpr (DOTS) {
+            if (i == 0 || ent[i - 1].group != group) {
 #pragma unroll
-              for (int i = 0; i < kPairs; ++i) {
-                const Pair t = xv[a][h].pair(i);
-                acc2[h][i].fma(f2, t);
-                if constexpr (DOTS) dot2.fma(t, wv[a][h].pair(i));
+              for (int h = 0; h < CHUNKS; ++h) {
+                const Raw<T, VEC> r = read(slot + kTileBytes, tile, h);
+                if constexpr (VEC == 1) {
+                  wv1[h] = to_f32(r.u);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < kPairs; ++k) wv2[h][k] = r.pair(k);
+                }
               }
             }
           }
+          Pair dot2 = Pair::of(0.0f, 0.0f);
+#pragma unroll
+          for (int h = 0; h < CHUNKS; ++h) {
+            const Raw<T, VEC> xv = read(slot, tile, h);
+            if constexpr (VEC == 1) {
+              const float t = to_f32(xv.u);
+              acc1[h] = fmaf(coef, t, acc1[h]);
+              if constexpr (DOTS) dot[a] = fmaf(t, wv1[h], dot[a]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < kPairs; ++k) {
+                const Pair t = xv.pair(k);
+                acc2[h][k].fma(f2, t);
+                if constexpr (DOTS) dot2.fma(t, wv2[h][k]);
+              }
+            }
+          }
+          if constexpr (DOTS && VEC > 1) {
+            float lo, hi;
+            dot2.get(&lo, &hi);
+            dot[a] = lo + hi;
+          }
+          if (ent[i + 1].group != group) {  // (past the last place: no group's number)
+            if (want_dw) flush(group, tile);
+            else clear();
+          }
+          if (++i == total) {
+            i = 0;
+            ++tile;
+          }
         }
-        if constexpr (DOTS && VEC > 1) {
-          float lo, hi;
-          dot2.get(&lo, &hi);
-          dot[a] = lo + hi;
-        }
-        // (the entry past the last has no group's number)
-        if (want_dw && ent[i0 + a + 1].group != group) flush(group);
       }
-    }
-    if constexpr (DOTS) {
-      // AHEAD sums over the lanes, by exchanging halves until a lane holds one
-      int o = 16;
+      if constexpr (DOTS) {
+        // four sums over the lanes, by exchanging halves until a lane holds one
 #pragma unroll
-      for (int h = AHEAD / 2; h >= 1; h /= 2) {
+        for (int h = 2, o = 16; h >= 1; h /= 2, o /= 2) {
 #pragma unroll
-        for (int i = 0; i < h; ++i) {
-          const bool high = lane & o;
-          const float give = high ? dot[i] : dot[i + h];
-          dot[i] = (high ? dot[i + h] : dot[i]) + __shfl_xor_sync(~0u, give, o);
+          for (int k = 0; k < h; ++k) {
+            const bool high = lane & o;
+            const float give = high ? dot[k] : dot[k + h];
+            dot[k] = (high ? dot[k + h] : dot[k]) + __shfl_xor_sync(~0u, give, o);
+          }
         }
-        o /= 2;
-      }
 #pragma unroll
-      for (int p = 16 / AHEAD; p; p /= 2) dot[0] += __shfl_xor_sync(~0u, dot[0], p);
-      constexpr int kLanes = 32 / AHEAD;
-      const int i = lane / kLanes;
-      if (lane % kLanes == 0 && i < n) dots[i0 + i] = (d0 ? dots[i0 + i] : 0.0f) + dot[0];
+        for (int o = 4; o; o /= 2) dot[0] += __shfl_xor_sync(~0u, dot[0], o);
+        if (tiles == 1) {
+          if (lane % 8 == 0 && f0 + lane / 8 < n) dots[f0 + lane / 8] = dot[0];
+        } else {
+          // one after the other: in a short list two of the four may be tiles of one place
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            if (lane == 8 * a && f0 + a < n) {
+              const int t = (f0 + a) / total, k = f0 + a - t * total;
+              dots[k] = (t ? dots[k] : 0.0f) + dot[0];
+            }
+            __syncwarp();
+          }
+        }
+      }
     }
   }
-  __device__ __forceinline__ void tile() {
-    clear();
-    int i0 = 0;
-#pragma unroll 1
-    for (; i0 + AHEAD <= total; i0 += AHEAD) batch<true>(i0, AHEAD);
-    if (i0 < total) batch<false>(i0, total - i0);
+  // Zeros to a row of dw.
+  __device__ __forceinline__ void zeros(int64_t col) const {
+    constexpr int kWide = VECOUT ? VEC : 1;
+    Vec<T, kWide> out;
+#pragma unroll
+    for (int v = 0; v < kWide; ++v) out.v[v] = 0.0f;
+    for (int64_t j = lane * kWide; j < c.d; j += 32 * kWide) out.store_stream(static_cast<T*>(c.dw) + col * c.d + j);
   }
 };
 
-// Adds a long column's pieces in their order (by the warp that ended last).
-template <typename T, int VEC>
-__device__ __noinline__ void join_pieces(const float* part, const float* part_bias, unsigned n_pieces, int64_t d, T* dw, T* dbias) {
-  const int lane = threadIdx.x % 32;
-  if (dw) {
-    constexpr int kHold = VEC == 1 ? 1 : 4;
-    for (int64_t j = int64_t(lane) * kHold; j < d; j += 32 * kHold) {
-      float out[kHold] = {};
-#pragma unroll 8
-      for (unsigned o = 0; o < n_pieces; ++o) {
-        Vec<float, kHold> t;
-        t.load(part + int64_t(o) * d + j);
-#pragma unroll
-        for (int v = 0; v < kHold; ++v) out[v] += t.v[v];
-      }
-#pragma unroll
-      for (int v = 0; v < kHold; ++v) dw[j + v] = from_f32<T>(out[v]);
-    }
-  }
-  if (dbias && lane == 0) {
-    float t = 0.0f;
-    for (unsigned o = 0; o < n_pieces; ++o) t += __ldcg(&part_bias[o]);
-    *dbias = from_f32<T>(t);
-  }
-}
-
-template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL, bool DOTS>
-__global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel(const ColParams q) {
+template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS, bool VECOUT>
+__global__ void __launch_bounds__(kColWarps * 32, DOTS ? 4 : 6) column_sums_kernel(const ColParams q) {
+  extern __shared__ __align__(16) unsigned char rings[];
   __shared__ Entry ent_all[kColWarps][kColPiece + 1];
   __shared__ Entry raw_all[kColWarps][kColPiece];  // the next item's places on their way
   __shared__ Item item_all[kColWarps][2];          // and the records of the two next items
@@ -843,8 +952,9 @@ __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel
   float* dots = dots_all[warp];
   T* dw = static_cast<T*>(c.dw);
   T* dbias = static_cast<T*>(c.dbias);
-  using Stream = ColumnStream<T, VEC, CHUNKS, AHEAD, FULL, DOTS>;
-  Stream st{c, ent, dots, nullptr, lane, 0, dw != nullptr, 0};
+  using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS, VECOUT>;
+  Stream st{c, rings + warp * (Stream::kSlots * Stream::kSlotBytes), ent, dots, nullptr, lane, 0,
+            static_cast<int>((c.d + Stream::kTile - 1) / Stream::kTile), dw != nullptr};
   const unsigned pieces = q.g.hdr->pieces, work = pieces + q.g.hdr->tasks, step = gridDim.x * kColWarps;
   // Records and places are copied to shared memory ahead of their use: the record two items ahead, the places one.
   auto fetch_item = [&](unsigned wk, int slot) {
@@ -886,9 +996,10 @@ __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel
     if (item.columns) {
       empty = ~__reduce_or_sync(~0u, lane < total ? 1u << (e.group - item.group) : 0u) & ((1u << item.columns) - 1u);
       if (total > 1) {
-        // groups (their place in the item) above s: one number to compare
-        const uint64_t key = (uint64_t(e.group - item.group) << 32) | e.s;
+        // groups (their place in the item, 3 bits) above s (29 bits): one number to compare
+        const uint32_t key = ((e.group - item.group) << 29) | e.s;
         rank = 0;
+#pragma unroll 4
         for (int i = 0; i < total; ++i) rank += __shfl_sync(~0u, key, i) < key;
       }
     }
@@ -896,14 +1007,10 @@ __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel
     if (lane == 0) ent[total].group = kNoPlace;
     __syncwarp();
     st.total = total;
-    st.part = n_pieces > 1 ? q.g.part + int64_t(slot) * c.d : nullptr;
-    if (st.want_dw || DOTS) {
-      for (st.d0 = 0; st.d0 < c.d; st.d0 += Stream::kTile) {
-        st.tile();
-        if (st.want_dw)
-          for (unsigned b = empty; b; b &= b - 1) st.flush(c0 + __ffs(b) - 1);  // (the sums are zero again)
-      }
-    }
+    st.part = n_pieces > 1 ? q.g.part + int64_t(slot) * q.g.part_ld : nullptr;
+    if (dw || DOTS) st.run();
+    if (dw)
+      for (unsigned b = empty; b; b &= b - 1) st.zeros(c0 + __ffs(b) - 1);
     __syncwarp();
     if (DOTS && lane < total) static_cast<T*>(c.dots)[ent[lane].s] = from_f32<T>(dots[lane]);
     float sum = 0.0f;
@@ -920,43 +1027,100 @@ __global__ void __launch_bounds__(kColWarps * 32, kColBlocks) column_sums_kernel
     }
     if (n_pieces == 1) continue;
     if (dbias && lane == 0) q.g.part_bias[slot] = sum;
-    __threadfence();
-    __syncwarp();
-    unsigned seen = 0;
-    if (lane == 0) seen = atomicAdd(&q.g.ticket[item.slot0], 1u);
-    seen = __shfl_sync(~0u, seen, 0);
-    if (seen != n_pieces - 1) continue;
-    __threadfence();
-    join_pieces<T, VEC>(q.g.part + int64_t(item.slot0) * c.d, q.g.part_bias + item.slot0, n_pieces, c.d, dw ? dw + c0 * c.d : nullptr,
-                        dbias ? dbias + c0 : nullptr);
+    const Join join{q.g.part, dbias ? q.g.part_bias : nullptr, q.g.ticket, 1, q.g.part_ld, 0, c.d, item.slot0, item.index, n_pieces};
+    join_pieces(join, dw ? dw + c0 * c.d : nullptr, static_cast<const T*>(nullptr), dbias ? dbias + c0 : nullptr);
   }
 }
 
-template <typename T, int VEC, int CHUNKS, int AHEAD, bool FULL>
-cudaError_t launch_columns_v(const ColParams& q, unsigned grid, cudaStream_t st) {
-  return q.c.dots ? launch_after(column_sums_kernel<T, VEC, CHUNKS, AHEAD, FULL, true>, grid, kColWarps * 32, 0, st, q)
-                  : launch_after(column_sums_kernel<T, VEC, CHUNKS, AHEAD, FULL, false>, grid, kColWarps * 32, 0, st, q);
+// Rows of `d` values copied to rows of `ld` (whole 16-byte vectors), zeros in between.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pad_rows_kernel(const T* src, int64_t lds, int64_t rows, int64_t d, T* dst, int64_t ld) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t per = (ld + 4 * kThreads - 1) / (4 * kThreads);
+  const int64_t r = blockIdx.x / per, j0 = (blockIdx.x - r * per) * (4 * kThreads) + threadIdx.x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t j = j0 + e * kThreads;
+    if (j < ld) dst[r * ld + j] = j < d ? src[r * lds + j] : from_f32<T>(0.0f);
+  }
+}
+
+template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS, bool VECOUT>
+cudaError_t launch_columns_d(const ColParams& q, cudaStream_t st) {
+  using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS, VECOUT>;
+  auto kernel = column_sums_kernel<T, VEC, CHUNKS, FULL, DOTS, VECOUT>;
+  constexpr int kSmem = kColWarps * Stream::kSlots * Stream::kSlotBytes;
+  static int each = 0;  // blocks that fit an SM
+  if (!each) {
+    int n = 0;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kColWarps * 32, kSmem);
+    if (e != cudaSuccess) return e;
+    each = n < 1 ? 1 : n;
+  }
+  const int64_t blocks = (q.g.max_pieces + q.g.max_tasks + kColWarps - 1) / kColWarps, fit = int64_t(each) * ops_sm_count();
+  return launch_after(kernel, static_cast<unsigned>(blocks < fit ? blocks : fit), kColWarps * 32, kSmem, st, q);
+}
+template <typename T, int VEC, int CHUNKS, bool FULL, bool VECOUT>
+cudaError_t launch_columns_v(const ColParams& q, cudaStream_t st) {
+  return q.c.dots ? launch_columns_d<T, VEC, CHUNKS, FULL, true, VECOUT>(q, st)
+                  : launch_columns_d<T, VEC, CHUNKS, FULL, false, VECOUT>(q, st);
+}
+
+bool column_vectors(const ColumnSums& c) {
+  const int vec = c.dtype == kF32 ? 4 : 8;
+  return c.d % vec == 0 && c.ldx % vec == 0 && aligned16(c.x) && (!c.dots || (c.ldw % vec == 0 && aligned16(c.w))) &&
+         (!c.dw || aligned16(c.dw));
 }
 
 template <typename T>
-cudaError_t launch_columns_t(const ColParams& q, cudaStream_t st) {
-  const ColumnSums& c = q.c;
+cudaError_t pad_rows(const void* src, int64_t lds, int64_t rows, int64_t d, void* dst, int64_t ld, cudaStream_t st) {
+  const int64_t blocks = rows * ((ld + 4 * kThreads - 1) / (4 * kThreads));
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_after(pad_rows_kernel<T>, static_cast<unsigned>(blocks), kThreads, 0, st, static_cast<const T*>(src), lds, rows, d,
+                      static_cast<T*>(dst), ld);
+}
+
+template <typename T>
+cudaError_t launch_columns_t(const ColParams& given, cudaStream_t st) {
   constexpr int kVec = 16 / sizeof(T);
-  cudaError_t e = launch_grouping<false, T>(c.places, c.coef, q.g, static_cast<T*>(c.dots), st);
+  ColParams q = given;
+  ColumnSums& c = q.c;
+  cudaError_t e = cudaSuccess;
+  if (q.padded) {
+    e = pad_rows<T>(c.x, c.ldx, c.places.rows, c.d, q.pad_x, q.pad_ld, st);
+    c.x = q.pad_x;
+    c.ldx = q.pad_ld;
+    if (e == cudaSuccess && c.dots) {
+      e = pad_rows<T>(c.w, c.ldw, c.places.n, c.d, q.pad_w, q.pad_ld, st);
+      c.w = q.pad_w;
+      c.ldw = q.pad_ld;
+    }
+  }
+  if (e == cudaSuccess) e = launch_grouping<false, T>(c.places, c.coef, q.g, static_cast<T*>(c.dots), st);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (q.g.max_pieces + q.g.max_tasks + kColWarps - 1) / kColWarps, fit = kColBlocks * ops_sm_count();
-  const bool vec = c.d % kVec == 0 && c.ldx % kVec == 0 && aligned16(c.x) && (!c.dots || (c.ldw % kVec == 0 && aligned16(c.w))) &&
-                   (!c.dw || aligned16(c.dw));
-  const unsigned grid = static_cast<unsigned>(blocks < fit ? blocks : fit);
-  if (!vec) return launch_columns_v<T, 1, 8, 2, false>(q, grid, st);
-  return c.d % (64 * kVec) == 0 ? launch_columns_v<T, kVec, 2, 2, true>(q, grid, st)
-                                : launch_columns_v<T, kVec, 2, 2, false>(q, grid, st);
+  if (q.padded) return launch_columns_v<T, kVec, 2, false, false>(q, st);
+  if (!column_vectors(c)) return launch_columns_v<T, 1, 8, false, true>(q, st);
+  return c.d % (64 * kVec) == 0 ? launch_columns_v<T, kVec, 2, true, true>(q, st) : launch_columns_v<T, kVec, 2, false, true>(q, st);
 }
 
 ColParams plan_columns(const ColumnSums& c, Scratch& sc) {
   ColParams q{};
   q.c = c;
-  q.g = plan_groups(sc, c.places.total, c.places.n, kColPiece, c.dw ? c.d : 0, 1, c.dbias != nullptr, true);
+  // Pieces small enough for three to each of 16 warps an SM: where a few columns hold most places, one of 32 places of 771
+  // f32 values kept its warp for 67 us.
+  int piece = kColPiece;
+  while (piece > 8 && c.places.total < int64_t(3) * piece * 16 * ops_sm_count()) piece /= 2;
+  q.g = plan_groups(sc, c.places.total, c.places.n, piece, c.dw ? c.d : 0, 1, c.dbias != nullptr, true);
+  // Rows that do not hold whole vectors are copied to some that do (a pass over x and w), unless there are few places.
+  if (!column_vectors(c) && (c.dw || c.dots) && 2 * c.places.total >= c.places.n) {
+    const int vec = c.dtype == kF32 ? 4 : 8, size = c.dtype == kF32 ? 4 : 2;
+    q.pad_ld = (c.d + vec - 1) / vec * vec;
+    q.pad_x = sc.take<char>(c.places.rows * q.pad_ld * size);
+    q.pad_w = c.dots ? sc.take<char>(c.places.n * q.pad_ld * size) : nullptr;
+    q.padded = true;
+  }
   return q;
 }
 

@@ -164,6 +164,7 @@ int check_places(const int64_t* idx, int64_t count, int per_row, int dtype, int6
   if (per_row && count > 0 && rows > kMaxExtent / count) return TOPK_EUNSUPPORTED;
   if (count > kMaxExtent) return TOPK_EUNSUPPORTED;
   const int64_t total = per_row ? rows * count : count;
+  if (total >= (int64_t(1) << 29)) return TOPK_EUNSUPPORTED;
   if (total > 0 && !idx) return TOPK_EINVAL;
   return TOPK_OK;
 }

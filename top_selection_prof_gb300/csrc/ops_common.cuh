@@ -43,6 +43,17 @@ struct Pair {
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
+// VEC values: 16 bytes, or one f32; one bf16 (which has no such copy) goes through a register.
+template <int VEC, typename T>
+__device__ __forceinline__ void copy_async(T* dst, const T* src) {
+  if constexpr (VEC > 1) copy_async16(dst, src);
+  else if constexpr (sizeof(T) == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+  else *dst = __ldg(src);
+}
+// Groups of copies, done in their order: all but the last N are in place after copy_async_wait_group<N>().
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // VEC consecutive values as they are stored.
@@ -50,6 +61,7 @@ template <typename T, int VEC>
 struct Raw {
   uint4 u;
   __device__ __forceinline__ void load_nc(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
   // Values 2 i and 2 i + 1 as f32.
   __device__ __forceinline__ Pair pair(int i) const {
@@ -62,6 +74,7 @@ template <typename T>
 struct Raw<T, 1> {
   T u;
   __device__ __forceinline__ void load_nc(const T* p) { u = __ldg(p); }
+  __device__ __forceinline__ void load(const T* p) { u = *p; }
   __device__ __forceinline__ void clear() { u = from_f32<T>(0.0f); }
 };
 
@@ -70,12 +83,21 @@ struct Raw<T, 1> {
 template <typename T, int VEC>
 struct Vec {
   static_assert(VEC == 1 || VEC * sizeof(T) == 16, "one value or 16 bytes");
+  static constexpr int kWide = VEC;
   float v[VEC];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (VEC == 1) {
       v[0] = to_f32(*p);
     } else {
       set(*reinterpret_cast<const uint4*>(p));
+    }
+  }
+  // (past the L1: what another block wrote in this launch)
+  __device__ __forceinline__ void load_cg(const T* p) {
+    if constexpr (VEC == 1) {
+      v[0] = to_f32(__ldcg(p));
+    } else {
+      set(__ldcg(reinterpret_cast<const uint4*>(p)));
     }
   }
   __device__ __forceinline__ void load_nc(const T* p) {
