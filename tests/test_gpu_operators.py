@@ -497,6 +497,42 @@ def test_another_stream_and_selections_in_between(tk):
         assert torch.equal(p, q) and torch.equal(p, r) and torch.equal(p, s)
 
 
+def test_autoencoder_step_against_autograd(tk):
+    """The example's step: its gradients against torch's own through the same selection in 64 bits."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "batchtopk_autoencoder.py")
+    spec = importlib.util.spec_from_file_location("batchtopk_autoencoder", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    rows, width, features, k = 96, 64, 700, 8
+    model = ex.Autoencoder(width, features, k, dtype=torch.float32)
+    data = ex.batches(width, 150, 6, rows, dtype=torch.float32)
+    x = next(data)
+    loss, y, grads = model.gradients(x)
+    p = {n: t.double().cpu().requires_grad_() for n, t in model.params.items()}
+    x64 = x.double().cpu()
+    z = torch.relu(x64 @ p["w_enc"].T + p["b_enc"])
+    top = z.detach().flatten().topk(rows * k + 1).values
+    assert float(top[-2] - top[-1]) > 1e-6          # the f32 activations select the same places
+    code = torch.where(z >= top[-2], z, 0.0)
+    want_y = code @ p["w_dec"] + p["b_dec"]
+    want = (want_y - x64).square().sum() / rows
+    want.backward()
+    # sums of at most max(rows, features, width) products, each factor itself such a sum: 4 n 2^-23 of the largest value's scale
+    tol = 4 * features * 2.0 ** -23
+    want, want_y = want.detach(), want_y.detach()
+    assert abs(float(loss) - float(want)) <= tol * float(want)
+    assert float((y.double().cpu() - want_y).abs().max()) <= tol * float(want_y.abs().max() + 1)
+    for n, g in grads.items():
+        scale = float(p[n].grad.abs().max())
+        assert float((g.double().cpu() - p[n].grad).abs().max()) <= tol * max(scale, 1.0), n
+    norm = float(model.step(x)[1])                  # the step itself: the norm of these gradients, and finite parameters
+    whole = math.sqrt(sum(float(t.grad.square().sum()) for t in p.values()))
+    assert abs(norm - whole) <= tol * whole
+    assert all(bool(t.isfinite().all()) for t in model.params.values())
+
+
 def test_refusals(tk):
     x, w = torch.ones(4, 8, device="cuda"), torch.ones(6, 8, device="cuda")
     i, v = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.ones(3, device="cuda")

@@ -734,24 +734,19 @@ cudaError_t launch_rows_t(const RowParams& q, cudaStream_t st) {
 // written where the column ends.  (131072 places of 512 bf16 values, with the
 // dots: loads into registers two ahead leave a warp 0.7 us a place, 57 us in
 // all; bulk copies of whole rows 95 us, one taking an SM some 70 ns.)
-// FULL: every tile is whole.  VECOUT: dw takes whole vectors too; else x and w
-// are copies with rows of whole vectors, zeros past d.
+// FULL: every tile is whole.
 constexpr int kColWarps = 4;
 
 struct ColParams {
   ColumnSums c;
   Groups g;
-  bool padded;    // x and w go through copies with rows of pad_ld values
-  int64_t pad_ld;
-  void* pad_x;
-  void* pad_w;
 };
 
-template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS, bool VECOUT>
+template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS>
 struct ColumnStream {
   static constexpr int kTile = 32 * VEC * CHUNKS;
   static constexpr int kTileBytes = kTile * sizeof(T);
-  static constexpr int kSlots = DOTS ? 6 : 8;
+  static constexpr int kSlots = DOTS ? 6 : 4;
   static constexpr int kSlotBytes = kTileBytes * (DOTS ? 2 : 1);
   static constexpr int kPairs = VEC / 2;
   const ColumnSums& c;
@@ -792,14 +787,9 @@ struct ColumnStream {
         }
         if (part) {
 #pragma unroll
-          for (int v = 0; v < VEC; ++v)
-            if (VECOUT || at(tile, h) + v < c.d) part[at(tile, h) + v] = out.v[v];
-        } else if constexpr (VECOUT) {
-          out.store_stream(static_cast<T*>(c.dw) + col * c.d + at(tile, h));
+          for (int v = 0; v < VEC; ++v) part[at(tile, h) + v] = out.v[v];
         } else {
-#pragma unroll
-          for (int v = 0; v < VEC; ++v)
-            if (at(tile, h) + v < c.d) static_cast<T*>(c.dw)[col * c.d + at(tile, h) + v] = from_f32<T>(out.v[v]);
+          out.store_stream(static_cast<T*>(c.dw) + col * c.d + at(tile, h));
         }
       }
     }
@@ -926,15 +916,14 @@ struct ColumnStream {
   }
   // Zeros to a row of dw.
   __device__ __forceinline__ void zeros(int64_t col) const {
-    constexpr int kWide = VECOUT ? VEC : 1;
-    Vec<T, kWide> out;
+    Vec<T, VEC> out;
 #pragma unroll
-    for (int v = 0; v < kWide; ++v) out.v[v] = 0.0f;
-    for (int64_t j = lane * kWide; j < c.d; j += 32 * kWide) out.store_stream(static_cast<T*>(c.dw) + col * c.d + j);
+    for (int v = 0; v < VEC; ++v) out.v[v] = 0.0f;
+    for (int64_t j = lane * VEC; j < c.d; j += 32 * VEC) out.store_stream(static_cast<T*>(c.dw) + col * c.d + j);
   }
 };
 
-template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS, bool VECOUT>
+template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS>
 __global__ void __launch_bounds__(kColWarps * 32, DOTS ? 4 : 6) column_sums_kernel(const ColParams q) {
   extern __shared__ __align__(16) unsigned char rings[];
   __shared__ Entry ent_all[kColWarps][kColPiece + 1];
@@ -952,7 +941,7 @@ __global__ void __launch_bounds__(kColWarps * 32, DOTS ? 4 : 6) column_sums_kern
   float* dots = dots_all[warp];
   T* dw = static_cast<T*>(c.dw);
   T* dbias = static_cast<T*>(c.dbias);
-  using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS, VECOUT>;
+  using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS>;
   Stream st{c, rings + warp * (Stream::kSlots * Stream::kSlotBytes), ent, dots, nullptr, lane, 0,
             static_cast<int>((c.d + Stream::kTile - 1) / Stream::kTile), dw != nullptr};
   const unsigned pieces = q.g.hdr->pieces, work = pieces + q.g.hdr->tasks, step = gridDim.x * kColWarps;
@@ -1032,24 +1021,10 @@ __global__ void __launch_bounds__(kColWarps * 32, DOTS ? 4 : 6) column_sums_kern
   }
 }
 
-// Rows of `d` values copied to rows of `ld` (whole 16-byte vectors), zeros in between.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pad_rows_kernel(const T* src, int64_t lds, int64_t rows, int64_t d, T* dst, int64_t ld) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int64_t per = (ld + 4 * kThreads - 1) / (4 * kThreads);
-  const int64_t r = blockIdx.x / per, j0 = (blockIdx.x - r * per) * (4 * kThreads) + threadIdx.x;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int64_t j = j0 + e * kThreads;
-    if (j < ld) dst[r * ld + j] = j < d ? src[r * lds + j] : from_f32<T>(0.0f);
-  }
-}
-
-template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS, bool VECOUT>
+template <typename T, int VEC, int CHUNKS, bool FULL, bool DOTS>
 cudaError_t launch_columns_d(const ColParams& q, cudaStream_t st) {
-  using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS, VECOUT>;
-  auto kernel = column_sums_kernel<T, VEC, CHUNKS, FULL, DOTS, VECOUT>;
+  using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS>;
+  auto kernel = column_sums_kernel<T, VEC, CHUNKS, FULL, DOTS>;
   constexpr int kSmem = kColWarps * Stream::kSlots * Stream::kSlotBytes;
   static int each = 0;  // blocks that fit an SM
   if (!each) {
@@ -1062,10 +1037,10 @@ cudaError_t launch_columns_d(const ColParams& q, cudaStream_t st) {
   const int64_t blocks = (q.g.max_pieces + q.g.max_tasks + kColWarps - 1) / kColWarps, fit = int64_t(each) * ops_sm_count();
   return launch_after(kernel, static_cast<unsigned>(blocks < fit ? blocks : fit), kColWarps * 32, kSmem, st, q);
 }
-template <typename T, int VEC, int CHUNKS, bool FULL, bool VECOUT>
+template <typename T, int VEC, int CHUNKS, bool FULL>
 cudaError_t launch_columns_v(const ColParams& q, cudaStream_t st) {
-  return q.c.dots ? launch_columns_d<T, VEC, CHUNKS, FULL, true, VECOUT>(q, st)
-                  : launch_columns_d<T, VEC, CHUNKS, FULL, false, VECOUT>(q, st);
+  return q.c.dots ? launch_columns_d<T, VEC, CHUNKS, FULL, true>(q, st)
+                  : launch_columns_d<T, VEC, CHUNKS, FULL, false>(q, st);
 }
 
 bool column_vectors(const ColumnSums& c) {
@@ -1075,34 +1050,13 @@ bool column_vectors(const ColumnSums& c) {
 }
 
 template <typename T>
-cudaError_t pad_rows(const void* src, int64_t lds, int64_t rows, int64_t d, void* dst, int64_t ld, cudaStream_t st) {
-  const int64_t blocks = rows * ((ld + 4 * kThreads - 1) / (4 * kThreads));
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_after(pad_rows_kernel<T>, static_cast<unsigned>(blocks), kThreads, 0, st, static_cast<const T*>(src), lds, rows, d,
-                      static_cast<T*>(dst), ld);
-}
-
-template <typename T>
-cudaError_t launch_columns_t(const ColParams& given, cudaStream_t st) {
+cudaError_t launch_columns_t(const ColParams& q, cudaStream_t st) {
+  const ColumnSums& c = q.c;
   constexpr int kVec = 16 / sizeof(T);
-  ColParams q = given;
-  ColumnSums& c = q.c;
-  cudaError_t e = cudaSuccess;
-  if (q.padded) {
-    e = pad_rows<T>(c.x, c.ldx, c.places.rows, c.d, q.pad_x, q.pad_ld, st);
-    c.x = q.pad_x;
-    c.ldx = q.pad_ld;
-    if (e == cudaSuccess && c.dots) {
-      e = pad_rows<T>(c.w, c.ldw, c.places.n, c.d, q.pad_w, q.pad_ld, st);
-      c.w = q.pad_w;
-      c.ldw = q.pad_ld;
-    }
-  }
-  if (e == cudaSuccess) e = launch_grouping<false, T>(c.places, c.coef, q.g, static_cast<T*>(c.dots), st);
+  const cudaError_t e = launch_grouping<false, T>(c.places, c.coef, q.g, static_cast<T*>(c.dots), st);
   if (e != cudaSuccess) return e;
-  if (q.padded) return launch_columns_v<T, kVec, 2, false, false>(q, st);
-  if (!column_vectors(c)) return launch_columns_v<T, 1, 8, false, true>(q, st);
-  return c.d % (64 * kVec) == 0 ? launch_columns_v<T, kVec, 2, true, true>(q, st) : launch_columns_v<T, kVec, 2, false, true>(q, st);
+  if (!column_vectors(c)) return launch_columns_v<T, 1, 8, false>(q, st);
+  return c.d % (64 * kVec) == 0 ? launch_columns_v<T, kVec, 2, true>(q, st) : launch_columns_v<T, kVec, 2, false>(q, st);
 }
 
 ColParams plan_columns(const ColumnSums& c, Scratch& sc) {
@@ -1113,14 +1067,6 @@ ColParams plan_columns(const ColumnSums& c, Scratch& sc) {
   int piece = kColPiece;
   while (piece > 8 && c.places.total < int64_t(3) * piece * 16 * ops_sm_count()) piece /= 2;
   q.g = plan_groups(sc, c.places.total, c.places.n, piece, c.dw ? c.d : 0, 1, c.dbias != nullptr, true);
-  // Rows that do not hold whole vectors are copied to some that do (a pass over x and w), unless there are few places.
-  if (!column_vectors(c) && (c.dw || c.dots) && 2 * c.places.total >= c.places.n) {
-    const int vec = c.dtype == kF32 ? 4 : 8, size = c.dtype == kF32 ? 4 : 2;
-    q.pad_ld = (c.d + vec - 1) / vec * vec;
-    q.pad_x = sc.take<char>(c.places.rows * q.pad_ld * size);
-    q.pad_w = c.dots ? sc.take<char>(c.places.n * q.pad_ld * size) : nullptr;
-    q.padded = true;
-  }
   return q;
 }
 
