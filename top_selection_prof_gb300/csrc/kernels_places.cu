@@ -67,6 +67,13 @@ struct Groups {
   int piece, share;   // most places of a piece, and of columns that share a warp
 };
 
+// The groupings that one call's kernels make together: by column, by row, or both.
+struct Groupings {
+  Groups g[2];
+  bool by_row[2];
+  int n;
+};
+
 Groups plan_groups(Scratch& sc, int64_t total, int64_t groups, int piece, int64_t d, int64_t d_tiles, bool bias, bool tasks) {
   Groups g{};
   g.n_groups = groups;
@@ -124,17 +131,20 @@ __device__ __forceinline__ float coef_of(const Coef& c, int64_t s) {
 }
 
 // ---- grouping -----------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) zero_groups_kernel(const Groups g) {
+__global__ void __launch_bounds__(kThreads) zero_groups_kernel(const Groupings all) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (i == 0) *g.hdr = GroupHeader{0, 0, 0, 0, 0};
-  if (i < g.n_groups) g.count[i] = 0;
-  if (i < g.n_tickets) g.ticket[i] = 0;
+  for (int k = 0; k < all.n; ++k) {
+    const Groups& g = all.g[k];
+    if (i == 0) *g.hdr = GroupHeader{0, 0, 0, 0, 0};
+    if (i < g.n_groups) g.count[i] = 0;
+    if (i < g.n_tickets) g.ticket[i] = 0;
+  }
 }
 
-template <bool BY_ROW, typename T>
-__global__ void __launch_bounds__(kThreads) count_places_kernel(const Places p, const Coef c, const Groups g, T* dots) {
+template <typename T>
+__global__ void __launch_bounds__(kThreads) count_places_kernel(const Places p, const Coef c, const Groupings all, T* dots) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t s = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -142,14 +152,15 @@ __global__ void __launch_bounds__(kThreads) count_places_kernel(const Places p, 
   uint32_t row, col;
   const bool in = locate(p, s, &row, &col);
   const float coef = coef_of<T>(c, s);
-  if (!in) {
-    g.seen[s] = make_uint4(0, 0, kNoPlace, 0);
-    if (dots) dots[s] = from_f32<T>(0.0f);
-    return;
-  }
-  const uint32_t group = BY_ROW ? row : col;
-  const uint32_t rank = atomicAdd(&g.count[group], 1u);
-  g.seen[s] = make_uint4(group, BY_ROW ? col : row, rank, __float_as_uint(coef));
+  uint32_t rank[2] = {kNoPlace, kNoPlace};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < all.n && in) rank[k] = atomicAdd(&all.g[k].count[all.by_row[k] ? row : col], 1u);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < all.n)
+      all.g[k].seen[s] = make_uint4(all.by_row[k] ? row : col, all.by_row[k] ? col : row, rank[k], __float_as_uint(coef));
+  if (!in && dots) dots[s] = from_f32<T>(0.0f);
 }
 
 // Inclusive sum over the block's threads; *total: of all.  (Two barriers.)
@@ -178,12 +189,15 @@ __device__ __forceinline__ unsigned block_scan(unsigned v, unsigned* total) {
 
 // A base for every group, from a scan over the block's groups and one atomic
 // on the running total; the pieces and the list of long groups likewise.
-__global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g) {
-  const unsigned piece = g.piece, share = g.share;
+__global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groupings all) {
   __shared__ unsigned block_base;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t i = int64_t(blockIdx.x) * kGroupsBlock + threadIdx.x;
+  const int64_t blocks0 = (all.g[0].n_groups + kGroupsBlock - 1) / kGroupsBlock;
+  const int which = blockIdx.x >= blocks0;
+  const Groups& g = all.g[which];
+  const unsigned piece = g.piece, share = g.share;
+  const int64_t i = (int64_t(blockIdx.x) - (which ? blocks0 : 0)) * kGroupsBlock + threadIdx.x;
   const unsigned cnt = i < g.n_groups ? g.count[i] : 0u;
   unsigned total;
   const unsigned incl = block_scan<kGroupsBlock>(cnt, &total);
@@ -219,28 +233,33 @@ __global__ void __launch_bounds__(kGroupsBlock) group_base_kernel(const Groups g
   }
 }
 
-__global__ void __launch_bounds__(kThreads) place_kernel(const Groups g, int64_t total) {
+__global__ void __launch_bounds__(kThreads) place_kernel(const Groupings all, int64_t total) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t s = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (s >= total) return;
-  const uint4 v = g.seen[s];
-  if (v.z == kNoPlace) return;
-  g.order[g.start[v.x] + v.z] = Entry{static_cast<uint32_t>(s), v.y, __uint_as_float(v.w), v.x};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k >= all.n) break;
+    const Groups& g = all.g[k];
+    const uint4 v = g.seen[s];
+    if (v.z != kNoPlace) g.order[g.start[v.x] + v.z] = Entry{static_cast<uint32_t>(s), v.y, __uint_as_float(v.w), v.x};
+  }
 }
 
 // Long groups in order of s, a block each: the rank of a place is the number
 // of smaller s in its group, counted directly for up to kSortSmall places and
 // by a bitmap of s, kBitmapBits at a time, beyond.
-__global__ void __launch_bounds__(kSortThreads) sort_long_kernel(const Groups g, int64_t total, int words) {
+__global__ void __launch_bounds__(kSortThreads) sort_long_kernel(const Groupings all, int64_t total, int words) {
   extern __shared__ uint32_t sort_smem[];
   uint32_t* bitmap = sort_smem;
   uint32_t* before = sort_smem + words;  // set bits before each word
   grid_dependency_wait();
   grid_launch_dependents();
-  const unsigned n_long = g.hdr->longs;
+  const unsigned long0 = all.g[0].hdr->longs, n_long = long0 + (all.n > 1 ? all.g[1].hdr->longs : 0u);
   for (unsigned l = blockIdx.x; l < n_long; l += gridDim.x) {
-    const unsigned group = g.longs[l];
+    const Groups& g = all.g[l >= long0];
+    const unsigned group = g.longs[l >= long0 ? l - long0 : l];
     const int cnt = static_cast<int>(g.count[group]);
     const Entry* src = g.order + g.start[group];
     Entry* dst = g.sorted + g.start[group];
@@ -300,26 +319,32 @@ __global__ void __launch_bounds__(kSortThreads) sort_long_kernel(const Groups g,
   }
 }
 
-template <bool BY_ROW, typename T>
-cudaError_t launch_grouping(const Places& p, const Coef& c, const Groups& g, T* dots, cudaStream_t st) {
-  const int64_t zero = g.n_groups > g.n_tickets ? g.n_groups : g.n_tickets;
-  cudaError_t e = launch_after(zero_groups_kernel, static_cast<unsigned>((zero + kThreads - 1) / kThreads), kThreads, 0, st, g);
+template <typename T>
+cudaError_t launch_grouping(const Places& p, const Coef& c, const Groupings& all, T* dots, cudaStream_t st) {
+  int64_t zero = 0, bases = 0, longs = 0;
+  for (int k = 0; k < all.n; ++k) {
+    const Groups& g = all.g[k];
+    const int64_t z = g.n_groups > g.n_tickets ? g.n_groups : g.n_tickets;
+    zero = z > zero ? z : zero;
+    bases += (g.n_groups + kGroupsBlock - 1) / kGroupsBlock;
+    longs += g.max_longs;
+  }
+  cudaError_t e = launch_after(zero_groups_kernel, static_cast<unsigned>((zero + kThreads - 1) / kThreads), kThreads, 0, st, all);
   const unsigned blocks = static_cast<unsigned>((p.total + kThreads - 1) / kThreads);
-  if (e == cudaSuccess && blocks) e = launch_after(count_places_kernel<BY_ROW, T>, blocks, kThreads, 0, st, p, c, g, dots);
+  if (e == cudaSuccess && blocks) e = launch_after(count_places_kernel<T>, blocks, kThreads, 0, st, p, c, all, dots);
   if (e != cudaSuccess) return e;
-  e = launch_after(group_base_kernel, static_cast<unsigned>((g.n_groups + kGroupsBlock - 1) / kGroupsBlock), kGroupsBlock, 0, st,
-                   g);
+  e = launch_after(group_base_kernel, static_cast<unsigned>(bases), kGroupsBlock, 0, st, all);
   if (e != cudaSuccess || !blocks) return e;  // (no places: every group is empty)
-  e = launch_after(place_kernel, blocks, kThreads, 0, st, g, p.total);
-  if (e != cudaSuccess || !g.max_longs) return e;
+  e = launch_after(place_kernel, blocks, kThreads, 0, st, all, p.total);
+  if (e != cudaSuccess || !longs) return e;
   const int64_t bits = p.total < kBitmapBits ? p.total : kBitmapBits;
   int words = static_cast<int>((bits + 31) / 32);
   if (words < kSortSmall) words = kSortSmall;
   e = cudaFuncSetAttribute(sort_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBitmapBits / 4));
   if (e != cudaSuccess) return e;
   const int64_t most = 3 * ops_sm_count();
-  return launch_after(sort_long_kernel, static_cast<unsigned>(g.max_longs < most ? g.max_longs : most), kSortThreads,
-                      static_cast<size_t>(words) * 8, st, g, p.total, words);
+  return launch_after(sort_long_kernel, static_cast<unsigned>(longs < most ? longs : most), kSortThreads,
+                      static_cast<size_t>(words) * 8, st, all, p.total, words);
 }
 
 // ---- sums by row ------------------------------------------------------------------
@@ -709,18 +734,7 @@ template <typename T>
 cudaError_t launch_rows_t(const RowParams& q, cudaStream_t st) {
   const RowSums& r = q.r;
   constexpr int kVec = 16 / sizeof(T);
-  cudaError_t e = cudaSuccess;
-  int64_t work;
-  if (r.places.per_row) {
-    work = r.places.rows * q.pieces_per_row;
-    if (q.pieces_per_row > 1)
-      e = launch_after(zero_groups_kernel, static_cast<unsigned>((q.g.n_tickets + kThreads - 1) / kThreads), kThreads, 0, st, q.g);
-  } else {
-    work = q.g.max_pieces + r.places.rows;
-    e = launch_grouping<true, T>(r.places, r.coef, q.g, static_cast<T*>(nullptr), st);
-  }
-  if (e != cudaSuccess) return e;
-  work *= q.d_tiles;
+  const int64_t work = (r.places.per_row ? r.places.rows * q.pieces_per_row : q.g.max_pieces + r.places.rows) * q.d_tiles;
   return row_vectors<T>(r) ? launch_rows_v<T, kVec>(q, work, st) : launch_rows_v<T, 1>(q, work, st);
 }
 
@@ -1053,8 +1067,6 @@ template <typename T>
 cudaError_t launch_columns_t(const ColParams& q, cudaStream_t st) {
   const ColumnSums& c = q.c;
   constexpr int kVec = 16 / sizeof(T);
-  const cudaError_t e = launch_grouping<false, T>(c.places, c.coef, q.g, static_cast<T*>(c.dots), st);
-  if (e != cudaSuccess) return e;
   if (!column_vectors(c)) return launch_columns_v<T, 1, 8, false>(q, st);
   return c.d % (64 * kVec) == 0 ? launch_columns_v<T, kVec, 2, true>(q, st) : launch_columns_v<T, kVec, 2, false>(q, st);
 }
@@ -1072,23 +1084,45 @@ ColParams plan_columns(const ColumnSums& c, Scratch& sc) {
 
 }  // namespace
 
-size_t row_sums_scratch_bytes(const RowSums& r) {
+size_t sums_scratch_bytes(const ColumnSums* c, const RowSums* r) {
   Scratch sc;
-  plan_rows(r, sc);
+  if (c) plan_columns(*c, sc);
+  if (r) plan_rows(*r, sc);
   return sc.used();
 }
-cudaError_t launch_row_sums(const RowSums& r, Scratch& sc, cudaStream_t st) {
-  const RowParams q = plan_rows(r, sc);
-  return r.dtype == kF32 ? launch_rows_t<float>(q, st) : launch_rows_t<__nv_bfloat16>(q, st);
-}
-size_t column_sums_scratch_bytes(const ColumnSums& c) {
-  Scratch sc;
-  plan_columns(c, sc);
-  return sc.used();
-}
-cudaError_t launch_column_sums(const ColumnSums& c, Scratch& sc, cudaStream_t st) {
-  const ColParams q = plan_columns(c, sc);
-  return c.dtype == kF32 ? launch_columns_t<float>(q, st) : launch_columns_t<__nv_bfloat16>(q, st);
+
+cudaError_t launch_sums(const ColumnSums* c, const RowSums* r, Scratch& sc, cudaStream_t st) {
+  ColParams cols{};
+  RowParams rows{};
+  Groupings all{};
+  if (c) {
+    cols = plan_columns(*c, sc);
+    all.g[all.n++] = cols.g;
+  }
+  if (r) {
+    rows = plan_rows(*r, sc);
+    if (!r->places.per_row) {
+      all.by_row[all.n] = true;
+      all.g[all.n++] = rows.g;
+    } else if (rows.pieces_per_row > 1) {  // (only its tickets, at zero)
+      Groupings one{};
+      one.g[0] = rows.g;
+      one.n = 1;
+      const cudaError_t e = launch_after(zero_groups_kernel, static_cast<unsigned>((rows.g.n_tickets + kThreads - 1) / kThreads),
+                                         kThreads, 0, st, one);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  const Places& p = c ? c->places : r->places;
+  const Coef& coef = c ? c->coef : r->coef;
+  const bool f32 = (c ? c->dtype : r->dtype) == kF32;
+  cudaError_t e = cudaSuccess;
+  if (all.n)
+    e = f32 ? launch_grouping<float>(p, coef, all, static_cast<float*>(c ? c->dots : nullptr), st)
+            : launch_grouping<__nv_bfloat16>(p, coef, all, static_cast<__nv_bfloat16*>(c ? c->dots : nullptr), st);
+  if (e == cudaSuccess && c) e = f32 ? launch_columns_t<float>(cols, st) : launch_columns_t<__nv_bfloat16>(cols, st);
+  if (e == cudaSuccess && r) e = f32 ? launch_rows_t<float>(rows, st) : launch_rows_t<__nv_bfloat16>(rows, st);
+  return e;
 }
 
 }  // namespace tk

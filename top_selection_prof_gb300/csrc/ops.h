@@ -131,10 +131,9 @@ struct ColumnSums {
   void* dbias;    // nullable, n values
   void* dots;     // nullable, one a place (0 where a position is out of range)
 };
-size_t row_sums_scratch_bytes(const RowSums& r);
-cudaError_t launch_row_sums(const RowSums& r, Scratch& sc, cudaStream_t st);
-size_t column_sums_scratch_bytes(const ColumnSums& c);
-cudaError_t launch_column_sums(const ColumnSums& c, Scratch& sc, cudaStream_t st);
+// Either or both (null: not wanted; both over the same places and coefficients).
+size_t sums_scratch_bytes(const ColumnSums* c, const RowSums* r);
+cudaError_t launch_sums(const ColumnSums* c, const RowSums* r, Scratch& sc, cudaStream_t st);
 
 // ---- gradient norm (kernels_norm.cu) --------------------------------------------
 struct ClipTensor {

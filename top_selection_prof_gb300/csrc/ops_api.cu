@@ -169,14 +169,10 @@ int check_places(const int64_t* idx, int64_t count, int per_row, int dtype, int6
   return TOPK_OK;
 }
 
-// Runs the sums by column and by row that are asked for (either null) on one scratch block, one after the other.
+// Runs the sums by column and by row and the column sums that are asked for (null: not) on one scratch block.
 int run_sums(const ColumnSums* cols, const RowSums* rws, const SlopeSums* sums_in, cudaStream_t st) {
   SlopeSums sums{};
-  size_t bytes = cols ? column_sums_scratch_bytes(*cols) : 0;
-  if (rws) {
-    const size_t b = row_sums_scratch_bytes(*rws);
-    bytes = b > bytes ? b : bytes;
-  }
+  size_t bytes = cols || rws ? sums_scratch_bytes(cols, rws) : 0;
   if (sums_in) {
     sums = *sums_in;
     Scratch sc;
@@ -185,13 +181,9 @@ int run_sums(const ColumnSums* cols, const RowSums* rws, const SlopeSums* sums_i
   }
   void* base = nullptr;
   cudaError_t e = block_of(st, bytes, &base);
-  if (e == cudaSuccess && cols) {
+  if (e == cudaSuccess && (cols || rws)) {
     Scratch sc(base);
-    e = launch_column_sums(*cols, sc, st);
-  }
-  if (e == cudaSuccess && rws) {
-    Scratch sc(base);
-    e = launch_row_sums(*rws, sc, st);
+    e = launch_sums(cols, rws, sc, st);
   }
   if (e == cudaSuccess && sums_in) {
     Scratch sc(base);
