@@ -342,7 +342,7 @@ int topk_select_noalloc(const void* x, int dtype, int64_t rows, int64_t n, int64
  *     order in which blocks run: the same call gives the same bits.
  *   - Outputs marked "nullable" are not computed when null.
  *   - Extents are below 2^31 and a selection's places below 2^29
- *     (EUNSUPPORTED beyond).  Scratch memory comes from
+ *     (EUNSUPPORTED beyond, and where a launch cannot count its blocks).  Scratch memory comes from
  *     a per-(device, stream) block of these operators, grown on demand.
  * ------------------------------------------------------------------------ */
 
@@ -420,7 +420,8 @@ int topk_grad_norm(const void* const* grads, const int64_t* counts, const int* d
 
 /*
  * The same norm, and out[i] = grads[i] * min(1, max_norm / (*norm + 1e-6)).
- * out[i] == grads[i] clips in place; otherwise the two do not overlap.  A norm
+ * out[i] == grads[i] clips in place; otherwise the two do not overlap.  A
+ * tensor is listed once.  A norm
  * that is not finite carries over to the results as the formula says.
  * EINVAL: max_norm < 0 or NaN.
  */

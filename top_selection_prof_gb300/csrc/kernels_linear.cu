@@ -132,7 +132,7 @@ cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStrea
   p.ldp = g.ldp;
   p.tiles_n = (g.n + kTile - 1) / kTile;
   const int64_t tiles = p.tiles_n * ((g.m + kTile - 1) / kTile);
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  if (tiles > INT32_MAX) return cudaErrorNotSupported;
   return launch_after(simt_product_kernel<T>, static_cast<unsigned>(tiles), kSimtThreads, 0, st, p);
 }
 
@@ -368,7 +368,7 @@ cudaError_t launch_slope_sums_t(const SlopeSums& s, cudaStream_t st) {
   const bool vec = slope_vectors<T>(s);
   const int64_t wide = 32 * (vec ? kVec : 1);
   const int64_t blocks = parts * ((s.n + wide - 1) / wide);
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);
   cudaError_t e = vec ? launch_slope_act<T, kVec>(s, each, grid, st) : launch_slope_act<T, 1>(s, each, grid, st);
   if (e == cudaSuccess && s.dbias)

@@ -901,7 +901,7 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
 cudaError_t align_rows(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_t ld, cudaStream_t st) {
   const int64_t rows = operand_rows(o, i, k), cols = operand_cols(o, i, k);
   const int64_t blocks = rows * ((cols + 1023) / 1024);
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
   return launch_after(align_rows_kernel, static_cast<unsigned>(blocks), 256, 0, st, static_cast<const __nv_bfloat16*>(o.p), o.ld,
                       rows, cols, dst, ld);
 }
@@ -931,13 +931,13 @@ size_t mma_scratch_bytes(const Product& g) {
 
 cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cudaStream_t st) {
   MmaPlan q;
-  if (!plan_mma(g, sc, &q)) return cudaErrorInvalidValue;
+  if (!plan_mma(g, sc, &q)) return cudaErrorNotSupported;
   const bool f32 = g.dtype == kF32;
   int* other = words + kOpsOther;
   cudaError_t e = cudaSuccess;
   if (f32) {
     Split a, b;
-    if (!split_of(g.a, g.m, g.k, q.copy_a, q.ld_a, &a) || !split_of(g.b, g.n, g.k, q.copy_b, q.ld_b, &b)) return cudaErrorInvalidValue;
+    if (!split_of(g.a, g.m, g.k, q.copy_a, q.ld_a, &a) || !split_of(g.b, g.n, g.k, q.copy_b, q.ld_b, &b)) return cudaErrorNotSupported;
     e = launch_after(split_rows_kernel, a.blocks + b.blocks, 256, 0, st, a, b, other, call);
   } else {
     if (q.copy_a) e = align_rows(g.a, g.m, g.k, q.copy_a, q.ld_a, st);

@@ -725,7 +725,7 @@ template <typename T, int VEC>
 cudaError_t launch_rows_v(const RowParams& q, int64_t work, cudaStream_t st) {
   const bool many = many_rows(q.r);
   const int64_t grid = many ? (work + kRowWarps - 1) / kRowWarps : work;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
   if (many)
     return launch_after(row_sums_warp_kernel<T, VEC, VEC == 1 ? kRowChunks1 : 1, VEC == 1 ? 4 : 8>, static_cast<unsigned>(grid),
                         kRowWarps * 32, 0, st, q);

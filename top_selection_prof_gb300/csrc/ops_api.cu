@@ -73,9 +73,11 @@ cudaError_t block_of(cudaStream_t st, size_t bytes, void** out, int** words = nu
   return cudaSuccess;
 }
 
+// cudaErrorNotSupported: more blocks or tiles than a launch counts.
 int status_of(cudaError_t e) {
   if (e == cudaSuccess) return TOPK_OK;
-  return e == cudaErrorMemoryAllocation ? TOPK_ENOMEM : TOPK_ECUDA;
+  cudaGetLastError();  // (reported here, not to the caller's next CUDA call)
+  return e == cudaErrorMemoryAllocation ? TOPK_ENOMEM : e == cudaErrorNotSupported ? TOPK_EUNSUPPORTED : TOPK_ECUDA;
 }
 
 // No exception leaves a C entry: the library's own containers can only run out of host memory.
