@@ -137,12 +137,12 @@ cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStrea
 }
 
 // ---------------------------------------------------------------------------
-// Products of few rows: y = act(x w^T + bias) + residual for at most kFewRows
-// rows of x, one pass over w at memory speed.  A warp takes kFewCols rows of w
-// (or a KS-th of their length), 16 bytes of each a lane and step, and keeps
-// kFewCols x R sums; the lanes' sums are added by exchanging halves.
+// Products of few rows: y = act(x w^T + bias) + residual, one pass over w for
+// each R <= 8 rows of x.  A warp takes kFewCols rows of w (or a KS-th of their
+// length), 16 bytes of each a lane and step, and keeps kFewCols x R sums, of
+// even and odd k side by side; the lanes' sums are added by exchanging halves.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 8, kFewCols = 4, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+constexpr int kFewCols = 4, kFewThreads = 256, kFewWarps = kFewThreads / 32;
 
 template <typename T>
 struct FewParams {
@@ -168,27 +168,64 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int groups = kFewWarps / ks, group = warp / ks, part = warp % ks;
   const int64_t n0 = (int64_t(blockIdx.x) * groups + group) * kFewCols;
+  const int64_t r0 = int64_t(blockIdx.y) * R;
   float acc[kSums] = {};
   const T* wp[kFewCols];
 #pragma unroll
   for (int c = 0; c < kFewCols; ++c) wp[c] = p.w + min(n0 + c, p.n - 1) * p.ldw;
   const T* xp[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) xp[r] = p.x + min(int64_t(r), p.rows - 1) * p.ldx;
+  for (int r = 0; r < R; ++r) xp[r] = p.x + min(r0 + r, p.rows - 1) * p.ldx;
   const int64_t k1 = min(p.k, (part + 1) * p.k_run);
-#pragma unroll 2
-  for (int64_t k = part * p.k_run + lane * VEC; k < k1; k += 32 * VEC) {
-    Vec<T, VEC> wv[kFewCols];
+  if constexpr (VEC == 1) {
+#pragma unroll 4
+    for (int64_t k = part * p.k_run + lane; k < k1; k += 32) {
+      float wv[kFewCols];
 #pragma unroll
-    for (int c = 0; c < kFewCols; ++c) wv[c].load_nc(wp[c] + k);
+      for (int c = 0; c < kFewCols; ++c) wv[c] = to_f32(__ldg(wp[c] + k));
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      Vec<T, VEC> xv;
-      xv.load_nc(xp[r] + k);
+      for (int r = 0; r < R; ++r) {
+        const float xv = to_f32(__ldg(xp[r] + k));
 #pragma unroll
-      for (int c = 0; c < kFewCols; ++c)
+        for (int c = 0; c < kFewCols; ++c) acc[c * R + r] = fmaf(wv[c], xv, acc[c * R + r]);
+      }
+    }
+  } else {
+    Pair two[kSums];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) acc[c * R + r] = fmaf(wv[c].v[v], xv.v[v], acc[c * R + r]);
+    for (int i = 0; i < kSums; ++i) two[i] = Pair::of(0.0f, 0.0f);
+    // the next step's part of w on its way
+    Raw<T, VEC> next[kFewCols];
+    int64_t k = part * p.k_run + lane * VEC;
+#pragma unroll
+    for (int c = 0; c < kFewCols; ++c)
+      if (k < k1) next[c].load_nc(wp[c] + k);
+#pragma unroll 1
+    for (; k < k1; k += 32 * VEC) {
+      Pair wv[kFewCols][VEC / 2];
+#pragma unroll
+      for (int c = 0; c < kFewCols; ++c) {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) wv[c][i] = next[c].pair(i);
+        if (k + 32 * VEC < k1) next[c].load_nc(wp[c] + k + 32 * VEC);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        Raw<T, VEC> xr;
+        xr.load_nc(xp[r] + k);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          const Pair xv = xr.pair(i);
+#pragma unroll
+          for (int c = 0; c < kFewCols; ++c) two[c * R + r].fma(wv[c][i], xv);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+      float lo, hi;
+      two[i].get(&lo, &hi);
+      acc[i] = lo + hi;
     }
   }
   // halves exchanged until a lane holds one sum: sum i in the lanes whose high bits say i
@@ -211,7 +248,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T
   if (part != 0 || lane >= kSums) return;
   float z = 0.0f;
   for (int q = 0; q < ks; ++q) z += sums[group * ks + q][lane];
-  const int64_t j = n0 + lane / R, i = lane % R;
+  const int64_t j = n0 + lane / R, i = r0 + lane % R;
   if (j >= p.n || i >= p.rows) return;
   z += p.bias ? to_f32(p.bias[j]) : 0.0f;
   if (p.pre) p.pre[i * p.ldp + j] = from_f32<T>(z);
@@ -220,17 +257,33 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T
   p.y[i * p.ldy + j] = from_f32<T>(z);
 }
 
+template <typename T, int VEC, int R>
+cudaError_t launch_few_r(const FewParams<T>& p, int ks, cudaStream_t st) {
+  const int64_t per = kFewCols * (kFewWarps / ks);
+  const dim3 grid(static_cast<unsigned>((p.n + per - 1) / per), static_cast<unsigned>((p.rows + R - 1) / R));
+  return launch_after(few_rows_kernel<T, VEC, R>, grid, kFewThreads, 0, st, p, ks);
+}
 template <typename T, int VEC>
 cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
-  const int64_t per = kFewCols * (kFewWarps / ks);
-  const unsigned grid = static_cast<unsigned>((p.n + per - 1) / per);
-  if (p.rows <= 1) return launch_after(few_rows_kernel<T, VEC, 1>, grid, kFewThreads, 0, st, p, ks);
-  if (p.rows <= 2) return launch_after(few_rows_kernel<T, VEC, 2>, grid, kFewThreads, 0, st, p, ks);
-  if (p.rows <= 4) return launch_after(few_rows_kernel<T, VEC, 4>, grid, kFewThreads, 0, st, p, ks);
-  return launch_after(few_rows_kernel<T, VEC, 8>, grid, kFewThreads, 0, st, p, ks);
+  if (p.rows <= 1) return launch_few_r<T, VEC, 1>(p, ks, st);
+  if (p.rows <= 2) return launch_few_r<T, VEC, 2>(p, ks, st);
+  if (p.rows <= 4) return launch_few_r<T, VEC, 4>(p, ks, st);
+  return launch_few_r<T, VEC, 8>(p, ks, st);
 }
 
-bool few_rows(const Product& g) { return g.m <= kFewRows && g.a.k_inner && g.b.k_inner; }
+// Whether the rows are few enough, by the times of both (us; w beyond the caches).  Measured, here and on the tensor cores:
+// bf16 rows 1, 4, 8, 16 of 512 -> 12288: 3.5, 4.8, 7.9, 14.4 and 8.4, 8.4, 8.4, 7.1; 4096 -> 16384: 23, 29, 64, 126 and
+// 41, 36, 37, 26; 16384 -> 512: 4.0, 5.4, 7.3, 13.3 and 45 to 47.  f32 rows 8, 16, 32 of 512 -> 12288: 8.3, 15, 27 and
+// 34, 32, 33; 4096 -> 16384: 89, 176, 330 and 243.
+bool few_rows(const Product& g) {
+  if (g.m > 32 || !g.a.k_inner || !g.b.k_inner) return false;
+  if (g.m <= 4) return true;
+  const double passes = static_cast<double>((g.m + 7) / 8), values = static_cast<double>(g.n) * g.k;
+  const double depth = static_cast<double>((g.k + 63) / 64), waves = static_cast<double>((g.n + 256 * 76 - 1) / (256 * 76));
+  if (g.dtype == kF32) return 2.0 + passes * values * 4 / 2.7e6 < 12.0 + waves * 6 * depth * 0.2 + values * 16 / 5e6;
+  const double products = waves * depth * 0.17, bytes = values * 2 / 5e6;
+  return 2.0 + passes * values * 2 / 2.1e6 < 6.0 + (products > bytes ? products : bytes);
+}
 
 template <typename T>
 cudaError_t launch_few(const Product& g, cudaStream_t st) {

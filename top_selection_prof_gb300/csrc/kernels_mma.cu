@@ -833,7 +833,7 @@ bool encode(CUtensorMap* map, bool f32, const void* p, int64_t cols, int64_t row
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr double kStageUs = 0.30;  // a stage of a tile, as timed
+constexpr double kStageUs = 0.30, kJoinUs = 11.0;  // a stage of a tile, and the way of its parts, as timed
 
 bool tma_rows(const void* p, int64_t ld, int size) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0; }
 
@@ -869,19 +869,37 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
   // (32 tiles of 192 stages) 60.7 -> 45.4 us, 12288 x 4096 x 512 (96 of 64) 48.0 -> 46.6; 300 x 4096 x 1000 (8 of 64)
   // 23.9 -> 25.1, 4096 x 1024 x 8192 (512 of 16) 44.5 -> 53.4, 2000 x 16384 x 4096 (128 of 256, where all SMs at once
   // draw the power limit) 158 -> 179.
-  const int64_t rest_waves = tiles / slots > 1 ? tiles / slots - 1 : 0;
+  int pairs = 0;
+  int64_t rest_waves = 0;
+  if (tiles < slots) {
+    // fewer tiles than pairs: as many pairs a tile as make the shortest run and its parts' way (a stage takes 0.17 us
+    // where few SMs work, 0.30 where all do)
+    auto stage_us = [&](double busy) { return 0.17 + 0.13 * busy / slots; };
+    double best = d.k_blocks * stage_us(static_cast<double>(tiles));
+    for (int64_t p = 2 * tiles; p < slots + tiles; p += tiles) {
+      const int64_t used = p < slots ? p : slots;
+      const double run = static_cast<double>(tiles) * d.k_blocks / used;
+      const double t = run * stage_us(static_cast<double>(used)) + kJoinUs + 0.8 * used / tiles;
+      if (run >= 2 && t < best) {
+        best = t;
+        pairs = static_cast<int>(used);
+      }
+    }
+  } else if (tiles % slots != 0) {
+    // the tiles past the last whole wave but one
+    rest_waves = tiles / slots - 1;
+    const int64_t shared = tiles - rest_waves * slots;
+    const double even = static_cast<double>(shared) * d.k_blocks / slots;
+    const double join = kJoinUs + 0.5 * slots / shared + 0.1 * static_cast<double>(tiles) * d.k_blocks / slots;
+    if ((2 * d.k_blocks - even) * kStageUs > join) pairs = slots;
+  }
   const int64_t shared = tiles - rest_waves * slots;
-  const double whole = static_cast<double>((tiles + slots - 1) / slots - rest_waves) * d.k_blocks;
-  const double even = static_cast<double>(shared) * d.k_blocks / slots;
-  const double parts = static_cast<double>(slots) / shared;
-  const double join = 12.0 + 0.5 * parts + 0.1 * static_cast<double>(tiles) * d.k_blocks / slots;
-  if (tiles % slots != 0 && (whole - even) * kStageUs > join && shared * d.k_blocks >= 2 * slots && shared * d.k_blocks <= INT32_MAX &&
-      shared * 2 * kEpiWarps <= kOpsWords - 64) {
-    d.pairs = slots;
+  if (pairs && shared * d.k_blocks <= INT32_MAX && shared * 2 * kEpiWarps <= kOpsWords - 64) {
+    d.pairs = pairs;
     d.waves = static_cast<int>(rest_waves);
     d.shared_tiles = static_cast<int>(shared);
-    d.run = static_cast<int>(shared * d.k_blocks / slots);
-    d.longer = static_cast<int>(shared * d.k_blocks % slots);
+    d.run = static_cast<int>(shared * d.k_blocks / pairs);
+    d.longer = static_cast<int>(shared * d.k_blocks % pairs);
   }
   // two slots a pair for runs, one for the rounds of f32
   if (d.shared_tiles || (f32 && d.depth > kRoundDepth)) q->part = sc.take<float>(int64_t(3) * d.pairs * kPairM * kTileN);

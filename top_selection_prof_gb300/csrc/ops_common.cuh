@@ -153,9 +153,9 @@ struct Vec {
 // Launches a kernel that calls grid_dependency_wait() before it touches memory:
 // it may start, and set itself up, while the grid before it in the stream ends.
 template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, const A&... args) {
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
