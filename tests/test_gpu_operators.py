@@ -222,6 +222,44 @@ def test_linear_backward_is_exact_on_whole_numbers(tk, dtype, rows, inner, outer
     same_bits(only[2], (dy.double() * (pre.double() > 0)).sum(0), "dbias alone")
 
 
+# Few rows: sums over outer in several chunks, rows past a group of eight, columns past a tile, aligned rows and others.
+FEW = [(1, 512, 3000), (4, 1032, 700), (5, 515, 4001), (8, 300, 129), (9, 128, 65), (13, 261, 5000), (24, 130, 2100),
+       (32, 516, 1000), (32, 77, 20011), (33, 77, 300)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,inner,outer", FEW)
+def test_linear_backward_of_few_rows_is_exact_on_whole_numbers(tk, dtype, rows, inner, outer):
+    g = gen(rows + inner * 5 + outer)
+    x, w, dy = ints((rows, inner), dtype, g), ints((outer, inner), dtype, g), ints((rows, outer), dtype, g)
+    for place in (lambda t: t.cuda(), strided, lambda t: strided(t, 16, 8)):
+        dx, dw, db = tk.linear_backward(place(dy), place(x), place(w))
+        same_bits(dx, dy.double() @ w.double(), "dx")
+        same_bits(dw, dy.double().T @ x.double(), "dw")
+        same_bits(db, dy.double().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,inner,outer", [(3, 70, 150), (12, 515, 900), (31, 132, 2050)])
+def test_linear_backward_of_few_rows_on_normal_values(tk, dtype, rows, inner, outer):
+    g = gen(rows)
+    x, w, dy = normals((rows, inner), dtype, g), normals((outer, inner), dtype, g, 0.1), normals((rows, outer), dtype, g)
+    dx, dw, _ = tk.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    x, w, dy = x.double(), w.double(), dy.double()
+    within(dx, dy @ w, dy.abs() @ w.abs(), outer, "dx")
+    within(dw, dy.T @ x, dy.abs().T @ x.abs(), rows, "dw")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_linear_backward_of_few_rows_keeps_nan_and_infinity_in_their_places(tk, dtype):
+    g = gen(2)
+    x, w, dy = (normals(s, dtype, g).abs() + 0.1 for s in ((5, 67), (301, 67), (5, 301)))
+    dy[1, 5], x[2, 6], w[300, 66] = math.nan, math.inf, math.inf
+    dx, dw, _ = tk.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    for got, want in ((dx, dy.double() @ w.double()), (dw, dy.double().T @ x.double())):
+        assert torch.equal(got.cpu().isnan(), want.isnan()) and torch.equal(got.cpu().isinf(), want.isinf())
+
+
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_linear_backward_of_smooth_activations(tk, dtype, act):

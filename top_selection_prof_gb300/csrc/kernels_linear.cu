@@ -430,6 +430,200 @@ cudaError_t launch_slope_sums_t(const SlopeSums& s, cudaStream_t st) {
   return e;
 }
 
+// ---------------------------------------------------------------------------
+// The gradients of up to 32 rows on the CUDA cores, every product and sum in
+// f32: w is read, or dw written, straight from and to memory, where the tensor
+// cores' path has to split f32 values into three bf16 parts or to lay out rows
+// that TMA cannot address.
+//
+// dx[r, j] = sum over i of dz[r, i] w[i, j]: a thread keeps VEC columns of
+// eight rows and goes down its chunk of w's rows, dz's values in shared memory;
+// the chunks' sums are added in their order by sum_parts_kernel.  Bound by the
+// loads of w, a pass of it for eight rows (4.9 TB/s at 2 x 4096 x 16384 f32).
+// ---------------------------------------------------------------------------
+constexpr int kAcrossThreads = 128, kAcrossDeep = 64;
+template <typename T, int VEC, int R>
+__global__ void __launch_bounds__(kAcrossThreads) few_rows_across_kernel(const Operand a, const Operand b, int64_t m, int64_t n,
+                                                                         int64_t k, int64_t chunk, float* part) {
+  constexpr int kPairs = VEC / 2;
+  __shared__ __align__(16) float as[kAcrossDeep][R];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t j = (int64_t(blockIdx.x) * kAcrossThreads + threadIdx.x) * VEC;
+  const int64_t k0 = int64_t(blockIdx.y) * chunk, k1 = min(k, k0 + chunk), r0 = int64_t(blockIdx.z) * R;
+  const T* ap = static_cast<const T*>(a.p) + r0 * a.ld;
+  const T* bp = static_cast<const T*>(b.p) + j;
+  const bool in = j < n;
+  Pair two[R][kPairs ? kPairs : 1];
+  float one[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    one[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) two[r][i] = Pair::of(0.0f, 0.0f);
+  }
+  for (int64_t i0 = k0; i0 < k1; i0 += kAcrossDeep) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < kAcrossDeep * R; e += kAcrossThreads) {
+      const int i = e % kAcrossDeep, r = e / kAcrossDeep;
+      as[i][r] = i0 + i < k1 && r0 + r < m ? to_f32(ap[r * a.ld + i0 + i]) : 0.0f;
+    }
+    __syncthreads();
+    const int deep = static_cast<int>(min(int64_t(kAcrossDeep), k1 - i0));
+    if (!in) continue;
+    constexpr int kAhead = 8;
+    for (int i = 0; i < deep; i += kAhead) {
+      Raw<T, VEC> v[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        v[e].clear();
+        if (i + e < deep) v[e].load_nc(bp + (i0 + i + e) * b.ld);
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (i + e >= deep) break;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float f = as[i + e][r];
+          if constexpr (VEC == 1) {
+            one[r] = fmaf(f, to_f32(v[e].u), one[r]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < kPairs; ++q) two[r][q].fma(Pair::of(f, f), v[e].pair(q));
+          }
+        }
+      }
+    }
+  }
+  if (!in) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r0 + r >= m) break;
+    float* dst = part + (int64_t(blockIdx.y) * m + r0 + r) * n + j;
+    if constexpr (VEC == 1) {
+      dst[0] = one[r];
+    } else {
+#pragma unroll
+      for (int q = 0; q < kPairs; ++q) {
+        float lo, hi;
+        two[r][q].get(&lo, &hi);
+        dst[2 * q] = lo;
+        dst[2 * q + 1] = hi;
+      }
+    }
+  }
+}
+
+// dw[i, j] = sum over few r of dz[r, i] x[r, j]: a thread makes 8 x 4 results,
+// its four columns 64 apart, so that a warp writes 32 neighbours whatever the
+// rows' alignment.  Bound by the stores of dw with up to some 8 rows (5.8 TB/s
+// at 2 x 4096 x 16384 f32), by the products above.
+constexpr int kOuterRows = 32, kOuterCols = 256, kOuterThreads = 256, kOuterMost = 32;
+template <typename T>
+__global__ void __launch_bounds__(kOuterThreads) few_outer_kernel(const Operand a, const Operand b, int64_t m, int64_t n, int k, T* c,
+                                                                  int64_t ldc, int64_t col_tiles) {
+  __shared__ __align__(16) float as[kOuterMost][kOuterRows];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t i0 = blockIdx.x / col_tiles * kOuterRows, j0 = blockIdx.x % col_tiles * kOuterCols;
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  const T* ap = static_cast<const T*>(a.p);
+  const T* bp = static_cast<const T*>(b.p);
+  for (int e = threadIdx.x; e < k * kOuterRows; e += kOuterThreads) {
+    const int i = e % kOuterRows, r = e / kOuterRows;
+    as[r][i] = i0 + i < m ? to_f32(ap[r * a.ld + i0 + i]) : 0.0f;
+  }
+  __syncthreads();
+  float acc[8][4] = {};
+#pragma unroll 4
+  for (int r = 0; r < k; ++r) {
+    float x[4], z[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t j = j0 + e * 64 + tx;
+      x[e] = j < n ? to_f32(__ldg(bp + r * b.ld + j)) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = as[r][ty * 8 + i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(z[i], x[e], acc[i][e]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = i0 + ty * 8 + i;
+    if (row >= m) break;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t j = j0 + e * 64 + tx;
+      if (j < n) c[row * ldc + j] = from_f32<T>(acc[i][e]);
+    }
+  }
+}
+
+bool plain_product(const Product& g) { return !g.bias && !g.residual && !g.pre && g.act == kActNone; }
+bool tma_rows(const void* p, int64_t ld, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * bytes % 16 == 0; }
+
+// Both rules compare the estimated times (us) of the two paths.  Measured for rows x inner x outer, here and on the tensor
+// cores, dx: f32 3 x 512 x 12288 14 and 66, 2 x 4096 x 16384 55 and 242, 12 x 2007 x 32552 177 and 255, 12 x 2008 x 32552
+// 112 and 252, 17 x 677 x 23699 96 and 109, 32 x 4096 x 16384 238 and 243; bf16 2 x 4096 x 16384 35 and 44, 5 x 2071 x 48416
+// 149 and 278, 12 x 2007 x 32552 182 and 172, 30 x 300 x 5000 18 and 36.
+bool few_across(const Product& g) {
+  if (!plain_product(g) || !g.a.k_inner || g.b.k_inner || g.m > 32 || g.ldc != g.n || g.m * g.n / 32 >= INT32_MAX) return false;
+  const double passes = static_cast<double>((g.m + 7) / 8), values = static_cast<double>(g.n) * g.k * 1e-6;
+  if (g.dtype == kF32) {
+    const bool vec = tma_rows(g.b.p, g.b.ld, 4) && g.n % 4 == 0;
+    return 6.0 + passes * values * (vec ? 0.9 : 1.6) < 30.0 + values * 4.0;
+  }
+  if (tma_rows(g.b.p, g.b.ld, 2)) return g.m <= 4 && g.n % 8 == 0;
+  return 6.0 + passes * values * 1.45 < 20.0 + values * 2.45;
+}
+// dw: f32 2 x 4096 x 16384 46 and 75, 12 x 2008 x 32552 79 and 77, 32 x 4096 x 16384 136 and 76, 12 x 2007 x 32552 84 and 171,
+// 16 x 2007 x 32552 96 and 170, 30 x 300 x 5000 12 and 19; bf16 5 x 2071 x 48416 82 and 103, 12 x 2007 x 32552 76 and 67,
+// 30 x 300 x 5000 11 and 18.
+bool few_outer(const Product& g) {
+  if (!plain_product(g) || g.a.k_inner || g.b.k_inner || g.k > kOuterMost) return false;
+  const double values = static_cast<double>(g.m) * g.n * 1e-6, here = 6.0 + values * (0.5 + 0.05 * static_cast<double>(g.k));
+  if (g.dtype == kF32) return here < 14.0 + values * (tma_rows(g.c, g.ldc, 4) ? 1.0 : 2.5);
+  const bool tma = tma_rows(g.a.p, g.a.ld, 2) && tma_rows(g.b.p, g.b.ld, 2) && tma_rows(g.c, g.ldc, 2);
+  return !tma && here < 10.0 + values * 0.9;
+}
+constexpr int kAcrossRows = 8;
+// Chunks of w's rows: four blocks an SM, of 64 rows at least.
+int64_t across_chunks(const Product& g) {
+  const int vec = g.dtype == kF32 ? 4 : 8;
+  const int64_t tiles = (g.n + kAcrossThreads * vec - 1) / (kAcrossThreads * vec) * ((g.m + kAcrossRows - 1) / kAcrossRows);
+  int64_t chunks = 4 * ops_sm_count() / tiles;
+  const int64_t most = (g.k + kAcrossDeep - 1) / kAcrossDeep;
+  chunks = chunks > most ? most : chunks;
+  return chunks < 1 ? 1 : chunks;
+}
+template <typename T>
+cudaError_t launch_across(const Product& g, Scratch& sc, cudaStream_t st) {
+  constexpr int kVec = 16 / sizeof(T);
+  const int64_t chunks = across_chunks(g);
+  float* part = sc.take<float>(chunks * g.m * g.n);
+  const int64_t chunk = (g.k + chunks - 1) / chunks;
+  const bool vec = g.n % kVec == 0 && g.b.ld % kVec == 0 && reinterpret_cast<uintptr_t>(g.b.p) % 16 == 0;
+  const int64_t wide = kAcrossThreads * (vec ? kVec : 1);
+  const dim3 grid(static_cast<unsigned>((g.n + wide - 1) / wide), static_cast<unsigned>((g.k + chunk - 1) / chunk),
+                  static_cast<unsigned>((g.m + kAcrossRows - 1) / kAcrossRows));
+  const cudaError_t e =
+      vec ? launch_after(few_rows_across_kernel<T, kVec, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k, chunk, part)
+          : launch_after(few_rows_across_kernel<T, 1, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k, chunk, part);
+  if (e != cudaSuccess) return e;
+  return launch_after(sum_parts_kernel<T>, static_cast<unsigned>((g.m * g.n + 31) / 32), kSumThreads, 0, st,
+                      static_cast<const float*>(part), int64_t(grid.y), g.m * g.n, static_cast<T*>(g.c));
+}
+template <typename T>
+cudaError_t launch_outer(const Product& g, cudaStream_t st) {
+  const int64_t col_tiles = (g.n + kOuterCols - 1) / kOuterCols, blocks = col_tiles * ((g.m + kOuterRows - 1) / kOuterRows);
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
+  return launch_after(few_outer_kernel<T>, static_cast<unsigned>(blocks), kOuterThreads, 0, st, g.a, g.b, g.m, g.n,
+                      static_cast<int>(g.k), static_cast<T*>(g.c), g.ldc, col_tiles);
+}
+
 }  // namespace
 
 int64_t slope_sums_parts(int64_t rows, int64_t n) {
@@ -441,12 +635,23 @@ cudaError_t launch_slope_sums(const SlopeSums& s, cudaStream_t st) {
   return s.dtype == kF32 ? launch_slope_sums_t<float>(s, st) : launch_slope_sums_t<__nv_bfloat16>(s, st);
 }
 
-size_t product_scratch_bytes(const Product& g) { return few_rows(g) ? 0 : mma_scratch_bytes(g); }
+size_t product_scratch_bytes(const Product& g) {
+  if (few_rows(g) || few_outer(g)) return 0;
+  if (few_across(g)) {
+    Scratch sc;
+    sc.take<float>(across_chunks(g) * g.m * g.n);
+    return sc.used();
+  }
+  return mma_scratch_bytes(g);
+}
 
 cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
-  if (few_rows(g)) return g.dtype == kF32 ? launch_few<float>(g, st) : launch_few<__nv_bfloat16>(g, st);
+  const bool f32 = g.dtype == kF32;
+  if (few_rows(g)) return f32 ? launch_few<float>(g, st) : launch_few<__nv_bfloat16>(g, st);
+  if (few_outer(g)) return f32 ? launch_outer<float>(g, st) : launch_outer<__nv_bfloat16>(g, st);
+  if (few_across(g)) return f32 ? launch_across<float>(g, sc, st) : launch_across<__nv_bfloat16>(g, sc, st);
   static std::atomic<int> calls{0};
-  const int call = g.dtype == kF32 ? 1 + (calls.fetch_add(1) & 0x3fffffff) : 0;
+  const int call = f32 ? 1 + (calls.fetch_add(1) & 0x3fffffff) : 0;
   return launch_mma(g, sc, words, call, st);
 }
 
