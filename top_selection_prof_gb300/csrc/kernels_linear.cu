@@ -142,7 +142,15 @@ cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStrea
 // length), 16 bytes of each a lane and step, and keeps kFewCols x R sums, of
 // even and odd k side by side; the lanes' sums are added by exchanging halves.
 // ---------------------------------------------------------------------------
-constexpr int kFewCols = 4, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+constexpr int kFewCols = 4, kFewWarps = 8;
+// Threads an SM holds at once, which bounds the registers of each.  Blocks of four warps where a thread has many: 8 rows of
+// f32 take 77 us at 4096 -> 16384 with 12 warps an SM, 91 with 8; 1 row 43 with 32 and 55 with 24.
+constexpr int few_resident(int vec, int rows) {
+  return vec == 1    ? (rows <= 2 ? 1024 : rows == 4 ? 768 : 512)
+         : rows == 1 ? 1024
+         : rows == 2 ? (vec == 4 ? 768 : 512)
+                     : (rows == 4 ? 512 : 384);
+}
 
 template <typename T>
 struct FewParams {
@@ -160,13 +168,13 @@ struct FewParams {
 };
 
 template <typename T, int VEC, int R>
-__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T> p, int ks) {
+__global__ void __launch_bounds__(few_resident(VEC, R)) few_rows_kernel(const FewParams<T> p, int ks) {
   constexpr int kSums = kFewCols * R;
   __shared__ float sums[kFewWarps][kSums];
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int groups = kFewWarps / ks, group = warp / ks, part = warp % ks;
+  const int groups = int(blockDim.x) / 32 / ks, group = warp / ks, part = warp % ks;
   const int64_t n0 = (int64_t(blockIdx.x) * groups + group) * kFewCols;
   const int64_t r0 = int64_t(blockIdx.y) * R;
   float acc[kSums] = {};
@@ -259,9 +267,10 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams<T
 
 template <typename T, int VEC, int R>
 cudaError_t launch_few_r(const FewParams<T>& p, int ks, cudaStream_t st) {
-  const int64_t per = kFewCols * (kFewWarps / ks);
+  const int warps = R == 8 && ks <= 4 ? 4 : kFewWarps;
+  const int64_t per = kFewCols * (warps / ks);
   const dim3 grid(static_cast<unsigned>((p.n + per - 1) / per), static_cast<unsigned>((p.rows + R - 1) / R));
-  return launch_after(few_rows_kernel<T, VEC, R>, grid, kFewThreads, 0, st, p, ks);
+  return launch_after(few_rows_kernel<T, VEC, R>, grid, 32 * warps, 0, st, p, ks);
 }
 template <typename T, int VEC>
 cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
@@ -271,16 +280,21 @@ cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
   return launch_few_r<T, VEC, 8>(p, ks, st);
 }
 
+bool tma_rows(const void* p, int64_t ld, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * bytes % 16 == 0; }
+
 // Whether the rows are few enough, by the times of both (us; w beyond the caches).  Measured, here and on the tensor cores:
 // bf16 rows 1, 4, 8, 16 of 512 -> 12288: 3.5, 4.8, 7.9, 14.4 and 8.4, 8.4, 8.4, 7.1; 4096 -> 16384: 23, 29, 64, 126 and
-// 41, 36, 37, 26; 16384 -> 512: 4.0, 5.4, 7.3, 13.3 and 45 to 47.  f32 rows 8, 16, 32 of 512 -> 12288: 8.3, 15, 27 and
-// 34, 32, 33; 4096 -> 16384: 89, 176, 330 and 243.
+// 41, 36, 37, 26; 16384 -> 512: 4.0, 5.4, 7.3, 13.3 and 45 to 47.  f32 rows 8, 16, 32 of 512 -> 12288: 8.3, 12, 27 and
+// 34, 32, 33; 4096 -> 16384: 77, 143, 310 and 243.  bf16 rows off 16-byte boundaries, 5 of 2071 -> 48416, 12, 24 and 32 of
+// 2007 -> 32552: 112, 150, 192 to 249 and 268, 165, 165; 16 and 32 of 515 -> 12288: 16, 28 and 23.
 bool few_rows(const Product& g) {
   if (g.m > 32 || !g.a.k_inner || !g.b.k_inner) return false;
   if (g.m <= 4) return true;
   const double passes = static_cast<double>((g.m + 7) / 8), values = static_cast<double>(g.n) * g.k;
+  const double v = values * 1e-6;
+  if (g.dtype != kF32 && !tma_rows(g.b.p, g.b.ld, 2)) return 6.0 + passes * v * 1.1 < 16.0 + v * 2.35;
   const double depth = static_cast<double>((g.k + 63) / 64), waves = static_cast<double>((g.n + 256 * 76 - 1) / (256 * 76));
-  if (g.dtype == kF32) return 2.0 + passes * values * 4 / 2.7e6 < 12.0 + waves * 6 * depth * 0.2 + values * 16 / 5e6;
+  if (g.dtype == kF32) return 2.0 + passes * values * 4 / 3.4e6 < 12.0 + waves * 6 * depth * 0.2 + values * 16 / 5e6;
   const double products = waves * depth * 0.17, bytes = values * 2 / 5e6;
   return 2.0 + passes * values * 2 / 2.1e6 < 6.0 + (products > bytes ? products : bytes);
 }
@@ -563,7 +577,6 @@ __global__ void __launch_bounds__(kOuterThreads) few_outer_kernel(const Operand 
 }
 
 bool plain_product(const Product& g) { return !g.bias && !g.residual && !g.pre && g.act == kActNone; }
-bool tma_rows(const void* p, int64_t ld, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * bytes % 16 == 0; }
 
 // Both rules compare the estimated times (us) of the two paths.  Measured for rows x inner x outer, here and on the tensor
 // cores, dx: f32 3 x 512 x 12288 14 and 66, 2 x 4096 x 16384 55 and 242, 12 x 2007 x 32552 177 and 255, 12 x 2008 x 32552
