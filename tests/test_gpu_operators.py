@@ -224,7 +224,7 @@ def test_linear_backward_is_exact_on_whole_numbers(tk, dtype, rows, inner, outer
 
 # Few rows: sums over outer in several chunks, rows past a group of eight, columns past a tile, aligned rows and others.
 FEW = [(1, 512, 3000), (4, 1032, 700), (5, 515, 4001), (8, 300, 129), (9, 128, 65), (13, 261, 5000), (24, 130, 2100),
-       (32, 516, 1000), (32, 77, 20011), (33, 77, 300)]
+       (32, 516, 1000), (32, 77, 20011), (33, 77, 300), (48, 515, 900), (49, 515, 900)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -237,6 +237,16 @@ def test_linear_backward_of_few_rows_is_exact_on_whole_numbers(tk, dtype, rows, 
         same_bits(dx, dy.double() @ w.double(), "dx")
         same_bits(dw, dy.double().T @ x.double(), "dw")
         same_bits(db, dy.double().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,inner,outer", FEW + [(2, 2050, 33), (40, 515, 13000), (41, 515, 1300), (7, 9000, 33)])
+def test_linear_of_few_rows_is_exact_on_whole_numbers(tk, dtype, rows, inner, outer):
+    g = gen(rows + inner + outer)
+    x, w, b = ints((rows, inner), dtype, g), ints((outer, inner), dtype, g), ints((outer,), dtype, g, -9, 9)
+    z = x.double() @ w.double().T + b.double()
+    for place in (lambda t: t.cuda(), strided, lambda t: strided(t, 16, 8)):
+        same_bits(tk.linear(place(x), place(w), b.cuda(), act="relu"), z.clamp(min=0), "relu")
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -144,12 +144,10 @@ cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStrea
 // ---------------------------------------------------------------------------
 constexpr int kFewCols = 4, kFewWarps = 8;
 // Threads an SM holds at once, which bounds the registers of each.  Blocks of four warps where a thread has many: 8 rows of
-// f32 take 77 us at 4096 -> 16384 with 12 warps an SM, 91 with 8; 1 row 43 with 32 and 55 with 24.
+// f32 take 75 us at 4096 -> 16384 with 12 warps an SM, 91 with 8; 1 row 43 with 32 and 55 with 24.  (Two rows have no variant
+// of their own: 36 us at 4096 -> 16384 bf16, 29 as four.)
 constexpr int few_resident(int vec, int rows) {
-  return vec == 1    ? (rows <= 2 ? 1024 : rows == 4 ? 768 : 512)
-         : rows == 1 ? 1024
-         : rows == 2 ? (vec == 4 ? 768 : 512)
-                     : (rows == 4 ? 512 : 384);
+  return rows == 1 ? 1024 : vec == 1 ? (rows == 4 ? 768 : 512) : (rows == 4 ? 512 : 384);
 }
 
 template <typename T>
@@ -175,8 +173,9 @@ __global__ void __launch_bounds__(few_resident(VEC, R)) few_rows_kernel(const Fe
   grid_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int groups = int(blockDim.x) / 32 / ks, group = warp / ks, part = warp % ks;
-  const int64_t n0 = (int64_t(blockIdx.x) * groups + group) * kFewCols;
-  const int64_t r0 = int64_t(blockIdx.y) * R;
+  const unsigned passes = static_cast<unsigned>((p.rows + R - 1) / R);  // side by side, so that w is in L2 for all but the first
+  const int64_t n0 = (int64_t(blockIdx.x / passes) * groups + group) * kFewCols;
+  const int64_t r0 = blockIdx.x % passes * R;
   float acc[kSums] = {};
   const T* wp[kFewCols];
 #pragma unroll
@@ -269,13 +268,13 @@ template <typename T, int VEC, int R>
 cudaError_t launch_few_r(const FewParams<T>& p, int ks, cudaStream_t st) {
   const int warps = R == 8 && ks <= 4 ? 4 : kFewWarps;
   const int64_t per = kFewCols * (warps / ks);
-  const dim3 grid(static_cast<unsigned>((p.n + per - 1) / per), static_cast<unsigned>((p.rows + R - 1) / R));
-  return launch_after(few_rows_kernel<T, VEC, R>, grid, 32 * warps, 0, st, p, ks);
+  const int64_t blocks = (p.n + per - 1) / per * ((p.rows + R - 1) / R);
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
+  return launch_after(few_rows_kernel<T, VEC, R>, static_cast<unsigned>(blocks), 32 * warps, 0, st, p, ks);
 }
 template <typename T, int VEC>
 cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
   if (p.rows <= 1) return launch_few_r<T, VEC, 1>(p, ks, st);
-  if (p.rows <= 2) return launch_few_r<T, VEC, 2>(p, ks, st);
   if (p.rows <= 4) return launch_few_r<T, VEC, 4>(p, ks, st);
   return launch_few_r<T, VEC, 8>(p, ks, st);
 }
@@ -284,17 +283,16 @@ bool tma_rows(const void* p, int64_t ld, int64_t bytes) { return reinterpret_cas
 
 // Whether the rows are few enough, by the times of both (us; w beyond the caches).  Measured, here and on the tensor cores:
 // bf16 rows 1, 4, 8, 16 of 512 -> 12288: 3.5, 4.8, 7.9, 14.4 and 8.4, 8.4, 8.4, 7.1; 4096 -> 16384: 23, 29, 64, 126 and
-// 41, 36, 37, 26; 16384 -> 512: 4.0, 5.4, 7.3, 13.3 and 45 to 47.  f32 rows 8, 16, 32 of 512 -> 12288: 8.3, 12, 27 and
-// 34, 32, 33; 4096 -> 16384: 77, 143, 310 and 243.  bf16 rows off 16-byte boundaries, 5 of 2071 -> 48416, 12, 24 and 32 of
-// 2007 -> 32552: 112, 150, 192 to 249 and 268, 165, 165; 16 and 32 of 515 -> 12288: 16, 28 and 23.
+// 41, 36, 37, 26; 16384 -> 512: 4.0, 5.4, 7.3, 13.3 and 45 to 47.  f32 rows 8, 32 and 40: 512 -> 12288 10,
+// 21, 27 and 33; 4096 -> 16384 75, 189, 227 and 245; 2007 -> 32552 108 (12), 197, 241 and 251.  bf16 rows off 16-byte
+// boundaries: 5 of 2071 -> 48416 87 and 268; 12, 24 and 32 of 2007 -> 32552 109, 158, 202 and 164; 32 of 515 -> 12288 27, 23.
 bool few_rows(const Product& g) {
-  if (g.m > 32 || !g.a.k_inner || !g.b.k_inner) return false;
-  if (g.m <= 4) return true;
+  if (g.m > 40 || !g.a.k_inner || !g.b.k_inner) return false;
+  if (g.m <= 4 || g.dtype == kF32) return true;
   const double passes = static_cast<double>((g.m + 7) / 8), values = static_cast<double>(g.n) * g.k;
   const double v = values * 1e-6;
-  if (g.dtype != kF32 && !tma_rows(g.b.p, g.b.ld, 2)) return 6.0 + passes * v * 1.1 < 16.0 + v * 2.35;
+  if (!tma_rows(g.b.p, g.b.ld, 2)) return 6.0 + passes * v * 0.85 < 16.0 + v * 2.35;
   const double depth = static_cast<double>((g.k + 63) / 64), waves = static_cast<double>((g.n + 256 * 76 - 1) / (256 * 76));
-  if (g.dtype == kF32) return 2.0 + passes * values * 4 / 3.4e6 < 12.0 + waves * 6 * depth * 0.2 + values * 16 / 5e6;
   const double products = waves * depth * 0.17, bytes = values * 2 / 5e6;
   return 2.0 + passes * values * 2 / 2.1e6 < 6.0 + (products > bytes ? products : bytes);
 }
@@ -445,37 +443,62 @@ cudaError_t launch_slope_sums_t(const SlopeSums& s, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// The gradients of up to 32 rows on the CUDA cores, every product and sum in
+// The gradients of few rows on the CUDA cores, every product and sum in
 // f32: w is read, or dw written, straight from and to memory, where the tensor
 // cores' path has to split f32 values into three bf16 parts or to lay out rows
 // that TMA cannot address.
 //
-// dx[r, j] = sum over i of dz[r, i] w[i, j]: a thread keeps VEC columns of
+// dx[r, j] = sum over i of dz[r, i] w[i, j]: a thread keeps a few columns of
 // eight rows and goes down its chunk of w's rows, dz's values in shared memory;
 // the chunks' sums are added in their order by sum_parts_kernel.  Bound by the
-// loads of w, a pass of it for eight rows (4.9 TB/s at 2 x 4096 x 16384 f32).
+// loads of w (5.0 TB/s at 2 x 4096 x 16384 f32).  f32 columns are read one by
+// one, a warp 32 neighbours: any alignment, and in 78 registers faster than 16
+// bytes a thread in 120 (12 x 2008 x 32552: 76 and 94 us).
 // ---------------------------------------------------------------------------
 constexpr int kAcrossThreads = 128, kAcrossDeep = 64;
+// A thread's values of a row of w: VEC side by side, or four that lie a block's width apart.
+template <typename T, int VEC>
+struct Across {
+  static constexpr int kCols = VEC;
+  Raw<T, VEC> raw;
+  __device__ __forceinline__ void load(const T* p, int) { raw.load_nc(p); }
+  __device__ __forceinline__ void clear() { raw.clear(); }
+  __device__ __forceinline__ Pair pair(int i) const { return raw.pair(i); }
+};
+template <typename T>
+struct Across<T, 1> {
+  static constexpr int kCols = 4;
+  Raw<T, 1> raw[4];
+  __device__ __forceinline__ void load(const T* p, int cols) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < cols) raw[e].load_nc(p + e * kAcrossThreads);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) raw[e].clear();
+  }
+  __device__ __forceinline__ Pair pair(int i) const { return Pair::of(to_f32(raw[2 * i].u), to_f32(raw[2 * i + 1].u)); }
+};
 template <typename T, int VEC, int R>
 __global__ void __launch_bounds__(kAcrossThreads) few_rows_across_kernel(const Operand a, const Operand b, int64_t m, int64_t n,
                                                                          int64_t k, int64_t chunk, float* part) {
-  constexpr int kPairs = VEC / 2;
+  using W = Across<T, VEC>;
+  constexpr int kPairs = W::kCols / 2, kStep = VEC == 1 ? kAcrossThreads : 1, kAhead = 8;
   __shared__ __align__(16) float as[kAcrossDeep][R];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t j = (int64_t(blockIdx.x) * kAcrossThreads + threadIdx.x) * VEC;
-  const int64_t k0 = int64_t(blockIdx.y) * chunk, k1 = min(k, k0 + chunk), r0 = int64_t(blockIdx.z) * R;
+  const unsigned passes = static_cast<unsigned>((m + R - 1) / R);  // side by side, so that w is in L2 for all but the first
+  const int64_t j = int64_t(blockIdx.x / passes) * kAcrossThreads * W::kCols + threadIdx.x * (VEC == 1 ? 1 : VEC);
+  const int64_t k0 = int64_t(blockIdx.y) * chunk, k1 = min(k, k0 + chunk), r0 = blockIdx.x % passes * R;
   const T* ap = static_cast<const T*>(a.p) + r0 * a.ld;
   const T* bp = static_cast<const T*>(b.p) + j;
-  const bool in = j < n;
-  Pair two[R][kPairs ? kPairs : 1];
-  float one[R];
+  const int cols = j >= n ? 0 : VEC > 1 ? VEC : static_cast<int>(min(int64_t(4), (n - j + kStep - 1) / kStep));
+  Pair two[R][kPairs];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    one[r] = 0.0f;
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) two[r][i] = Pair::of(0.0f, 0.0f);
-  }
   for (int64_t i0 = k0; i0 < k1; i0 += kAcrossDeep) {
     __syncthreads();
     for (int e = threadIdx.x; e < kAcrossDeep * R; e += kAcrossThreads) {
@@ -484,46 +507,39 @@ __global__ void __launch_bounds__(kAcrossThreads) few_rows_across_kernel(const O
     }
     __syncthreads();
     const int deep = static_cast<int>(min(int64_t(kAcrossDeep), k1 - i0));
-    if (!in) continue;
-    constexpr int kAhead = 8;
+    if (!cols) continue;
     for (int i = 0; i < deep; i += kAhead) {
-      Raw<T, VEC> v[kAhead];
+      W v[kAhead];
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         v[e].clear();
-        if (i + e < deep) v[e].load_nc(bp + (i0 + i + e) * b.ld);
+        if (i + e < deep) v[e].load(bp + (i0 + i + e) * b.ld, cols);
       }
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         if (i + e >= deep) break;
+        Pair w[kPairs];
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) w[q] = v[e].pair(q);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float f = as[i + e][r];
-          if constexpr (VEC == 1) {
-            one[r] = fmaf(f, to_f32(v[e].u), one[r]);
-          } else {
 #pragma unroll
-            for (int q = 0; q < kPairs; ++q) two[r][q].fma(Pair::of(f, f), v[e].pair(q));
-          }
+          for (int q = 0; q < kPairs; ++q) two[r][q].fma(Pair::of(f, f), w[q]);
         }
       }
     }
   }
-  if (!in) return;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (r0 + r >= m) break;
     float* dst = part + (int64_t(blockIdx.y) * m + r0 + r) * n + j;
-    if constexpr (VEC == 1) {
-      dst[0] = one[r];
-    } else {
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) {
-        float lo, hi;
-        two[r][q].get(&lo, &hi);
-        dst[2 * q] = lo;
-        dst[2 * q + 1] = hi;
-      }
+    for (int q = 0; q < kPairs; ++q) {
+      float lo, hi;
+      two[r][q].get(&lo, &hi);
+      if (2 * q < cols) dst[2 * q * kStep] = lo;
+      if (2 * q + 1 < cols) dst[(2 * q + 1) * kStep] = hi;
     }
   }
 }
@@ -578,20 +594,16 @@ __global__ void __launch_bounds__(kOuterThreads) few_outer_kernel(const Operand 
 
 bool plain_product(const Product& g) { return !g.bias && !g.residual && !g.pre && g.act == kActNone; }
 
-// Both rules compare the estimated times (us) of the two paths.  Measured for rows x inner x outer, here and on the tensor
-// cores, dx: f32 3 x 512 x 12288 14 and 66, 2 x 4096 x 16384 55 and 242, 12 x 2007 x 32552 177 and 255, 12 x 2008 x 32552
-// 112 and 252, 17 x 677 x 23699 96 and 109, 32 x 4096 x 16384 238 and 243; bf16 2 x 4096 x 16384 35 and 44, 5 x 2071 x 48416
-// 149 and 278, 12 x 2007 x 32552 182 and 172, 30 x 300 x 5000 18 and 36.
+// Whether dx is formed by passes over w.  Measured (us) for rows x inner x outer, here and on the tensor cores: f32
+// 3 x 512 x 12288 14 and 66, 2 x 4096 x 16384 54 and 242, 12 x 2007 x 32552 76 and 255, 32 x 2007 x 32552 146 and 258; bf16
+// off 16-byte boundaries 5 x 2071 x 48416 83 and 278, 12, 24 and 32 x 2007 x 32552 85, 124, 164 and 168; bf16 that TMA
+// addresses 2 x 4096 x 16384 35 and 42, 8 x 512 x 65536 28 and 41, 16 x 4096 x 16384 72 and 35.
 bool few_across(const Product& g) {
-  if (!plain_product(g) || !g.a.k_inner || g.b.k_inner || g.m > 32 || g.ldc != g.n || g.m * g.n / 32 >= INT32_MAX) return false;
-  const double passes = static_cast<double>((g.m + 7) / 8), values = static_cast<double>(g.n) * g.k * 1e-6;
-  if (g.dtype == kF32) {
-    const bool vec = tma_rows(g.b.p, g.b.ld, 4) && g.n % 4 == 0;
-    return 6.0 + passes * values * (vec ? 0.9 : 1.6) < 30.0 + values * 4.0;
-  }
-  if (tma_rows(g.b.p, g.b.ld, 2)) return g.m <= 4 && g.n % 8 == 0;
-  return 6.0 + passes * values * 1.45 < 20.0 + values * 2.45;
+  if (!plain_product(g) || !g.a.k_inner || g.b.k_inner || g.ldc != g.n || g.m * g.n / 32 >= INT32_MAX) return false;
+  if (g.dtype == kF32) return g.m <= 48;
+  return tma_rows(g.b.p, g.b.ld, 2) ? g.m <= 8 && g.n % 8 == 0 : g.m <= 32;
 }
+// Whether dw is, by the estimated times (us) of the two paths.
 // dw: f32 2 x 4096 x 16384 46 and 75, 12 x 2008 x 32552 79 and 77, 32 x 4096 x 16384 136 and 76, 12 x 2007 x 32552 84 and 171,
 // 16 x 2007 x 32552 96 and 170, 30 x 300 x 5000 12 and 19; bf16 5 x 2071 x 48416 82 and 103, 12 x 2007 x 32552 76 and 67,
 // 30 x 300 x 5000 11 and 18.
@@ -603,28 +615,35 @@ bool few_outer(const Product& g) {
   return !tma && here < 10.0 + values * 0.9;
 }
 constexpr int kAcrossRows = 8;
-// Chunks of w's rows: four blocks an SM, of 64 rows at least.
+bool across_vec(const Product& g) { return g.dtype != kF32 && tma_rows(g.b.p, g.b.ld, 2) && g.n % 8 == 0; }
+int64_t across_tiles(const Product& g) {
+  const int64_t wide = kAcrossThreads * (across_vec(g) ? 8 : 4);
+  return (g.n + wide - 1) / wide * ((g.m + kAcrossRows - 1) / kAcrossRows);
+}
+// Chunks of w's rows, of 64 at least: as many blocks as the SMs hold at once (12 x 2007 x 32552 f32, 4, 6 and 12 blocks an
+// SM: 108, 76 and 79 us; 2 x 4096 x 16384 bf16, whose threads hold eight columns: 36, 42 and 38).
 int64_t across_chunks(const Product& g) {
-  const int vec = g.dtype == kF32 ? 4 : 8;
-  const int64_t tiles = (g.n + kAcrossThreads * vec - 1) / (kAcrossThreads * vec) * ((g.m + kAcrossRows - 1) / kAcrossRows);
-  int64_t chunks = 4 * ops_sm_count() / tiles;
+  int64_t chunks = (across_vec(g) ? 4 : 6) * ops_sm_count() / across_tiles(g);
   const int64_t most = (g.k + kAcrossDeep - 1) / kAcrossDeep;
   chunks = chunks > most ? most : chunks;
   return chunks < 1 ? 1 : chunks;
 }
 template <typename T>
 cudaError_t launch_across(const Product& g, Scratch& sc, cudaStream_t st) {
-  constexpr int kVec = 16 / sizeof(T);
   const int64_t chunks = across_chunks(g);
   float* part = sc.take<float>(chunks * g.m * g.n);
   const int64_t chunk = (g.k + chunks - 1) / chunks;
-  const bool vec = g.n % kVec == 0 && g.b.ld % kVec == 0 && reinterpret_cast<uintptr_t>(g.b.p) % 16 == 0;
-  const int64_t wide = kAcrossThreads * (vec ? kVec : 1);
-  const dim3 grid(static_cast<unsigned>((g.n + wide - 1) / wide), static_cast<unsigned>((g.k + chunk - 1) / chunk),
-                  static_cast<unsigned>((g.m + kAcrossRows - 1) / kAcrossRows));
-  const cudaError_t e =
-      vec ? launch_after(few_rows_across_kernel<T, kVec, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k, chunk, part)
-          : launch_after(few_rows_across_kernel<T, 1, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k, chunk, part);
+  if (across_tiles(g) > INT32_MAX) return cudaErrorNotSupported;
+  const dim3 grid(static_cast<unsigned>(across_tiles(g)), static_cast<unsigned>((g.k + chunk - 1) / chunk));
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2) {
+    e = across_vec(g) ? launch_after(few_rows_across_kernel<T, 8, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k,
+                                     chunk, part)
+                      : launch_after(few_rows_across_kernel<T, 1, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k,
+                                     chunk, part);
+  } else {
+    e = launch_after(few_rows_across_kernel<T, 1, kAcrossRows>, grid, kAcrossThreads, 0, st, g.a, g.b, g.m, g.n, g.k, chunk, part);
+  }
   if (e != cudaSuccess) return e;
   return launch_after(sum_parts_kernel<T>, static_cast<unsigned>((g.m * g.n + 31) / 32), kSumThreads, 0, st,
                       static_cast<const float*>(part), int64_t(grid.y), g.m * g.n, static_cast<T*>(g.c));
