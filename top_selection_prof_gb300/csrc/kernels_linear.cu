@@ -144,10 +144,11 @@ cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStrea
 // ---------------------------------------------------------------------------
 constexpr int kFewCols = 4, kFewWarps = 8;
 // Threads an SM holds at once, which bounds the registers of each.  Blocks of four warps where a thread has many: 8 rows of
-// f32 take 75 us at 4096 -> 16384 with 12 warps an SM, 91 with 8; 1 row 43 with 32 and 55 with 24.  (Two rows have no variant
-// of their own: 36 us at 4096 -> 16384 bf16, 29 as four.)
+// f32 take 75 us at 4096 -> 16384 with 12 warps an SM, 91 with 8; 1 row 43 with 32 and 55 with 24.  Two rows
+// have no variant of their own (36 us at 4096 -> 16384 bf16, 29 as four), nor two to four off 16-byte boundaries (4097 ->
+// 16384 f32: 86 us, 69 as eight); one such row keeps eight steps of w on their way (bf16: 38 us, 98 with four).
 constexpr int few_resident(int vec, int rows) {
-  return rows == 1 ? 1024 : vec == 1 ? (rows == 4 ? 768 : 512) : (rows == 4 ? 512 : 384);
+  return vec == 1 ? 512 : rows == 1 ? 1024 : rows == 4 ? 512 : 384;
 }
 
 template <typename T>
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(few_resident(VEC, R)) few_rows_kernel(const Fe
   for (int r = 0; r < R; ++r) xp[r] = p.x + min(r0 + r, p.rows - 1) * p.ldx;
   const int64_t k1 = min(p.k, (part + 1) * p.k_run);
   if constexpr (VEC == 1) {
-#pragma unroll 4
+#pragma unroll (R == 1 ? 8 : 4)
     for (int64_t k = part * p.k_run + lane; k < k1; k += 32) {
       float wv[kFewCols];
 #pragma unroll
@@ -275,7 +276,9 @@ cudaError_t launch_few_r(const FewParams<T>& p, int ks, cudaStream_t st) {
 template <typename T, int VEC>
 cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
   if (p.rows <= 1) return launch_few_r<T, VEC, 1>(p, ks, st);
-  if (p.rows <= 4) return launch_few_r<T, VEC, 4>(p, ks, st);
+  if constexpr (VEC > 1) {
+    if (p.rows <= 4) return launch_few_r<T, VEC, 4>(p, ks, st);
+  }
   return launch_few_r<T, VEC, 8>(p, ks, st);
 }
 
@@ -291,7 +294,7 @@ bool few_rows(const Product& g) {
   if (g.m <= 4 || g.dtype == kF32) return true;
   const double passes = static_cast<double>((g.m + 7) / 8), values = static_cast<double>(g.n) * g.k;
   const double v = values * 1e-6;
-  if (!tma_rows(g.b.p, g.b.ld, 2)) return 6.0 + passes * v * 0.85 < 16.0 + v * 2.35;
+  if (!tma_rows(g.b.p, g.b.ld, 2)) return 6.0 + passes * v * 0.82 < 16.0 + v * 2.35;
   const double depth = static_cast<double>((g.k + 63) / 64), waves = static_cast<double>((g.n + 256 * 76 - 1) / (256 * 76));
   const double products = waves * depth * 0.17, bytes = values * 2 / 5e6;
   return 2.0 + passes * values * 2 / 2.1e6 < 6.0 + (products > bytes ? products : bytes);
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kAcrossThreads) few_rows_across_kernel(const O
 
 // dw[i, j] = sum over few r of dz[r, i] x[r, j]: a thread makes 8 x 4 results,
 // its four columns 64 apart, so that a warp writes 32 neighbours whatever the
-// rows' alignment.  Bound by the stores of dw with up to some 8 rows (5.8 TB/s
+// rows' alignment.  Bound by the stores of dw with up to some 8 rows (5.9 TB/s
 // at 2 x 4096 x 16384 f32), by the products above.
 constexpr int kOuterRows = 32, kOuterCols = 256, kOuterThreads = 256, kOuterMost = 32;
 template <typename T>
@@ -564,21 +567,27 @@ __global__ void __launch_bounds__(kOuterThreads) few_outer_kernel(const Operand 
     as[r][i] = i0 + i < m ? to_f32(ap[r * a.ld + i0 + i]) : 0.0f;
   }
   __syncthreads();
-  float acc[8][4] = {};
+  Pair acc[4][4];  // two rows in each
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = Pair::of(0.0f, 0.0f);
 #pragma unroll 4
   for (int r = 0; r < k; ++r) {
-    float x[4], z[8];
+    float x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t j = j0 + e * 64 + tx;
       x[e] = j < n ? to_f32(__ldg(bp + r * b.ld + j)) : 0.0f;
     }
+    const float4 z0 = *reinterpret_cast<const float4*>(&as[r][ty * 8]), z1 = *reinterpret_cast<const float4*>(&as[r][ty * 8 + 4]);
+    const Pair z[4] = {Pair::of(z0.x, z0.y), Pair::of(z0.z, z0.w), Pair::of(z1.x, z1.y), Pair::of(z1.z, z1.w)};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = as[r][ty * 8 + i];
+    for (int e = 0; e < 4; ++e) {
+      const Pair xx = Pair::of(x[e], x[e]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(z[i], x[e], acc[i][e]);
+      for (int i = 0; i < 4; ++i) acc[i][e].fma(z[i], xx);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -587,7 +596,9 @@ __global__ void __launch_bounds__(kOuterThreads) few_outer_kernel(const Operand 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t j = j0 + e * 64 + tx;
-      if (j < n) c[row * ldc + j] = from_f32<T>(acc[i][e]);
+      float lo, hi;
+      acc[i / 2][e].get(&lo, &hi);
+      if (j < n) c[row * ldc + j] = from_f32<T>(i % 2 ? hi : lo);
     }
   }
 }
@@ -603,16 +614,17 @@ bool few_across(const Product& g) {
   if (g.dtype == kF32) return g.m <= 48;
   return tma_rows(g.b.p, g.b.ld, 2) ? g.m <= 8 && g.n % 8 == 0 : g.m <= 32;
 }
-// Whether dw is, by the estimated times (us) of the two paths.
-// dw: f32 2 x 4096 x 16384 46 and 75, 12 x 2008 x 32552 79 and 77, 32 x 4096 x 16384 136 and 76, 12 x 2007 x 32552 84 and 171,
-// 16 x 2007 x 32552 96 and 170, 30 x 300 x 5000 12 and 19; bf16 5 x 2071 x 48416 82 and 103, 12 x 2007 x 32552 76 and 67,
-// 30 x 300 x 5000 11 and 18.
+// Whether dw is formed from few rows, by the estimated times (us) of the two paths.  Measured, here and on the tensor cores:
+// f32 2, 8, 16 and 32 x 4096 x 16384 46, 57, 85, 128 and 75; 12 and 32 x 2007 x 32552 80, 134 and 170; 32 x 512 x 12288 16
+// and 21; bf16 5 x 2071 x 48416 78 and 102, 12 x 2007 x 32552 72 and 67, 2 x 4096 x 16384 39 and 28, 8 and 32 x 512 x 12288
+// 11, 17 and 15, 30 x 300 x 5000 11 and 19.
 bool few_outer(const Product& g) {
   if (!plain_product(g) || g.a.k_inner || g.b.k_inner || g.k > kOuterMost) return false;
-  const double values = static_cast<double>(g.m) * g.n * 1e-6, here = 6.0 + values * (0.5 + 0.05 * static_cast<double>(g.k));
-  if (g.dtype == kF32) return here < 14.0 + values * (tma_rows(g.c, g.ldc, 4) ? 1.0 : 2.5);
+  const double values = static_cast<double>(g.m) * g.n * 1e-6, k = static_cast<double>(g.k);
+  if (g.dtype == kF32) return 5.0 + values * (0.6 + 0.04 * k) < 16.0 + values * (tma_rows(g.c, g.ldc, 4) ? 0.88 : 2.37);
+  const double here = 4.0 + values * (0.5 + 0.047 * k);
   const bool tma = tma_rows(g.a.p, g.a.ld, 2) && tma_rows(g.b.p, g.b.ld, 2) && tma_rows(g.c, g.ldc, 2);
-  return !tma && here < 10.0 + values * 0.9;
+  return here < (tma ? 14.0 + values * 0.195 : 12.5 + values * 0.83);
 }
 constexpr int kAcrossRows = 8;
 bool across_vec(const Product& g) { return g.dtype != kF32 && tma_rows(g.b.p, g.b.ld, 2) && g.n % 8 == 0; }
