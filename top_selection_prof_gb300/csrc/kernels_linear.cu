@@ -285,7 +285,7 @@ cudaError_t launch_few_v(const FewParams<T>& p, int ks, cudaStream_t st) {
 bool tma_rows(const void* p, int64_t ld, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * bytes % 16 == 0; }
 
 // Whether the rows are few enough, by the times of both (us; w beyond the caches).  Measured, here and on the tensor cores:
-// bf16 rows 1, 4, 8, 16 of 512 -> 12288: 3.5, 4.8, 7.9, 14.4 and 8.4, 8.4, 8.4, 7.1; 4096 -> 16384: 23, 29, 64, 126 and
+// bf16 rows 1, 4, 8, 16 of 512 -> 12288: 3.5, 4.8, 7.9, 14.4 and 8.4, 8.4, 8.4, 7.1; 4096 -> 16384: 23, 29, 48, 77 and
 // 41, 36, 37, 26; 16384 -> 512: 4.0, 5.4, 7.3, 13.3 and 45 to 47.  f32 rows 8, 32 and 40: 512 -> 12288 10,
 // 21, 27 and 33; 4096 -> 16384 75, 189, 227 and 245; 2007 -> 32552 108 (12), 197, 241 and 251.  bf16 rows off 16-byte
 // boundaries: 5 of 2071 -> 48416 87 and 268; 12, 24 and 32 of 2007 -> 32552 109, 158, 202 and 164; 32 of 515 -> 12288 27, 23.
