@@ -43,12 +43,21 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kStageBytesOut = 4096;   // staging of one epilogue warp: 32 rows x 128 bytes
 
-// f32: the tensor cores' sums are cut off, not rounded, so that a long sum
-// drifts (K = 4096 in one accumulator: 4.5e-6 of the result).  After kRoundDepth
-// stages of k (all six products of them) the sums go to f32 registers, which
-// are added to those before and kept in scratch: the drift stays that of
-// K = 512 (5e-7).
-constexpr int kRoundDepth = 8, kRoundStages = 6 * kRoundDepth;
+// The tensor cores' sums are cut off, not rounded, so that a long sum drifts
+// (K = 4096 in one accumulator: 4.5e-6 of the result, and in proportion to K).
+// After a round of k the sums therefore go to f32 registers, where they are
+// added to those before (rounded); the last round's accumulator takes their
+// total.  Rounds are eight stages of k (all six products of them) for f32,
+// which leaves 5e-7, and 32 for bf16, which leaves 2.3e-6 whatever K, what an
+// f32 sum of some 10^4 terms has.  Each reading of an accumulator holds the
+// products up by some 0.3 us (bf16 8192 x 8192 x 8192: one sum 588 us, rounds of
+// 32 stages 619, of 16 631, of 8 655).
+template <typename T>
+constexpr int kTerms = sizeof(T) == 4 ? 6 : 1;       // products of parts
+template <typename T>
+constexpr int kRoundDepth = sizeof(T) == 4 ? 8 : 32;  // stages of k in a round
+template <typename T>
+constexpr int kRoundStages = kTerms<T> * kRoundDepth<T>;
 constexpr int kTileN = 256;            // columns of c in a pair's tile (and of tensor memory in an accumulator)
 constexpr int kPairM = 2 * kTileM;     // its rows
 constexpr int kRowsB = kTileN / 2;     // rows of b that one CTA brings in
@@ -190,6 +199,24 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// The same of 8 columns, and back.
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const float* v) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -425,9 +452,9 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
           int k0 = kb * kDeepK, part_a = 0, part_b = 0;
           if constexpr (sizeof(T) == 4) {
             // a round's products of parts one after the other: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
-            const int round = kb / kRoundStages, in = kb - round * kRoundStages;
-            const int deep = min(kRoundDepth, p.deal.depth - round * kRoundDepth), term = in / deep;
-            k0 = (round * kRoundDepth + in - term * deep) * kDeepK;
+            const int round = kb / kRoundStages<T>, in = kb - round * kRoundStages<T>;
+            const int deep = min(kRoundDepth<T>, p.deal.depth - round * kRoundDepth<T>), term = in / deep;
+            k0 = (round * kRoundDepth<T> + in - term * deep) * kDeepK;
             part_a = 0x001102 >> (4 * term) & 3;
             part_b = 0x010120 >> (4 * term) & 3;
           }
@@ -469,7 +496,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
         uint32_t d = tmem + buf * kTileN;
         bool fresh = true;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (sizeof(T) == 4 && kb != w.kb0 && kb % kRoundStages == 0) {  // the round's sums go out, the next begins
+          if (kb != w.kb0 && kb % kRoundStages<T> == 0) {  // the round's sums go out, the next begins
             mma_commit(acc_full(buf));
             buf ^= 1;
             if (buf == 0) acc_phase ^= 1;
@@ -515,53 +542,62 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
       const bool lies = row0 < p.m && n0 + half * kHalf < p.n;  // else nothing of the warp's part lies in c
       // a warp's part of a slot: four columns of each of its 32 rows together
       const int64_t region = (int64_t(rank) * kEpiWarps + e) * (32 * kHalf) + lane * 4;
-      float* own = p.part + int64_t(w.slot >= 0 ? w.slot : 2 * p.deal.pairs + static_cast<int>(blockIdx.x / 2)) * (kPairM * kTileN) + region;
-      // this round's sums to the warp's own slot, onto those before
-      auto drain = [&](bool onto) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < kHalf; c0 += 32) {
-          float v[32];
-          tmem_load32(tmem + buf * kTileN + half * kHalf + c0 + (uint32_t(quad * 32) << 16), v);
-          float4* dst = reinterpret_cast<float4*>(own) + c0 / 4 * 32;
-          float4 t[8];
-          if (onto) {
+      const uint32_t quad_at = half * kHalf + (uint32_t(quad * 32) << 16);
+      // rounds before the last: their sums in registers (more than 8 columns on their way at a time would spill)
+      float sum[kHalf] = {};
+      bool held = false;
+      for (int kb = (w.kb0 / kRoundStages<T> + 1) * kRoundStages<T>; kb < w.kb1; kb += kRoundStages<T>) {
+        if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
+        fence_after();
+        if (lies) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = __ldcg(dst + i * 32);
-          }
-          tmem_wait_load();
+          for (int c = 0; c < kHalf; c += 8) {
+            float v[8];
+            tmem_load8(tmem + buf * kTileN + quad_at + c, v);
+            tmem_wait_load();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 z = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (onto) z = make_float4(z.x + t[i].x, z.y + t[i].y, z.z + t[i].z, z.w + t[i].w);
-            __stcg(dst + i * 32, z);
+            for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
           }
         }
-      };
-      bool held = false;  // the slot holds earlier rounds
-      if constexpr (sizeof(T) == 4) {
-        for (int kb = (w.kb0 / kRoundStages + 1) * kRoundStages; kb < w.kb1; kb += kRoundStages) {
-          if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
-          fence_after();
-          if (lies) drain(held);
-          free_accumulator(lane, acc_empty(buf));
-          buf ^= 1;
-          if (buf == 0) acc_phase ^= 1;
-          held = true;
-        }
+        free_accumulator(lane, acc_empty(buf));
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1;
+        held = true;
       }
       // (a warp that gave up goes on without waiting, so that the others' barriers are still met)
       if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
       fence_after();
-      const uint32_t acc = tmem + buf * kTileN + half * kHalf + (uint32_t(quad * 32) << 16);
+      const uint32_t acc = tmem + buf * kTileN + quad_at;
       if (!lies) {
         free_accumulator(lane, acc_empty(buf));
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1;
         continue;
       }
+      if (held) {  // the accumulator takes the total
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 8) {
+          float v[8];
+          tmem_load8(acc + c, v);
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += sum[c + i];
+          tmem_store8(acc + c, v);
+        }
+        tmem_wait_store();
+      }
       int first = 0, parts = 0;  // pairs whose runs make up a shared tile
       if (w.slot >= 0) {
-        drain(held);
+        float4* own = reinterpret_cast<float4*>(p.part + int64_t(w.slot) * (kPairM * kTileN) + region);
+#pragma unroll 1
+        for (int c0 = 0; c0 < kHalf; c0 += 32) {
+          float v[32];
+          tmem_load32(acc + c0, v);
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            __stcg(own + c0 / 4 * 32 + i * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        }
         free_accumulator(lane, acc_empty(buf));
         __threadfence();
         runs_of_tile(p.deal, w.shared, &first, &parts);
@@ -578,17 +614,6 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
         if (w.slot < 0) {
           tmem_load32(acc + c, v);
           tmem_wait_load();
-          if (held) {
-            const float4* t = reinterpret_cast<const float4*>(own) + c / 4 * 32;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 z = __ldcg(t + i * 32);
-              v[4 * i] += z.x;
-              v[4 * i + 1] += z.y;
-              v[4 * i + 2] += z.z;
-              v[4 * i + 3] += z.w;
-            }
-          }
         } else {
           const int k0 = w.shared * p.deal.k_blocks;
           auto part_of = [&](int pair) {
@@ -901,8 +926,7 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
     d.run = static_cast<int>(shared * d.k_blocks / pairs);
     d.longer = static_cast<int>(shared * d.k_blocks % pairs);
   }
-  // two slots a pair for runs, one for the rounds of f32
-  if (d.shared_tiles || (f32 && d.depth > kRoundDepth)) q->part = sc.take<float>(int64_t(3) * d.pairs * kPairM * kTileN);
+  if (d.shared_tiles) q->part = sc.take<float>(int64_t(2) * d.pairs * kPairM * kTileN);
   q->ld_a = g.a.ld;
   q->ld_b = g.b.ld;
   if (f32 || !tma_rows(g.a.p, g.a.ld, 2)) {
