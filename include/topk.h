@@ -364,8 +364,10 @@ int topk_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const vo
  * dx = dz w, dw = dz^T x, dbias = the column sums of dz (each nullable; the
  * residual's gradient is dy itself).  pre is read unless act is NONE; for RELU
  * the layer's own output serves when it had no residual (the signs agree).
- * BF16: dz is rounded to BF16 once before the two products (dbias sums it
- * unrounded).  x is needed for dw only and w for dx only.
+ * BF16 with GELU or SILU: dz enters the two products with 16 bits (of its
+ * rounding to BF16 and of what that left; BF16's own 8 where x or w holds a
+ * value that is not finite); dbias sums it in f32.  x is needed for dw only
+ * and w for dx only.
  */
 int topk_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
                          const void* pre, int64_t ldp, int dtype, int64_t rows, int64_t inner, int64_t outer, int act,

@@ -43,3 +43,55 @@ def test_long_bf16_sums_stay_f32(tk, rows, inner, outer):
     r = -s.bfloat16()
     y = tk.linear(x.cuda(), w.cuda(), residual=r.cuda())
     rounds_from(y, s + r.double(), (128 * 2.0 ** -23 + (inner / 2048 + 16) * 2.0 ** -24) * s)
+
+
+def phi(z):
+    return torch.exp(-0.5 * z * z) * 0.3989422804014327
+
+
+def slope64(z, act):
+    s = torch.sigmoid(z)
+    return torch.special.ndtr(z) + z * phi(z) if act == "gelu" else s * (1 + z * (1 - s))
+
+
+# rows, inner, outer: products on the tensor cores, by passes over few rows (dx of 5 and 24, dw of both), rows on and off
+# 16-byte boundaries
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("rows,inner,outer", [(300, 96, 104), (257, 77, 99), (5, 96, 100), (24, 77, 99), (700, 260, 333)])
+def test_smooth_bf16_gradients_keep_dz(tk, rows, inner, outer, act):
+    """dz = dy act'(pre) has no bf16 value: rounding it to one before the products would show in every sum.
+
+    dz enters with 16 bits (2^-17 of it) and its own f32 error (16 units of 2^-23 of |dy| (|slope| + 0.25)); a sum of n
+    products in f32 is within n + 4 units of 2^-23 of the magnitudes.
+    """
+    g = gen(rows + outer)
+    bf = torch.bfloat16
+    x, w, dy = normals((rows, inner), bf, g), normals((outer, inner), bf, g), normals((rows, outer), bf, g)
+    pre = normals((rows, outer), bf, g, 2.0)
+    dx, dw, _ = tk.linear_backward(dy.cuda(), x.cuda(), w.cuda(), pre=pre.cuda(), act=act)
+    slope = slope64(pre.double(), act)
+    dz, mag = dy.double() * slope, dy.double().abs() * (slope.abs() + 0.25)
+    for got, want, m, n in ((dx, dz @ w.double(), mag @ w.double().abs(), outer),
+                            (dw, dz.T @ x.double(), mag.T @ x.double().abs(), rows)):
+        rounds_from(got, want, ((n + 4 + 16) * 2.0 ** -23 + 2.0 ** -17) * m)
+
+
+@pytest.mark.parametrize("rows", [5, 30, 300])
+def test_smooth_bf16_gradients_keep_infinities(tk, rows):
+    """An infinity in w or x meets one sign of each dz, whatever parts dz enters in; dz of infinity and NaN likewise."""
+    g = gen(rows)
+    bf, inner, outer = torch.bfloat16, 96, 200
+    x, w = normals((rows, inner), bf, g).abs() + 0.1, normals((outer, inner), bf, g).abs() + 0.1
+    dy, pre = normals((rows, outer), bf, g).abs() + 0.1, normals((rows, outer), bf, g).abs() + 0.1
+    x[2, 6], w[140, 95], w[3, 0] = torch.inf, -torch.inf, torch.inf
+    for bad in (False, True):
+        if bad:
+            dy[1, 5], dy[4, 9] = torch.inf, torch.nan
+        dz = dy.double() * slope64(pre.double(), "silu")
+        dx, dw, _ = tk.linear_backward(dy.cuda(), x.cuda(), w.cuda(), pre=pre.cuda(), act="silu")
+        for got, want, n in ((dx, dz @ w.double(), outer), (dw, dz.T @ x.double(), rows)):
+            same = want.isnan() | want.isinf()
+            assert torch.equal(got.cpu().double()[same].nan_to_num(7.0), want[same].nan_to_num(7.0))
+            # all terms positive; dz has bf16's own bits at least (2^-8 of it)
+            want = torch.where(same, torch.zeros_like(want), want)
+            rounds_from(torch.where(same, 0, got.cpu()), want, (2.0 ** -8 + (n + 20) * 2.0 ** -23) * want)

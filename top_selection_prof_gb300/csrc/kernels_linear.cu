@@ -360,7 +360,20 @@ __global__ void __launch_bounds__(kSumThreads) slope_sums_kernel(const SlopeSums
           u.set_raw(z[a]);
 #pragma unroll
           for (int c = 0; c < VEC; ++c) t.v[c] *= act_slope<T>(u.v[c], ACT);
-          if (dz) t.store(dz + i * s.n + j);
+          if (dz) {
+            t.store(dz + i * s.lddz + j);
+            if constexpr (sizeof(T) == 2 && ACT != kActRelu) {  // (relu's dz is dy or 0)
+              if (s.rest) {
+                Vec<T, VEC> left;
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                  const float lead = to_f32(from_f32<T>(t.v[c]));
+                  left.v[c] = fabsf(lead) < INFINITY ? t.v[c] - lead : 0.0f;
+                }
+                left.store(dz + s.rest + i * s.lddz + j);
+              }
+            }
+          }
         }
 #pragma unroll
         for (int c = 0; c < VEC; ++c) acc[c] += t.v[c];
@@ -506,7 +519,12 @@ __global__ void __launch_bounds__(kAcrossThreads) few_rows_across_kernel(const O
     __syncthreads();
     for (int e = threadIdx.x; e < kAcrossDeep * R; e += kAcrossThreads) {
       const int i = e % kAcrossDeep, r = e / kAcrossDeep;
-      as[i][r] = i0 + i < k1 && r0 + r < m ? to_f32(ap[r * a.ld + i0 + i]) : 0.0f;
+      float v = 0.0f;
+      if (i0 + i < k1 && r0 + r < m) {
+        v = to_f32(ap[r * a.ld + i0 + i]);
+        if (a.rest) v += to_f32(ap[a.rest + r * a.ld + i0 + i]);
+      }
+      as[i][r] = v;
     }
     __syncthreads();
     const int deep = static_cast<int>(min(int64_t(kAcrossDeep), k1 - i0));
@@ -564,7 +582,12 @@ __global__ void __launch_bounds__(kOuterThreads) few_outer_kernel(const Operand 
   const T* bp = static_cast<const T*>(b.p);
   for (int e = threadIdx.x; e < k * kOuterRows; e += kOuterThreads) {
     const int i = e % kOuterRows, r = e / kOuterRows;
-    as[r][i] = i0 + i < m ? to_f32(ap[r * a.ld + i0 + i]) : 0.0f;
+    float v = 0.0f;
+    if (i0 + i < m) {
+      v = to_f32(ap[r * a.ld + i0 + i]);
+      if (a.rest) v += to_f32(ap[a.rest + r * a.ld + i0 + i]);
+    }
+    as[r][i] = v;
   }
   __syncthreads();
   Pair acc[4][4];  // two rows in each
@@ -695,7 +718,7 @@ cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream
   if (few_outer(g)) return f32 ? launch_outer<float>(g, st) : launch_outer<__nv_bfloat16>(g, st);
   if (few_across(g)) return f32 ? launch_across<float>(g, sc, st) : launch_across<__nv_bfloat16>(g, sc, st);
   static std::atomic<int> calls{0};
-  const int call = f32 ? 1 + (calls.fetch_add(1) & 0x3fffffff) : 0;
+  const int call = f32 || g.a.rest ? 1 + (calls.fetch_add(1) & 0x3fffffff) : 0;
   return launch_mma(g, sc, words, call, st);
 }
 

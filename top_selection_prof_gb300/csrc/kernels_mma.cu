@@ -25,6 +25,12 @@
 // infinity would meet a zero part (NaN): where the split finds one, the
 // product is made on the CUDA cores and this kernel does nothing.
 //
+// A bf16 operand a whose values have a rest (the gradient of a smooth
+// activation) is multiplied as two parts, the rest first: a stage is one of
+// twice as many.  The rest's sign is its own, so an infinity in b would meet
+// both signs, or a zero (NaN): where one is found, the leading part takes the
+// rest's place too and the sums are halved.
+//
 // Every wait has a limit, after which the status word is set and the kernel
 // winds up.
 #include <cstdint>
@@ -52,12 +58,10 @@ constexpr int kStageBytesOut = 4096;   // staging of one epilogue warp: 32 rows 
 // f32 sum of some 10^4 terms has.  Each reading of an accumulator holds the
 // products up by some 0.3 us (bf16 8192 x 8192 x 8192: one sum 588 us, rounds of
 // 32 stages 619, of 16 631, of 8 655).
-template <typename T>
-constexpr int kTerms = sizeof(T) == 4 ? 6 : 1;       // products of parts
-template <typename T>
-constexpr int kRoundDepth = sizeof(T) == 4 ? 8 : 32;  // stages of k in a round
-template <typename T>
-constexpr int kRoundStages = kTerms<T> * kRoundDepth<T>;
+// (TERMS: the products of parts that make one of values.)
+constexpr int kTermsF32 = 6, kTermsRest = 2;
+template <int TERMS>
+constexpr int kRoundDepthOf = TERMS == kTermsF32 ? 8 : 32;  // stages of k in a round
 constexpr int kTileN = 256;            // columns of c in a pair's tile (and of tensor memory in an accumulator)
 constexpr int kPairM = 2 * kTileM;     // its rows
 constexpr int kRowsB = kTileN / 2;     // rows of b that one CTA brings in
@@ -75,7 +79,7 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 struct Deal {
   int tiles_m, tiles_n;
   int k_blocks;       // stages of a tile
-  int depth;          // those of one product of parts (k_blocks for bf16)
+  int depth;          // those of one product of parts (k_blocks where values have one part)
   int pairs;
   int waves;
   int shared_tiles;   // 0: every pair's tiles are whole (the last wave may be short)
@@ -105,7 +109,7 @@ struct MmaParams {
   int64_t ldp;
   float* part;             // sums of parts of k: 2 slots a pair, each kPairM x kTileN
   unsigned* ticket;        // 2 kEpiWarps a shared tile, zero between launches
-  const int* mark;         // f32: the kernel does nothing where *mark == call
+  const int* mark;         // *mark == call: an operand of parts holds a value that is not finite
   int call;
   int* status;
 };
@@ -383,6 +387,11 @@ __device__ __forceinline__ void add_bias32(float* v, const float* bias) {
   }
 }
 
+__device__ __forceinline__ void halve32(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= 0.5f;
+}
+
 // The pairs whose runs meet shared tile t, [first, first + parts).
 __device__ __forceinline__ void runs_of_tile(const Deal& d, int t, int* first, int* parts) {
   *first = d.run_of(t * d.k_blocks);
@@ -395,8 +404,9 @@ __device__ __forceinline__ void free_accumulator(int lane, uint32_t bar) {
   if (lane == 0) bar_arrive(map_to_rank(bar, 0));
 }
 
-template <typename T>
+template <typename T, int TERMS>
 __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant__ MmaParams p) {
+  constexpr int kRoundDepth = kRoundDepthOf<TERMS>, kRoundStages = TERMS * kRoundDepth;
   const T* bias = static_cast<const T*>(p.bias);
   const T* residual = static_cast<const T*>(p.residual);
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -433,7 +443,9 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
   grid_launch_dependents();
 
   Worker worker(p.deal, blockIdx.x / 2);
-  if (sizeof(T) == 4 && *p.mark == p.call) worker.leave();
+  const bool marked = TERMS > 1 && *p.mark == p.call;
+  if (TERMS == kTermsF32 && marked) worker.leave();  // (made on the CUDA cores)
+  const bool twice = TERMS == kTermsRest && marked;
   Work w;
   bool ok = true;
 
@@ -450,13 +462,14 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
           const uint32_t bar = map_to_rank(full(stage), 0);
           bar_expect(bar, kStage);
           int k0 = kb * kDeepK, part_a = 0, part_b = 0;
-          if constexpr (sizeof(T) == 4) {
-            // a round's products of parts one after the other: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
-            const int round = kb / kRoundStages<T>, in = kb - round * kRoundStages<T>;
-            const int deep = min(kRoundDepth<T>, p.deal.depth - round * kRoundDepth<T>), term = in / deep;
-            k0 = (round * kRoundDepth<T> + in - term * deep) * kDeepK;
-            part_a = 0x001102 >> (4 * term) & 3;
-            part_b = 0x010120 >> (4 * term) & 3;
+          if constexpr (TERMS > 1) {
+            // a round's products of parts one after the other: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), or (1,0) (0,0)
+            const int round = kb / kRoundStages, in = kb - round * kRoundStages;
+            const int deep = min(kRoundDepth, p.deal.depth - round * kRoundDepth), term = in / deep;
+            k0 = (round * kRoundDepth + in - term * deep) * kDeepK;
+            part_a = (TERMS == kTermsF32 ? 0x001102 : 0x01) >> (4 * term) & 3;
+            part_b = (TERMS == kTermsF32 ? 0x010120 : 0x00) >> (4 * term) & 3;
+            if (twice) part_a = 0;
           }
           if (p.a_k) {
             tma_load(sa, &p.a, k0, m0, part_a, bar);
@@ -496,7 +509,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
         uint32_t d = tmem + buf * kTileN;
         bool fresh = true;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (kb != w.kb0 && kb % kRoundStages<T> == 0) {  // the round's sums go out, the next begins
+          if (kb != w.kb0 && kb % kRoundStages == 0) {  // the round's sums go out, the next begins
             mma_commit(acc_full(buf));
             buf ^= 1;
             if (buf == 0) acc_phase ^= 1;
@@ -546,7 +559,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
       // rounds before the last: their sums in registers (more than 8 columns on their way at a time would spill)
       float sum[kHalf] = {};
       bool held = false;
-      for (int kb = (w.kb0 / kRoundStages<T> + 1) * kRoundStages<T>; kb < w.kb1; kb += kRoundStages<T>) {
+      for (int kb = (w.kb0 / kRoundStages + 1) * kRoundStages; kb < w.kb1; kb += kRoundStages) {
         if (ok) ok = __all_sync(~0u, bar_wait(acc_full(buf), acc_phase));
         fence_after();
         if (lies) {
@@ -641,6 +654,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             }
           }
         }
+        if (twice) halve32(v);
         if (bias) add_bias32(v, bias_own + c);
       };
       if (sizeof(T) == 2 && w.slot < 0 && !p.pre_ptr && !residual) {
@@ -677,6 +691,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             if (s + 1 < kHalf / 32) tmem_load32(acc + 32 * (s + 1), v[(s + 1) & 1]);
             else free_accumulator(lane, acc_empty(buf));
             float* z = v[s & 1];
+            if (twice) halve32(z);
             if (bias) add_bias32(z, bias_own + 32 * s);
             if (p.act == kActRelu) apply_act<T, 32>(z, kActRelu);
             else if (p.act == kActSilu) apply_act<T, 32>(z, kActSilu);
@@ -691,6 +706,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             tmem_load32(acc + 32 * s, z);
             tmem_wait_load();
             if (s + 1 == kHalf / 32) free_accumulator(lane, acc_empty(buf));
+            if (twice) halve32(z);
             if (bias) add_bias32(z, bias_own + 32 * s);
             apply_act<T, 32>(z, kActGelu);
             finish(s, z);
@@ -826,6 +842,28 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const Split a, const Sp
   if (!finite) *other = call;
 }
 
+// *other becomes `call` when a value of a bf16 matrix is not finite; a thread looks at eight values of a row.
+__global__ void __launch_bounds__(256) mark_other_kernel(const __nv_bfloat16* p, int64_t ld, int64_t rows, int64_t cols, int* other,
+                                                         int call) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t per = (cols + 7) / 8, at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= rows * per) return;
+  const int64_t r = at / per, c = (at - r * per) * 8;
+  const __nv_bfloat16* q = p + r * ld + c;
+  bool finite = true;
+  if (c + 8 <= cols && reinterpret_cast<uintptr_t>(q) % 16 == 0) {
+    Raw<__nv_bfloat16, 8> v;
+    v.load_nc(q);
+    const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) finite = finite && !__vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u);
+  } else {
+    for (int i = 0; i < 8 && c + i < cols; ++i) finite = finite && fabsf(to_f32(q[i])) < INFINITY;
+  }
+  if (!finite) *other = call;
+}
+
 // ---- host ------------------------------------------------------------------------------
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -884,8 +922,8 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
   d.tiles_n = static_cast<int>(tn);
   const bool f32 = g.dtype == kF32;
   d.depth = static_cast<int>((g.k + kDeepK - 1) / kDeepK);
-  if (f32 && d.depth > INT32_MAX / 6) return false;
-  d.k_blocks = f32 ? 6 * d.depth : d.depth;
+  if ((f32 || g.a.rest) && d.depth > INT32_MAX / kTermsF32) return false;
+  d.k_blocks = (f32 ? kTermsF32 : g.a.rest ? kTermsRest : 1) * d.depth;
   const int slots = ops_sm_count() / 2 > 0 ? ops_sm_count() / 2 : 1;
   d.pairs = static_cast<int>(tiles < slots ? tiles : slots);
   d.waves = static_cast<int>((tiles + d.pairs - 1) / d.pairs);
@@ -955,11 +993,19 @@ bool split_of(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_
   return true;
 }
 
-template <typename T>
+cudaError_t mark_other(const Operand& o, int64_t i, int64_t k, int* other, int call, cudaStream_t st) {
+  const int64_t rows = operand_rows(o, i, k), cols = operand_cols(o, i, k);
+  const int64_t blocks = (rows * ((cols + 7) / 8) + 255) / 256;
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
+  return launch_after(mark_other_kernel, static_cast<unsigned>(blocks), 256, 0, st, static_cast<const __nv_bfloat16*>(o.p), o.ld,
+                      rows, cols, other, call);
+}
+
+template <typename T, int TERMS>
 cudaError_t launch_mma_t(const MmaParams& p, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(mma_kernel<T, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_after(mma_kernel<T>, static_cast<unsigned>(2 * p.deal.pairs), kThreads, kSmem, st, p);
+  return launch_after(mma_kernel<T, TERMS>, static_cast<unsigned>(2 * p.deal.pairs), kThreads, kSmem, st, p);
 }
 
 }  // namespace
@@ -984,6 +1030,7 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   } else {
     if (q.copy_a) e = align_rows(g.a, g.m, g.k, q.copy_a, q.ld_a, st);
     if (e == cudaSuccess && q.copy_b) e = align_rows(g.b, g.n, g.k, q.copy_b, q.ld_b, st);
+    if (e == cudaSuccess && g.a.rest) e = mark_other(g.b, g.n, g.k, other, call, st);
   }
   if (e == cudaSuccess && f32) e = launch_simt(g, other, call, st);
   if (e != cudaSuccess) return e;
@@ -999,9 +1046,10 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   const void* a = q.copy_a ? q.copy_a : g.a.p;
   const void* b = q.copy_b ? q.copy_b : g.b.p;
   const int64_t ra = operand_rows(g.a, g.m, g.k), rb = operand_rows(g.b, g.n, g.k);
-  const int parts = f32 ? 3 : 1;
-  bool ok = encode(&p.a, false, a, operand_cols(g.a, g.m, g.k), ra, q.ld_a, parts, ra, 64, p.a_k ? kTileM : kDeepK);
-  ok = ok && encode(&p.b, false, b, operand_cols(g.b, g.n, g.k), rb, q.ld_b, parts, rb, 64, p.b_k ? kRowsB : kDeepK);
+  // (the parts of a lie ra rows apart, the rest of bf16 values too)
+  if (g.a.rest && (q.copy_a || g.a.rest != ra * g.a.ld)) return cudaErrorInvalidValue;
+  bool ok = encode(&p.a, false, a, operand_cols(g.a, g.m, g.k), ra, q.ld_a, f32 ? 3 : g.a.rest ? 2 : 1, ra, 64, p.a_k ? kTileM : kDeepK);
+  ok = ok && encode(&p.b, false, b, operand_cols(g.b, g.n, g.k), rb, q.ld_b, f32 ? 3 : 1, rb, 64, p.b_k ? kRowsB : kDeepK);
   p.bias = g.bias;
   p.residual = g.residual;
   p.ldr = g.ldr;
@@ -1021,7 +1069,8 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   if (p.tma_c) ok = ok && encode(&p.c, f32, g.c, g.n, g.m, g.ldc, 1, g.m, 128 / size, 32);
   if (p.tma_pre) ok = ok && encode(&p.pre, f32, g.pre, g.n, g.m, g.ldp, 1, g.m, 128 / size, 32);
   if (!ok) return cudaErrorInvalidValue;
-  return f32 ? launch_mma_t<float>(p, st) : launch_mma_t<__nv_bfloat16>(p, st);
+  if (f32) return launch_mma_t<float, kTermsF32>(p, st);
+  return g.a.rest ? launch_mma_t<__nv_bfloat16, kTermsRest>(p, st) : launch_mma_t<__nv_bfloat16, 1>(p, st);
 }
 
 }  // namespace tk

@@ -44,11 +44,14 @@ int ops_sm_count();
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 
 // A matrix operand of a product over a shared index k: element (i, k) at
-// p[i * ld + k] when k_inner, else at p[k * ld + i].
+// p[i * ld + k] when k_inner, else at p[k * ld + i].  An operand a of bf16
+// values may hold more bits than they have: what their rounding left, rounded
+// in its turn, then lies `rest` values further on (rows on 16-byte boundaries).
 struct Operand {
   const void* p;
   int64_t ld;
   bool k_inner;
+  int64_t rest = 0;  // 0: none
 };
 // c[i, j] = act(sum_k a(i, k) b(j, k) + bias[j]) + residual[i, j]; the value
 // before act is written to pre when that is not null.  All of one dtype.
@@ -74,8 +77,9 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
 cudaError_t launch_simt(const Product& g, const int* mark, int call, cudaStream_t st);
 size_t mma_scratch_bytes(const Product& g);
 
-// dz = dy * act'(pre) (act != none; dz contiguous) and the column sums of dz
-// into dbias (nullable).  With act == none only the sums are formed, from dy.
+// dz = dy * act'(pre) (act != none) and the column sums of dz into dbias
+// (nullable).  With act == none only the sums are formed, from dy.  bf16: what
+// dz's rounding left goes, rounded, to dz + rest (0: not wanted).
 struct SlopeSums {
   const void* dy;
   int64_t lddy;
@@ -85,6 +89,7 @@ struct SlopeSums {
   int64_t rows, n;
   int act;
   void* dz;     // nullable with act == none
+  int64_t lddz, rest;
   void* dbias;  // nullable
   float* part;  // slope_sums_parts(rows, n) * n values, when dbias is wanted
 };
