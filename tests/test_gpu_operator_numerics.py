@@ -95,3 +95,30 @@ def test_smooth_bf16_gradients_keep_infinities(tk, rows):
             # all terms positive; dz has bf16's own bits at least (2^-8 of it)
             want = torch.where(same, torch.zeros_like(want), want)
             rounds_from(torch.where(same, 0, got.cpu()), want, (2.0 ** -8 + (n + 20) * 2.0 ** -23) * want)
+
+
+@pytest.mark.parametrize("inner", [1, 2])
+def test_f32_products_of_parts_keep_all_bits(tk, inner):
+    """Operands whose low bits are all ones, in sums so short that nothing else hides what a product of parts drops.
+
+    Each of the inner products, and the sum, is cut off by at most 2^-23 of the result; the dropped products of parts are at
+    most 2^-24 of a product, and the cuts of the smaller ones 6 x 2^-30.
+    """
+    g = gen(inner)
+    top = torch.randint(0, 128, (200, 2), generator=g, dtype=torch.int32)
+    sign = torch.randint(0, 2, (200, 1), generator=g, dtype=torch.int32)
+    bits = (0x3F80FFFF + (top << 16)) | (sign << 31)
+    x, w = bits[:100, :inner].contiguous().view(torch.float32), bits[100:, :inner].contiguous().view(torch.float32)
+    x[0], w[0] = 1 + 2.0 ** -7 - 2.0 ** -23, 1 + 2.0 ** -7 - 2.0 ** -23
+    want = x.double() @ w.double().T
+    got = tk.linear(x.cuda(), w.cuda()).double().cpu()
+    assert float(((got - want) / want).abs().max()) <= (inner + 1 + 0.5 + 6 / 128) * 2.0 ** -23
+
+
+def test_f32_products_at_the_end_of_the_range(tk):
+    """Values whose leading bf16 part would be infinite; a product with them is finite all the same."""
+    big = torch.tensor([[3.4028234e38], [3.3953139e38], [-3.4e38], [3.38e38]]).repeat(20, 1)
+    w = torch.tensor([[0.5], [1.0], [2.0 ** -100], [0.0]]).repeat(20, 1)
+    got = tk.linear(big.cuda(), w.cuda()).double().cpu()
+    want = big.double() @ w.double().T
+    assert float(((got - want).abs() / want.abs().clamp(min=1e-300)).max()) <= 2.0 ** -22

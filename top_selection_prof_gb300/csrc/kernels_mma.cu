@@ -18,12 +18,15 @@
 // that do so for the same rows and columns the last one (by a ticket) adds the
 // parts in order of k and writes the result.  Nothing waits for another run.
 //
-// F32 operands are taken apart into three bf16 parts each (8 + 8 + 8 bits, no
-// remainder), and the six products of parts whose orders add up to at most two
-// are summed, the smallest first: the dropped ones are below 2^-23 of a
-// product.  So a stage is one of six times as many; results are f32.  An
-// infinity would meet a zero part (NaN): where the split finds one, the
-// product is made on the CUDA cores and this kernel does nothing.
+// F32 operands are taken apart into three bf16 parts each, every part what the
+// ones before it left, rounded to nearest (8 + 8 + 8 bits and two signs: nothing
+// is left), and the six products of parts whose orders add up to at most two
+// are summed, the smallest first.  The dropped ones are at most 2^-24 of a
+// product (parts of orders one and two are within 2^-8 and 2^-17 of a value's
+// exponent) and of either sign; with parts that were cut off they had the
+// product's sign and reached 2^-21.  So a stage is one of six times as many;
+// results are f32.  An infinity would meet a zero part (NaN): where the split
+// finds one, the product is made on the CUDA cores and this kernel does nothing.
 //
 // A bf16 operand a whose values have a rest (the gradient of a smooth
 // activation) is multiplied as two parts, the rest first: a stage is one of
@@ -802,8 +805,9 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* sr
 }
 
 // The three bf16 parts of both f32 operands, `plane` values apart, rows of `ld`
-// values.  A part is the leading 8 bits of what the parts before it left, so
-// the three hold all 24.  *other becomes `call` when a value is not finite.
+// values.  A part is what the parts before it left, rounded to bf16, and the
+// three hold all 24 bits.  *other becomes `call` when a value is not finite, or
+// its leading part would not be.
 struct Split {
   const float* src;
   int64_t lds, rows, cols;
@@ -827,17 +831,19 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const Split a, const Sp
 #pragma unroll
   for (int e = 0; e < kSplitEach; ++e) v[e] = c + e < s.cols ? src[e] : 0.0f;
 #pragma unroll
-  for (int e = 0; e < kSplitEach; ++e) finite = finite && fabsf(v[e]) < INFINITY;
+  for (int e = 0; e < kSplitEach; ++e) finite = finite && fabsf(v[e]) < 0x1.ffp127f;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    uint32_t top[kSplitEach];
+    uint32_t two[kSplitEach / 2];
 #pragma unroll
-    for (int e = 0; e < kSplitEach; ++e) {
-      top[e] = __float_as_uint(v[e]) & 0xffff0000u;
-      v[e] -= __uint_as_float(top[e]);
+    for (int e = 0; e < kSplitEach; e += 2) {
+      const __nv_bfloat162 top = __floats2bfloat162_rn(v[e], v[e + 1]);
+      two[e / 2] = *reinterpret_cast<const uint32_t*>(&top);
+      v[e] -= __uint_as_float(two[e / 2] << 16);
+      v[e + 1] -= __uint_as_float(two[e / 2] & 0xffff0000u);
     }
     // (rows of the parts hold a multiple of 8 values: the last store may go past cols, not past the row)
-    *reinterpret_cast<uint2*>(s.dst + q * s.plane + r * s.ld + c) = make_uint2((top[0] >> 16) | top[1], (top[2] >> 16) | top[3]);
+    *reinterpret_cast<uint2*>(s.dst + q * s.plane + r * s.ld + c) = make_uint2(two[0], two[1]);
   }
   if (!finite) *other = call;
 }
