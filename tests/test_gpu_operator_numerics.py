@@ -122,3 +122,48 @@ def test_f32_products_at_the_end_of_the_range(tk):
     got = tk.linear(big.cuda(), w.cuda()).double().cpu()
     want = big.double() @ w.double().T
     assert float(((got - want).abs() / want.abs().clamp(min=1e-300)).max()) <= 2.0 ** -22
+
+
+def spread(shape, g, low, high):
+    """Values of either sign with random bits, their exponents uniform over [low, high]."""
+    m = 1 + torch.rand(shape, generator=g, dtype=torch.float64)
+    e = torch.randint(low, high + 1, shape, generator=g).double()
+    return (torch.where(torch.rand(shape, generator=g) < 0.5, -m, m) * 2.0 ** e).float()
+
+
+# exponents of x and of w: x near f32's smallest normal values, below them, over a wide range, both operands small, a small
+# one that meets a large one (a product that no scaling holds), and ordinary ones
+ENDS = [((-125, -112), (0, 0)), ((-147, -127), (1, 2)), ((-140, 5), (-3, 3)), ((-140, -20), (-140, 20)), ((-140, 40), (-140, 40)),
+        ((-126, -100), (60, 126)), ((90, 100), (20, 22))]
+
+
+@pytest.mark.parametrize("x_ends,w_ends", ENDS)
+@pytest.mark.parametrize("rows,inner,outer", [(70, 3, 90), (300, 200, 264)])
+def test_f32_products_over_the_whole_range(tk, rows, inner, outer, x_ends, w_ends):
+    """Every value of f32 keeps its bits, and each row its own scale: the bound of an f32 sum, or of a denormal's spacing."""
+    g = gen(rows + x_ends[0] + w_ends[0])
+    x, w = spread((rows, inner), g, *x_ends), spread((outer, inner), g, *w_ends)
+    x[1], x[2, 0], w[5] = 0.0, 1.5, 0.0
+    b = spread((outer,), g, -130, -126)
+    dy = spread((rows, outer), g, *x_ends)
+    y = tk.linear(x.cuda(), w.cuda(), b.cuda())
+    dx, dw, _ = tk.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    x, w, b, dy = x.double(), w.double(), b.double(), dy.double()
+    for got, p, q, more in ((y, x, w.T, b), (dx, dy, w, 0.0 * w[:1]), (dw, dy.T, x, 0.0 * x[:1])):
+        want, mag, n = p @ q + more, p.abs() @ q.abs() + more.abs(), p.shape[1]
+        got = got.double().cpu()
+        end = want.abs() >= 2.0 ** 127
+        bound = (n + 4) * 2.0 ** -23 * mag + n * 2.0 ** -149
+        assert bool(((got - want).abs() <= bound)[~end].all()), float(((got - want).abs() / bound)[~end].max())
+
+
+def test_small_and_infinite_values_together(tk):
+    g = gen(3)
+    x, w = spread((60, 40), g, -120, -115), spread((50, 40), g, 0, 1)
+    x[7, 3] = torch.inf
+    want = x.double() @ w.double().T
+    got = tk.linear(x.cuda(), w.cuda()).double().cpu()
+    assert torch.equal(got[7], want[7])
+    rest = torch.arange(60) != 7
+    bound = 44 * 2.0 ** -23 * (x.double().abs() @ w.double().abs().T)[rest]
+    assert bool(((got - want).abs()[rest] <= bound).all())

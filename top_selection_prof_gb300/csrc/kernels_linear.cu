@@ -13,10 +13,11 @@ namespace {
 // ---------------------------------------------------------------------------
 // f32 products on the CUDA cores: what runs in the tensor cores' place when an
 // operand holds an infinity or NaN (their three-part form has no such
-// values).  One block of 256 threads makes a 128 x 128 tile of c from 16-deep
-// slices in shared memory, 8 x 8 results a thread in registers, every product
-// and sum in f32.  It does nothing, at the cost of its launch, unless the
-// operands' split left this call's mark.
+// values), or values of both ends of f32's range meet.  One block of 256
+// threads makes a 128 x 128 tile of c from 16-deep slices in shared memory,
+// 8 x 8 results a thread in registers, every product and sum in f32.  It does
+// nothing, at the cost of its launch, unless the operands' split left this
+// call's marks.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128, kDeep = 16, kSimtThreads = 256;
 constexpr int kTilePad = kTile + 4;
@@ -37,7 +38,7 @@ struct SimtParams {
   T* pre;
   int64_t ldp;
   int64_t tiles_n;
-  const int* mark;  // the product is made only where *mark == call (nullable)
+  const int* marks;  // the product is made only where these say so for `call`
   int call;
 };
 
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_product_kernel(const SimtPa
   __shared__ float as[kDeep][kTilePad], bs[kDeep][kTilePad];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (p.mark && *p.mark != p.call) return;
+  if (!parts_plan(p.marks, p.call).cores) return;
   const int64_t m0 = (blockIdx.x / p.tiles_n) * kTile, n0 = (blockIdx.x % p.tiles_n) * kTile;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float acc[8][8] = {};
@@ -108,10 +109,10 @@ __global__ void __launch_bounds__(kSimtThreads) simt_product_kernel(const SimtPa
   }
 }
 
-cudaError_t launch_simt_t(const Product& g, const int* mark, int call, cudaStream_t st) {
+cudaError_t launch_simt_t(const Product& g, const int* marks, int call, cudaStream_t st) {
   using T = float;
   SimtParams<T> p;
-  p.mark = mark;
+  p.marks = marks;
   p.call = call;
   p.a = static_cast<const T*>(g.a.p);
   p.b = static_cast<const T*>(g.b.p);
@@ -722,6 +723,6 @@ cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream
   return launch_mma(g, sc, words, call, st);
 }
 
-cudaError_t launch_simt(const Product& g, const int* mark, int call, cudaStream_t st) { return launch_simt_t(g, mark, call, st); }
+cudaError_t launch_simt(const Product& g, const int* marks, int call, cudaStream_t st) { return launch_simt_t(g, marks, call, st); }
 
 }  // namespace tk

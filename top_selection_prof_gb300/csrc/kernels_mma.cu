@@ -27,6 +27,8 @@
 // product's sign and reached 2^-21.  So a stage is one of six times as many;
 // results are f32.  An infinity would meet a zero part (NaN): where the split
 // finds one, the product is made on the CUDA cores and this kernel does nothing.
+// An operand with values whose third part bf16 cannot hold is split anew,
+// scaled by a power of two that the results are freed of.
 //
 // A bf16 operand a whose values have a rest (the gradient of a smooth
 // activation) is multiplied as two parts, the rest first: a stage is one of
@@ -112,7 +114,7 @@ struct MmaParams {
   int64_t ldp;
   float* part;             // sums of parts of k: 2 slots a pair, each kPairM x kTileN
   unsigned* ticket;        // 2 kEpiWarps a shared tile, zero between launches
-  const int* mark;         // *mark == call: an operand of parts holds a value that is not finite
+  const int* marks;        // of operands in parts, as `call` left them
   int call;
   int* status;
 };
@@ -390,9 +392,9 @@ __device__ __forceinline__ void add_bias32(float* v, const float* bias) {
   }
 }
 
-__device__ __forceinline__ void halve32(float* v) {
+__device__ __forceinline__ void scale32(float* v, float f) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= 0.5f;
+  for (int i = 0; i < 32; ++i) v[i] *= f;
 }
 
 // The pairs whose runs meet shared tile t, [first, first + parts).
@@ -446,9 +448,16 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
   grid_launch_dependents();
 
   Worker worker(p.deal, blockIdx.x / 2);
-  const bool marked = TERMS > 1 && *p.mark == p.call;
-  if (TERMS == kTermsF32 && marked) worker.leave();  // (made on the CUDA cores)
-  const bool twice = TERMS == kTermsRest && marked;
+  bool twice = false;   // the leading part in the rest's place too
+  float undo = 1.0f;    // a power of two that the sums are multiplied by
+  if constexpr (TERMS == kTermsF32) {
+    const PartsPlan plan = parts_plan(p.marks, p.call);
+    if (plan.cores) worker.leave();
+    undo = (plan.scale_a ? kUnscale : 1.0f) * (plan.scale_b ? kUnscale : 1.0f);
+  } else if constexpr (TERMS == kTermsRest) {
+    twice = p.marks[kMarkOther] == p.call;
+    if (twice) undo = 0.5f;
+  }
   Work w;
   bool ok = true;
 
@@ -657,7 +666,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             }
           }
         }
-        if (twice) halve32(v);
+        if (undo != 1.0f) scale32(v, undo);
         if (bias) add_bias32(v, bias_own + c);
       };
       if (sizeof(T) == 2 && w.slot < 0 && !p.pre_ptr && !residual) {
@@ -694,7 +703,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             if (s + 1 < kHalf / 32) tmem_load32(acc + 32 * (s + 1), v[(s + 1) & 1]);
             else free_accumulator(lane, acc_empty(buf));
             float* z = v[s & 1];
-            if (twice) halve32(z);
+            if (undo != 1.0f) scale32(z, undo);
             if (bias) add_bias32(z, bias_own + 32 * s);
             if (p.act == kActRelu) apply_act<T, 32>(z, kActRelu);
             else if (p.act == kActSilu) apply_act<T, 32>(z, kActSilu);
@@ -709,7 +718,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
             tmem_load32(acc + 32 * s, z);
             tmem_wait_load();
             if (s + 1 == kHalf / 32) free_accumulator(lane, acc_empty(buf));
-            if (twice) halve32(z);
+            if (undo != 1.0f) scale32(z, undo);
             if (bias) add_bias32(z, bias_own + 32 * s);
             apply_act<T, 32>(z, kActGelu);
             finish(s, z);
@@ -806,8 +815,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __nv_bfloat16* sr
 
 // The three bf16 parts of both f32 operands, `plane` values apart, rows of `ld`
 // values.  A part is what the parts before it left, rounded to bf16, and the
-// three hold all 24 bits.  *other becomes `call` when a value is not finite, or
-// its leading part would not be.
+// three hold all 24 bits of a value of kSmall or more.
 struct Split {
   const float* src;
   int64_t lds, rows, cols;
@@ -816,22 +824,21 @@ struct Split {
   unsigned blocks;
 };
 constexpr int kSplitEach = 4;  // values of a thread, next to each other
-__global__ void __launch_bounds__(256) split_rows_kernel(const Split a, const Split b, int* other, int call) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const bool second = blockIdx.x >= a.blocks;
-  const Split& s = second ? b : a;
-  const int64_t per = (s.cols + kSplitEach - 1) / kSplitEach;
-  const int64_t at = int64_t(blockIdx.x - (second ? a.blocks : 0)) * 256 + threadIdx.x;
-  if (at >= s.rows * per) return;
-  const int64_t r = at / per, c = (at - r * per) * kSplitEach;
+// The values from place `at` on, times `scale`; *most and *least: the largest magnitude, and the smallest but zero (NaN
+// counts as infinity).
+__device__ __forceinline__ void split_values(const Split& s, int64_t at, float scale, float* most, float* least) {
+  const int64_t per = (s.cols + kSplitEach - 1) / kSplitEach, r = at / per, c = (at - r * per) * kSplitEach;
   const float* src = s.src + r * s.lds + c;
   float v[kSplitEach];
-  bool finite = true;
 #pragma unroll
   for (int e = 0; e < kSplitEach; ++e) v[e] = c + e < s.cols ? src[e] : 0.0f;
 #pragma unroll
-  for (int e = 0; e < kSplitEach; ++e) finite = finite && fabsf(v[e]) < 0x1.ffp127f;
+  for (int e = 0; e < kSplitEach; ++e) {
+    const float m = fabsf(v[e]);
+    *most = m <= *most ? *most : m < INFINITY ? m : INFINITY;
+    if (m > 0.0f) *least = fminf(*least, m);
+    v[e] *= scale;
+  }
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
     uint32_t two[kSplitEach / 2];
@@ -845,11 +852,37 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const Split a, const Sp
     // (rows of the parts hold a multiple of 8 values: the last store may go past cols, not past the row)
     *reinterpret_cast<uint2*>(s.dst + q * s.plane + r * s.ld + c) = make_uint2(two[0], two[1]);
   }
-  if (!finite) *other = call;
+}
+__device__ __forceinline__ int64_t split_places(const Split& s) { return s.rows * ((s.cols + kSplitEach - 1) / kSplitEach); }
+
+__global__ void __launch_bounds__(256) split_rows_kernel(const Split a, const Split b, int* marks, int call) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const bool second = blockIdx.x >= a.blocks;
+  const Split& s = second ? b : a;
+  const int64_t at = int64_t(blockIdx.x - (second ? a.blocks : 0)) * 256 + threadIdx.x;
+  if (at >= split_places(s)) return;
+  float most = 0.0f, least = INFINITY;
+  split_values(s, at, 1.0f, &most, &least);
+  if (!(most < 0x1.ffp127f)) marks[kMarkOther] = call;  // (what rounds to bf16's infinity included)
+  if (most >= kLarge) marks[kMarkLarge] = call;
+  if (least < kSmall) marks[second ? kMarkSmallB : kMarkSmallA] = call;
+}
+// The same again, scaled, for an operand that is marked so (a few blocks an SM: nothing, mostly).
+__global__ void __launch_bounds__(256) split_scaled_kernel(const Split a, const Split b, const int* marks, int call) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const PartsPlan plan = parts_plan(marks, call);
+  float most = 0.0f, least = 0.0f;
+  const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+  if (plan.scale_a)
+    for (int64_t at = first; at < split_places(a); at += step) split_values(a, at, kScale, &most, &least);
+  if (plan.scale_b)
+    for (int64_t at = first; at < split_places(b); at += step) split_values(b, at, kScale, &most, &least);
 }
 
-// *other becomes `call` when a value of a bf16 matrix is not finite; a thread looks at eight values of a row.
-__global__ void __launch_bounds__(256) mark_other_kernel(const __nv_bfloat16* p, int64_t ld, int64_t rows, int64_t cols, int* other,
+// kMarkOther becomes `call` when a value of a bf16 matrix is not finite; a thread looks at eight values of a row.
+__global__ void __launch_bounds__(256) mark_other_kernel(const __nv_bfloat16* p, int64_t ld, int64_t rows, int64_t cols, int* marks,
                                                          int call) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -867,7 +900,7 @@ __global__ void __launch_bounds__(256) mark_other_kernel(const __nv_bfloat16* p,
   } else {
     for (int i = 0; i < 8 && c + i < cols; ++i) finite = finite && fabsf(to_f32(q[i])) < INFINITY;
   }
-  if (!finite) *other = call;
+  if (!finite) marks[kMarkOther] = call;
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -999,12 +1032,12 @@ bool split_of(const Operand& o, int64_t i, int64_t k, __nv_bfloat16* dst, int64_
   return true;
 }
 
-cudaError_t mark_other(const Operand& o, int64_t i, int64_t k, int* other, int call, cudaStream_t st) {
+cudaError_t mark_other(const Operand& o, int64_t i, int64_t k, int* marks, int call, cudaStream_t st) {
   const int64_t rows = operand_rows(o, i, k), cols = operand_cols(o, i, k);
   const int64_t blocks = (rows * ((cols + 7) / 8) + 255) / 256;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   return launch_after(mark_other_kernel, static_cast<unsigned>(blocks), 256, 0, st, static_cast<const __nv_bfloat16*>(o.p), o.ld,
-                      rows, cols, other, call);
+                      rows, cols, marks, call);
 }
 
 template <typename T, int TERMS>
@@ -1027,18 +1060,21 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   MmaPlan q;
   if (!plan_mma(g, sc, &q)) return cudaErrorNotSupported;
   const bool f32 = g.dtype == kF32;
-  int* other = words + kOpsOther;
+  int* marks = words + kOpsMarks;
   cudaError_t e = cudaSuccess;
   if (f32) {
     Split a, b;
     if (!split_of(g.a, g.m, g.k, q.copy_a, q.ld_a, &a) || !split_of(g.b, g.n, g.k, q.copy_b, q.ld_b, &b)) return cudaErrorNotSupported;
-    e = launch_after(split_rows_kernel, a.blocks + b.blocks, 256, 0, st, a, b, other, call);
+    e = launch_after(split_rows_kernel, a.blocks + b.blocks, 256, 0, st, a, b, marks, call);
+    const unsigned few = 4 * static_cast<unsigned>(ops_sm_count()), most = a.blocks > b.blocks ? a.blocks : b.blocks;
+    if (e == cudaSuccess)
+      e = launch_after(split_scaled_kernel, most < few ? most : few, 256, 0, st, a, b, static_cast<const int*>(marks), call);
   } else {
     if (q.copy_a) e = align_rows(g.a, g.m, g.k, q.copy_a, q.ld_a, st);
     if (e == cudaSuccess && q.copy_b) e = align_rows(g.b, g.n, g.k, q.copy_b, q.ld_b, st);
-    if (e == cudaSuccess && g.a.rest) e = mark_other(g.b, g.n, g.k, other, call, st);
+    if (e == cudaSuccess && g.a.rest) e = mark_other(g.b, g.n, g.k, marks, call, st);
   }
-  if (e == cudaSuccess && f32) e = launch_simt(g, other, call, st);
+  if (e == cudaSuccess && f32) e = launch_simt(g, marks, call, st);
   if (e != cudaSuccess) return e;
   MmaParams p{};
   p.m = g.m;
@@ -1064,7 +1100,7 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   p.ldc = g.ldc;
   p.pre_ptr = g.pre;
   p.ldp = g.ldp;
-  p.mark = other;
+  p.marks = marks;
   p.call = call;
   p.part = q.part;
   p.ticket = reinterpret_cast<unsigned*>(words) + 64;

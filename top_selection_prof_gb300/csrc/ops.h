@@ -34,8 +34,11 @@ cudaError_t ops_take_status(cudaStream_t st, int* status);
 
 // Words that each (device, stream) keeps for the operators, zero at first: [0]
 // the status that a kernel sets when a wait runs out, [32] and [64..] tickets
-// that every kernel leaves at zero, [kOpsOther] the last call that met a value that is not finite.
-constexpr int64_t kOpsWords = 16384, kOpsOther = 48;
+// that every kernel leaves at zero, [kOpsMarks..] what the operands of the tensor cores' products hold.
+constexpr int64_t kOpsWords = 16384, kOpsMarks = 48;
+// Each mark is the number of the last call that found: a value that is not finite (or not as bf16), a value of a or of b
+// too small for parts (f32 only), a value of either too large to be scaled.
+enum : int { kMarkOther = 0, kMarkSmallA = 1, kMarkSmallB = 2, kMarkLarge = 3 };
 
 // SMs of the current device.
 int ops_sm_count();
@@ -71,10 +74,9 @@ struct Product {
 // words: the stream's kOpsWords.
 cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st);
 size_t product_scratch_bytes(const Product& g);
-// The same on the tensor cores (kernels_mma.cu).  F32: words[kOpsOther] becomes `call` when an operand holds a value that
-// is not finite; launch_simt, which makes the product when it finds that mark, then runs in their place.
+// The same on the tensor cores (kernels_mma.cu), or by launch_simt's kernel where the marks that `call` leaves say so.
 cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cudaStream_t st);
-cudaError_t launch_simt(const Product& g, const int* mark, int call, cudaStream_t st);
+cudaError_t launch_simt(const Product& g, const int* marks, int call, cudaStream_t st);
 size_t mma_scratch_bytes(const Product& g);
 
 // dz = dy * act'(pre) (act != none) and the column sums of dz into dbias

@@ -150,6 +150,20 @@ struct Vec {
   }
 };
 
+// What an f32 product by parts does with operands that are marked.  The third part of a value below kSmall would leave
+// bf16's range (2^-133): such an operand is scaled by kScale, unless a value of kLarge or more in either could then
+// overflow a sum (k < 2^31: 2^31 (2^32 kScale)^2 = 2^127); then, as with an infinity, the product goes to the CUDA cores.
+constexpr float kSmall = 0x1p-110f, kLarge = 0x1p32f, kScale = 0x1p16f, kUnscale = 0x1p-16f;
+struct PartsPlan {
+  bool cores;             // made on the CUDA cores
+  bool scale_a, scale_b;
+};
+__device__ __forceinline__ PartsPlan parts_plan(const int* marks, int call) {
+  const bool a = marks[kMarkSmallA] == call, b = marks[kMarkSmallB] == call;
+  const bool cores = marks[kMarkOther] == call || ((a || b) && marks[kMarkLarge] == call);
+  return {cores, a && !cores, b && !cores};
+}
+
 // Launches a kernel that calls grid_dependency_wait() before it touches memory:
 // it may start, and set itself up, while the grid before it in the stream ends.
 template <typename... A>
