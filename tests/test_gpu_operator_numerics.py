@@ -167,3 +167,42 @@ def test_small_and_infinite_values_together(tk):
     rest = torch.arange(60) != 7
     bound = 44 * 2.0 ** -23 * (x.double().abs() @ w.double().abs().T)[rest]
     assert bool(((got - want).abs()[rest] <= bound).all())
+
+
+def gelu_and_slope(z):
+    below = 0.5 * torch.special.erfc(z * -0.5 ** 0.5)   # (ndtr cancels, in 64 bits too)
+    return z * below, below + z * phi(z), below + z.abs() * phi(z)
+
+
+def silu_and_slope(z):
+    # (sigmoid(z) itself, not 1 - sigmoid(-z), so that nothing cancels)
+    s = torch.exp(-torch.nn.functional.softplus(-z))
+    t = torch.exp(-torch.nn.functional.softplus(z))
+    return z * s, s * (1 + z * t), s * (1 + z.abs() * t)
+
+
+def values_and_slopes(tk, z, act):
+    """act(z) by few rows and by many, act'(z): each a value of z by itself."""
+    one = torch.ones(2, 1, dtype=z.dtype, device="cuda")
+    many = tk.linear(z.cuda()[:, None], one, act=act)[:, 0]
+    few = torch.cat([tk.linear(p[:, None].contiguous(), one, act=act)[:, 1] for p in z.cuda().split(31)])
+    dy, x = torch.ones(1, z.numel(), dtype=z.dtype, device="cuda"), torch.ones(1, 1, dtype=z.dtype, device="cuda")
+    w = torch.ones(z.numel(), 1, dtype=z.dtype, device="cuda")
+    slope = tk.linear_backward(dy, x, w, pre=z.cuda()[None], act=act, need=(False, False, True))[2]
+    return many, few, slope
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gelu_in_its_tails(tk, dtype):
+    """Within a few units of each value, not of the largest.
+
+    f32: z^2 2^-23 from the rounding of the arguments of erfc and exp (whose logarithms change by z^2 / 2 times theirs), 4 units
+    of 2^-23 for the functions and 4 for the operations; bf16: 4.8e-6 for the fitted tail and 2^-22 for each approximation.
+    """
+    z = torch.linspace(-9, 9, 2001).to(dtype)
+    value, slope, mag = gelu_and_slope(z.double())
+    rel = (z.double() ** 2 + 8) * 2.0 ** -23 + (4.8e-6 + 2.0 ** -20 if dtype == torch.bfloat16 else 0.0)
+    many, few, got = values_and_slopes(tk, z, "gelu")
+    rounds_from(many, value, rel * value.abs())
+    rounds_from(few, value, rel * value.abs())
+    rounds_from(got, slope, rel * mag)
