@@ -206,3 +206,18 @@ def test_gelu_in_its_tails(tk, dtype):
     rounds_from(many, value, rel * value.abs())
     rounds_from(few, value, rel * value.abs())
     rounds_from(got, slope, rel * mag)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_silu_in_its_tails(tk, dtype):
+    """The same: 8 units of 2^-23 (bf16: 2^-20 for the approximations), z's exponential to its argument's rounding, and, where
+    e^z is denormal, its spacing (bf16: the approximation has no denormal values, so 2^-126) times |z|."""
+    z = torch.cat([torch.linspace(-103, 20, 3001), torch.linspace(-3, 3, 601)]).to(dtype)
+    value, slope, mag = silu_and_slope(z.double())
+    bf16 = dtype == torch.bfloat16
+    rel = (z.double().abs() + 8) * 2.0 ** -23 + (2.0 ** -20 if bf16 else 0.0)
+    end = (z.double().abs() + 2) * 2.0 ** (-126 if bf16 else -149)
+    many, few, got = values_and_slopes(tk, z, "silu")
+    rounds_from(many, value, rel * value.abs() + end)
+    rounds_from(few, value, rel * value.abs() + end)
+    rounds_from(got, slope, rel * mag + end)

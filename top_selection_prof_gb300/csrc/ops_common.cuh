@@ -221,6 +221,16 @@ __device__ __forceinline__ float relu(float z) {
   return y;
 }
 
+// s = 1 / (1 + e^-z) and t = 1 - s, both from e^-|z|: neither cancels, nor overflows below z = -88, where z s is still 1e-36.
+template <typename T>
+__device__ __forceinline__ void logistic(float z, float* s, float* t) {
+  const float a = fabsf(z);
+  const float e = sizeof(T) == 2 ? fast_exp2(a * -1.44269504f) : expf(-a);
+  const float r = sizeof(T) == 2 ? fast_rcp(1.0f + e) : 1.0f / (1.0f + e);
+  *s = z < 0.0f ? e * r : r;
+  *t = z < 0.0f ? r : e * r;
+}
+
 template <typename T>
 __device__ __forceinline__ float act_value(float z, int act) {
   constexpr bool kFast = sizeof(T) == 2;
@@ -234,12 +244,11 @@ __device__ __forceinline__ float act_value(float z, int act) {
         return z >= 0.0f ? z - low : low;
       }
       return z == -INFINITY ? 0.0f : z * normal_cdf(z);
-    case kActSilu:
-      if constexpr (kFast) {
-        const float c = z < -100.0f ? -100.0f : z;
-        return c * fast_rcp(1.0f + fast_exp2(c * -1.44269504f));
-      }
-      return z == -INFINITY ? 0.0f : z / (1.0f + expf(-z));
+    case kActSilu: {
+      float s, t;
+      logistic<T>(z, &s, &t);
+      return z == -INFINITY ? 0.0f : z * s;
+    }
     default: return z;
   }
 }
@@ -257,9 +266,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
       }
       return normal_cdf(z) + z * expf(-0.5f * z * z) * 0.3989422804014327f;
     case kActSilu: {
-      if (fabsf(z) > 80.0f) return z > 0.0f ? 1.0f : 0.0f;
-      const float s = kFast ? fast_rcp(1.0f + fast_exp2(z * -1.44269504f)) : 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
+      if (fabsf(z) == INFINITY) return z > 0.0f ? 1.0f : 0.0f;
+      float s, t;
+      logistic<T>(z, &s, &t);
+      return s * (1.0f + z * t);
     }
     default: return 1.0f;
   }
