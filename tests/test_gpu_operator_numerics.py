@@ -221,3 +221,17 @@ def test_silu_in_its_tails(tk, dtype):
     rounds_from(many, value, rel * value.abs() + end)
     rounds_from(few, value, rel * value.abs() + end)
     rounds_from(got, slope, rel * mag + end)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", [[20_000], [70_001], [1 << 22, 3, 100_003]])
+@pytest.mark.parametrize("value", [0.7, 0.1, 0.3, 1.9, None])
+def test_norm_of_equal_values(tk, value, sizes, dtype):
+    """Roundings that all go one way: four f32 squares (eight of bf16, exact) in one f32 sum are within 2.5 (4.4) x 2^-24 of
+    it, the sums of those lose 2^-47, the root halves that, and the norm's own rounding adds 2^-24."""
+    g = gen(7)
+    ts = [normals((n,), dtype, g) if value is None else torch.full((n,), value, dtype=dtype) for n in sizes]
+    want = float(torch.cat(ts).double().norm())
+    dev = [t.cuda() for t in ts]
+    assert abs(float(tk.grad_norm(dev)) - want) <= (4.4 / 2 + 1) * 2.0 ** -24 * want
+    assert abs(float(tk.clip_grad_norm_(dev, 1.0)) - want) <= (4.4 / 2 + 1) * 2.0 ** -24 * want

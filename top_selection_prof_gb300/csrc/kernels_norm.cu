@@ -4,11 +4,15 @@
 // The tensors' values are cut into chunks, dealt to the blocks in turn (all
 // blocks then read close to each other: one run a block took 45 us where this
 // takes 28); the table of tensors goes to the kernel as its parameter, so
-// nothing is copied to the device.  A thread sums a chunk's squares in f32
-// and adds the chunks' sums in two f32 (a sum and what its rounding lost: the
-// card's f64 is slow); the blocks' sums are added in f64 in their order.  Where
-// the f32 squares overflow, or are so small that bits are lost, the chunk is
-// summed again in f64, so that the norm is exact to f32 for any finite input.
+// nothing is copied to the device.  A thread sums the squares of one 16-byte
+// vector in f32 and adds the vectors' sums in two f32 (a sum and what its
+// rounding lost: the card's f64 is slow); the blocks' sums are added in f64 in
+// their order.  A vector's sum of four f32 squares is within 2.5 x 2^-24 of it
+// (of eight bf16 squares, which are exact, 4.4), and the norm, its own rounding
+// included, within 4 x 2^-24, equal values that all round the same way included
+// (sums of 128 squares in one f32: 13 x 2^-24 for values of 0.7).  Where the
+// f32 squares overflow, or are so small that bits are lost, the chunk is summed
+// again in f64, so that this holds for any finite input.
 //
 // Few values (at most kFewValues) take one launch: a cluster of blocks holds
 // them in registers, exchanges its sums through distributed shared memory and
@@ -148,23 +152,32 @@ struct Squares {
 template <typename T>
 __device__ __forceinline__ void part_squares(const T* p, int64_t n, uint64_t policy, Squares* to) {
   constexpr int kVec = 16 / sizeof(T);
-  float sum = 0.0f, most = 0.0f;
-  auto add = [&](float v) {
-    sum = fmaf(v, v, sum);
-    most = fmaxf(most, fabsf(v));
-  };
+  TwoSum sum{0.0f, 0.0f};
+  float most = 0.0f;
   each_value<T, false>(
       p, n, policy,
       [&](const Vec<T, kVec>& v, int64_t) {
+        float s = 0.0f;
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) add(v.v[c]);
+        for (int c = 0; c < kVec; ++c) {
+          s = fmaf(v.v[c], v.v[c], s);
+          most = fmaxf(most, fabsf(v.v[c]));
+        }
+        sum.add(s);
       },
-      [&](float v, int64_t) { add(v); });
+      [&](float v, int64_t) {
+        sum.add(v * v);
+        most = fmaxf(most, fabsf(v));
+      });
   // f32 squares neither overflow nor lose bits between these (a block's sum of them stays below 2^127 for any tensor
   // that fits the card); zeros stay what they are, NaN and infinities go on through f64
-  if (most == 0.0f && sum == 0.0f) return;
-  if (most > 1e-15f && most < 1e12f && sum < INFINITY) to->sum.add(sum);
-  else to->wide += part_squares_wide(p, n, policy);
+  if (most == 0.0f && sum.hi == 0.0f) return;
+  if (most > 1e-15f && most < 1e12f && sum.hi < INFINITY) {
+    to->sum.add(sum.hi);
+    to->sum.lo += sum.lo;
+  } else {
+    to->wide += part_squares_wide(p, n, policy);
+  }
 }
 
 template <int N>
@@ -320,18 +333,24 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kFewThreads)
       where[e] = lo;
     }
   }
-  // in f32 over a warp, then f64; all in f64 where the squares leave f32 or lose bits (the card's f64 is slow)
-  float sum32 = 0.0f, most = 0.0f;
+  // in two f32 over a warp, then f64; all in f64 where the squares leave f32 or lose bits (the card's f64 is slow)
+  TwoSum two{0.0f, 0.0f};
+  float most = 0.0f;
 #pragma unroll
   for (int e = 0; e < kFewEach; ++e) {
-    sum32 = fmaf(v[e], v[e], sum32);
+    two.add(v[e] * v[e]);
     most = fmaxf(most, fabsf(v[e]));
   }
   double sum;
   if (__all_sync(~0u, most == 0.0f || !(most < INFINITY) || (most > 1e-15f && most < 1e17f))) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum32 += __shfl_xor_sync(~0u, sum32, o);
-    sum = static_cast<double>(sum32);
+    for (int o = 16; o; o >>= 1) {
+      const float hi = __shfl_xor_sync(~0u, two.hi, o), lo = __shfl_xor_sync(~0u, two.lo, o);
+      two.add(hi);
+      two.lo += lo;
+    }
+    // (an infinity or NaN in hi leaves NaN in lo)
+    sum = fabsf(two.hi) < INFINITY ? static_cast<double>(two.hi) + two.lo : static_cast<double>(two.hi);
   } else {
     sum = 0.0;
 #pragma unroll
