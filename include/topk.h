@@ -29,8 +29,10 @@
  *     more expected survivors than one refinement block caches, 32 MiB of
  *     bin regions into which the filter places its survivors); it grows on
  *     demand with stream-ordered allocation and is never shrunk.  Calls that
- *     share a stream are ordered; calls on different streams use different
- *     workspaces.
+ *     share a stream are ordered, whichever threads make them (a call holds
+ *     the stream's workspace until its last launch is enqueued); calls on
+ *     different streams, and on the per-thread default streams of different
+ *     threads, use different workspaces.
  *   - Errors are returned as topk_status_t codes; nothing is thrown across the
  *     ABI and no message is printed.
  */

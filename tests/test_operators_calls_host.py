@@ -1,0 +1,146 @@
+"""What the host code of the operators asks the CUDA runtime for, seen by a stand-in for it (fake_cudart.cpp): no GPU.
+
+The library's own objects are linked with the stand-in, and the C entries are called with addresses that nothing touches.
+"""
+import ctypes
+import os
+import re
+import subprocess
+import threading
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+VP = ctypes.c_void_p
+F32, BF16 = 0, 1
+
+
+@pytest.fixture(scope="session")
+def fake_path(tmp_path_factory):
+    from top_selection_prof_gb300 import build
+    objects = [os.path.join(build.BUILD, os.path.splitext(s)[0] + ".o") for s in build.SOURCES]
+    sources = [os.path.join(build.CSRC, f) for f in os.listdir(build.CSRC)]
+    if not all(map(os.path.exists, objects)) or min(map(os.path.getmtime, objects)) < max(map(os.path.getmtime, sources)):
+        build.build()
+    out = str(tmp_path_factory.mktemp("fake") / "libtopk_fake.so")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", include, "-o", out,
+                    os.path.join(ROOT, "tests", "fake_cudart.cpp"), *objects, "-lpthread", "-Wl,-z,defs,-Bsymbolic"], check=True)
+    return out
+
+
+@pytest.fixture
+def lib(fake_path, tmp_path):
+    """The library anew for each test: a copy, as one path is loaded once."""
+    import shutil
+    from top_selection_prof_gb300 import _lib
+    path = str(tmp_path / "lib.so")
+    shutil.copy(fake_path, path)
+    lib = ctypes.CDLL(path)
+    lib.fake_take_log.restype = ctypes.c_char_p
+    lib.fake_set_capturing.argtypes = [VP, ctypes.c_int]
+    real = _lib.get()
+    for name in _lib.EXPORTS:
+        getattr(lib, name).argtypes = getattr(real, name).argtypes
+        getattr(lib, name).restype = getattr(real, name).restype
+    return lib
+
+
+def at(i):
+    return VP((i + 1) << 40)   # never touched
+
+
+def events(lib):
+    got = []
+    for line in lib.fake_take_log().decode().splitlines():
+        m = re.match(r"(\w+) thread=(\d+) device=(\d+) stream=(\d+) (\S+)", line)
+        got.append((m[1], int(m[2]), int(m[3]), int(m[4]), m[5]))
+    return got
+
+
+def linear(lib, stream=0, dtype=F32, rows=300, inner=64, outer=512):
+    return lib.topk_linear(at(0), inner, at(1), inner, None, None, 0, dtype, rows, inner, outer, 0, at(2), outer, None, 0, stream)
+
+
+def linear_backward(lib, stream=0, dtype=BF16, rows=300, inner=64, outer=512, act=3):
+    return lib.topk_linear_backward(at(0), outer, at(1), inner, at(2), inner, at(3), outer, dtype, rows, inner, outer, act, at(4),
+                                    at(5), at(6), stream)
+
+
+def decode_backward(lib, stream=0, dtype=F32, rows=300, n=2000, d=512, count=5000):
+    return lib.topk_decode_backward(at(0), d, at(1), at(2), count, 0, at(3), d, dtype, rows, n, d, at(4), at(5), at(6), stream)
+
+
+def clip(lib, stream=0, num=700, count=1000):
+    ptrs = (VP * num)(*[(i + 1) << 20 for i in range(num)])
+    return lib.topk_clip_grad_norm(ptrs, ptrs, (ctypes.c_int64 * num)(*[count] * num), (ctypes.c_int * num)(*[F32] * num), num,
+                                   1.0, at(2), stream)
+
+
+def select(lib, stream=0):
+    return lib.topk_select_global(at(0), BF16, 512, 16384, 4096, 1, 1e-3, at(1), at(2), stream)
+
+
+CALLS = [linear, linear_backward, decode_backward, clip, select]
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda c: c.__name__)
+def test_threads_on_one_stream_do_not_mix_their_launches(lib, call):
+    """A call's launches share scratch: those of another thread's call on the stream may not come between them."""
+    assert call(lib) == 0
+    chain = sum(e[0] == "launch" for e in events(lib))
+    assert chain > 1
+    assert call(lib) == 0            # (the first call also made its scratch)
+    assert sum(e[0] == "launch" for e in events(lib)) == chain
+    lib.fake_set_launch_us(200)
+    failed = []
+
+    def work():
+        for _ in range(6):
+            if call(lib) != 0:
+                failed.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    lib.fake_set_launch_us(0)
+    who = [e[1] for e in events(lib) if e[0] == "launch"]
+    assert not failed and len(who) == 4 * 6 * chain
+    assert all(len(set(who[i:i + chain])) == 1 for i in range(0, len(who), chain))
+
+
+def test_scratch_grown_by_one_thread_is_not_another_calls(lib):
+    """A larger call releases the block in stream order: after the whole chain that uses it, not in its middle."""
+    assert linear(lib, inner=2048) == 0
+    chain = sum(e[0] == "launch" for e in events(lib))
+    lib.fake_set_launch_us(300)
+    small = threading.Thread(target=lambda: [linear(lib, inner=2048) for _ in range(8)])
+    large = threading.Thread(target=lambda: [linear(lib, rows=300 << i, inner=2048) for i in range(1, 6)])
+    small.start(), large.start()
+    small.join(), large.join()
+    lib.fake_set_launch_us(0)
+    done = {}   # launches of each thread
+    log = events(lib)
+    assert sum(e[0] == "free" for e in log) >= 3
+    for e in log:
+        if e[0] == "launch":
+            done[e[1]] = done.get(e[1], 0) + 1
+        if e[0] == "free":
+            assert all(n % chain == 0 for n in done.values())
+
+
+def test_threads_have_scratch_of_their_own_on_the_per_thread_stream(lib):
+    per_thread = 2   # cudaStreamPerThread: one handle, a stream of each thread
+    made = []
+
+    def work():
+        assert linear(lib, stream=per_thread) == 0
+        made.append([e[4] for e in events(lib) if e[0] == "malloc"])
+
+    for _ in range(2):
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+    assert len(made) == 2 and made[0] and made[1]

@@ -5,6 +5,8 @@
 
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <mutex>
+#include <tuple>
 
 // Functions both the host and the kernels use (this header is also compiled
 // by the host compiler, which knows no CUDA qualifiers).
@@ -324,6 +326,30 @@ int64_t select_xbuf_stride(int64_t k);
 cudaError_t launch_select(const Problem& p, const SelectJob& job, int64_t source_bound, int* cluster,
                           cudaStream_t st);
 int64_t select_max_k();
+
+// ---- what the library keeps for a stream (topk_api.cu) ------------------------
+// Scratch and status words are found by device and stream; those of the
+// per-thread default stream, one handle for a stream of each thread, by the
+// thread too.
+struct StreamKey {
+  int dev = 0;
+  cudaStream_t st = nullptr;
+  uint64_t thread = 0;  // of the per-thread default stream
+  bool operator<(const StreamKey& o) const {
+    return std::tie(dev, st, thread) < std::tie(o.dev, o.st, o.thread);
+  }
+};
+cudaError_t stream_key(cudaStream_t st, StreamKey* key);
+// Holds what is kept for a stream, from when a call takes its scratch until
+// its last launch is enqueued: the launches of two threads' calls on one stream
+// then follow one another whole, as the scratch they share needs.
+class StreamHold {
+ public:
+  explicit StreamHold(const StreamKey& key);
+
+ private:
+  std::unique_lock<std::mutex> lock_;
+};
 
 // ---- the C ABI's pipeline on caller-provided scratch (topk_api.cu) -----------
 // Counters that pick which copy of the alternating zero-kept regions a call

@@ -6,7 +6,6 @@
 #include <map>
 #include <mutex>
 #include <new>
-#include <utility>
 #include <vector>
 
 #include "../../include/topk.h"
@@ -38,40 +37,45 @@ struct Block {
   int* words = nullptr;  // kOpsWords
 };
 std::mutex g_mu;
-std::map<std::pair<int, cudaStream_t>, Block> g_blocks;
+std::map<StreamKey, Block> g_blocks;
 
-cudaError_t block_of(cudaStream_t st, size_t bytes, void** out, int** words = nullptr) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(g_mu);
-  Block& b = g_blocks[std::make_pair(dev, st)];
-  if (b.bytes < bytes) {
-    const size_t grow = (bytes + bytes / 4 + 0xFFFFF) & ~size_t(0xFFFFF);
-    void* p = nullptr;
-    e = cudaMallocAsync(&p, grow, st);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
+// One call's use of its stream's block: the stream is held until the call's last launch is enqueued.
+class Call {
+ public:
+  explicit Call(cudaStream_t st) : st_(st), key_error_(stream_key(st, &key_)), hold_(key_) {}
+  cudaError_t scratch(size_t bytes, void** out, int** words = nullptr) {
+    if (key_error_ != cudaSuccess) return key_error_;
+    std::unique_lock<std::mutex> lock(g_mu);
+    Block& b = g_blocks[key_];  // (nodes do not move; this one is the holder's)
+    lock.unlock();
+    cudaError_t e = cudaSuccess;
+    if (b.bytes < bytes) {
+      const size_t grow = (bytes + bytes / 4 + 0xFFFFF) & ~size_t(0xFFFFF);
+      void* p = nullptr;
+      e = cudaMallocAsync(&p, grow, st_);
+      if (e != cudaSuccess) return e;
+      if (b.ptr) cudaFreeAsync(b.ptr, st_);
+      b.ptr = p;
+      b.bytes = grow;
     }
-    if (b.ptr) cudaFreeAsync(b.ptr, st);
-    b.ptr = p;
-    b.bytes = grow;
-  }
-  if (words && !b.words) {
-    int* w = nullptr;
-    e = cudaMallocAsync(&w, sizeof(int) * kOpsWords, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(w, 0, sizeof(int) * kOpsWords, st);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
+    if (words && !b.words) {
+      int* w = nullptr;
+      e = cudaMallocAsync(&w, sizeof(int) * kOpsWords, st_);
+      if (e == cudaSuccess) e = cudaMemsetAsync(w, 0, sizeof(int) * kOpsWords, st_);
+      if (e != cudaSuccess) return e;
+      b.words = w;
     }
-    b.words = w;
+    *out = b.ptr;
+    if (words) *words = b.words;
+    return cudaSuccess;
   }
-  *out = b.ptr;
-  if (words) *words = b.words;
-  return cudaSuccess;
-}
+
+ private:
+  cudaStream_t st_;
+  StreamKey key_;
+  cudaError_t key_error_;
+  StreamHold hold_;
+};
 
 // cudaErrorNotSupported: more blocks or tiles than a launch counts.
 int status_of(cudaError_t e) {
@@ -106,7 +110,8 @@ int linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* b
   const Product g{{x, ldx, true}, {w, ldw, true}, rows, outer, inner, dtype, bias, residual, ldr, act, y, ldy, pre, ldp};
   void* base = nullptr;
   int* words = nullptr;
-  cudaError_t e = block_of(st, product_scratch_bytes(g), &base, &words);
+  Call call(st);
+  cudaError_t e = call.scratch(product_scratch_bytes(g), &base, &words);
   if (e != cudaSuccess) return status_of(e);
   Scratch sc(base);
   return status_of(launch_product(g, sc, words, st));
@@ -149,7 +154,8 @@ int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, co
   const size_t px = dx ? product_scratch_bytes(gx) : 0, pw = dw ? product_scratch_bytes(gw) : 0;
   void* base = nullptr;
   int* words = nullptr;
-  cudaError_t e = block_of(st, plan.used() + (px > pw ? px : pw), &base, &words);
+  Call call(st);
+  cudaError_t e = call.scratch(plan.used() + (px > pw ? px : pw), &base, &words);
   if (e != cudaSuccess) return status_of(e);
   Scratch sc(base);
   lay(sc);
@@ -188,7 +194,8 @@ int run_sums(const ColumnSums* cols, const RowSums* rws, const SlopeSums* sums_i
     bytes = sc.used() > bytes ? sc.used() : bytes;
   }
   void* base = nullptr;
-  cudaError_t e = block_of(st, bytes, &base);
+  Call call(st);
+  cudaError_t e = call.scratch(bytes, &base);
   if (e == cudaSuccess && (cols || rws)) {
     Scratch sc(base);
     e = launch_sums(cols, rws, sc, st);
@@ -213,7 +220,8 @@ int clip(const void* const* grads, void* const* out, const int64_t* counts, cons
   }
   void* base = nullptr;
   int* words = nullptr;
-  const cudaError_t e = block_of(st, clip_scratch_bytes(), &base, &words);
+  Call call(st);
+  const cudaError_t e = call.scratch(clip_scratch_bytes(), &base, &words);
   if (e != cudaSuccess) return status_of(e);
   Scratch sc(base);
   return status_of(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, words, sc, st));
@@ -222,12 +230,14 @@ int clip(const void* const* grads, void* const* out, const int64_t* counts, cons
 }  // namespace
 
 cudaError_t ops_take_status(cudaStream_t st, int* status) {
-  int dev = 0, *word = nullptr;
-  cudaError_t e = cudaGetDevice(&dev);
+  int* word = nullptr;
+  StreamKey key;
+  cudaError_t e = stream_key(st, &key);
   if (e != cudaSuccess) return e;
+  const StreamHold hold(key);
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    const auto it = g_blocks.find(std::make_pair(dev, st));
+    const auto it = g_blocks.find(key);
     if (it != g_blocks.end()) word = it->second.words;
   }
   *status = kDevOk;

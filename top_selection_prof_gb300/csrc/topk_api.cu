@@ -43,16 +43,16 @@ struct Workspace {
   ScratchCounters counters;  // pick the alternating zero-kept regions (see the layout below)
 };
 std::mutex g_ws_mu;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+std::map<StreamKey, Workspace> g_ws;
 
 // Returns a device block of at least `bytes` for this (device, stream); grows
 // with stream-ordered allocation (the old block is released in stream order).
 cudaError_t workspace(cudaStream_t st, size_t bytes, void** out, ScratchCounters** counters = nullptr) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  StreamKey key;
+  cudaError_t e = stream_key(st, &key);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace& w = g_ws[std::make_pair(dev, st)];
+  Workspace& w = g_ws[key];
   if (w.bytes < bytes) {
     size_t grow = bytes + bytes / 4;
     grow = (grow + 0xFFFFF) & ~size_t(0xFFFFF);
@@ -88,13 +88,16 @@ cudaError_t acquire(const ScratchSource& src, cudaStream_t st, size_t bytes, voi
 
 // The device status word of the last call on each (device, stream), or null
 // when that call kept none; read back by topk_last_status.
-std::map<std::pair<int, cudaStream_t>, int*> g_last_status;
+std::map<StreamKey, int*> g_last_status;
 void record_status_word(cudaStream_t st, int* word) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return;
+  StreamKey key;
+  if (stream_key(st, &key) != cudaSuccess) return;
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  g_last_status[std::make_pair(dev, st)] = word;
+  g_last_status[key] = word;
 }
+
+std::mutex g_hold_mu;
+std::map<StreamKey, std::mutex> g_holds;  // (std::map nodes do not move)
 
 // Every workspace starts with the same prefix, whatever the call's layout:
 // the device header, two halves of the sample histograms, the fused
@@ -362,6 +365,9 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
     stats->t = plan.t;
     stats->M = plan.M;
   }
+  StreamKey key;
+  TK_TRY(stream_key(st, &key));
+  const StreamHold hold(key);
   // (a fixed block that is too small: nothing has been launched yet)
   auto scratch_status = [](cudaError_t e) { return e == kScratchTooSmall ? TOPK_EUNSUPPORTED : status_of(e); };
 
@@ -701,6 +707,23 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
 
 }  // namespace
 
+cudaError_t stream_key(cudaStream_t st, StreamKey* key) {
+  static std::atomic<uint64_t> threads{0};
+  static thread_local const uint64_t thread = ++threads;  // (never given twice, unlike a thread's id)
+  key->st = st;
+  key->thread = st == cudaStreamPerThread ? thread : 0;
+  return cudaGetDevice(&key->dev);
+}
+
+StreamHold::StreamHold(const StreamKey& key) {
+  std::mutex* mu;
+  {
+    std::lock_guard<std::mutex> lock(g_hold_mu);
+    mu = &g_holds[key];
+  }
+  lock_ = std::unique_lock<std::mutex>(*mu);
+}
+
 int select_with_fixed_scratch(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int largest,
                               double eps, void* out_vals, int64_t* out_idx, cudaStream_t st, bool global,
                               const FixedScratch& fs) {
@@ -951,12 +974,12 @@ int topk_tuning(topk_tuning_t* out) {
 
 int topk_last_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int dev = 0;
-  TK_TRY(cudaGetDevice(&dev));
+  StreamKey key;
+  TK_TRY(stream_key(st, &key));
   int* word = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_ws_mu);
-    auto it = g_last_status.find(std::make_pair(dev, st));
+    auto it = g_last_status.find(key);
     if (it != g_last_status.end()) word = it->second;
   }
   TK_TRY(cudaStreamSynchronize(st));
