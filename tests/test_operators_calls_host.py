@@ -7,6 +7,7 @@ import os
 import re
 import subprocess
 import threading
+import time
 
 import pytest
 
@@ -117,7 +118,8 @@ def test_scratch_grown_by_one_thread_is_not_another_calls(lib):
     chain = sum(e[0] == "launch" for e in events(lib))
     lib.fake_set_launch_us(300)
     small = threading.Thread(target=lambda: [linear(lib, inner=2048) for _ in range(8)])
-    large = threading.Thread(target=lambda: [linear(lib, rows=300 << i, inner=2048) for i in range(1, 6)])
+    # (out of step with the other's launches)
+    large = threading.Thread(target=lambda: [(time.sleep(0.0004), linear(lib, rows=300 << i, inner=2048)) for i in range(1, 6)])
     small.start(), large.start()
     small.join(), large.join()
     lib.fake_set_launch_us(0)
