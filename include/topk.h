@@ -343,9 +343,16 @@ int topk_select_noalloc(const void* x, int dtype, int64_t rows, int64_t n, int64
  *     result is rounded once, to nearest even.  Results do not depend on the
  *     order in which blocks run: the same call gives the same bits.
  *   - Outputs marked "nullable" are not computed when null.
- *   - Extents are below 2^31 and a selection's places below 2^29
- *     (EUNSUPPORTED beyond, and where a launch cannot count its blocks).  Scratch memory comes from
- *     a per-(device, stream) block of these operators, grown on demand.
+ *   - Extents are below 2^31 and a selection's places below 2^29 (EUNSUPPORTED
+ *     beyond, and where a launch cannot count its blocks).
+ *   - Scratch memory comes from a per-(device, stream) block of these
+ *     operators, apart from the selection's workspace but grown and held like
+ *     it.  A call on a stream that is being captured takes its scratch from the
+ *     graph instead (allocated, and released, where it stands in it), so that
+ *     graphs may be replayed on any stream, beside other calls.  A device wait
+ *     that gives up in a replay is told to topk_last_status of the stream that
+ *     was captured if topk_linear, topk_linear_backward or a norm ran on it
+ *     before that; otherwise it is not told.
  * ------------------------------------------------------------------------ */
 
 /* z, max(z, 0), z Phi(z) with the normal distribution function Phi, z / (1 + e^-z). */

@@ -50,3 +50,85 @@ def test_threads_on_one_stream(tk):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def operators(tk, s):
+    """Every operator that keeps scratch or words, on the tensors of s."""
+    y, pre = tk.linear(s["x"], s["w"], act="gelu", save_pre=True)
+    dx, dw, db = tk.linear_backward(s["dy"], s["x"], s["w"], pre=pre, act="gelu")
+    z = tk.decode(s["v"], s["i"], s["w"], s["x"].shape[0])
+    dv, dd, _ = tk.decode_backward(z, s["v"], s["i"], s["w"])
+    sx, sw, _ = tk.linear_backward_selected(dv, s["v"], s["i"], s["x"], s["w"])
+    few = tk.linear(s["x"][:3], s["w"])
+    norm = tk.grad_norm([dw, dd, sw] * 20)
+    return [y, pre, dx, dw, db, z, dv, dd, sx, sw, few, norm]
+
+
+def inputs(dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    rows, inner, outer = 300, 96, 2000
+    i = torch.randperm(rows * outer, generator=g)[:4000]
+    i[:300] = torch.arange(300) * outer + 7      # a long column
+    s = dict(x=(rows, inner), w=(outer, inner), dy=(rows, outer), v=(4000,))
+    return {**{k: torch.randn(z, generator=g).to(dtype).cuda() for k, z in s.items()}, "i": i.cuda()}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_captured_calls_replay(tk, dtype):
+    """A graph of the operators, captured before anything ran on its stream, gives what the calls give: with other inputs, after
+    an input that was not finite, beside another graph of the same stream and with calls in between that grow their scratch."""
+    s, other = inputs(dtype, 1), inputs(dtype, 2)
+    side = torch.cuda.Stream()
+    graphs = []
+    for state in (s, other):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            out = operators(tk, state)
+        graphs.append((g, out, state))
+    for seed in (3, 4, 5):
+        new = inputs(dtype, seed)
+        if seed == 4:
+            new["x"][5, 7] = torch.inf
+        for g, out, state in graphs:
+            for k in state:
+                state[k].copy_(new[k])
+            g.replay()
+        big = normals((700, 4096), dtype, seed), normals((600, 4096), dtype, seed + 1)
+        with torch.cuda.stream(side):
+            tk.linear(*big)
+        want = operators(tk, new)
+        torch.cuda.synchronize()
+        for _, out, _ in graphs:
+            for p, q in zip(out, want):
+                assert torch.equal(p.nan_to_num(7.0), q.nan_to_num(7.0)) and torch.equal(p.isnan(), q.isnan())
+
+
+def test_captured_product_takes_the_tensor_cores_again(tk):
+    """An input that is not finite sends an f32 product to the CUDA cores in the replays that see it, not in those after."""
+    x, w = normals((2048, 2048), torch.float32, 1), normals((2048, 2048), torch.float32, 2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(4):
+            y = tk.linear(x, w)
+
+    def time():
+        a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+        g.replay()
+        a.record()
+        for _ in range(5):
+            g.replay()
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b)
+
+    before = time()
+    first = y.clone()
+    keep = x[3, 3].clone()
+    x[3, 3] = torch.nan
+    g.replay()
+    torch.cuda.synchronize()
+    assert y[3].isnan().all() and y[4].isfinite().all()
+    x[3, 3] = keep
+    after = time()
+    assert torch.equal(y, first)     # (the CUDA cores' sums have other bits)
+    assert after < 3 * before

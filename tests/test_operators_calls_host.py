@@ -146,3 +146,25 @@ def test_threads_have_scratch_of_their_own_on_the_per_thread_stream(lib):
         t.start()
         t.join()
     assert len(made) == 2 and made[0] and made[1]
+
+
+@pytest.mark.parametrize("call", [linear, linear_backward, decode_backward, clip], ids=lambda c: c.__name__)
+@pytest.mark.parametrize("before", [False, True])
+def test_captured_calls_use_memory_of_their_graph(lib, call, before):
+    """Captured: scratch that is made and released in the graph, words at zero in each replay, and nothing of it kept."""
+    stream = 64
+    if before:
+        assert call(lib, stream=stream) == 0
+        outside = {e[4] for e in events(lib) if e[0] == "malloc"}
+    lib.fake_set_capturing(stream, 1)
+    for _ in range(2):
+        assert call(lib, stream=stream) == 0
+        log = [e for e in events(lib) if e[3] == stream]
+        made, freed = ([e[4] for e in log if e[0] == kind] for kind in ("malloc", "free"))
+        assert len(made) == 1 and made == freed
+        assert log[0][0] == "malloc" and log[-1][0] == "free"     # before the first launch, after the last
+    lib.fake_set_capturing(stream, 0)
+    assert call(lib, stream=stream) == 0
+    log = events(lib)
+    assert not any(e[0] == "free" for e in log)
+    assert any(e[0] == "malloc" for e in log) != before          # its own block, made outside the graph

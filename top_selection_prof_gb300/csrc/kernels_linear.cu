@@ -713,7 +713,7 @@ size_t product_scratch_bytes(const Product& g) {
   return mma_scratch_bytes(g);
 }
 
-cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st) {
+cudaError_t launch_product(const Product& g, Scratch& sc, const Words& words, cudaStream_t st) {
   const bool f32 = g.dtype == kF32;
   if (few_rows(g)) return f32 ? launch_few<float>(g, st) : launch_few<__nv_bfloat16>(g, st);
   if (few_outer(g)) return f32 ? launch_outer<float>(g, st) : launch_outer<__nv_bfloat16>(g, st);

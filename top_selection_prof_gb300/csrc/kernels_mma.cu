@@ -1056,11 +1056,11 @@ size_t mma_scratch_bytes(const Product& g) {
   return sc.used();
 }
 
-cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cudaStream_t st) {
+cudaError_t launch_mma(const Product& g, Scratch& sc, const Words& words, int call, cudaStream_t st) {
   MmaPlan q;
   if (!plan_mma(g, sc, &q)) return cudaErrorNotSupported;
   const bool f32 = g.dtype == kF32;
-  int* marks = words + kOpsMarks;
+  int* marks = words.at + kOpsMarks;
   cudaError_t e = cudaSuccess;
   if (f32) {
     Split a, b;
@@ -1103,8 +1103,8 @@ cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cuda
   p.marks = marks;
   p.call = call;
   p.part = q.part;
-  p.ticket = reinterpret_cast<unsigned*>(words) + 64;
-  p.status = words;
+  p.ticket = reinterpret_cast<unsigned*>(words.at) + 64;
+  p.status = words.status;
   const int size = f32 ? 4 : 2;
   p.tma_c = tma_rows(g.c, g.ldc, size);
   p.tma_pre = g.pre && tma_rows(g.pre, g.ldp, size);

@@ -470,10 +470,10 @@ size_t clip_scratch_bytes() {
   return sc.used();
 }
 
-cudaError_t launch_clip(const ClipTensor* list, int64_t num, bool scale, float max_norm, float* norm, int* words, Scratch& sc,
-                        cudaStream_t st) {
+cudaError_t launch_clip(const ClipTensor* list, int64_t num, bool scale, float max_norm, float* norm, const Words& words,
+                        Scratch& sc, cudaStream_t st) {
   NormScratch s = take_norm(sc);
-  s.ticket = reinterpret_cast<unsigned*>(words) + 32;
+  s.ticket = reinterpret_cast<unsigned*>(words.at) + 32;
   int64_t values = 0, tensors = 0;
   for (int64_t i = 0; i < num; ++i) {
     values += list[i].count;

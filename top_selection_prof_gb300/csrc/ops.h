@@ -32,13 +32,19 @@ class Scratch {
 // stream must have been synchronised): kDevOk or kDevTimeout.
 cudaError_t ops_take_status(cudaStream_t st, int* status);
 
-// Words that each (device, stream) keeps for the operators, zero at first: [0]
-// the status that a kernel sets when a wait runs out, [32] and [64..] tickets
-// that every kernel leaves at zero, [kOpsMarks..] what the operands of the tensor cores' products hold.
+// Words that each (device, stream) keeps for the operators, zero at first, as
+// those of a captured call are at each replay: [0] the status that a kernel sets
+// when a wait runs out, [32] and [64..] tickets that every kernel leaves at zero,
+// [kOpsMarks..] what the operands of the tensor cores' products hold.
 constexpr int64_t kOpsWords = 16384, kOpsMarks = 48;
 // Each mark is the number of the last call that found: a value that is not finite (or not as bf16), a value of a or of b
 // too small for parts (f32 only), a value of either too large to be scaled.
 enum : int { kMarkOther = 0, kMarkSmallA = 1, kMarkSmallB = 2, kMarkLarge = 3 };
+
+struct Words {
+  int* at = nullptr;      // kOpsWords
+  int* status = nullptr;  // where a wait that runs out is told
+};
 
 // SMs of the current device.
 int ops_sm_count();
@@ -71,11 +77,10 @@ struct Product {
   void* pre;             // nullable
   int64_t ldp;
 };
-// words: the stream's kOpsWords.
-cudaError_t launch_product(const Product& g, Scratch& sc, int* words, cudaStream_t st);
+cudaError_t launch_product(const Product& g, Scratch& sc, const Words& words, cudaStream_t st);
 size_t product_scratch_bytes(const Product& g);
 // The same on the tensor cores (kernels_mma.cu), or by launch_simt's kernel where the marks that `call` leaves say so.
-cudaError_t launch_mma(const Product& g, Scratch& sc, int* words, int call, cudaStream_t st);
+cudaError_t launch_mma(const Product& g, Scratch& sc, const Words& words, int call, cudaStream_t st);
 cudaError_t launch_simt(const Product& g, const int* marks, int call, cudaStream_t st);
 size_t mma_scratch_bytes(const Product& g);
 
@@ -151,7 +156,7 @@ struct ClipTensor {
 };
 size_t clip_scratch_bytes();
 // scale == false: the norm alone.
-cudaError_t launch_clip(const ClipTensor* t, int64_t num, bool scale, float max_norm, float* norm, int* words,
+cudaError_t launch_clip(const ClipTensor* t, int64_t num, bool scale, float max_norm, float* norm, const Words& words,
                         Scratch& sc, cudaStream_t st);
 
 }  // namespace tk

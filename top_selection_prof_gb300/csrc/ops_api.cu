@@ -28,6 +28,13 @@ int ops_sm_count() {
 
 namespace {
 
+// cudaErrorNotSupported: more blocks or tiles than a launch counts.
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return TOPK_OK;
+  cudaGetLastError();  // (reported here, not to the caller's next CUDA call)
+  return e == cudaErrorMemoryAllocation ? TOPK_ENOMEM : e == cudaErrorNotSupported ? TOPK_EUNSUPPORTED : TOPK_ECUDA;
+}
+
 // Scratch blocks of the operators, apart from the selection's (which keeps
 // words at zero between calls).  Grown with stream-ordered allocation, the old
 // block released in stream order, never shrunk.
@@ -39,24 +46,46 @@ struct Block {
 std::mutex g_mu;
 std::map<StreamKey, Block> g_blocks;
 
-// One call's use of its stream's block: the stream is held until the call's last launch is enqueued.
+// One call's use of its stream's block: the stream is held until the call's
+// last launch is enqueued.  A call that is captured into a graph has a block of
+// its own, made and released by the graph: the stream's block may be replaced
+// while the graph lives, and the graph may be replayed beside the stream's calls.
 class Call {
  public:
   explicit Call(cudaStream_t st) : st_(st), key_error_(stream_key(st, &key_)), hold_(key_) {}
-  cudaError_t scratch(size_t bytes, void** out, int** words = nullptr) {
+  cudaError_t scratch(size_t bytes, void** out, Words* words = nullptr) {
     if (key_error_ != cudaSuccess) return key_error_;
+    cudaStreamCaptureStatus capture;
+    const cudaError_t asked = cudaStreamIsCapturing(st_, &capture);
+    if (asked != cudaSuccess) return asked;
     std::unique_lock<std::mutex> lock(g_mu);
     Block& b = g_blocks[key_];  // (nodes do not move; this one is the holder's)
     lock.unlock();
     cudaError_t e = cudaSuccess;
+    if (capture != cudaStreamCaptureStatusNone) {
+      const size_t head = words ? sizeof(int) * kOpsWords : 0;
+      *out = nullptr;
+      if (!head && !bytes) return cudaSuccess;
+      e = cudaMallocAsync(&graph_, head + bytes, st_);
+      if (e != cudaSuccess) {
+        graph_ = nullptr;
+        return e;
+      }
+      *out = static_cast<char*>(graph_) + head;
+      if (!words) return cudaSuccess;
+      words->at = static_cast<int*>(graph_);
+      words->status = b.words ? b.words : words->at;  // (a word that topk_last_status finds, if there is one)
+      return cudaMemsetAsync(graph_, 0, head, st_);
+    }
     if (b.bytes < bytes) {
       const size_t grow = (bytes + bytes / 4 + 0xFFFFF) & ~size_t(0xFFFFF);
       void* p = nullptr;
       e = cudaMallocAsync(&p, grow, st_);
       if (e != cudaSuccess) return e;
-      if (b.ptr) cudaFreeAsync(b.ptr, st_);
+      if (b.ptr) e = cudaFreeAsync(b.ptr, st_);
       b.ptr = p;
       b.bytes = grow;
+      if (e != cudaSuccess) return e;
     }
     if (words && !b.words) {
       int* w = nullptr;
@@ -66,8 +95,16 @@ class Call {
       b.words = w;
     }
     *out = b.ptr;
-    if (words) *words = b.words;
+    if (words) *words = Words{b.words, b.words};
     return cudaSuccess;
+  }
+  // The status of a call whose launches gave e.
+  int end(cudaError_t e) {
+    if (graph_) {
+      const cudaError_t released = cudaFreeAsync(graph_, st_);
+      if (e == cudaSuccess) e = released;
+    }
+    return status_of(e);
   }
 
  private:
@@ -75,14 +112,8 @@ class Call {
   StreamKey key_;
   cudaError_t key_error_;
   StreamHold hold_;
+  void* graph_ = nullptr;
 };
-
-// cudaErrorNotSupported: more blocks or tiles than a launch counts.
-int status_of(cudaError_t e) {
-  if (e == cudaSuccess) return TOPK_OK;
-  cudaGetLastError();  // (reported here, not to the caller's next CUDA call)
-  return e == cudaErrorMemoryAllocation ? TOPK_ENOMEM : e == cudaErrorNotSupported ? TOPK_EUNSUPPORTED : TOPK_ECUDA;
-}
 
 // No exception leaves a C entry: the library's own containers can only run out of host memory.
 template <typename F>
@@ -109,12 +140,12 @@ int linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* b
   if (rows > kMaxExtent || inner > kMaxExtent || outer > kMaxExtent) return TOPK_EUNSUPPORTED;
   const Product g{{x, ldx, true}, {w, ldw, true}, rows, outer, inner, dtype, bias, residual, ldr, act, y, ldy, pre, ldp};
   void* base = nullptr;
-  int* words = nullptr;
+  Words words;
   Call call(st);
   cudaError_t e = call.scratch(product_scratch_bytes(g), &base, &words);
-  if (e != cudaSuccess) return status_of(e);
+  if (e != cudaSuccess) return call.end(e);
   Scratch sc(base);
-  return status_of(launch_product(g, sc, words, st));
+  return call.end(launch_product(g, sc, words, st));
 }
 
 int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre,
@@ -153,10 +184,10 @@ int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, co
   lay(plan);
   const size_t px = dx ? product_scratch_bytes(gx) : 0, pw = dw ? product_scratch_bytes(gw) : 0;
   void* base = nullptr;
-  int* words = nullptr;
+  Words words;
   Call call(st);
   cudaError_t e = call.scratch(plan.used() + (px > pw ? px : pw), &base, &words);
-  if (e != cudaSuccess) return status_of(e);
+  if (e != cudaSuccess) return call.end(e);
   Scratch sc(base);
   lay(sc);
   if (make_dz || dbias) e = launch_slope_sums(s, st);
@@ -168,7 +199,7 @@ int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, co
     Scratch own = sc;
     e = launch_product(gw, own, words, st);
   }
-  return status_of(e);
+  return call.end(e);
 }
 
 // Checks the places of a selection; TOPK_OK or the error.
@@ -205,7 +236,7 @@ int run_sums(const ColumnSums* cols, const RowSums* rws, const SlopeSums* sums_i
     sums.part = sc.take<float>(slope_sums_parts(sums.rows, sums.n) * sums.n);
     e = launch_slope_sums(sums, st);
   }
-  return status_of(e);
+  return call.end(e);
 }
 
 int clip(const void* const* grads, void* const* out, const int64_t* counts, const int* dtypes, int64_t num, bool scale,
@@ -219,12 +250,12 @@ int clip(const void* const* grads, void* const* out, const int64_t* counts, cons
     list[static_cast<size_t>(i)] = ClipTensor{grads[i], scale ? out[i] : nullptr, counts[i], dtypes[i]};
   }
   void* base = nullptr;
-  int* words = nullptr;
+  Words words;
   Call call(st);
   const cudaError_t e = call.scratch(clip_scratch_bytes(), &base, &words);
-  if (e != cudaSuccess) return status_of(e);
+  if (e != cudaSuccess) return call.end(e);
   Scratch sc(base);
-  return status_of(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, words, sc, st));
+  return call.end(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, words, sc, st));
 }
 
 }  // namespace
