@@ -33,6 +33,9 @@
  *     the stream's workspace until its last launch is enqueued); calls on
  *     different streams, and on the per-thread default streams of different
  *     threads, use different workspaces.
+ *     A call on a stream that is being captured takes its
+ *     workspace from the graph instead (allocated, and released, where it stands
+ *     in it); its status is not told to topk_last_status.
  *   - Errors are returned as topk_status_t codes; nothing is thrown across the
  *     ABI and no message is printed.
  */

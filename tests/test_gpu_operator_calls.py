@@ -132,3 +132,20 @@ def test_captured_product_takes_the_tensor_cores_again(tk):
     after = time()
     assert torch.equal(y, first)     # (the CUDA cores' sums have other bits)
     assert after < 3 * before
+
+
+# paths of the selection: the whole tensor (bins, grid refinement), one long row, rows by blocks, rows by clusters
+@pytest.mark.parametrize("rows,n,k,whole", [(512, 16384, 4096, True), (1, 1 << 22, 64, False), (300, 4096, 32, False),
+                                            (4, 100_000, 2000, False)])
+def test_captured_selection_replays(tk, rows, n, k, whole):
+    """A captured selection gives what the call gives, with other inputs, replay after replay."""
+    x = normals((rows, n), torch.float32, 1)
+    call = tk.select_global if whole else tk.select
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        v, i = call(x, k)
+    for seed in range(2, 7):
+        x.copy_(normals((rows, n), torch.float32, seed))
+        g.replay()
+        want = call(x, k)
+        assert torch.equal(v, want[0]) and torch.equal(i, want[1])

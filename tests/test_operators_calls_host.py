@@ -148,7 +148,7 @@ def test_threads_have_scratch_of_their_own_on_the_per_thread_stream(lib):
     assert len(made) == 2 and made[0] and made[1]
 
 
-@pytest.mark.parametrize("call", [linear, linear_backward, decode_backward, clip], ids=lambda c: c.__name__)
+@pytest.mark.parametrize("call", CALLS, ids=lambda c: c.__name__)
 @pytest.mark.parametrize("before", [False, True])
 def test_captured_calls_use_memory_of_their_graph(lib, call, before):
     """Captured: scratch that is made and released in the graph, words at zero in each replay, and nothing of it kept."""

@@ -45,12 +45,37 @@ struct Workspace {
 std::mutex g_ws_mu;
 std::map<StreamKey, Workspace> g_ws;
 
+// A captured call's workspace, made and released by the graph where the call
+// stands in it: the pooled block may be replaced while the graph lives, and a
+// replay always has the same alternating regions, which nothing cleared.
+struct GraphWorkspace {
+  cudaStream_t st;
+  void* ptr = nullptr;
+  ScratchCounters counters;
+  explicit GraphWorkspace(cudaStream_t s) : st(s) {}
+  ~GraphWorkspace() {
+    if (ptr) cudaFreeAsync(ptr, st);
+  }
+};
+size_t ws_prefix();
+
 // Returns a device block of at least `bytes` for this (device, stream); grows
 // with stream-ordered allocation (the old block is released in stream order).
-cudaError_t workspace(cudaStream_t st, size_t bytes, void** out, ScratchCounters** counters = nullptr) {
+cudaError_t workspace(cudaStream_t st, size_t bytes, void** out, ScratchCounters** counters, GraphWorkspace* graph) {
   StreamKey key;
   cudaError_t e = stream_key(st, &key);
   if (e != cudaSuccess) return e;
+  cudaStreamCaptureStatus capture;
+  e = cudaStreamIsCapturing(st, &capture);
+  if (e != cudaSuccess) return e;
+  if (capture != cudaStreamCaptureStatusNone) {
+    e = cudaMallocAsync(&graph->ptr, bytes, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(graph->ptr, 0, ws_prefix(), st);
+    else graph->ptr = nullptr;
+    *out = graph->ptr;
+    if (counters) *counters = &graph->counters;
+    return e;
+  }
   std::lock_guard<std::mutex> lock(g_ws_mu);
   Workspace& w = g_ws[key];
   if (w.bytes < bytes) {
@@ -77,9 +102,9 @@ struct ScratchSource {
 };
 constexpr cudaError_t kScratchTooSmall = cudaErrorInvalidValue;  // (mapped to TOPK_EUNSUPPORTED)
 
-cudaError_t acquire(const ScratchSource& src, cudaStream_t st, size_t bytes, void** out,
+cudaError_t acquire(const ScratchSource& src, cudaStream_t st, size_t bytes, void** out, GraphWorkspace* graph,
                     ScratchCounters** counters = nullptr) {
-  if (!src.fixed) return workspace(st, bytes, out, counters);
+  if (!src.fixed) return workspace(st, bytes, out, counters, graph);
   if (bytes > src.fixed->bytes) return kScratchTooSmall;
   *out = src.fixed->base;
   if (counters) *counters = src.fixed->counters;
@@ -87,7 +112,7 @@ cudaError_t acquire(const ScratchSource& src, cudaStream_t st, size_t bytes, voi
 }
 
 // The device status word of the last call on each (device, stream), or null
-// when that call kept none; read back by topk_last_status.
+// when that call kept none (or its graph did); read back by topk_last_status.
 std::map<StreamKey, int*> g_last_status;
 void record_status_word(cudaStream_t st, int* word) {
   StreamKey key;
@@ -368,6 +393,7 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
   StreamKey key;
   TK_TRY(stream_key(st, &key));
   const StreamHold hold(key);
+  GraphWorkspace graph(st);
   // (a fixed block that is too small: nothing has been launched yet)
   auto scratch_status = [](cudaError_t e) { return e == kScratchTooSmall ? TOPK_EUNSUPPORTED : status_of(e); };
 
@@ -378,13 +404,13 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
     int* status = nullptr;
     if (stats) {
       void* ws = nullptr;
-      const cudaError_t e = acquire(src, st, ws_prefix(), &ws);
+      const cudaError_t e = acquire(src, st, ws_prefix(), &ws, &graph);
       if (e != cudaSuccess) return scratch_status(e);
       status = &static_cast<DevHeader*>(ws)->status;
       TK_TRY(cudaMemsetAsync(status, 0, sizeof(int), st));
     }
     TK_TRY(launch_rows(p, k, out_vals, out_idx, status, st));
-    record_status_word(st, status);
+    record_status_word(st, graph.ptr ? nullptr : status);
     if (stats) {
       stats->launches = 1;
       stats->cluster = 1;
@@ -399,7 +425,7 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
   if (plan.path == TOPK_PATH_DIRECT) {
     // the status word and the sort's exchange buffer
     void* ws = nullptr;
-    const cudaError_t e = acquire(src, st, ws_prefix() + sizeof(uint64_t) * p.nsel * k, &ws);
+    const cudaError_t e = acquire(src, st, ws_prefix() + sizeof(uint64_t) * p.nsel * k, &ws, &graph);
     if (e != cudaSuccess) return scratch_status(e);
     DevHeader* hdr = static_cast<DevHeader*>(ws);
     TK_TRY(cudaMemsetAsync(&hdr->status, 0, sizeof(int), st));
@@ -414,7 +440,7 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
     int nl = 0;
     job.launch_count = &nl;
     TK_TRY(launch_select(p, job, p.len, &cluster, st));
-    record_status_word(st, &hdr->status);
+    record_status_word(st, graph.ptr ? nullptr : &hdr->status);
     if (stats) {
       stats->launches = nl;
       stats->cluster = cluster;
@@ -478,7 +504,7 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
   void* ws = nullptr;
   ScratchCounters* wcnt = nullptr;
   {
-    const cudaError_t e = acquire(src, st, off, &ws, &wcnt);
+    const cudaError_t e = acquire(src, st, off, &ws, &graph, &wcnt);
     if (e != cudaSuccess) return scratch_status(e);
   }
   char* base = static_cast<char*>(ws);
@@ -680,7 +706,7 @@ int run(const void* x, int dtype, int64_t rows, int64_t n, int64_t k, int larges
 #endif
   }
   if (plan.path == TOPK_PATH_PROFK) TK_TRY(mark(5));
-  record_status_word(st, &hdr->status);
+  record_status_word(st, graph.ptr ? nullptr : &hdr->status);
 
   if (stats) {
     DevHeader h;
