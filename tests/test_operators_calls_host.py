@@ -168,3 +168,18 @@ def test_captured_calls_use_memory_of_their_graph(lib, call, before):
     log = events(lib)
     assert not any(e[0] == "free" for e in log)
     assert any(e[0] == "malloc" for e in log) != before          # its own block, made outside the graph
+
+
+@pytest.mark.parametrize("call", [linear, linear_backward, decode_backward, clip], ids=lambda c: c.__name__)
+def test_a_second_device_is_set_up_like_the_first(lib, call):
+    """What a kernel needs before its launch (its shared memory) belongs to a device, not to the process."""
+    launches = []
+    for device in (0, 1, 0):
+        lib.fake_set_device(device)
+        for dtype in (F32, BF16) if call is not clip else (None,):
+            assert (call(lib) if call is clip else call(lib, dtype=dtype)) == 0
+        log = events(lib)
+        assert {e[2] for e in log} == {device}
+        launches.append([e[4] for e in log if e[0] == "launch"])
+    assert launches[0] == launches[1] == launches[2]
+    lib.fake_set_device(0)

@@ -428,7 +428,9 @@ template <int N>
 cudaError_t launch_many(const ClipTensor* list, int64_t num, bool scale, float max_norm, float* norm, const NormScratch& s,
                         cudaStream_t st) {
   // as many blocks as fit at once, so that they end near the same time
-  static int each = 0;
+  static PerDevice fits;
+  std::atomic<int>* known = fits.here();
+  int each = known ? known->load() : 0;
   if (!each) {
     int a = 0, b = 0;
     cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a, squares_kernel<N>, kThreads, 0);
@@ -436,6 +438,7 @@ cudaError_t launch_many(const ClipTensor* list, int64_t num, bool scale, float m
     if (e != cudaSuccess) return e;
     a = a < b ? a : b;
     each = a < 1 ? 1 : a;
+    if (known) *known = each;
   }
   const int64_t fit = int64_t(each) * ops_sm_count(), most = fit < kMaxBlocks ? fit : kMaxBlocks;
   TensorTable<N> t;

@@ -1042,13 +1042,16 @@ cudaError_t launch_columns_d(const ColParams& q, cudaStream_t st) {
   using Stream = ColumnStream<T, VEC, CHUNKS, FULL, DOTS>;
   auto kernel = column_sums_kernel<T, VEC, CHUNKS, FULL, DOTS>;
   constexpr int kSmem = kColWarps * Stream::kSlots * Stream::kSlotBytes;
-  static int each = 0;  // blocks that fit an SM
+  static PerDevice fits;  // blocks that fit an SM (the attribute, too, is the device's)
+  std::atomic<int>* known = fits.here();
+  int each = known ? known->load() : 0;
   if (!each) {
     int n = 0;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kColWarps * 32, kSmem);
     if (e != cudaSuccess) return e;
     each = n < 1 ? 1 : n;
+    if (known) *known = each;
   }
   const int64_t blocks = (q.g.max_pieces + q.g.max_tasks + kColWarps - 1) / kColWarps, fit = int64_t(each) * ops_sm_count();
   return launch_after(kernel, static_cast<unsigned>(blocks < fit ? blocks : fit), kColWarps * 32, kSmem, st, q);

@@ -3,6 +3,7 @@
 // declarations shared by their C entries (ops_api.cu) and their kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -44,6 +45,20 @@ enum : int { kMarkOther = 0, kMarkSmallA = 1, kMarkSmallB = 2, kMarkLarge = 3 };
 struct Words {
   int* at = nullptr;      // kOpsWords
   int* status = nullptr;  // where a wait that runs out is told
+};
+
+// A number found once for each device (0: not yet).
+class PerDevice {
+ public:
+  // The current device's number; null when there is no telling it apart.
+  std::atomic<int>* here() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMost ? &of_[dev] : nullptr;
+  }
+
+ private:
+  static constexpr int kMost = 64;
+  std::atomic<int> of_[kMost] = {};
 };
 
 // SMs of the current device.

@@ -16,14 +16,13 @@
 namespace tk {
 
 int ops_sm_count() {
-  static int sms[64] = {};
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  if (!sms[dev]) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    sms[dev] = v;
-  }
-  return sms[dev];
+  static PerDevice sms;
+  std::atomic<int>* n = sms.here();
+  int dev = 0, v = n ? n->load() : 0;
+  if (v) return v;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+  if (n) *n = v;
+  return v;
 }
 
 namespace {
