@@ -346,6 +346,9 @@ int topk_select_noalloc(const void* x, int dtype, int64_t rows, int64_t n, int64
  *     result is rounded once, to nearest even.  Results do not depend on the
  *     order in which blocks run: the same call gives the same bits.
  *   - Outputs marked "nullable" are not computed when null.
+ *   - Outputs overlap neither inputs nor each other (EINVAL; views of one
+ *     buffer may lie between each other when their rows are equally far apart),
+ *     except where an entry point says so.
  *   - Extents are below 2^31 and a selection's places below 2^29 (EUNSUPPORTED
  *     beyond, and where a launch cannot count its blocks).
  *   - Scratch memory comes from a per-(device, stream) block of these

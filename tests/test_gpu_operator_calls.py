@@ -149,3 +149,15 @@ def test_captured_selection_replays(tk, rows, n, k, whole):
         g.replay()
         want = call(x, k)
         assert torch.equal(v, want[0]) and torch.equal(i, want[1])
+
+
+def test_results_over_their_inputs_are_refused(tk):
+    x, w = torch.ones(50, 64, device="cuda"), torch.ones(64, 64, device="cuda")
+    both = torch.ones(50, 128, device="cuda")
+    for call in (lambda: tk.linear(x, w, out=x), lambda: tk.linear(x, w, out=w[:50]),
+                 lambda: tk.linear(x, w, residual=both[:, :64], out=both[:, 32:96])):
+        with pytest.raises(tk.TopkError) as err:
+            call()
+        assert err.value.status == -1
+    assert torch.equal(tk.linear(both[:, :64], w, out=both[:, 64:]), torch.full((50, 64), 64.0, device="cuda"))
+    assert torch.equal(both[:, :64], x) and torch.equal(w, torch.ones_like(w))

@@ -183,3 +183,64 @@ def test_a_second_device_is_set_up_like_the_first(lib, call):
         launches.append([e[4] for e in log if e[0] == "launch"])
     assert launches[0] == launches[1] == launches[2]
     lib.fake_set_device(0)
+
+
+def span(p, rows, cols, ld):
+    return {p + r * ld + c for r in range(rows) for c in range(cols)}
+
+
+def test_outputs_that_overlap_are_refused(lib):
+    """linear's y and the other tensors at every place of a small buffer, against the sets of bytes they have."""
+    base, rows, inner, outer = 1 << 20, 3, 2, 2
+    seen = set()
+    for ldx in (2, 5):
+        for ldy in (2, 5):
+            for shift in range(-16, 17):
+                x = span(base, rows, 4 * inner, 4 * ldx)
+                y = span(base + 4 * shift, rows, 4 * outer, 4 * ldy)
+                rc = lib.topk_linear(base, ldx, at(1), inner, None, None, 0, F32, rows, inner, outer, 0, base + 4 * shift, ldy, None,
+                                     0, None)
+                # (rows of unequal distance: any two ranges that meet)
+                met = bool(x & y) if ldx == ldy else max(x) >= min(y) and max(y) >= min(x)
+                assert rc == (-1 if met else 0), (ldx, ldy, shift)
+                seen.add((ldx == ldy, met))
+    assert len(seen) == 4
+    b = at(0).value
+    for refused, kw in ((True, dict(y=b)), (True, dict(y=b + 64)), (False, dict(r=at(2).value)), (True, dict(r=at(2).value + 4)),
+                        (True, dict(r=at(2).value, ldr=600)), (True, dict(pre=at(2).value)), (True, dict(pre=b)),
+                        (True, dict(r=at(3).value, pre=at(3).value)), (True, dict(bias=at(2).value + 400)), (False, dict(pre=at(3).value)),
+                        (True, dict(y=at(1).value - 4))):
+        a = dict(bias=None, r=None, ldr=512, y=at(2).value, pre=None)
+        a.update(kw)
+        rc = lib.topk_linear(b, 64, at(1), 64, a["bias"], a["r"], a["ldr"], F32, 300, 64, 512, 0, a["y"], 512, a["pre"], 512, None)
+        assert rc == (-1 if refused else 0), kw
+
+
+@pytest.mark.parametrize("i,j", [(4, 0), (4, 2), (4, 3), (5, 1), (6, 0), (5, 4), (6, 5)])
+def test_gradients_that_overlap_are_refused(lib, i, j):
+    p = [at(k).value for k in range(7)]
+    call = lambda: lib.topk_linear_backward(p[0], 512, p[1], 64, p[2], 64, p[3], 512, BF16, 300, 64, 512, 3, p[4], p[5], p[6], None)  # noqa: E731
+    assert call() == 0
+    p[i] = p[j] + 16
+    assert call() == -1
+
+
+def test_selections_and_norms_that_overlap_are_refused(lib):
+    def decode_(y):
+        return lib.topk_decode(at(0), at(1), 5, 0, at(2), 8, at(3), F32, 4, 6, 8, y, None)
+
+    def back(dvals, dw):
+        return lib.topk_decode_backward(at(0), 8, at(1), at(2), 5, 0, at(3), 8, F32, 4, 6, 8, dvals, dw, at(6), None)
+
+    def selected(dx, db):
+        return lib.topk_linear_backward_selected(at(0), at(1), at(2), 5, 0, at(3), 8, at(4), 8, F32, 4, 8, 6, 1, dx, at(6), db, None)
+
+    def clip_(src, dst):
+        one = (VP * 1)(src), (VP * 1)(dst), (ctypes.c_int64 * 1)(100), (ctypes.c_int * 1)(F32)
+        return lib.topk_clip_grad_norm(*one, 1, 1.0, at(2), None)
+
+    assert decode_(at(4)) == 0 and back(at(4), at(5)) == 0 and selected(at(5), at(7)) == 0
+    assert all(decode_(at(i)) == -1 for i in range(4))
+    assert all(back(at(i), at(5)) == -1 and back(at(5), at(i)) == -1 for i in (0, 1, 2, 3, 6) if i != 1) and back(at(4), at(4)) == -1
+    assert all(selected(at(i), at(7)) == -1 and selected(at(5), at(i)) == -1 for i in (0, 1, 2, 3, 4, 6))
+    assert clip_(1 << 20, 1 << 20) == 0 and clip_(1 << 20, (1 << 20) + 400) == 0 and clip_(1 << 20, (1 << 20) + 396) == -1

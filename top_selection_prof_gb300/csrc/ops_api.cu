@@ -3,9 +3,11 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "../../include/topk.h"
@@ -129,6 +131,37 @@ bool known_act(int act) { return act >= TOPK_ACT_NONE && act <= TOPK_ACT_SILU; }
 constexpr int64_t kMaxExtent = INT32_MAX;
 size_t value_bytes(int dtype) { return dtype == TOPK_F32 ? 4 : 2; }
 
+// Where a matrix lies: `rows` runs of `row` bytes, `ld` bytes from one to the next.  At null: none.
+struct Span {
+  uintptr_t at;
+  int64_t rows, row, ld;
+};
+Span matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+  return {reinterpret_cast<uintptr_t>(p), rows, cols * size, ld * size};
+}
+Span vector(const void* p, int64_t n, int64_t size) { return matrix(p, 1, n, n, size); }
+// Whether two matrices have a byte in common; those whose rows lie differently far apart count as having one wherever their
+// ranges meet.
+bool meet(Span a, Span b) {
+  if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.row < 1 || b.row < 1) return false;
+  if (b.at < a.at) std::swap(a, b);
+  if (b.at - a.at >= static_cast<uintptr_t>((a.rows - 1) * a.ld + a.row)) return false;
+  if (a.rows > 1 && b.rows > 1 && a.ld != b.ld) return true;
+  // b begins in a run of a, or, where a has another run, in the gap before it
+  const int64_t ld = a.rows > 1 ? a.ld : b.ld, d = static_cast<int64_t>((b.at - a.at) % static_cast<uintptr_t>(ld));
+  return a.rows == 1 || d < a.row || d + b.row > ld;
+}
+// Whether an output has a byte in common with an input or another output.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meet(*o, i)) return true;
+    for (auto p = outs.begin(); p != o; ++p)
+      if (meet(*o, *p)) return true;
+  }
+  return false;
+}
+
 int linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* residual, int64_t ldr,
            int dtype, int64_t rows, int64_t inner, int64_t outer, int act, void* y, int64_t ldy, void* pre, int64_t ldp,
            cudaStream_t st) {
@@ -137,6 +170,14 @@ int linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* b
   if (!x || !w || !y || ldx < inner || ldw < inner || ldy < outer) return TOPK_EINVAL;
   if ((residual && ldr < outer) || (pre && ldp < outer)) return TOPK_EINVAL;
   if (rows > kMaxExtent || inner > kMaxExtent || outer > kMaxExtent) return TOPK_EUNSUPPORTED;
+  const int64_t size = static_cast<int64_t>(value_bytes(dtype));
+  const Span my = matrix(y, rows, outer, ldy, size), mr = matrix(residual, rows, outer, ldr, size);
+  // (in place: each value of the residual is read where its result is then written)
+  const bool in_place = my.at == mr.at && (my.ld == mr.ld || rows == 1);
+  if (clash({my, matrix(pre, rows, outer, ldp, size)},
+            {matrix(x, rows, inner, ldx, size), matrix(w, outer, inner, ldw, size), vector(bias, outer, size)}) ||
+      (!in_place && meet(my, mr)) || meet(matrix(pre, rows, outer, ldp, size), mr))
+    return TOPK_EINVAL;
   const Product g{{x, ldx, true}, {w, ldw, true}, rows, outer, inner, dtype, bias, residual, ldr, act, y, ldy, pre, ldp};
   void* base = nullptr;
   Words words;
@@ -161,6 +202,11 @@ int linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, co
   }
   if (!dy || lddy < outer || (dw && (!x || ldx < inner)) || (dx && (!w || ldw < inner))) return TOPK_EINVAL;
   if (act != TOPK_ACT_NONE && (!pre || ldp < outer)) return TOPK_EINVAL;
+  const int64_t size = static_cast<int64_t>(value_bytes(dtype));
+  if (clash({vector(dx, rows * inner, size), vector(dw, outer * inner, size), vector(dbias, outer, size)},
+            {matrix(dy, rows, outer, lddy, size), matrix(act != TOPK_ACT_NONE ? pre : nullptr, rows, outer, ldp, size),
+             matrix(dw ? x : nullptr, rows, inner, ldx, size), matrix(dx ? w : nullptr, outer, inner, ldw, size)}))
+    return TOPK_EINVAL;
   SlopeSums s{dy, lddy, pre, ldp, dtype, rows, outer, act, nullptr, 0, 0, dbias, nullptr};
   const bool make_dz = act != TOPK_ACT_NONE && (dx || dw);
   // bf16: a smooth activation's dz has more bits than bf16 holds; a second array keeps eight more (half the error of the
@@ -246,6 +292,8 @@ int clip(const void* const* grads, void* const* out, const int64_t* counts, cons
   for (int64_t i = 0; i < num; ++i) {
     if (counts[i] < 0 || !known_dtype(dtypes[i]) || (counts[i] > 0 && (!grads[i] || (scale && !out[i])))) return TOPK_EINVAL;
     if (counts[i] > (int64_t(1) << 44)) return TOPK_EUNSUPPORTED;
+    const int64_t size = static_cast<int64_t>(value_bytes(dtypes[i]));
+    if (scale && grads[i] != out[i] && meet(vector(grads[i], counts[i], size), vector(out[i], counts[i], size))) return TOPK_EINVAL;
     list[static_cast<size_t>(i)] = ClipTensor{grads[i], scale ? out[i] : nullptr, counts[i], dtypes[i]};
   }
   void* base = nullptr;
@@ -310,6 +358,12 @@ int topk_linear_backward_selected(const void* dvals, const void* vals, const int
     const Places p{idx, count, per_row != 0, rows, outer, per_row ? rows * count : count};
     if (p.total > 0 && (!dvals || (act == TOPK_ACT_RELU && !vals))) return TOPK_EINVAL;
     if ((dw && rows > 0 && (!x || ldx < inner)) || (dx && (!w || ldw < inner))) return TOPK_EINVAL;
+    const int64_t size = static_cast<int64_t>(value_bytes(dtype));
+    if (clash({vector(dx, rows * inner, size), vector(dw, outer * inner, size), vector(dbias, outer, size)},
+              {vector(dvals, p.total, size), vector(act == TOPK_ACT_RELU ? vals : nullptr, p.total, size),
+               vector(idx, p.total, sizeof(int64_t)), matrix(dw ? x : nullptr, rows, inner, ldx, size),
+               matrix(dx ? w : nullptr, outer, inner, ldw, size)}))
+      return TOPK_EINVAL;
     const Coef coef{dvals, act == TOPK_ACT_RELU ? vals : nullptr};
     const ColumnSums c{p, coef, dtype, x, ldx, inner, nullptr, 0, dw, dbias, nullptr};
     const RowSums r{p, coef, dtype, w, ldw, inner, nullptr, dx};
@@ -324,6 +378,10 @@ int topk_decode(const void* vals, const int64_t* idx, int64_t count, int per_row
     if (rows == 0) return TOPK_OK;
     const Places p{idx, count, per_row != 0, rows, n, per_row ? rows * count : count};
     if (!y || !w || ldw < d || (p.total > 0 && !vals)) return TOPK_EINVAL;
+    const int64_t size = static_cast<int64_t>(value_bytes(dtype));
+    if (clash({vector(y, rows * d, size)}, {vector(vals, p.total, size), vector(idx, p.total, sizeof(int64_t)),
+                                            matrix(w, n, d, ldw, size), vector(bias, d, size)}))
+      return TOPK_EINVAL;
     const RowSums r{p, Coef{vals, nullptr}, dtype, w, ldw, d, bias, y};
     return run_sums(nullptr, &r, nullptr, static_cast<cudaStream_t>(stream));
   });
@@ -337,6 +395,11 @@ int topk_decode_backward(const void* dy, int64_t lddy, const void* vals, const i
     const Places p{idx, count, per_row != 0, rows, n, per_row ? rows * count : count};
     if (rows > 0 && (dvals || dw || dbias) && (!dy || lddy < d)) return TOPK_EINVAL;
     if (p.total > 0 && ((dw && !vals) || (dvals && (!w || ldw < d)))) return TOPK_EINVAL;
+    const int64_t size = static_cast<int64_t>(value_bytes(dtype));
+    if (clash({vector(dvals, p.total, size), vector(dw, n * d, size), vector(dbias, d, size)},
+              {matrix(dy, rows, d, lddy, size), vector(dw ? vals : nullptr, p.total, size), vector(idx, p.total, sizeof(int64_t)),
+               matrix(dvals ? w : nullptr, n, d, ldw, size)}))
+      return TOPK_EINVAL;
     if (rows == 0) {  // sums over no rows
       cudaStream_t st = static_cast<cudaStream_t>(stream);
       cudaError_t e = cudaSuccess;
