@@ -161,3 +161,47 @@ def test_results_over_their_inputs_are_refused(tk):
         assert err.value.status == -1
     assert torch.equal(tk.linear(both[:, :64], w, out=both[:, 64:]), torch.full((50, 64), 64.0, device="cuda"))
     assert torch.equal(both[:, :64], x) and torch.equal(w, torch.ones_like(w))
+
+
+LONG = 100_000_000   # cycles, some 50 ms
+
+
+def test_outputs_on_another_stream_do_not_take_memory_in_use(tk):
+    """An output written by a side stream at once is not in memory that the current stream still has to read."""
+    side = torch.cuda.Stream()
+    x, w = torch.ones(300, 64, device="cuda"), torch.ones(512, 64, device="cuda")
+    v, i = torch.ones(900, device="cuda"), torch.arange(900, device="cuda") * 7
+    torch.cuda.synchronize()
+    calls = {(300, 512): lambda: tk.linear(x, w, stream=side), (300, 64): lambda: tk.decode(v, i, w, 300, stream=side),
+             (512, 64): lambda: tk.decode_backward(x, v, i, w, stream=side)[1], (4096,): lambda: tk.select_global(x, 4096, stream=side)[0]}
+    for shape, call in calls.items():
+        t = torch.full(shape, 5.0, device="cuda")
+        torch.cuda._sleep(LONG)
+        keep = t.clone()       # waits for the sleep
+        del t                  # its memory goes back to the current stream's pool
+        out = call()
+        torch.cuda.synchronize()
+        assert out.shape == shape and bool((keep == 5.0).all())
+
+
+def test_outputs_and_inputs_live_as_long_as_both_streams_use_them(tk):
+    side = torch.cuda.Stream()
+    w = torch.ones(512, 64, device="cuda")
+    x = torch.ones(300, 64, device="cuda")
+    torch.cuda.synchronize()
+    y = tk.linear(x, w, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(LONG)
+    keep = y.clone()           # on the current stream, later
+    del y
+    again = [tk.linear(x, w[:512], bias=w[:, 0].contiguous(), stream=side) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert bool((keep == 64.0).all()) and all(bool((a == 65.0).all()) for a in again)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(LONG)
+    y = tk.linear(x, w, stream=side)     # reads x after the sleep
+    v, _ = tk.select_global(x, 100, stream=side)
+    del x
+    other = [torch.full((300, 64), 9.0, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert bool((y == 64.0).all()) and bool((v == 1.0).all()) and len(other) == 3

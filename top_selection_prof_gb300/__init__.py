@@ -81,8 +81,10 @@ def _run(x, k, largest, eps, global_, opt, want_stats, stream):
     code = _dtype_code(x2)
     out_shape = (k,) if global_ else (rows, k)
     with torch.cuda.device(x2.device):
-        vals = torch.empty(out_shape, dtype=x2.dtype, device=x2.device)
-        idx = torch.empty(out_shape, dtype=torch.int64, device=x2.device)
+        vals = _empty(out_shape, x2.dtype, x2.device, stream)
+        idx = _empty(out_shape, torch.int64, x2.device, stream)
+        if stream is not None:
+            x2.record_stream(stream)
         st = _lib.TopkStats() if want_stats else None
         lib = _lib.get()
         sp = _stream_ptr(x2, stream)
@@ -173,5 +175,5 @@ def prof_filter(x, tau, M: int, global_: bool = False, largest: bool = True, str
     return buf, counts
 
 
-from .operators import (clip_grad_norm, clip_grad_norm_, decode, decode_backward, grad_norm, linear,  # noqa: E402
+from .operators import (_empty, clip_grad_norm, clip_grad_norm_, decode, decode_backward, grad_norm, linear,  # noqa: E402
                         linear_backward, linear_backward_selected)

@@ -11,6 +11,12 @@ As for the selection, every step runs in the library's CUDA kernels; this
 module checks tensors, allocates outputs and passes pointers and the stream.
 Inputs are float32 or bfloat16 CUDA tensors, all of one dtype and device in a
 call; matrices may be strided by row, with their last dimension contiguous.
+
+stream=: the stream that a call runs on, the current one by default.  As with
+torch's own streams the caller orders another one (wait_stream) after what makes
+the inputs and before what uses the outputs; their memory is kept for both
+streams.  Nothing is recorded for autograd: outputs never require gradients, and
+the *_backward functions are what an autograd.Function calls.
 """
 from __future__ import annotations
 
@@ -68,6 +74,17 @@ def _vector(t, dtype, device, n, name):
     return t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream):
+    """An output: memory of the stream that writes it (the current one may still read what memory of its own held), kept
+    until the current one, too, has done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 _FUNCTIONS = {}
 
 
@@ -112,11 +129,11 @@ def linear(x, w, bias=None, act: str = "none", residual=None, save_pre: bool = F
         _like(residual, dtype, device, "residual")
         pr, ldr = residual.data_ptr(), _matrix(residual, rows, outer, "residual")
     if out is None:
-        out, ldy = torch.empty((rows, outer), dtype=dtype, device=device), outer
+        out, ldy = _empty((rows, outer), dtype, device, stream), outer
     else:
         _like(out, dtype, device, "out")
         ldy = _matrix(out, rows, outer, "out")
-    pre = torch.empty((rows, outer), dtype=dtype, device=device) if save_pre else None
+    pre = _empty((rows, outer), dtype, device, stream) if save_pre else None
     _call("topk_linear", device, stream, (x, w, bias, residual, out, pre), x.data_ptr(), ldx, w.data_ptr(), ldw, pb, pr,
           ldr, code, rows, inner, outer, _act(act), out.data_ptr(), ldy, pre.data_ptr() if save_pre else None, outer)
     return (out, pre) if save_pre else out
@@ -145,9 +162,9 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", need=(True, True, Tru
         ldp = _matrix(pre, rows, outer, "pre")
     else:
         pre = None
-    dx = torch.empty((rows, inner), dtype=dtype, device=device) if need[0] else None
-    dw = torch.empty((outer, inner), dtype=dtype, device=device) if need[1] else None
-    db = torch.empty((outer,), dtype=dtype, device=device) if need[2] else None
+    dx = _empty((rows, inner), dtype, device, stream) if need[0] else None
+    dw = _empty((outer, inner), dtype, device, stream) if need[1] else None
+    db = _empty((outer,), dtype, device, stream) if need[2] else None
     _call("topk_linear_backward", device, stream, (dy, x, w, pre, dx, dw, db), dy.data_ptr(), lddy, x.data_ptr(), ldx,
           w.data_ptr(), ldw, None if pre is None else pre.data_ptr(), ldp, code, rows, inner, outer, a,
           None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
@@ -190,9 +207,9 @@ def linear_backward_selected(dvals, vals, idx, x, w, act: str = "relu", need=(Tr
     ldx, ldw = _matrix(x, rows, inner, "x"), _matrix(w, outer, inner, "w")
     count, per_row = _places(idx, rows, device)
     pd, pv = _of_places(dvals, idx, dtype, device, "dvals"), _of_places(vals, idx, dtype, device, "vals")
-    dx = torch.empty((rows, inner), dtype=dtype, device=device) if need[0] else None
-    dw = torch.empty((outer, inner), dtype=dtype, device=device) if need[1] else None
-    db = torch.empty((outer,), dtype=dtype, device=device) if need[2] else None
+    dx = _empty((rows, inner), dtype, device, stream) if need[0] else None
+    dw = _empty((outer, inner), dtype, device, stream) if need[1] else None
+    db = _empty((outer,), dtype, device, stream) if need[2] else None
     _call("topk_linear_backward_selected", device, stream, (dvals, vals, idx, x, w, dx, dw, db), pd, pv,
           idx.data_ptr(), count, per_row, x.data_ptr(), ldx, w.data_ptr(), ldw, code, rows, inner, outer, _act(act),
           None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
@@ -211,7 +228,7 @@ def decode(vals, idx, w, rows: int, bias=None, stream=None):
     count, per_row = _places(idx, rows, device)
     pv = _of_places(vals, idx, dtype, device, "vals")
     pb = None if bias is None else _vector(bias, dtype, device, d, "bias")
-    y = torch.empty((rows, d), dtype=dtype, device=device)
+    y = _empty((rows, d), dtype, device, stream)
     _call("topk_decode", device, stream, (vals, idx, w, bias, y), pv, idx.data_ptr(), count, per_row, w.data_ptr(), ldw,
           pb, code, rows, n, d, y.data_ptr())
     return y
@@ -229,9 +246,9 @@ def decode_backward(dy, vals, idx, w, need=(True, True, True), stream=None):
     lddy, ldw = _matrix(dy, rows, d, "dy"), _matrix(w, n, d, "w")
     count, per_row = _places(idx, rows, device)
     pv = _of_places(vals, idx, dtype, device, "vals")
-    dv = torch.empty_like(vals) if need[0] else None
-    dw = torch.empty((n, d), dtype=dtype, device=device) if need[1] else None
-    db = torch.empty((d,), dtype=dtype, device=device) if need[2] else None
+    dv = _empty(vals.shape, dtype, device, stream) if need[0] else None
+    dw = _empty((n, d), dtype, device, stream) if need[1] else None
+    db = _empty((d,), dtype, device, stream) if need[2] else None
     _call("topk_decode_backward", device, stream, (dy, vals, idx, w, dv, dw, db), dy.data_ptr(), lddy, pv,
           idx.data_ptr(), count, per_row, w.data_ptr(), ldw, code, rows, n, d, None if dv is None else dv.data_ptr(),
           None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr())
@@ -268,7 +285,7 @@ def _norm(tensors, max_norm, out, stream):
         raise ValueError("needs at least one tensor")
     ptrs, counts, codes = _table(tensors, "tensors")
     device = tensors[0].device
-    norm = torch.empty((), dtype=torch.float32, device=device)
+    norm = _empty((), torch.float32, device, stream)
     if max_norm is None:
         _call("topk_grad_norm", device, stream, (*tensors, norm), ptrs, counts, codes, len(tensors), norm.data_ptr())
         return norm
