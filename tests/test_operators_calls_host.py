@@ -244,3 +244,17 @@ def test_selections_and_norms_that_overlap_are_refused(lib):
     assert all(back(at(i), at(5)) == -1 and back(at(5), at(i)) == -1 for i in (0, 1, 2, 3, 6) if i != 1) and back(at(4), at(4)) == -1
     assert all(selected(at(i), at(7)) == -1 and selected(at(5), at(i)) == -1 for i in (0, 1, 2, 3, 4, 6))
     assert clip_(1 << 20, 1 << 20) == 0 and clip_(1 << 20, (1 << 20) + 400) == 0 and clip_(1 << 20, (1 << 20) + 396) == -1
+
+
+def test_a_wait_that_ran_out_is_told_once(lib):
+    """The status word that a kernel sets when a device wait gives up, written here by the test."""
+    stream, timeout, etimeout = 64, 1, -5
+    assert lib.topk_last_status(stream) == 0
+    assert linear(lib, stream=stream) == 0
+    zeroed = [e[4] for e in events(lib) if e[0] == "memset"]
+    assert len(zeroed) == 1
+    word = ctypes.c_int.from_address(int(zeroed[0], 16))
+    assert lib.topk_last_status(stream) == 0
+    word.value = timeout
+    assert lib.topk_last_status(stream) == etimeout
+    assert lib.topk_last_status(stream) == 0 and word.value == 0
