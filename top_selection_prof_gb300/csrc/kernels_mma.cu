@@ -967,7 +967,7 @@ bool plan_mma(const Product& g, Scratch& sc, MmaPlan* q) {
   d.pairs = static_cast<int>(tiles < slots ? tiles : slots);
   d.waves = static_cast<int>((tiles + d.pairs - 1) / d.pairs);
   d.shared_tiles = 0;
-  // Equal runs pay when the stages they save outweigh the parts' way through scratch.  Measured: 4096 x 12288 x 512
+  // Equal runs pay when the stages they save outweigh the parts' way through scratch.  Measured (one sum a tile): 4096 x 12288 x 512
   // (32 tiles of 192 stages) 60.7 -> 45.4 us, 12288 x 4096 x 512 (96 of 64) 48.0 -> 46.6; 300 x 4096 x 1000 (8 of 64)
   // 23.9 -> 25.1, 4096 x 1024 x 8192 (512 of 16) 44.5 -> 53.4, 2000 x 16384 x 4096 (128 of 256, where all SMs at once
   // draw the power limit) 158 -> 179.
