@@ -131,13 +131,13 @@ bool known_act(int act) { return act >= TOPK_ACT_NONE && act <= TOPK_ACT_SILU; }
 constexpr int64_t kMaxExtent = INT32_MAX;
 size_t value_bytes(int dtype) { return dtype == TOPK_F32 ? 4 : 2; }
 
-// Where a matrix lies: `rows` runs of `row` bytes, `ld` bytes from one to the next.  At null: none.
+// Where a matrix lies: `rows` runs of `row` bytes, `ld` bytes from one to the next (0: there is one).  At null: none.
 struct Span {
   uintptr_t at;
   int64_t rows, row, ld;
 };
 Span matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
-  return {reinterpret_cast<uintptr_t>(p), rows, cols * size, ld * size};
+  return {reinterpret_cast<uintptr_t>(p), rows, cols * size, rows > 1 ? ld * size : 0};
 }
 Span vector(const void* p, int64_t n, int64_t size) { return matrix(p, 1, n, n, size); }
 // Whether two matrices have a byte in common; those whose rows lie differently far apart count as having one wherever their
@@ -146,10 +146,10 @@ bool meet(Span a, Span b) {
   if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.row < 1 || b.row < 1) return false;
   if (b.at < a.at) std::swap(a, b);
   if (b.at - a.at >= static_cast<uintptr_t>((a.rows - 1) * a.ld + a.row)) return false;
-  if (a.rows > 1 && b.rows > 1 && a.ld != b.ld) return true;
-  // b begins in a run of a, or, where a has another run, in the gap before it
-  const int64_t ld = a.rows > 1 ? a.ld : b.ld, d = static_cast<int64_t>((b.at - a.at) % static_cast<uintptr_t>(ld));
-  return a.rows == 1 || d < a.row || d + b.row > ld;
+  if (a.rows == 1 || (b.rows > 1 && a.ld != b.ld)) return true;
+  // b begins in a run of a, or in the gap before the next one
+  const int64_t d = static_cast<int64_t>((b.at - a.at) % static_cast<uintptr_t>(a.ld));
+  return d < a.row || d + b.row > a.ld;
 }
 // Whether an output has a byte in common with an input or another output.
 bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
