@@ -31,8 +31,8 @@
 // scaled by a power of two that the results are freed of.
 //
 // A bf16 operand a whose values have a rest (the gradient of a smooth
-// activation) is multiplied as two parts, the rest first: a stage is one of
-// twice as many.  The rest's sign is its own, so an infinity in b would meet
+// activation) is multiplied as two parts, a stage of k of both in turn: twice
+// as many stages.  The rest's sign is its own, so an infinity in b would meet
 // both signs, or a zero (NaN): where one is found, the leading part takes the
 // rest's place too and the sums are halved.
 //
@@ -59,14 +59,14 @@ constexpr int kStageBytesOut = 4096;   // staging of one epilogue warp: 32 rows 
 // After a round of k the sums therefore go to f32 registers, where they are
 // added to those before (rounded); the last round's accumulator takes their
 // total.  Rounds are eight stages of k (all six products of them) for f32,
-// which leaves 5e-7, and 32 for bf16, which leaves 2.3e-6 whatever K, what an
-// f32 sum of some 10^4 terms has.  Each reading of an accumulator holds the
-// products up by some 0.3 us (bf16 8192 x 8192 x 8192: one sum 588 us, rounds of
-// 32 stages 619, of 16 631, of 8 655).
+// which leaves 5e-7, and 32 for bf16 (16 where each has two products), which
+// leaves 2.3e-6 whatever K, what an f32 sum of some 10^4 terms has.  Each
+// reading of an accumulator holds the products up by some 0.3 us (bf16 8192 x
+// 8192 x 8192: one sum 588 us, rounds of 32 stages 619, of 16 631, of 8 655).
 // (TERMS: the products of parts that make one of values.)
 constexpr int kTermsF32 = 6, kTermsRest = 2;
 template <int TERMS>
-constexpr int kRoundDepthOf = TERMS == kTermsF32 ? 8 : 32;  // stages of k in a round
+constexpr int kRoundDepthOf = TERMS == kTermsF32 ? 8 : TERMS == kTermsRest ? 16 : 32;  // stages of k in a round
 constexpr int kTileN = 256;            // columns of c in a pair's tile (and of tensor memory in an accumulator)
 constexpr int kPairM = 2 * kTileM;     // its rows
 constexpr int kRowsB = kTileN / 2;     // rows of b that one CTA brings in
@@ -474,13 +474,18 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kThreads, 1) mma_kernel(co
           const uint32_t bar = map_to_rank(full(stage), 0);
           bar_expect(bar, kStage);
           int k0 = kb * kDeepK, part_a = 0, part_b = 0;
-          if constexpr (TERMS > 1) {
-            // a round's products of parts one after the other: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), or (1,0) (0,0)
+          if constexpr (TERMS == kTermsF32) {
+            // a round's products of parts one after the other: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
             const int round = kb / kRoundStages, in = kb - round * kRoundStages;
             const int deep = min(kRoundDepth, p.deal.depth - round * kRoundDepth), term = in / deep;
             k0 = (round * kRoundDepth + in - term * deep) * kDeepK;
-            part_a = (TERMS == kTermsF32 ? 0x001102 : 0x01) >> (4 * term) & 3;
-            part_b = (TERMS == kTermsF32 ? 0x010120 : 0x00) >> (4 * term) & 3;
+            part_a = 0x001102 >> (4 * term) & 3;
+            part_b = 0x010120 >> (4 * term) & 3;
+          } else if constexpr (TERMS == kTermsRest) {
+            // rest and leading part of a stage of k in turn: b's slice is then in L2 (one after the other over a round,
+            // 2000 x 4096 x 16384 took 871 us instead of 757)
+            k0 = (kb >> 1) * kDeepK;
+            part_a = ~kb & 1;
             if (twice) part_a = 0;
           }
           if (p.a_k) {
