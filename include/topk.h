@@ -253,7 +253,8 @@ const char* topk_status_str(int status);
  * `wait_limit_ns`, `inject_wait_timeout` and `recall` after it, `shortfalls`
  * at the end of topk_stats_t, topk_last_status, topk_autotune and topk_tuning
  * (cost_ratio = 0 meaning "measured"); 0.4.0 (400) added the operators
- * around the selection at the end of this header.
+ * around the selection; 0.5.0 (500) those of a language model at the end of
+ * this header.
  * Fill the struct with topk_options_init from the same version's library. */
 int topk_version(void);
 
@@ -444,6 +445,41 @@ int topk_grad_norm(const void* const* grads, const int64_t* counts, const int* d
  */
 int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* counts, const int* dtypes,
                         int64_t num, double max_norm, float* norm, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators of a language model around the selection: the next token out of
+ * its logits, tokens sorted by the experts they were routed to and back, and
+ * the positions of a key-value cache that stay.  What is said of the operators
+ * above (layout, rounding, overlap, scratch, capture) holds for these too.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A token of each row of logits (rows x n), drawn with the number u[r] of
+ * [0, 1).  Tokens stand in the selection's order (logit descending, index
+ * ascending); with z = (logit - the row's largest) / temperature a token
+ * weighs e^z.  Kept are
+ *   the tokens that weigh at least min_p (the largest weighs 1),
+ *   of those the first top_k (0: all),
+ *   of those the shortest prefix whose weights sum to top_p of theirs or more,
+ * at least one in each case; tokens[r] is the first in order at which the sum
+ * of the weights passes u[r] times that of all kept, and logprobs[r] the
+ * logarithm of its share of that.  A temperature of 0 takes the largest logit.
+ * NaN and -inf are never drawn; a row of nothing else gives -1 and -inf.
+ * Where a logit is +inf, only such are drawn.
+ *   Sums are formed as in at least 32 bits more than their largest term's
+ * rounding to f32 would leave: the token is that of 64-bit arithmetic, but
+ * where u[r] is within about 2^-30 of a border; weights below 2^-48 count as 0.
+ *   Each of temperature, top_k, top_p and min_p is a number, or one a row
+ * (device, `rows` values) where its pointer is not null, the number then
+ * being ignored; numbers are rounded to f32.  A row's temperature that is not
+ * above 0 (NaN too) takes the largest logit, its top_k below 1 keeps all, its
+ * top_p and min_p outside [0, 1] count as the nearer end, or as unset where NaN.
+ *   Limits: n <= 262144 (EUNSUPPORTED beyond); rows == 0 is a no-op.
+ *   EINVAL: a number that is negative, NaN or infinite, top_p or min_p above 1.
+ */
+int topk_sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t n, const float* u, double temperature,
+                const float* temperatures, int64_t top_k, const int32_t* top_ks, double top_p, const float* top_ps,
+                double min_p, const float* min_ps, int64_t* tokens, float* logprobs, void* stream);
 
 #ifdef __cplusplus
 }

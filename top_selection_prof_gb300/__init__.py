@@ -10,7 +10,8 @@ inputs must be CUDA tensors and the library must be built.
     vals, idx = tk.select_global(acts, K)        # BatchTopK: over the flattened tensor
 
 Around the selection, a sparse autoencoder's step (operators.py): linear, decode, their gradients, and the
-gradient norm with clipping.
+gradient norm with clipping; and what a language model does with one (language.py): the next token out of its
+logits, tokens sorted by expert and back, the positions of a cache that stay.
 """
 from __future__ import annotations
 
@@ -23,7 +24,7 @@ from ._lib import (PATH_NAMES, TOPK_BF16, TOPK_F32, TOPK_PATH_AUTO, TOPK_PATH_DI
 __all__ = ["select", "select_global", "select_ex", "plan", "prof_sample", "prof_filter", "index_bits",
            "options", "TopkError", "TOPK_PATH_AUTO", "TOPK_PATH_DIRECT", "TOPK_PATH_PROFK", "TOPK_PATH_EXACT",
            "TOPK_RULE_EXACT", "TOPK_RULE_ALG1", "linear", "linear_backward", "linear_backward_selected", "decode",
-           "decode_backward", "grad_norm", "clip_grad_norm", "clip_grad_norm_"]
+           "decode_backward", "grad_norm", "clip_grad_norm", "clip_grad_norm_", "sample"]
 
 
 def _torch():
@@ -177,3 +178,4 @@ def prof_filter(x, tau, M: int, global_: bool = False, largest: bool = True, str
 
 from .operators import (_empty, clip_grad_norm, clip_grad_norm_, decode, decode_backward, grad_norm, linear,  # noqa: E402
                         linear_backward, linear_backward_selected)
+from .language import sample  # noqa: E402

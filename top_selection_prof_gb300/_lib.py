@@ -19,7 +19,7 @@ EXPORTS = ("topk_options_init", "topk_select", "topk_select_global", "topk_selec
            "topk_status_str", "topk_version", "topk_index_bits", "topk_prof_sample", "topk_prof_filter",
            "topk_select_noalloc", "topk_last_status", "topk_autotune", "topk_tuning", "topk_linear",
            "topk_linear_backward", "topk_linear_backward_selected", "topk_decode", "topk_decode_backward",
-           "topk_grad_norm", "topk_clip_grad_norm")
+           "topk_grad_norm", "topk_clip_grad_norm", "topk_sample")
 
 
 class TopkOptions(ctypes.Structure):
@@ -99,7 +99,9 @@ def get():
         lib.topk_grad_norm.argtypes = [ptrs, ctypes.POINTER(i64), ctypes.POINTER(c_int), i64, vp, vp]
         lib.topk_clip_grad_norm.argtypes = [ptrs, ptrs, ctypes.POINTER(i64), ctypes.POINTER(c_int), i64, c_double, vp,
                                             vp]
-        for name in EXPORTS[-7:]:
+        lib.topk_sample.argtypes = [vp, i64, c_int, i64, i64, vp, c_double, vp, i64, vp, c_double, vp, c_double, vp, vp, vp,
+                                    vp]
+        for name in EXPORTS[EXPORTS.index("topk_linear"):]:
             getattr(lib, name).restype = c_int
         _lib = lib
     return _lib

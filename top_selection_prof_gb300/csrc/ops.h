@@ -1,6 +1,6 @@
 // Internal interface of the operators around the selection (the linear layer,
-// the products of a selection with a dictionary, the gradient norm): host
-// declarations shared by their C entries (ops_api.cu) and their kernels.
+// the products of a selection with a dictionary, the gradient norm; a language
+// model's tokens, experts and cache): host declarations shared by their C entries (ops_api.cu) and their kernels.
 #pragma once
 
 #include <atomic>
@@ -173,5 +173,24 @@ size_t clip_scratch_bytes();
 // scale == false: the norm alone.
 cudaError_t launch_clip(const ClipTensor* t, int64_t num, bool scale, float max_norm, float* norm, const Words& words,
                         Scratch& sc, cudaStream_t st);
+
+// ---- tokens from logits (kernels_tokens.cu) ------------------------------------
+constexpr int64_t kTokensMaxLen = int64_t(1) << 18;
+// Each parameter is one number, or one a row where its pointer is not null.
+struct TokenDraw {
+  const void* x;
+  int64_t ld;
+  int dtype;
+  int64_t rows;
+  int n;
+  const float* u;
+  float temperature, top_p, min_p;
+  int top_k;
+  const float *temperatures, *top_ps, *min_ps;
+  const int32_t* top_ks;
+  int64_t* tokens;
+  float* logprobs;
+};
+cudaError_t launch_tokens(const TokenDraw& p, cudaStream_t st);
 
 }  // namespace tk

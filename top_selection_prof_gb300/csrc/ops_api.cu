@@ -1,5 +1,6 @@
 // C entries of the operators around the selection (declared in include/topk.h):
 // argument checks, the per-(device, stream) scratch block and the launches.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -305,6 +306,29 @@ int clip(const void* const* grads, void* const* out, const int64_t* counts, cons
   return call.end(launch_clip(list.data(), num, scale, static_cast<float>(max_norm), norm, words, sc, st));
 }
 
+// A parameter that is one number, or one a row: numbers are checked.
+bool outside(const void* rows, double v, double low, double high) { return !rows && !(v >= low && v <= high); }
+
+int sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t n, const float* u, double temperature,
+           const float* temperatures, int64_t top_k, const int32_t* top_ks, double top_p, const float* top_ps, double min_p,
+           const float* min_ps, int64_t* tokens, float* logprobs, cudaStream_t st) {
+  if (!known_dtype(dtype) || rows < 0 || n < 1) return TOPK_EINVAL;
+  if (outside(temperatures, temperature, 0.0, FLT_MAX) || (!top_ks && top_k < 0) || outside(top_ps, top_p, 0.0, 1.0) ||
+      outside(min_ps, min_p, 0.0, 1.0))
+    return TOPK_EINVAL;
+  if (rows == 0) return TOPK_OK;
+  if (!logits || !u || !tokens || !logprobs || ld < n) return TOPK_EINVAL;
+  if (rows > kMaxExtent || n > kTokensMaxLen) return TOPK_EUNSUPPORTED;
+  if (clash({vector(tokens, rows, 8), vector(logprobs, rows, 4)},
+            {matrix(logits, rows, n, ld, static_cast<int64_t>(value_bytes(dtype))), vector(u, rows, 4), vector(temperatures, rows, 4),
+             vector(top_ks, rows, 4), vector(top_ps, rows, 4), vector(min_ps, rows, 4)}))
+    return TOPK_EINVAL;
+  const TokenDraw p{logits, ld, dtype, rows, static_cast<int>(n), u, static_cast<float>(temperature), static_cast<float>(top_p),
+                    static_cast<float>(min_p), top_ks || top_k > n ? 0 : static_cast<int>(top_k), temperatures, top_ps, min_ps, top_ks,
+                    tokens, logprobs};
+  return status_of(launch_tokens(p, st));
+}
+
 }  // namespace
 
 cudaError_t ops_take_status(cudaStream_t st, int* status) {
@@ -426,6 +450,15 @@ int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_
                         int64_t num, double max_norm, float* norm, void* stream) {
   return guarded([&] {
     return clip(grads, out, counts, dtypes, num, true, max_norm, norm, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t n, const float* u, double temperature,
+                const float* temperatures, int64_t top_k, const int32_t* top_ks, double top_p, const float* top_ps,
+                double min_p, const float* min_ps, int64_t* tokens, float* logprobs, void* stream) {
+  return guarded([&] {
+    return sample(logits, ld, dtype, rows, n, u, temperature, temperatures, top_k, top_ks, top_p, top_ps, min_p, min_ps, tokens,
+                  logprobs, static_cast<cudaStream_t>(stream));
   });
 }
 
