@@ -481,6 +481,92 @@ int topk_sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t
                 const float* temperatures, int64_t top_k, const int32_t* top_ks, double top_p, const float* top_ps,
                 double min_p, const float* min_ps, int64_t* tokens, float* logprobs, void* stream);
 
+/*
+ * Rows sorted by expert.  idx (tokens x k, as topk_select writes it: an expert
+ * of 0 ... experts - 1 for each token and choice) sends token t's row of x
+ * (tokens x d) to k experts.  xs (tokens k rows of d, contiguous) holds the
+ * rows of expert 0 first, then those of expert 1, ..., each expert's in the
+ * order of t k + j; place[t k + j] is the row's number in xs; expert e has
+ * rows offsets[e] to offsets[e + 1] - 1 (experts + 1 values).  A choice out of
+ * range (-1 where a token was dropped) has place -1; the rows of xs that are
+ * left over, at its end, are zeros.
+ *   The gradient of x is topk_combine of xs's, without weights.
+ *   Limits: experts <= 4096, tokens k < 2^29 (EUNSUPPORTED beyond; below, rows
+ * < 2^29 too).
+ */
+int topk_dispatch(const void* x, int64_t ldx, const int64_t* idx, int dtype, int64_t tokens, int64_t k, int64_t experts,
+                  int64_t d, void* xs, int64_t* place, int64_t* offsets, void* stream);
+
+/*
+ * The way back: y[t] = the sum over j of weights[t k + j] ys[place[t k + j]]
+ * (ys: rows x d, weights: tokens x k of the same dtype, nullable: all 1; y:
+ * tokens x d).  A place out of range adds nothing.
+ */
+int topk_combine(const void* ys, int64_t ldys, int64_t rows, const int64_t* place, const void* weights, int dtype,
+                 int64_t tokens, int64_t k, int64_t d, void* y, void* stream);
+
+/*
+ * Gradients of topk_combine from dy (tokens x d): dys[r] = the sum of
+ * weights[t k + j] dy[t] over the places that are r (rows x d; zeros where
+ * none is), dweights[t k + j] = dy[t] . ys[place[t k + j]] (0 where the place
+ * is out of range); each nullable.  ys is needed for dweights only.  Rows that
+ * topk_dispatch placed are each listed once; a row that is listed more often
+ * is summed all the same, more slowly.
+ */
+int topk_combine_backward(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t rows, const int64_t* place,
+                          const void* weights, int dtype, int64_t tokens, int64_t k, int64_t d, void* dys, void* dweights,
+                          void* stream);
+
+/* A tensor of batch x heads x rows rows of contiguous values: distances between them, in elements (0 or more). */
+typedef struct {
+  void* data;
+  int64_t batch, head, row;
+} topk_view_t;
+
+/*
+ * What stays in a key-value cache that is cut down to `keep` positions: the
+ * last `recent` ones of each sequence and, of the others, those with the
+ * largest scores (NaN above all numbers, equal ones by position).
+ *   keys, values: batch x heads x capacity rows of key_dim and value_dim
+ *     values of `dtype`, of which the first lengths[b] positions hold tokens
+ *     (device, int64; below 0 counts as 0, above the capacity as that).
+ *   score: f32, batch x heads rows of capacity values (its `row` is not used):
+ *     the attention weight that each position has had.
+ *   weights (NULL: none): what is added to it first, batch x (heads group) x
+ *     queries rows of capacity values of weights_dtype; query heads h group
+ *     ... h group + group - 1 read head h.  A weight that is NaN (a query
+ *     whose mask left nothing) counts as 0; behind lengths[b] none is read for
+ *     its value.  The sum is exact to f32's rounding; score is not changed.
+ * Contiguous results: out_keys and out_values, the rows of what stays, in the
+ * order of their positions (batch x heads x keep rows); out_score their score;
+ * out_kept their positions; out_lengths[b] = min(lengths[b], keep).  Behind
+ * that, rows and scores are zeros and positions -1.
+ *   Limits: batch heads capacity and batch heads keep <= 2^40, dims <= 2^20
+ * (EUNSUPPORTED beyond).  EINVAL: keep < 1, recent outside [0, keep].
+ */
+int topk_evict(const topk_view_t* keys, const topk_view_t* values, const topk_view_t* score, const int64_t* lengths,
+               const topk_view_t* weights, int weights_dtype, int64_t group, int64_t queries, int dtype, int64_t batch,
+               int64_t heads, int64_t capacity, int64_t key_dim, int64_t value_dim, int64_t keep, int64_t recent,
+               void* out_keys, void* out_values, float* out_score, int64_t* out_kept, int64_t* out_lengths, void* stream);
+
+/*
+ * The single-token form, in place: a new token's key and value (batch x heads
+ * rows; their `row` is not used) go into each head's cache of `capacity`
+ * slots.  lengths[b] is the number of tokens before it, and its position.
+ * weights (as above, by slot) are added to the scores of the slots in use
+ * first.  While there are fewer tokens than slots, the token takes slot
+ * lengths[b]; then, the slot with the least score (NaN above all numbers,
+ * equal ones: the lowest slot) of those whose position is below lengths[b] -
+ * recent.  The slot's score becomes 0 and its position lengths[b]; slots[b
+ * heads + h] is the slot, or -1 where every position is recent (nothing is
+ * stored then).  positions: int64, batch x heads rows of capacity values.
+ *   EINVAL: recent outside [0, capacity - 1].
+ */
+int topk_replace(const topk_view_t* keys, const topk_view_t* values, const topk_view_t* score, const topk_view_t* positions,
+                 const int64_t* lengths, const topk_view_t* key, const topk_view_t* value, const topk_view_t* weights,
+                 int weights_dtype, int64_t group, int64_t queries, int dtype, int64_t batch, int64_t heads,
+                 int64_t capacity, int64_t key_dim, int64_t value_dim, int64_t recent, int64_t* slots, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

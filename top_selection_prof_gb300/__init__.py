@@ -24,7 +24,8 @@ from ._lib import (PATH_NAMES, TOPK_BF16, TOPK_F32, TOPK_PATH_AUTO, TOPK_PATH_DI
 __all__ = ["select", "select_global", "select_ex", "plan", "prof_sample", "prof_filter", "index_bits",
            "options", "TopkError", "TOPK_PATH_AUTO", "TOPK_PATH_DIRECT", "TOPK_PATH_PROFK", "TOPK_PATH_EXACT",
            "TOPK_RULE_EXACT", "TOPK_RULE_ALG1", "linear", "linear_backward", "linear_backward_selected", "decode",
-           "decode_backward", "grad_norm", "clip_grad_norm", "clip_grad_norm_", "sample"]
+           "decode_backward", "grad_norm", "clip_grad_norm", "clip_grad_norm_", "sample", "dispatch",
+           "combine", "combine_backward", "evict", "replace_"]
 
 
 def _torch():
@@ -178,4 +179,4 @@ def prof_filter(x, tau, M: int, global_: bool = False, largest: bool = True, str
 
 from .operators import (_empty, clip_grad_norm, clip_grad_norm_, decode, decode_backward, grad_norm, linear,  # noqa: E402
                         linear_backward, linear_backward_selected)
-from .language import sample  # noqa: E402
+from .language import combine, combine_backward, dispatch, evict, replace_, sample  # noqa: E402

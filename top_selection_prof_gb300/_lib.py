@@ -19,7 +19,8 @@ EXPORTS = ("topk_options_init", "topk_select", "topk_select_global", "topk_selec
            "topk_status_str", "topk_version", "topk_index_bits", "topk_prof_sample", "topk_prof_filter",
            "topk_select_noalloc", "topk_last_status", "topk_autotune", "topk_tuning", "topk_linear",
            "topk_linear_backward", "topk_linear_backward_selected", "topk_decode", "topk_decode_backward",
-           "topk_grad_norm", "topk_clip_grad_norm", "topk_sample")
+           "topk_grad_norm", "topk_clip_grad_norm", "topk_sample", "topk_dispatch",
+           "topk_combine", "topk_combine_backward", "topk_evict", "topk_replace")
 
 
 class TopkOptions(ctypes.Structure):
@@ -41,6 +42,10 @@ class TopkStats(ctypes.Structure):
 class TopkTuning(ctypes.Structure):
     _fields_ = [("tau_a_ns", ctypes.c_double), ("tau_b_ns", ctypes.c_double), ("cost_ratio", ctypes.c_double),
                 ("crossover_n", ctypes.c_int64), ("crossover_k", ctypes.c_int64)]
+
+
+class TopkView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("row", ctypes.c_int64)]
 
 
 class TopkPlan(ctypes.Structure):
@@ -101,6 +106,14 @@ def get():
                                             vp]
         lib.topk_sample.argtypes = [vp, i64, c_int, i64, i64, vp, c_double, vp, i64, vp, c_double, vp, c_double, vp, vp, vp,
                                     vp]
+        lib.topk_dispatch.argtypes = [vp, i64, vp, c_int, i64, i64, i64, i64, vp, vp, vp, vp]
+        lib.topk_combine.argtypes = [vp, i64, i64, vp, vp, c_int, i64, i64, i64, vp, vp]
+        lib.topk_combine_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, c_int, i64, i64, i64, vp, vp, vp]
+        view = ctypes.POINTER(TopkView)
+        lib.topk_evict.argtypes = [view, view, view, vp, view, c_int, i64, i64, c_int, i64, i64, i64, i64, i64, i64, i64, vp, vp,
+                                   vp, vp, vp, vp]
+        lib.topk_replace.argtypes = [view, view, view, view, vp, view, view, view, c_int, i64, i64, c_int, i64, i64, i64, i64,
+                                     i64, i64, vp, vp]
         for name in EXPORTS[EXPORTS.index("topk_linear"):]:
             getattr(lib, name).restype = c_int
         _lib = lib

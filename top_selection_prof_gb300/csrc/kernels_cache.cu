@@ -1,0 +1,445 @@
+// The positions of a key-value cache that stay, by accumulated attention weight.
+//
+// A head's score is the sum of the attention weights that its queries gave a
+// position, held in f32.  What a call adds is summed in pairs of f32 (the error
+// of each addition kept and added in its turn), so that a score is the exact
+// sum rounded once and the choice does not depend on how the sum was split.
+//
+// evict: sums by position over all SMs; the choice, a cluster a head: the score of
+// the last one kept by three digits of its key, then the kept positions in
+// order by counting; and the rows of both caches moved to their new places.
+// replace: one token, one launch: a cluster a head adds the weights, finds the
+// least score and writes the new row over it.
+#include <cooperative_groups.h>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ops_common.cuh"
+
+namespace tk {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostBlocks = 8;   // of a cluster
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// hi + lo, to about 2^-48.  A value that is not finite ends up in hi alone.
+struct Sum2 {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float s = hi + v, b = s - hi;
+    lo += (hi - (s - b)) + (v - b);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum2& o) {
+    add(o.hi);
+    lo += o.lo;
+  }
+  __device__ __forceinline__ float value() const { return fabsf(hi) < INFINITY ? hi + lo : hi; }
+};
+// A weight that is NaN (of a query whose mask left nothing) counts as 0.
+__device__ __forceinline__ float counted(float w) { return w == w ? w : 0.0f; }
+
+__device__ __forceinline__ int64_t clamped(int64_t v, int64_t most) { return v < 0 ? 0 : v > most ? most : v; }
+
+// ---- sums by position ------------------------------------------------------------
+struct WeightSums {
+  View weights;       // batch, query head, query
+  int64_t group, queries, heads, capacity;
+  View score;         // batch, head
+  const int64_t* lengths;
+  float* out;         // batch x heads x capacity
+};
+constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+
+// A block: 32 vectors of positions of one head, the head's query rows dealt to its warps.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSums p) {
+  __shared__ float2 part[kSumWarps][32 * VEC];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t chunks = (p.capacity + 32 * VEC - 1) / (32 * VEC), bh = blockIdx.x / chunks, b = bh / p.heads, h = bh % p.heads;
+  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = (blockIdx.x - bh * chunks) * 32 * VEC;
+  if (at0 >= len) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t at = at0 + lane * VEC;
+  Sum2 sum[VEC];
+  const int64_t n = p.group * p.queries;
+  if (at < len) {
+    constexpr int kAhead = 4;
+    for (int64_t i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
+      Raw<T, VEC> v[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int64_t i = i0 + a * kSumWarps;
+        v[a].clear();
+        if (i < n) {
+          const int64_t g = i / p.queries, q = i - g * p.queries;
+          const T* row = static_cast<const T*>(p.weights.data) + b * p.weights.batch + (h * p.group + g) * p.weights.head + q * p.weights.row;
+          v[a].load_nc(row + at);
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        Vec<T, VEC> x;
+        x.set_raw(v[a]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e].add(counted(x.v[e]));
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) part[warp][lane * VEC + e] = make_float2(sum[e].hi, sum[e].lo);
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * VEC; i += kSumThreads) {
+    if (at0 + i >= len) break;
+    Sum2 all;
+    all.add(static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + i]);
+    for (int w = 0; w < kSumWarps; ++w) all.add(Sum2{part[w][i].x, part[w][i].y});
+    p.out[bh * p.capacity + at0 + i] = all.value();
+  }
+}
+
+// ---- the choice -------------------------------------------------------------------
+struct Choice {
+  const float* score;     // batch x heads rows, `ld` apart by head and `ld_batch` by batch
+  int64_t ld_batch, ld, heads, capacity;
+  const int64_t* lengths;
+  int64_t batch, keep, recent;
+  float* out_score;       // batch x heads x keep
+  int64_t* kept;
+  int64_t* out_lengths;
+};
+constexpr int kDigits = 2048;  // 11 bits of a key at a time (the last 10)
+
+struct ChoiceShared {
+  unsigned hist[kDigits];      // this block's
+  unsigned total[kDigits];     // the cluster's
+  unsigned warp_sum[kWarps];
+  unsigned found, above;
+  unsigned over[kMostBlocks], even[kMostBlocks];  // of each block, in every block
+  int64_t warp_slot[kWarps];
+};
+
+// Sum over the threads before this one; *all: of the block.
+__device__ __forceinline__ unsigned scan_before(ChoiceShared& s, unsigned v, unsigned* all) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  unsigned incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned t = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) s.warp_sum[warp] = incl;
+  __syncthreads();
+  unsigned before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const unsigned t = s.warp_sum[w];
+    if (w < warp) before += t;
+    sum += t;
+  }
+  *all = sum;
+  __syncthreads();
+  return before + incl - v;
+}
+
+__global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
+  __shared__ ChoiceShared s;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t bh = blockIdx.x / blocks, b = bh / p.heads, h = bh % p.heads;
+  const float* score = p.score + b * p.ld_batch + h * p.ld;
+  const int64_t len = clamped(p.lengths[b], p.capacity);
+  const int64_t kept = min(len, p.keep), old = len - min(p.recent, len);  // the last ones stay
+  const unsigned want = static_cast<unsigned>(len > p.keep ? p.keep - (len - old) : old);  // of the others
+  // this block's run of positions
+  const int64_t run = ((len + blocks - 1) / blocks + 3) / 4 * 4;
+  const int64_t begin = min(len, run * rank), end = min(len, begin + run);
+  cluster_sync();               // (every block has started before another reaches into its memory)
+  uint32_t key = 0, mask = 0;   // of the last one kept
+  unsigned left = want;         // of those with the key's bits under the mask
+  const bool choose = want < old;
+  if (choose && want > 0) {
+    for (int digit = 0; digit < 3; ++digit) {
+      const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
+      for (int i = threadIdx.x; i < kDigits; i += kThreads) s.hist[i] = 0;
+      __syncthreads();
+      for (int64_t i = begin + threadIdx.x; i < min(end, old); i += kThreads) {
+        const uint32_t k = order_key_f32(__float_as_uint(score[i]));
+        if ((k & mask) == key) atomicAdd(&s.hist[(~k >> shift) & ((1u << bits) - 1)], 1u);
+      }
+      cluster_sync();
+      const int share = kDigits / blocks;
+      for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
+        unsigned n = 0;
+        for (int q = 0; q < blocks; ++q) n += cluster.map_shared_rank(&s, q)->hist[i];
+        for (int q = 0; q < blocks; ++q) cluster.map_shared_rank(&s, q)->total[i] = n;
+      }
+      cluster_sync();
+      unsigned n[kDigits / kThreads], sum = 0, all;
+#pragma unroll
+      for (int q = 0; q < kDigits / kThreads; ++q) sum += n[q] = s.total[threadIdx.x * (kDigits / kThreads) + q];
+      unsigned before = scan_before(s, sum, &all);
+#pragma unroll
+      for (int q = 0; q < kDigits / kThreads; ++q) {
+        if (before < left && left <= before + n[q]) {
+          s.found = threadIdx.x * (kDigits / kThreads) + q;
+          s.above = before;
+        }
+        before += n[q];
+      }
+      __syncthreads();
+      key |= (~s.found & ((1u << bits) - 1)) << shift;
+      mask |= ((1u << bits) - 1) << shift;
+      left -= s.above;
+      __syncthreads();
+    }
+  }
+  // kept: the recent ones, scores above the key's, and the first `left` that equal it
+  auto state = [&](int64_t i) -> int {  // 2: kept, 1: equal, 0
+    if (i >= old || !choose) return 2;
+    if (want == 0) return 0;
+    const uint32_t k = order_key_f32(__float_as_uint(score[i]));
+    return k > key ? 2 : k == key ? 1 : 0;
+  };
+  unsigned over = 0, even = 0;
+  for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
+    const int st = state(i);
+    over += st == 2;
+    even += st == 1;
+  }
+  unsigned all_over, all_even;
+  scan_before(s, over, &all_over);
+  scan_before(s, even, &all_even);
+  if (threadIdx.x < blocks) {
+    ChoiceShared* peer = cluster.map_shared_rank(&s, threadIdx.x);
+    peer->over[rank] = all_over;
+    peer->even[rank] = all_even;
+  }
+  cluster_sync();
+  int64_t slot = 0;
+  unsigned equals = 0;  // equal ones before
+  for (int q = 0; q < rank; ++q) {
+    slot += s.over[q];
+    equals += s.even[q];
+  }
+  slot += min(equals, left);
+  for (int64_t i0 = begin; i0 < end; i0 += kThreads) {
+    const int64_t i = i0 + threadIdx.x;
+    const int st = i < end ? state(i) : 0;
+    unsigned n_even, n_kept;
+    const unsigned e = equals + scan_before(s, st == 1, &n_even);
+    const bool stays = st == 2 || (st == 1 && e < left);
+    const unsigned at = scan_before(s, stays, &n_kept);
+    if (stays) {
+      p.kept[bh * p.keep + slot + at] = i;
+      p.out_score[bh * p.keep + slot + at] = score[i];
+    }
+    equals += n_even;
+    slot += n_kept;
+  }
+  for (int64_t i = kept + rank * kThreads + threadIdx.x; i < p.keep; i += int64_t(blocks) * kThreads) {
+    p.kept[bh * p.keep + i] = -1;
+    p.out_score[bh * p.keep + i] = 0.0f;
+  }
+  if (h == 0 && rank == 0 && threadIdx.x == 0) p.out_lengths[b] = kept;
+}
+
+// ---- moving rows ------------------------------------------------------------------
+struct MoveKept {
+  View in[2];          // keys, values
+  void* out[2];        // batch x heads x keep x dim
+  int64_t dim[2];
+  const int64_t* kept;
+  int64_t heads, keep, total;  // batch x heads x keep
+  int share;           // threads a row
+};
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) move_kept_kernel(const MoveKept p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t i = int64_t(blockIdx.x) * (256 / p.share) + threadIdx.x / p.share;
+  if (i >= p.total) return;
+  const int64_t bh = i / p.keep, b = bh / p.heads, h = bh % p.heads, from = p.kept[i];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const T* src = static_cast<const T*>(p.in[w].data) + b * p.in[w].batch + h * p.in[w].head + from * p.in[w].row;
+    T* dst = static_cast<T*>(p.out[w]) + i * p.dim[w];
+    for (int64_t c = int64_t(threadIdx.x % p.share) * VEC; c < p.dim[w]; c += int64_t(p.share) * VEC) {
+      Raw<T, VEC> v;
+      v.clear();
+      if (from >= 0) v.load_nc(src + c);
+      if constexpr (VEC == 1) dst[c] = v.u;
+      else __stcs(reinterpret_cast<uint4*>(dst + c), v.u);
+    }
+  }
+}
+
+// ---- one token ----------------------------------------------------------------------
+template <typename W>
+__device__ __forceinline__ float weight_at(const W* row, int64_t i) { return counted(to_f32(row[i])); }
+
+// A cluster a head: adds the group's weights to the scores, finds the slot and writes the token there.
+template <typename W>
+__global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
+  __shared__ uint64_t warp_least[kWarps];
+  __shared__ uint64_t leasts[kMostBlocks];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t bh = blockIdx.x / blocks, b = bh / p.heads, h = bh % p.heads;
+  const int64_t seen = max(p.lengths[b], int64_t(0)), len = min(seen, p.capacity);
+  float* score = static_cast<float*>(p.score.data) + b * p.score.batch + h * p.score.head;
+  int64_t* positions = static_cast<int64_t*>(p.positions.data) + b * p.positions.batch + h * p.positions.head;
+  const W* weights = static_cast<const W*>(p.weights.data);
+  if (weights) weights += b * p.weights.batch + h * p.group * p.weights.head;
+  const int64_t run = (p.capacity + blocks - 1) / blocks;
+  const int64_t begin = min(len, run * rank), end = min(len, begin + run);
+  uint64_t least = ~uint64_t(0);  // (score, slot) of the least that may go
+  for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
+    Sum2 sum;
+    sum.add(score[i]);
+    if (weights) {
+      for (int64_t g = 0; g < p.group; ++g)
+        for (int64_t q = 0; q < p.queries; ++q) sum.add(weight_at(weights + g * p.weights.head + q * p.weights.row, i));
+      score[i] = sum.value();
+    }
+    if (seen >= p.capacity && (p.recent == 0 || positions[i] < seen - p.recent)) {
+      const uint64_t key = static_cast<uint64_t>(order_key_f32(__float_as_uint(sum.value()))) << 32 | static_cast<uint32_t>(i);
+      least = min(least, key);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(~0u, least, o));
+  if (threadIdx.x % 32 == 0) warp_least[threadIdx.x / 32] = least;
+  cluster_sync();
+  if (threadIdx.x < blocks) {
+    for (int w = 0; w < kWarps; ++w) least = min(least, warp_least[w]);
+    *cluster.map_shared_rank(&leasts[rank], threadIdx.x) = least;
+  }
+  cluster_sync();
+  for (int q = 0; q < blocks; ++q) least = q ? min(least, leasts[q]) : leasts[0];
+  // (where every slot is recent, the token is not stored)
+  const int64_t slot = seen < p.capacity ? seen : least == ~uint64_t(0) ? -1 : static_cast<int64_t>(static_cast<uint32_t>(least));
+  if (rank != 0) return;
+  if (threadIdx.x == 0) {
+    p.slots[bh] = slot;
+    if (slot >= 0) {
+      score[slot] = 0.0f;
+      positions[slot] = seen;
+    }
+  }
+  if (slot < 0) return;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const View& in = w ? p.value : p.key;
+    const View& out = w ? p.values : p.keys;
+    const int64_t dim = w ? p.value_dim : p.key_dim;
+    const int64_t src = b * in.batch + h * in.head, dst = b * out.batch + h * out.head + slot * out.row;
+    for (int64_t c = threadIdx.x; c < dim; c += kThreads) {
+      if (p.dtype == kF32) static_cast<float*>(out.data)[dst + c] = static_cast<const float*>(in.data)[src + c];
+      else static_cast<__nv_bfloat16*>(out.data)[dst + c] = static_cast<const __nv_bfloat16*>(in.data)[src + c];
+    }
+  }
+}
+
+// Blocks of a cluster a head: more where heads are few, down to `least` positions each.
+int blocks_for(int64_t rows, int64_t positions, int64_t least) {
+  int blocks = 1;
+  while (blocks < kMostBlocks && rows * blocks * 2 <= 2 * ops_sm_count() && positions > blocks * least) blocks *= 2;
+  return blocks;
+}
+
+template <typename P>
+cudaError_t launch_clusters(void (*kernel)(P), const P& p, int64_t rows, int blocks, cudaStream_t st) {
+  if (rows * blocks > INT32_MAX) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+bool aligned_view(const View& v, int64_t size) {
+  return (reinterpret_cast<uintptr_t>(v.data) | static_cast<uintptr_t>(v.batch * size) | static_cast<uintptr_t>(v.head * size) |
+          static_cast<uintptr_t>(v.row * size)) % 16 == 0;
+}
+
+template <typename T>
+cudaError_t add_weights(const Evict& p, float* out, cudaStream_t st) {
+  constexpr int kVec = 16 / sizeof(T);
+  const WeightSums w{p.weights, p.group, p.queries, p.heads, p.capacity, p.score, p.lengths, out};
+  // (the last vector of a row may reach past its length, not past the capacity)
+  const bool wide = aligned_view(p.weights, sizeof(T)) && p.capacity % kVec == 0;
+  const int64_t each = 32 * (wide ? kVec : 1);
+  const int64_t blocks = (p.capacity + each - 1) / each * p.batch * p.heads;
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  return wide ? launch_after(weight_sums_kernel<T, kVec>, grid, kSumThreads, 0, st, w) : launch_after(weight_sums_kernel<T, 1>, grid, kSumThreads, 0, st, w);
+}
+
+template <typename T>
+cudaError_t move_kept(const Evict& p, cudaStream_t st) {
+  constexpr int kVec = 16 / sizeof(T);
+  MoveKept m{{p.keys, p.values}, {p.out_keys, p.out_values}, {p.key_dim, p.value_dim}, p.out_kept, p.heads, p.keep, p.batch * p.heads * p.keep, 0};
+  const int64_t size = sizeof(T);
+  const bool wide = aligned_view(p.keys, size) && aligned_view(p.values, size) && p.key_dim % kVec == 0 && p.value_dim % kVec == 0 &&
+                    (reinterpret_cast<uintptr_t>(p.out_keys) | reinterpret_cast<uintptr_t>(p.out_values)) % 16 == 0;
+  const int64_t dim = p.key_dim > p.value_dim ? p.key_dim : p.value_dim;
+  m.share = 8;
+  while (m.share < 256 && m.share * (wide ? kVec : 1) < dim) m.share *= 2;
+  const int64_t blocks = (m.total + 256 / m.share - 1) / (256 / m.share);
+  if (blocks > INT32_MAX) return cudaErrorNotSupported;
+  return wide ? launch_after(move_kept_kernel<T, kVec>, static_cast<unsigned>(blocks), 256, 0, st, m)
+              : launch_after(move_kept_kernel<T, 1>, static_cast<unsigned>(blocks), 256, 0, st, m);
+}
+
+}  // namespace
+
+size_t evict_scratch_bytes(const Evict& p) {
+  Scratch sc;
+  if (p.weights.data) sc.take<float>(p.batch * p.heads * p.capacity);
+  return sc.used();
+}
+
+cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st) {
+  Choice c{static_cast<const float*>(p.score.data), p.score.batch, p.score.head, p.heads, p.capacity, p.lengths, p.batch, p.keep,
+           p.recent, p.out_score, p.out_kept, p.out_lengths};
+  if (p.weights.data) {
+    float* sums = sc.take<float>(p.batch * p.heads * p.capacity);
+    const cudaError_t e = p.weights_dtype == kF32 ? add_weights<float>(p, sums, st) : add_weights<__nv_bfloat16>(p, sums, st);
+    if (e != cudaSuccess) return e;
+    c.score = sums;
+    c.ld_batch = p.heads * p.capacity;
+    c.ld = p.capacity;
+  }
+  cudaError_t e = launch_clusters(choice_kernel, c, p.batch * p.heads, blocks_for(p.batch * p.heads, p.capacity, 2048), st);
+  if (e != cudaSuccess) return e;
+  return p.dtype == kF32 ? move_kept<float>(p, st) : move_kept<__nv_bfloat16>(p, st);
+}
+
+cudaError_t launch_replace(const Replace& p, cudaStream_t st) {
+  const int64_t rows = p.batch * p.heads;
+  const int blocks = blocks_for(rows, p.capacity, 512);
+  return p.weights_dtype == kF32 ? launch_clusters(replace_kernel<float>, p, rows, blocks, st)
+                                 : launch_clusters(replace_kernel<__nv_bfloat16>, p, rows, blocks, st);
+}
+
+}  // namespace tk

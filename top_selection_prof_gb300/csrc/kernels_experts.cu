@@ -1,0 +1,498 @@
+// Tokens sorted by the experts they were routed to, and back.
+//
+// Sorting is a counting sort that keeps the order of equal ones: place s =
+// t k + j goes behind all places of smaller experts and the earlier ones of its
+// own.  Places without an expert stand behind all, so that every row of the
+// result has one place, and those rows are zeros.  All of it is bound by the
+// rows moved: tokens are walked in order, each row of x (or of y, dy) is read or
+// written once, and the rows by expert once.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ops_common.cuh"
+
+namespace tk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kFewPlaces = 1024;   // places that every block ranks for itself
+
+// The expert of place s; `experts` where it has none.
+__device__ __forceinline__ int expert_of(const int64_t* idx, int64_t s, int experts) {
+  const int64_t v = idx[s];
+  return v >= 0 && v < experts ? static_cast<int>(v) : experts;
+}
+
+// ---- ranks ------------------------------------------------------------------------
+// counts[b * (experts + 1) + e]: places of expert e in block b's run of `chunk` places.
+__global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const int64_t* idx, int64_t total, int64_t chunk, int experts,
+                                                                    unsigned* counts) {
+  extern __shared__ unsigned held[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int e = threadIdx.x; e <= experts; e += kSortThreads) held[e] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * chunk, end = min(begin + chunk, total);
+  for (int64_t s = begin + threadIdx.x; s < end; s += kSortThreads) atomicAdd(&held[expert_of(idx, s, experts)], 1u);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= experts; e += kSortThreads) counts[int64_t(blockIdx.x) * (experts + 1) + e] = held[e];
+}
+
+// Row of every place: rows[s], or ~row of the zeros for a place without an expert.
+__global__ void __launch_bounds__(kSortThreads) expert_rank_kernel(const int64_t* idx, int64_t total, int64_t chunk, int experts,
+                                                                   const unsigned* counts, int* rows, int64_t* place, int64_t* offsets) {
+  extern __shared__ unsigned held[];
+  __shared__ unsigned warp_sum[kSortWarps];
+  unsigned* all = held;                  // places of each expert, then where the next place of this block goes
+  unsigned* before = held + experts + 1; // those of the blocks before
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int kinds = experts + 1;
+  for (int e = threadIdx.x; e < 2 * kinds; e += kSortThreads) held[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x) * kinds; i += kSortThreads) {
+    const unsigned v = counts[i];
+    const int b = i / kinds, e = i - b * kinds;
+    if (v) {
+      atomicAdd(&all[e], v);
+      if (b < static_cast<int>(blockIdx.x)) atomicAdd(&before[e], v);
+    }
+  }
+  __syncthreads();
+  // bases by a scan over the experts, a run of them a thread
+  const int run = (kinds + kSortThreads - 1) / kSortThreads;
+  const int e0 = min(kinds, static_cast<int>(threadIdx.x) * run), e1 = min(kinds, e0 + run);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  unsigned sum = 0;
+  for (int e = e0; e < e1; ++e) sum += all[e];
+  unsigned incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned v = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  unsigned base = incl - sum;
+  for (int w = 0; w < warp; ++w) base += warp_sum[w];
+  for (int e = e0; e < e1; ++e) {
+    const unsigned n = all[e];
+    if (blockIdx.x == 0) offsets[e] = base;  // (offsets[experts]: the start of those without an expert)
+    all[e] = base + before[e];
+    base += n;
+  }
+  __syncthreads();
+  // the block's places in order, a warp after another
+  const int64_t begin = blockIdx.x * chunk, end = min(begin + chunk, total);
+  for (int64_t s0 = begin; s0 < end; s0 += kSortThreads) {
+    const int64_t s = s0 + threadIdx.x;
+    const int e = s < end ? expert_of(idx, s, experts) : -1;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w == warp) {
+        const unsigned same = __match_any_sync(~0u, e);
+        if (e >= 0) {
+          const unsigned row = all[e] + __popc(same & lanemask_lt());
+          rows[s] = e < experts ? static_cast<int>(row) : ~static_cast<int>(row);
+          place[s] = e < experts ? static_cast<int64_t>(row) : -1;
+          __syncwarp(same);
+          if ((same & lanemask_lt()) == 0) all[e] += __popc(same);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- moving rows --------------------------------------------------------------------
+struct MoveRows {
+  const void* x;
+  int64_t ldx, tokens, d;
+  int k, experts;
+  const int64_t* idx;
+  int64_t* place;
+  int64_t* offsets;
+  const int* rows;
+  void* xs;
+};
+
+// Writes token t's row to the k rows of its places (zeros to those without an expert), `threads` threads of which this is `at`.
+template <typename T, int VEC>
+__device__ __forceinline__ void spread_row(const MoveRows& p, int64_t t, const int* rows, int at, int threads) {
+  const T* src = static_cast<const T*>(p.x) + t * p.ldx;
+  T* xs = static_cast<T*>(p.xs);
+  for (int64_t c = int64_t(at) * VEC; c < p.d; c += int64_t(threads) * VEC) {
+    Raw<T, VEC> v, zero;
+    v.load_nc(src + c);
+    zero.clear();
+    for (int j = 0; j < p.k; ++j) {
+      const int r = rows[j];
+      const int64_t row = r < 0 ? ~r : r;
+      T* dst = xs + row * p.d + c;
+      if constexpr (VEC == 1) *dst = r < 0 ? zero.u : v.u;
+      else __stcs(reinterpret_cast<uint4*>(dst), r < 0 ? zero.u : v.u);
+    }
+  }
+}
+
+// Few places: block t ranks token t's places by counting those that stand before them and moves its row; the last block forms
+// the offsets.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const MoveRows p) {
+  __shared__ int rows[kFewPlaces];
+  extern __shared__ unsigned held[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int total = static_cast<int>(p.tokens) * p.k;
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (t == p.tokens) {
+    const int kinds = p.experts + 1;
+    for (int e = threadIdx.x; e < kinds; e += kThreads) held[e] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < total; s += kThreads) atomicAdd(&held[expert_of(p.idx, s, p.experts)], 1u);
+    __syncthreads();
+    if (warp == 0) {
+      unsigned base = 0;
+      for (int e0 = 0; e0 < kinds; e0 += 32) {
+        const unsigned n = e0 + lane < kinds ? held[e0 + lane] : 0;
+        unsigned incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned v = __shfl_up_sync(~0u, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (e0 + lane < kinds) p.offsets[e0 + lane] = base + incl - n;
+        base += __shfl_sync(~0u, incl, 31);
+      }
+    }
+    return;
+  }
+  for (int j = warp; j < p.k; j += kThreads / 32) {
+    const int s = static_cast<int>(t) * p.k + j;
+    const int e = expert_of(p.idx, s, p.experts);
+    int row = 0;
+    for (int i = lane; i < total; i += 32) {
+      const int other = expert_of(p.idx, i, p.experts);
+      row += other < e || (other == e && i < s);
+    }
+    row = __reduce_add_sync(~0u, row);
+    if (lane == 0) {
+      rows[j] = e < p.experts ? row : ~row;
+      p.place[s] = e < p.experts ? row : -1;
+    }
+  }
+  __syncthreads();
+  spread_row<T, VEC>(p, t, rows, threadIdx.x, kThreads);
+}
+
+// `share` threads a token (a power of two).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const MoveRows p, int share) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t t = int64_t(blockIdx.x) * (kThreads / share) + threadIdx.x / share;
+  if (t < p.tokens) spread_row<T, VEC>(p, t, p.rows + t * p.k, threadIdx.x % share, share);
+}
+
+// ---- back ---------------------------------------------------------------------------
+struct JoinRows {
+  const void* ys;
+  int64_t ldy, rows, tokens, d;
+  int k;
+  const int64_t* place;
+  const void* weights;  // nullable
+  void* y;
+  const void* dy;       // gradients: of y
+  int64_t lddy;
+  unsigned* listed;     // how often each row is listed
+  void* dys;            // nullable
+  void* dweights;       // nullable
+};
+constexpr int kTogether = 8;  // rows of a token that are read together
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const JoinRows p, int share) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t t = int64_t(blockIdx.x) * (kThreads / share) + threadIdx.x / share;
+  if (t >= p.tokens) return;
+  const T* ys = static_cast<const T*>(p.ys);
+  const T* w = static_cast<const T*>(p.weights) + (p.weights ? t * p.k : 0);
+  const int64_t* place = p.place + t * p.k;
+  for (int64_t c = int64_t(threadIdx.x % share) * VEC; c < p.d; c += int64_t(share) * VEC) {
+    float sum[VEC] = {};
+    for (int j0 = 0; j0 < p.k; j0 += kTogether) {
+      Raw<T, VEC> v[kTogether];
+      float f[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        const int64_t r = j0 + j < p.k ? place[j0 + j] : -1;
+        f[j] = 0.0f;
+        v[j].clear();
+        if (r >= 0 && r < p.rows) {
+          v[j].load_nc(ys + r * p.ldy + c);
+          f[j] = p.weights ? to_f32(w[j0 + j]) : 1.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        Vec<T, VEC> x;
+        x.set_raw(v[j]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] = fmaf(f[j], x.v[e], sum[e]);
+      }
+    }
+    Vec<T, VEC> out;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out.v[e] = sum[e];
+    out.store_stream(static_cast<T*>(p.y) + t * p.d + c);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) clear_listed_kernel(unsigned* listed, int64_t rows) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t r = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (r < rows) listed[r] = 0;
+}
+__global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* place, int64_t total, unsigned* listed, int64_t rows) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t s = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (s >= total) return;
+  const int64_t r = place[s];
+  if (r >= 0 && r < rows) atomicAdd(&listed[r], 1u);
+}
+
+// Blocks of tokens, `share` threads each (32 or more): what a place's row gets where no other place lists it, and the products
+// that are the weights' gradients.  Behind them blocks of rows: zeros for rows that no place lists, and the sums, in order
+// of place, for rows that more than one does (found anew among all places: permutations have none).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRows p, int share, int64_t token_blocks) {
+  __shared__ float dots[kThreads / 32][kTogether];
+  __shared__ int todo[kThreads];
+  __shared__ unsigned n_todo, n_found;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const T* ys = static_cast<const T*>(p.ys);
+  const T* dy = static_cast<const T*>(p.dy);
+  const T* weights = static_cast<const T*>(p.weights);
+  T* dys = static_cast<T*>(p.dys);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (blockIdx.x < token_blocks) {
+    const int64_t t = int64_t(blockIdx.x) * (kThreads / share) + threadIdx.x / share;
+    const bool in = t < p.tokens;
+    const int at = threadIdx.x % share;
+    for (int j0 = 0; j0 < p.k; j0 += kTogether) {
+      int64_t row[kTogether];
+      float f[kTogether], dot[kTogether] = {};
+      bool sole[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        const int64_t s = t * p.k + j0 + j;
+        row[j] = in && j0 + j < p.k ? p.place[s] : -1;
+        if (row[j] >= p.rows) row[j] = -1;
+        f[j] = row[j] >= 0 && weights ? to_f32(weights[s]) : 1.0f;
+        sole[j] = dys && row[j] >= 0 && p.listed[row[j]] == 1;
+      }
+      for (int64_t c = int64_t(at) * VEC; in && c < p.d; c += int64_t(share) * VEC) {
+        Vec<T, VEC> g;
+        g.load_nc(dy + t * p.lddy + c);
+        Raw<T, VEC> v[kTogether];
+        if (p.dweights) {
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j)
+            if (row[j] >= 0) v[j].load_nc(ys + row[j] * p.ldy + c);
+        }
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+          if (row[j] < 0) continue;
+          if (p.dweights) {
+            Vec<T, VEC> x;
+            x.set_raw(v[j]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dot[j] = fmaf(x.v[e], g.v[e], dot[j]);
+          }
+          if (sole[j]) {
+            Vec<T, VEC> out;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) out.v[e] = f[j] * g.v[e];
+            out.store_stream(dys + row[j] * p.d + c);
+          }
+        }
+      }
+      if (!p.dweights) continue;
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot[j] += __shfl_xor_sync(~0u, dot[j], o);
+        if (lane == 0) dots[warp][j] = dot[j];
+      }
+      __syncthreads();
+      if (in && at < kTogether && j0 + at < p.k) {
+        float sum = 0.0f;
+        for (int w = 0; w < share / 32; ++w) sum += dots[warp + w][at];
+        static_cast<T*>(p.dweights)[t * p.k + j0 + at] = from_f32<T>(sum);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  if (threadIdx.x == 0) n_todo = 0;
+  __syncthreads();
+  const int64_t r0 = (int64_t(blockIdx.x) - token_blocks) * kThreads;
+  if (r0 + threadIdx.x < p.rows && p.listed[r0 + threadIdx.x] != 1) todo[atomicAdd(&n_todo, 1u)] = threadIdx.x;
+  __syncthreads();
+  const int64_t total = p.tokens * p.k;
+  for (unsigned q = 0; q < n_todo; ++q) {
+    const int64_t r = r0 + todo[q];
+    const unsigned times = p.listed[r];
+    for (int64_t c0 = 0; c0 < p.d; c0 += kThreads * VEC) {
+      const int64_t c = c0 + threadIdx.x * VEC;
+      Vec<T, VEC> sum;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum.v[e] = 0.0f;
+      unsigned seen = 0;
+      for (int64_t s0 = 0; seen < times && s0 < total; s0 += kThreads) {
+        const bool hit = s0 + threadIdx.x < total && p.place[s0 + threadIdx.x] == r;
+        const unsigned hits = __ballot_sync(~0u, hit);
+        __shared__ unsigned hit_mask[kThreads / 32];
+        __syncthreads();
+        if (lane == 0) hit_mask[warp] = hits;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 32; ++w)
+          for (unsigned m = hit_mask[w]; m; m &= m - 1) {
+            const int64_t s = s0 + w * 32 + __ffs(static_cast<int>(m)) - 1;
+            ++seen;
+            if (c >= p.d) continue;
+            const float f = weights ? to_f32(weights[s]) : 1.0f;
+            Vec<T, VEC> g;
+            g.load_nc(dy + s / p.k * p.lddy + c);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum.v[e] = fmaf(f, g.v[e], sum.v[e]);
+          }
+      }
+      if (c < p.d) sum.store_stream(dys + r * p.d + c);
+    }
+    __syncthreads();
+  }
+}
+
+// Whether rows can be read and written 16 bytes at a time.
+bool whole_vectors(int64_t size, int64_t d, std::initializer_list<const void*> at, std::initializer_list<int64_t> lds) {
+  uintptr_t low = static_cast<uintptr_t>(d * size);
+  for (const void* p : at) low |= reinterpret_cast<uintptr_t>(p);
+  for (int64_t ld : lds) low |= static_cast<uintptr_t>(ld * size);
+  return low % 16 == 0;
+}
+// Threads that share a token's row: a power of two, one vector each or more, a warp at least.
+int share_of(int64_t d, int vec) {
+  int share = 32;
+  while (share < kThreads && int64_t(share) * vec < d) share *= 2;
+  return share;
+}
+int64_t blocks_of(int64_t tokens, int share) { return (tokens + kThreads / share - 1) / (kThreads / share); }
+
+struct SortPlan {
+  int64_t blocks, chunk;
+  unsigned* counts;
+  int* rows;
+};
+// Blocks that rank the places: each reads the counts of all, so not more than 65536 counts.
+SortPlan plan_sort(Scratch& sc, const Dispatch& p) {
+  const int64_t total = p.tokens * p.k, sms = ops_sm_count();
+  SortPlan s;
+  s.blocks = (total + kSortThreads - 1) / kSortThreads;
+  if (s.blocks > sms) s.blocks = sms;
+  const int64_t most = 65536 / (p.experts + 1);
+  if (s.blocks > most) s.blocks = most < 8 ? 8 : most;
+  s.chunk = (total + s.blocks - 1) / s.blocks;
+  s.counts = sc.take<unsigned>(s.blocks * (p.experts + 1));
+  s.rows = sc.take<int>(total);
+  return s;
+}
+
+template <typename T, int VEC>
+cudaError_t move(const Dispatch& p, Scratch& sc, cudaStream_t st) {
+  MoveRows m{p.x, p.ldx, p.tokens, p.d, static_cast<int>(p.k), static_cast<int>(p.experts), p.idx, p.place, p.offsets, nullptr, p.xs};
+  const int64_t total = p.tokens * p.k;
+  if (total <= kFewPlaces)
+    return launch_after(dispatch_few_kernel<T, VEC>, static_cast<unsigned>(p.tokens + 1), kThreads, sizeof(unsigned) * (p.experts + 1), st, m);
+  const SortPlan s = plan_sort(sc, p);
+  m.rows = s.rows;
+  const size_t held = sizeof(unsigned) * static_cast<size_t>(p.experts + 1);
+  cudaError_t e = launch_after(expert_count_kernel, static_cast<unsigned>(s.blocks), kSortThreads, held, st, p.idx, total, s.chunk, m.experts, s.counts);
+  if (e == cudaSuccess)
+    e = launch_after(expert_rank_kernel, static_cast<unsigned>(s.blocks), kSortThreads, 2 * held, st, p.idx, total, s.chunk, m.experts,
+                     static_cast<const unsigned*>(s.counts), s.rows, p.place, p.offsets);
+  if (e != cudaSuccess) return e;
+  const int share = share_of(p.d, VEC);
+  return launch_after(dispatch_kernel<T, VEC>, static_cast<unsigned>(blocks_of(p.tokens, share)), kThreads, 0, st, m, share);
+}
+
+JoinRows join_of(const Combine& p) {
+  return JoinRows{p.ys, p.ldys, p.rows, p.tokens, p.d, static_cast<int>(p.k), p.place, p.weights, p.y, p.dy, p.lddy, nullptr, p.dys, p.dweights};
+}
+
+template <typename T, int VEC>
+cudaError_t backward(const Combine& p, Scratch& sc, cudaStream_t st) {
+  JoinRows q = join_of(p);
+  const int share = share_of(p.d, VEC);
+  const int64_t token_blocks = blocks_of(p.tokens, share), total = p.tokens * p.k;
+  int64_t row_blocks = 0;
+  if (p.dys) {
+    q.listed = sc.take<unsigned>(p.rows);
+    row_blocks = (p.rows + kThreads - 1) / kThreads;
+    cudaError_t e = launch_after(clear_listed_kernel, static_cast<unsigned>(row_blocks), kThreads, 0, st, q.listed, p.rows);
+    const unsigned blocks = static_cast<unsigned>((total + kThreads - 1) / kThreads);
+    if (e == cudaSuccess && blocks) e = launch_after(count_listed_kernel, blocks, kThreads, 0, st, p.place, total, q.listed, p.rows);
+    if (e != cudaSuccess) return e;
+  }
+  if (token_blocks + row_blocks > INT32_MAX) return cudaErrorNotSupported;
+  if (token_blocks + row_blocks == 0) return cudaSuccess;
+  return launch_after(combine_backward_kernel<T, VEC>, static_cast<unsigned>(token_blocks + row_blocks), kThreads, 0, st, q, share, token_blocks);
+}
+
+}  // namespace
+
+size_t dispatch_scratch_bytes(const Dispatch& p) {
+  if (p.tokens * p.k <= kFewPlaces) return 0;
+  Scratch sc;
+  plan_sort(sc, p);
+  return sc.used();
+}
+
+cudaError_t launch_dispatch(const Dispatch& p, Scratch& sc, cudaStream_t st) {
+  if (p.tokens + 1 > INT32_MAX) return cudaErrorNotSupported;
+  const bool f32 = p.dtype == kF32;
+  const bool wide = whole_vectors(f32 ? 4 : 2, p.d, {p.x, p.xs}, {p.ldx});
+  if (f32) return wide ? move<float, 4>(p, sc, st) : move<float, 1>(p, sc, st);
+  return wide ? move<__nv_bfloat16, 8>(p, sc, st) : move<__nv_bfloat16, 1>(p, sc, st);
+}
+
+cudaError_t launch_combine(const Combine& p, cudaStream_t st) {
+  const bool f32 = p.dtype == kF32;
+  const bool wide = whole_vectors(f32 ? 4 : 2, p.d, {p.ys, p.y}, {p.ldys});
+  const JoinRows q = join_of(p);
+  const int share = share_of(p.d, wide ? (f32 ? 4 : 8) : 1);
+  const unsigned blocks = static_cast<unsigned>(blocks_of(p.tokens, share));
+  if (f32) return wide ? launch_after(combine_kernel<float, 4>, blocks, kThreads, 0, st, q, share) : launch_after(combine_kernel<float, 1>, blocks, kThreads, 0, st, q, share);
+  return wide ? launch_after(combine_kernel<__nv_bfloat16, 8>, blocks, kThreads, 0, st, q, share)
+              : launch_after(combine_kernel<__nv_bfloat16, 1>, blocks, kThreads, 0, st, q, share);
+}
+
+size_t combine_backward_scratch_bytes(const Combine& p) {
+  Scratch sc;
+  if (p.dys) sc.take<unsigned>(p.rows);
+  return sc.used();
+}
+
+cudaError_t launch_combine_backward(const Combine& p, Scratch& sc, cudaStream_t st) {
+  const bool f32 = p.dtype == kF32;
+  const bool wide = whole_vectors(f32 ? 4 : 2, p.d, {p.dy, p.dweights ? p.ys : nullptr, p.dys}, {p.lddy, p.dweights ? p.ldys : 0});
+  if (f32) return wide ? backward<float, 4>(p, sc, st) : backward<float, 1>(p, sc, st);
+  return wide ? backward<__nv_bfloat16, 8>(p, sc, st) : backward<__nv_bfloat16, 1>(p, sc, st);
+}
+
+}  // namespace tk

@@ -193,4 +193,70 @@ struct TokenDraw {
 };
 cudaError_t launch_tokens(const TokenDraw& p, cudaStream_t st);
 
+// ---- rows by expert and back (kernels_experts.cu) ------------------------------
+constexpr int64_t kMostExperts = 4096;
+struct Dispatch {
+  const void* x;
+  int64_t ldx;
+  const int64_t* idx;
+  int64_t tokens, k, experts, d;
+  int dtype;
+  void* xs;
+  int64_t* place;
+  int64_t* offsets;
+};
+size_t dispatch_scratch_bytes(const Dispatch& p);
+cudaError_t launch_dispatch(const Dispatch& p, Scratch& sc, cudaStream_t st);
+// y, or from dy: dys and dweights (each nullable).
+struct Combine {
+  const void* ys;
+  int64_t ldys, rows;
+  const int64_t* place;
+  const void* weights;  // nullable
+  int64_t tokens, k, d;
+  int dtype;
+  void* y;
+  const void* dy;
+  int64_t lddy;
+  void* dys;
+  void* dweights;
+};
+cudaError_t launch_combine(const Combine& p, cudaStream_t st);
+size_t combine_backward_scratch_bytes(const Combine& p);
+cudaError_t launch_combine_backward(const Combine& p, Scratch& sc, cudaStream_t st);
+
+// ---- what stays in a cache (kernels_cache.cu) ----------------------------------
+// Rows of contiguous values: distances, in elements, between batches, heads and rows.
+struct View {
+  void* data;
+  int64_t batch, head, row;
+};
+struct Evict {
+  View keys, values;  // batch, head, position
+  View score;         // f32; batch, head (positions are contiguous)
+  const int64_t* lengths;
+  View weights;       // batch, query head, query (positions are contiguous); data may be null
+  int weights_dtype;
+  int64_t group, queries;
+  int dtype;
+  int64_t batch, heads, capacity, key_dim, value_dim, keep, recent;
+  void *out_keys, *out_values;
+  float* out_score;
+  int64_t *out_kept, *out_lengths;
+};
+size_t evict_scratch_bytes(const Evict& p);
+cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st);
+struct Replace {
+  View keys, values, score, positions;  // in place
+  const int64_t* lengths;
+  View key, value;    // batch, head
+  View weights;
+  int weights_dtype;
+  int64_t group, queries;
+  int dtype;
+  int64_t batch, heads, capacity, key_dim, value_dim, recent;
+  int64_t* slots;
+};
+cudaError_t launch_replace(const Replace& p, cudaStream_t st);
+
 }  // namespace tk

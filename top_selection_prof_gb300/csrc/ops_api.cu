@@ -329,6 +329,174 @@ int sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t n, c
   return status_of(launch_tokens(p, st));
 }
 
+// Whether rows of experts are described soundly; TOPK_OK or the error.
+int check_rows(int dtype, int64_t tokens, int64_t k, int64_t d, int64_t rows) {
+  if (!known_dtype(dtype) || tokens < 0 || k < 1 || d < 1 || rows < 0) return TOPK_EINVAL;
+  if (tokens > kMaxExtent || k > kMaxExtent || d > kMaxExtent || rows >= (int64_t(1) << 29)) return TOPK_EUNSUPPORTED;
+  return tokens * k >= (int64_t(1) << 29) ? TOPK_EUNSUPPORTED : TOPK_OK;
+}
+
+int dispatch(const Dispatch& p, cudaStream_t st) {
+  if (p.experts < 1) return TOPK_EINVAL;
+  if (int e = check_rows(p.dtype, p.tokens, p.k, p.d, 0)) return e;
+  if (p.experts > kMostExperts) return TOPK_EUNSUPPORTED;
+  if (!p.offsets) return TOPK_EINVAL;
+  const int64_t size = static_cast<int64_t>(value_bytes(p.dtype)), total = p.tokens * p.k;
+  if (p.tokens == 0) return status_of(cudaMemsetAsync(p.offsets, 0, sizeof(int64_t) * static_cast<size_t>(p.experts + 1), st));
+  if (!p.x || p.ldx < p.d || !p.idx || !p.xs || !p.place) return TOPK_EINVAL;
+  if (clash({vector(p.xs, total * p.d, size), vector(p.place, total, 8), vector(p.offsets, p.experts + 1, 8)},
+            {matrix(p.x, p.tokens, p.d, p.ldx, size), vector(p.idx, total, 8)}))
+    return TOPK_EINVAL;
+  void* base = nullptr;
+  Call call(st);
+  const cudaError_t e = call.scratch(dispatch_scratch_bytes(p), &base);
+  if (e != cudaSuccess) return call.end(e);
+  Scratch sc(base);
+  return call.end(launch_dispatch(p, sc, st));
+}
+
+int combine(const Combine& p, cudaStream_t st) {
+  if (int e = check_rows(p.dtype, p.tokens, p.k, p.d, p.rows)) return e;
+  if (p.tokens == 0) return TOPK_OK;
+  if (!p.place || !p.y || (p.rows > 0 && (!p.ys || p.ldys < p.d))) return TOPK_EINVAL;
+  const int64_t size = static_cast<int64_t>(value_bytes(p.dtype));
+  if (clash({vector(p.y, p.tokens * p.d, size)}, {matrix(p.ys, p.rows, p.d, p.ldys, size), vector(p.place, p.tokens * p.k, 8),
+                                                  vector(p.weights, p.tokens * p.k, size)}))
+    return TOPK_EINVAL;
+  return status_of(launch_combine(p, st));
+}
+
+int combine_backward(const Combine& p, cudaStream_t st) {
+  if (int e = check_rows(p.dtype, p.tokens, p.k, p.d, p.rows)) return e;
+  if (!p.dys && !p.dweights) return TOPK_OK;
+  const int64_t size = static_cast<int64_t>(value_bytes(p.dtype)), total = p.tokens * p.k;
+  if (p.tokens == 0)
+    return p.dys ? status_of(cudaMemsetAsync(p.dys, 0, static_cast<size_t>(size * p.rows * p.d), st)) : TOPK_OK;
+  if (!p.place || !p.dy || p.lddy < p.d || (p.dweights && p.rows > 0 && (!p.ys || p.ldys < p.d))) return TOPK_EINVAL;
+  if (clash({vector(p.dys, p.rows * p.d, size), vector(p.dweights, total, size)},
+            {matrix(p.dweights ? p.ys : nullptr, p.rows, p.d, p.ldys, size), matrix(p.dy, p.tokens, p.d, p.lddy, size),
+             vector(p.place, total, 8), vector(p.weights, total, size)}))
+    return TOPK_EINVAL;
+  void* base = nullptr;
+  Call call(st);
+  const cudaError_t e = call.scratch(combine_backward_scratch_bytes(p), &base);
+  if (e != cudaSuccess) return call.end(e);
+  Scratch sc(base);
+  return call.end(launch_combine_backward(p, sc, st));
+}
+
+// A cache's tensor: `row` contiguous bytes at each of batch x heads x rows places.
+struct Rows4 {
+  uintptr_t at;
+  int64_t n[3], by[3], row;  // places and the bytes between them, by batch, head and row
+  Rows4(const View& v, int64_t batch, int64_t heads, int64_t rows, int64_t dim, int64_t size)
+      : at(reinterpret_cast<uintptr_t>(v.data)), n{batch, heads, rows}, by{v.batch * size, v.head * size, v.row * size}, row(dim * size) {}
+  bool sound() const { return by[0] >= 0 && by[1] >= 0 && by[2] >= 0; }
+  bool any() const { return at && n[0] > 0 && n[1] > 0 && n[2] > 0 && row > 0; }
+  int64_t reach() const { return (n[0] - 1) * by[0] + (n[1] - 1) * by[1] + (n[2] - 1) * by[2] + row; }
+  // Whether no byte belongs to two places (as far as the distances, from the smallest on, each pass what lies within).
+  bool apart() const {
+    int64_t within = row;
+    bool used[3] = {};
+    for (int step = 0; step < 3; ++step) {
+      int d = -1;
+      for (int i = 0; i < 3; ++i)
+        if (!used[i] && n[i] > 1 && (d < 0 || by[i] < by[d])) d = i;
+      if (d < 0) break;
+      if (by[d] < within) return false;
+      used[d] = true;
+      within = (n[d] - 1) * by[d] + within;
+    }
+    return true;
+  }
+};
+// Whether two have a byte in common; where their distances differ, whether their ranges meet.
+bool meet(Rows4 a, Rows4 b) {
+  if (!a.any() || !b.any()) return false;
+  if (b.at < a.at) std::swap(a, b);
+  if (b.at - a.at >= static_cast<uintptr_t>(a.reach())) return false;
+  int64_t ld = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.by[i] != b.by[i])) return true;
+    if (a.n[i] > 1 && (ld == 0 || a.by[i] < ld)) ld = a.by[i];
+  }
+  if (ld < 1) return true;
+  for (int i = 0; i < 3; ++i)
+    if (a.n[i] > 1 && a.by[i] % ld) return true;
+  const int64_t d = static_cast<int64_t>((b.at - a.at) % static_cast<uintptr_t>(ld));
+  return d < a.row || d + b.row > ld;
+}
+bool clash(std::initializer_list<Rows4> outs, std::initializer_list<Rows4> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Rows4& i : ins)
+      if (meet(*o, i)) return true;
+    for (auto p = outs.begin(); p != o; ++p)
+      if (meet(*o, *p)) return true;
+  }
+  return false;
+}
+View view_of(const topk_view_t* v) { return v ? View{v->data, v->batch, v->head, v->row} : View{nullptr, 0, 0, 0}; }
+
+int check_cache(int dtype, int weights_dtype, bool weighted, int64_t batch, int64_t heads, int64_t capacity, int64_t key_dim,
+                int64_t value_dim, int64_t group, int64_t queries) {
+  if (!known_dtype(dtype) || batch < 0 || heads < 1 || capacity < 1 || key_dim < 1 || value_dim < 1) return TOPK_EINVAL;
+  if (weighted && (!known_dtype(weights_dtype) || group < 1 || queries < 0)) return TOPK_EINVAL;
+  if (batch > kMaxExtent || heads > kMaxExtent || capacity > kMaxExtent || key_dim > kMaxExtent || value_dim > kMaxExtent ||
+      (weighted && (group > kMaxExtent || queries > kMaxExtent)) || batch * heads > kMaxExtent)
+    return TOPK_EUNSUPPORTED;
+  // (byte counts stay below 2^63)
+  const int64_t most = int64_t(1) << 40, dim = key_dim > value_dim ? key_dim : value_dim;
+  if (dim > (1 << 20) || batch * heads > most / capacity || (weighted && group * queries > most / heads)) return TOPK_EUNSUPPORTED;
+  return TOPK_OK;
+}
+
+int evict(const Evict& p, cudaStream_t st) {
+  const bool weighted = p.weights.data != nullptr;
+  if (int e = check_cache(p.dtype, p.weights_dtype, weighted, p.batch, p.heads, p.capacity, p.key_dim, p.value_dim, p.group, p.queries)) return e;
+  if (p.keep < 1 || p.recent < 0 || p.recent > p.keep) return TOPK_EINVAL;
+  if (p.keep > kMaxExtent || p.batch * p.heads > (int64_t(1) << 40) / p.keep) return TOPK_EUNSUPPORTED;
+  if (p.batch == 0) return TOPK_OK;
+  if (!p.keys.data || !p.values.data || !p.score.data || !p.lengths || !p.out_keys || !p.out_values || !p.out_score || !p.out_kept || !p.out_lengths)
+    return TOPK_EINVAL;
+  const int64_t size = static_cast<int64_t>(value_bytes(p.dtype)), rows = p.batch * p.heads;
+  const Rows4 keys(p.keys, p.batch, p.heads, p.capacity, p.key_dim, size), values(p.values, p.batch, p.heads, p.capacity, p.value_dim, size);
+  const Rows4 score(p.score, p.batch, p.heads, 1, p.capacity, 4);
+  const Rows4 weights(p.weights, p.batch, p.heads * p.group, p.queries, weighted ? p.capacity : 0,
+                      weighted ? static_cast<int64_t>(value_bytes(p.weights_dtype)) : 1);
+  if (!keys.sound() || !values.sound() || !score.sound() || (weighted && !weights.sound())) return TOPK_EINVAL;
+  auto flat = [](const void* at, int64_t n, int64_t bytes) { return Rows4(View{const_cast<void*>(at), 0, 0, 0}, 1, 1, 1, n, bytes); };
+  if (clash({flat(p.out_keys, rows * p.keep * p.key_dim, size), flat(p.out_values, rows * p.keep * p.value_dim, size),
+             flat(p.out_score, rows * p.keep, 4), flat(p.out_kept, rows * p.keep, 8), flat(p.out_lengths, p.batch, 8)},
+            {keys, values, score, weights, flat(p.lengths, p.batch, 8)}))
+    return TOPK_EINVAL;
+  void* base = nullptr;
+  Call call(st);
+  const cudaError_t e = call.scratch(evict_scratch_bytes(p), &base);
+  if (e != cudaSuccess) return call.end(e);
+  Scratch sc(base);
+  return call.end(launch_evict(p, sc, st));
+}
+
+int replace(const Replace& p, cudaStream_t st) {
+  const bool weighted = p.weights.data != nullptr;
+  if (int e = check_cache(p.dtype, p.weights_dtype, weighted, p.batch, p.heads, p.capacity, p.key_dim, p.value_dim, p.group, p.queries)) return e;
+  if (p.recent < 0 || p.recent >= p.capacity) return TOPK_EINVAL;
+  if (p.batch == 0) return TOPK_OK;
+  if (!p.keys.data || !p.values.data || !p.score.data || !p.positions.data || !p.lengths || !p.key.data || !p.value.data || !p.slots) return TOPK_EINVAL;
+  const int64_t size = static_cast<int64_t>(value_bytes(p.dtype));
+  const Rows4 keys(p.keys, p.batch, p.heads, p.capacity, p.key_dim, size), values(p.values, p.batch, p.heads, p.capacity, p.value_dim, size);
+  const Rows4 score(p.score, p.batch, p.heads, 1, p.capacity, 4), positions(p.positions, p.batch, p.heads, 1, p.capacity, 8);
+  const Rows4 key(p.key, p.batch, p.heads, 1, p.key_dim, size), value(p.value, p.batch, p.heads, 1, p.value_dim, size);
+  const Rows4 weights(p.weights, p.batch, p.heads * p.group, p.queries, weighted ? p.capacity : 0,
+                      weighted ? static_cast<int64_t>(value_bytes(p.weights_dtype)) : 1);
+  const Rows4 slots(View{p.slots, p.heads, 1, 0}, p.batch, p.heads, 1, 1, 8), lengths(View{const_cast<int64_t*>(p.lengths), 1, 0, 0}, p.batch, 1, 1, 1, 8);
+  for (const Rows4* r : {&keys, &values, &score, &positions})
+    if (!r->sound() || !r->apart()) return TOPK_EINVAL;
+  if (!key.sound() || !value.sound() || (weighted && !weights.sound())) return TOPK_EINVAL;
+  if (clash({keys, values, score, positions, slots}, {key, value, weights, lengths})) return TOPK_EINVAL;
+  return status_of(launch_replace(p, st));
+}
+
 }  // namespace
 
 cudaError_t ops_take_status(cudaStream_t st, int* status) {
@@ -459,6 +627,52 @@ int topk_sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t
   return guarded([&] {
     return sample(logits, ld, dtype, rows, n, u, temperature, temperatures, top_k, top_ks, top_p, top_ps, min_p, min_ps, tokens,
                   logprobs, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_dispatch(const void* x, int64_t ldx, const int64_t* idx, int dtype, int64_t tokens, int64_t k, int64_t experts,
+                  int64_t d, void* xs, int64_t* place, int64_t* offsets, void* stream) {
+  return guarded([&] {
+    return dispatch(Dispatch{x, ldx, idx, tokens, k, experts, d, dtype, xs, place, offsets}, static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_combine(const void* ys, int64_t ldys, int64_t rows, const int64_t* place, const void* weights, int dtype,
+                 int64_t tokens, int64_t k, int64_t d, void* y, void* stream) {
+  return guarded([&] {
+    return combine(Combine{ys, ldys, rows, place, weights, tokens, k, d, dtype, y, nullptr, 0, nullptr, nullptr},
+                   static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_combine_backward(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t rows, const int64_t* place,
+                          const void* weights, int dtype, int64_t tokens, int64_t k, int64_t d, void* dys, void* dweights,
+                          void* stream) {
+  return guarded([&] {
+    return combine_backward(Combine{ys, ldys, rows, place, weights, tokens, k, d, dtype, nullptr, dy, lddy, dys, dweights},
+                            static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_evict(const topk_view_t* keys, const topk_view_t* values, const topk_view_t* score, const int64_t* lengths,
+               const topk_view_t* weights, int weights_dtype, int64_t group, int64_t queries, int dtype, int64_t batch,
+               int64_t heads, int64_t capacity, int64_t key_dim, int64_t value_dim, int64_t keep, int64_t recent,
+               void* out_keys, void* out_values, float* out_score, int64_t* out_kept, int64_t* out_lengths, void* stream) {
+  return guarded([&] {
+    return evict(Evict{view_of(keys), view_of(values), view_of(score), lengths, view_of(weights), weights_dtype, group, queries, dtype,
+                       batch, heads, capacity, key_dim, value_dim, keep, recent, out_keys, out_values, out_score, out_kept, out_lengths},
+                 static_cast<cudaStream_t>(stream));
+  });
+}
+
+int topk_replace(const topk_view_t* keys, const topk_view_t* values, const topk_view_t* score, const topk_view_t* positions,
+                 const int64_t* lengths, const topk_view_t* key, const topk_view_t* value, const topk_view_t* weights,
+                 int weights_dtype, int64_t group, int64_t queries, int dtype, int64_t batch, int64_t heads,
+                 int64_t capacity, int64_t key_dim, int64_t value_dim, int64_t recent, int64_t* slots, void* stream) {
+  return guarded([&] {
+    return replace(Replace{view_of(keys), view_of(values), view_of(score), view_of(positions), lengths, view_of(key), view_of(value),
+                           view_of(weights), weights_dtype, group, queries, dtype, batch, heads, capacity, key_dim, value_dim, recent, slots},
+                   static_cast<cudaStream_t>(stream));
   });
 }
 

@@ -2,14 +2,26 @@
 
     tokens, logprobs = tk.sample(logits, u, temperature=0.8, top_k=50, top_p=0.95)   # u: one random number a row
 
+    vals, idx = tk.select(router_logits, k)                       # k experts a token
+    xs, place, offsets = tk.dispatch(x, idx, experts)             # expert e: xs[offsets[e]:offsets[e + 1]]
+    y = tk.combine(ys, place, weights)                            # the way back
+    dys, dweights = tk.combine_backward(dy, ys, place, weights)
+    dx = tk.combine(dxs, place)                                   # dispatch's gradient
+
+    keys, values, score, kept, lengths = tk.evict(keys, values, score, lengths, keep, recent=64, weights=attention)
+    slots = tk.replace_(keys, values, score, positions, lengths, key, value, recent=64, weights=attention)
+
 As in operators.py: float32 or bfloat16 CUDA tensors with contiguous last dimensions, every step in the library's
 kernels, stream= as there, nothing recorded for autograd.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
-from .operators import _call, _empty, _first, _matrix, _vector
+from ._lib import TopkView
+from .operators import _CODES, _call, _empty, _first, _like, _matrix, _of_places, _vector
 
 
 def _by_row(v, dtype, device, rows, name):
@@ -45,3 +57,152 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
                                           tokens, logprobs), logits.data_ptr(), ld, code, rows, n, pu, t, pt, k, pk, p, pp, m, pm,
           tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs
+
+
+def _choices(t, tokens, device, name):
+    """k of an int64 tensor (tokens, k)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int64 or t.device != device:
+        raise TypeError("%s must be an int64 tensor on %s" % (name, device))
+    if t.dim() != 2 or (tokens is not None and t.shape[0] != tokens) or t.shape[1] < 1 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with shape (tokens, k), k >= 1, got %s" % (name, tuple(t.shape)))
+    return t.shape[1]
+
+
+def dispatch(x, idx, experts: int, stream=None):
+    """(xs, place, offsets): the rows of x (tokens, d) in the order of their experts.
+
+    idx (tokens, k), int64: each token's experts, as select gives them; one out of range (-1: dropped) has none.
+    xs (tokens * k, d): the rows of expert e are xs[offsets[e]:offsets[e + 1]], in the order of their tokens; rows left over
+    at the end are zeros.  place (tokens, k): each choice's row in xs, or -1.  offsets (experts + 1,): int64."""
+    code = _first(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (tokens, d)")
+    tokens, d = x.shape
+    dtype, device = x.dtype, x.device
+    ldx = _matrix(x, tokens, d, "x")
+    k = _choices(idx, tokens, device, "idx")
+    xs = _empty((tokens * k, d), dtype, device, stream)
+    place = _empty((tokens, k), torch.int64, device, stream)
+    offsets = _empty((max(experts, 0) + 1,), torch.int64, device, stream)
+    _call("topk_dispatch", device, stream, (x, idx, xs, place, offsets), x.data_ptr(), ldx, idx.data_ptr(), code, tokens, k,
+          experts, d, xs.data_ptr(), place.data_ptr(), offsets.data_ptr())
+    return xs, place, offsets
+
+
+def combine(ys, place, weights=None, stream=None):
+    """y (tokens, d): y[t] = sum of weights[t, j] ys[place[t, j]] over j; places out of range add nothing.
+
+    place (tokens, k) as from dispatch; weights (tokens, k) of ys's dtype, or None: all 1 (dispatch's gradient)."""
+    code = _first(ys)
+    if ys.dim() != 2:
+        raise ValueError("ys must be 2-D (rows, d)")
+    rows, d = ys.shape
+    dtype, device = ys.dtype, ys.device
+    ldys = _matrix(ys, rows, d, "ys")
+    k = _choices(place, None, device, "place")
+    pw = None if weights is None else _of_places(weights, place, dtype, device, "weights")
+    y = _empty((place.shape[0], d), dtype, device, stream)
+    _call("topk_combine", device, stream, (ys, place, weights, y), ys.data_ptr(), ldys, rows, place.data_ptr(), pw, code,
+          place.shape[0], k, d, y.data_ptr())
+    return y
+
+
+def combine_backward(dy, ys, place, weights=None, need=(True, True), stream=None):
+    """(dys, dweights) of combine from dy (tokens, d); None where `need` is false."""
+    code = _first(dy)
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D (tokens, d)")
+    tokens, d = dy.shape
+    dtype, device = dy.dtype, dy.device
+    _like(ys, dtype, device, "ys")
+    if ys.dim() != 2:
+        raise ValueError("ys must be 2-D (rows, d)")
+    rows = ys.shape[0]
+    lddy, ldys = _matrix(dy, tokens, d, "dy"), _matrix(ys, rows, d, "ys")
+    k = _choices(place, tokens, device, "place")
+    pw = None if weights is None else _of_places(weights, place, dtype, device, "weights")
+    dys = _empty((rows, d), dtype, device, stream) if need[0] else None
+    dw = _empty((tokens, k), dtype, device, stream) if need[1] else None
+    _call("topk_combine_backward", device, stream, (dy, ys, place, weights, dys, dw), dy.data_ptr(), lddy, ys.data_ptr(), ldys,
+          rows, place.data_ptr(), pw, code, tokens, k, d, None if dys is None else dys.data_ptr(),
+          None if dw is None else dw.data_ptr())
+    return dys, dw
+
+
+def _view(t, dtype, device, shape, name):
+    """A TopkView of a tensor (batch, heads, rows, values), or without the dimension of rows, whose values are contiguous."""
+    _like(t, dtype, device, name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    by = t.stride()
+    if by[-1] != 1 and shape[-1] > 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    return TopkView(t.data_ptr(), by[0], by[1], by[2] if len(shape) == 4 else 0)
+
+
+def _cache(keys, values, score, lengths, weights):
+    """Checks what evict and replace_ have in common: (code, batch, heads, capacity, views, weights' view, dtype, group, queries)."""
+    code = _first(keys)
+    if keys.dim() != 4:
+        raise ValueError("keys must be 4-D (batch, heads, capacity, dim)")
+    batch, heads, capacity, _ = keys.shape
+    dtype, device = keys.dtype, keys.device
+    if not isinstance(values, torch.Tensor) or values.dim() != 4:
+        raise ValueError("values must be 4-D (batch, heads, capacity, dim)")
+    views = (_view(keys, dtype, device, keys.shape, "keys"),
+             _view(values, dtype, device, (batch, heads, capacity, values.shape[3]), "values"),
+             _view(score, torch.float32, device, (batch, heads, capacity), "score"))
+    _vector(lengths, torch.int64, device, batch, "lengths")
+    if weights is None:
+        return code, batch, heads, capacity, views, None, code, 1, 0
+    if not isinstance(weights, torch.Tensor) or weights.dtype not in _CODES or weights.dim() != 4:
+        raise TypeError("weights must be a 4-D float32 or bfloat16 tensor (batch, query heads, queries, capacity)")
+    query_heads, queries = weights.shape[1], weights.shape[2]
+    if query_heads < heads or query_heads % heads:
+        raise ValueError("weights must have a multiple of the cache's %d heads, got %d" % (heads, query_heads))
+    view = _view(weights, weights.dtype, device, (batch, query_heads, queries, capacity), "weights")
+    return code, batch, heads, capacity, views, view, _CODES[weights.dtype], query_heads // heads, queries
+
+
+def evict(keys, values, score, lengths, keep: int, recent: int = 0, weights=None, stream=None):
+    """(keys, values, score, kept, lengths): a cache cut down to `keep` positions of each head.
+
+    keys, values (batch, heads, capacity, dim); score (batch, heads, capacity), float32: the attention weight that each
+    position has had; lengths (batch,), int64: the positions that hold tokens.  What stays: the last `recent` ones and
+    those of the others with the largest scores (equal ones by position), in the order of their positions.
+    weights (batch, query heads, queries, capacity), float32 or bfloat16: what the queries of each head's group gave,
+    added first (a NaN counts as 0).  kept (batch, heads, keep): positions, -1 behind the new lengths, where rows and
+    scores are zeros.  Nothing is changed in place."""
+    code, batch, heads, capacity, views, view, wcode, group, queries = _cache(keys, values, score, lengths, weights)
+    dtype, device = keys.dtype, keys.device
+    kd, vd = keys.shape[3], values.shape[3]
+    rows = max(keep, 0)
+    ok, ov = _empty((batch, heads, rows, kd), dtype, device, stream), _empty((batch, heads, rows, vd), dtype, device, stream)
+    osc = _empty((batch, heads, rows), torch.float32, device, stream)
+    kept = _empty((batch, heads, rows), torch.int64, device, stream)
+    ol = _empty((batch,), torch.int64, device, stream)
+    _call("topk_evict", device, stream, (keys, values, score, lengths, weights, ok, ov, osc, kept, ol),
+          *map(ctypes.byref, views), lengths.data_ptr(), None if view is None else ctypes.byref(view), wcode, group, queries,
+          code, batch, heads, capacity, kd, vd, keep, recent, ok.data_ptr(), ov.data_ptr(), osc.data_ptr(), kept.data_ptr(),
+          ol.data_ptr())
+    return ok, ov, osc, kept, ol
+
+
+def replace_(keys, values, score, positions, lengths, key, value, recent: int = 0, weights=None, stream=None):
+    """Puts one new token into each sequence's cache, in place; returns the slots (batch, heads) that it took.
+
+    lengths (batch,): tokens before it.  While there are fewer than slots it takes the next one; then the one whose
+    score is least, of those that hold positions before the last `recent` (equal ones: the lowest slot).  key, value
+    (batch, heads, dim); positions (batch, heads, capacity), int64: the position in each slot; weights as in evict, by slot,
+    added to the scores first.  The slot's score becomes 0.  lengths is not changed."""
+    code, batch, heads, capacity, views, view, wcode, group, queries = _cache(keys, values, score, lengths, weights)
+    dtype, device = keys.dtype, keys.device
+    kd, vd = keys.shape[3], values.shape[3]
+    at = _view(positions, torch.int64, device, (batch, heads, capacity), "positions")
+    new = _view(key, dtype, device, (batch, heads, kd), "key"), _view(value, dtype, device, (batch, heads, vd), "value")
+    slots = _empty((batch, heads), torch.int64, device, stream)
+    _call("topk_replace", device, stream, (keys, values, score, positions, lengths, key, value, weights, slots),
+          *map(ctypes.byref, views), ctypes.byref(at), lengths.data_ptr(), *map(ctypes.byref, new),
+          None if view is None else ctypes.byref(view), wcode, group, queries, code, batch, heads, capacity, kd, vd, recent,
+          slots.data_ptr())
+    return slots
