@@ -15,12 +15,14 @@
 // token as in 64 bits.  (In f32 sums, one row in some thousand of a flat
 // distribution over 100000 tokens would give a neighbour of the right token.)
 //
-// A cluster holds a row in its shared memory, a part a block, and reads it from
-// memory once.  Bins of t (64 an octave, 16 octaves at a time) take the counts and
-// masses; the first block of the cluster adds them up, finds the bin where the
-// border lies, has the others send it the tokens of that bin (or of all bins up to
-// it where those are few) and finds the token among them by digits of (value,
-// index).  A bin with more tokens than it can hold is narrowed by digits over the cluster first.
+// The filter of the selection, applied to a row: a sample gives a threshold that
+// some hundred tokens reach.  One pass over the row lists those (the head) and,
+// where the rest can matter, adds the others (the tail) up by bins of t, 64 an octave.  The
+// first block of a row's cluster then searches the head by digits of (value,
+// index), or the tail: the bin where the border lies, whose tokens the blocks send
+// it in a second pass.  A bin with more tokens than it can hold is narrowed by
+// digits first, and a head that it cannot hold (a row of equal values) is searched
+// like a tail.
 #include <cfloat>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -39,15 +41,23 @@ constexpr int kOctaves = 16;                 // octaves that one histogram cover
 constexpr int kBins = kSub * kOctaves;
 constexpr int kWindows = 3;                  // weights below 2^-48 of the largest count as zero
 constexpr float kDeepest = kOctaves * kWindows;
-constexpr int kCap = 2048;                   // tokens that the first block searches itself
-constexpr int kEach = kCap / kThreads;
+constexpr int kHeadCap = 2560;               // tokens that the first block searches itself, of the head
+constexpr int kListCap = 1536;               // and of bins
+constexpr int kHead = 1024;                  // tokens that the head should have
+constexpr int kHeadOnly = 256;               // a top_k up to this is searched in the head alone
 constexpr int kIndexBits = 18;
 constexpr int kTailBits = 14;                // bits below a mass's unit that the sum behind the histogram keeps
+constexpr int64_t kPartMost = 131072;         // tokens of a block's part
+constexpr int kMostBlocks = 8;               // of a cluster
+// bf16 values of 2^-13 to 2^9 and their negatives are counted by value first
+constexpr unsigned kLeastValue = 0x3900, kValues = 0x4400 - 0x3900;
 constexpr int kDigitBits = 9;                // of the search by digits: a bin a thread
 static_assert(kTokensMaxLen <= int64_t(1) << kIndexBits, "an index fits its bits");
 static_assert(kBins == 2 * kThreads && (1 << kDigitBits) == kThreads, "bins by thread");
 
-// 2^30 x 2^-(i/64 + 1/128): the weight in the middle of bin i of an octave.
+constexpr double kLargest = 1073741822.0;    // the largest weight
+// kLargest x 2^-(i/64 + 1/128): the weight in the middle of bin i of an octave.  (So every weight is below 2^30, and the
+// two halves of kPartMost weights sum to less than 2^32.)
 struct Middles {
   unsigned v[kSub];
 };
@@ -61,7 +71,7 @@ constexpr Middles middles() {
   }
   root = of;
   Middles m{};
-  double w = 1073741824.0 / root;
+  double w = kLargest / root;
   for (int i = 0; i < kSub; ++i) {
     m.v[i] = static_cast<unsigned>(w + 0.5);
     w /= root * root;
@@ -70,9 +80,9 @@ constexpr Middles middles() {
 }
 __constant__ Middles kMiddles = middles();
 
-// How a row's values become weights: t = (most - x) (hi + lo), for x >= least.
+// How values become weights: t = (most - x) (hi + lo), for x >= least and not x >= below (NaN: no bound).
 struct Scale {
-  float most, least, hi, lo;
+  float most, least, below, hi, lo;
 };
 
 // round(64 t - 1/2): the bin of x, from 0 on; -1 for what has no weight (NaN and -inf among it).
@@ -81,7 +91,7 @@ __device__ __forceinline__ int bin_of(float x, const Scale& s, float* depth) {
   const float d = x == s.most ? 0.0f : s.most - x;
   const float t = d * s.hi;
   *depth = t;
-  if (!(x >= s.least) || !(t < kDeepest)) return -1;
+  if (!(x >= s.least) || x >= s.below || !(t < kDeepest)) return -1;
   return __float_as_int(fmaf(t, static_cast<float>(kSub), -0.5f) + kMagic) - __float_as_int(kMagic);
 }
 // The weight of x in bin j: the result times 2^-(30 + j / 64) (j / 64 a whole number), below 2^30.
@@ -113,37 +123,81 @@ __device__ __forceinline__ int index_of(uint64_t key) {
 enum : int { kOpDone, kOpBins, kOpBits, kOpDigits, kOpGather };
 // What the first block asks of all.
 struct Order {
+  Scale scale;
   int op, window;
   int from, to;           // bins [from, to) of the window
   uint64_t mask, value;   // keys with key & mask == value
   int shift;              // digits: (key >> shift) of kDigitBits
+  float low, high;        // no value of the bins lies outside
+  int unused;
 };
 
+// Tokens in no order with their masses, and the sums of those before each first digit of their keys that differs.
+template <int CAP>
+struct PileShared {
+  uint64_t key[CAP], mass[CAP];
+  uint64_t mass_before[kThreads + 1];
+  unsigned count_before[kThreads + 1];
+  unsigned n;       // listed (where more than CAP: not all)
+  Scale scale;      // what they weigh, in the unit of a window
+  int window;
+  int shift;        // the first digit's place
+  uint64_t above;   // the keys' common bits over it
+  uint64_t total;   // mass of those with a weight, and how many
+  unsigned count;
+};
+
+// All state of a block is here: what a thread keeps beside its registers goes through the little L1 that is left.
 struct Shared {
-  unsigned count[kBins], low[kBins], high[kBins];  // this block's; a bin's mass is low + high 2^15
+  unsigned count[kBins];                 // this block's bins; a bin's mass is low + high 2^15
+  alignas(16) unsigned low[kBins];
+  unsigned high[kBins];
   unsigned middle[kSub];
-  float maxes[16];            // of each block, in every block
   uint64_t warp_mass[kWarps];
   unsigned warp_count[kWarps];
-  uint64_t tail;              // this block's mass behind the window
+  unsigned group_max[32];
+  uint64_t tail;                         // this block's mass behind the window
   Order order;
+  const void* row;                       // this block's part: indices begin ... end - 1 of n
+  int begin, end, n;
+  Scale scale;                           // of the first pass
+  PileShared<kHeadCap> head;                     // (of each block its own part, then the first block's has all)
   // of the first block
+  float maxes[kMostBlocks];
+  uint64_t tails[kMostBlocks], ors[kMostBlocks], ands[kMostBlocks];
+  // the tail: the window's bins, and sums before each
+  Scale tail_scale;
+  int window;
   uint64_t mass_before[kBins + 1];
   unsigned count_before[kBins + 1];
-  uint64_t tails[16], ors[16], ands[16];
-  uint64_t list[kCap];
-  unsigned listed;
+  uint64_t mass, behind;                 // of the window; behind it (kTailBits more)
+  unsigned counted;
+  union {
+    PileShared<kListCap> list;                   // bins [list_from, list_to) of list_window
+    unsigned by_value[2 * kValues];      // bf16: tokens of each value, while bins are filled
+  };
+  int list_window, list_from, list_to;
+  // a crossing: the token where a sum passes a border, and the mass up to and with it
   int found;
-  uint64_t found_key;
+  uint64_t found_key, found_before, found_mass;
+  unsigned few, bits[4];
+  uint64_t few_key[32], few_mass[32];
+  float least;
 };
+// The block's own.  (Not handed down as a reference: the compiler has to see that it is shared memory.)
+__device__ __forceinline__ Shared& own() {
+  extern __shared__ __align__(16) unsigned char smem[];
+  return *reinterpret_cast<Shared*>(smem);
+}
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One value for each thread of the block: sums over the threads before.
-__device__ __forceinline__ void scan_before(Shared& s, uint64_t mass, unsigned count, uint64_t* mass_before, unsigned* count_before,
-                                            uint64_t* mass_all, unsigned* count_all) {
+// One value for each thread of the block: sums over the threads before, and over all.
+__device__ __forceinline__ void scan_before(uint64_t mass, unsigned count, uint64_t* mass_before, unsigned* count_before, uint64_t* mass_all,
+                                            unsigned* count_all) {
+  Shared& s = own();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint64_t m = mass;
   unsigned c = count;
@@ -181,484 +235,822 @@ __device__ __forceinline__ void scan_before(Shared& s, uint64_t mass, unsigned c
   __syncthreads();
 }
 
-template <typename T>
-struct Part {        // this block's part of the row
-  const T* data;     // shared memory; what is outside the row is -inf
-  int slots;         // multiple of a vector
-  int index0;        // index in the row of slot 0 (may be negative)
-  template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    constexpr int kVec = 16 / sizeof(T);
-    for (int at = threadIdx.x * kVec; at < slots; at += kThreads * kVec) {
-      Vec<T, kVec> v;
-      v.load(data + at);
+// f(values, as they are stored, index of the first) for the block's part of the row, 16 bytes of values at a time; what is outside
+// the row is -inf.
+template <typename T, int kAhead, typename F>
+__device__ __forceinline__ void each_vector(F f) {
+  constexpr int kVec = 16 / sizeof(T);
+  const Shared& s = own();
+  const T* row = static_cast<const T*>(s.row);
+  const int begin = s.begin, end = s.end, n = s.n;
+  for (int at = begin + threadIdx.x * kVec; at < end; at += kAhead * kThreads * kVec) {
+    Raw<T, kVec> raw[kAhead];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) f(v.v[e], index0 + at + e);
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = at + a * kThreads * kVec;
+      raw[a].clear();
+      if (i >= 0 && i + kVec <= n && i < end) raw[a].u = ld_stream_v4(row + i);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = at + a * kThreads * kVec;
+      if (i >= end) break;
+      if (!(i >= 0 && i + kVec <= n)) {  // (an end of the row)
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const T x = i + e >= 0 && i + e < n ? row[i + e] : from_f32<T>(-INFINITY);
+          if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(x);
+          else w[e / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x)) << 16 * (e % 2);
+        }
+        raw[a].u = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      Vec<T, kVec> v;
+      v.set_raw(raw[a]);
+      f(v, raw[a], i);
     }
   }
-};
+}
 
-// What every block of the cluster does for one order; `first`: the first block's shared memory.
 template <typename T>
-__device__ void serve(Shared& s, Shared& first, cg::cluster_group& cluster, const Order& o, const Part<T>& part, const Scale& scale) {
-  const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
-  const int lane = threadIdx.x % 32;
-  const int base = o.window * kBins;
-  if (o.op == kOpBins || o.op == kOpDigits) {
-    for (int b = threadIdx.x; b < kBins; b += kThreads) s.count[b] = s.low[b] = s.high[b] = 0;
-    if (threadIdx.x == 0) s.tail = 0;
-    __syncthreads();
-    uint64_t tail = 0;
-    part.each([&](float x, int index) {
-      float t;
-      const int j = bin_of(x, scale, &t) - base;
-      if (o.op == kOpBins) {
-        if (j < 0 || t >= kDeepest) return;
-        const unsigned w = weight_in(x, j + base, t, scale, s.middle);
-        if (j < kBins) {
-          atomicAdd(&s.count[j], 1u);
-          atomicAdd(&s.low[j], w & 0x7fffu);
-          atomicAdd(&s.high[j], w >> 15);
-        } else {
-          const int up = kOctaves - 1 + kTailBits - j / kSub;
-          tail += up >= 0 ? static_cast<uint64_t>(w) << up : w >> -up;
+__device__ __forceinline__ void clear_bins() {
+  Shared& s = own();
+  for (int b = threadIdx.x; b < kBins; b += kThreads) s.count[b] = s.low[b] = s.high[b] = 0;
+  if constexpr (sizeof(T) == 2)
+    for (unsigned i = threadIdx.x; i < 2 * kValues; i += kThreads) s.by_value[i] = 0;
+  if (threadIdx.x == 0) s.tail = 0;
+}
+// Adds `times` tokens of value x to its bin of the window that begins `base` bins down, or to the mass behind it.
+__device__ __forceinline__ void add_to_bins(float x, unsigned times, const Scale& scale, int base, uint64_t* tail) {
+  Shared& s = own();
+  float t;
+  const int j = bin_of(x, scale, &t) - base;
+  if (j < 0) return;
+  const unsigned w = weight_in(x, j + base, t, scale, s.middle);
+  if (j < kBins) {
+    atomicAdd(&s.count[j], times);
+    atomicAdd(&s.low[j], (w & 0x7fffu) * times);
+    atomicAdd(&s.high[j], (w >> 15) * times);
+  } else {
+    const int up = kOctaves - 1 + kTailBits - j / kSub;
+    const uint64_t m = static_cast<uint64_t>(w) * times;
+    *tail += up >= 0 ? m << up : m >> -up;
+  }
+}
+// The bins of the block's part.  (They are clear, and the counts by value.)  A bf16 row has few values among its tokens: they
+// are counted by value, one atomic each, and each value's weight is formed once.
+template <typename T, typename F>
+__device__ __forceinline__ void fill_bins(const Scale& scale, int base, F look) {
+  constexpr int kVec = 16 / sizeof(T);
+  Shared& s = own();
+  uint64_t tail = 0;
+  if constexpr (sizeof(T) == 4) {
+    each_vector<T, 2>([&](const Vec<T, kVec>& v, const Raw<T, kVec>&, int i) {
+      look(v, i);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) add_to_bins(v.v[e], 1, scale, base, &tail);
+    });
+  } else {
+    each_vector<T, 4>([&](const Vec<T, kVec>& v, const Raw<T, kVec>& raw, int i) {
+      look(v, i);
+      const uint32_t w[4] = {raw.u.x, raw.u.y, raw.u.z, raw.u.w};
+      bool all = true;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const unsigned h = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+        const unsigned at = (h & 0x7fffu) - kLeastValue;
+        if (at < kValues) atomicAdd(&s.by_value[at + (h >> 15) * kValues], 1u);
+        else all = false;
+      }
+      if (!all) {
+#pragma unroll 1
+        for (int e = 0; e < kVec; ++e) {
+          const uint32_t pair = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
+          const unsigned h = e & 1 ? pair >> 16 : pair & 0xffffu;
+          if ((h & 0x7fffu) - kLeastValue >= kValues) add_to_bins(__uint_as_float(h << 16), 1, scale, base, &tail);
         }
-      } else if (j >= o.from && j < o.to) {
-        const uint64_t key = token_key(x, index);
-        if ((key & o.mask) != o.value) return;
-        const unsigned w = weight_in(x, j + base, t, scale, s.middle);
-        const int digit = (1 << kDigitBits) - 1 - static_cast<int>((key >> o.shift) & ((1 << kDigitBits) - 1));
-        atomicAdd(&s.count[digit], 1u);
-        atomicAdd(&s.low[digit], w & 0x7fffu);
-        atomicAdd(&s.high[digit], w >> 15);
       }
     });
-    if (o.op == kOpBins) {
-#pragma unroll
-      for (int d = 16; d; d >>= 1) tail += __shfl_xor_sync(~0u, tail, d);
-      if (lane == 0 && tail) atomicAdd(reinterpret_cast<unsigned long long*>(&s.tail), static_cast<unsigned long long>(tail));
+    __syncthreads();
+#pragma unroll 1
+    for (unsigned at = threadIdx.x; at < 2 * kValues; at += kThreads) {
+      const unsigned times = s.by_value[at];
+      const unsigned h = at < kValues ? kLeastValue + at : 0x8000u + kLeastValue + at - kValues;
+      if (times) add_to_bins(__uint_as_float(h << 16), times, scale, base, &tail);
     }
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) tail += __shfl_xor_sync(~0u, tail, d);
+  if (threadIdx.x % 32 == 0 && tail) atomicAdd(reinterpret_cast<unsigned long long*>(&s.tail), static_cast<unsigned long long>(tail));
+}
+// Each block adds up its share of the cluster's bins and puts them into the first block's.  (After a cluster barrier.)
+__device__ __forceinline__ void join_bins() {
+  Shared& s = own();
+  cg::cluster_group cluster = cg::this_cluster();
+  Shared* first = cluster.map_shared_rank(&s, 0);
+  const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
+  const int share = (kBins + blocks - 1) / blocks;
+  for (int b = rank * share + threadIdx.x; b < min((rank + 1) * share, kBins); b += kThreads) {
+    unsigned count = 0;
+    uint64_t low = 0, high = 0;
+    for (int p = 0; p < blocks; ++p) {
+      const Shared* peer = cluster.map_shared_rank(&s, p);
+      count += peer->count[b];
+      low += peer->low[b];
+      high += peer->high[b];
+    }
+    first->mass_before[b] = low + (high << 15);
+    first->count_before[b] = count;
+  }
+  if (threadIdx.x == 0) first->tails[rank] = s.tail;
+}
+
+// The first block's order, put into every block's memory.
+__device__ __forceinline__ void tell() {
+  Shared& s = own();
+  static_assert(sizeof(Order) % 8 == 0, "whole words");
+  constexpr int kWords = sizeof(Order) / 8;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = static_cast<int>(cluster.num_blocks());
+  if (blocks > 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < (blocks - 1) * kWords; i += kThreads)
+      reinterpret_cast<uint64_t*>(&cluster.map_shared_rank(&s, 1 + i / kWords)->order)[i % kWords] = reinterpret_cast<const uint64_t*>(&s.order)[i % kWords];
+  }
+  cluster_sync();
+}
+template <bool HEAD>
+__device__ __forceinline__ auto& pile(Shared& s) {
+  if constexpr (HEAD) return s.head;
+  else return s.list;
+}
+// Moves this block's part of a pile to the first block's.  (Before a cluster barrier.)
+template <bool HEAD>
+__device__ __forceinline__ void hand_over() {
+  Shared& s = own();
+  auto& from = pile<HEAD>(s);
+  auto& to = pile<HEAD>(*cg::this_cluster().map_shared_rank(&s, 0));
+  __syncthreads();
+  if (threadIdx.x == 0) s.found = static_cast<int>(atomicAdd(&to.n, from.n));
+  __syncthreads();
+  constexpr unsigned kCap = HEAD ? kHeadCap : kListCap;
+  const unsigned n = min(from.n, kCap), at = static_cast<unsigned>(s.found);
+  for (unsigned i = threadIdx.x; i < n; i += kThreads)
+    if (at + i < kCap) to.key[at + i] = from.key[i];
+}
+
+// What every block of the cluster does for the order that it holds.
+template <typename T>
+__device__ __noinline__ void serve() {
+  constexpr int kVec = 16 / sizeof(T);
+  Shared& s = own();
+  const Scale scale = s.order.scale;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int op = s.order.op, base = s.order.window * kBins;
+  if (op == kOpBins) {
+    clear_bins<T>();
+    __syncthreads();
+    fill_bins<T>(scale, base, [](const Vec<T, kVec>&, int) {});
     cluster_sync();
-    // each block adds up its share of the bins and puts them into the first block's
-    const int share = kBins / blocks;
-    for (int b = rank * share + threadIdx.x; b < (rank + 1) * share; b += kThreads) {
-      unsigned count = 0;
-      uint64_t low = 0, high = 0;
-      for (int p = 0; p < blocks; ++p) {
-        const Shared* peer = cluster.map_shared_rank(&s, p);
-        count += peer->count[b];
-        low += peer->low[b];
-        high += peer->high[b];
-      }
-      first.mass_before[b] = low + (high << 15);
-      first.count_before[b] = count;
+    join_bins();
+  } else {
+    if (op == kOpGather) {
+      if (threadIdx.x == 0) s.list.n = 0;
+      cluster_sync();  // (before others add to the first block's)
     }
-    if (threadIdx.x == 0) first.tails[rank] = s.tail;
-  } else if (o.op == kOpBits) {
-    uint64_t any = 0, all = ~uint64_t(0);
-    part.each([&](float x, int index) {
-      float t;
-      const int j = bin_of(x, scale, &t) - base;
-      if (j < o.from || j >= o.to) return;
-      const uint64_t key = token_key(x, index);
-      any |= key;
-      all &= key;
-    });
+    if (op == kOpDigits) {
+      clear_bins<T>();
+      __syncthreads();
+    }
+    const float low = s.order.low, high = s.order.high;
+    uint64_t any = 0, none = 0;
+    each_vector<T, 4>([&](const Vec<T, kVec>& v, const Raw<T, kVec>&, int i) {
+      unsigned near = 0;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      any |= __shfl_xor_sync(~0u, any, d);
-      all &= __shfl_xor_sync(~0u, all, d);
-    }
-    __syncthreads();
-    if (lane == 0) s.warp_mass[threadIdx.x / 32] = any;
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int w = 1; w < kWarps; ++w) any |= s.warp_mass[w];
-    __syncthreads();
-    if (lane == 0) s.warp_mass[threadIdx.x / 32] = all;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kWarps; ++w) all &= s.warp_mass[w];
-      first.ors[rank] = any;
-      first.ands[rank] = all;
-    }
-  } else if (o.op == kOpGather) {
-    part.each([&](float x, int index) {
-      float t;
-      const int j = bin_of(x, scale, &t) - base;
-      if (j < o.from || j >= o.to) return;
-      const uint64_t key = token_key(x, index);
-      if ((key & o.mask) != o.value) return;
-      const unsigned at = atomicAdd(&first.listed, 1u);
-      if (at < kCap) first.list[at] = key;
+      for (int e = 0; e < kVec; ++e) near |= v.v[e] >= low && v.v[e] <= high ? 1u << e : 0;
+#pragma unroll 1
+      for (; near; near &= near - 1) {
+        const int e = __ffs(static_cast<int>(near)) - 1;
+        float x = v.v[0];
+#pragma unroll
+        for (int q = 1; q < kVec; ++q) x = e == q ? v.v[q] : x;
+        float t;
+        const int j = bin_of(x, scale, &t) - base;
+        if (j < s.order.from || j >= s.order.to) continue;
+        const uint64_t key = token_key(x, i + e);
+        if ((key & s.order.mask) != s.order.value) continue;
+        if (op == kOpGather) {
+          const unsigned at = atomicAdd(&s.list.n, 1u);
+          if (at < kListCap) s.list.key[at] = key;
+        } else if (op == kOpBits) {
+          any |= key;
+          none |= ~key;
+        } else {
+          const unsigned w = weight_in(x, j + base, t, scale, s.middle);
+          const int digit = (1 << kDigitBits) - 1 - static_cast<int>((key >> s.order.shift) & ((1 << kDigitBits) - 1));
+          atomicAdd(&s.count[digit], 1u);
+          atomicAdd(&s.low[digit], w & 0x7fffu);
+          atomicAdd(&s.high[digit], w >> 15);
+        }
+      }
     });
+    if (op == kOpGather) {
+      if (rank != 0) hand_over<false>();
+    } else if (op == kOpDigits) {
+      cluster_sync();
+      join_bins();
+    } else {
+      Shared* first = cluster.map_shared_rank(&s, 0);
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
+        uint64_t v = which ? none : any;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v |= __shfl_xor_sync(~0u, v, d);
+        if (threadIdx.x % 32 == 0) s.warp_mass[threadIdx.x / 32] = v;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          for (int w = 1; w < kWarps; ++w) v |= s.warp_mass[w];
+          if (which) first->ands[rank] = ~v;
+          else first->ors[rank] = v;
+        }
+        __syncthreads();
+      }
+    }
   }
   cluster_sync();
 }
 
-// Where a sum over the order passes a border: the token, and the mass up to and with it (in the unit of window 0).
-struct Crossing {
-  bool found;
-  uint64_t key, through;
-};
+// ---- the first block's searches: every thread of the block calls them -----------------
+// A token's mass in units of the window that begins kOctaves x window octaves down: 2^45 for its largest weight.  0: none.
+__device__ __forceinline__ uint64_t mass_of(uint64_t key, const Scale& scale, int window, const unsigned* middle) {
+  const float x = value_of(key);
+  float t;
+  const int j = bin_of(x, scale, &t);
+  return j < 0 ? 0 : (static_cast<uint64_t>(weight_in(x, j, t, scale, middle)) << (kOctaves - 1)) >> (j / kSub - kOctaves * window);
+}
+__device__ __forceinline__ int digit_of(uint64_t key, int at) {
+  return (1 << kDigitBits) - 1 - static_cast<int>((key >> at) & ((1 << kDigitBits) - 1));
+}
+// Counts and masses by digit: three limbs of 15 bits each.
+__device__ __forceinline__ void clear_digits() {
+  Shared& s = own();
+  s.count[threadIdx.x] = s.low[threadIdx.x] = s.low[kThreads + threadIdx.x] = s.high[threadIdx.x] = 0;
+}
+__device__ __forceinline__ void add_digit(int d, uint64_t m) {
+  Shared& s = own();
+  atomicAdd(&s.count[d], 1u);
+  atomicAdd(&s.low[d], static_cast<unsigned>(m) & 0x7fffu);
+  atomicAdd(&s.low[kThreads + d], static_cast<unsigned>(m >> 15) & 0x7fffu);
+  atomicAdd(&s.high[d], static_cast<unsigned>(m >> 30));
+}
+__device__ __forceinline__ uint64_t digit_mass(int d) {
+  const Shared& s = own();
+  return s.low[d] + (static_cast<uint64_t>(s.low[kThreads + d]) << 15) + (static_cast<uint64_t>(s.high[d]) << 30);
+}
 
-// The first block's search.  Every thread of the block calls its functions and has the same results.
-template <typename T>
-struct Search {
-  Shared& s;
-  cg::cluster_group& cluster;
-  const Part<T>& part;
-  const Scale& scale;
-  int window;                          // the bins in s are this window's
-  uint64_t mass;                       // of the window
-  unsigned count;
-  uint64_t tail;                       // mass behind it, kTailBits more
-  int list_window, list_from, list_to; // bins whose tokens are listed
-  unsigned listed;
-
-  __device__ void ask(const Order& o) {
-    if (threadIdx.x == 0) s.order = o;
-    cluster_sync();
-    serve(s, s, cluster, o, part, scale);
-  }
-  // Sums before each bin, from the bins' own.
-  __device__ void add_up() {
-    const int b = 2 * threadIdx.x;
-    const uint64_t m0 = s.mass_before[b], m1 = s.mass_before[b + 1];
-    const unsigned c0 = s.count_before[b], c1 = s.count_before[b + 1];
-    uint64_t mb;
-    unsigned cb;
-    scan_before(s, m0 + m1, c0 + c1, &mb, &cb, &mass, &count);
-    s.mass_before[b] = mb;
-    s.mass_before[b + 1] = mb + m0;
-    s.count_before[b] = cb;
-    s.count_before[b + 1] = cb + c0;
-    if (threadIdx.x == 0) {
-      s.mass_before[kBins] = mass;
-      s.count_before[kBins] = count;
-    }
-    __syncthreads();
-  }
-  // Bins hold sums of 30-bit weights; a mass is that at the octave's place.
-  __device__ void to_masses() {
-    for (int b = threadIdx.x; b < kBins; b += kThreads) s.mass_before[b] <<= kOctaves - 1 - b / kSub;
-    __syncthreads();
-  }
-  __device__ void take_window(int w) {
-    to_masses();
-    add_up();
-    tail = 0;
-    for (int p = 0; p < static_cast<int>(cluster.num_blocks()); ++p) tail += s.tails[p];
-    window = w;
-  }
-  __device__ void need_window(int w) {
-    if (window == w) return;
-    ask(Order{kOpBins, w, 0, 0, 0, 0, 0});
-    take_window(w);
-  }
-  // The bin (or digit) with before[b] <= target < before[b + 1].
-  template <typename V>
-  __device__ int find(const V* before, V target) {
+// The masses of a pile's tokens, and their sums by the first digit.
+template <bool HEAD>
+__device__ __forceinline__ void prepare_pile() {
+  Shared& s = own();
+  auto& p = pile<HEAD>(s);
+  constexpr int kEach = (HEAD ? kHeadCap : kListCap) / kThreads;
+  const int lane = threadIdx.x % 32;
+  const unsigned n = min(p.n, static_cast<unsigned>(kEach * kThreads));
+  const Scale scale = p.scale;
+  const int window = p.window;
+  uint64_t any = 0, none = 0;
+  clear_digits();
+  if (threadIdx.x < 4) s.bits[threadIdx.x] = 0;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int b = 2 * threadIdx.x + q;
-      if (before[b] <= target && target < before[b + 1]) s.found = b;
-    }
-    __syncthreads();
-    const int b = s.found;
-    __syncthreads();
-    return b;
+  for (int q = 0; q < kEach; ++q) {
+    const unsigned i = q * kThreads + threadIdx.x;
+    const uint64_t key = i < n ? p.key[i] : 0, m = mass_of(key, scale, window, s.middle);  // (0: key 0 has the value NaN)
+    p.mass[i] = m;
+    any |= m ? key : 0;
+    none |= m ? ~key : 0;
   }
+  const unsigned b0 = __reduce_or_sync(~0u, static_cast<unsigned>(any)), b1 = __reduce_or_sync(~0u, static_cast<unsigned>(any >> 32));
+  const unsigned b2 = __reduce_or_sync(~0u, static_cast<unsigned>(none)), b3 = __reduce_or_sync(~0u, static_cast<unsigned>(none >> 32));
+  __syncthreads();
+  if (lane < 4) atomicOr(&s.bits[lane], lane == 0 ? b0 : lane == 1 ? b1 : lane == 2 ? b2 : b3);
+  __syncthreads();
+  any = (static_cast<uint64_t>(s.bits[1]) << 32) | s.bits[0];
+  const uint64_t differ = any & ((static_cast<uint64_t>(s.bits[3]) << 32) | s.bits[2]);
+  const int top = 64 - __clzll(static_cast<long long>(differ)), shift = top > kDigitBits ? top - kDigitBits : 0;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const unsigned i = q * kThreads + threadIdx.x;
+    const uint64_t m = p.mass[i];
+    if (m) add_digit(digit_of(p.key[i], shift), m);
+  }
+  __syncthreads();
+  uint64_t mb, mass;
+  unsigned cb, count;
+  scan_before(digit_mass(threadIdx.x), s.count[threadIdx.x], &mb, &cb, &mass, &count);
+  p.mass_before[threadIdx.x] = mb;
+  p.count_before[threadIdx.x] = cb;
+  if (threadIdx.x == 0) {
+    p.mass_before[kThreads] = p.total = mass;
+    p.count_before[kThreads] = p.count = count;
+    p.n = n;
+    p.shift = shift;
+    p.above = (any >> shift) & ~uint64_t((1 << kDigitBits) - 1);
+  }
+  __syncthreads();
+}
 
-  // The token among the listed ones of a bin where the sum passes `target`: a count, or a sum of weights.
-  __device__ uint64_t among_listed(int bin, bool by_count, uint64_t target, uint64_t* before, unsigned* own) {
-    uint64_t key[kEach];
-    unsigned w[kEach];
-    bool in[kEach];
-    uint64_t any = 0, all = ~uint64_t(0);
+// The token of a pile where the sum over its order passes `target` (below the count or mass), by digits of the keys down to 32
+// tokens: found_key, and found_mass, the mass through it.
+template <bool HEAD>
+__device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
+  Shared& s = own();
+  auto& p = pile<HEAD>(s);
+  constexpr int kEach = (HEAD ? kHeadCap : kListCap) / kThreads;
+  {
+    const uint64_t m0 = p.mass_before[threadIdx.x], c0 = p.count_before[threadIdx.x];
+    const uint64_t b0 = by_count ? c0 : m0, b1 = by_count ? p.count_before[threadIdx.x + 1] : p.mass_before[threadIdx.x + 1];
+    if (b0 <= target && target < b1) {
+      s.found = static_cast<int>(threadIdx.x);
+      s.found_before = b0;
+      s.found_mass = m0;
+    }
+    if (threadIdx.x == 0) s.few = 0;
+    __syncthreads();
+  }
+  int at = p.shift;
+  uint64_t before = s.found_mass;
+  target -= s.found_before;
+  uint64_t prefix = p.above | static_cast<uint64_t>((1 << kDigitBits) - 1 - s.found);
+  unsigned left = p.count_before[s.found + 1] - p.count_before[s.found];
+  const unsigned n = p.n;
+  __syncthreads();
+#pragma unroll 1
+  while (left > 32) {  // (at > 0: keys differ)
+    const int next = at > kDigitBits ? at - kDigitBits : 0;
+    clear_digits();
+    __syncthreads();
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
       const unsigned i = q * kThreads + threadIdx.x;
-      in[q] = i < listed;
-      key[q] = in[q] ? s.list[i] : 0;
-      const float x = value_of(key[q]);
-      float t;
-      const int j = bin_of(x, scale, &t);
-      in[q] = in[q] && j == bin;
-      w[q] = in[q] ? weight_in(x, j, t, scale, s.middle) : 0;
-      if (in[q]) {
-        any |= key[q];
-        all &= key[q];
-      }
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      any |= __shfl_xor_sync(~0u, any, d);
-      all &= __shfl_xor_sync(~0u, all, d);
-    }
-    if (threadIdx.x % 32 == 0) {
-      s.warp_mass[threadIdx.x / 32] = any;
-      s.mass_before[threadIdx.x / 32] = all;  // (scratch here; saved by the caller)
+      const uint64_t m = i < n ? p.mass[i] : 0, key = p.key[i];
+      if (m && key >> at == prefix) add_digit(digit_of(key, next), m);
     }
     __syncthreads();
-    any = 0;
-    all = ~uint64_t(0);
-    for (int i = 0; i < kWarps; ++i) {
-      any |= s.warp_mass[i];
-      all &= s.mass_before[i];
+    const uint64_t m = digit_mass(threadIdx.x);
+    const unsigned c = s.count[threadIdx.x];
+    uint64_t mb, ma;
+    unsigned cb, ca;
+    scan_before(m, c, &mb, &cb, &ma, &ca);
+    const uint64_t f0 = by_count ? cb : mb, f1 = by_count ? cb + c : mb + m;
+    if (f0 <= target && target < f1) {
+      s.found = static_cast<int>(threadIdx.x);
+      s.found_before = f0;
+      s.found_mass = mb;
     }
     __syncthreads();
-    uint64_t differ = any ^ all;  // (one token: none)
-    *before = 0;
-    while (differ) {
-      const int top = 63 - __clzll(static_cast<long long>(differ));
-      const int shift = top >= kDigitBits - 1 ? top - (kDigitBits - 1) : 0;
-      s.count[threadIdx.x] = s.low[threadIdx.x] = s.high[threadIdx.x] = 0;
-      __syncthreads();
-      int digit[kEach];
-#pragma unroll
-      for (int q = 0; q < kEach; ++q) {
-        digit[q] = (1 << kDigitBits) - 1 - static_cast<int>((key[q] >> shift) & ((1 << kDigitBits) - 1));
-        if (!in[q]) continue;
-        atomicAdd(&s.count[digit[q]], 1u);
-        atomicAdd(&s.low[digit[q]], w[q] & 0x7fffu);
-        atomicAdd(&s.high[digit[q]], w[q] >> 15);
-      }
-      __syncthreads();
-      const uint64_t m = s.low[threadIdx.x] + (static_cast<uint64_t>(s.high[threadIdx.x]) << 15);
-      const unsigned c = s.count[threadIdx.x];
-      uint64_t mb, ma;
-      unsigned cb, ca;
-      scan_before(s, m, c, &mb, &cb, &ma, &ca);
-      const uint64_t b0 = by_count ? cb : mb, b1 = by_count ? cb + c : mb + m;
-      if (b0 <= target && target < b1) {
-        s.found = static_cast<int>(threadIdx.x);
-        s.tails[0] = mb;
-        s.tails[1] = b0;
-      }
-      __syncthreads();
-      const int sel = s.found;
-      *before += s.tails[0];
-      target -= s.tails[1];
-      const bool sole = s.count[sel] == 1;
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kEach; ++q) in[q] = in[q] && digit[q] == sel;
-      differ = sole || shift == 0 ? 0 : differ & ((uint64_t(1) << shift) - 1);
-    }
-#pragma unroll
-    for (int q = 0; q < kEach; ++q)
-      if (in[q]) {
-        s.found_key = key[q];
-        s.found = static_cast<int>(w[q]);
-      }
+    before += s.found_mass;
+    target -= s.found_before;
+    left = s.count[s.found];
+    // (the digit's bits above `at` are the prefix's own)
+    prefix = prefix << (at - next) | (static_cast<uint64_t>((1 << kDigitBits) - 1 - s.found) & ((uint64_t(1) << (at - next)) - 1));
+    at = next;
     __syncthreads();
-    const uint64_t k = s.found_key;
-    *own = static_cast<unsigned>(s.found);
-    __syncthreads();
-    return k;
   }
-
-  // The token of bin b of the window where the sum (relative to the bin's start) passes `target`.
-  __device__ uint64_t in_bin(int b, bool by_count, uint64_t target, uint64_t* before, unsigned* own) {
-    uint64_t mask = 0, value = 0, past = 0;
-    unsigned held = s.count_before[b + 1] - s.count_before[b];
-    if (!(list_window == window && b >= list_from && b < list_to)) {
-      int from = b;
-      if (s.count_before[b + 1] <= kCap) from = 0;
-      else if (held > kCap) {
-        // narrowed by digits over the cluster: the window's sums are made anew afterwards
-        const int w = window;
-        ask(Order{kOpBits, w, b, b + 1, 0, 0, 0});
-        uint64_t any = 0, all = ~uint64_t(0);
-        for (int p = 0; p < static_cast<int>(cluster.num_blocks()); ++p) {
-          any |= s.ors[p];
-          all &= s.ands[p];
-        }
-        int top = 64 - __clzll(static_cast<long long>(any ^ all));
-        mask = ~((uint64_t(1) << top) - 1);
-        value = all & mask;
-        while (held > kCap) {
-          const int shift = top > kDigitBits ? top - kDigitBits : 0;
-          ask(Order{kOpDigits, w, b, b + 1, mask, value, shift});
-          add_up();
-          const int digit = by_count ? find(s.count_before, static_cast<unsigned>(target)) : find(s.mass_before, target);
-          held = s.count_before[digit + 1] - s.count_before[digit];
-          past += s.mass_before[digit];
-          target -= by_count ? s.count_before[digit] : s.mass_before[digit];
-          // (digits below bit `shift` are still open; the digit's own bits above `top` are the mask's)
-          const uint64_t bits = static_cast<uint64_t>((1 << kDigitBits) - 1 - digit) << shift;
-          const uint64_t open = (uint64_t(1) << shift) - 1;
-          value = (value & mask) | (bits & ~mask);
-          mask = ~open;
-          value &= mask;
-          top = shift;
-          __syncthreads();
-        }
-        window = -1;
-        if (threadIdx.x == 0) s.listed = 0;
-        ask(Order{kOpGather, w, b, b + 1, mask, value, 0});
-        list_window = -1;
-        listed = min(s.listed, static_cast<unsigned>(kCap));
-        const uint64_t key = among_listed(w * kBins + b, by_count, target, before, own);
-        *before += past;
-        return key;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const unsigned i = q * kThreads + threadIdx.x;
+    const uint64_t m = i < n ? p.mass[i] : 0, key = p.key[i];
+    if (m && key >> at == prefix) {
+      const unsigned f = atomicAdd(&s.few, 1u);
+      if (f < 32) {
+        s.few_key[f] = key;
+        s.few_mass[f] = m;
       }
-      if (threadIdx.x == 0) s.listed = 0;
-      ask(Order{kOpGather, window, from, b + 1, 0, 0, 0});
-      list_window = window;
-      list_from = from;
-      list_to = b + 1;
-      listed = min(s.listed, static_cast<unsigned>(kCap));
     }
-    // (the search by digits uses the first places of the bins' sums)
-    uint64_t saved = 0;
-    if (threadIdx.x < kWarps) saved = s.mass_before[threadIdx.x];
-    __syncthreads();
-    const uint64_t key = among_listed(window * kBins + b, by_count, target, before, own);
-    if (threadIdx.x < kWarps) s.mass_before[threadIdx.x] = saved;
-    __syncthreads();
-    return key;
   }
-
-  __device__ Crossing where(bool by_count, uint64_t target) {
-    uint64_t done = 0;  // mass of the windows before, in the unit of window 0
-    for (int w = 0; w < kWindows; ++w) {
-      need_window(w);
-      uint64_t t = by_count ? target : (target - done) << (kOctaves * w);
-      const uint64_t all = by_count ? count : mass;
-      const bool last = tail == 0;
-      if (t >= all && last && !by_count && all) t = all - 1;  // (sums of different units, rounded: the last token)
-      if (t < all) {
-        const int b = by_count ? find(s.count_before, static_cast<unsigned>(t)) : find(s.mass_before, t);
-        const uint64_t start = s.mass_before[b], first = by_count ? s.count_before[b] : start;
-        const int up = kOctaves - 1 - b / kSub;
-        uint64_t before;
-        unsigned own;
-        const uint64_t key = in_bin(b, by_count, by_count ? t - first : (t - first) >> up, &before, &own);
-        return Crossing{true, key, done + ((start + ((before + own) << up)) >> (kOctaves * w))};
-      }
-      if (last) break;
-      if (by_count) target -= count;
-      done += mass >> (kOctaves * w);
-      if (!by_count && target < done) target = done;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const unsigned few = min(s.few, 32u);
+    const uint64_t key = threadIdx.x < few ? s.few_key[threadIdx.x] : 0, m = threadIdx.x < few ? s.few_mass[threadIdx.x] : 0;
+    uint64_t mb = 0, cb = 0;
+#pragma unroll 4
+    for (unsigned f = 0; f < few; ++f) {
+      const bool earlier = s.few_key[f] > key;
+      mb += earlier ? s.few_mass[f] : 0;
+      cb += earlier;
     }
-    return Crossing{false, 0, 0};
+    const uint64_t f0 = by_count ? cb : mb, f1 = by_count ? cb + 1 : mb + m;
+    if (key && f0 <= target && target < f1) {
+      s.found_key = key;
+      s.found_mass = before + mb + m;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__device__ __forceinline__ void ask(int op, int w, int from, int to, uint64_t mask, uint64_t value, int shift) {
+  Shared& s = own();
+  if (threadIdx.x == 0) {
+    // bins [from, to) hold no value outside low ... high (a hundredth of a bin is left at either end, and the differences' rounding)
+    const Scale scale = s.tail_scale;
+    const float deep = (static_cast<float>(w * kBins + to) + 0.01f) / kSub / scale.hi;
+    const float high = (static_cast<float>(w * kBins + from) - 0.01f) / kSub / scale.hi;
+    const float d = fabsf(scale.most) * 0x1p-20f;
+    const bool sure = fabsf(scale.most) < FLT_MAX;
+    if (op == kOpBins) s.list_window = -1;
+    s.order = Order{scale, op, w, from, to, mask, value, shift, sure ? scale.most - deep - d : -FLT_MAX,
+                    sure && from > 0 ? scale.most - high + d : INFINITY, 0};
+  }
+  tell();
+  serve<T>();
+}
+// Sums before each bin, from the bins' own.
+__device__ __noinline__ void add_up_bins() {
+  Shared& s = own();
+  const int b = 2 * threadIdx.x;
+  const uint64_t m0 = s.mass_before[b], m1 = s.mass_before[b + 1];
+  const unsigned c0 = s.count_before[b], c1 = s.count_before[b + 1];
+  uint64_t mb, mass;
+  unsigned cb, count;
+  scan_before(m0 + m1, c0 + c1, &mb, &cb, &mass, &count);
+  s.mass_before[b] = mb;
+  s.mass_before[b + 1] = mb + m0;
+  s.count_before[b] = cb;
+  s.count_before[b + 1] = cb + c0;
+  if (threadIdx.x == 0) {
+    s.mass_before[kBins] = s.mass = mass;
+    s.count_before[kBins] = s.counted = count;
+  }
+  __syncthreads();
+}
+// Takes the bins that the blocks have joined as window w's: they hold sums of 30-bit weights, a mass is that at the octave's place.
+__device__ __noinline__ void take_window(int w) {
+  Shared& s = own();
+  for (int b = 2 * threadIdx.x; b < 2 * static_cast<int>(threadIdx.x) + 2; ++b) s.mass_before[b] <<= kOctaves - 1 - b / kSub;
+  if (threadIdx.x == 0) {
+    uint64_t tail = 0;
+    const int blocks = static_cast<int>(cg::this_cluster().num_blocks());
+    for (int q = 0; q < blocks; ++q) tail += s.tails[q];
+    s.behind = tail;
+    s.window = w;
+  }
+  add_up_bins();
+}
+template <typename T>
+__device__ __noinline__ void need_window(int w) {
+  if (own().window == w) return;
+  ask<T>(kOpBins, w, 0, kBins, 0, 0, 0);
+  take_window(w);
+}
+// The bin (or digit) where the sums before pass the target.
+__device__ __noinline__ int find_bin(bool by_count, uint64_t target) {
+  Shared& s = own();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int b = q * kThreads + threadIdx.x;
+    const uint64_t b0 = by_count ? s.count_before[b] : s.mass_before[b], b1 = by_count ? s.count_before[b + 1] : s.mass_before[b + 1];
+    if (b0 <= target && target < b1) s.found = b;
+  }
+  __syncthreads();
+  const int b = s.found;
+  __syncthreads();
+  return b;
+}
+
+// The token of bin b of the window where the sum passes `target`, as search_pile; masses in the window's unit.
+template <typename T>
+__device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target) {
+  Shared& s = own();
+  const int w = s.window, up = kOctaves - 1 - b / kSub;
+  uint64_t start;                        // mass before the list
+  if (s.list_window == w && b >= s.list_from && b < s.list_to) {
+    start = s.mass_before[s.list_from];
+    target -= by_count ? s.count_before[s.list_from] : start;
+  } else {
+    const int from = s.count_before[b + 1] <= kListCap ? 0 : b;
+    unsigned held = s.count_before[b + 1] - s.count_before[from];
+    uint64_t mask = 0, value = 0;
+    start = s.mass_before[from];
+    target -= by_count ? s.count_before[from] : start;
+    if (held > kListCap) {
+      // narrowed by digits over the cluster: the window's sums are made anew afterwards
+      ask<T>(kOpBits, w, b, b + 1, 0, 0, 0);
+      uint64_t any = 0, all = ~uint64_t(0);
+      const int blocks = static_cast<int>(cg::this_cluster().num_blocks());
+      for (int q = 0; q < blocks; ++q) {
+        any |= s.ors[q];
+        all &= s.ands[q];
+      }
+      int top = 64 - __clzll(static_cast<long long>(any ^ all));
+      mask = ~((uint64_t(1) << top) - 1);
+      value = all & mask;
+      if (!by_count) target >>= up;      // (in 30-bit weights)
+      uint64_t past = 0;
+#pragma unroll 1
+      while (held > kListCap) {
+        const int shift = top > kDigitBits ? top - kDigitBits : 0;
+        ask<T>(kOpDigits, w, b, b + 1, mask, value, shift);
+        add_up_bins();
+        const int digit = find_bin(by_count, target);
+        held = s.count_before[digit + 1] - s.count_before[digit];
+        past += s.mass_before[digit];
+        target -= by_count ? s.count_before[digit] : s.mass_before[digit];
+        // (digits below bit `shift` are still open; the digit's own bits above `top` are the mask's)
+        const uint64_t bits = static_cast<uint64_t>((1 << kDigitBits) - 1 - digit) << shift;
+        value = (value & mask) | (bits & ~mask);
+        mask = ~((uint64_t(1) << shift) - 1);
+        value &= mask;
+        top = shift;
+        __syncthreads();
+      }
+      start += past << up;
+      if (!by_count) target <<= up;
+      if (threadIdx.x == 0) s.window = -1;
+    }
+    ask<T>(kOpGather, w, from, b + 1, mask, value, 0);
+    if (threadIdx.x == 0) {
+      s.list_window = mask ? -1 : w;
+      s.list_from = from;
+      s.list_to = b + 1;
+      s.list.scale = s.tail_scale;
+      s.list.window = w;
+    }
+    __syncthreads();
+    prepare_pile<false>();
+  }
+  search_pile<false>(by_count, target);
+  if (threadIdx.x == 0) s.found_mass += start;
+}
+
+// The token where the sum over the tail passes `target`; masses in the unit of window 0.  False where it does not.
+template <typename T>
+__device__ __forceinline__ bool search_tail(bool by_count, uint64_t target) {
+  Shared& s = own();
+  uint64_t done = 0;  // mass of the windows before
+#pragma unroll 1
+  for (int w = 0; w < kWindows; ++w) {
+    need_window<T>(w);
+    uint64_t t = by_count ? target : (target - done) << (kOctaves * w);
+    const uint64_t all = by_count ? s.counted : s.mass;
+    const bool last = s.behind == 0;
+    if (t >= all && last && !by_count && all) t = all - 1;  // (sums of different units, rounded: the last token)
+    if (t < all) {
+      search_bin<T>(find_bin(by_count, t), by_count, t);
+      if (threadIdx.x == 0) s.found_mass = done + (s.found_mass >> (kOctaves * w));
+      __syncthreads();
+      return true;
+    }
+    if (last) break;
+    if (by_count) target -= s.counted;
+    done += s.mass >> (kOctaves * w);
+    if (!by_count && target < done) target = done;
+  }
+  return false;
+}
+
+// a b / 2^shift, rounded down, for results below 2^64.
+__device__ __forceinline__ uint64_t scaled(uint64_t a, uint64_t b, int shift) {
+  const uint64_t low = a * b, high = __umul64hi(a, b);
+  if (shift <= 0) return low << -shift;
+  if (shift < 64) return low >> shift | high << (64 - shift);
+  return shift < 128 ? high >> (shift - 64) : 0;
+}
+// f a for f in (0, 1), rounded down; below: the largest whole number that is less.
+__device__ __forceinline__ uint64_t share_of(float f, uint64_t a, bool below) {
+  const unsigned bits = __float_as_uint(f), e = bits >> 23;
+  const unsigned m = e ? (bits & 0x7fffffu) | 0x800000u : bits;
+  const int shift = e ? 150 - static_cast<int>(e) : 149;
+  if (!below) return scaled(a, m, shift);
+  // (a m - 1) / 2^shift
+  const uint64_t low = a * m, high = __umul64hi(a, m) - (low == 0), less = low - 1;
+  if (shift < 64) return less >> shift | high << (64 - shift);
+  return shift < 128 ? high >> (shift - 64) : 0;
+}
+// The tail's masses in the head's unit: times weight / 2^(30 + depth), rounded down.
+struct Unit {
+  unsigned weight, inverse;  // (2^54 / weight, rounded down)
+  int depth;
+  __device__ __forceinline__ uint64_t in_head(uint64_t m) const { return scaled(m, weight, 30 + depth); }
+  __device__ __forceinline__ uint64_t in_tail(uint64_t m) const {
+    const uint64_t a = scaled(m, inverse, 24 - depth), left = m - min(m, in_head(a));
+    return a + scaled(left, inverse, 24 - depth);
   }
 };
 
+// The block's part of the row, read once: its maximum, its part of the head, and, where `rest`, its bins.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, int slots) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ float first_pass(bool rest) {
   constexpr int kVec = 16 / sizeof(T);
-  Shared& s = *reinterpret_cast<Shared*>(smem);
-  T* data = reinterpret_cast<T*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+  Shared& s = own();
+  const Scale scale = s.scale;
+  const float tau = scale.most;
+  float most = -INFINITY;
+  auto look = [&](const Vec<T, kVec>& v, int i) {
+    float top = v.v[0];
+#pragma unroll
+    for (int e = 1; e < kVec; ++e) top = fmaxf(top, v.v[e]);
+    most = fmaxf(most, top);
+    if (top >= tau) {
+      unsigned over = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) over |= v.v[e] >= tau ? 1u << e : 0;
+#pragma unroll 1
+      for (; over; over &= over - 1) {
+        const int e = __ffs(static_cast<int>(over)) - 1;
+        float x = v.v[0];
+#pragma unroll
+        for (int q = 1; q < kVec; ++q) x = e == q ? v.v[q] : x;
+        const unsigned at = atomicAdd(&s.head.n, 1u);
+        if (at < kHeadCap) s.head.key[at] = token_key(x, i + e);
+      }
+    }
+  };
+  if (rest) fill_bins<T>(scale, 0, look);
+  else each_vector<T, 4>([&](const Vec<T, kVec>& v, const Raw<T, kVec>&, int i) { look(v, i); });
+  return most;
+}
+
+// `slots`: tokens of a block's part; the threshold is number `order` of the 32 maxima of `runs` times 16 tokens each, `step`
+// apart (runs == 0: none).
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, int slots, int runs, int order, int step_) {
+  constexpr int kVec = 16 / sizeof(T);
+  Shared& s = own();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t row = blockIdx.x / blocks;
+  const T* x = static_cast<const T*>(p.x) + row * p.ld;
   if (threadIdx.x < kSub) s.middle[threadIdx.x] = kMiddles.v[threadIdx.x];
-  if (threadIdx.x == 0) s.found = 0;
+  if (threadIdx.x == 0) {
+    s.found = 0;
+    s.head.n = 0;
+    s.window = s.list_window = -1;
+    const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kVec);
+    s.row = x;
+    s.begin = rank * slots - lead;
+    s.end = min((rank + 1) * slots - lead, p.n);
+    s.n = p.n;
+  }
+  clear_bins<T>();
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // the block's part into shared memory, with the row's maximum; slots start on a 16-byte boundary at or before the row
-  const T* x = static_cast<const T*>(p.x) + row * p.ld;
-  const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kVec);
-  Part<T> part{data, slots, rank * slots - lead};
-  float most = -INFINITY;
-  for (int at = threadIdx.x * kVec; at < slots; at += kThreads * kVec) {
-    const int i = part.index0 + at;
-    Vec<T, kVec> v;
-    if (i >= 0 && i + kVec <= p.n) {
-      v.set(ld_stream_v4(x + i));
-    } else {
+  const float temperature = p.temperatures ? p.temperatures[row] : p.temperature;
+  const bool greedy = !(temperature > 0.0f);
+  const int top_k = greedy ? 1 : p.top_ks ? p.top_ks[row] : p.top_k;
+  const bool rest = !(top_k > 0 && top_k <= kHeadOnly);  // (the tail will hardly matter otherwise)
+
+  // the threshold: the same in all blocks of the cluster
+  float tau = -FLT_MAX;
+  if (runs > 0) {
+    float top = -INFINITY;
+    const int group = threadIdx.x / 16;
+#pragma unroll 4
+    for (int i = 0; i < runs; ++i) top = fmaxf(top, to_f32(x[(i * 32 + group) * step_ + threadIdx.x % 16]));
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) v.v[e] = i + e >= 0 && i + e < p.n ? to_f32(x[i + e]) : -INFINITY;
+    for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (threadIdx.x % 16 == 0) s.group_max[group] = __float_as_uint(top);
+    __syncthreads();
+    top = __uint_as_float(s.group_max[lane]);
+    int place = 0;
+#pragma unroll 8
+    for (int q = 0; q < 32; ++q) {
+      const float other = __shfl_sync(~0u, top, q);
+      place += other > top || (other == top && q < lane);
     }
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) most = fmaxf(most, v.v[e]);
-    v.store(data + at);
+    top = __shfl_sync(~0u, top, __ffs(static_cast<int>(__ballot_sync(~0u, place == order))) - 1);
+    if (top > -INFINITY) tau = top;
   }
+  if (threadIdx.x == 0) {
+    const double per = greedy ? INFINITY : p.temperatures ? 1.4426950408889634 / static_cast<double>(temperature) : p.per;  // log2(e) / T
+    const bool within = per < FLT_MAX;
+    const float hi = within ? static_cast<float>(per) : FLT_MAX;
+    s.scale = Scale{tau, -FLT_MAX, tau, hi, within ? static_cast<float>(per - static_cast<double>(hi)) : 0.0f};
+  }
+  cluster_sync();  // (every block has started, with nothing in its lists)
+
+  float most = first_pass<T>(rest);
 #pragma unroll
   for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
-  if (threadIdx.x % 32 == 0) s.warp_count[threadIdx.x / 32] = __float_as_uint(most);
-  cluster_sync();  // (every block has started, too)
-  if (threadIdx.x < blocks) {
+  if (lane == 0) s.warp_count[warp] = __float_as_uint(most);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) most = fmaxf(most, __uint_as_float(s.warp_count[w]));
-    cluster.map_shared_rank(&s, threadIdx.x)->maxes[rank] = most;
+    cluster.map_shared_rank(&s, 0)->maxes[rank] = most;
   }
+  if (rank != 0) hand_over<true>();
   cluster_sync();
-  most = s.maxes[0];
-  for (int b = 1; b < blocks; ++b) most = fmaxf(most, s.maxes[b]);
-  if (most == -INFINITY) {  // nothing that may be drawn (in every block alike)
-    if (rank == 0 && threadIdx.x == 0) {
-      p.tokens[row] = -1;
-      p.logprobs[row] = -INFINITY;
-    }
-    return;
+  if (rest) {
+    join_bins();
+    cluster_sync();
   }
-
-  const float temperature = p.temperatures ? p.temperatures[row] : p.temperature;
-  const float min_p = p.min_ps ? p.min_ps[row] : p.min_p;
-  const bool greedy = !(temperature > 0.0f);
-  Scale scale{most, -FLT_MAX, FLT_MAX, 0.0f};
-  if (!greedy) {
-    const double per = 1.4426950408889634 / static_cast<double>(temperature);
-    if (per < FLT_MAX) {
-      scale.hi = static_cast<float>(per);
-      scale.lo = static_cast<float>(per - static_cast<double>(scale.hi));
-    }
-    if (min_p > 0.0f) {  // w >= min_p: x >= max + T ln(min_p)
-      const double least = static_cast<double>(most) + static_cast<double>(temperature) * log(static_cast<double>(min_p));
-      const float f = __double2float_ru(least);
-      scale.least = fminf(fmaxf(f, -FLT_MAX), most);
-    }
-  } else {
-    scale.least = most;
-  }
-
-  Shared& first = *cluster.map_shared_rank(&s, 0);
-  serve(s, first, cluster, Order{kOpBins, 0, 0, 0, 0, 0, 0}, part, scale);
   if (rank != 0) {
+#pragma unroll 1
     for (;;) {
       cluster_sync();
-      const Order o = first.order;
-      if (o.op == kOpDone) break;
-      serve(s, first, cluster, o, part, scale);
+      if (s.order.op == kOpDone) return;
+      serve<T>();
     }
-    cluster_sync();
-    return;
   }
-  Search<T> search{s, cluster, part, scale, 0, 0, 0, 0, -1, 0, 0, 0};
-  search.take_window(0);
-  uint64_t kept = search.mass + (search.tail >> kTailBits);
-  const int top_k = greedy ? 1 : p.top_ks ? p.top_ks[row] : p.top_k;
-  const float top_p = p.top_ps ? p.top_ps[row] : p.top_p;
-  const float u = p.u[row];
-  if (top_k > 0 && top_k < p.n) {
-    const Crossing c = search.where(true, static_cast<uint64_t>(top_k - 1));
-    if (c.found) kept = c.through;
-  }
-  if (top_p < 1.0f) {
-    // the first prefix with a mass of at least top_p of it: the sum before its last token is below that
-    const double border = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(kept));
-    const uint64_t target = border < 1.0 ? 0 : static_cast<uint64_t>(border) - 1;
-    const Crossing c = search.where(false, target < kept ? target : kept - 1);
-    if (c.found && c.through < kept) kept = c.through;
-  }
-  const double drawn = (u > 0.0f ? static_cast<double>(u) : 0.0) * static_cast<double>(kept);
-  const uint64_t target = drawn < static_cast<double>(kept) ? static_cast<uint64_t>(drawn) : kept;
-  const Crossing c = search.where(false, target < kept ? target : kept - 1);
+
+  most = s.maxes[0];
+  for (int b = 1; b < blocks; ++b) most = fmaxf(most, s.maxes[b]);
+  const bool listed = s.head.n <= kHeadCap;  // (else all is the tail)
+  const Scale scale = s.scale;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    p.tokens[row] = c.found ? index_of(c.key) : -1;
-    const float x0 = value_of(c.key);
-    const double z = greedy || x0 == most ? 0.0 : (static_cast<double>(x0) - static_cast<double>(most)) / static_cast<double>(temperature);
-    const double share = static_cast<double>(kept) * 0x1p-45;  // (the largest weight is 2^45)
-    p.logprobs[row] = fminf(static_cast<float>(z - log(share)), 0.0f);
-    s.order = Order{kOpDone, 0, 0, 0, 0, 0, 0};
+    float least = -FLT_MAX;
+    const float min_p = p.min_ps ? p.min_ps[row] : p.min_p;
+    if (greedy) {
+      least = most;
+    } else if (min_p > 0.0f) {  // w >= min_p: x >= max + T ln(min_p)
+      const double depth = p.min_ps ? log(static_cast<double>(min_p)) : p.log_min_p;
+      const float f = __double2float_ru(static_cast<double>(most) + static_cast<double>(temperature) * depth);
+      least = fminf(fmaxf(f, -FLT_MAX), most);
+    }
+    s.least = least;
+    s.tail_scale = listed ? Scale{tau, least, tau, scale.hi, scale.lo} : Scale{most, least, NAN, scale.hi, scale.lo};
+    s.head.scale = Scale{most, least, NAN, scale.hi, scale.lo};
+    s.head.window = 0;
+    if (!listed) s.head.n = 0;
   }
-  cluster_sync();
-  cluster_sync();
+  __syncthreads();
+  // the tail's unit: the weight of its largest value
+  Unit unit{1u << 30, 1u << 24, 0};
+  bool more = true;
+  if (listed) {
+    float t;
+    const Scale from{most, -FLT_MAX, NAN, scale.hi, scale.lo};
+    const int j = bin_of(tau, from, &t);
+    more = j >= 0 && s.least < tau;
+    if (more) {
+      const unsigned w = weight_in(tau, j, t, from, s.middle);
+      unit = Unit{w + ((w + (1u << 28)) >> 29), 0, j / kSub};  // (w / kLargest 2^30)
+      unit.inverse = __float2uint_rd(__frcp_rd(__uint2float_ru(unit.weight)) * 0x1p54f) - 2;
+    }
+  }
+  bool found = false;
+  uint64_t kept = 0;
+  if (most > -INFINITY) {  // (else nothing may be drawn)
+    if (listed && more && rest && s.least == -FLT_MAX) take_window(0);
+    prepare_pile<true>();
+    const uint64_t head_mass = s.head.total;
+    const unsigned head_count = s.head.count;
+    // in steps: the first top_k tokens, or all; what top_p leaves of them; the token
+    bool in_head = true;
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {
+      uint64_t target = ~uint64_t(0);  // (no border)
+      if (step == 0) {
+        in_head = static_cast<unsigned>(top_k) <= head_count;
+        if (top_k > 0 && top_k < p.n && (in_head || more)) target = static_cast<uint64_t>(top_k - 1) - (in_head ? 0 : head_count);
+      } else {
+        const float f = step == 2 ? p.u[row] : p.top_ps ? p.top_ps[row] : p.top_p;
+        if (step == 1 && !(f < 1.0f)) continue;
+        target = !(f > 0.0f) ? 0 : f < 1.0f ? share_of(f, kept, step == 1) : kept - 1;
+        in_head = !more || (listed && target < head_mass);
+        target = in_head ? min(target, head_mass - 1) : unit.in_tail(target - head_mass);
+      }
+      found = false;
+      if (target != ~uint64_t(0)) {
+        if (!in_head) found = search_tail<T>(step == 0, target);
+        if (!found && (in_head || (step && listed))) {
+          search_pile<true>(step == 0, in_head ? target : head_mass - 1);
+          in_head = found = true;
+        }
+      }
+      if (step == 2) break;
+      if (found) {
+        const uint64_t through = in_head ? s.found_mass : head_mass + unit.in_head(s.found_mass);
+        kept = step ? min(kept, through) : through;
+      } else if (step == 0) {
+        kept = head_mass;
+        if (more) {
+          need_window<T>(0);
+          kept += unit.in_head(s.mass + (s.behind >> kTailBits));
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (threadIdx.x == 0) {
+    p.tokens[row] = found ? index_of(s.found_key) : -1;
+    // z - ln(kept), with z = -t ln 2 in two parts
+    const float x0 = value_of(s.found_key);
+    const float d = x0 == most ? 0.0f : most - x0, bb = d - most, left = x0 == most ? 0.0f : (most - (d - bb)) - (x0 + bb);
+    const float t = d * scale.hi, more_t = fmaf(d, scale.hi, -t) + fmaf(d, scale.lo, left * scale.hi);
+    const float z = greedy ? 0.0f : t * 0.693147182f;
+    const float low = greedy ? 0.0f : fmaf(t, 0.693147182f, -z) + fmaf(more_t, 0.693147182f, t * -1.90465421e-9f);
+    const uint64_t one = static_cast<uint64_t>(kLargest) << (kOctaves - 1);
+    const float share = greedy ? 0.0f : log1pf(static_cast<float>(kept > one ? kept - one : 0) * static_cast<float>(0x1p-15 / kLargest));
+    p.logprobs[row] = found ? 0.0f - static_cast<float>(static_cast<double>(z) + low + share) : -INFINITY;
+    s.order.op = kOpDone;
+  }
+  tell();
 }
 
 }  // namespace
@@ -666,21 +1058,27 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
 template <typename T>
 static cudaError_t launch(const TokenDraw& p, cudaStream_t st) {
   constexpr int64_t kVec = 16 / sizeof(T);
-  // blocks a row: 64 KB of it each, so that two blocks share an SM and one loads while the other searches; more where rows
-  // are few, down to 4096 tokens each
+  // blocks a row: as many as fill the SMs with two each, down to 2048 tokens
   const int64_t len = p.n + kVec;
-  int blocks = 1;
-  while (blocks < 8 && (len * static_cast<int64_t>(sizeof(T)) > blocks * 65536 || (p.rows * blocks * 2 <= ops_sm_count() && len > blocks * 4096)))
-    blocks *= 2;
+  int64_t blocks = 2 * ops_sm_count() / p.rows;
+  if (blocks > len / 2048) blocks = len / 2048;
+  const int64_t least = (p.n + kPartMost - 1) / kPartMost;
+  blocks = blocks < least ? least : blocks > kMostBlocks ? kMostBlocks : blocks;
   const int64_t slots = ((len + blocks - 1) / blocks + kVec - 1) / kVec * kVec;
-  const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(slots) * sizeof(T);
-  cudaError_t e = cudaFuncSetAttribute(token_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e != cudaSuccess) return e;
   if (p.rows * blocks > INT32_MAX) return cudaErrorNotSupported;
+  // the threshold: of 32 maxima of m tokens each, number i (from 0) has about (1/32 + ... + 1/(32 - i)) n / m tokens above it
+  int runs = 0, order = 0;
+  if (p.n > kHeadCap) {
+    runs = static_cast<int>((p.n * 69 / 100 / kHead + 15) / 16);
+    double above = 1.0 / 32;
+    while (order < 31 && above * p.n < 16.0 * runs * kHead) above += 1.0 / (32 - ++order);
+  }
+  cudaError_t e = cudaFuncSetAttribute(token_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows * blocks));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -690,7 +1088,8 @@ static cudaError_t launch(const TokenDraw& p, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_kernel<T>, p, static_cast<int>(slots));
+  return cudaLaunchKernelEx(&cfg, token_kernel<T>, p, static_cast<int>(slots), runs, order,
+                            runs ? (p.n - 16) / (32 * runs) : 0);
 }
 
 cudaError_t launch_tokens(const TokenDraw& p, cudaStream_t st) {

@@ -190,6 +190,7 @@ struct TokenDraw {
   const int32_t* top_ks;
   int64_t* tokens;
   float* logprobs;
+  double per, log_min_p;  // log2(e) / temperature and ln(min_p) of the numbers
 };
 cudaError_t launch_tokens(const TokenDraw& p, cudaStream_t st);
 

@@ -323,9 +323,9 @@ int sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t n, c
             {matrix(logits, rows, n, ld, static_cast<int64_t>(value_bytes(dtype))), vector(u, rows, 4), vector(temperatures, rows, 4),
              vector(top_ks, rows, 4), vector(top_ps, rows, 4), vector(min_ps, rows, 4)}))
     return TOPK_EINVAL;
-  const TokenDraw p{logits, ld, dtype, rows, static_cast<int>(n), u, static_cast<float>(temperature), static_cast<float>(top_p),
-                    static_cast<float>(min_p), top_ks || top_k > n ? 0 : static_cast<int>(top_k), temperatures, top_ps, min_ps, top_ks,
-                    tokens, logprobs};
+  const float t = static_cast<float>(temperature), m = static_cast<float>(min_p);
+  const TokenDraw p{logits, ld, dtype, rows, static_cast<int>(n), u, t, static_cast<float>(top_p), m, top_ks || top_k > n ? 0 : static_cast<int>(top_k), temperatures, top_ps, min_ps, top_ks,
+                    tokens, logprobs, t > 0.0f ? 1.4426950408889634 / static_cast<double>(t) : 0.0, m > 0.0f ? std::log(static_cast<double>(m)) : 0.0};
   return status_of(launch_tokens(p, st));
 }
 
