@@ -57,50 +57,101 @@ struct WeightSums {
 };
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
 
-// A block: 32 vectors of positions of one head, the head's query rows dealt to its warps.
+// Two sums of two f32 each, side by side.
+struct Sum2Pair {
+  Pair hi = Pair::of(0.0f, 0.0f), lo = Pair::of(0.0f, 0.0f);
+  __device__ __forceinline__ static Pair plus(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+  }
+  __device__ __forceinline__ static Pair minus(Pair a, Pair b) {
+    Pair r = a;
+    r.fma(b, Pair::of(-1.0f, -1.0f));
+    return r;
+  }
+  __device__ __forceinline__ void add(Pair v) {
+    const Pair s = plus(hi, v), b = minus(s, hi);
+    lo = plus(lo, plus(minus(hi, minus(s, b)), minus(v, b)));
+    hi = s;
+  }
+};
+
+// What a thread holds of 32 VEC (or 32 x 4) positions: 16 bytes side by side, or four values 32 apart.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSums p) {
-  __shared__ float2 part[kSumWarps][32 * VEC];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int64_t chunks = (p.capacity + 32 * VEC - 1) / (32 * VEC), bh = blockIdx.x / chunks, b = bh / p.heads, h = bh % p.heads;
-  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = (blockIdx.x - bh * chunks) * 32 * VEC;
-  if (at0 >= len) return;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t at = at0 + lane * VEC;
-  Sum2 sum[VEC];
-  const int64_t n = p.group * p.queries;
-  if (at < len) {
-    constexpr int kAhead = 4;
-    for (int64_t i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
-      Raw<T, VEC> v[kAhead];
+struct Places {
+  static constexpr int kWide = VEC > 1 ? VEC : 4;
+  Raw<T, VEC> r[VEC > 1 ? 1 : kWide];
+  __device__ __forceinline__ static int at(int lane, int e) { return VEC > 1 ? lane * VEC + e : e * 32 + lane; }
+  // (the last vector of a row may reach past its length, not past the capacity)
+  __device__ __forceinline__ void load(const T* row, int lane, int64_t left) {
+    if constexpr (VEC > 1) {
+      r[0].clear();
+      if (lane * VEC < left) r[0].load_nc(row + lane * VEC);
+    } else {
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int64_t i = i0 + a * kSumWarps;
-        v[a].clear();
-        if (i < n) {
-          const int64_t g = i / p.queries, q = i - g * p.queries;
-          const T* row = static_cast<const T*>(p.weights.data) + b * p.weights.batch + (h * p.group + g) * p.weights.head + q * p.weights.row;
-          v[a].load_nc(row + at);
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        Vec<T, VEC> x;
-        x.set_raw(v[a]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[e].add(counted(x.v[e]));
+      for (int e = 0; e < kWide; ++e) {
+        r[e].clear();
+        if (e * 32 + lane < left) r[e].load_nc(row + e * 32 + lane);
       }
     }
   }
+  __device__ __forceinline__ Pair pair(int i) const {
+    if constexpr (VEC > 1) return r[0].pair(i);
+    else return Pair::of(to_f32(r[2 * i].u), to_f32(r[2 * i + 1].u));
+  }
+};
+
+// A block: 32 pieces of positions of one head, the head's query rows dealt to its warps.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSums p) {
+  using P = Places<T, VEC>;
+  constexpr int kWide = P::kWide, kAhead = VEC > 1 ? 8 : 4;
+  __shared__ float2 part[kSumWarps][32 * kWide];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t chunks = (p.capacity + 32 * kWide - 1) / (32 * kWide), bh = blockIdx.x / chunks, b = bh / p.heads, h = bh % p.heads;
+  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = (blockIdx.x - bh * chunks) * 32 * kWide;
+  if (at0 >= len) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  Sum2Pair sum[kWide / 2];
+  const int n = static_cast<int>(p.group * p.queries), queries = static_cast<int>(p.queries);
+  const T* base = static_cast<const T*>(p.weights.data) + b * p.weights.batch + h * p.group * p.weights.head + at0;
+  for (int i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
+    P v[kAhead];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) part[warp][lane * VEC + e] = make_float2(sum[e].hi, sum[e].lo);
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * kSumWarps, g = i / queries;
+      v[a].load(base + g * p.weights.head + (i - g * queries) * p.weights.row, lane, i < n ? len - at0 : 0);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+      for (int e = 0; e < kWide / 2; ++e) sum[e].add(v[a].pair(e));
+  }
+#pragma unroll
+  for (int e = 0; e < kWide / 2; ++e) {
+    float h0, h1, l0, l1;
+    sum[e].hi.get(&h0, &h1);
+    sum[e].lo.get(&l0, &l1);
+    part[warp][P::at(lane, 2 * e)] = make_float2(h0, l0);
+    part[warp][P::at(lane, 2 * e + 1)] = make_float2(h1, l1);
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * VEC; i += kSumThreads) {
+  for (int i = threadIdx.x; i < 32 * kWide; i += kSumThreads) {
     if (at0 + i >= len) break;
     Sum2 all;
     all.add(static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + i]);
-    for (int w = 0; w < kSumWarps; ++w) all.add(Sum2{part[w][i].x, part[w][i].y});
+    bool number = true;
+    for (int w = 0; w < kSumWarps; ++w) {
+      number = number && part[w][i].x == part[w][i].x;
+      all.add(Sum2{part[w][i].x, part[w][i].y});
+    }
+    if (!number) {  // a weight is NaN, or infinities met: anew, without the NaN ones
+      all = Sum2{};
+      all.add(static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + i]);
+      for (int q = 0; q < n; ++q) all.add(counted(to_f32(base[(q / queries) * p.weights.head + (q % queries) * p.weights.row + i])));
+    }
     p.out[bh * p.capacity + at0 + i] = all.value();
   }
 }
@@ -117,13 +168,12 @@ struct Choice {
 };
 constexpr int kDigits = 2048;  // 11 bits of a key at a time (the last 10)
 
-struct ChoiceShared {
-  unsigned hist[kDigits];      // this block's
+struct __align__(16) ChoiceShared {
+  unsigned hist[kDigits];      // this block's; zero between digits
   unsigned total[kDigits];     // the cluster's
   unsigned warp_sum[kWarps];
-  unsigned found, above;
+  unsigned found, above, held;
   unsigned over[kMostBlocks], even[kMostBlocks];  // of each block, in every block
-  int64_t warp_slot[kWarps];
 };
 
 // Sum over the threads before this one; *all: of the block.
@@ -149,10 +199,13 @@ __device__ __forceinline__ unsigned scan_before(ChoiceShared& s, unsigned v, uns
   return before + incl - v;
 }
 
+// EACH positions a thread, in a run, whose keys stay in registers; 0: as many as it takes, read anew in each pass.
+template <int EACH>
 __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
   __shared__ ChoiceShared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
+  for (int i = threadIdx.x; i < kDigits; i += kThreads) s.hist[i] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t bh = blockIdx.x / blocks, b = bh / p.heads, h = bh % p.heads;
@@ -160,22 +213,39 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
   const int64_t len = clamped(p.lengths[b], p.capacity);
   const int64_t kept = min(len, p.keep), old = len - min(p.recent, len);  // the last ones stay
   const unsigned want = static_cast<unsigned>(len > p.keep ? p.keep - (len - old) : old);  // of the others
-  // this block's run of positions
-  const int64_t run = ((len + blocks - 1) / blocks + 3) / 4 * 4;
-  const int64_t begin = min(len, run * rank), end = min(len, begin + run);
+  // this thread's run of positions
+  const int64_t each = EACH ? EACH : (len + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
+  const int64_t begin = min(len, (int64_t(rank) * kThreads + threadIdx.x) * each), end = min(len, begin + each);
+  const bool choose = want < old;
+  uint32_t keys[EACH ? EACH : 1];
+  if constexpr (EACH > 0) {
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) keys[e] = begin + e < end ? order_key_f32(__float_as_uint(score[begin + e])) : 0;
+  }
+  auto key_at = [&](int64_t i, int e) -> uint32_t {
+    if constexpr (EACH > 0) return keys[e];
+    else return order_key_f32(__float_as_uint(score[i]));
+  };
+  auto run = [&](auto f) {
+    if constexpr (EACH > 0) {
+#pragma unroll
+      for (int e = 0; e < EACH; ++e)
+        if (begin + e < end) f(begin + e, e);
+    } else {
+      for (int64_t i = begin; i < end; ++i) f(i, 0);
+    }
+  };
   cluster_sync();               // (every block has started before another reaches into its memory)
   uint32_t key = 0, mask = 0;   // of the last one kept
   unsigned left = want;         // of those with the key's bits under the mask
-  const bool choose = want < old;
   if (choose && want > 0) {
+#pragma unroll 1
     for (int digit = 0; digit < 3; ++digit) {
       const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
-      for (int i = threadIdx.x; i < kDigits; i += kThreads) s.hist[i] = 0;
-      __syncthreads();
-      for (int64_t i = begin + threadIdx.x; i < min(end, old); i += kThreads) {
-        const uint32_t k = order_key_f32(__float_as_uint(score[i]));
-        if ((k & mask) == key) atomicAdd(&s.hist[(~k >> shift) & ((1u << bits) - 1)], 1u);
-      }
+      run([&](int64_t i, int e) {
+        const uint32_t k = key_at(i, e);
+        if (i < old && (k & mask) == key) atomicAdd(&s.hist[(~k >> shift) & ((1u << bits) - 1)], 1u);
+      });
       cluster_sync();
       const int share = kDigits / blocks;
       for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
@@ -185,14 +255,18 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
       }
       cluster_sync();
       unsigned n[kDigits / kThreads], sum = 0, all;
+      const uint4 four = *reinterpret_cast<const uint4*>(&s.total[threadIdx.x * 4]);
+      n[0] = four.x, n[1] = four.y, n[2] = four.z, n[3] = four.w;
+      *reinterpret_cast<uint4*>(&s.hist[threadIdx.x * 4]) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int q = 0; q < kDigits / kThreads; ++q) sum += n[q] = s.total[threadIdx.x * (kDigits / kThreads) + q];
+      for (int q = 0; q < kDigits / kThreads; ++q) sum += n[q];
       unsigned before = scan_before(s, sum, &all);
 #pragma unroll
       for (int q = 0; q < kDigits / kThreads; ++q) {
         if (before < left && left <= before + n[q]) {
           s.found = threadIdx.x * (kDigits / kThreads) + q;
           s.above = before;
+          s.held = n[q];
         }
         before += n[q];
       }
@@ -200,52 +274,46 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
       key |= (~s.found & ((1u << bits) - 1)) << shift;
       mask |= ((1u << bits) - 1) << shift;
       left -= s.above;
+      const bool all_of_them = s.held == left;
       __syncthreads();
+      if (all_of_them) break;  // (the digits below do not matter)
     }
   }
-  // kept: the recent ones, scores above the key's, and the first `left` that equal it
-  auto state = [&](int64_t i) -> int {  // 2: kept, 1: equal, 0
+  // kept: the recent ones, scores above the key's, and the first `left` of those that equal it
+  auto state = [&](int64_t i, int e) -> int {  // 2: kept, 1: equal, 0
     if (i >= old || !choose) return 2;
     if (want == 0) return 0;
-    const uint32_t k = order_key_f32(__float_as_uint(score[i]));
+    const uint32_t k = key_at(i, e) & mask;
     return k > key ? 2 : k == key ? 1 : 0;
   };
-  unsigned over = 0, even = 0;
-  for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
-    const int st = state(i);
+  unsigned over = 0, even = 0, all_over, all_even;
+  run([&](int64_t i, int e) {
+    const int st = state(i, e);
     over += st == 2;
     even += st == 1;
-  }
-  unsigned all_over, all_even;
-  scan_before(s, over, &all_over);
-  scan_before(s, even, &all_even);
+  });
+  over = scan_before(s, over, &all_over);
+  even = scan_before(s, even, &all_even);
   if (threadIdx.x < blocks) {
     ChoiceShared* peer = cluster.map_shared_rank(&s, threadIdx.x);
     peer->over[rank] = all_over;
     peer->even[rank] = all_even;
   }
   cluster_sync();
-  int64_t slot = 0;
-  unsigned equals = 0;  // equal ones before
   for (int q = 0; q < rank; ++q) {
-    slot += s.over[q];
-    equals += s.even[q];
+    over += s.over[q];
+    even += s.even[q];
   }
-  slot += min(equals, left);
-  for (int64_t i0 = begin; i0 < end; i0 += kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const int st = i < end ? state(i) : 0;
-    unsigned n_even, n_kept;
-    const unsigned e = equals + scan_before(s, st == 1, &n_even);
-    const bool stays = st == 2 || (st == 1 && e < left);
-    const unsigned at = scan_before(s, stays, &n_kept);
-    if (stays) {
-      p.kept[bh * p.keep + slot + at] = i;
-      p.out_score[bh * p.keep + slot + at] = score[i];
-    }
-    equals += n_even;
-    slot += n_kept;
-  }
+  int64_t slot = bh * p.keep + over + min(even, left);
+  run([&](int64_t i, int e) {
+    const int st = state(i, e);
+    const bool stays = st == 2 || (st == 1 && even < left);
+    even += st == 1;
+    if (!stays) return;
+    p.kept[slot] = i;
+    p.out_score[slot] = score[i];
+    ++slot;
+  });
   for (int64_t i = kept + rank * kThreads + threadIdx.x; i < p.keep; i += int64_t(blocks) * kThreads) {
     p.kept[bh * p.keep + i] = -1;
     p.out_score[bh * p.keep + i] = 0.0f;
@@ -269,26 +337,40 @@ __global__ void __launch_bounds__(256) move_kept_kernel(const MoveKept p) {
   const int64_t i = int64_t(blockIdx.x) * (256 / p.share) + threadIdx.x / p.share;
   if (i >= p.total) return;
   const int64_t bh = i / p.keep, b = bh / p.heads, h = bh % p.heads, from = p.kept[i];
+  const int at = threadIdx.x % p.share;
+  const int dims[2] = {static_cast<int>(p.dim[0]), static_cast<int>(p.dim[1])}, most = max(dims[0], dims[1]);
+  const T* src[2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const T* src = static_cast<const T*>(p.in[w].data) + b * p.in[w].batch + h * p.in[w].head + from * p.in[w].row;
-    T* dst = static_cast<T*>(p.out[w]) + i * p.dim[w];
-    for (int64_t c = int64_t(threadIdx.x % p.share) * VEC; c < p.dim[w]; c += int64_t(p.share) * VEC) {
-      Raw<T, VEC> v;
-      v.clear();
-      if (from >= 0) v.load_nc(src + c);
-      if constexpr (VEC == 1) dst[c] = v.u;
-      else __stcs(reinterpret_cast<uint4*>(dst + c), v.u);
-    }
+  for (int w = 0; w < 2; ++w) src[w] = static_cast<const T*>(p.in[w].data) + b * p.in[w].batch + h * p.in[w].head + from * p.in[w].row;
+  // (the loads of both first, and without vectors four values of each)
+  constexpr int kEach = VEC > 1 ? 1 : 4;
+  for (int c0 = at * VEC; c0 < most; c0 += p.share * VEC * kEach) {
+    Raw<T, VEC> v[2][kEach];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int c = c0 + e * p.share;
+        v[w][e].clear();
+        if (from >= 0 && c < dims[w]) v[w][e].load_nc(src[w] + c);
+      }
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int c = c0 + e * p.share;
+        T* dst = static_cast<T*>(p.out[w]) + i * p.dim[w] + c;
+        if (c >= dims[w]) continue;
+        if constexpr (VEC == 1) *dst = v[w][e].u;
+        else __stcs(reinterpret_cast<uint4*>(dst), v[w][e].u);
+      }
   }
 }
 
 // ---- one token ----------------------------------------------------------------------
-template <typename W>
-__device__ __forceinline__ float weight_at(const W* row, int64_t i) { return counted(to_f32(row[i])); }
-
-// A cluster a head: adds the group's weights to the scores, finds the slot and writes the token there.
-template <typename W>
+// A cluster a head: adds the group's weights to the scores, finds the slot and writes the token there.  A thread holds WIDE slots
+// side by side, whose weights, score and positions are all under way at once; where rows are not on 16-byte boundaries, one.
+template <typename W, int WIDE>
 __global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
   __shared__ uint64_t warp_least[kWarps];
   __shared__ uint64_t leasts[kMostBlocks];
@@ -302,20 +384,68 @@ __global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
   int64_t* positions = static_cast<int64_t*>(p.positions.data) + b * p.positions.batch + h * p.positions.head;
   const W* weights = static_cast<const W*>(p.weights.data);
   if (weights) weights += b * p.weights.batch + h * p.group * p.weights.head;
-  const int64_t run = (p.capacity + blocks - 1) / blocks;
-  const int64_t begin = min(len, run * rank), end = min(len, begin + run);
+  const int n = weights ? static_cast<int>(p.group * p.queries) : 0, queries = static_cast<int>(p.queries);
+  const bool full = seen >= p.capacity;
   uint64_t least = ~uint64_t(0);  // (score, slot) of the least that may go
-  for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
-    Sum2 sum;
-    sum.add(score[i]);
-    if (weights) {
-      for (int64_t g = 0; g < p.group; ++g)
-        for (int64_t q = 0; q < p.queries; ++q) sum.add(weight_at(weights + g * p.weights.head + q * p.weights.row, i));
-      score[i] = sum.value();
+  for (int64_t i = (int64_t(rank) * kThreads + threadIdx.x) * WIDE; i < len; i += int64_t(blocks) * kThreads * WIDE) {
+    // (a run's slots behind `len` are read, not written: they lie within the capacity)
+    Sum2 sum[WIDE];
+    int64_t at[WIDE];
+    if constexpr (WIDE > 1) {
+#pragma unroll
+      for (int e = 0; e < WIDE; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(score + i + e);
+        sum[e].hi = v.x, sum[e + 1].hi = v.y, sum[e + 2].hi = v.z, sum[e + 3].hi = v.w;
+      }
+    } else {
+      sum[0].hi = score[i];
     }
-    if (seen >= p.capacity && (p.recent == 0 || positions[i] < seen - p.recent)) {
-      const uint64_t key = static_cast<uint64_t>(order_key_f32(__float_as_uint(sum.value()))) << 32 | static_cast<uint32_t>(i);
-      least = min(least, key);
+    if (full && p.recent > 0) {
+      if constexpr (WIDE > 1) {
+#pragma unroll
+        for (int e = 0; e < WIDE; e += 2) {
+          const longlong2 v = *reinterpret_cast<const longlong2*>(positions + i + e);
+          at[e] = v.x, at[e + 1] = v.y;
+        }
+      } else {
+        at[0] = positions[i];
+      }
+    }
+    constexpr int kAhead = 4;
+    for (int r0 = 0; r0 < n; r0 += kAhead) {
+      Raw<W, WIDE> v[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int r = r0 + a, g = r / queries;
+        v[a].clear();
+        if (r < n) v[a].load_nc(weights + g * p.weights.head + (r - g * queries) * p.weights.row + i);
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        Vec<W, WIDE> x;
+        x.set_raw(v[a]);
+#pragma unroll
+        for (int e = 0; e < WIDE; ++e) sum[e].add(counted(x.v[e]));
+      }
+    }
+    float value[WIDE];
+#pragma unroll
+    for (int e = 0; e < WIDE; ++e) {
+      value[e] = sum[e].value();
+      if (full && (p.recent == 0 || at[e] < seen - p.recent))
+        least = min(least, static_cast<uint64_t>(order_key_f32(__float_as_uint(value[e]))) << 32 | static_cast<uint32_t>(i + e));
+    }
+    if (n) {
+      if (WIDE > 1 && i + WIDE <= len) {
+        if constexpr (WIDE > 1) {
+#pragma unroll
+          for (int e = 0; e < WIDE; e += 4) *reinterpret_cast<float4*>(score + i + e) = make_float4(value[e], value[e + 1], value[e + 2], value[e + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < WIDE; ++e)
+          if (i + e < len) score[i + e] = value[e];
+      }
     }
   }
 #pragma unroll
@@ -386,9 +516,8 @@ template <typename T>
 cudaError_t add_weights(const Evict& p, float* out, cudaStream_t st) {
   constexpr int kVec = 16 / sizeof(T);
   const WeightSums w{p.weights, p.group, p.queries, p.heads, p.capacity, p.score, p.lengths, out};
-  // (the last vector of a row may reach past its length, not past the capacity)
   const bool wide = aligned_view(p.weights, sizeof(T)) && p.capacity % kVec == 0;
-  const int64_t each = 32 * (wide ? kVec : 1);
+  const int64_t each = 32 * (wide ? kVec : 4);
   const int64_t blocks = (p.capacity + each - 1) / each * p.batch * p.heads;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);
@@ -404,7 +533,7 @@ cudaError_t move_kept(const Evict& p, cudaStream_t st) {
                     (reinterpret_cast<uintptr_t>(p.out_keys) | reinterpret_cast<uintptr_t>(p.out_values)) % 16 == 0;
   const int64_t dim = p.key_dim > p.value_dim ? p.key_dim : p.value_dim;
   m.share = 8;
-  while (m.share < 256 && m.share * (wide ? kVec : 1) < dim) m.share *= 2;
+  while (m.share < 256 && m.share * (wide ? kVec : 4) < dim) m.share *= 2;
   const int64_t blocks = (m.total + 256 / m.share - 1) / (256 / m.share);
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   return wide ? launch_after(move_kept_kernel<T, kVec>, static_cast<unsigned>(blocks), 256, 0, st, m)
@@ -430,16 +559,27 @@ cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st) {
     c.ld_batch = p.heads * p.capacity;
     c.ld = p.capacity;
   }
-  cudaError_t e = launch_clusters(choice_kernel, c, p.batch * p.heads, blocks_for(p.batch * p.heads, p.capacity, 2048), st);
+  const int64_t rows = p.batch * p.heads;
+  const int blocks = blocks_for(rows, p.capacity, 2048);
+  // positions a thread: in registers up to 16
+  const int64_t each = (p.capacity + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
+  cudaError_t e = launch_clusters(each <= 4 ? choice_kernel<4> : each <= 16 ? choice_kernel<16> : choice_kernel<0>, c, rows, blocks, st);
   if (e != cudaSuccess) return e;
   return p.dtype == kF32 ? move_kept<float>(p, st) : move_kept<__nv_bfloat16>(p, st);
 }
 
-cudaError_t launch_replace(const Replace& p, cudaStream_t st) {
+template <typename W>
+static cudaError_t replace_by(const Replace& p, cudaStream_t st) {
+  constexpr int kVec = 16 / sizeof(W);
   const int64_t rows = p.batch * p.heads;
-  const int blocks = blocks_for(rows, p.capacity, 512);
-  return p.weights_dtype == kF32 ? launch_clusters(replace_kernel<float>, p, rows, blocks, st)
-                                 : launch_clusters(replace_kernel<__nv_bfloat16>, p, rows, blocks, st);
+  auto on = [](const View& v, int64_t size) { return aligned_view(View{v.data, v.batch, v.head, 0}, size); };
+  const bool wide = p.capacity % kVec == 0 && on(p.score, 4) && on(p.positions, 8) && (!p.weights.data || aligned_view(p.weights, sizeof(W)));
+  if (wide) return launch_clusters(replace_kernel<W, kVec>, p, rows, blocks_for(rows, p.capacity, 2048), st);
+  return launch_clusters(replace_kernel<W, 1>, p, rows, blocks_for(rows, p.capacity, 512), st);
+}
+
+cudaError_t launch_replace(const Replace& p, cudaStream_t st) {
+  return p.weights_dtype == kF32 ? replace_by<float>(p, st) : replace_by<__nv_bfloat16>(p, st);
 }
 
 }  // namespace tk

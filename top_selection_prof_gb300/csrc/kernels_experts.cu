@@ -105,6 +105,63 @@ __global__ void __launch_bounds__(kSortThreads) expert_rank_kernel(const int64_t
 }
 
 // ---- moving rows --------------------------------------------------------------------
+// What one of `share` threads holds of a row of d values: 16 bytes side by side where rows allow it, else four values `share`
+// apart, so that as many bytes are under way and a warp's loads are whole lines all the same.
+template <typename T, int VEC>
+struct Piece {
+  static constexpr int kWide = VEC > 1 ? VEC : 4;
+  Raw<T, VEC> r[VEC > 1 ? 1 : kWide];
+  __device__ __forceinline__ static int first(int at) { return at * VEC; }
+  __device__ __forceinline__ static int step(int share) { return share * kWide; }
+  __device__ __forceinline__ void load(const T* row, int c, int d, int share) {
+    if constexpr (VEC > 1) {
+      r[0].load_nc(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kWide; ++e) {
+        r[e].clear();
+        if (c + e * share < d) r[e].load_nc(row + c + e * share);
+      }
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (auto& v : r) v.clear();
+  }
+  __device__ __forceinline__ void values(float* f) const {
+    if constexpr (VEC > 1) {
+      Vec<T, VEC> v;
+      v.set_raw(r[0]);
+#pragma unroll
+      for (int e = 0; e < kWide; ++e) f[e] = v.v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < kWide; ++e) f[e] = to_f32(r[e].u);
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int c, int d, int share) const {
+    if constexpr (VEC > 1) {
+      __stcs(reinterpret_cast<uint4*>(row + c), r[0].u);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kWide; ++e)
+        if (c + e * share < d) row[c + e * share] = r[e].u;
+    }
+  }
+  __device__ __forceinline__ static void store(const float* f, T* row, int c, int d, int share) {
+    if constexpr (VEC > 1) {
+      Vec<T, VEC> v;
+#pragma unroll
+      for (int e = 0; e < kWide; ++e) v.v[e] = f[e];
+      v.store_stream(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kWide; ++e)
+        if (c + e * share < d) row[c + e * share] = from_f32<T>(f[e]);
+    }
+  }
+};
+
 struct MoveRows {
   const void* x;
   int64_t ldx, tokens, d;
@@ -116,21 +173,21 @@ struct MoveRows {
   void* xs;
 };
 
-// Writes token t's row to the k rows of its places (zeros to those without an expert), `threads` threads of which this is `at`.
+// Writes token t's row to the k rows of its places (zeros to those without an expert), `share` threads of which this is `at`.
 template <typename T, int VEC>
-__device__ __forceinline__ void spread_row(const MoveRows& p, int64_t t, const int* rows, int at, int threads) {
+__device__ __forceinline__ void spread_row(const MoveRows& p, int64_t t, const int* rows, int at, int share) {
+  using P = Piece<T, VEC>;
+  const int d = static_cast<int>(p.d);
   const T* src = static_cast<const T*>(p.x) + t * p.ldx;
-  T* xs = static_cast<T*>(p.xs);
-  for (int64_t c = int64_t(at) * VEC; c < p.d; c += int64_t(threads) * VEC) {
-    Raw<T, VEC> v, zero;
-    v.load_nc(src + c);
+  for (int c = P::first(at); c < d; c += P::step(share)) {
+    P v, zero;
+    v.load(src, c, d, share);
     zero.clear();
     for (int j = 0; j < p.k; ++j) {
       const int r = rows[j];
-      const int64_t row = r < 0 ? ~r : r;
-      T* dst = xs + row * p.d + c;
-      if constexpr (VEC == 1) *dst = r < 0 ? zero.u : v.u;
-      else __stcs(reinterpret_cast<uint4*>(dst), r < 0 ? zero.u : v.u);
+      T* dst = static_cast<T*>(p.xs) + static_cast<int64_t>(r < 0 ? ~r : r) * p.d;
+      if (r < 0) zero.store(dst, c, d, share);
+      else v.store(dst, c, d, share);
     }
   }
 }
@@ -210,6 +267,7 @@ struct JoinRows {
   void* dweights;       // nullable
 };
 constexpr int kTogether = 8;  // rows of a token that are read together
+constexpr int kRowsBlock = 32; // rows that a block of rows looks after
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const JoinRows p, int share) {
@@ -220,33 +278,33 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const JoinRows p, int
   const T* ys = static_cast<const T*>(p.ys);
   const T* w = static_cast<const T*>(p.weights) + (p.weights ? t * p.k : 0);
   const int64_t* place = p.place + t * p.k;
-  for (int64_t c = int64_t(threadIdx.x % share) * VEC; c < p.d; c += int64_t(share) * VEC) {
-    float sum[VEC] = {};
+  using P = Piece<T, VEC>;
+  const int d = static_cast<int>(p.d);
+  for (int c = P::first(threadIdx.x % share); c < d; c += P::step(share)) {
+    float sum[P::kWide] = {};
     for (int j0 = 0; j0 < p.k; j0 += kTogether) {
-      Raw<T, VEC> v[kTogether];
+      P v[kTogether];
       float f[kTogether];
 #pragma unroll
       for (int j = 0; j < kTogether; ++j) {
         const int64_t r = j0 + j < p.k ? place[j0 + j] : -1;
         f[j] = 0.0f;
-        v[j].clear();
         if (r >= 0 && r < p.rows) {
-          v[j].load_nc(ys + r * p.ldy + c);
+          v[j].load(ys + r * p.ldy, c, d, share);
           f[j] = p.weights ? to_f32(w[j0 + j]) : 1.0f;
+        } else {
+          v[j].clear();
         }
       }
 #pragma unroll
       for (int j = 0; j < kTogether; ++j) {
-        Vec<T, VEC> x;
-        x.set_raw(v[j]);
+        float x[P::kWide];
+        v[j].values(x);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum[e] = fmaf(f[j], x.v[e], sum[e]);
+        for (int e = 0; e < P::kWide; ++e) sum[e] = fmaf(f[j], x[e], sum[e]);
       }
     }
-    Vec<T, VEC> out;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) out.v[e] = sum[e];
-    out.store_stream(static_cast<T*>(p.y) + t * p.d + c);
+    P::store(sum, static_cast<T*>(p.y) + t * p.d, c, d, share);
   }
 }
 
@@ -271,8 +329,8 @@ __global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* p
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRows p, int share, int64_t token_blocks) {
   __shared__ float dots[kThreads / 32][kTogether];
-  __shared__ int todo[kThreads];
-  __shared__ unsigned n_todo, n_found;
+  __shared__ unsigned listed[kRowsBlock];
+  __shared__ unsigned hit_mask[kThreads / 32];
   grid_dependency_wait();
   grid_launch_dependents();
   const T* ys = static_cast<const T*>(p.ys);
@@ -296,29 +354,31 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
         f[j] = row[j] >= 0 && weights ? to_f32(weights[s]) : 1.0f;
         sole[j] = dys && row[j] >= 0 && p.listed[row[j]] == 1;
       }
-      for (int64_t c = int64_t(at) * VEC; in && c < p.d; c += int64_t(share) * VEC) {
-        Vec<T, VEC> g;
-        g.load_nc(dy + t * p.lddy + c);
-        Raw<T, VEC> v[kTogether];
+      using P = Piece<T, VEC>;
+      const int d = static_cast<int>(p.d);
+      for (int c = P::first(at); in && c < d; c += P::step(share)) {
+        P raw, v[kTogether];
+        raw.load(dy + t * p.lddy, c, d, share);
         if (p.dweights) {
 #pragma unroll
           for (int j = 0; j < kTogether; ++j)
-            if (row[j] >= 0) v[j].load_nc(ys + row[j] * p.ldy + c);
+            if (row[j] >= 0) v[j].load(ys + row[j] * p.ldy, c, d, share);
         }
+        float g[P::kWide];
+        raw.values(g);
 #pragma unroll
         for (int j = 0; j < kTogether; ++j) {
           if (row[j] < 0) continue;
+          float x[P::kWide];
           if (p.dweights) {
-            Vec<T, VEC> x;
-            x.set_raw(v[j]);
+            v[j].values(x);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) dot[j] = fmaf(x.v[e], g.v[e], dot[j]);
+            for (int e = 0; e < P::kWide; ++e) dot[j] = fmaf(x[e], g[e], dot[j]);
           }
           if (sole[j]) {
-            Vec<T, VEC> out;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) out.v[e] = f[j] * g.v[e];
-            out.store_stream(dys + row[j] * p.d + c);
+            for (int e = 0; e < P::kWide; ++e) x[e] = f[j] * g[e];
+            P::store(x, dys + row[j] * p.d, c, d, share);
           }
         }
       }
@@ -339,15 +399,21 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
     }
     return;
   }
-  if (threadIdx.x == 0) n_todo = 0;
+  const int64_t r0 = (int64_t(blockIdx.x) - token_blocks) * kRowsBlock;
+  if (threadIdx.x < kRowsBlock) listed[threadIdx.x] = r0 + threadIdx.x < p.rows ? p.listed[r0 + threadIdx.x] : 1;
   __syncthreads();
-  const int64_t r0 = (int64_t(blockIdx.x) - token_blocks) * kThreads;
-  if (r0 + threadIdx.x < p.rows && p.listed[r0 + threadIdx.x] != 1) todo[atomicAdd(&n_todo, 1u)] = threadIdx.x;
-  __syncthreads();
+  using P = Piece<T, VEC>;
+  const int d = static_cast<int>(p.d);
+  P zero;
+  zero.clear();
+  for (int q = warp; q < kRowsBlock; q += kThreads / 32)
+    if (listed[q] == 0)
+      for (int c = P::first(lane); c < d; c += P::step(32)) zero.store(dys + (r0 + q) * p.d, c, d, 32);
   const int64_t total = p.tokens * p.k;
-  for (unsigned q = 0; q < n_todo; ++q) {
-    const int64_t r = r0 + todo[q];
-    const unsigned times = p.listed[r];
+  for (int q = 0; q < kRowsBlock; ++q) {
+    const unsigned times = listed[q];
+    if (times < 2) continue;
+    const int64_t r = r0 + q;
     for (int64_t c0 = 0; c0 < p.d; c0 += kThreads * VEC) {
       const int64_t c = c0 + threadIdx.x * VEC;
       Vec<T, VEC> sum;
@@ -357,7 +423,6 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
       for (int64_t s0 = 0; seen < times && s0 < total; s0 += kThreads) {
         const bool hit = s0 + threadIdx.x < total && p.place[s0 + threadIdx.x] == r;
         const unsigned hits = __ballot_sync(~0u, hit);
-        __shared__ unsigned hit_mask[kThreads / 32];
         __syncthreads();
         if (lane == 0) hit_mask[warp] = hits;
         __syncthreads();
@@ -375,7 +440,6 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
       }
       if (c < p.d) sum.store_stream(dys + r * p.d + c);
     }
-    __syncthreads();
   }
 }
 
@@ -386,10 +450,11 @@ bool whole_vectors(int64_t size, int64_t d, std::initializer_list<const void*> a
   for (int64_t ld : lds) low |= static_cast<uintptr_t>(ld * size);
   return low % 16 == 0;
 }
-// Threads that share a token's row: a power of two, one vector each or more, a warp at least.
+// Threads that share a token's row: a power of two, one piece each or more, a warp at least.
 int share_of(int64_t d, int vec) {
+  const int wide = vec > 1 ? vec : 4;
   int share = 32;
-  while (share < kThreads && int64_t(share) * vec < d) share *= 2;
+  while (share < kThreads && int64_t(share) * wide < d) share *= 2;
   return share;
 }
 int64_t blocks_of(int64_t tokens, int share) { return (tokens + kThreads / share - 1) / (kThreads / share); }
@@ -443,8 +508,8 @@ cudaError_t backward(const Combine& p, Scratch& sc, cudaStream_t st) {
   int64_t row_blocks = 0;
   if (p.dys) {
     q.listed = sc.take<unsigned>(p.rows);
-    row_blocks = (p.rows + kThreads - 1) / kThreads;
-    cudaError_t e = launch_after(clear_listed_kernel, static_cast<unsigned>(row_blocks), kThreads, 0, st, q.listed, p.rows);
+    row_blocks = (p.rows + kRowsBlock - 1) / kRowsBlock;
+    cudaError_t e = launch_after(clear_listed_kernel, static_cast<unsigned>((p.rows + kThreads - 1) / kThreads), kThreads, 0, st, q.listed, p.rows);
     const unsigned blocks = static_cast<unsigned>((total + kThreads - 1) / kThreads);
     if (e == cudaSuccess && blocks) e = launch_after(count_listed_kernel, blocks, kThreads, 0, st, p.place, total, q.listed, p.rows);
     if (e != cudaSuccess) return e;

@@ -446,7 +446,7 @@ int check_cache(int dtype, int weights_dtype, bool weighted, int64_t batch, int6
     return TOPK_EUNSUPPORTED;
   // (byte counts stay below 2^63)
   const int64_t most = int64_t(1) << 40, dim = key_dim > value_dim ? key_dim : value_dim;
-  if (dim > (1 << 20) || batch * heads > most / capacity || (weighted && group * queries > most / heads)) return TOPK_EUNSUPPORTED;
+  if (dim > (1 << 20) || batch * heads > most / capacity || (weighted && (group * queries > kMaxExtent || group * queries > most / heads))) return TOPK_EUNSUPPORTED;
   return TOPK_OK;
 }
 
