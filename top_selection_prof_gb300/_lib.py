@@ -109,7 +109,7 @@ def get():
         lib.topk_dispatch.argtypes = [vp, i64, vp, c_int, i64, i64, i64, i64, vp, vp, vp, vp]
         lib.topk_combine.argtypes = [vp, i64, i64, vp, vp, c_int, i64, i64, i64, vp, vp]
         lib.topk_combine_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, c_int, i64, i64, i64, vp, vp, vp]
-        view = ctypes.POINTER(TopkView)
+        view = vp  # (a TopkView's address, or its bytes)
         lib.topk_evict.argtypes = [view, view, view, vp, view, c_int, i64, i64, c_int, i64, i64, i64, i64, i64, i64, i64, vp, vp,
                                    vp, vp, vp, vp]
         lib.topk_replace.argtypes = [view, view, view, view, vp, view, view, view, c_int, i64, i64, c_int, i64, i64, i64, i64,

@@ -16,12 +16,14 @@ kernels, stream= as there, nothing recorded for autograd.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 import torch
 
-from ._lib import TopkView
 from .operators import _CODES, _call, _empty, _first, _like, _matrix, _of_places, _vector
+
+_F32, _I64 = torch.float32, torch.int64
+_VIEW = struct.Struct("4q").pack    # a topk_view_t
 
 
 def _by_row(v, dtype, device, rows, name):
@@ -45,27 +47,27 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     rows, n = logits.shape
     device = logits.device
     ld = _matrix(logits, rows, n, "logits")
-    f32 = torch.float32
-    pu = _vector(u, f32, device, rows, "u")
-    t, pt = _by_row(temperature, f32, device, rows, "temperature")
+    pu = _vector(u, _F32, device, rows, "u")
+    t, pt = _by_row(temperature, _F32, device, rows, "temperature")
     k, pk = _by_row(top_k, torch.int32, device, rows, "top_k")
-    p, pp = _by_row(top_p, f32, device, rows, "top_p")
-    m, pm = _by_row(min_p, f32, device, rows, "min_p")
-    tokens = _empty((rows,), torch.int64, device, stream)
-    logprobs = _empty((rows,), f32, device, stream)
-    _call("topk_sample", device, stream, (logits, u, *(v for v in (temperature, top_k, top_p, min_p) if isinstance(v, torch.Tensor)),
-                                          tokens, logprobs), logits.data_ptr(), ld, code, rows, n, pu, t, pt, k, pk, p, pp, m, pm,
+    p, pp = _by_row(top_p, _F32, device, rows, "top_p")
+    m, pm = _by_row(min_p, _F32, device, rows, "min_p")
+    tokens = _empty((rows,), _I64, device, stream)
+    logprobs = _empty((rows,), _F32, device, stream)
+    used = (logits, u, temperature if pt else None, top_k if pk else None, top_p if pp else None, min_p if pm else None, tokens, logprobs)
+    _call("topk_sample", device, stream, used, logits.data_ptr(), ld, code, rows, n, pu, t, pt, k, pk, p, pp, m, pm,
           tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs
 
 
 def _choices(t, tokens, device, name):
     """k of an int64 tensor (tokens, k)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int64 or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I64 or t.device != device:
         raise TypeError("%s must be an int64 tensor on %s" % (name, device))
-    if t.dim() != 2 or (tokens is not None and t.shape[0] != tokens) or t.shape[1] < 1 or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with shape (tokens, k), k >= 1, got %s" % (name, tuple(t.shape)))
-    return t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or (tokens is not None and shape[0] != tokens) or shape[1] < 1 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with shape (tokens, k), k >= 1, got %s" % (name, tuple(shape)))
+    return shape[1]
 
 
 def dispatch(x, idx, experts: int, stream=None):
@@ -82,8 +84,8 @@ def dispatch(x, idx, experts: int, stream=None):
     ldx = _matrix(x, tokens, d, "x")
     k = _choices(idx, tokens, device, "idx")
     xs = _empty((tokens * k, d), dtype, device, stream)
-    place = _empty((tokens, k), torch.int64, device, stream)
-    offsets = _empty((max(experts, 0) + 1,), torch.int64, device, stream)
+    place = _empty((tokens, k), _I64, device, stream)
+    offsets = _empty((max(experts, 0) + 1,), _I64, device, stream)
     _call("topk_dispatch", device, stream, (x, idx, xs, place, offsets), x.data_ptr(), ldx, idx.data_ptr(), code, tokens, k,
           experts, d, xs.data_ptr(), place.data_ptr(), offsets.data_ptr())
     return xs, place, offsets
@@ -129,39 +131,47 @@ def combine_backward(dy, ys, place, weights=None, need=(True, True), stream=None
     return dys, dw
 
 
-def _view(t, dtype, device, shape, name):
-    """A TopkView of a tensor (batch, heads, rows, values), or without the dimension of rows, whose values are contiguous."""
-    _like(t, dtype, device, name)
+def _view(t, dtype, index, shape, name):
+    """A topk_view_t of a tensor (batch, heads, rows, values), or without the dimension of rows, whose values are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        raise TypeError("%s must be a %s tensor on cuda:%d" % (name, dtype, index))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     by = t.stride()
     if by[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s must be contiguous along its last dimension" % name)
-    return TopkView(t.data_ptr(), by[0], by[1], by[2] if len(shape) == 4 else 0)
+    return _VIEW(t.data_ptr(), by[0], by[1], by[2])
 
 
 def _cache(keys, values, score, lengths, weights):
-    """Checks what evict and replace_ have in common: (code, batch, heads, capacity, views, weights' view, dtype, group, queries)."""
+    """Checks what evict and replace_ have in common: ((batch, heads, capacity, key dim, value dim), dtype, device index, views of
+    keys, values and score, lengths' pointer, (weights' view, dtype, group, queries, the cache's dtype))."""
     code = _first(keys)
-    if keys.dim() != 4:
+    shape = keys.shape
+    if len(shape) != 4:
         raise ValueError("keys must be 4-D (batch, heads, capacity, dim)")
-    batch, heads, capacity, _ = keys.shape
-    dtype, device = keys.dtype, keys.device
+    batch, heads, capacity, kd = shape
+    dtype, index = keys.dtype, keys.get_device()
     if not isinstance(values, torch.Tensor) or values.dim() != 4:
         raise ValueError("values must be 4-D (batch, heads, capacity, dim)")
-    views = (_view(keys, dtype, device, keys.shape, "keys"),
-             _view(values, dtype, device, (batch, heads, capacity, values.shape[3]), "values"),
-             _view(score, torch.float32, device, (batch, heads, capacity), "score"))
-    _vector(lengths, torch.int64, device, batch, "lengths")
+    vd = values.shape[3]
+    views = (_view(keys, dtype, index, shape, "keys"), _view(values, dtype, index, (batch, heads, capacity, vd), "values"),
+             _view(score, _F32, index, (batch, heads, capacity), "score"))
+    if not isinstance(lengths, torch.Tensor) or lengths.dtype is not _I64 or lengths.get_device() != index:
+        raise TypeError("lengths must be an int64 tensor on cuda:%d" % index)
+    if lengths.shape != (batch,) or not lengths.is_contiguous():
+        raise ValueError("lengths must be contiguous with %d values" % batch)
     if weights is None:
-        return code, batch, heads, capacity, views, None, code, 1, 0
-    if not isinstance(weights, torch.Tensor) or weights.dtype not in _CODES or weights.dim() != 4:
-        raise TypeError("weights must be a 4-D float32 or bfloat16 tensor (batch, query heads, queries, capacity)")
-    query_heads, queries = weights.shape[1], weights.shape[2]
-    if query_heads < heads or query_heads % heads:
-        raise ValueError("weights must have a multiple of the cache's %d heads, got %d" % (heads, query_heads))
-    view = _view(weights, weights.dtype, device, (batch, query_heads, queries, capacity), "weights")
-    return code, batch, heads, capacity, views, view, _CODES[weights.dtype], query_heads // heads, queries
+        added = None, code, 1, 0, code
+    else:
+        if not isinstance(weights, torch.Tensor) or weights.dtype not in _CODES or weights.dim() != 4:
+            raise TypeError("weights must be a 4-D float32 or bfloat16 tensor (batch, query heads, queries, capacity)")
+        _, query_heads, queries, _ = weights.shape
+        if query_heads < heads or query_heads % heads:
+            raise ValueError("weights must have a multiple of the cache's %d heads, got %d" % (heads, query_heads))
+        view = _view(weights, weights.dtype, index, (batch, query_heads, queries, capacity), "weights")
+        added = view, _CODES[weights.dtype], query_heads // heads, queries, code
+    return (batch, heads, capacity, kd, vd), dtype, index, views, lengths.data_ptr(), added
 
 
 def evict(keys, values, score, lengths, keep: int, recent: int = 0, weights=None, stream=None):
@@ -173,18 +183,14 @@ def evict(keys, values, score, lengths, keep: int, recent: int = 0, weights=None
     weights (batch, query heads, queries, capacity), float32 or bfloat16: what the queries of each head's group gave,
     added first (a NaN counts as 0).  kept (batch, heads, keep): positions, -1 behind the new lengths, where rows and
     scores are zeros.  Nothing is changed in place."""
-    code, batch, heads, capacity, views, view, wcode, group, queries = _cache(keys, values, score, lengths, weights)
-    dtype, device = keys.dtype, keys.device
-    kd, vd = keys.shape[3], values.shape[3]
-    rows = max(keep, 0)
+    sizes, dtype, _, views, pl, added = _cache(keys, values, score, lengths, weights)
+    batch, heads, _, kd, vd = sizes
+    device, rows = keys.device, max(keep, 0)
     ok, ov = _empty((batch, heads, rows, kd), dtype, device, stream), _empty((batch, heads, rows, vd), dtype, device, stream)
-    osc = _empty((batch, heads, rows), torch.float32, device, stream)
-    kept = _empty((batch, heads, rows), torch.int64, device, stream)
-    ol = _empty((batch,), torch.int64, device, stream)
-    _call("topk_evict", device, stream, (keys, values, score, lengths, weights, ok, ov, osc, kept, ol),
-          *map(ctypes.byref, views), lengths.data_ptr(), None if view is None else ctypes.byref(view), wcode, group, queries,
-          code, batch, heads, capacity, kd, vd, keep, recent, ok.data_ptr(), ov.data_ptr(), osc.data_ptr(), kept.data_ptr(),
-          ol.data_ptr())
+    osc, kept = _empty((batch, heads, rows), _F32, device, stream), _empty((batch, heads, rows), _I64, device, stream)
+    ol = _empty((batch,), _I64, device, stream)
+    _call("topk_evict", device, stream, (keys, values, score, lengths, weights, ok, ov, osc, kept, ol), *views, pl, *added, *sizes,
+          keep, recent, ok.data_ptr(), ov.data_ptr(), osc.data_ptr(), kept.data_ptr(), ol.data_ptr())
     return ok, ov, osc, kept, ol
 
 
@@ -195,14 +201,12 @@ def replace_(keys, values, score, positions, lengths, key, value, recent: int = 
     score is least, of those that hold positions before the last `recent` (equal ones: the lowest slot).  key, value
     (batch, heads, dim); positions (batch, heads, capacity), int64: the position in each slot; weights as in evict, by slot,
     added to the scores first.  The slot's score becomes 0.  lengths is not changed."""
-    code, batch, heads, capacity, views, view, wcode, group, queries = _cache(keys, values, score, lengths, weights)
-    dtype, device = keys.dtype, keys.device
-    kd, vd = keys.shape[3], values.shape[3]
-    at = _view(positions, torch.int64, device, (batch, heads, capacity), "positions")
-    new = _view(key, dtype, device, (batch, heads, kd), "key"), _view(value, dtype, device, (batch, heads, vd), "value")
-    slots = _empty((batch, heads), torch.int64, device, stream)
-    _call("topk_replace", device, stream, (keys, values, score, positions, lengths, key, value, weights, slots),
-          *map(ctypes.byref, views), ctypes.byref(at), lengths.data_ptr(), *map(ctypes.byref, new),
-          None if view is None else ctypes.byref(view), wcode, group, queries, code, batch, heads, capacity, kd, vd, recent,
-          slots.data_ptr())
+    sizes, dtype, index, views, pl, added = _cache(keys, values, score, lengths, weights)
+    batch, heads, capacity, kd, vd = sizes
+    device = keys.device
+    at = _view(positions, _I64, index, (batch, heads, capacity), "positions")
+    k, v = _view(key, dtype, index, (batch, heads, kd), "key"), _view(value, dtype, index, (batch, heads, vd), "value")
+    slots = _empty((batch, heads), _I64, device, stream)
+    _call("topk_replace", device, stream, (keys, values, score, positions, lengths, key, value, weights, slots), *views, at, pl, k, v,
+          *added, *sizes, recent, slots.data_ptr())
     return slots
