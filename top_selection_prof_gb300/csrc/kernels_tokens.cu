@@ -35,7 +35,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSub = 64;                     // bins an octave of weight
 constexpr int kOctaves = 16;                 // octaves that one histogram covers
 constexpr int kBins = kSub * kOctaves;
@@ -51,9 +51,10 @@ constexpr int64_t kPartMost = 131072;         // tokens of a block's part
 constexpr int kMostBlocks = 8;               // of a cluster
 // bf16 values of 2^-13 to 2^9 and their negatives are counted by value first
 constexpr unsigned kLeastValue = 0x3900, kValues = 0x4400 - 0x3900;
-constexpr int kDigitBits = 9;                // of the search by digits: a bin a thread
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;  // of the search by digits
+constexpr int kGroup = kThreads / 32;        // of the threshold: threads that form one of 32 maxima
 static_assert(kTokensMaxLen <= int64_t(1) << kIndexBits, "an index fits its bits");
-static_assert(kBins == 2 * kThreads && (1 << kDigitBits) == kThreads, "bins by thread");
+static_assert(kBins == 4 * kThreads && kDigits == 2 * kThreads, "bins and digits by thread");
 
 constexpr double kLargest = 1073741822.0;    // the largest weight
 // kLargest x 2^-(i/64 + 1/128): the weight in the middle of bin i of an octave.  (So every weight is below 2^30, and the
@@ -136,8 +137,8 @@ struct Order {
 template <int CAP>
 struct PileShared {
   uint64_t key[CAP], mass[CAP];
-  uint64_t mass_before[kThreads + 1];
-  unsigned count_before[kThreads + 1];
+  uint64_t mass_before[kDigits + 1];
+  unsigned count_before[kDigits + 1];
   unsigned n;       // listed (where more than CAP: not all)
   Scale scale;      // what they weigh, in the unit of a window
   int window;
@@ -183,6 +184,7 @@ struct Shared {
   unsigned few, bits[4];
   uint64_t few_key[32], few_mass[32];
   float least;
+  float top_p, u;
 };
 // The block's own.  (Not handed down as a reference: the compiler has to see that it is shared memory.)
 __device__ __forceinline__ Shared& own() {
@@ -235,40 +237,73 @@ __device__ __forceinline__ void scan_before(uint64_t mass, unsigned count, uint6
   __syncthreads();
 }
 
-// f(values, as they are stored, index of the first) for the block's part of the row, 16 bytes of values at a time; what is outside
-// the row is -inf.
-template <typename T, int kAhead, typename F>
-__device__ __forceinline__ void each_vector(F f) {
+// 16 bytes of the row at an end of it, what is outside as -inf.
+template <typename T>
+__device__ __noinline__ uint4 end_of_row(const T* row, int i, int n) {
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int e = 0; e < 16 / static_cast<int>(sizeof(T)); ++e) {
+    const T x = i + e >= 0 && i + e < n ? row[i + e] : from_f32<T>(-INFINITY);
+    if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(x);
+    else w[e / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x)) << 16 * (e % 2);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 16 bytes of the row from value i on.
+template <typename T>
+__device__ __forceinline__ uint4 vector_at(int i) {
   constexpr int kVec = 16 / sizeof(T);
   const Shared& s = own();
   const T* row = static_cast<const T*>(s.row);
-  const int begin = s.begin, end = s.end, n = s.n;
-  for (int at = begin + threadIdx.x * kVec; at < end; at += kAhead * kThreads * kVec) {
-    Raw<T, kVec> raw[kAhead];
+  return i >= 0 && i + kVec <= s.n ? ld_stream_v4(row + i) : end_of_row(row, i, s.n);
+}
+// f(16 bytes of values, index of the first) over the block's part of the row; what is outside the row is -inf.  After each
+// kAhead of them, note(those for which f was true, index of the first) where there are any.
+template <typename T, int kAhead, typename F, typename N>
+__device__ __forceinline__ void each_vector(F f, N note) {
+  constexpr int kVec = 16 / sizeof(T), kStep = kThreads * kVec;
+  const Shared& s = own();
+  const T* row = static_cast<const T*>(s.row);
+  const int end = s.end, n = s.n;
+  const unsigned inside = n >= kVec ? n - kVec + 1 : 0;  // first values of whole vectors
+  // (each is followed by the load of the one kAhead further on, so that as many are always under way)
+  int at = s.begin + threadIdx.x * kVec;
+  Raw<T, kVec> raw[kAhead];
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a)
+    if (at + a * kStep < end && static_cast<unsigned>(at + a * kStep) < inside) raw[a].u = ld_stream_v4(row + at + a * kStep);
+#pragma unroll 1
+  for (; at < end; at += kAhead * kStep) {
+    unsigned hits = 0;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int i = at + a * kThreads * kVec;
-      raw[a].clear();
-      if (i >= 0 && i + kVec <= n && i < end) raw[a].u = ld_stream_v4(row + i);
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = at + a * kThreads * kVec;
+      const int i = at + a * kStep, next = i + kAhead * kStep;
       if (i >= end) break;
-      if (!(i >= 0 && i + kVec <= n)) {  // (an end of the row)
-        uint32_t w[4] = {};
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const T x = i + e >= 0 && i + e < n ? row[i + e] : from_f32<T>(-INFINITY);
-          if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(x);
-          else w[e / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x)) << 16 * (e % 2);
-        }
-        raw[a].u = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      Vec<T, kVec> v;
-      v.set_raw(raw[a]);
-      f(v, raw[a], i);
+      if (static_cast<unsigned>(i) >= inside) raw[a].u = end_of_row(row, i, n);
+      if (f(raw[a], i)) hits |= 1u << a;
+      if (next < end && static_cast<unsigned>(next) < inside) raw[a].u = ld_stream_v4(row + next);
     }
+    if (hits) note(hits, at);
+  }
+}
+// Keeps the indices of noted vectors: s.few of them, those from the number `most` on not held.
+template <typename T>
+__device__ __forceinline__ void keep_noted(unsigned* noted, unsigned most, unsigned hits, int at) {
+  constexpr int kStep = kThreads * 16 / sizeof(T);
+  unsigned place = atomicAdd(&own().few, static_cast<unsigned>(__popc(hits)));
+#pragma unroll 1
+  for (; hits; hits &= hits - 1, ++place)
+    if (place < most) noted[place] = static_cast<unsigned>(at + (__ffs(static_cast<int>(hits)) - 1) * kStep);
+}
+// The largest of 16 bytes of values (NaN where all are).
+template <typename T>
+__device__ __forceinline__ float top_of(const Raw<T, 16 / sizeof(T)>& raw) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(raw.u.x), __uint_as_float(raw.u.y)), fmaxf(__uint_as_float(raw.u.z), __uint_as_float(raw.u.w)));
+  } else {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw.u);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
   }
 }
 
@@ -280,63 +315,96 @@ __device__ __forceinline__ void clear_bins() {
     for (unsigned i = threadIdx.x; i < 2 * kValues; i += kThreads) s.by_value[i] = 0;
   if (threadIdx.x == 0) s.tail = 0;
 }
-// Adds `times` tokens of value x to its bin of the window that begins `base` bins down, or to the mass behind it.
-__device__ __forceinline__ void add_to_bins(float x, unsigned times, const Scale& scale, int base, uint64_t* tail) {
+// Adds `times` tokens of each value x to its bin of the window that begins `base` bins down, or to the mass behind it.  (The N
+// weights are formed side by side.)
+template <int N>
+__device__ __forceinline__ void add_to_bins(const float* x, const unsigned* times, const Scale& scale, int base, uint64_t* tail) {
   Shared& s = own();
-  float t;
-  const int j = bin_of(x, scale, &t) - base;
-  if (j < 0) return;
-  const unsigned w = weight_in(x, j + base, t, scale, s.middle);
-  if (j < kBins) {
-    atomicAdd(&s.count[j], times);
-    atomicAdd(&s.low[j], (w & 0x7fffu) * times);
-    atomicAdd(&s.high[j], (w >> 15) * times);
-  } else {
-    const int up = kOctaves - 1 + kTailBits - j / kSub;
-    const uint64_t m = static_cast<uint64_t>(w) * times;
-    *tail += up >= 0 ? m << up : m >> -up;
+  int j[N];
+  unsigned w[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    float t;
+    j[e] = bin_of(x[e], scale, &t) - base;
+    w[e] = weight_in(x[e], max(j[e] + base, 0), t, scale, s.middle);
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (j[e] >= 0 && j[e] < kBins) {
+      atomicAdd(&s.count[j[e]], times[e]);
+      atomicAdd(&s.low[j[e]], (w[e] & 0x7fffu) * times[e]);
+      atomicAdd(&s.high[j[e]], (w[e] >> 15) * times[e]);
+    } else if (j[e] >= kBins) {
+      const int up = kOctaves - 1 + kTailBits - j[e] / kSub;
+      const uint64_t m = static_cast<uint64_t>(w[e]) * times[e];
+      *tail += up >= 0 ? m << up : m >> -up;
+    }
   }
 }
 // The bins of the block's part.  (They are clear, and the counts by value.)  A bf16 row has few values among its tokens: they
 // are counted by value, one atomic each, and each value's weight is formed once.
-template <typename T, typename F>
-__device__ __forceinline__ void fill_bins(const Scale& scale, int base, F look) {
+template <typename T, typename F, typename N>
+__device__ __forceinline__ void fill_bins(const Scale& scale, int base, F look, N note) {
   constexpr int kVec = 16 / sizeof(T);
   Shared& s = own();
   uint64_t tail = 0;
   if constexpr (sizeof(T) == 4) {
-    each_vector<T, 2>([&](const Vec<T, kVec>& v, const Raw<T, kVec>&, int i) {
-      look(v, i);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) add_to_bins(v.v[e], 1, scale, base, &tail);
-    });
+    each_vector<T, 4>([&](const Raw<T, kVec>& raw, int i) -> bool {
+      Vec<T, kVec> v;
+      v.set_raw(raw);
+      const unsigned one[kVec] = {1, 1, 1, 1};
+      add_to_bins<kVec>(v.v, one, scale, base, &tail);
+      return look(raw, i);
+    }, note);
   } else {
-    each_vector<T, 4>([&](const Vec<T, kVec>& v, const Raw<T, kVec>& raw, int i) {
-      look(v, i);
+    each_vector<T, 8>([&](const Raw<T, kVec>& raw, int i) -> bool {
       const uint32_t w[4] = {raw.u.x, raw.u.y, raw.u.z, raw.u.w};
-      bool all = true;
+      uint32_t a[4], low = 0xffffffffu, high = 0;  // without signs, two a word
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const unsigned h = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-        const unsigned at = (h & 0x7fffu) - kLeastValue;
-        if (at < kValues) atomicAdd(&s.by_value[at + (h >> 15) * kValues], 1u);
-        else all = false;
+      for (int q = 0; q < 4; ++q) {
+        a[q] = w[q] & 0x7fff7fffu;
+        low = __vminu2(low, a[q]);
+        high = __vmaxu2(high, a[q]);
       }
-      if (!all) {
+      low = min(low & 0xffffu, low >> 16);
+      high = max(high & 0xffffu, high >> 16);
+      if (low >= kLeastValue && high < kLeastValue + kValues) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // (both halves at once: below 2^16 each)
+          const uint32_t at = (a[q] - kLeastValue * 0x10001u) + ((w[q] >> 15) & 0x10001u) * kValues;
+          atomicAdd(&s.by_value[at & 0xffffu], 1u);
+          atomicAdd(&s.by_value[at >> 16], 1u);
+        }
+      } else {
 #pragma unroll 1
         for (int e = 0; e < kVec; ++e) {
           const uint32_t pair = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
-          const unsigned h = e & 1 ? pair >> 16 : pair & 0xffffu;
-          if ((h & 0x7fffu) - kLeastValue >= kValues) add_to_bins(__uint_as_float(h << 16), 1, scale, base, &tail);
+          const unsigned h = e & 1 ? pair >> 16 : pair & 0xffffu, at = (h & 0x7fffu) - kLeastValue;
+          if (at < kValues) atomicAdd(&s.by_value[at + (h >> 15) * kValues], 1u);
+          else {
+            const float x = __uint_as_float(h << 16);
+            const unsigned one = 1;
+            add_to_bins<1>(&x, &one, scale, base, &tail);
+          }
         }
       }
-    });
+      return look(raw, i);
+    }, note);
     __syncthreads();
+    constexpr int kTogether = 4;
 #pragma unroll 1
-    for (unsigned at = threadIdx.x; at < 2 * kValues; at += kThreads) {
-      const unsigned times = s.by_value[at];
-      const unsigned h = at < kValues ? kLeastValue + at : 0x8000u + kLeastValue + at - kValues;
-      if (times) add_to_bins(__uint_as_float(h << 16), times, scale, base, &tail);
+    for (unsigned at0 = threadIdx.x; at0 < 2 * kValues; at0 += kTogether * kThreads) {
+      float x[kTogether];
+      unsigned times[kTogether], any = 0;
+#pragma unroll
+      for (int e = 0; e < kTogether; ++e) {
+        const unsigned at = at0 + e * kThreads;
+        any |= times[e] = at < 2 * kValues ? s.by_value[at] : 0;
+        // (a value without tokens has no bin)
+        x[e] = times[e] ? __uint_as_float((at < kValues ? kLeastValue + at : 0x8000u + kLeastValue + at - kValues) << 16) : -INFINITY;
+      }
+      if (any) add_to_bins<kTogether>(x, times, scale, base, &tail);
     }
   }
 #pragma unroll
@@ -411,7 +479,7 @@ __device__ __noinline__ void serve() {
   if (op == kOpBins) {
     clear_bins<T>();
     __syncthreads();
-    fill_bins<T>(scale, base, [](const Vec<T, kVec>&, int) {});
+    fill_bins<T>(scale, base, [](const Raw<T, kVec>&, int) { return false; }, [](unsigned, int) {});
     cluster_sync();
     join_bins();
   } else {
@@ -425,36 +493,72 @@ __device__ __noinline__ void serve() {
     }
     const float low = s.order.low, high = s.order.high;
     uint64_t any = 0, none = 0;
-    each_vector<T, 4>([&](const Vec<T, kVec>& v, const Raw<T, kVec>&, int i) {
-      unsigned near = 0;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) near |= v.v[e] >= low && v.v[e] <= high ? 1u << e : 0;
-#pragma unroll 1
-      for (; near; near &= near - 1) {
-        const int e = __ffs(static_cast<int>(near)) - 1;
-        float x = v.v[0];
-#pragma unroll
-        for (int q = 1; q < kVec; ++q) x = e == q ? v.v[q] : x;
-        float t;
-        const int j = bin_of(x, scale, &t) - base;
-        if (j < s.order.from || j >= s.order.to) continue;
-        const uint64_t key = token_key(x, i + e);
-        if ((key & s.order.mask) != s.order.value) continue;
-        if (op == kOpGather) {
-          const unsigned at = atomicAdd(&s.list.n, 1u);
-          if (at < kListCap) s.list.key[at] = key;
-        } else if (op == kOpBits) {
-          any |= key;
-          none |= ~key;
-        } else {
-          const unsigned w = weight_in(x, j + base, t, scale, s.middle);
-          const int digit = (1 << kDigitBits) - 1 - static_cast<int>((key >> s.order.shift) & ((1 << kDigitBits) - 1));
-          atomicAdd(&s.count[digit], 1u);
-          atomicAdd(&s.low[digit], w & 0x7fffu);
-          atomicAdd(&s.high[digit], w >> 15);
-        }
+    auto take = [&](float x, int index) {
+      if (!(x >= low && x <= high)) return;
+      float t;
+      const int j = bin_of(x, scale, &t) - base;
+      if (j < s.order.from || j >= s.order.to) return;
+      const uint64_t key = token_key(x, index);
+      if ((key & s.order.mask) != s.order.value) return;
+      if (op == kOpGather) {
+        const unsigned at = atomicAdd(&s.list.n, 1u);
+        if (at < kListCap) s.list.key[at] = key;
+      } else if (op == kOpBits) {
+        any |= key;
+        none |= ~key;
+      } else {
+        const unsigned w = weight_in(x, j + base, t, scale, s.middle);
+        const int digit = kDigits - 1 - static_cast<int>((key >> s.order.shift) & (kDigits - 1));
+        atomicAdd(&s.count[digit], 1u);
+        atomicAdd(&s.low[digit], w & 0x7fffu);
+        atomicAdd(&s.high[digit], w >> 15);
       }
-    });
+    };
+    // 16 bytes with a value of the bins are noted first: most have none, and the rest is for whole warps then
+    unsigned* noted = reinterpret_cast<unsigned*>(s.list.mass);
+    constexpr unsigned kNoted = sizeof(s.list.mass) / sizeof(unsigned);
+    if (threadIdx.x == 0) s.few = 0;
+    __syncthreads();
+    if constexpr (sizeof(T) == 4) {
+      each_vector<T, 8>([&](const Raw<T, kVec>& raw, int) {
+        Vec<T, kVec> v;
+        v.set_raw(raw);
+        bool near = false;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) near |= v.v[e] >= low && v.v[e] <= high;
+        return near;
+      }, [&](unsigned hits, int at) { keep_noted<T>(noted, kNoted, hits, at); });
+    } else {
+      // (rounded down and up: a bf16 value is within the one bounds if it is within the others, but for some more at the ends)
+      const __nv_bfloat162 low2 = __bfloat162bfloat162(__float2bfloat16_rd(low)), high2 = __bfloat162bfloat162(__float2bfloat16_ru(high));
+      each_vector<T, 8>([&](const Raw<T, kVec>& raw, int) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw.u);
+        unsigned near = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) near |= __hge2_mask(h[q], low2) & __hle2_mask(h[q], high2);
+        return near != 0;
+      }, [&](unsigned hits, int at) { keep_noted<T>(noted, kNoted, hits, at); });
+    }
+    __syncthreads();
+    const unsigned found = s.few;
+    __syncthreads();
+    auto take_all = [&](const Raw<T, kVec>& raw, int i) {
+      Vec<T, kVec> v;
+      v.set_raw(raw);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) take(v.v[e], i + e);
+      return false;
+    };
+    if (found <= kNoted) {
+#pragma unroll 1
+      for (unsigned q = threadIdx.x; q < found; q += kThreads) {
+        Raw<T, kVec> raw;
+        raw.u = vector_at<T>(static_cast<int>(noted[q]));
+        take_all(raw, static_cast<int>(noted[q]));
+      }
+    } else {
+      each_vector<T, 1>(take_all, [](unsigned, int) {});
+    }
     if (op == kOpGather) {
       if (rank != 0) hand_over<false>();
     } else if (op == kOpDigits) {
@@ -490,23 +594,24 @@ __device__ __forceinline__ uint64_t mass_of(uint64_t key, const Scale& scale, in
   return j < 0 ? 0 : (static_cast<uint64_t>(weight_in(x, j, t, scale, middle)) << (kOctaves - 1)) >> (j / kSub - kOctaves * window);
 }
 __device__ __forceinline__ int digit_of(uint64_t key, int at) {
-  return (1 << kDigitBits) - 1 - static_cast<int>((key >> at) & ((1 << kDigitBits) - 1));
+  return kDigits - 1 - static_cast<int>((key >> at) & (kDigits - 1));
 }
 // Counts and masses by digit: three limbs of 15 bits each.
 __device__ __forceinline__ void clear_digits() {
   Shared& s = own();
-  s.count[threadIdx.x] = s.low[threadIdx.x] = s.low[kThreads + threadIdx.x] = s.high[threadIdx.x] = 0;
+#pragma unroll
+  for (int d = threadIdx.x; d < kDigits; d += kThreads) s.count[d] = s.low[d] = s.low[kDigits + d] = s.high[d] = 0;
 }
 __device__ __forceinline__ void add_digit(int d, uint64_t m) {
   Shared& s = own();
   atomicAdd(&s.count[d], 1u);
   atomicAdd(&s.low[d], static_cast<unsigned>(m) & 0x7fffu);
-  atomicAdd(&s.low[kThreads + d], static_cast<unsigned>(m >> 15) & 0x7fffu);
+  atomicAdd(&s.low[kDigits + d], static_cast<unsigned>(m >> 15) & 0x7fffu);
   atomicAdd(&s.high[d], static_cast<unsigned>(m >> 30));
 }
 __device__ __forceinline__ uint64_t digit_mass(int d) {
   const Shared& s = own();
-  return s.low[d] + (static_cast<uint64_t>(s.low[kThreads + d]) << 15) + (static_cast<uint64_t>(s.high[d]) << 30);
+  return s.low[d] + (static_cast<uint64_t>(s.low[kDigits + d]) << 15) + (static_cast<uint64_t>(s.high[d]) << 30);
 }
 
 // The masses of a pile's tokens, and their sums by the first digit.
@@ -514,18 +619,16 @@ template <bool HEAD>
 __device__ __forceinline__ void prepare_pile() {
   Shared& s = own();
   auto& p = pile<HEAD>(s);
-  constexpr int kEach = (HEAD ? kHeadCap : kListCap) / kThreads;
   const int lane = threadIdx.x % 32;
-  const unsigned n = min(p.n, static_cast<unsigned>(kEach * kThreads));
+  const unsigned n = min(p.n, static_cast<unsigned>(HEAD ? kHeadCap : kListCap));
   const Scale scale = p.scale;
   const int window = p.window;
   uint64_t any = 0, none = 0;
   clear_digits();
   if (threadIdx.x < 4) s.bits[threadIdx.x] = 0;
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const unsigned i = q * kThreads + threadIdx.x;
-    const uint64_t key = i < n ? p.key[i] : 0, m = mass_of(key, scale, window, s.middle);  // (0: key 0 has the value NaN)
+#pragma unroll 1
+  for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = p.key[i], m = mass_of(key, scale, window, s.middle);
     p.mass[i] = m;
     any |= m ? key : 0;
     none |= m ? ~key : 0;
@@ -538,24 +641,28 @@ __device__ __forceinline__ void prepare_pile() {
   any = (static_cast<uint64_t>(s.bits[1]) << 32) | s.bits[0];
   const uint64_t differ = any & ((static_cast<uint64_t>(s.bits[3]) << 32) | s.bits[2]);
   const int top = 64 - __clzll(static_cast<long long>(differ)), shift = top > kDigitBits ? top - kDigitBits : 0;
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const unsigned i = q * kThreads + threadIdx.x;
+#pragma unroll 1
+  for (unsigned i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t m = p.mass[i];
     if (m) add_digit(digit_of(p.key[i], shift), m);
   }
   __syncthreads();
+  const int d = 2 * threadIdx.x;
+  const uint64_t m0 = digit_mass(d), m1 = digit_mass(d + 1);
+  const unsigned c0 = s.count[d], c1 = s.count[d + 1];
   uint64_t mb, mass;
   unsigned cb, count;
-  scan_before(digit_mass(threadIdx.x), s.count[threadIdx.x], &mb, &cb, &mass, &count);
-  p.mass_before[threadIdx.x] = mb;
-  p.count_before[threadIdx.x] = cb;
+  scan_before(m0 + m1, c0 + c1, &mb, &cb, &mass, &count);
+  p.mass_before[d] = mb;
+  p.mass_before[d + 1] = mb + m0;
+  p.count_before[d] = cb;
+  p.count_before[d + 1] = cb + c0;
   if (threadIdx.x == 0) {
-    p.mass_before[kThreads] = p.total = mass;
-    p.count_before[kThreads] = p.count = count;
+    p.mass_before[kDigits] = p.total = mass;
+    p.count_before[kDigits] = p.count = count;
     p.n = n;
     p.shift = shift;
-    p.above = (any >> shift) & ~uint64_t((1 << kDigitBits) - 1);
+    p.above = (any >> shift) & ~uint64_t(kDigits - 1);
   }
   __syncthreads();
 }
@@ -566,22 +673,22 @@ template <bool HEAD>
 __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
   Shared& s = own();
   auto& p = pile<HEAD>(s);
-  constexpr int kEach = (HEAD ? kHeadCap : kListCap) / kThreads;
-  {
-    const uint64_t m0 = p.mass_before[threadIdx.x], c0 = p.count_before[threadIdx.x];
-    const uint64_t b0 = by_count ? c0 : m0, b1 = by_count ? p.count_before[threadIdx.x + 1] : p.mass_before[threadIdx.x + 1];
+#pragma unroll
+  for (int d = threadIdx.x; d < kDigits; d += kThreads) {
+    const uint64_t m0 = p.mass_before[d], c0 = p.count_before[d];
+    const uint64_t b0 = by_count ? c0 : m0, b1 = by_count ? p.count_before[d + 1] : p.mass_before[d + 1];
     if (b0 <= target && target < b1) {
-      s.found = static_cast<int>(threadIdx.x);
+      s.found = d;
       s.found_before = b0;
       s.found_mass = m0;
     }
-    if (threadIdx.x == 0) s.few = 0;
-    __syncthreads();
   }
+  if (threadIdx.x == 0) s.few = 0;
+  __syncthreads();
   int at = p.shift;
   uint64_t before = s.found_mass;
   target -= s.found_before;
-  uint64_t prefix = p.above | static_cast<uint64_t>((1 << kDigitBits) - 1 - s.found);
+  uint64_t prefix = p.above | static_cast<uint64_t>(kDigits - 1 - s.found);
   unsigned left = p.count_before[s.found + 1] - p.count_before[s.found];
   const unsigned n = p.n;
   __syncthreads();
@@ -590,37 +697,37 @@ __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
     const int next = at > kDigitBits ? at - kDigitBits : 0;
     clear_digits();
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kEach; ++q) {
-      const unsigned i = q * kThreads + threadIdx.x;
-      const uint64_t m = i < n ? p.mass[i] : 0, key = p.key[i];
+#pragma unroll 1
+    for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+      const uint64_t m = p.mass[i], key = p.key[i];
       if (m && key >> at == prefix) add_digit(digit_of(key, next), m);
     }
     __syncthreads();
-    const uint64_t m = digit_mass(threadIdx.x);
-    const unsigned c = s.count[threadIdx.x];
+    const int d = 2 * threadIdx.x;
+    const uint64_t m0 = digit_mass(d), m1 = digit_mass(d + 1);
+    const unsigned c0 = s.count[d], c1 = s.count[d + 1];
     uint64_t mb, ma;
     unsigned cb, ca;
-    scan_before(m, c, &mb, &cb, &ma, &ca);
-    const uint64_t f0 = by_count ? cb : mb, f1 = by_count ? cb + c : mb + m;
-    if (f0 <= target && target < f1) {
-      s.found = static_cast<int>(threadIdx.x);
-      s.found_before = f0;
-      s.found_mass = mb;
+    scan_before(m0 + m1, c0 + c1, &mb, &cb, &ma, &ca);
+    const uint64_t f0 = by_count ? cb : mb, f1 = f0 + (by_count ? c0 : m0), f2 = f1 + (by_count ? c1 : m1);
+    if (f0 <= target && target < f2) {
+      const bool second = f1 <= target;
+      s.found = d + second;
+      s.found_before = second ? f1 : f0;
+      s.found_mass = second ? mb + m0 : mb;
     }
     __syncthreads();
     before += s.found_mass;
     target -= s.found_before;
     left = s.count[s.found];
     // (the digit's bits above `at` are the prefix's own)
-    prefix = prefix << (at - next) | (static_cast<uint64_t>((1 << kDigitBits) - 1 - s.found) & ((uint64_t(1) << (at - next)) - 1));
+    prefix = prefix << (at - next) | (static_cast<uint64_t>(kDigits - 1 - s.found) & ((uint64_t(1) << (at - next)) - 1));
     at = next;
     __syncthreads();
   }
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const unsigned i = q * kThreads + threadIdx.x;
-    const uint64_t m = i < n ? p.mass[i] : 0, key = p.key[i];
+#pragma unroll 1
+  for (unsigned i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t m = p.mass[i], key = p.key[i];
     if (m && key >> at == prefix) {
       const unsigned f = atomicAdd(&s.few, 1u);
       if (f < 32) {
@@ -669,16 +776,23 @@ __device__ __forceinline__ void ask(int op, int w, int from, int to, uint64_t ma
 // Sums before each bin, from the bins' own.
 __device__ __noinline__ void add_up_bins() {
   Shared& s = own();
-  const int b = 2 * threadIdx.x;
-  const uint64_t m0 = s.mass_before[b], m1 = s.mass_before[b + 1];
-  const unsigned c0 = s.count_before[b], c1 = s.count_before[b + 1];
-  uint64_t mb, mass;
-  unsigned cb, count;
-  scan_before(m0 + m1, c0 + c1, &mb, &cb, &mass, &count);
-  s.mass_before[b] = mb;
-  s.mass_before[b + 1] = mb + m0;
-  s.count_before[b] = cb;
-  s.count_before[b + 1] = cb + c0;
+  constexpr int kEach = kBins / kThreads;
+  const int b = kEach * threadIdx.x;
+  uint64_t m[kEach], sum = 0, mb, mass;
+  unsigned c[kEach], number = 0, cb, count;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    sum += m[q] = s.mass_before[b + q];
+    number += c[q] = s.count_before[b + q];
+  }
+  scan_before(sum, number, &mb, &cb, &mass, &count);
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    s.mass_before[b + q] = mb;
+    s.count_before[b + q] = cb;
+    mb += m[q];
+    cb += c[q];
+  }
   if (threadIdx.x == 0) {
     s.mass_before[kBins] = s.mass = mass;
     s.count_before[kBins] = s.counted = count;
@@ -688,7 +802,9 @@ __device__ __noinline__ void add_up_bins() {
 // Takes the bins that the blocks have joined as window w's: they hold sums of 30-bit weights, a mass is that at the octave's place.
 __device__ __noinline__ void take_window(int w) {
   Shared& s = own();
-  for (int b = 2 * threadIdx.x; b < 2 * static_cast<int>(threadIdx.x) + 2; ++b) s.mass_before[b] <<= kOctaves - 1 - b / kSub;
+  constexpr int kEach = kBins / kThreads;  // (the bins that this thread then adds up)
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) s.mass_before[kEach * threadIdx.x + q] <<= kOctaves - 1 - (kEach * threadIdx.x + q) / kSub;
   if (threadIdx.x == 0) {
     uint64_t tail = 0;
     const int blocks = static_cast<int>(cg::this_cluster().num_blocks());
@@ -708,8 +824,7 @@ __device__ __noinline__ void need_window(int w) {
 __device__ __noinline__ int find_bin(bool by_count, uint64_t target) {
   Shared& s = own();
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int b = q * kThreads + threadIdx.x;
+  for (int b = threadIdx.x; b < kBins; b += kThreads) {
     const uint64_t b0 = by_count ? s.count_before[b] : s.mass_before[b], b1 = by_count ? s.count_before[b + 1] : s.mass_before[b + 1];
     if (b0 <= target && target < b1) s.found = b;
   }
@@ -758,7 +873,7 @@ __device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target
         past += s.mass_before[digit];
         target -= by_count ? s.count_before[digit] : s.mass_before[digit];
         // (digits below bit `shift` are still open; the digit's own bits above `top` are the mask's)
-        const uint64_t bits = static_cast<uint64_t>((1 << kDigitBits) - 1 - digit) << shift;
+        const uint64_t bits = static_cast<uint64_t>(kDigits - 1 - digit) << shift;
         value = (value & mask) | (bits & ~mask);
         mask = ~((uint64_t(1) << shift) - 1);
         value &= mask;
@@ -841,39 +956,48 @@ struct Unit {
 
 // The block's part of the row, read once: its maximum, its part of the head, and, where `rest`, its bins.
 template <typename T>
-__device__ __forceinline__ float first_pass(bool rest) {
+__device__ __noinline__ float first_pass(bool rest) {
   constexpr int kVec = 16 / sizeof(T);
   Shared& s = own();
   const Scale scale = s.scale;
   const float tau = scale.most;
   float most = -INFINITY;
-  auto look = [&](const Vec<T, kVec>& v, int i) {
-    float top = v.v[0];
-#pragma unroll
-    for (int e = 1; e < kVec; ++e) top = fmaxf(top, v.v[e]);
+  // 16 bytes with a token of the head are noted, and gone through again afterwards: some hundred among thousands
+  unsigned* noted = reinterpret_cast<unsigned*>(s.head.mass);
+  constexpr unsigned kNoted = sizeof(s.head.mass) / sizeof(unsigned);
+  auto look = [&](const Raw<T, kVec>& raw, int) {
+    const float top = top_of<T>(raw);
     most = fmaxf(most, top);
-    if (top >= tau) {
-      unsigned over = 0;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) over |= v.v[e] >= tau ? 1u << e : 0;
-#pragma unroll 1
-      for (; over; over &= over - 1) {
-        const int e = __ffs(static_cast<int>(over)) - 1;
-        float x = v.v[0];
-#pragma unroll
-        for (int q = 1; q < kVec; ++q) x = e == q ? v.v[q] : x;
-        const unsigned at = atomicAdd(&s.head.n, 1u);
-        if (at < kHeadCap) s.head.key[at] = token_key(x, i + e);
-      }
-    }
+    return top >= tau;
   };
-  if (rest) fill_bins<T>(scale, 0, look);
-  else each_vector<T, 4>([&](const Vec<T, kVec>& v, const Raw<T, kVec>&, int i) { look(v, i); });
+  auto note = [&](unsigned hits, int at) { keep_noted<T>(noted, kNoted, hits, at); };
+  if (rest) fill_bins<T>(scale, 0, look, note);
+  else each_vector<T, 8>(look, note);
+  __syncthreads();
+  const unsigned found = s.few;
+  if (found > kNoted) {
+    if (threadIdx.x == 0) atomicAdd(&s.head.n, kHeadCap + 1u);  // (too many)
+  } else {
+#pragma unroll 1
+    for (unsigned q = threadIdx.x; q < found; q += kThreads) {
+      const int i = static_cast<int>(noted[q]);
+      Raw<T, kVec> raw;
+      raw.u = vector_at<T>(i);
+      Vec<T, kVec> v;
+      v.set_raw(raw);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (v.v[e] >= tau) {
+          const unsigned at = atomicAdd(&s.head.n, 1u);
+          if (at < kHeadCap) s.head.key[at] = token_key(v.v[e], i + e);
+        }
+    }
+  }
   return most;
 }
 
-// `slots`: tokens of a block's part; the threshold is number `order` of the 32 maxima of `runs` times 16 tokens each, `step`
-// apart (runs == 0: none).
+// `slots`: tokens of a block's part; the threshold is number `order` of the 32 maxima of `runs` times kGroup tokens each,
+// `step_` apart (runs == 0: none).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, int slots, int runs, int order, int step_) {
   constexpr int kVec = 16 / sizeof(T);
@@ -886,6 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
   if (threadIdx.x < kSub) s.middle[threadIdx.x] = kMiddles.v[threadIdx.x];
   if (threadIdx.x == 0) {
     s.found = 0;
+    s.few = 0;
     s.head.n = 0;
     s.window = s.list_window = -1;
     const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kVec);
@@ -897,6 +1022,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
   clear_bins<T>();
   grid_dependency_wait();
   grid_launch_dependents();
+  if (threadIdx.x == 32) {
+    s.u = p.u[row];
+    s.top_p = p.top_ps ? p.top_ps[row] : p.top_p;
+    s.least = p.min_ps ? p.min_ps[row] : p.min_p;
+  }
 
   const float temperature = p.temperatures ? p.temperatures[row] : p.temperature;
   const bool greedy = !(temperature > 0.0f);
@@ -907,12 +1037,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
   float tau = -FLT_MAX;
   if (runs > 0) {
     float top = -INFINITY;
-    const int group = threadIdx.x / 16;
-#pragma unroll 4
-    for (int i = 0; i < runs; ++i) top = fmaxf(top, to_f32(x[(i * 32 + group) * step_ + threadIdx.x % 16]));
+    const int group = threadIdx.x / kGroup;
+#pragma unroll 8
+    for (int i = 0; i < runs; ++i) top = fmaxf(top, to_f32(x[(i * 32 + group) * step_ + threadIdx.x % kGroup]));
 #pragma unroll
-    for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    if (threadIdx.x % 16 == 0) s.group_max[group] = __float_as_uint(top);
+    for (int d = kGroup / 2; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (threadIdx.x % kGroup == 0) s.group_max[group] = __float_as_uint(top);
     __syncthreads();
     top = __uint_as_float(s.group_max[lane]);
     int place = 0;
@@ -964,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
   __syncthreads();
   if (threadIdx.x == 0) {
     float least = -FLT_MAX;
-    const float min_p = p.min_ps ? p.min_ps[row] : p.min_p;
+    const float min_p = s.least;
     if (greedy) {
       least = most;
     } else if (min_p > 0.0f) {  // w >= min_p: x >= max + T ln(min_p)
@@ -1009,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
         in_head = static_cast<unsigned>(top_k) <= head_count;
         if (top_k > 0 && top_k < p.n && (in_head || more)) target = static_cast<uint64_t>(top_k - 1) - (in_head ? 0 : head_count);
       } else {
-        const float f = step == 2 ? p.u[row] : p.top_ps ? p.top_ps[row] : p.top_p;
+        const float f = step == 2 ? s.u : s.top_p;
         if (step == 1 && !(f < 1.0f)) continue;
         target = !(f > 0.0f) ? 0 : f < 1.0f ? share_of(f, kept, step == 1) : kept - 1;
         in_head = !more || (listed && target < head_mass);
@@ -1055,41 +1185,66 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
 
 }  // namespace
 
+static cudaLaunchConfig_t config(int blocks, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of that many blocks that the device runs at once (a cluster's blocks lie on neighbouring SMs: 37 of eight blocks, two an
+// SM, took two rounds on 152 SMs).
+template <typename T>
+static int clusters_at_once(int blocks) {
+  static PerDevice known[kMostBlocks + 1];
+  std::atomic<int>* k = known[blocks].here();
+  int n = k ? k->load() : 0;
+  if (n) return n;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(blocks, attr);
+  if (cudaOccupancyMaxActiveClusters(&n, token_kernel<T>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  if (k) *k = n;
+  return n;
+}
+
 template <typename T>
 static cudaError_t launch(const TokenDraw& p, cudaStream_t st) {
   constexpr int64_t kVec = 16 / sizeof(T);
-  // blocks a row: as many as fill the SMs with two each, down to 2048 tokens
-  const int64_t len = p.n + kVec;
+  // blocks a row: as many as let all rows' clusters run at once, down to 2048 tokens each
+  const int64_t len = p.n + kVec, least = (p.n + kPartMost - 1) / kPartMost;
+  cudaError_t e = cudaFuncSetAttribute(token_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+  if (e != cudaSuccess) return e;
   int64_t blocks = 2 * ops_sm_count() / p.rows;
   if (blocks > len / 2048) blocks = len / 2048;
-  const int64_t least = (p.n + kPartMost - 1) / kPartMost;
   blocks = blocks < least ? least : blocks > kMostBlocks ? kMostBlocks : blocks;
+  while (blocks > least && clusters_at_once<T>(static_cast<int>(blocks)) < p.rows) --blocks;
   const int64_t slots = ((len + blocks - 1) / blocks + kVec - 1) / kVec * kVec;
   if (p.rows * blocks > INT32_MAX) return cudaErrorNotSupported;
   // the threshold: of 32 maxima of m tokens each, number i (from 0) has about (1/32 + ... + 1/(32 - i)) n / m tokens above it
   int runs = 0, order = 0;
   if (p.n > kHeadCap) {
-    runs = static_cast<int>((p.n * 69 / 100 / kHead + 15) / 16);
+    runs = static_cast<int>((p.n * 69 / 100 / kHead + kGroup - 1) / kGroup);
     double above = 1.0 / 32;
-    while (order < 31 && above * p.n < 16.0 * runs * kHead) above += 1.0 / (32 - ++order);
+    while (order < 31 && above * p.n < 1.0 * kGroup * runs * kHead) above += 1.0 / (32 - ++order);
   }
-  cudaError_t e = cudaFuncSetAttribute(token_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.rows * blocks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Shared);
-  cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
+  cudaLaunchConfig_t cfg = config(static_cast<int>(blocks), attr);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows * blocks));
+  cfg.stream = st;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, token_kernel<T>, p, static_cast<int>(slots), runs, order,
-                            runs ? (p.n - 16) / (32 * runs) : 0);
+                            runs ? (p.n - kGroup) / (32 * runs) : 0);
 }
 
 cudaError_t launch_tokens(const TokenDraw& p, cudaStream_t st) {
