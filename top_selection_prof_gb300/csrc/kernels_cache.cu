@@ -102,11 +102,11 @@ struct Places {
   }
 };
 
-// A block: 32 pieces of positions of one head, the head's query rows dealt to its warps.
-template <typename T, int VEC>
+// A block: 32 pieces of positions of one head, the head's query rows dealt to its warps, kAhead of them under way.
+template <typename T, int VEC, int kAhead>
 __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSums p) {
   using P = Places<T, VEC>;
-  constexpr int kWide = P::kWide, kAhead = VEC > 1 ? 8 : 4;
+  constexpr int kWide = P::kWide;
   __shared__ float2 part[kSumWarps][32 * kWide];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -119,15 +119,18 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSu
   const T* base = static_cast<const T*>(p.weights.data) + b * p.weights.batch + h * p.group * p.weights.head + at0;
   for (int i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
     P v[kAhead];
+    int g = i0 / queries, q = i0 - g * queries;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * kSumWarps, g = i / queries;
-      v[a].load(base + g * p.weights.head + (i - g * queries) * p.weights.row, lane, i < n ? len - at0 : 0);
+      v[a].load(base + g * p.weights.head + q * p.weights.row, lane, i0 + a * kSumWarps < n ? len - at0 : 0);
+      for (q += kSumWarps; q >= queries; q -= queries) ++g;
     }
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+    for (int a = 0; a < kAhead; ++a) {
+      if (i0 + a * kSumWarps >= n) break;
 #pragma unroll
       for (int e = 0; e < kWide / 2; ++e) sum[e].add(v[a].pair(e));
+    }
   }
 #pragma unroll
   for (int e = 0; e < kWide / 2; ++e) {
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(256) move_kept_kernel(const MoveKept p) {
 // A cluster a head: adds the group's weights to the scores, finds the slot and writes the token there.  A thread holds WIDE slots
 // side by side, whose weights, score and positions are all under way at once; where rows are not on 16-byte boundaries, one.
 template <typename W, int WIDE>
-__global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
+__global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
   __shared__ uint64_t warp_least[kWarps];
   __shared__ uint64_t leasts[kMostBlocks];
   cg::cluster_group cluster = cg::this_cluster();
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
   for (int64_t i = (int64_t(rank) * kThreads + threadIdx.x) * WIDE; i < len; i += int64_t(blocks) * kThreads * WIDE) {
     // (a run's slots behind `len` are read, not written: they lie within the capacity)
     Sum2 sum[WIDE];
-    int64_t at[WIDE];
+    unsigned may = full && p.recent == 0 ? ~0u : 0;  // slots that may go
     if constexpr (WIDE > 1) {
 #pragma unroll
       for (int e = 0; e < WIDE; e += 4) {
@@ -405,10 +408,10 @@ __global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
 #pragma unroll
         for (int e = 0; e < WIDE; e += 2) {
           const longlong2 v = *reinterpret_cast<const longlong2*>(positions + i + e);
-          at[e] = v.x, at[e + 1] = v.y;
+          may |= (v.x < seen - p.recent ? 1u << e : 0) | (v.y < seen - p.recent ? 2u << e : 0);
         }
       } else {
-        at[0] = positions[i];
+        may = positions[i] < seen - p.recent;
       }
     }
     constexpr int kAhead = 4;
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) replace_kernel(const Replace p) {
 #pragma unroll
     for (int e = 0; e < WIDE; ++e) {
       value[e] = sum[e].value();
-      if (full && (p.recent == 0 || at[e] < seen - p.recent))
+      if (may >> e & 1)
         least = min(least, static_cast<uint64_t>(order_key_f32(__float_as_uint(value[e]))) << 32 | static_cast<uint32_t>(i + e));
     }
     if (n) {
@@ -521,7 +524,10 @@ cudaError_t add_weights(const Evict& p, float* out, cudaStream_t st) {
   const int64_t blocks = (p.capacity + each - 1) / each * p.batch * p.heads;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(blocks);
-  return wide ? launch_after(weight_sums_kernel<T, kVec>, grid, kSumThreads, 0, st, w) : launch_after(weight_sums_kernel<T, 1>, grid, kSumThreads, 0, st, w);
+  // (few rows a warp: four at a time and more blocks an SM)
+  if (p.group * p.queries <= 4 * kSumWarps || !wide)
+    return wide ? launch_after(weight_sums_kernel<T, kVec, 4>, grid, kSumThreads, 0, st, w) : launch_after(weight_sums_kernel<T, 1, 4>, grid, kSumThreads, 0, st, w);
+  return launch_after(weight_sums_kernel<T, kVec, 16>, grid, kSumThreads, 0, st, w);
 }
 
 template <typename T>
