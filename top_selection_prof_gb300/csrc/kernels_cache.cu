@@ -202,7 +202,7 @@ __device__ __forceinline__ unsigned scan_before(ChoiceShared& s, unsigned v, uns
   return before + incl - v;
 }
 
-// EACH positions a thread, in a run, whose keys stay in registers; 0: as many as it takes, read anew in each pass.
+// Up to EACH positions a thread, in a run, whose keys stay in registers; 0: as many as it takes, read anew in each pass.
 template <int EACH>
 __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
   __shared__ ChoiceShared s;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
   const int64_t kept = min(len, p.keep), old = len - min(p.recent, len);  // the last ones stay
   const unsigned want = static_cast<unsigned>(len > p.keep ? p.keep - (len - old) : old);  // of the others
   // this thread's run of positions
-  const int64_t each = EACH ? EACH : (len + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
+  const int64_t each = (len + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
   const int64_t begin = min(len, (int64_t(rank) * kThreads + threadIdx.x) * each), end = min(len, begin + each);
   const bool choose = want < old;
   uint32_t keys[EACH ? EACH : 1];
@@ -569,7 +569,7 @@ cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st) {
   const int blocks = blocks_for(rows, p.capacity, 2048);
   // positions a thread: in registers up to 16
   const int64_t each = (p.capacity + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
-  cudaError_t e = launch_clusters(each <= 4 ? choice_kernel<4> : each <= 16 ? choice_kernel<16> : choice_kernel<0>, c, rows, blocks, st);
+  cudaError_t e = launch_clusters(each <= 4 ? choice_kernel<4> : each <= 8 ? choice_kernel<8> : each <= 16 ? choice_kernel<16> : choice_kernel<0>, c, rows, blocks, st);
   if (e != cudaSuccess) return e;
   return p.dtype == kF32 ? move_kept<float>(p, st) : move_kept<__nv_bfloat16>(p, st);
 }

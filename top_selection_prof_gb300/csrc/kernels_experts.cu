@@ -116,22 +116,22 @@ __global__ void __launch_bounds__(kSortThreads) expert_rank_kernel(const int64_t
 }
 
 // ---- moving rows --------------------------------------------------------------------
-// What one of `share` threads holds of a row of d values: 16 bytes side by side where rows allow it, else four values `share`
-// apart, so that as many bytes are under way and a warp's loads are whole lines all the same.
+// What one of `share` threads (whole warps) holds of a row of d values: 16 bytes side by side where rows allow it, else four
+// values 32 apart, so that as many bytes are under way and a warp's loads are whole lines all the same.
 template <typename T, int VEC>
 struct Piece {
   static constexpr int kWide = VEC > 1 ? VEC : 4;
   Raw<T, VEC> r[VEC > 1 ? 1 : kWide];
-  __device__ __forceinline__ static int first(int at) { return at * VEC; }
+  __device__ __forceinline__ static int first(int at) { return VEC > 1 ? at * VEC : at / 32 * (32 * kWide) + at % 32; }
   __device__ __forceinline__ static int step(int share) { return share * kWide; }
-  __device__ __forceinline__ void load(const T* row, int c, int d, int share) {
+  __device__ __forceinline__ void load(const T* row, int c, int d) {
     if constexpr (VEC > 1) {
       r[0].load_nc(row + c);
     } else {
 #pragma unroll
       for (int e = 0; e < kWide; ++e) {
         r[e].clear();
-        if (c + e * share < d) r[e].load_nc(row + c + e * share);
+        if (c + e * 32 < d) r[e].load_nc(row + c + e * 32);
       }
     }
   }
@@ -150,16 +150,16 @@ struct Piece {
       for (int e = 0; e < kWide; ++e) f[e] = to_f32(r[e].u);
     }
   }
-  __device__ __forceinline__ void store(T* row, int c, int d, int share) const {
+  __device__ __forceinline__ void store(T* row, int c, int d) const {
     if constexpr (VEC > 1) {
       __stcs(reinterpret_cast<uint4*>(row + c), r[0].u);
     } else {
 #pragma unroll
       for (int e = 0; e < kWide; ++e)
-        if (c + e * share < d) row[c + e * share] = r[e].u;
+        if (c + e * 32 < d) row[c + e * 32] = r[e].u;
     }
   }
-  __device__ __forceinline__ static void store(const float* f, T* row, int c, int d, int share) {
+  __device__ __forceinline__ static void store(const float* f, T* row, int c, int d) {
     if constexpr (VEC > 1) {
       Vec<T, VEC> v;
 #pragma unroll
@@ -168,7 +168,7 @@ struct Piece {
     } else {
 #pragma unroll
       for (int e = 0; e < kWide; ++e)
-        if (c + e * share < d) row[c + e * share] = from_f32<T>(f[e]);
+        if (c + e * 32 < d) row[c + e * 32] = from_f32<T>(f[e]);
     }
   }
 };
@@ -192,13 +192,13 @@ __device__ __forceinline__ void spread_row(const MoveRows& p, int64_t t, const i
   const T* src = static_cast<const T*>(p.x) + t * p.ldx;
   for (int c = P::first(at); c < d; c += P::step(share)) {
     P v, zero;
-    v.load(src, c, d, share);
+    v.load(src, c, d);
     zero.clear();
     for (int j = 0; j < p.k; ++j) {
       const int r = rows[j];
       T* dst = static_cast<T*>(p.xs) + static_cast<int64_t>(r < 0 ? ~r : r) * p.d;
-      if (r < 0) zero.store(dst, c, d, share);
-      else v.store(dst, c, d, share);
+      if (r < 0) zero.store(dst, c, d);
+      else v.store(dst, c, d);
     }
   }
 }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const JoinRows p, int
         const int64_t r = j0 + j < p.k ? place[j0 + j] : -1;
         f[j] = 0.0f;
         if (r >= 0 && r < p.rows) {
-          v[j].load(ys + r * p.ldy, c, d, share);
+          v[j].load(ys + r * p.ldy, c, d);
           f[j] = p.weights ? to_f32(w[j0 + j]) : 1.0f;
         } else {
           v[j].clear();
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const JoinRows p, int
         for (int e = 0; e < P::kWide; ++e) sum[e] = fmaf(f[j], x[e], sum[e]);
       }
     }
-    P::store(sum, static_cast<T*>(p.y) + t * p.d, c, d, share);
+    P::store(sum, static_cast<T*>(p.y) + t * p.d, c, d);
   }
 }
 
@@ -389,11 +389,11 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
         for (int j = 0; j < kTogether; ++j) times[j] = dys && now.row[j] >= 0 ? p.listed[now.row[j]] : 0;
         for (int c = P::first(at); in && c < d; c += P::step(share)) {
           P raw, v[kTogether];
-          raw.load(dy + t * p.lddy, c, d, share);
+          raw.load(dy + t * p.lddy, c, d);
           if (p.dweights) {
 #pragma unroll
             for (int j = 0; j < kTogether; ++j)
-              if (now.row[j] >= 0) v[j].load(ys + now.row[j] * p.ldy, c, d, share);
+              if (now.row[j] >= 0) v[j].load(ys + now.row[j] * p.ldy, c, d);
           }
           if (j0 == 0 && c == P::first(at)) next.load(p, t + step, 0);
           float g[P::kWide];
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
             if (times[j] == 1) {
 #pragma unroll
               for (int e = 0; e < P::kWide; ++e) x[e] = now.f[j] * g[e];
-              P::store(x, dys + now.row[j] * p.d, c, d, share);
+              P::store(x, dys + now.row[j] * p.d, c, d);
             }
             if (p.dweights) {
               v[j].values(x);
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
   zero.clear();
   for (int q = warp; q < kRowsBlock; q += kThreads / 32)
     if (listed[q] == 0)
-      for (int c = P::first(lane); c < d; c += P::step(32)) zero.store(dys + (r0 + q) * p.d, c, d, 32);
+      for (int c = P::first(lane); c < d; c += P::step(32)) zero.store(dys + (r0 + q) * p.d, c, d);
   const int64_t total = p.tokens * p.k;
   for (int q = 0; q < kRowsBlock; ++q) {
     const unsigned times = listed[q];
