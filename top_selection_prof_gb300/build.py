@@ -1,7 +1,8 @@
 """Builds libtopk_gb300.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library exporting the C ABI of include/topk.h.  Usage:
+library exporting the C ABI of include/topk.h; and the Python module that makes
+language.py's calls of it (_language_calls.so, with torch's headers).  Usage:
     python -m top_selection_prof_gb300.build [--verbose]
 """
 from __future__ import annotations
@@ -20,6 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["topk_api.cu", "kernels_sample.cu", "kernels_filter.cu", "kernels_fallback.cu", "kernels_select.cu",
            "kernels_rows.cu", "params.cpp", "topk_noalloc.cu", "ops_api.cu", "kernels_linear.cu", "kernels_mma.cu", "kernels_places.cu",
            "kernels_norm.cu", "kernels_tokens.cu", "kernels_experts.cu", "kernels_cache.cu"]
+CALLS = os.path.join(HERE, "_language_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,16 +46,48 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _run(cmd, what):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s:\n%s\n%s" % (what, " ".join(cmd), res.stderr))
+
+
+def _compile_calls() -> str:
+    """The object of the Python module: host code with the headers of this machine's Python and torch."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "language_calls.o")
+    _run([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-w", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+          "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", cuda, "-c", os.path.join(CSRC, "language_calls.cpp"), "-o", obj], "g++ failed for language_calls.cpp")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS + ".tmp"
+    _run([shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + os.path.basename(LIB), "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          "-Wl,-rpath,$ORIGIN"], "link failed for the Python module")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        calls = calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", *ARCH, "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
     os.replace(tmp, LIB)
+    _link_calls(calls)
     return LIB
 
 
