@@ -43,8 +43,8 @@ constexpr int kWindows = 3;                  // weights below 2^-48 of the large
 constexpr float kDeepest = kOctaves * kWindows;
 constexpr int kHeadCap = 2560;               // tokens that the first block searches itself, of the head
 constexpr int kListCap = 1536;               // and of bins
-constexpr int kHead = 1024;                  // tokens that the head should have
-constexpr int kHeadOnly = 256;               // a top_k up to this is searched in the head alone
+constexpr int kHead = 1024;                  // tokens that the head should have; for one top_k of all rows up to a quarter of
+constexpr int kLeastHead = 128;              // that, four times the top_k
 constexpr int kIndexBits = 18;
 constexpr int kTailBits = 14;                // bits below a mass's unit that the sum behind the histogram keeps
 constexpr int64_t kPartMost = 131072;         // tokens of a block's part
@@ -126,11 +126,13 @@ enum : int { kOpDone, kOpBins, kOpBits, kOpDigits, kOpGather };
 struct Order {
   Scale scale;
   int op, window;
-  int from, to;           // bins [from, to) of the window
+  int from, to;           // bins [from, to) of the window,
+  int from2, to2;         // and [from2, to2) behind them (gathered only)
   uint64_t mask, value;   // keys with key & mask == value
   int shift;              // digits: (key >> shift) of kDigitBits
-  float low, high;        // no value of the bins lies outside
   int unused;
+  float low, high;        // no value of the first bins lies outside,
+  float low2, high2;      // and none of the others outside these
 };
 
 // Tokens in no order with their masses, and the sums of those before each first digit of their keys that differs.
@@ -174,17 +176,19 @@ struct Shared {
   uint64_t mass, behind;                 // of the window; behind it (kTailBits more)
   unsigned counted;
   union {
-    PileShared<kListCap> list;                   // bins [list_from, list_to) of list_window
+    PileShared<kListCap> list;           // bins [list_from, list_to) and, behind them, [list_from2, list_to2) of list_window
     unsigned by_value[2 * kValues];      // bf16: tokens of each value, while bins are filled
   };
-  int list_window, list_from, list_to;
+  int list_window, list_from, list_to, list_from2, list_to2;
   // a crossing: the token where a sum passes a border, and the mass up to and with it
   int found;
   uint64_t found_key, found_before, found_mass;
   unsigned few, bits[4];
+  int bins[2];
   uint64_t few_key[32], few_mass[32];
   float least;
   float top_p, u;
+  int listed;                            // whether the head is (else all is the tail)
 };
 // The block's own.  (Not handed down as a reference: the compiler has to see that it is shared memory.)
 __device__ __forceinline__ Shared& own() {
@@ -392,14 +396,15 @@ __device__ __forceinline__ void fill_bins(const Scale& scale, int base, F look, 
       return look(raw, i);
     }, note);
     __syncthreads();
-    constexpr int kTogether = 4;
+    // (a warp takes 128 neighbouring values at a time: most such runs have tokens throughout, or none)
+    constexpr unsigned kTogether = 4;
 #pragma unroll 1
-    for (unsigned at0 = threadIdx.x; at0 < 2 * kValues; at0 += kTogether * kThreads) {
+    for (unsigned at0 = threadIdx.x / 32 * (32 * kTogether) + threadIdx.x % 32; at0 < 2 * kValues; at0 += kTogether * kThreads) {
       float x[kTogether];
       unsigned times[kTogether], any = 0;
 #pragma unroll
-      for (int e = 0; e < kTogether; ++e) {
-        const unsigned at = at0 + e * kThreads;
+      for (unsigned e = 0; e < kTogether; ++e) {
+        const unsigned at = at0 + e * 32;
         any |= times[e] = at < 2 * kValues ? s.by_value[at] : 0;
         // (a value without tokens has no bin)
         x[e] = times[e] ? __uint_as_float((at < kValues ? kLeastValue + at : 0x8000u + kLeastValue + at - kValues) << 16) : -INFINITY;
@@ -491,13 +496,13 @@ __device__ __noinline__ void serve() {
       clear_bins<T>();
       __syncthreads();
     }
-    const float low = s.order.low, high = s.order.high;
+    const float low = s.order.low, high = s.order.high, other_low = s.order.low2, other_high = s.order.high2;
     uint64_t any = 0, none = 0;
     auto take = [&](float x, int index) {
-      if (!(x >= low && x <= high)) return;
+      if (!(x >= low && x <= high) && !(x >= other_low && x <= other_high)) return;
       float t;
       const int j = bin_of(x, scale, &t) - base;
-      if (j < s.order.from || j >= s.order.to) return;
+      if ((j < s.order.from || j >= s.order.to) && (j < s.order.from2 || j >= s.order.to2)) return;
       const uint64_t key = token_key(x, index);
       if ((key & s.order.mask) != s.order.value) return;
       if (op == kOpGather) {
@@ -525,17 +530,19 @@ __device__ __noinline__ void serve() {
         v.set_raw(raw);
         bool near = false;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) near |= v.v[e] >= low && v.v[e] <= high;
+        for (int e = 0; e < kVec; ++e) near |= (v.v[e] >= low && v.v[e] <= high) || (v.v[e] >= other_low && v.v[e] <= other_high);
         return near;
       }, [&](unsigned hits, int at) { keep_noted<T>(noted, kNoted, hits, at); });
     } else {
       // (rounded down and up: a bf16 value is within the one bounds if it is within the others, but for some more at the ends)
       const __nv_bfloat162 low2 = __bfloat162bfloat162(__float2bfloat16_rd(low)), high2 = __bfloat162bfloat162(__float2bfloat16_ru(high));
+      const __nv_bfloat162 other_low2 = __bfloat162bfloat162(__float2bfloat16_rd(other_low)), other_high2 = __bfloat162bfloat162(__float2bfloat16_ru(other_high));
       each_vector<T, 8>([&](const Raw<T, kVec>& raw, int) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw.u);
         unsigned near = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) near |= __hge2_mask(h[q], low2) & __hle2_mask(h[q], high2);
+        for (int q = 0; q < 4; ++q)
+          near |= (__hge2_mask(h[q], low2) & __hle2_mask(h[q], high2)) | (__hge2_mask(h[q], other_low2) & __hle2_mask(h[q], other_high2));
         return near != 0;
       }, [&](unsigned hits, int at) { keep_noted<T>(noted, kNoted, hits, at); });
     }
@@ -756,19 +763,48 @@ __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
   __syncthreads();
 }
 
+// a b / 2^shift, rounded down, for results below 2^64.
+__device__ __forceinline__ uint64_t scaled(uint64_t a, uint64_t b, int shift) {
+  const uint64_t low = a * b, high = __umul64hi(a, b);
+  if (shift <= 0) return low << -shift;
+  if (shift < 64) return low >> shift | high << (64 - shift);
+  return shift < 128 ? high >> (shift - 64) : 0;
+}
+// f a for f in (0, 1), rounded down; below: the largest whole number that is less.
+__device__ __forceinline__ uint64_t share_of(float f, uint64_t a, bool below) {
+  const unsigned bits = __float_as_uint(f), e = bits >> 23;
+  const unsigned m = e ? (bits & 0x7fffffu) | 0x800000u : bits;
+  const int shift = e ? 150 - static_cast<int>(e) : 149;
+  if (!below) return scaled(a, m, shift);
+  // (a m - 1) / 2^shift
+  const uint64_t low = a * m, high = __umul64hi(a, m) - (low == 0), less = low - 1;
+  if (shift < 64) return less >> shift | high << (64 - shift);
+  return shift < 128 ? high >> (shift - 64) : 0;
+}
+// The tail's masses in the head's unit: times weight / 2^(30 + depth), rounded down.
+struct Unit {
+  unsigned weight, inverse;  // (2^54 / weight, rounded down)
+  int depth;
+  __device__ __forceinline__ uint64_t in_head(uint64_t m) const { return scaled(m, weight, 30 + depth); }
+  __device__ __forceinline__ uint64_t in_tail(uint64_t m) const {
+    const uint64_t a = scaled(m, inverse, 24 - depth), left = m - min(m, in_head(a));
+    return a + scaled(left, inverse, 24 - depth);
+  }
+};
+
 template <typename T>
-__device__ __forceinline__ void ask(int op, int w, int from, int to, uint64_t mask, uint64_t value, int shift) {
+__device__ __forceinline__ void ask(int op, int w, int from, int to, uint64_t mask, uint64_t value, int shift, int from2 = 0, int to2 = 0) {
   Shared& s = own();
   if (threadIdx.x == 0) {
-    // bins [from, to) hold no value outside low ... high (a hundredth of a bin is left at either end, and the differences' rounding)
+    // a hundredth of a bin is left at either end, and room for the differences' rounding
     const Scale scale = s.tail_scale;
-    const float deep = (static_cast<float>(w * kBins + to) + 0.01f) / kSub / scale.hi;
-    const float high = (static_cast<float>(w * kBins + from) - 0.01f) / kSub / scale.hi;
-    const float d = fabsf(scale.most) * 0x1p-20f;
+    const float d = fabsf(scale.most) * 0x1p-20f, bin = 1.0f / kSub / scale.hi;
     const bool sure = fabsf(scale.most) < FLT_MAX;
+    auto lowest = [&](int t) { return sure ? scale.most - (static_cast<float>(w * kBins + t) + 0.01f) * bin - d : -FLT_MAX; };
+    auto highest = [&](int f) { return sure && f > 0 ? scale.most - (static_cast<float>(w * kBins + f) - 0.01f) * bin + d : INFINITY; };
     if (op == kOpBins) s.list_window = -1;
-    s.order = Order{scale, op, w, from, to, mask, value, shift, sure ? scale.most - deep - d : -FLT_MAX,
-                    sure && from > 0 ? scale.most - high + d : INFINITY, 0};
+    s.order = Order{scale, op, w, from, to, from2, to2, mask, value, shift, 0, lowest(to), highest(from),
+                    from2 < to2 ? lowest(to2) : INFINITY, from2 < to2 ? highest(from2) : -INFINITY};
   }
   tell();
   serve<T>();
@@ -820,35 +856,51 @@ __device__ __noinline__ void need_window(int w) {
   ask<T>(kOpBins, w, 0, kBins, 0, 0, 0);
   take_window(w);
 }
-// The bin (or digit) where the sums before pass the target.
-__device__ __noinline__ int find_bin(bool by_count, uint64_t target) {
+// The bins (or digits) where the sums before pass N targets.
+template <int N>
+__device__ __noinline__ void find_bins(bool by_count, const uint64_t (&target)[N], int (&bin)[N]) {
   Shared& s = own();
 #pragma unroll
   for (int b = threadIdx.x; b < kBins; b += kThreads) {
     const uint64_t b0 = by_count ? s.count_before[b] : s.mass_before[b], b1 = by_count ? s.count_before[b + 1] : s.mass_before[b + 1];
-    if (b0 <= target && target < b1) s.found = b;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (b0 <= target[q] && target[q] < b1) s.bins[q] = b;
   }
   __syncthreads();
-  const int b = s.found;
+#pragma unroll
+  for (int q = 0; q < N; ++q) bin[q] = s.bins[q];
   __syncthreads();
-  return b;
+}
+__device__ __forceinline__ int find_bin(bool by_count, uint64_t target) {
+  const uint64_t t[1] = {target};
+  int b[1];
+  find_bins<1>(by_count, t, b);
+  return b[0];
 }
 
-// The token of bin b of the window where the sum passes `target`, as search_pile; masses in the window's unit.
+// The token of bin b of the window where the sum passes `target`, as search_pile; masses in the window's unit.  Bins [also,
+// also_to) before b are listed with it where there is room: the next search's.
 template <typename T>
-__device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target) {
+__device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target, int also, int also_to) {
   Shared& s = own();
   const int w = s.window, up = kOctaves - 1 - b / kSub;
   uint64_t start;                        // mass before the list
   if (s.list_window == w && b >= s.list_from && b < s.list_to) {
     start = s.mass_before[s.list_from];
     target -= by_count ? s.count_before[s.list_from] : start;
+  } else if (s.list_window == w && b >= s.list_from2 && b < s.list_to2) {
+    const int f = s.list_from, t = s.list_to, f2 = s.list_from2;
+    start = s.mass_before[f2] - (s.mass_before[t] - s.mass_before[f]);
+    target -= by_count ? s.count_before[f2] - (s.count_before[t] - s.count_before[f]) : start;
   } else {
     const int from = s.count_before[b + 1] <= kListCap ? 0 : b;
     unsigned held = s.count_before[b + 1] - s.count_before[from];
     uint64_t mask = 0, value = 0;
     start = s.mass_before[from];
-    target -= by_count ? s.count_before[from] : start;
+    if (from == 0 || s.count_before[also_to] - s.count_before[also] + held > kListCap) also = also_to = 0;
+    if (also < also_to) start -= s.mass_before[also_to] - s.mass_before[also];
+    target -= by_count ? s.count_before[from] - (s.count_before[also_to] - s.count_before[also]) : start;
     if (held > kListCap) {
       // narrowed by digits over the cluster: the window's sums are made anew afterwards
       ask<T>(kOpBits, w, b, b + 1, 0, 0, 0);
@@ -884,11 +936,14 @@ __device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target
       if (!by_count) target <<= up;
       if (threadIdx.x == 0) s.window = -1;
     }
-    ask<T>(kOpGather, w, from, b + 1, mask, value, 0);
+    if (also < also_to) ask<T>(kOpGather, w, also, also_to, mask, value, 0, from, b + 1);
+    else ask<T>(kOpGather, w, from, b + 1, mask, value, 0);
     if (threadIdx.x == 0) {
       s.list_window = mask ? -1 : w;
-      s.list_from = from;
-      s.list_to = b + 1;
+      s.list_from = also < also_to ? also : from;
+      s.list_to = also < also_to ? also_to : b + 1;
+      s.list_from2 = also < also_to ? from : 0;
+      s.list_to2 = also < also_to ? b + 1 : 0;
       s.list.scale = s.tail_scale;
       s.list.window = w;
     }
@@ -899,9 +954,10 @@ __device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target
   if (threadIdx.x == 0) s.found_mass += start;
 }
 
-// The token where the sum over the tail passes `target`; masses in the unit of window 0.  False where it does not.
+// The token where the sum over the tail passes `target`; masses in the unit of window 0.  False where it does not.  `ahead`: what
+// is kept ends here, and the token is searched next, whose bin is known but for one or two: they are listed too.
 template <typename T>
-__device__ __forceinline__ bool search_tail(bool by_count, uint64_t target) {
+__device__ __forceinline__ bool search_tail(bool by_count, uint64_t target, bool ahead, const Unit& unit) {
   Shared& s = own();
   uint64_t done = 0;  // mass of the windows before
 #pragma unroll 1
@@ -912,7 +968,22 @@ __device__ __forceinline__ bool search_tail(bool by_count, uint64_t target) {
     const bool last = s.behind == 0;
     if (t >= all && last && !by_count && all) t = all - 1;  // (sums of different units, rounded: the last token)
     if (t < all) {
-      search_bin<T>(find_bin(by_count, t), by_count, t);
+      const int b = find_bin(by_count, t);
+      int also = 0, also_to = 0;
+      if (ahead && w == 0) {
+        // u of what is kept, that being between the masses before and behind the bin
+        const uint64_t head = s.listed ? s.head.total : 0;
+        const float u = s.u > 0.0f ? fminf(s.u, 0x1.fffffep-1f) : 0.0f;
+        const uint64_t low = share_of(u, head + unit.in_head(s.mass_before[b]), false), high = share_of(u, head + unit.in_head(s.mass_before[b + 1]), false);
+        if (low >= head) {
+          const uint64_t ends[2] = {unit.in_tail(low - head), unit.in_tail(high - head)};
+          int bins[2];
+          find_bins<2>(false, ends, bins);
+          also = min(bins[0], b);
+          also_to = min(bins[1] + 1, b);
+        }
+      }
+      search_bin<T>(b, by_count, t, also, also_to);
       if (threadIdx.x == 0) s.found_mass = done + (s.found_mass >> (kOctaves * w));
       __syncthreads();
       return true;
@@ -924,35 +995,6 @@ __device__ __forceinline__ bool search_tail(bool by_count, uint64_t target) {
   }
   return false;
 }
-
-// a b / 2^shift, rounded down, for results below 2^64.
-__device__ __forceinline__ uint64_t scaled(uint64_t a, uint64_t b, int shift) {
-  const uint64_t low = a * b, high = __umul64hi(a, b);
-  if (shift <= 0) return low << -shift;
-  if (shift < 64) return low >> shift | high << (64 - shift);
-  return shift < 128 ? high >> (shift - 64) : 0;
-}
-// f a for f in (0, 1), rounded down; below: the largest whole number that is less.
-__device__ __forceinline__ uint64_t share_of(float f, uint64_t a, bool below) {
-  const unsigned bits = __float_as_uint(f), e = bits >> 23;
-  const unsigned m = e ? (bits & 0x7fffffu) | 0x800000u : bits;
-  const int shift = e ? 150 - static_cast<int>(e) : 149;
-  if (!below) return scaled(a, m, shift);
-  // (a m - 1) / 2^shift
-  const uint64_t low = a * m, high = __umul64hi(a, m) - (low == 0), less = low - 1;
-  if (shift < 64) return less >> shift | high << (64 - shift);
-  return shift < 128 ? high >> (shift - 64) : 0;
-}
-// The tail's masses in the head's unit: times weight / 2^(30 + depth), rounded down.
-struct Unit {
-  unsigned weight, inverse;  // (2^54 / weight, rounded down)
-  int depth;
-  __device__ __forceinline__ uint64_t in_head(uint64_t m) const { return scaled(m, weight, 30 + depth); }
-  __device__ __forceinline__ uint64_t in_tail(uint64_t m) const {
-    const uint64_t a = scaled(m, inverse, 24 - depth), left = m - min(m, in_head(a));
-    return a + scaled(left, inverse, 24 - depth);
-  }
-};
 
 // The block's part of the row, read once: its maximum, its part of the head, and, where `rest`, its bins.
 template <typename T>
@@ -972,7 +1014,7 @@ __device__ __noinline__ float first_pass(bool rest) {
   };
   auto note = [&](unsigned hits, int at) { keep_noted<T>(noted, kNoted, hits, at); };
   if (rest) fill_bins<T>(scale, 0, look, note);
-  else each_vector<T, 8>(look, note);
+  else each_vector<T, 12>(look, note);
   __syncthreads();
   const unsigned found = s.few;
   if (found > kNoted) {
@@ -996,10 +1038,10 @@ __device__ __noinline__ float first_pass(bool rest) {
   return most;
 }
 
-// `slots`: tokens of a block's part; the threshold is number `order` of the 32 maxima of `runs` times kGroup tokens each,
+// `slots`: tokens of a block's part; `head`: those that the head should have; the threshold is number `order` of the 32 maxima of `runs` times kGroup tokens each,
 // `step_` apart (runs == 0: none).
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, int slots, int runs, int order, int step_) {
+__global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, int slots, int head, int runs, int order, int step_) {
   constexpr int kVec = 16 / sizeof(T);
   Shared& s = own();
   cg::cluster_group cluster = cg::this_cluster();
@@ -1019,7 +1061,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
     s.end = min((rank + 1) * slots - lead, p.n);
     s.n = p.n;
   }
-  clear_bins<T>();
   grid_dependency_wait();
   grid_launch_dependents();
   if (threadIdx.x == 32) {
@@ -1031,7 +1072,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
   const float temperature = p.temperatures ? p.temperatures[row] : p.temperature;
   const bool greedy = !(temperature > 0.0f);
   const int top_k = greedy ? 1 : p.top_ks ? p.top_ks[row] : p.top_k;
-  const bool rest = !(top_k > 0 && top_k <= kHeadOnly);  // (the tail will hardly matter otherwise)
+  const bool rest = !(top_k > 0 && top_k <= head / 4);  // (the tail will hardly matter otherwise)
+
+  if (rest) clear_bins<T>();
 
   // the threshold: the same in all blocks of the cluster
   float tau = -FLT_MAX;
@@ -1089,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
 
   most = s.maxes[0];
   for (int b = 1; b < blocks; ++b) most = fmaxf(most, s.maxes[b]);
-  const bool listed = s.head.n <= kHeadCap;  // (else all is the tail)
+  const bool listed = s.head.n <= kHeadCap;
   const Scale scale = s.scale;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -1103,6 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
       least = fminf(fmaxf(f, -FLT_MAX), most);
     }
     s.least = least;
+    s.listed = listed;
     s.tail_scale = listed ? Scale{tau, least, tau, scale.hi, scale.lo} : Scale{most, least, NAN, scale.hi, scale.lo};
     s.head.scale = Scale{most, least, NAN, scale.hi, scale.lo};
     s.head.window = 0;
@@ -1147,7 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
       }
       found = false;
       if (target != ~uint64_t(0)) {
-        if (!in_head) found = search_tail<T>(step == 0, target);
+        if (!in_head) found = search_tail<T>(step == 0, target, step == 1, unit);
         if (!found && (in_head || (step && listed))) {
           search_pile<true>(step == 0, in_head ? target : head_mass - 1);
           in_head = found = true;
@@ -1231,10 +1275,12 @@ static cudaError_t launch(const TokenDraw& p, cudaStream_t st) {
   if (p.rows * blocks > INT32_MAX) return cudaErrorNotSupported;
   // the threshold: of 32 maxima of m tokens each, number i (from 0) has about (1/32 + ... + 1/(32 - i)) n / m tokens above it
   int runs = 0, order = 0;
+  int head = kHead;
+  if (!p.top_ks && p.top_k > 0 && p.top_k < kHead / 4) head = 4 * p.top_k > kLeastHead ? 4 * p.top_k : kLeastHead;
   if (p.n > kHeadCap) {
-    runs = static_cast<int>((p.n * 69 / 100 / kHead + kGroup - 1) / kGroup);
+    runs = static_cast<int>((static_cast<int64_t>(p.n) * 69 / 100 / head + kGroup - 1) / kGroup);
     double above = 1.0 / 32;
-    while (order < 31 && above * p.n < 1.0 * kGroup * runs * kHead) above += 1.0 / (32 - ++order);
+    while (order < 31 && above * p.n < 1.0 * kGroup * runs * head) above += 1.0 / (32 - ++order);
   }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config(static_cast<int>(blocks), attr);
@@ -1243,7 +1289,7 @@ static cudaError_t launch(const TokenDraw& p, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_kernel<T>, p, static_cast<int>(slots), runs, order,
+  return cudaLaunchKernelEx(&cfg, token_kernel<T>, p, static_cast<int>(slots), head, runs, order,
                             runs ? (p.n - kGroup) / (32 * runs) : 0);
 }
 
