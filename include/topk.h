@@ -466,9 +466,9 @@ int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_
  * logarithm of its share of that.  A temperature of 0 takes the largest logit.
  * NaN and -inf are never drawn; a row of nothing else gives -1 and -inf.
  * Where a logit is +inf, only such are drawn.
- *   Sums are formed as in at least 32 bits more than their largest term's
- * rounding to f32 would leave: the token is that of 64-bit arithmetic, but
- * where u[r] is within about 2^-30 of a border; weights below 2^-48 count as 0.
+ *   Weights are formed to 30 bits and their sums are exact, so the token is that
+ * of 64-bit arithmetic unless u[r] (or a filter's border) is within about 2^-29
+ * of the edge between two; weights below 2^-48 of the largest count as 0.
  *   Each of temperature, top_k, top_p and min_p is a number, or one a row
  * (device, `rows` values) where its pointer is not null, the number then
  * being ignored; numbers are rounded to f32.  A row's temperature that is not
@@ -491,8 +491,8 @@ int topk_sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t
  * range (-1 where a token was dropped) has place -1; the rows of xs that are
  * left over, at its end, are zeros.
  *   The gradient of x is topk_combine of xs's, without weights.
- *   Limits: experts <= 4096, tokens k < 2^29 (EUNSUPPORTED beyond; below, rows
- * < 2^29 too).
+ *   Limits: experts <= 4096, tokens k < 2^29, d <= 2^30 (EUNSUPPORTED beyond; for
+ * the way back, rows < 2^29 too).
  */
 int topk_dispatch(const void* x, int64_t ldx, const int64_t* idx, int dtype, int64_t tokens, int64_t k, int64_t experts,
                   int64_t d, void* xs, int64_t* place, int64_t* offsets, void* stream);

@@ -224,6 +224,36 @@ def test_shares_are_the_distributions(tk):
     assert float((count - share).abs().max()) <= 1.0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n", [(310, 131072), (310, 131073), (160, 262144)])
+def test_equal_tokens_in_the_largest_parts(tk, rows, n, dtype):
+    """As many equal weights as a block adds up: token floor(u n), with sums that would pass 32 bits if a half were larger."""
+    u = ((torch.arange(rows) + 0.5) / rows).cuda()
+    x = torch.full((rows, n), -1.25, dtype=dtype, device="cuda")
+    tokens, logprobs = tk.sample(x, u)
+    assert torch.equal(tokens, (u.double() * n).long())
+    assert float((logprobs.double() + math.log(n)).abs().max()) <= 2.0 ** -23 * math.log(n) + 2.0 ** -28
+    x[:, 7] = 0.0
+    tokens, _ = tk.sample(x, u, top_k=n - 1)
+    order = torch.cat([torch.tensor([7]), torch.arange(7), torch.arange(8, n)]).cuda()
+    w = torch.full((n - 1,), math.exp(-1.25), dtype=torch.float64, device="cuda")
+    w[0] = 1.0
+    cum = w.cumsum(0) / w.sum()
+    at = torch.searchsorted(cum, u.double(), right=True)
+    near = (cum[(at - 1).clamp(min=0)] - u.double()).abs().minimum((cum[at] - u.double()).abs()) < EDGE
+    assert bool(((tokens == order[at]) | near).all())
+
+
+def test_the_same_call_gives_the_same_tokens(tk):
+    for dtype in (torch.bfloat16, torch.float32):
+        x, u = logits(60, 70_003, dtype, 21)
+        for kw in (dict(top_p=0.9), dict(temperature=4.0), dict(top_k=5000, top_p=0.95, min_p=1e-4)):
+            first = tk.sample(x, u, **kw)
+            for _ in range(5):
+                again = tk.sample(x, u, **kw)
+                assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_capture_streams_and_no_rows(tk):
     x, u = logits(7, 50_021, torch.float32, 12)
     y, v = logits(7, 50_021, torch.float32, 13)

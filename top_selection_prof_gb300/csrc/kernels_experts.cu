@@ -6,6 +6,13 @@
 // result has one place, and those rows are zeros.  All of it is bound by the
 // rows moved: tokens are walked in order, each row of x (or of y, dy) is read or
 // written once, and the rows by expert once.
+//
+// One GB300, inputs changing between calls: dispatch of 8192 x 8 rows of 2048
+// bf16 (302 MB) 52 us, 5.8 TB/s: the rows 44 us, counts and ranks before them
+// the rest; combine of them 51 us, 5.9 TB/s; their gradients (604 MB less the
+// rows read twice) 120 us; the gradients of 4093 x 6 rows of 1001 f32, none on a
+// 16-byte boundary, 52 us (a 213 MB case whose scalar loads and stores bound it).
+// 16 x 4 rows of 4096 bf16 are dispatched in 4.2 us by one launch.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -380,6 +387,9 @@ __global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* p
   if (r >= 0 && r < rows) atomicAdd(&listed[r], 1u);
 }
 
+// Four rows of a token together: with eight, 128 registers left 16 warps an SM (136 us instead of 120 for 8192 x 8 rows of 2048
+// bf16, 59 instead of 52 for the odd f32 ones); with two, 133 and 52.
+//
 // Blocks of tokens, `share` threads each (32 or more): what a place's row gets where no other place lists it, and the products
 // that are the weights' gradients.  Behind them blocks of rows: zeros for rows that no place lists, and the sums, in order
 // of place, for rows that more than one does (found anew among all places: permutations have none).
@@ -582,7 +592,8 @@ cudaError_t backward(const Combine& p, Scratch& sc, cudaStream_t st) {
   cudaError_t fits = blocks_at_once(combine_backward_kernel<T, VEC>, known, &token_blocks);
   if (fits != cudaSuccess) return fits;
   int64_t row_blocks = 0;
-  if (p.dys) {
+  if (p.rows == 0) q.dys = nullptr;
+  if (q.dys) {
     q.listed = sc.take<unsigned>(p.rows);
     row_blocks = (p.rows + kRowsBlock - 1) / kRowsBlock;
     cudaError_t e = launch_after(clear_listed_kernel, static_cast<unsigned>((p.rows + kThreads - 1) / kThreads), kThreads, 0, st, q.listed, p.rows);

@@ -332,7 +332,7 @@ int sample(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t n, c
 // Whether rows of experts are described soundly; TOPK_OK or the error.
 int check_rows(int dtype, int64_t tokens, int64_t k, int64_t d, int64_t rows) {
   if (!known_dtype(dtype) || tokens < 0 || k < 1 || d < 1 || rows < 0) return TOPK_EINVAL;
-  if (tokens > kMaxExtent || k > kMaxExtent || d > kMaxExtent || rows >= (int64_t(1) << 29)) return TOPK_EUNSUPPORTED;
+  if (tokens > kMaxExtent || k > kMaxExtent || d > (1 << 30) || rows >= (int64_t(1) << 29)) return TOPK_EUNSUPPORTED;
   return tokens * k >= (int64_t(1) << 29) ? TOPK_EUNSUPPORTED : TOPK_OK;
 }
 

@@ -44,6 +44,8 @@ def _call(name, stream, *args):
     if stream is None:
         out = fn(*args)
     else:
+        if isinstance(args[0], torch.Tensor) and args[0].is_cuda and args[0].device != stream.device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, args[0].device))
         with torch.cuda.stream(stream):
             out = fn(*args)
         if type(out) is not int:
