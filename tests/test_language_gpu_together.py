@@ -4,9 +4,9 @@ the cache cut down at the end."""
 import pytest
 import torch
 
-from .test_gpu_cache import evict64, replace64
-from .test_gpu_experts import combine64, sort64
-from .test_gpu_tokens import check, f32
+from .test_language_gpu_cache import evict64, replace64
+from .test_language_gpu_experts import combine64, sort64
+from .test_language_gpu_tokens import check, f32
 
 pytestmark = pytest.mark.gpu
 
