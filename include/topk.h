@@ -541,8 +541,8 @@ typedef struct {
  * order of their positions (batch x heads x keep rows); out_score their score;
  * out_kept their positions; out_lengths[b] = min(lengths[b], keep).  Behind
  * that, rows and scores are zeros and positions -1.
- *   Limits: batch heads capacity and batch heads keep <= 2^40, dims <= 2^20
- * (EUNSUPPORTED beyond).  EINVAL: keep < 1, recent outside [0, keep].
+ *   Limits: batch heads capacity and batch heads keep <= 2^40, dims <= 2^20,
+ * group queries <= 2^30 (EUNSUPPORTED beyond).  EINVAL: keep < 1, recent outside [0, keep].
  */
 int topk_evict(const topk_view_t* keys, const topk_view_t* values, const topk_view_t* score, const int64_t* lengths,
                const topk_view_t* weights, int weights_dtype, int64_t group, int64_t queries, int dtype, int64_t batch,

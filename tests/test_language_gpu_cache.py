@@ -243,6 +243,20 @@ def test_replace_in_one_buffer(tk):
     check_replace(tk, s, 8, on)
 
 
+@pytest.mark.parametrize("dim", [0, 1, 2, 3, 4])
+def test_keys_and_values_stacked(tk, dim):
+    s = step(3, 4, 2, 64, 32, 32, torch.bfloat16, 9)
+    on = cuda(s)
+    on["keys"], on["values"] = torch.stack([on["keys"], on["values"]], dim).unbind(dim) if dim < 4 else (
+        torch.cat([on["keys"], on["values"]], -1).split(32, -1))
+    check_replace(tk, s, 8, on)
+    state, _ = replace64(s, 8)
+    s.update(state)
+    s["lengths"], s["weights"] = torch.tensor([64, 30, 64]), None
+    on["lengths"], on["weights"] = s["lengths"].cuda(), None
+    check_evict(tk, s, 20, 4, on)
+
+
 def test_a_conversation_past_its_cache(tk):
     """Token after token into a cache of 24 slots, then cut to 10: what is held is always what the definition holds."""
     g = gen(7)

@@ -1,6 +1,7 @@
 """Refusals of the operators of a language model at the C ABI (no kernel is launched here), and what their host code asks the
 CUDA runtime for, by the stand-in that the other operators' tests use."""
 import ctypes
+import random
 import threading
 
 import pytest
@@ -166,6 +167,47 @@ def test_replace_takes_keys_and_values_of_one_buffer(lib):  # noqa: F811
     assert replace(lib, keys=view(at(0), *by), values=view(VP(at(0).value + 4 * D - 4), *by)) == EINVAL
     assert replace(lib, keys=view(at(0), *by), values=view(VP(at(0).value + 4 * D + 4), *by)) == EINVAL
     assert replace(lib, weights=None) == 0 and replace(lib, batch=0, keys=None) == 0
+
+
+@pytest.mark.parametrize("first", range(4))
+def test_keys_and_values_stacked_along_any_dimension(lib, first):  # noqa: F811
+    # (batch, heads, capacity) with the two caches side by side before the first, second, ... of them, or in each row
+    n, by, step = [B, H, N], [0, 0, 0], D
+    for d in (3, 2, 1, 0):
+        if d < 3:
+            by[d], step = step, step * n[d]
+        if d == first:
+            apart, step = step, step * 2
+    both = VP(at(0).value + 4 * apart)
+    assert replace(lib, keys=view(at(0), *by), values=view(both, *by)) == 0
+    assert replace(lib, values=view(at(0), *by), keys=view(both, *by)) == 0
+    for off in (-4, 4):
+        assert replace(lib, keys=view(at(0), *by), values=view(VP(both.value + off), *by)) == (0 if first == 0 and off > 0 else EINVAL)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_caches_that_meet_are_refused_and_no_others(lib, seed):  # noqa: F811
+    r = random.Random(seed)
+    n = [r.choice([1, 2, 3, 5]) for _ in range(3)]
+    dims = [r.choice([1, 3, 8]), r.choice([1, 3, 8])]
+    order, by, step = r.sample(range(3), 3), [0, 0, 0], max(dims) * r.choice([1, 2]) + r.randrange(3)
+    for d in order:
+        by[d], step = step, step * n[d] + r.choice([0, 0, 5, step])
+    for _ in range(60):
+        off = r.randrange(-step - 5, step + 5)
+        bytes_at = [{4 * (base + i * by[0] + j * by[1] + k * by[2] + c) for i in range(n[0]) for j in range(n[1]) for k in range(n[2]) for c in range(dim)}
+                    for base, dim in ((0, dims[0]), (off, dims[1]))]
+        got = replace(lib, keys=view(at(0), *by), values=view(VP(at(0).value + 4 * off), *by), score=view(at(2), n[1] * n[2], n[2]),
+                      positions=view(at(3), n[1] * n[2], n[2]), key=view(at(5), 64, 8), value=view(at(6), 64, 8), weights=None, batch=n[0], heads=n[1],
+                      capacity=n[2], kd=dims[0], vd=dims[1], recent=0)
+        assert got == (EINVAL if bytes_at[0] & bytes_at[1] else 0), (n, by, dims, off)
+
+
+def test_weights_of_one_row_repeated_are_bounded(lib):  # noqa: F811
+    for call in (evict, replace):
+        assert call(lib, weights=view(at(9 if call is replace else 14), 0, 0, 0), group=1 << 15, queries=(1 << 15) + 1) == EUNSUPPORTED
+        assert call(lib, weights=view(at(9 if call is replace else 14), 0, 0, 0), group=1 << 15, queries=1 << 15) == 0
+    events(lib)
 
 
 CHAINS = [dispatch, combine_backward, evict]

@@ -1,5 +1,6 @@
 // C entries of the operators around the selection (declared in include/topk.h):
 // argument checks, the per-(device, stream) scratch block and the launches.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -410,21 +411,29 @@ struct Rows4 {
     return true;
   }
 };
-// Whether two have a byte in common; where their distances differ, whether their ranges meet.
-bool meet(Rows4 a, Rows4 b) {
+// Whether a row of a's and one of b's, b being `off` bytes behind, have a byte in common, by the distances order[level ... 2] (the
+// largest first): a place of one against one of the other, of which the distance leaves two to try, since all that lies
+// within one of its steps is shorter than it.
+bool meet_at(const Rows4& a, const Rows4& b, int64_t off, const int* order, int level) {
+  while (level < 3 && a.n[order[level]] < 2) ++level;
+  if (level == 3) return off < a.row && -off < b.row;
+  const int64_t d = a.by[order[level]], most = a.n[order[level]] - 1;
+  const int64_t low = off >= 0 ? off / d : -((-off + d - 1) / d);
+  for (int64_t q = low; q <= low + 1; ++q)
+    if (q >= -most && q <= most && meet_at(a, b, off - q * d, order, level + 1)) return true;
+  return false;
+}
+// Whether two have a byte in common; where they lie on different grids, whether their ranges meet.
+bool meet(const Rows4& a, const Rows4& b) {
   if (!a.any() || !b.any()) return false;
-  if (b.at < a.at) std::swap(a, b);
+  if (b.at < a.at) return meet(b, a);
   if (b.at - a.at >= static_cast<uintptr_t>(a.reach())) return false;
-  int64_t ld = 0;
-  for (int i = 0; i < 3; ++i) {
-    if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.by[i] != b.by[i])) return true;
-    if (a.n[i] > 1 && (ld == 0 || a.by[i] < ld)) ld = a.by[i];
-  }
-  if (ld < 1) return true;
   for (int i = 0; i < 3; ++i)
-    if (a.n[i] > 1 && a.by[i] % ld) return true;
-  const int64_t d = static_cast<int64_t>((b.at - a.at) % static_cast<uintptr_t>(ld));
-  return d < a.row || d + b.row > ld;
+    if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.by[i] != b.by[i])) return true;
+  if (!a.apart() || !b.apart()) return true;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return a.by[x] > a.by[y]; });
+  return meet_at(a, b, static_cast<int64_t>(b.at - a.at), order, 0);
 }
 bool clash(std::initializer_list<Rows4> outs, std::initializer_list<Rows4> ins) {
   for (auto o = outs.begin(); o != outs.end(); ++o) {
@@ -446,7 +455,7 @@ int check_cache(int dtype, int weights_dtype, bool weighted, int64_t batch, int6
     return TOPK_EUNSUPPORTED;
   // (byte counts stay below 2^63)
   const int64_t most = int64_t(1) << 40, dim = key_dim > value_dim ? key_dim : value_dim;
-  if (dim > (1 << 20) || batch * heads > most / capacity || (weighted && (group * queries > kMaxExtent || group * queries > most / heads))) return TOPK_EUNSUPPORTED;
+  if (dim > (1 << 20) || batch * heads > most / capacity || (weighted && (group * queries > (1 << 30) || group * queries > most / heads))) return TOPK_EUNSUPPORTED;
   return TOPK_OK;
 }
 
