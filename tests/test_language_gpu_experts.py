@@ -271,3 +271,12 @@ def test_refusals(tk):
                        (lambda: tk.combine_backward(x, x.double(), idx), TypeError)):
         with pytest.raises(kind):
             call()
+
+
+def test_need_that_is_neither_true_nor_false(tk):
+    dy, ys, place = torch.ones(2, 8, device="cuda"), torch.ones(2, 8, device="cuda"), torch.zeros(2, 1, dtype=torch.int64, device="cuda")
+    for need in ((torch.ones(2), True), (True, torch.ones(2)), (True,)):
+        with pytest.raises((RuntimeError, TypeError)):
+            tk.combine_backward(dy, ys, place, need=need)
+    dys, dw = tk.combine_backward(dy, ys, place, need=(0, 1))
+    assert dys is None and torch.equal(dw, torch.full((2, 1), 8.0, device="cuda"))

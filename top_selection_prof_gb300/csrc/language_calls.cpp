@@ -241,7 +241,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 
 // dy, ys, place, weights, whether dys is wanted, whether dweights is
 PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call<6>(n_args, [&] {
+  return call<6>(n_args, [&]() -> PyObject* {
     const at::Tensor& dy = tensor(a[0], "dy");
     const int code = first(dy);
     two_dims(dy, "dy", "(tokens, d)");
@@ -253,7 +253,8 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const at::Tensor& place = choices(a[2], tokens, device, "place");
     const void* weights = of_places(a[3], place, dy.scalar_type(), device, "weights");
     const int64_t k = place.size(1);
-    const bool want_dys = PyObject_IsTrue(a[4]) == 1, want_dweights = PyObject_IsTrue(a[5]) == 1;
+    const int want_dys = PyObject_IsTrue(a[4]), want_dweights = want_dys < 0 ? -1 : PyObject_IsTrue(a[5]);
+    if (want_dweights < 0) return nullptr;
     Launch launch(device);
     at::Tensor dys, dweights;
     if (want_dys) dys = empty({rows, d}, dy.scalar_type(), device);
