@@ -56,7 +56,8 @@ __device__ __forceinline__ int64_t clamped(int64_t v, int64_t most) { return v <
 // ---- sums by position ------------------------------------------------------------
 struct WeightSums {
   View weights;       // batch, query head, query
-  int64_t group, queries, heads, capacity;
+  int64_t group, queries, capacity;
+  unsigned heads, chunks;  // (32-bit: a 64-bit division takes a hundred instructions, in every thread)
   View score;         // batch, head
   const int64_t* lengths;
   float* out;         // batch x heads x capacity
@@ -72,8 +73,8 @@ struct Sum2Pair {
     return r;
   }
   __device__ __forceinline__ static Pair minus(Pair a, Pair b) {
-    Pair r = a;
-    r.fma(b, Pair::of(-1.0f, -1.0f));
+    Pair r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
     return r;
   }
   __device__ __forceinline__ void add(Pair v) {
@@ -89,18 +90,15 @@ struct Places {
   static constexpr int kWide = VEC > 1 ? VEC : 4;
   Raw<T, VEC> r[VEC > 1 ? 1 : kWide];
   __device__ __forceinline__ static int at(int lane, int e) { return VEC > 1 ? lane * VEC + e : e * 32 + lane; }
-  // (the last vector of a row may reach past its length, not past the capacity)
-  __device__ __forceinline__ void load(const T* row, int lane, int64_t left) {
-    if constexpr (VEC > 1) {
-      r[0].clear();
-      if (lane * VEC < left) r[0].load_nc(row + lane * VEC);
-    } else {
+  // (positions behind `left`, which no sum is taken of, are read at the row's start; the last vector of a row may reach past its
+  // length, not past the capacity)
+  __device__ __forceinline__ static void offsets(int* off, int lane, int64_t left) {
 #pragma unroll
-      for (int e = 0; e < kWide; ++e) {
-        r[e].clear();
-        if (e * 32 + lane < left) r[e].load_nc(row + e * 32 + lane);
-      }
-    }
+    for (int e = 0; e < (VEC > 1 ? 1 : kWide); ++e) off[e] = at(lane, e) < left ? at(lane, e) : 0;
+  }
+  __device__ __forceinline__ void load(const T* row, const int* off) {
+#pragma unroll
+    for (int e = 0; e < (VEC > 1 ? 1 : kWide); ++e) r[e].load_nc(row + off[e]);
   }
   __device__ __forceinline__ Pair pair(int i) const {
     if constexpr (VEC > 1) return r[0].pair(i);
@@ -110,14 +108,14 @@ struct Places {
 
 // A block: 32 pieces of positions of one head, the head's query rows dealt to its warps, kAhead of them under way.
 template <typename T, int VEC, int kAhead>
-__global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSums p) {
+__global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const WeightSums p) {
   using P = Places<T, VEC>;
   constexpr int kWide = P::kWide;
   __shared__ float2 part[kSumWarps][32 * kWide];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t chunks = (p.capacity + 32 * kWide - 1) / (32 * kWide), bh = blockIdx.x / chunks, b = bh / p.heads, h = bh % p.heads;
-  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = (blockIdx.x - bh * chunks) * 32 * kWide;
+  const unsigned bh = blockIdx.x / p.chunks, b = bh / p.heads, h = bh % p.heads;
+  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = int64_t(blockIdx.x - bh * p.chunks) * 32 * kWide;
   if (at0 >= len) return;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   Sum2Pair sum[kWide / 2];
@@ -126,18 +124,25 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSu
   static_assert(32 * kWide <= kSumThreads, "a position a thread at the end");
   const bool sums = threadIdx.x < 32 * kWide && at0 + threadIdx.x < len;
   const float before = sums ? static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + threadIdx.x] : 0.0f;
+  int off[VEC > 1 ? 1 : kWide];
+  P::offsets(off, lane, len - at0);
   // (a group's rows are mostly as far apart as a head's own)
   const bool even = p.weights.head == p.queries * p.weights.row;
+  const int64_t step = kSumWarps * p.weights.row;
+  const T* row = base + warp * p.weights.row;
   for (int i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
     P v[kAhead];
+    const bool all = i0 + (kAhead - 1) * kSumWarps < n;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = i0 + a * kSumWarps, g = even ? 0 : i / queries;
-      v[a].load(base + g * p.weights.head + (i - g * queries) * p.weights.row, lane, i < n ? len - at0 : 0);
+    for (int a = 0; a < kAhead; ++a, row += step) {
+      const int i = i0 + a * kSumWarps;
+      if (!all && i >= n) break;
+      if (!even) row = base + i / queries * p.weights.head + i % queries * p.weights.row;
+      v[a].load(row, off);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      if (i0 + a * kSumWarps >= n) break;
+      if (!all && i0 + a * kSumWarps >= n) break;
 #pragma unroll
       for (int e = 0; e < kWide / 2; ++e) sum[e].add(v[a].pair(e));
     }
@@ -166,15 +171,16 @@ __global__ void __launch_bounds__(kSumThreads) weight_sums_kernel(const WeightSu
     all.add(before);
     for (int q = 0; q < n; ++q) all.add(counted(to_f32(base[(q / queries) * p.weights.head + (q % queries) * p.weights.row + at])));
   }
-  p.out[bh * p.capacity + at0 + at] = all.value();
+  p.out[int64_t(bh) * p.capacity + at0 + at] = all.value();
 }
 
 // ---- the choice -------------------------------------------------------------------
 struct Choice {
   const float* score;     // batch x heads rows, `ld` apart by head and `ld_batch` by batch
-  int64_t ld_batch, ld, heads, capacity;
+  int64_t ld_batch, ld, capacity;
+  unsigned heads;
   const int64_t* lengths;
-  int64_t batch, keep, recent;
+  int64_t keep, recent;
   float* out_score;       // batch x heads x keep
   int64_t* kept;
   int64_t* out_lengths;
@@ -214,38 +220,41 @@ __device__ __forceinline__ unsigned scan_before(ChoiceShared& s, unsigned v, uns
 
 // Up to EACH positions a thread, in a run, whose keys stay in registers; 0: as many as it takes, read anew in each pass.
 template <int EACH>
-__global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
+__global__ void __launch_bounds__(kThreads, 2) choice_kernel(const Choice p) {
   __shared__ ChoiceShared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
   for (int i = threadIdx.x; i < kDigits; i += kThreads) s.hist[i] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t bh = blockIdx.x / blocks, b = bh / p.heads, h = bh % p.heads;
+  const unsigned bh = blockIdx.x / static_cast<unsigned>(blocks), b = bh / p.heads, h = bh % p.heads;
   const float* score = p.score + b * p.ld_batch + h * p.ld;
   const int64_t len = clamped(p.lengths[b], p.capacity);
   const int64_t kept = min(len, p.keep), old = len - min(p.recent, len);  // the last ones stay
   const unsigned want = static_cast<unsigned>(len > p.keep ? p.keep - (len - old) : old);  // of the others
   // this thread's run of positions
-  const int64_t each = (len + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
+  const int64_t each = (len + blocks * kThreads - 1) / kThreads >> (31 - __clz(blocks));  // (blocks: a power of two)
   const int64_t begin = min(len, (int64_t(rank) * kThreads + threadIdx.x) * each), end = min(len, begin + each);
   const bool choose = want < old;
-  uint32_t keys[EACH ? EACH : 1];
+  // (in 32 bits, by the number in the run: how many there are, and how many of them are not recent)
+  const int mine = static_cast<int>(end - begin), mine_old = static_cast<int>(clamped(old - begin, mine));
+  float held[EACH ? EACH : 1];
   if constexpr (EACH > 0) {
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) keys[e] = begin + e < end ? order_key_f32(__float_as_uint(score[begin + e])) : 0;
+    for (int e = 0; e < EACH; ++e) held[e] = e < mine ? score[begin + e] : 0.0f;
   }
-  auto key_at = [&](int64_t i, int e) -> uint32_t {
-    if constexpr (EACH > 0) return keys[e];
-    else return order_key_f32(__float_as_uint(score[i]));
+  auto score_at = [&](int e) -> float {
+    if constexpr (EACH > 0) return held[e];
+    else return score[begin + e];
   };
-  auto run = [&](auto f) {
+  auto key_at = [&](int e) -> uint32_t { return order_key_f32(__float_as_uint(score_at(e))); };
+  auto run = [&](int n, auto f) {
     if constexpr (EACH > 0) {
 #pragma unroll
       for (int e = 0; e < EACH; ++e)
-        if (begin + e < end) f(begin + e, e);
+        if (e < n) f(e);
     } else {
-      for (int64_t i = begin; i < end; ++i) f(i, 0);
+      for (int e = 0; e < n; ++e) f(e);
     }
   };
   cluster_sync();               // (every block has started before another reaches into its memory)
@@ -255,9 +264,9 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
 #pragma unroll 1
     for (int digit = 0; digit < 3; ++digit) {
       const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
-      run([&](int64_t i, int e) {
-        const uint32_t k = key_at(i, e);
-        if (i < old && (k & mask) == key) atomicAdd(&s.hist[(~k >> shift) & ((1u << bits) - 1)], 1u);
+      run(mine_old, [&](int e) {
+        const uint32_t k = key_at(e);
+        if ((k & mask) == key) atomicAdd(&s.hist[(~k >> shift) & ((1u << bits) - 1)], 1u);
       });
       cluster_sync();
       const int share = kDigits / blocks;
@@ -293,20 +302,27 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
     }
   }
   // kept: the recent ones, scores above the key's, and the first `left` of those that equal it
-  auto state = [&](int64_t i, int e) -> int {  // 2: kept, 1: equal, 0
-    if (i >= old || !choose) return 2;
+  auto state = [&](int e) -> int {  // 2: kept, 1: equal, 0
+    if (e >= mine_old || !choose) return 2;
     if (want == 0) return 0;
-    const uint32_t k = key_at(i, e) & mask;
+    const uint32_t k = key_at(e) & mask;
     return k > key ? 2 : k == key ? 1 : 0;
   };
   unsigned over = 0, even = 0, all_over, all_even;
-  run([&](int64_t i, int e) {
-    const int st = state(i, e);
+  run(mine, [&](int e) {
+    const int st = state(e);
     over += st == 2;
     even += st == 1;
   });
-  over = scan_before(s, over, &all_over);
-  even = scan_before(s, even, &all_even);
+  if constexpr (EACH > 0) {  // both sums in one: less than 2^16 each
+    static_assert(EACH * kThreads < 65536, "halves of 32 bits");
+    unsigned all;
+    const unsigned both = scan_before(s, over << 16 | even, &all);
+    over = both >> 16, even = both & 0xffff, all_over = all >> 16, all_even = all & 0xffff;
+  } else {
+    over = scan_before(s, over, &all_over);
+    even = scan_before(s, even, &all_even);
+  }
   if (threadIdx.x < blocks) {
     ChoiceShared* peer = cluster.map_shared_rank(&s, threadIdx.x);
     peer->over[rank] = all_over;
@@ -317,19 +333,19 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
     over += s.over[q];
     even += s.even[q];
   }
-  int64_t slot = bh * p.keep + over + min(even, left);
-  run([&](int64_t i, int e) {
-    const int st = state(i, e);
+  int64_t slot = int64_t(bh) * p.keep + over + min(even, left);
+  run(mine, [&](int e) {
+    const int st = state(e);
     const bool stays = st == 2 || (st == 1 && even < left);
     even += st == 1;
     if (!stays) return;
-    p.kept[slot] = i;
-    p.out_score[slot] = score[i];
+    p.kept[slot] = begin + e;
+    p.out_score[slot] = score_at(e);
     ++slot;
   });
   for (int64_t i = kept + rank * kThreads + threadIdx.x; i < p.keep; i += int64_t(blocks) * kThreads) {
-    p.kept[bh * p.keep + i] = -1;
-    p.out_score[bh * p.keep + i] = 0.0f;
+    p.kept[int64_t(bh) * p.keep + i] = -1;
+    p.out_score[int64_t(bh) * p.keep + i] = 0.0f;
   }
   if (h == 0 && rank == 0 && threadIdx.x == 0) p.out_lengths[b] = kept;
 }
@@ -338,45 +354,62 @@ __global__ void __launch_bounds__(kThreads) choice_kernel(const Choice p) {
 struct MoveKept {
   View in[2];          // keys, values
   void* out[2];        // batch x heads x keep x dim
-  int64_t dim[2];
+  int dim[2];
   const int64_t* kept;
-  int64_t heads, keep, total;  // batch x heads x keep
-  int share;           // threads a row
+  int64_t keep;
+  unsigned heads, chunks;  // runs of rows in a head
+  int used, rows;      // threads a row, and rows that a block has threads for
 };
+constexpr int kMoveThreads = 256;
+// A block: p.rows rows of a head times kMoveTogether, whose loads are under way together.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) move_kept_kernel(const MoveKept p) {
+__global__ void __launch_bounds__(kMoveThreads) move_kept_kernel(const MoveKept p) {
+  constexpr int kTogether = VEC > 1 ? 2 : 1, kEach = VEC > 1 ? 1 : 4;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t i = int64_t(blockIdx.x) * (256 / p.share) + threadIdx.x / p.share;
-  if (i >= p.total) return;
-  const int64_t bh = i / p.keep, b = bh / p.heads, h = bh % p.heads, from = p.kept[i];
-  const int at = threadIdx.x % p.share;
-  const int dims[2] = {static_cast<int>(p.dim[0]), static_cast<int>(p.dim[1])}, most = max(dims[0], dims[1]);
+  const unsigned bh = blockIdx.x / p.chunks, b = bh / p.heads, h = bh % p.heads;
+  const int mine = threadIdx.x / p.used, at = threadIdx.x % p.used;
+  if (mine >= p.rows) return;
+  const int64_t i0 = int64_t(blockIdx.x - bh * p.chunks) * (p.rows * kTogether) + mine;
+  const int64_t* kept = p.kept + int64_t(bh) * p.keep;
+  int64_t from[kTogether];
+#pragma unroll
+  for (int r = 0; r < kTogether; ++r) from[r] = i0 + r * p.rows < p.keep ? kept[i0 + r * p.rows] : -1;
+  const int most = max(p.dim[0], p.dim[1]);
   const T* src[2];
+  T* dst[2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) src[w] = static_cast<const T*>(p.in[w].data) + b * p.in[w].batch + h * p.in[w].head + from * p.in[w].row;
+  for (int w = 0; w < 2; ++w) {
+    src[w] = static_cast<const T*>(p.in[w].data) + b * p.in[w].batch + h * p.in[w].head;
+    dst[w] = static_cast<T*>(p.out[w]) + (int64_t(bh) * p.keep + i0) * p.dim[w];
+  }
   // (the loads of both first, and without vectors four values of each)
-  constexpr int kEach = VEC > 1 ? 1 : 4;
-  for (int c0 = at * VEC; c0 < most; c0 += p.share * VEC * kEach) {
-    Raw<T, VEC> v[2][kEach];
+  for (int c0 = at * VEC; c0 < most; c0 += p.used * VEC * kEach) {
+    Raw<T, VEC> v[kTogether][2][kEach];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int r = 0; r < kTogether; ++r)
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const int c = c0 + e * p.share;
-        v[w][e].clear();
-        if (from >= 0 && c < dims[w]) v[w][e].load_nc(src[w] + c);
-      }
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+        for (int e = 0; e < kEach; ++e) {
+          const int c = c0 + e * p.used;
+          v[r][w][e].clear();
+          if (from[r] >= 0 && c < p.dim[w]) v[r][w][e].load_nc(src[w] + from[r] * p.in[w].row + c);
+        }
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const int c = c0 + e * p.share;
-        T* dst = static_cast<T*>(p.out[w]) + i * p.dim[w] + c;
-        if (c >= dims[w]) continue;
-        if constexpr (VEC == 1) *dst = v[w][e].u;
-        else __stcs(reinterpret_cast<uint4*>(dst), v[w][e].u);
-      }
+    for (int r = 0; r < kTogether; ++r) {
+      if (i0 + r * p.rows >= p.keep) break;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int c = c0 + e * p.used;
+          T* to = dst[w] + r * p.rows * p.dim[w] + c;
+          if (c >= p.dim[w]) continue;
+          if constexpr (VEC == 1) *to = v[r][w][e].u;
+          else __stcs(reinterpret_cast<uint4*>(to), v[r][w][e].u);
+        }
+    }
   }
 }
 
@@ -391,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t bh = blockIdx.x / blocks, b = bh / p.heads, h = bh % p.heads;
+  const unsigned bh = blockIdx.x / static_cast<unsigned>(blocks), heads = static_cast<unsigned>(p.heads), b = bh / heads, h = bh % heads;
   const int64_t seen = max(p.lengths[b], int64_t(0)), len = min(seen, p.capacity);
   float* score = static_cast<float*>(p.score.data) + b * p.score.batch + h * p.score.head;
   int64_t* positions = static_cast<int64_t*>(p.positions.data) + b * p.positions.batch + h * p.positions.head;
@@ -528,32 +561,33 @@ bool aligned_view(const View& v, int64_t size) {
 template <typename T>
 cudaError_t add_weights(const Evict& p, float* out, cudaStream_t st) {
   constexpr int kVec = 16 / sizeof(T);
-  const WeightSums w{p.weights, p.group, p.queries, p.heads, p.capacity, p.score, p.lengths, out};
   const bool wide = aligned_view(p.weights, sizeof(T)) && p.capacity % kVec == 0;
   const int64_t each = 32 * (wide ? kVec : 4);
-  const int64_t blocks = (p.capacity + each - 1) / each * p.batch * p.heads;
+  const int64_t chunks = (p.capacity + each - 1) / each, blocks = chunks * p.batch * p.heads;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
+  const WeightSums w{p.weights, p.group, p.queries, p.capacity, static_cast<unsigned>(p.heads), static_cast<unsigned>(chunks), p.score, p.lengths, out};
   const unsigned grid = static_cast<unsigned>(blocks);
   // (few rows a warp: four at a time and more blocks an SM)
   if (p.group * p.queries <= 4 * kSumWarps || !wide)
     return wide ? launch_after(weight_sums_kernel<T, kVec, 4>, grid, kSumThreads, 0, st, w) : launch_after(weight_sums_kernel<T, 1, 4>, grid, kSumThreads, 0, st, w);
-  return launch_after(weight_sums_kernel<T, kVec, 16>, grid, kSumThreads, 0, st, w);
+  return launch_after(weight_sums_kernel<T, kVec, 8>, grid, kSumThreads, 0, st, w);
 }
 
 template <typename T>
 cudaError_t move_kept(const Evict& p, cudaStream_t st) {
   constexpr int kVec = 16 / sizeof(T);
-  MoveKept m{{p.keys, p.values}, {p.out_keys, p.out_values}, {p.key_dim, p.value_dim}, p.out_kept, p.heads, p.keep, p.batch * p.heads * p.keep, 0};
   const int64_t size = sizeof(T);
   const bool wide = aligned_view(p.keys, size) && aligned_view(p.values, size) && p.key_dim % kVec == 0 && p.value_dim % kVec == 0 &&
                     (reinterpret_cast<uintptr_t>(p.out_keys) | reinterpret_cast<uintptr_t>(p.out_values)) % 16 == 0;
-  const int64_t dim = p.key_dim > p.value_dim ? p.key_dim : p.value_dim;
-  m.share = 8;
-  while (m.share < 256 && m.share * (wide ? kVec : 4) < dim) m.share *= 2;
-  const int64_t blocks = (m.total + 256 / m.share - 1) / (256 / m.share);
+  const int dim = static_cast<int>(p.key_dim > p.value_dim ? p.key_dim : p.value_dim);
+  // whole rows by as many threads as they have pieces (18 of 16 bytes: 14 rows a block, not 8), or longer ones in turns
+  const int pieces = (dim + (wide ? kVec : 4) - 1) / (wide ? kVec : 4), used = pieces < kMoveThreads ? pieces : kMoveThreads, rows = kMoveThreads / used;
+  const int64_t each = rows * (wide ? 2 : 1), chunks = (p.keep + each - 1) / each, blocks = chunks * p.batch * p.heads;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
-  return wide ? launch_after(move_kept_kernel<T, kVec>, static_cast<unsigned>(blocks), 256, 0, st, m)
-              : launch_after(move_kept_kernel<T, 1>, static_cast<unsigned>(blocks), 256, 0, st, m);
+  const MoveKept m{{p.keys, p.values}, {p.out_keys, p.out_values}, {static_cast<int>(p.key_dim), static_cast<int>(p.value_dim)}, p.out_kept, p.keep,
+                   static_cast<unsigned>(p.heads), static_cast<unsigned>(chunks), used, rows};
+  return wide ? launch_after(move_kept_kernel<T, kVec>, static_cast<unsigned>(blocks), kMoveThreads, 0, st, m)
+              : launch_after(move_kept_kernel<T, 1>, static_cast<unsigned>(blocks), kMoveThreads, 0, st, m);
 }
 
 }  // namespace
@@ -565,7 +599,7 @@ size_t evict_scratch_bytes(const Evict& p) {
 }
 
 cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st) {
-  Choice c{static_cast<const float*>(p.score.data), p.score.batch, p.score.head, p.heads, p.capacity, p.lengths, p.batch, p.keep,
+  Choice c{static_cast<const float*>(p.score.data), p.score.batch, p.score.head, p.capacity, static_cast<unsigned>(p.heads), p.lengths, p.keep,
            p.recent, p.out_score, p.out_kept, p.out_lengths};
   if (p.weights.data) {
     float* sums = sc.take<float>(p.batch * p.heads * p.capacity);
