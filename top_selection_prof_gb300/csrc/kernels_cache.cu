@@ -416,9 +416,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kept_kernel(const MoveKept 
 // ---- one token ----------------------------------------------------------------------
 // A cluster a head: adds the group's weights to the scores, finds the slot and writes the token there.  A thread holds WIDE slots
 // side by side, whose weights, score and positions are all under way at once; where rows are not on 16-byte boundaries, one.
+constexpr int kReplaceThreads = 256, kReplaceWarps = kReplaceThreads / 32;
 template <typename W, int WIDE>
-__global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
-  __shared__ uint64_t warp_least[kWarps];
+__global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Replace p) {
+  __shared__ uint64_t warp_least[kReplaceWarps];
   __shared__ uint64_t leasts[kMostBlocks];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
@@ -431,9 +432,10 @@ __global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
   const W* weights = static_cast<const W*>(p.weights.data);
   if (weights) weights += b * p.weights.batch + h * p.group * p.weights.head;
   const int n = weights ? static_cast<int>(p.group * p.queries) : 0, queries = static_cast<int>(p.queries);
+  const bool even = p.weights.head == p.queries * p.weights.row;  // (a group's rows as far apart as a head's own)
   const bool full = seen >= p.capacity;
   uint64_t least = ~uint64_t(0);  // (score, slot) of the least that may go
-  for (int64_t i = (int64_t(rank) * kThreads + threadIdx.x) * WIDE; i < len; i += int64_t(blocks) * kThreads * WIDE) {
+  for (int64_t i = (int64_t(rank) * kReplaceThreads + threadIdx.x) * WIDE; i < len; i += int64_t(blocks) * kReplaceThreads * WIDE) {
     // (a run's slots behind `len` are read, not written: they lie within the capacity)
     Sum2 sum[WIDE];
     unsigned may = full && p.recent == 0 ? ~0u : 0;  // slots that may go
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
       Raw<W, WIDE> v[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int r = r0 + a, g = r / queries;
+        const int r = r0 + a, g = even ? 0 : r / queries;
         v[a].clear();
         if (r < n) v[a].load_nc(weights + g * p.weights.head + (r - g * queries) * p.weights.row + i);
       }
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
   if (threadIdx.x % 32 == 0) warp_least[threadIdx.x / 32] = least;
   cluster_sync();
   if (threadIdx.x < blocks) {
-    for (int w = 0; w < kWarps; ++w) least = min(least, warp_least[w]);
+    for (int w = 0; w < kReplaceWarps; ++w) least = min(least, warp_least[w]);
     *cluster.map_shared_rank(&leasts[rank], threadIdx.x) = least;
   }
   cluster_sync();
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) replace_kernel(const Replace p) {
     const View& out = w ? p.values : p.keys;
     const int64_t dim = w ? p.value_dim : p.key_dim;
     const int64_t src = b * in.batch + h * in.head, dst = b * out.batch + h * out.head + slot * out.row;
-    for (int64_t c = threadIdx.x; c < dim; c += kThreads) {
+    for (int64_t c = threadIdx.x; c < dim; c += kReplaceThreads) {
       if (p.dtype == kF32) static_cast<float*>(out.data)[dst + c] = static_cast<const float*>(in.data)[src + c];
       else static_cast<__nv_bfloat16*>(out.data)[dst + c] = static_cast<const __nv_bfloat16*>(in.data)[src + c];
     }
@@ -536,11 +538,11 @@ int blocks_for(int64_t rows, int64_t positions, int64_t least) {
 }
 
 template <typename P>
-cudaError_t launch_clusters(void (*kernel)(P), const P& p, int64_t rows, int blocks, cudaStream_t st) {
+cudaError_t launch_clusters(void (*kernel)(P), const P& p, int64_t rows, int blocks, int threads, cudaStream_t st) {
   if (rows * blocks > INT32_MAX) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * blocks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -613,7 +615,7 @@ cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st) {
   const int blocks = blocks_for(rows, p.capacity, 2048);
   // positions a thread: in registers up to 16
   const int64_t each = (p.capacity + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
-  cudaError_t e = launch_clusters(each <= 4 ? choice_kernel<4> : each <= 8 ? choice_kernel<8> : each <= 16 ? choice_kernel<16> : choice_kernel<0>, c, rows, blocks, st);
+  cudaError_t e = launch_clusters(each <= 4 ? choice_kernel<4> : each <= 8 ? choice_kernel<8> : each <= 16 ? choice_kernel<16> : choice_kernel<0>, c, rows, blocks, kThreads, st);
   if (e != cudaSuccess) return e;
   return p.dtype == kF32 ? move_kept<float>(p, st) : move_kept<__nv_bfloat16>(p, st);
 }
@@ -624,8 +626,8 @@ static cudaError_t replace_by(const Replace& p, cudaStream_t st) {
   const int64_t rows = p.batch * p.heads;
   auto on = [](const View& v, int64_t size) { return aligned_view(View{v.data, v.batch, v.head, 0}, size); };
   const bool wide = p.capacity % kVec == 0 && on(p.score, 4) && on(p.positions, 8) && (!p.weights.data || aligned_view(p.weights, sizeof(W)));
-  if (wide) return launch_clusters(replace_kernel<W, kVec>, p, rows, blocks_for(rows, p.capacity, 2048), st);
-  return launch_clusters(replace_kernel<W, 1>, p, rows, blocks_for(rows, p.capacity, 512), st);
+  if (wide) return launch_clusters(replace_kernel<W, kVec>, p, rows, blocks_for(rows, p.capacity, 2048), kReplaceThreads, st);
+  return launch_clusters(replace_kernel<W, 1>, p, rows, blocks_for(rows, p.capacity, 512), kReplaceThreads, st);
 }
 
 cudaError_t launch_replace(const Replace& p, cudaStream_t st) {
