@@ -48,7 +48,7 @@ constexpr int kOctaves = 16;                 // octaves that one histogram cover
 constexpr int kBins = kSub * kOctaves;
 constexpr int kWindows = 3;                  // weights below 2^-48 of the largest count as zero
 constexpr float kDeepest = kOctaves * kWindows;
-constexpr int kHeadCap = 2560;               // tokens that the first block searches itself, of the head
+constexpr int kHeadCap = 2240;               // tokens that the first block searches itself, of the head
 constexpr int kListCap = 1536;               // and of bins
 constexpr int kHead = 1024;                  // tokens that the head should have; for one top_k of all rows up to a quarter of
 constexpr int kLeastHead = 128;              // that, four times the top_k
