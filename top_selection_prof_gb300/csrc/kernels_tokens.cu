@@ -318,6 +318,24 @@ __device__ __forceinline__ float top_of(const Raw<T, 16 / sizeof(T)>& raw) {
   }
 }
 
+// take(value, its number) for the values of 16 bytes that are wanted: mostly one, so one at a time (eight in a row in the code, run
+// once a call, took longer to fetch than to run).
+template <typename T, typename W, typename F>
+__device__ __forceinline__ void each_of(const Raw<T, 16 / sizeof(T)>& raw, W wanted, F take) {
+  constexpr int kVec = 16 / sizeof(T);
+  Vec<T, kVec> v;
+  v.set_raw(raw);
+  unsigned in = 0;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) in |= wanted(v.v[e]) ? 1u << e : 0;
+#pragma unroll 1
+  for (; in; in &= in - 1) {
+    const int e = __ffs(static_cast<int>(in)) - 1, word = e * static_cast<int>(sizeof(T)) / 4;
+    const uint32_t w = word < 2 ? word == 0 ? raw.u.x : raw.u.y : word == 2 ? raw.u.z : raw.u.w;
+    take(__uint_as_float(sizeof(T) == 4 ? w : e & 1 ? w & 0xffff0000u : w << 16), e);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void clear_bins() {
   Shared& s = own();
@@ -495,23 +513,23 @@ __device__ __noinline__ void serve() {
     cluster_sync();
     join_bins();
   } else {
-    if (op == kOpGather) {
-      if (threadIdx.x == 0) s.list.n = 0;
-      cluster_sync();  // (before others add to the first block's)
-    }
+    if (rank != 0 && threadIdx.x == 0) s.list.n = 0;  // (the first block's: before the order, as others add to it)
     if (op == kOpDigits) {
       clear_bins<T>();
       __syncthreads();
     }
     const float low = s.order.low, high = s.order.high, other_low = s.order.low2, other_high = s.order.high2;
     uint64_t any = 0, none = 0;
+    const int from = s.order.from, to = s.order.to, from2 = s.order.from2, to2 = s.order.to2;
+    const uint64_t mask = s.order.mask, value = s.order.value;
+    const int shift = s.order.shift;
+    auto near = [&](float x) { return (x >= low && x <= high) || (x >= other_low && x <= other_high); };
     auto take = [&](float x, int index) {
-      if (!(x >= low && x <= high) && !(x >= other_low && x <= other_high)) return;
       float t;
       const int j = bin_of(x, scale, &t) - base;
-      if ((j < s.order.from || j >= s.order.to) && (j < s.order.from2 || j >= s.order.to2)) return;
+      if ((j < from || j >= to) && (j < from2 || j >= to2)) return;
       const uint64_t key = token_key(x, index);
-      if ((key & s.order.mask) != s.order.value) return;
+      if ((key & mask) != value) return;
       if (op == kOpGather) {
         const unsigned at = atomicAdd(&s.list.n, 1u);
         if (at < kListCap) s.list.key[at] = key;
@@ -520,7 +538,7 @@ __device__ __noinline__ void serve() {
         none |= ~key;
       } else {
         const unsigned w = weight_in(x, j + base, t, scale, s.middle);
-        const int digit = kDigits - 1 - static_cast<int>((key >> s.order.shift) & (kDigits - 1));
+        const int digit = kDigits - 1 - static_cast<int>((key >> shift) & (kDigits - 1));
         atomicAdd(&s.count[digit], 1u);
         atomicAdd(&s.low[digit], w & 0x7fffu);
         atomicAdd(&s.high[digit], w >> 15);
@@ -557,10 +575,7 @@ __device__ __noinline__ void serve() {
     const unsigned found = s.few;
     __syncthreads();
     auto take_all = [&](const Raw<T, kVec>& raw, int i) {
-      Vec<T, kVec> v;
-      v.set_raw(raw);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) take(v.v[e], i + e);
+      each_of<T>(raw, near, [&](float x, int e) { take(x, i + e); });
       return false;
     };
     if (found <= kNoted) {
@@ -810,6 +825,7 @@ __device__ __forceinline__ void ask(int op, int w, int from, int to, uint64_t ma
     auto lowest = [&](int t) { return sure ? scale.most - (static_cast<float>(w * kBins + t) + 0.01f) * bin - d : -FLT_MAX; };
     auto highest = [&](int f) { return sure && f > 0 ? scale.most - (static_cast<float>(w * kBins + f) - 0.01f) * bin + d : INFINITY; };
     if (op == kOpBins) s.list_window = -1;
+    if (op == kOpGather) s.list.n = 0;
     s.order = Order{scale, op, w, from, to, from2, to2, mask, value, shift, 0, lowest(to), highest(from),
                     from2 < to2 ? lowest(to2) : INFINITY, from2 < to2 ? highest(from2) : -INFINITY};
   }
@@ -1032,14 +1048,10 @@ __device__ __noinline__ float first_pass(bool rest) {
       const int i = static_cast<int>(noted[q]);
       Raw<T, kVec> raw;
       raw.u = vector_at<T>(i);
-      Vec<T, kVec> v;
-      v.set_raw(raw);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        if (v.v[e] >= tau) {
-          const unsigned at = atomicAdd(&s.head.n, 1u);
-          if (at < kHeadCap) s.head.key[at] = token_key(v.v[e], i + e);
-        }
+      each_of<T>(raw, [&](float x) { return x >= tau; }, [&](float x, int e) {
+        const unsigned at = atomicAdd(&s.head.n, 1u);
+        if (at < kHeadCap) s.head.key[at] = token_key(x, i + e);
+      });
     }
   }
   return most;
