@@ -52,7 +52,7 @@ constexpr int kHeadCap = 2240;               // tokens that the first block sear
 constexpr int kListCap = 1536;               // and of bins
 constexpr int kHead = 1024;                  // tokens that the head should have; for one top_k of all rows up to a quarter of
 constexpr int kLeastHead = 128;              // that, four times the top_k
-constexpr int kIndexBits = 18;
+constexpr int kIndexBits = 18, kKeyBits = 32 + kIndexBits;
 constexpr int kTailBits = 14;                // bits below a mass's unit that the sum behind the histogram keeps
 constexpr int64_t kPartMost = 131072;         // tokens of a block's part
 constexpr int kMostBlocks = 8;               // of a cluster
@@ -120,6 +120,11 @@ __device__ __forceinline__ unsigned weight_in(float x, int j, float t, const Sca
 __device__ __forceinline__ uint64_t token_key(float x, int index) {
   return (static_cast<uint64_t>(order_key_f32(__float_as_uint(x))) << kIndexBits) |
          static_cast<uint64_t>((1 << kIndexBits) - 1 - index);
+}
+// A bf16 value leaves the 16 bits under it zeros in its key, or ones where it is negative: how many of them are next below bit `at`.
+template <typename T>
+__device__ __forceinline__ int filled_bits(int at) {
+  return sizeof(T) == 2 && at > kIndexBits && at <= kIndexBits + 16 ? at - kIndexBits : 0;
 }
 __device__ __forceinline__ float value_of(uint64_t key) {
   return __uint_as_float(value_bits_f32(static_cast<uint32_t>(key >> kIndexBits)));
@@ -698,7 +703,7 @@ __device__ __forceinline__ void prepare_pile() {
 
 // The token of a pile where the sum over its order passes `target` (below the count or mass), by digits of the keys down to 32
 // tokens: found_key, and found_mass, the mass through it.
-template <bool HEAD>
+template <typename T, bool HEAD>
 __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
   Shared& s = own();
   auto& p = pile<HEAD>(s);
@@ -723,6 +728,9 @@ __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
   __syncthreads();
 #pragma unroll 1
   while (left > 32) {  // (at > 0: keys differ)
+    const int skip = filled_bits<T>(at);
+    prefix = prefix << skip | ((prefix >> (kKeyBits - 1 - at) & 1) ? 0 : (uint64_t(1) << skip) - 1);
+    at -= skip;
     const int next = at > kDigitBits ? at - kDigitBits : 0;
     clear_digits();
     __syncthreads();
@@ -903,9 +911,9 @@ __device__ __forceinline__ int find_bin(bool by_count, uint64_t target) {
 }
 
 // The token of bin b of the window where the sum passes `target`, as search_pile; masses in the window's unit.  Bins [also,
-// also_to) before b are listed with it where there is room: the next search's.
+// also_to) before b are listed with it where there is room: the next search's; where that is not `known`, all before b.
 template <typename T>
-__device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target, int also, int also_to) {
+__device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target, bool known, int also, int also_to) {
   Shared& s = own();
   const int w = s.window, up = kOctaves - 1 - b / kSub;
   uint64_t start;                        // mass before the list
@@ -917,7 +925,7 @@ __device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target
     start = s.mass_before[f2] - (s.mass_before[t] - s.mass_before[f]);
     target -= by_count ? s.count_before[f2] - (s.count_before[t] - s.count_before[f]) : start;
   } else {
-    const int from = s.count_before[b + 1] <= kListCap ? 0 : b;
+    const int from = known || s.count_before[b + 1] > kListCap ? b : 0;
     unsigned held = s.count_before[b + 1] - s.count_before[from];
     uint64_t mask = 0, value = 0;
     start = s.mass_before[from];
@@ -940,6 +948,11 @@ __device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target
       uint64_t past = 0;
 #pragma unroll 1
       while (held > kListCap) {
+        const int skip = filled_bits<T>(top);
+        top -= skip;
+        const uint64_t filled = ((uint64_t(1) << skip) - 1) << top;
+        mask |= filled;
+        if (!(value >> (kKeyBits - 1) & 1)) value |= filled;
         const int shift = top > kDigitBits ? top - kDigitBits : 0;
         ask<T>(kOpDigits, w, b, b + 1, mask, value, shift);
         add_up_bins();
@@ -973,7 +986,7 @@ __device__ __forceinline__ void search_bin(int b, bool by_count, uint64_t target
     __syncthreads();
     prepare_pile<false>();
   }
-  search_pile<false>(by_count, target);
+  search_pile<T, false>(by_count, target);
   if (threadIdx.x == 0) s.found_mass += start;
 }
 
@@ -1006,7 +1019,7 @@ __device__ __forceinline__ bool search_tail(bool by_count, uint64_t target, bool
           also_to = min(bins[1] + 1, b);
         }
       }
-      search_bin<T>(b, by_count, t, also, also_to);
+      search_bin<T>(b, by_count, t, ahead && w == 0, also, also_to);
       if (threadIdx.x == 0) s.found_mass = done + (s.found_mass >> (kOctaves * w));
       __syncthreads();
       return true;
@@ -1212,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
       if (target != ~uint64_t(0)) {
         if (!in_head) found = search_tail<T>(step == 0, target, step == 1, unit);
         if (!found && (in_head || (step && listed))) {
-          search_pile<true>(step == 0, in_head ? target : head_mass - 1);
+          search_pile<T, true>(step == 0, in_head ? target : head_mass - 1);
           in_head = found = true;
         }
       }
