@@ -383,7 +383,7 @@ __device__ __forceinline__ void fill_bins(const Scale& scale, int base, F look, 
   Shared& s = own();
   uint64_t tail = 0;
   if constexpr (sizeof(T) == 4) {
-    each_vector<T, 4>([&](const Raw<T, kVec>& raw, int i) -> bool {
+    each_vector<T, 3>([&](const Raw<T, kVec>& raw, int i) -> bool {
       Vec<T, kVec> v;
       v.set_raw(raw);
       const unsigned one[kVec] = {1, 1, 1, 1};
@@ -391,7 +391,7 @@ __device__ __forceinline__ void fill_bins(const Scale& scale, int base, F look, 
       return look(raw, i);
     }, note);
   } else {
-    each_vector<T, 8>([&](const Raw<T, kVec>& raw, int i) -> bool {
+    each_vector<T, 2>([&](const Raw<T, kVec>& raw, int i) -> bool {
       const uint32_t w[4] = {raw.u.x, raw.u.y, raw.u.z, raw.u.w};
       uint32_t a[4], low = 0xffffffffu, high = 0;  // without signs, two a word
 #pragma unroll
@@ -555,7 +555,7 @@ __device__ __noinline__ void serve() {
     if (threadIdx.x == 0) s.few = 0;
     __syncthreads();
     if constexpr (sizeof(T) == 4) {
-      each_vector<T, 8>([&](const Raw<T, kVec>& raw, int) {
+      each_vector<T, 2>([&](const Raw<T, kVec>& raw, int) {
         Vec<T, kVec> v;
         v.set_raw(raw);
         bool near = false;
@@ -567,7 +567,7 @@ __device__ __noinline__ void serve() {
       // (rounded down and up: a bf16 value is within the one bounds if it is within the others, but for some more at the ends)
       const __nv_bfloat162 low2 = __bfloat162bfloat162(__float2bfloat16_rd(low)), high2 = __bfloat162bfloat162(__float2bfloat16_ru(high));
       const __nv_bfloat162 other_low2 = __bfloat162bfloat162(__float2bfloat16_rd(other_low)), other_high2 = __bfloat162bfloat162(__float2bfloat16_ru(other_high));
-      each_vector<T, 8>([&](const Raw<T, kVec>& raw, int) {
+      each_vector<T, 2>([&](const Raw<T, kVec>& raw, int) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw.u);
         unsigned near = 0;
 #pragma unroll
@@ -823,7 +823,7 @@ struct Unit {
 };
 
 template <typename T>
-__device__ __forceinline__ void ask(int op, int w, int from, int to, uint64_t mask, uint64_t value, int shift, int from2 = 0, int to2 = 0) {
+__device__ __noinline__ void ask(int op, int w, int from, int to, uint64_t mask, uint64_t value, int shift, int from2 = 0, int to2 = 0) {
   Shared& s = own();
   if (threadIdx.x == 0) {
     // a hundredth of a bin is left at either end, and room for the differences' rounding
