@@ -12,10 +12,11 @@
 // least score and writes the new row over it.
 //
 // One GB300, inputs changing between calls: 8 heads x 32768 positions x 128 queries bf16,
-// 4096 kept of 128 + 128 values (102 MB): 44 us, of which the sums take about
-// 20 (91 instructions for each 8 values a lane: the pairs' additions are what bounds them), the
-// choice 10, the rows 8.  Replacing one of 4096 slots in 512 heads, four bf16 weights a
-// slot (51 MB): 15.7 us; in 8 heads of 2048: 6.3 us, launch and barriers.
+// 4096 kept of 128 + 128 values (102 MB): 36.5 us, of which the sums take 17 (67 MB), the
+// choice 11 (eight barriers of a cluster and the scans between them), the rows 6 (34 MB); 48 heads x 5001 f32, up to 1021
+// rows of 72 + 72 kept: 26.5 us, of which the rows 9 (56 MB).  Replacing one of 4096 slots in 512 heads, four bf16 weights a
+// slot (51 MB): 16 us; in 8 heads of 2048: 4.5 us, launch and barriers.  (Blocks of
+// 256 threads, four an SM, so that 512 heads run at once: with 512, two an SM, 19 us instead of 16.)
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -106,7 +107,8 @@ struct Places {
   }
 };
 
-// A block: 32 pieces of positions of one head, the head's query rows dealt to its warps, kAhead of them under way.
+// A block: 32 pieces of positions of one head, the head's query rows dealt to its warps, kAhead of them under way.  (Four
+// blocks an SM with eight rows each under way: two with sixteen took 41.5 us instead of 38.5 for evict as a whole, six with four 42.)
 template <typename T, int VEC, int kAhead>
 __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const WeightSums p) {
   using P = Places<T, VEC>;

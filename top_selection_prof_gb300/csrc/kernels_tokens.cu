@@ -25,11 +25,15 @@
 // like a tail.
 //
 // One GB300, inputs changing between calls: 256 x 131072 f32 with a top_k of 200
-// 48 us (134 MB: the pass over the rows takes 28 of them, 4.8 TB/s, what is before and after it is
-// latency: the sample 4, the searches 10); 96 x 131072 bf16, nucleus of 0.9, 66 us (the pass 18, of
-// which the values' weights 7, two searches in the tail 14 each); 37 x 100003 f32 without filters 36 us; 1 x 65536 13 us.
+// 38 us (134 MB: the pass over the rows takes 23 of them, 5.8 TB/s, what a plain read of them takes too; what is before
+// and after it is latency: the sample 4, the searches 10); 96 x 131072 bf16, nucleus of 0.9, 50 us (the pass
+// 14, of which the values' weights 6, the search of the nucleus's end 13, of the token 4); 37 x 100003 f32
+// without filters 33 us; 1 x 65536 12 us.
+// What is once over a row is bound by instructions that are run once and fetched for it: short loops took
+// less than unrolled ones all through the searches (62 -> 50 us for the nucleus).
 // 256 threads of 128 registers, two blocks an SM: with 512 of 64 the searches' state went through
-// the 28 KB of L1 that the shared memory leaves, and every step took 1.6 times as long.
+// the L1, and every step took 1.6 times as long.  99 KB of shared memory a block at most: from there on 28 KB of L1 are
+// left instead of 60, too few for the loads under way (the first case 48 us instead of 41).
 #include <cfloat>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -202,6 +206,7 @@ struct Shared {
   float top_p, u;
   int listed;                            // whether the head is (else all is the tail)
 };
+static_assert(sizeof(Shared) <= 99328, "two blocks leave 60 KB of L1");
 // The block's own.  (Not handed down as a reference: the compiler has to see that it is shared memory.)
 __device__ __forceinline__ Shared& own() {
   extern __shared__ __align__(16) unsigned char smem[];
