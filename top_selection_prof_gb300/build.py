@@ -70,7 +70,7 @@ def _link_calls(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = CALLS + ".tmp"
-    _run([shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + os.path.basename(LIB), "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+    _run([shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + os.path.basename(LIB), "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10",
           "-Wl,-rpath,$ORIGIN"], "link failed for the Python module")
     os.replace(tmp, CALLS)
 

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cstdarg>
@@ -136,8 +137,9 @@ class Launch {
   c10::cuda::CUDAGuard guard_;
   PyThreadState* state_;
 };
+// (torch's own allocation without the dispatcher, which takes as long again)
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType dtype, const at::Device& device) {
-  return at::empty(sizes, at::TensorOptions().dtype(dtype).device(device));
+  return at::Tensor(at::detail::empty_cuda(sizes, dtype, device, std::nullopt));
 }
 void* stream_of(const at::Device& device) { return c10::cuda::getCurrentCUDAStream(device.index()).stream(); }
 
