@@ -10,8 +10,8 @@
 // One GB300, inputs changing between calls: dispatch of 8192 x 8 rows of 2048
 // bf16 (302 MB) 52 us, 5.8 TB/s: the rows 44 us, counts and ranks before them
 // the rest; combine of them 51 us, 5.9 TB/s; their gradients (604 MB less the
-// rows read twice) 120 us; the gradients of 4093 x 6 rows of 1001 f32, none on a
-// 16-byte boundary, 52 us (a 213 MB case whose scalar loads and stores bound it).
+// rows read twice) 104 us; the gradients of 4093 x 6 rows of 1001 f32, none on a
+// 16-byte boundary, 47 us (a 213 MB case whose scalar loads and stores bound it).
 // 16 x 4 rows of 4096 bf16 are dispatched in 4.2 us by one launch.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* p
   if (r >= 0 && r < rows) atomicAdd(&listed[r], 1u);
 }
 
-// Four rows of a token together: with eight, 128 registers left 16 warps an SM (136 us instead of 120 for 8192 x 8 rows of 2048
-// bf16, 59 instead of 52 for the odd f32 ones); with two, 133 and 52.
+// Four rows of a token together: with eight, 128 registers left 16 warps an SM (with one piece a thread 136 us instead of 120 for
+// 8192 x 8 rows of 2048 bf16, 59 instead of 52 for the odd f32 ones); with two, 133 and 52.
 //
 // Blocks of tokens, `share` threads each (32 or more): what a place's row gets where no other place lists it, and the products
 // that are the weights' gradients.  Behind them blocks of rows: zeros for rows that no place lists, and the sums, in order
@@ -585,7 +585,9 @@ JoinRows join_of(const Combine& p) {
 template <typename T, int VEC>
 cudaError_t backward(const Combine& p, Scratch& sc, cudaStream_t st) {
   JoinRows q = join_of(p);
-  const int share = share_of(p.d, VEC > 1 ? VEC : 4);
+  // (four pieces a thread: what a token costs beside them, its places and the sums over its threads, counts less.  With one piece
+  // 120 us instead of 104 for 8192 x 8 rows of 2048 bf16 and 75 instead of 68 for 4093 x 6 of 2001; with eight 111 and 72.)
+  const int share = share_of(p.d, 4 * (VEC > 1 ? VEC : 4));
   int64_t token_blocks = blocks_of(p.tokens, share);
   const int64_t total = p.tokens * p.k;
   static PerDevice known;
