@@ -9,7 +9,7 @@
 //
 // One GB300, inputs changing between calls: dispatch of 8192 x 8 rows of 2048
 // bf16 (302 MB) 52 us, 5.8 TB/s: the rows 44 us, counts and ranks before them
-// the rest; combine of them 51 us, 5.9 TB/s; their gradients (604 MB less the
+// the rest; combine of them 49 us, 6.2 TB/s; their gradients (604 MB less the
 // rows read twice) 104 us; the gradients of 4093 x 6 rows of 1001 f32, none on a
 // 16-byte boundary, 47 us (a 213 MB case whose scalar loads and stores bound it).
 // 16 x 4 rows of 4096 bf16 are dispatched in 4.2 us by one launch.
@@ -627,7 +627,9 @@ cudaError_t launch_dispatch(const Dispatch& p, Scratch& sc, cudaStream_t st) {
 
 template <typename T, int VEC>
 static cudaError_t forward(const Combine& p, cudaStream_t st) {
-  const int share = share_of(p.d, 16 / static_cast<int>(sizeof(T)));
+  // (two pieces a thread: 49 us instead of 51 for 8192 x 8 rows of 2048 bf16, 22 instead of 23.5 for 4093 x 6 of 1001 f32; dispatch, which
+  // writes k rows for each it reads, takes 57 us with two and 53 with one)
+  const int share = share_of(p.d, 2 * 16 / static_cast<int>(sizeof(T)));
   return launch_after(combine_kernel<T, VEC>, static_cast<unsigned>(blocks_of(p.tokens, share)), kThreads, 0, st, join_of(p), share);
 }
 
