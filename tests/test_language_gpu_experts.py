@@ -62,6 +62,13 @@ def test_dispatch(tk, tokens, k, experts, d, dtype):
         check_dispatch(tk, x, routed(tokens, k, experts, tokens + k, dropped), experts)
 
 
+@pytest.mark.parametrize("experts", [1, 31, 32, 318, 319, 320, 321, 511, 1024, 4096])
+@pytest.mark.parametrize("tokens,k", [(513, 2), (1024, 1), (1025, 1), (40_000, 4)])
+def test_dispatch_around_the_ranks_limits(tk, tokens, k, experts):
+    x = torch.randn(tokens, 8, generator=gen(experts)).cuda()
+    check_dispatch(tk, x, routed(tokens, k, experts, experts), experts)
+
+
 def test_dispatch_of_one_expert_and_of_strided_rows(tk):
     for dtype in DTYPES:
         big = torch.randn(3000, 150, generator=gen(1)).to(dtype).cuda()

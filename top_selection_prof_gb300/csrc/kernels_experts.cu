@@ -8,7 +8,7 @@
 // written once, and the rows by expert once.
 //
 // One GB300, inputs changing between calls: dispatch of 8192 x 8 rows of 2048
-// bf16 (302 MB) 52 us, 5.8 TB/s: the rows 44 us, counts and ranks before them
+// bf16 (302 MB) 51.5 us, 5.9 TB/s: the rows 44 us, counts and ranks before them
 // the rest; combine of them 49 us, 6.2 TB/s; their gradients (604 MB less the
 // rows read twice) 104 us; the gradients of 4093 x 6 rows of 1001 f32, none on a
 // 16-byte boundary, 47 us (a 213 MB case whose scalar loads and stores bound it).
@@ -22,8 +22,10 @@ namespace tk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kByWarp = 512;       // experts (and one) that are counted by warp
+// (1024 threads that rank: dispatch of 65536 places 52.5 us in a graph, 56 with 512)
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kByWarp = 320;       // experts (and one) that are counted by warp: as many as 48 KB hold
+static_assert((2 + kSortWarps) * kByWarp * sizeof(unsigned) < 48 * 1024 - 256, "the counts fit without more being asked for");
 constexpr int kFewPlaces = 1024;   // places that every block ranks for itself
 
 // The expert of place s; `experts` where it has none.
