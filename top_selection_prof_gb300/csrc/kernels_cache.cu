@@ -532,10 +532,10 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
   }
 }
 
-// Blocks of a cluster a head: more where heads are few, down to `least` positions each.
-int blocks_for(int64_t rows, int64_t positions, int64_t least) {
+// Blocks of a cluster a head: more where heads are few, `on_sm` on each SM, down to `least` positions each.
+int blocks_for(int64_t rows, int64_t positions, int64_t least, int on_sm) {
   int blocks = 1;
-  while (blocks < kMostBlocks && rows * blocks * 2 <= 2 * ops_sm_count() && positions > blocks * least) blocks *= 2;
+  while (blocks < kMostBlocks && rows * blocks * 2 <= on_sm * ops_sm_count() && positions > blocks * least) blocks *= 2;
   return blocks;
 }
 
@@ -614,7 +614,7 @@ cudaError_t launch_evict(const Evict& p, Scratch& sc, cudaStream_t st) {
     c.ld = p.capacity;
   }
   const int64_t rows = p.batch * p.heads;
-  const int blocks = blocks_for(rows, p.capacity, 2048);
+  const int blocks = blocks_for(rows, p.capacity, 2048, 2);
   // positions a thread: in registers up to 16
   const int64_t each = (p.capacity + int64_t(blocks) * kThreads - 1) / (int64_t(blocks) * kThreads);
   cudaError_t e = launch_clusters(each <= 4 ? choice_kernel<4> : each <= 8 ? choice_kernel<8> : each <= 16 ? choice_kernel<16> : choice_kernel<0>, c, rows, blocks, kThreads, st);
@@ -628,8 +628,8 @@ static cudaError_t replace_by(const Replace& p, cudaStream_t st) {
   const int64_t rows = p.batch * p.heads;
   auto on = [](const View& v, int64_t size) { return aligned_view(View{v.data, v.batch, v.head, 0}, size); };
   const bool wide = p.capacity % kVec == 0 && on(p.score, 4) && on(p.positions, 8) && (!p.weights.data || aligned_view(p.weights, sizeof(W)));
-  if (wide) return launch_clusters(replace_kernel<W, kVec>, p, rows, blocks_for(rows, p.capacity, 2048), kReplaceThreads, st);
-  return launch_clusters(replace_kernel<W, 1>, p, rows, blocks_for(rows, p.capacity, 512), kReplaceThreads, st);
+  if (wide) return launch_clusters(replace_kernel<W, kVec>, p, rows, blocks_for(rows, p.capacity, 2048, 4), kReplaceThreads, st);
+  return launch_clusters(replace_kernel<W, 1>, p, rows, blocks_for(rows, p.capacity, 512, 4), kReplaceThreads, st);
 }
 
 cudaError_t launch_replace(const Replace& p, cudaStream_t st) {
