@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kept_kernel(const MoveKept 
 
 // ---- one token ----------------------------------------------------------------------
 // A cluster a head: adds the group's weights to the scores, finds the slot and writes the token there.  A thread holds WIDE slots
-// side by side, whose weights, score and positions are all under way at once; where rows are not on 16-byte boundaries, one.
+// side by side, whose weights, score and positions are all under way at once; where rows are not on 16-byte boundaries, four that
+// lie a block's width apart.
 constexpr int kReplaceThreads = 256, kReplaceWarps = kReplaceThreads / 32;
 template <typename W, int WIDE>
 __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Replace p) {
@@ -437,9 +438,11 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
   const bool even = p.weights.head == p.queries * p.weights.row;  // (a group's rows as far apart as a head's own)
   const bool full = seen >= p.capacity;
   uint64_t least = ~uint64_t(0);  // (score, slot) of the least that may go
-  for (int64_t i = (int64_t(rank) * kReplaceThreads + threadIdx.x) * WIDE; i < len; i += int64_t(blocks) * kReplaceThreads * WIDE) {
+  constexpr int kHeld = WIDE > 1 ? WIDE : 4;
+  auto slot_of = [](int64_t i, int e) { return WIDE > 1 ? i + e : i + e * kReplaceThreads; };
+  for (int64_t i = int64_t(rank) * kReplaceThreads * kHeld + threadIdx.x * WIDE; i < len; i += int64_t(blocks) * kReplaceThreads * kHeld) {
     // (a run's slots behind `len` are read, not written: they lie within the capacity)
-    Sum2 sum[WIDE];
+    Sum2 sum[kHeld];
     unsigned may = full && p.recent == 0 ? ~0u : 0;  // slots that may go
     if constexpr (WIDE > 1) {
 #pragma unroll
@@ -448,7 +451,8 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
         sum[e].hi = v.x, sum[e + 1].hi = v.y, sum[e + 2].hi = v.z, sum[e + 3].hi = v.w;
       }
     } else {
-      sum[0].hi = score[i];
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) sum[e].hi = slot_of(i, e) < len ? score[slot_of(i, e)] : 0.0f;
     }
     if (full && p.recent > 0) {
       if constexpr (WIDE > 1) {
@@ -458,32 +462,40 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
           may |= (v.x < seen - p.recent ? 1u << e : 0) | (v.y < seen - p.recent ? 2u << e : 0);
         }
       } else {
-        may = positions[i] < seen - p.recent;
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) may |= slot_of(i, e) < len && positions[slot_of(i, e)] < seen - p.recent ? 1u << e : 0;
       }
     }
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 4, kParts = WIDE > 1 ? 1 : kHeld;
     for (int r0 = 0; r0 < n; r0 += kAhead) {
-      Raw<W, WIDE> v[kAhead];
+      Raw<W, WIDE> v[kAhead][kParts];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         const int r = r0 + a, g = even ? 0 : r / queries;
-        v[a].clear();
-        if (r < n) v[a].load_nc(weights + g * p.weights.head + (r - g * queries) * p.weights.row + i);
+        const W* row = weights + g * p.weights.head + (r - g * queries) * p.weights.row;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          v[a][q].clear();
+          if (r < n && slot_of(i, q) < len) v[a][q].load_nc(row + slot_of(i, q));
+        }
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        Vec<W, WIDE> x;
-        x.set_raw(v[a]);
 #pragma unroll
-        for (int e = 0; e < WIDE; ++e) sum[e].add(counted(x.v[e]));
+        for (int q = 0; q < kParts; ++q) {
+          Vec<W, WIDE> x;
+          x.set_raw(v[a][q]);
+#pragma unroll
+          for (int e = 0; e < WIDE; ++e) sum[q + e].add(counted(x.v[e]));
+        }
       }
     }
-    float value[WIDE];
+    float value[kHeld];
 #pragma unroll
-    for (int e = 0; e < WIDE; ++e) {
+    for (int e = 0; e < kHeld; ++e) {
       value[e] = sum[e].value();
-      if (may >> e & 1)
-        least = min(least, static_cast<uint64_t>(order_key_f32(__float_as_uint(value[e]))) << 32 | static_cast<uint32_t>(i + e));
+      if (may >> e & 1 && (WIDE > 1 || slot_of(i, e) < len))
+        least = min(least, static_cast<uint64_t>(order_key_f32(__float_as_uint(value[e]))) << 32 | static_cast<uint32_t>(slot_of(i, e)));
     }
     if (n) {
       if (WIDE > 1 && i + WIDE <= len) {
@@ -493,8 +505,8 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < WIDE; ++e)
-          if (i + e < len) score[i + e] = value[e];
+        for (int e = 0; e < kHeld; ++e)
+          if (slot_of(i, e) < len) score[slot_of(i, e)] = value[e];
       }
     }
   }
