@@ -113,6 +113,13 @@ def test_evict(tk, batch, heads, group, queries, n, kd, vd, keep, recent, dtype)
     check_evict(tk, case(batch, heads, group, queries, n, kd, vd, dtype, n), keep, recent)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [7, 31, 32, 33, 63, 64, 65, 80, 127, 128, 129, 136])
+@pytest.mark.parametrize("group,queries", [(8, 60), (1, 33), (3, 1)])
+def test_evict_of_few_positions(tk, n, group, queries, dtype):
+    check_evict(tk, case(3, 2, group, queries, n, 16, 8, dtype, n + queries), max(1, n // 2), n // 8)
+
+
 @pytest.mark.parametrize("wdtype", DTYPES)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", [1000, 9001])

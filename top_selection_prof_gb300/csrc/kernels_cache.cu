@@ -63,7 +63,7 @@ struct WeightSums {
   const int64_t* lengths;
   float* out;         // batch x heads x capacity
 };
-constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32, kFewLanes = 8;
 
 // Two sums of two f32 each, side by side.
 struct Sum2Pair {
@@ -85,12 +85,12 @@ struct Sum2Pair {
   }
 };
 
-// What a thread holds of 32 VEC (or 32 x 4) positions: 16 bytes side by side, or four values 32 apart.
-template <typename T, int VEC>
+// What one of LANES threads holds of LANES x VEC (or LANES x 4) positions: 16 bytes side by side, or four values LANES apart.
+template <typename T, int VEC, int LANES>
 struct Places {
   static constexpr int kWide = VEC > 1 ? VEC : 4;
   Raw<T, VEC> r[VEC > 1 ? 1 : kWide];
-  __device__ __forceinline__ static int at(int lane, int e) { return VEC > 1 ? lane * VEC + e : e * 32 + lane; }
+  __device__ __forceinline__ static int at(int lane, int e) { return VEC > 1 ? lane * VEC + e : e * LANES + lane; }
   // (positions behind `left`, which no sum is taken of, are read at the row's start; the last vector of a row may reach past its
   // length, not past the capacity)
   __device__ __forceinline__ static void offsets(int* off, int lane, int64_t left) {
@@ -107,44 +107,45 @@ struct Places {
   }
 };
 
-// A block: 32 pieces of positions of one head, the head's query rows dealt to its warps, kAhead of them under way.  (Four
-// blocks an SM with eight rows each under way: two with sixteen took 41.5 us instead of 38.5 for evict as a whole, six with four 42.)
-template <typename T, int VEC, int kAhead>
+// A block: LANES pieces of positions of one head, the head's query rows dealt to its groups of LANES threads (a warp; eight where there
+// are few positions: 294 heads x 80 positions x 480 queries bf16 42 -> 25 us for evict), kAhead of them under way.  (Four blocks an SM with eight rows
+// each under way: two with sixteen took 41.5 us instead of 38.5 for evict as a whole, six with four 42.)
+template <typename T, int VEC, int kAhead, int LANES = 32>
 __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const WeightSums p) {
-  using P = Places<T, VEC>;
-  constexpr int kWide = P::kWide;
-  __shared__ float2 part[kSumWarps][32 * kWide];
+  using P = Places<T, VEC, LANES>;
+  constexpr int kWide = P::kWide, kGroups = kSumThreads / LANES;
+  __shared__ float2 part[kGroups][LANES * kWide];
   grid_dependency_wait();
   grid_launch_dependents();
   const unsigned bh = blockIdx.x / p.chunks, b = bh / p.heads, h = bh % p.heads;
-  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = int64_t(blockIdx.x - bh * p.chunks) * 32 * kWide;
+  const int64_t len = clamped(p.lengths[b], p.capacity), at0 = int64_t(blockIdx.x - bh * p.chunks) * LANES * kWide;
   if (at0 >= len) return;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   Sum2Pair sum[kWide / 2];
   const int n = static_cast<int>(p.group * p.queries), queries = static_cast<int>(p.queries);
   const T* base = static_cast<const T*>(p.weights.data) + b * p.weights.batch + h * p.group * p.weights.head + at0;
-  static_assert(32 * kWide <= kSumThreads, "a position a thread at the end");
-  const bool sums = threadIdx.x < 32 * kWide && at0 + threadIdx.x < len;
+  static_assert(LANES * kWide <= kSumThreads, "a position a thread at the end");
+  const bool sums = threadIdx.x < LANES * kWide && at0 + threadIdx.x < len;
   const float before = sums ? static_cast<const float*>(p.score.data)[b * p.score.batch + h * p.score.head + at0 + threadIdx.x] : 0.0f;
   int off[VEC > 1 ? 1 : kWide];
   P::offsets(off, lane, len - at0);
   // (a group's rows are mostly as far apart as a head's own)
   const bool even = p.weights.head == p.queries * p.weights.row;
-  const int64_t step = kSumWarps * p.weights.row;
-  const T* row = base + warp * p.weights.row;
-  for (int i0 = warp; i0 < n; i0 += kSumWarps * kAhead) {
+  const int64_t step = kGroups * p.weights.row;
+  const T* row = base + group * p.weights.row;
+  for (int i0 = group; i0 < n; i0 += kGroups * kAhead) {
     P v[kAhead];
-    const bool all = i0 + (kAhead - 1) * kSumWarps < n;
+    const bool all = i0 + (kAhead - 1) * kGroups < n;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a, row += step) {
-      const int i = i0 + a * kSumWarps;
+      const int i = i0 + a * kGroups;
       if (!all && i >= n) break;
       if (!even) row = base + i / queries * p.weights.head + i % queries * p.weights.row;
       v[a].load(row, off);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      if (!all && i0 + a * kSumWarps >= n) break;
+      if (!all && i0 + a * kGroups >= n) break;
 #pragma unroll
       for (int e = 0; e < kWide / 2; ++e) sum[e].add(v[a].pair(e));
     }
@@ -154,8 +155,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const Weigh
     float h0, h1, l0, l1;
     sum[e].hi.get(&h0, &h1);
     sum[e].lo.get(&l0, &l1);
-    part[warp][P::at(lane, 2 * e)] = make_float2(h0, l0);
-    part[warp][P::at(lane, 2 * e + 1)] = make_float2(h1, l1);
+    part[group][P::at(lane, 2 * e)] = make_float2(h0, l0);
+    part[group][P::at(lane, 2 * e + 1)] = make_float2(h1, l1);
   }
   __syncthreads();
   if (!sums) return;
@@ -164,9 +165,9 @@ __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const Weigh
   all.add(before);
   bool number = true;
 #pragma unroll
-  for (int w = 0; w < kSumWarps; ++w) {
-    number = number && part[w][at].x == part[w][at].x;
-    all.add(Sum2{part[w][at].x, part[w][at].y});
+  for (int g = 0; g < kGroups; ++g) {
+    number = number && part[g][at].x == part[g][at].x;
+    all.add(Sum2{part[g][at].x, part[g][at].y});
   }
   if (!number) {  // a weight is NaN, or infinities met: anew, without the NaN ones
     all = Sum2{};
@@ -578,11 +579,16 @@ template <typename T>
 cudaError_t add_weights(const Evict& p, float* out, cudaStream_t st) {
   constexpr int kVec = 16 / sizeof(T);
   const bool wide = aligned_view(p.weights, sizeof(T)) && p.capacity % kVec == 0;
-  const int64_t each = 32 * (wide ? kVec : 4);
+  const int held = wide ? kVec : 4;
+  const bool few = p.capacity <= 16 * held;  // (a warp's threads would mostly have none)
+  const int64_t each = (few ? kFewLanes : 32) * held;
   const int64_t chunks = (p.capacity + each - 1) / each, blocks = chunks * p.batch * p.heads;
   if (blocks > INT32_MAX) return cudaErrorNotSupported;
   const WeightSums w{p.weights, p.group, p.queries, p.capacity, static_cast<unsigned>(p.heads), static_cast<unsigned>(chunks), p.score, p.lengths, out};
   const unsigned grid = static_cast<unsigned>(blocks);
+  if (few)
+    return wide ? launch_after(weight_sums_kernel<T, kVec, 4, kFewLanes>, grid, kSumThreads, 0, st, w)
+                : launch_after(weight_sums_kernel<T, 1, 4, kFewLanes>, grid, kSumThreads, 0, st, w);
   // (few rows a warp: four at a time and more blocks an SM)
   if (p.group * p.queries <= 4 * kSumWarps || !wide)
     return wide ? launch_after(weight_sums_kernel<T, kVec, 4>, grid, kSumThreads, 0, st, w) : launch_after(weight_sums_kernel<T, 1, 4>, grid, kSumThreads, 0, st, w);
