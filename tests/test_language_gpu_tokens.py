@@ -108,6 +108,16 @@ def test_filters(tk, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [300, 2239, 2240, 2241, 2600])
+def test_rows_around_what_one_block_holds(tk, n, dtype):
+    x, u = logits(5, n, dtype, n)
+    x[1, ::3], x[2, :] = -math.inf, x[2, 0].item()
+    for kw in (dict(), dict(top_p=0.9, min_p=0.01), dict(top_k=n - 1), dict(temperature=1e30), dict(temperature=3e38, top_k=n - 1, top_p=0.5),
+               dict(temperature=1e38, top_k=7)):
+        draw(tk, x, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,n", [(1, 131072), (3, 262144), (40, 70001), (170, 12289)])
 def test_sizes(tk, rows, n, dtype):
     x, u = logits(rows, n, dtype, rows)

@@ -1109,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const TokenDraw p, i
   const float temperature = p.temperatures ? p.temperatures[row] : p.temperature;
   const bool greedy = !(temperature > 0.0f);
   const int top_k = greedy ? 1 : p.top_ks ? p.top_ks[row] : p.top_k;
-  const bool rest = !(top_k > 0 && top_k <= head / 4);  // (the tail will hardly matter otherwise)
+  const bool rest = runs > 0 && !(top_k > 0 && top_k <= head / 4);  // (the tail is empty, or will hardly matter, otherwise)
 
   if (rest) clear_bins<T>();
 
