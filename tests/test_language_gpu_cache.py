@@ -242,6 +242,37 @@ def test_replace_where_nothing_may_go_and_not_numbers(tk):
     check_replace(tk, s, 0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [61, 64, 4096, 4097])
+@pytest.mark.parametrize("recent", [0, 1, 7])
+def test_positions_behind_the_length_stay(tk, n, recent, dtype):
+    """A slot whose position is not below lengths - recent is never given up, with recent 0 neither: tokens that were taken back, or
+    slots that are held by a large position."""
+    s = step(4, 2, 2, n, 16, 16, dtype, n)
+    g = gen(n)
+    s["positions"] = torch.argsort(torch.rand(4, 2, 2 * n, generator=g), -1)[..., :n].contiguous()
+    s["lengths"] = torch.tensor([n, n + 5, 2 * n, n])
+    s["positions"][3, 0] += n                                # none of its slots may go
+    s["positions"][3, 1] += n
+    s["positions"][3, 1, n // 2] = n - 1 - recent            # one
+    on = cuda(s)
+    score, want = added(s).float(), torch.empty(4, 2, dtype=torch.int64)
+    for b in range(4):
+        for h in range(2):
+            may = (s["positions"][b, h] < int(s["lengths"][b]) - recent).nonzero()[:, 0]
+            want[b, h] = may[score[b, h, may].sort(stable=True).indices[0]] if may.numel() else -1
+    assert want[3].tolist() == [-1, n // 2]
+    got = tk.replace_(*(on[k] for k in ("keys", "values", "score", "positions", "lengths", "key", "value")), recent=recent, weights=on["weights"])
+    assert torch.equal(got.cpu(), want)
+    for b in range(4):
+        for h in range(2):
+            slot = int(want[b, h])
+            if slot >= 0:
+                s["keys"][b, h, slot], s["values"][b, h, slot] = s["key"][b, h], s["value"][b, h]
+                score[b, h, slot], s["positions"][b, h, slot] = 0.0, s["lengths"][b]
+    assert torch.equal(on["score"].cpu(), score) and all(torch.equal(on[k].cpu(), s[k]) for k in ("keys", "values", "positions"))
+
+
 def test_replace_in_one_buffer(tk):
     s = step(3, 4, 2, 64, 32, 32, torch.bfloat16, 6)
     on = cuda(s)

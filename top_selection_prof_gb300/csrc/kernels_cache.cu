@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
   for (int64_t i = int64_t(rank) * kReplaceThreads * kHeld + threadIdx.x * WIDE; i < len; i += int64_t(blocks) * kReplaceThreads * kHeld) {
     // (a run's slots behind `len` are read, not written: they lie within the capacity)
     Sum2 sum[kHeld];
-    unsigned may = full && p.recent == 0 ? ~0u : 0;  // slots that may go
+    unsigned may = 0;  // slots that may go
     if constexpr (WIDE > 1) {
 #pragma unroll
       for (int e = 0; e < WIDE; e += 4) {
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
 #pragma unroll
       for (int e = 0; e < kHeld; ++e) sum[e].hi = slot_of(i, e) < len ? score[slot_of(i, e)] : 0.0f;
     }
-    if (full && p.recent > 0) {
+    if (full) {  // (with recent == 0 too: a slot's position may lie behind the length, of a token that was taken back)
       if constexpr (WIDE > 1) {
 #pragma unroll
         for (int e = 0; e < WIDE; e += 2) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
 #pragma unroll
     for (int e = 0; e < kHeld; ++e) {
       value[e] = sum[e].value();
-      if (may >> e & 1 && (WIDE > 1 || slot_of(i, e) < len))
+      if (may >> e & 1)
         least = min(least, static_cast<uint64_t>(order_key_f32(__float_as_uint(value[e]))) << 32 | static_cast<uint32_t>(slot_of(i, e)));
     }
     if (n) {

@@ -108,7 +108,7 @@ def replace_(keys, values, score, positions, lengths, key, value, recent: int = 
     """Puts one new token into each sequence's cache, in place; returns the slots (batch, heads) that it took.
 
     lengths (batch,): tokens before it.  While there are fewer than slots it takes the next one; then the one whose
-    score is least, of those that hold positions before the last `recent` (equal ones: the lowest slot).  key, value
-    (batch, heads, dim); positions (batch, heads, capacity), int64: the position in each slot; weights as in evict, by slot,
+    score is least, of those whose position is below lengths - recent (equal ones: the lowest slot; none: slot -1, and
+    nothing is stored).  key, value (batch, heads, dim); positions (batch, heads, capacity), int64: the position in each slot; weights as in evict, by slot,
     added to the scores first.  The slot's score becomes 0.  lengths is not changed."""
     return _call("replace", stream, keys, values, score, positions, lengths, key, value, recent, weights)
