@@ -466,9 +466,11 @@ int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_
  * logarithm of its share of that.  A temperature of 0 takes the largest logit.
  * NaN and -inf are never drawn; a row of nothing else gives -1 and -inf.
  * Where a logit is +inf, only such are drawn.
- *   Weights are formed to 30 bits and their sums are exact, so the token is that
- * of 64-bit arithmetic unless u[r] (or a filter's border) is within about 2^-29
- * of the edge between two; weights below 2^-48 of the largest count as 0.
+ *   Weights are formed to 30 bits and added up as whole numbers, the largest as
+ * 2^45 (what is less than 1 is dropped, from each of the up to some thousand
+ * largest tokens and from the others' sum), so the token is that of 64-bit
+ * arithmetic unless u[r] (or a filter's border) is within about 2^-29 of the edge
+ * between two; weights below 2^-48 of the largest count as 0.
  *   Each of temperature, top_k, top_p and min_p is a number, or one a row
  * (device, `rows` values) where its pointer is not null, the number then
  * being ignored; numbers are rounded to f32.  A row's temperature that is not

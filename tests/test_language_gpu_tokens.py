@@ -162,6 +162,21 @@ def test_deep_tails(tk, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_deep_head_counts_towards_top_k(tk, dtype):
+    """All tokens but one lie 45 to 48 octaves below the likeliest: they weigh next to nothing, and are the first top_k all the same.
+    (With u = 1 the last that is kept, to EDGE, may be any that is kept, and none that is not.)"""
+    n = 5000
+    g = torch.Generator().manual_seed(15)
+    x = -math.log(2.0) * (45.05 + 2.9 * torch.rand(6, n, generator=g))
+    x[torch.arange(6), torch.randint(0, n, (6,), generator=g)] = 0.0
+    x = x.to(dtype).cuda()
+    for u in (1.0, 1 - 2.0 ** -24, 0.5):
+        for top_k in (2, 40, 300, 1500, 4000):
+            draw(tk, x, torch.full((6,), u, device="cuda"), top_k=top_k)
+            draw(tk, x, torch.full((6,), u, device="cuda"), top_k=torch.full((6,), top_k, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_masked_rows(tk, dtype):
     """-inf, NaN and the type's lowest value in masked places, rows with one token or none left, infinities."""
     n = 5003

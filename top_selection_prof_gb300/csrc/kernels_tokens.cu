@@ -625,12 +625,14 @@ __device__ __noinline__ void serve() {
 }
 
 // ---- the first block's searches: every thread of the block calls them -----------------
-// A token's mass in units of the window that begins kOctaves x window octaves down: 2^45 for its largest weight.  0: none.
-__device__ __forceinline__ uint64_t mass_of(uint64_t key, const Scale& scale, int window, const unsigned* middle) {
+// A token's mass in units of the window that begins kOctaves x window octaves down: 2^45 for its largest weight (a token of the
+// head that weighs less than one unit has none, and is one of its tokens all the same).  False: it has no weight.
+__device__ __forceinline__ bool mass_of(uint64_t key, const Scale& scale, int window, const unsigned* middle, uint64_t* mass) {
   const float x = value_of(key);
   float t;
   const int j = bin_of(x, scale, &t);
-  return j < 0 ? 0 : (static_cast<uint64_t>(weight_in(x, j, t, scale, middle)) << (kOctaves - 1)) >> (j / kSub - kOctaves * window);
+  *mass = j < 0 ? 0 : (static_cast<uint64_t>(weight_in(x, j, t, scale, middle)) << (kOctaves - 1)) >> (j / kSub - kOctaves * window);
+  return j >= 0;
 }
 __device__ __forceinline__ int digit_of(uint64_t key, int at) {
   return kDigits - 1 - static_cast<int>((key >> at) & (kDigits - 1));
@@ -653,7 +655,7 @@ __device__ __forceinline__ uint64_t digit_mass(int d) {
   return s.low[d] + (static_cast<uint64_t>(s.low[kDigits + d]) << 15) + (static_cast<uint64_t>(s.high[d]) << 30);
 }
 
-// The masses of a pile's tokens, and their sums by the first digit.
+// The masses of a pile's tokens, and their sums by the first digit.  (A token without weight gets the key 0, which is no value's.)
 template <bool HEAD>
 __device__ __forceinline__ void prepare_pile() {
   Shared& s = own();
@@ -667,10 +669,13 @@ __device__ __forceinline__ void prepare_pile() {
   if (threadIdx.x < 4) s.bits[threadIdx.x] = 0;
 #pragma unroll 1
   for (unsigned i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t key = p.key[i], m = mass_of(key, scale, window, s.middle);
+    const uint64_t key = p.key[i];
+    uint64_t m;
+    const bool weighs = mass_of(key, scale, window, s.middle, &m);
     p.mass[i] = m;
-    any |= m ? key : 0;
-    none |= m ? ~key : 0;
+    if (!weighs) p.key[i] = 0;
+    any |= weighs ? key : 0;
+    none |= weighs ? ~key : 0;
   }
   const unsigned b0 = __reduce_or_sync(~0u, static_cast<unsigned>(any)), b1 = __reduce_or_sync(~0u, static_cast<unsigned>(any >> 32));
   const unsigned b2 = __reduce_or_sync(~0u, static_cast<unsigned>(none)), b3 = __reduce_or_sync(~0u, static_cast<unsigned>(none >> 32));
@@ -682,8 +687,8 @@ __device__ __forceinline__ void prepare_pile() {
   const int top = 64 - __clzll(static_cast<long long>(differ)), shift = top > kDigitBits ? top - kDigitBits : 0;
 #pragma unroll 1
   for (unsigned i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t m = p.mass[i];
-    if (m) add_digit(digit_of(p.key[i], shift), m);
+    const uint64_t key = p.key[i];
+    if (key) add_digit(digit_of(key, shift), p.mass[i]);
   }
   __syncthreads();
   const int d = 2 * threadIdx.x;
@@ -742,7 +747,7 @@ __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
 #pragma unroll 1
     for (unsigned i = threadIdx.x; i < n; i += kThreads) {
       const uint64_t m = p.mass[i], key = p.key[i];
-      if (m && key >> at == prefix) add_digit(digit_of(key, next), m);
+      if (key && key >> at == prefix) add_digit(digit_of(key, next), m);
     }
     __syncthreads();
     const int d = 2 * threadIdx.x;
@@ -770,7 +775,7 @@ __device__ __forceinline__ void search_pile(bool by_count, uint64_t target) {
 #pragma unroll 1
   for (unsigned i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t m = p.mass[i], key = p.key[i];
-    if (m && key >> at == prefix) {
+    if (key && key >> at == prefix) {
       const unsigned f = atomicAdd(&s.few, 1u);
       if (f < 32) {
         s.few_key[f] = key;
