@@ -538,7 +538,9 @@ typedef struct {
  *     queries rows of capacity values of weights_dtype; query heads h group
  *     ... h group + group - 1 read head h.  A weight that is NaN (a query
  *     whose mask left nothing) counts as 0; behind lengths[b] none is read for
- *     its value.  The sum is exact to f32's rounding; score is not changed.
+ *     its value.  The sum is rounded to f32 once and off by at most (rows + 32)
+ *     2^-45 of the magnitudes' sum before that, with group queries rows; score
+ *     is not changed.
  * Contiguous results: out_keys and out_values, the rows of what stays, in the
  * order of their positions (batch x heads x keep rows); out_score their score;
  * out_kept their positions; out_lengths[b] = min(lengths[b], keep).  Behind

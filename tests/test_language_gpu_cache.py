@@ -138,6 +138,32 @@ def test_sums_are_exact_to_their_rounding(tk):
     assert float(got[2][0, 0, 5]) == float(torch.tensor(1.0 + 799 * 2.0 ** -25, dtype=torch.float64).float())
 
 
+@pytest.mark.parametrize("op,rows", [("evict", 1 << 18), ("evict", 4096), ("replace", 1 << 16), ("replace", 1 << 14)])
+@pytest.mark.parametrize("n", [63, 70, 72])
+def test_sums_of_many_rows(tk, op, rows, n):
+    """Ones (a row of each thread's, or the score) and rows of 2^-26 with some bits behind, which the sums' second parts would round
+    away as they grow.  A sum of K rows at a time rounds off at most (K + 3) / 2 of 2^-48 of the magnitudes' sum a row, 5.5 with
+    K = 8, and joining 32 parts 8 of them each: (rows + 32) 2^-45 in all, and half a step."""
+    w = (2.0 ** -26 + 2.0 ** -37 * (0.5 + torch.arange(n, dtype=torch.float64) / (2 * n))).float()
+    s = case(1, 1, 8, 0, n, 8, 8, torch.float32, 1)
+    s["score"], s["lengths"] = torch.ones(1, 1, n), torch.tensor([n])
+    on = cuda(s)
+    on["weights"] = w.cuda().expand(1, 8, rows // 8, n).contiguous()
+    ones = 8 if op == "evict" else 0
+    on["weights"].view(rows, n)[:ones] = 1.0
+    want = 1.0 + ones + (rows - ones) * w.double()
+    if op == "evict":
+        got = tk.evict(on["keys"], on["values"], on["score"], on["lengths"], n, weights=on["weights"])[2][0, 0].cpu()
+    else:
+        positions, key, value = torch.arange(n).expand(1, 1, n).contiguous().cuda(), on["keys"][:, :, 0].clone(), on["values"][:, :, 0].clone()
+        slot = tk.replace_(on["keys"], on["values"], on["score"], positions, on["lengths"], key, value, weights=on["weights"])
+        got = on["score"][0, 0].cpu()
+        assert float(got[int(slot)]) == 0.0
+        want[int(slot)] = 0.0
+    bound = 2.0 ** -24 * want + (rows + 32) * 2.0 ** -45 * want
+    assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound.clamp(min=1e-30)).max())
+
+
 def test_scores_and_weights_that_are_not_numbers(tk):
     for dtype in DTYPES:
         s = case(2, 1, 2, 3, 500, 16, 16, dtype, 2)

@@ -1,9 +1,15 @@
 // The positions of a key-value cache that stay, by accumulated attention weight.
 //
 // A head's score is the sum of the attention weights that its queries gave a
-// position, held in f32.  What a call adds is summed in pairs of f32 (the error
-// of each addition kept and added in its turn), so that a score is the exact
-// sum rounded once and the choice does not depend on how the sum was split.
+// position, held in f32.  What a call adds is summed in pairs of f32: the error
+// of each addition is kept in the second, which is brought below the first's
+// last bit again after every few rows.  (Without that it grew with the rows, and
+// what was rounded off it too: 2^14 weights of 2^-26 beside a one were off by two
+// half steps, 2^16 by eight.)  With u = 2^-24, K rows at a time and S the sum of the magnitudes,
+// a row's addition to the second, at most (1 + K) u S, rounds off u of that: (K + 3) / 2 u^2 S
+// a row on average, 5.5 u^2 S at most here, and joining the groups of a block 8 u^2 S each.  So a
+// score is off by half a step and at most (rows + 32) 2^-45 S, and only where scores lie
+// that close can a choice depend on how a sum was split.
 //
 // evict: sums by position over all SMs; the choice, a cluster a head: the score of
 // the last one kept by two or three digits of its key, then the kept positions in
@@ -35,7 +41,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// hi + lo, to about 2^-48.  A value that is not finite ends up in hi alone.
+// hi + lo.  A value that is not finite ends up in hi alone.
 struct Sum2 {
   float hi = 0.0f, lo = 0.0f;
   __device__ __forceinline__ void add(float v) {
@@ -46,6 +52,13 @@ struct Sum2 {
   __device__ __forceinline__ void add(const Sum2& o) {
     add(o.hi);
     lo += o.lo;
+  }
+  // lo to below hi's last bit, after a few additions.
+  __device__ __forceinline__ void settle() {
+    const float s = hi + lo;
+    if (!(fabsf(s) < INFINITY)) return;
+    lo -= s - hi;
+    hi = s;
   }
   __device__ __forceinline__ float value() const { return fabsf(hi) < INFINITY ? hi + lo : hi; }
 };
@@ -81,6 +94,12 @@ struct Sum2Pair {
   __device__ __forceinline__ void add(Pair v) {
     const Pair s = plus(hi, v), b = minus(s, hi);
     lo = plus(lo, plus(minus(hi, minus(s, b)), minus(v, b)));
+    hi = s;
+  }
+  // (an infinity becomes NaN, and its sum is made anew)
+  __device__ __forceinline__ void settle() {
+    const Pair s = plus(hi, lo);
+    lo = minus(lo, minus(s, hi));
     hi = s;
   }
 };
@@ -149,6 +168,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const Weigh
 #pragma unroll
       for (int e = 0; e < kWide / 2; ++e) sum[e].add(v[a].pair(e));
     }
+#pragma unroll
+    for (int e = 0; e < kWide / 2; ++e) sum[e].settle();
   }
 #pragma unroll
   for (int e = 0; e < kWide / 2; ++e) {
@@ -168,11 +189,15 @@ __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const Weigh
   for (int g = 0; g < kGroups; ++g) {
     number = number && part[g][at].x == part[g][at].x;
     all.add(Sum2{part[g][at].x, part[g][at].y});
+    all.settle();
   }
-  if (!number) {  // a weight is NaN, or infinities met: anew, without the NaN ones
+  if (!number) {  // a weight is NaN or infinite: anew, without the NaN ones
     all = Sum2{};
     all.add(before);
-    for (int q = 0; q < n; ++q) all.add(counted(to_f32(base[(q / queries) * p.weights.head + (q % queries) * p.weights.row + at])));
+    for (int q = 0; q < n; ++q) {
+      all.add(counted(to_f32(base[(q / queries) * p.weights.head + (q % queries) * p.weights.row + at])));
+      all.settle();
+    }
   }
   p.out[int64_t(bh) * p.capacity + at0 + at] = all.value();
 }
@@ -490,6 +515,8 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
           for (int e = 0; e < WIDE; ++e) sum[q + e].add(counted(x.v[e]));
         }
       }
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) sum[e].settle();
     }
     float value[kHeld];
 #pragma unroll
