@@ -373,6 +373,39 @@ def test_capture_and_streams(tk):
     assert tk.evict(B["keys"][:0], B["values"][:0], B["score"][:0], B["lengths"][:0], 5)[0].shape == (0, 2, 5, 64)
 
 
+def test_a_backward_pass_that_saved_a_cache_raises(tk):
+    """replace_ counts as an in-place change of its four tensors and of what they are views of, and of nothing else."""
+    names = ("keys", "values", "score", "positions", "lengths", "key", "value")
+    s = cuda(step(2, 2, 1, 64, 32, 32, torch.float32, 12))
+    both = torch.cat([s["keys"], s["values"]], -1)
+    s["keys"], s["values"] = both[..., :32], both[..., 32:]
+
+    def call(recent=3):
+        return tk.replace_(*(s[k] for k in names), recent=recent, weights=s["weights"])
+
+    for k in ("keys", "values", "score", "positions"):
+        x = torch.ones(s[k].shape, device="cuda", requires_grad=True)
+        y = x.gather(-1, s[k].clamp_(0, 63)) if k == "positions" else x * s[k]     # (what the product, the gather saved)
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    x = torch.ones(s["key"].shape, device="cuda", requires_grad=True)
+    (x * s["key"] * s["value"]).sum().backward(inputs=[x])
+    before = {k: s[k]._version for k in names}
+    y = x * s["key"]
+    call()
+    y.sum().backward()
+    after = {k: s[k]._version for k in names}
+    assert [after[k] - before[k] for k in names] == [2, 2, 1, 1, 0, 0, 0]   # (keys and values share one buffer's count)
+    with pytest.raises(tk.TopkError):
+        call(recent=64)
+    assert {k: s[k]._version for k in names} == after
+    with torch.inference_mode():
+        s = {k: v.clone() for k, v in s.items()}
+        want = call()
+    assert call().shape == want.shape
+
+
 def test_refusals(tk):
     s = cuda(step(2, 2, 1, 50, 8, 8, torch.float32, 11))
 

@@ -328,6 +328,12 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// Tells autograd that t was written to, as torch's in-place operators do: a backward pass that saved it before raises an error
+// instead of reading the new values.  (Tensors of inference mode keep no count.)
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // keys, values, score, positions, lengths, key, value, recent, weights
 PyObject* replace(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return call<9>(n_args, [&] {
@@ -345,6 +351,8 @@ PyObject* replace(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                              c.weights_code, c.group, c.queries, c.code, c.batch, c.heads, c.capacity, c.key_dim, c.value_dim, recent,
                              static_cast<int64_t*>(slots.data_ptr()), stream_of(device));
     launch.done();
+    if (status == TOPK_OK)
+      for (int i = 0; i < 4; ++i) changed(tensor(a[i], ""));
     return give(status, {slots});
   });
 }
