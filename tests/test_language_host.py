@@ -1,12 +1,15 @@
 """Refusals of the operators of a language model at the C ABI (no kernel is launched here), and what their host code asks the
 CUDA runtime for, by the stand-in that the other operators' tests use."""
 import ctypes
+import os
 import random
+import subprocess
+import sys
 import threading
 
 import pytest
 
-from top_selection_prof_gb300 import _lib
+from top_selection_prof_gb300 import _lib, build, language
 
 from .test_operators_calls_host import at, events, fake_path, lib  # noqa: F401
 
@@ -268,3 +271,52 @@ def test_a_second_device_is_set_up_like_the_first(lib, call):  # noqa: F811
         launches.append([e[4] for e in log if e[0] == "launch"])
     assert launches[0] == launches[1] == launches[2] and launches[0]
     lib.fake_set_device(0)
+
+
+# ---- the build ----------------------------------------------------------------------
+@pytest.fixture
+def tools(tmp_path, monkeypatch):
+    """build() with compilers that only write their output, and fail for commands with a word of `fails`; the commands."""
+    fails, ran = [], []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        bad = any(word in part for word in fails for part in cmd)
+        if not bad:
+            with open(cmd[cmd.index("-o") + 1], "w") as f:
+                f.write("made")
+        return subprocess.CompletedProcess(cmd, int(bad), "", "no header" if bad else "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    for name, at in (("LIB", "libtopk_gb300.so"), ("CALLS", "_language_calls.so"), ("BUILD", "objects")):
+        monkeypatch.setattr(build, name, str(tmp_path / at))
+    return fails, ran
+
+
+def test_the_library_is_built_whatever_becomes_of_the_module(tools, monkeypatch, capsys):
+    fails, ran = tools
+    build.build()
+    assert os.path.exists(build.LIB) and os.path.exists(build.CALLS)
+    os.remove(build.LIB)
+    fails.append("language_calls.cpp")
+    with pytest.raises(RuntimeError, match="no header"):
+        build.build()
+    assert os.path.exists(build.LIB)
+    # without torch: no module (a stale one is linked to another library), and no error
+    os.remove(build.LIB)
+    monkeypatch.setitem(sys.modules, "torch", None)
+    del ran[:]
+    assert build.build() == build.LIB
+    assert os.path.exists(build.LIB) and not os.path.exists(build.CALLS) and not any("language_calls" in part for cmd in ran for part in cmd)
+    assert "torch cannot be imported" in capsys.readouterr().err
+
+
+def test_a_module_that_cannot_be_loaded_says_why(monkeypatch, tmp_path):
+    monkeypatch.setattr(_lib, "get", lambda: None)
+    monkeypatch.setattr(language, "_module", None)
+    monkeypatch.setitem(sys.modules, "top_selection_prof_gb300._language_calls", None)
+    monkeypatch.delattr("top_selection_prof_gb300._language_calls", raising=False)
+    for at, why in ((__file__, "another torch"), (str(tmp_path / "none.so"), "not built")):
+        monkeypatch.setattr(language, "CALLS_PATH", at)
+        with pytest.raises(RuntimeError, match=why):
+            language._calls()

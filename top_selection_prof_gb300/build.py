@@ -1,8 +1,9 @@
 """Builds libtopk_gb300.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library exporting the C ABI of include/topk.h; and the Python module that makes
-language.py's calls of it (_language_calls.so, with torch's headers).  Usage:
+library exporting the C ABI of include/topk.h; and, where torch is installed with
+its CUDA headers and libraries, the Python module that makes language.py's calls
+of it (_language_calls.so).  The library needs neither Python nor torch.  Usage:
     python -m top_selection_prof_gb300.build [--verbose]
 """
 from __future__ import annotations
@@ -52,6 +53,21 @@ def _run(cmd, what):
         raise RuntimeError("%s:\n%s\n%s" % (what, " ".join(cmd), res.stderr))
 
 
+def _calls_lack() -> str | None:
+    """What this machine lacks for the Python module, or None."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError as e:
+        return "torch cannot be imported (%s)" % e
+    at = os.path.dirname(torch.__file__)
+    for f in (os.path.join(sysconfig.get_paths()["include"], "Python.h"), os.path.join(at, "include", "c10", "cuda", "CUDAStream.h"),
+              os.path.join(at, "lib", "libc10_cuda.so"), os.path.join(at, "lib", "libtorch_cuda.so")):
+        if not os.path.exists(f):
+            return "there is no %s" % f
+    return None
+
+
 def _compile_calls() -> str:
     """The object of the Python module: host code with the headers of this machine's Python and torch."""
     import sysconfig
@@ -60,7 +76,7 @@ def _compile_calls() -> str:
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "language_calls.o")
-    _run([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-w", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+    _run([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
           "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
           "-isystem", cuda, "-c", os.path.join(CSRC, "language_calls.cpp"), "-o", obj], "g++ failed for language_calls.cpp")
     return obj
@@ -78,16 +94,18 @@ def _link_calls(obj: str) -> None:
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls)
+        lack = _calls_lack()
+        calls = None if lack else ex.submit(_compile_calls)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        calls = calls.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), "-shared", *ARCH, "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
-    os.replace(tmp, LIB)
-    _link_calls(calls)
+        tmp = LIB + ".tmp"
+        _run([nvcc(), "-shared", *ARCH, "-o", tmp, *objs], "link failed")
+        os.replace(tmp, LIB)
+        if calls:  # (the library is there, whatever becomes of the module)
+            _link_calls(calls.result())
+        else:
+            if os.path.exists(CALLS):
+                os.remove(CALLS)  # (it was linked to another library)
+            sys.stderr.write("the module of language.py's calls is not built: %s\n" % lack)
     return LIB
 
 

@@ -17,22 +17,26 @@ kernels, stream= as there, nothing recorded for autograd.  The calls are checked
 """
 from __future__ import annotations
 
+import os
+
 import torch
 
 from . import _lib
 
+CALLS_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_language_calls.so")
 _module = None
 
 
 def _calls():
-    """The compiled module; raises if it has not been built (there is no fallback)."""
+    """The compiled module; raises if it has not been built for this torch (there is no fallback)."""
     global _module
     if _module is None:
         _lib.get()
         try:
             from . import _language_calls
         except ImportError as e:
-            raise RuntimeError("_language_calls.so is not built; run `python -m top_selection_prof_gb300.build`") from e
+            why = "cannot be loaded (%s): was it built with another torch?  Run" % e if os.path.exists(CALLS_PATH) else "is not built; run"
+            raise RuntimeError("_language_calls.so %s `python -m top_selection_prof_gb300.build`" % why) from e
         _module = _language_calls
     return _module
 
