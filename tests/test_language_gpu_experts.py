@@ -177,6 +177,25 @@ def test_strided_rows(tk):
                 assert (a.double() - b.double()).abs().max() <= 256 * 2.0 ** -16 * b.double().abs().max()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [256, 255, 1001])
+def test_strided_rows_give_the_gradients_of_contiguous_ones(tk, dtype, d):
+    """Rows that start on 16-byte boundaries and off them.  Each row of dys is one product, bit for bit; dweights' sums of d products
+    may be formed in another order on the other path."""
+    g = gen(d)
+    place = torch.randperm(400, generator=g).view(100, 4)
+    ys, dy, w = (torch.randn(s, generator=g).to(dtype) for s in ((400, d), (100, d), (100, 4)))
+    want, _, dw, size = backward64(dy.double(), ys.double(), place, w.double())
+    for o, gap in ((0, 8), (8, 48), (1, 0), (3, 5), (0, 1)):
+        by, bdy = torch.full((400, o + d + gap), torch.nan, dtype=dtype, device="cuda"), torch.full((100, o + d + gap), torch.nan, dtype=dtype, device="cuda")
+        by[:, o:o + d], bdy[:, o:o + d] = ys.cuda(), dy.cuda()
+        got = tk.combine_backward(bdy[:, o:o + d], by[:, o:o + d], place.cuda(), w.cuda())
+        assert torch.equal(got[0].cpu(), want.to(dtype))
+        within(got[1], dw, size, d, dtype)
+        y = combine64(ys.double(), place, w.double())
+        within(tk.combine(by[:, o:o + d], place.cuda(), w.cuda()), y.sum(1), y.abs().sum(1), 4, dtype)
+
+
 def test_values_that_are_not_finite_stay_in_their_rows(tk):
     g = gen(5)
     place = torch.randperm(300, generator=g).view(100, 3)
