@@ -126,6 +126,22 @@ def test_sizes(tk, rows, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n", [(160, 131073), (5, 150_001), (160, 200_003), (200, 262_144)])
+def test_rows_that_take_two_blocks_or_more(tk, rows, n, dtype):
+    """More tokens than one block adds up, in a few rows and in more than run at once, with filters.  (Rows repeat eight, each with
+    its own number.)"""
+    few, _ = logits(8, n, dtype, rows)
+    x = few.repeat(rows // 8 + 1, 1)[:rows].contiguous()
+    u = ((torch.arange(rows) + 0.5) / rows).cuda()
+    for kw in (dict(top_p=0.95), dict(top_k=50, top_p=0.9, min_p=0.01), dict(temperature=2.0, min_p=0.02), dict(top_k=n // 2, temperature=4.0)):
+        tokens, logprobs = tk.sample(x, u, **kw)
+        some = slice(0, rows, max(1, rows // 10))
+        check(x[some], u[some], tokens[some], logprobs[some], **{**dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0), **kw})
+        again = tk.sample(few[:rows], u[:8], **kw)      # (more blocks a row: the same bits)
+        assert torch.equal(again[0], tokens[:8]) and torch.equal(again[1], logprobs[:8])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_flat_and_equal_rows(tk, dtype):
     """One bin holds more tokens than a block searches: equal values, nearly equal ones, two values, a long flat tail."""
     n = 100_000
