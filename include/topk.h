@@ -513,7 +513,9 @@ int topk_combine(const void* ys, int64_t ldys, int64_t rows, const int64_t* plac
  * none is), dweights[t k + j] = dy[t] . ys[place[t k + j]] (0 where the place
  * is out of range); each nullable.  ys is needed for dweights only.  Rows that
  * topk_dispatch placed are each listed once; a row that is listed more often
- * is summed all the same, more slowly.
+ * is summed in the order of its places.  From 129 places on a row that takes a
+ * scan over all places, for each such row and each 256 16-byte pieces of it
+ * (256 values where rows are not on 16-byte boundaries).
  */
 int topk_combine_backward(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t rows, const int64_t* place,
                           const void* weights, int dtype, int64_t tokens, int64_t k, int64_t d, void* dys, void* dweights,

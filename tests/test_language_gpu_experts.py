@@ -148,6 +148,57 @@ def test_combine_and_its_gradients(tk, tokens, k, rows, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [1, 40, 257, 2100])
+def test_rows_that_many_places_list(tk, d, dtype):
+    """From none to some hundred places a row, on both sides of what a warp ranks; the sums are in the order of the places, so a call
+    gives the same bits whenever it runs."""
+    g = gen(d)
+    times = [0, 1, 2, 3, 31, 32, 33, 0, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 1, 700, 2, 0, 1, 5]
+    k = 4
+    flat = torch.cat([torch.full((t,), r) for r, t in enumerate(times)] + [torch.tensor([-1, len(times), 1 << 40])])
+    flat = torch.cat([flat, torch.full((-flat.numel() % k,), -1)])
+    place = flat[torch.randperm(flat.numel(), generator=g)].view(-1, k)
+    tokens, rows = place.shape[0], len(times)
+    dy, ys, w = (torch.randn(s, generator=g).to(dtype) for s in ((tokens, d), (rows, d), (tokens, k)))
+    for weights in (w, None):
+        wc = None if weights is None else weights.cuda()
+        dys, size, dw, dwsize = backward64(dy.double(), ys.double(), place, None if weights is None else weights.double())
+        got = tk.combine_backward(dy.cuda(), ys.cuda(), place.cuda(), wc)
+        # a sum of m products: m roundings of its row
+        m = torch.tensor(times, dtype=torch.float64)[:, None]
+        assert bool(((got[0].double().cpu() - dys).abs() <= m * 2.0 ** -24 * size + half_step(dtype) * dys.abs() + 1e-38).all())
+        within(got[1], dw, dwsize, d, dtype)
+        for _ in range(5):
+            again = tk.combine_backward(dy.cuda(), ys.cuda(), place.cuda(), wc)
+            assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    dy, w = torch.randint(-2, 3, (tokens, d), generator=g).to(dtype), torch.randint(0, 2, (tokens, k), generator=g).to(dtype)
+    want = backward64(dy.double(), ys.double(), place, w.double())[0].to(dtype)
+    assert torch.equal(tk.combine_backward(dy.cuda(), ys.cuda(), place.cuda(), w.cuda())[0].cpu(), want)
+
+
+def test_the_time_of_rows_listed_twice_grows_with_the_places(tk):
+    """Eight times the places take about eight times as long, not sixty-four: a quarter of that is the border."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    took = []
+    for tokens in (4096, 32768):
+        place = torch.randperm(tokens * 8, device="cuda", generator=g).remainder_(tokens * 4).view(tokens, 8)
+        dy, ys = torch.randn(tokens, 64, device="cuda", generator=g), torch.randn(tokens * 4, 64, device="cuda", generator=g)
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            tk.combine_backward(dy, ys, place, need=(True, False))
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        took.append(min(times))
+        dys = tk.combine_backward(dy, ys, place, need=(True, False))[0]
+        order = place.view(-1).sort(stable=True).indices.view(-1, 2) // 8
+        assert torch.equal(dys, dy[order[:, 0]] + dy[order[:, 1]])
+    assert took[1] <= 16 * took[0], took
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_whole_numbers_are_exact(tk, dtype):
     g = gen(3)
     tokens, k, rows, d = 600, 8, 900, 200

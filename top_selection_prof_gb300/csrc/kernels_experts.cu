@@ -307,12 +307,14 @@ struct JoinRows {
   void* y;
   const void* dy;       // gradients: of y
   int64_t lddy;
-  unsigned* listed;     // how often each row is listed
+  unsigned* listed;     // how often each row is listed,
+  int *first, *last, *next;  // one of its places, and a chain of the others, in no order: one of them, and from each the next
   void* dys;            // nullable
   void* dweights;       // nullable
 };
 constexpr int kRowsTogether = 4;  // rows of a token that are read together
 constexpr int kRowsBlock = 32; // rows that a block of rows looks after
+constexpr int kChain = 128;    // places of a row that a warp ranks (256, of 8 KB a block: 68 us instead of 65 for 4093 x 6 rows of 2001 bf16)
 
 // What a token's places hold: their rows (-1: none) and weights, kTogether of them from the j0-th on.
 template <typename T, int kTogether>
@@ -380,13 +382,66 @@ __global__ void __launch_bounds__(kThreads) clear_listed_kernel(unsigned* listed
   const int64_t r = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (r < rows) listed[r] = 0;
 }
-__global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* place, int64_t total, unsigned* listed, int64_t rows) {
+__global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* place, int64_t total, unsigned* listed, int* first, int* last, int* next,
+                                                                int64_t rows) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t s = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (s >= total) return;
   const int64_t r = place[s];
-  if (r >= 0 && r < rows) atomicAdd(&listed[r], 1u);
+  if (r < 0 || r >= rows) return;
+  // (a chain's end is what `last` held before: it is walked by its length)
+  if (atomicAdd(&listed[r], 1u) == 0) first[r] = static_cast<int>(s);
+  else next[s] = atomicExch(&last[r], static_cast<int>(s));
+}
+
+// A warp: the sum of row r, which `times` (2 or more) places list, in their order.  The chain's order is the atomics', so the places
+// are ranked first.  (By value: with the kernel's parameters handed down by their address all of it read them from memory.)
+template <typename T, int VEC>
+__device__ __noinline__ void sum_chain(const int* next, int first, int last, int times, int k, const T* dy, int64_t lddy, const T* weights,
+                                       int d, T* dst, int* places) {
+  using P = Piece<T, VEC, 4>;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) {
+    places[0] = first;
+    int s = last;
+    for (int i = 1;; s = next[s]) {
+      places[i] = s;
+      if (++i == times) break;
+    }
+  }
+  __syncwarp();
+  int held[kChain / 32], rank[kChain / 32];
+#pragma unroll
+  for (int e = 0; e < kChain / 32; ++e) {
+    held[e] = e * 32 + lane < times ? places[e * 32 + lane] : 0;
+    rank[e] = 0;
+  }
+  for (int i = 0; i < times; ++i) {
+    const int other = places[i];
+#pragma unroll
+    for (int e = 0; e < kChain / 32; ++e) rank[e] += other < held[e];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < kChain / 32; ++e)
+    if (e * 32 + lane < times) places[rank[e]] = held[e];
+  __syncwarp();
+  for (int c = P::first(lane); c < d; c += P::step(32)) {
+    float sum[P::kWide] = {};
+    for (int i = 0; i < times; ++i) {
+      const int s = places[i];
+      const float f = weights ? to_f32(weights[s]) : 1.0f;
+      P raw;
+      raw.load(dy + int64_t(s / k) * lddy, c, d);
+      float g[P::kWide];
+      raw.values(g);
+#pragma unroll
+      for (int e = 0; e < P::kWide; ++e) sum[e] = fmaf(f, g[e], sum[e]);
+    }
+    P::store(sum, dst, c, d);
+  }
+  __syncwarp();
 }
 
 // Four rows of a token together: with eight, 128 registers left 16 warps an SM (with one piece a thread 136 us instead of 120 for
@@ -394,13 +449,17 @@ __global__ void __launch_bounds__(kThreads) count_listed_kernel(const int64_t* p
 //
 // Blocks of tokens, `share` threads each (32 or more): what a place's row gets where no other place lists it, and the products
 // that are the weights' gradients.  Behind them blocks of rows: zeros for rows that no place lists, and the sums, in order
-// of place, for rows that more than one does (found anew among all places: permutations have none).
+// of place, for rows that more than one does (permutations have none): by a warp from the row's chain, or, where more than kChain
+// do, by the block from a scan over all places, which only that few rows can take.  (With the scan for
+// all, 32768 rows of 512 f32 that 65536 places list twice took 7.2 ms, and four times that for each doubling: minutes for
+// 2^24 places.)
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRows p, int share, int64_t token_blocks) {
   constexpr int kTogether = kRowsTogether;
   __shared__ float dots[kThreads / 32][kTogether];
   __shared__ unsigned listed[kRowsBlock];
   __shared__ unsigned hit_mask[kThreads / 32];
+  __shared__ int places[kThreads / 32][kChain];
   grid_dependency_wait();
   grid_launch_dependents();
   const T* ys = static_cast<const T*>(p.ys);
@@ -472,17 +531,26 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
     return;
   }
   const int64_t r0 = (int64_t(blockIdx.x) - token_blocks) * kRowsBlock;
-  if (threadIdx.x < kRowsBlock) listed[threadIdx.x] = r0 + threadIdx.x < p.rows ? p.listed[r0 + threadIdx.x] : 1;
-  __syncthreads();
+  unsigned mine = 1;
+  if (threadIdx.x < kRowsBlock) listed[threadIdx.x] = mine = r0 + threadIdx.x < p.rows ? p.listed[r0 + threadIdx.x] : 1;
+  const bool shared = __syncthreads_or(mine > 1);
   P zero;
   zero.clear();
   for (int q = warp; q < kRowsBlock; q += kThreads / 32)
     if (listed[q] == 0)
       for (int c = P::first(lane); c < d; c += P::step(32)) zero.store(dys + (r0 + q) * p.d, c, d);
+  if (!shared) return;  // (asked of the block at once: with the question by row, and a call behind it, 46 us instead of 31 for 16384 x 8 rows of 64)
+#pragma unroll 1
+  for (int q = warp; q < kRowsBlock; q += kThreads / 32) {
+    if (listed[q] > 1 && listed[q] <= kChain) {
+      const int64_t r = r0 + q;
+      sum_chain<T, VEC>(p.next, p.first[r], p.last[r], static_cast<int>(listed[q]), p.k, dy, p.lddy, weights, d, dys + r * p.d, places[warp]);
+    }
+  }
   const int64_t total = p.tokens * p.k;
   for (int q = 0; q < kRowsBlock; ++q) {
     const unsigned times = listed[q];
-    if (times < 2) continue;
+    if (times <= kChain) continue;
     const int64_t r = r0 + q;
     for (int64_t c0 = 0; c0 < p.d; c0 += kThreads * VEC) {
       const int64_t c = c0 + threadIdx.x * VEC;
@@ -581,7 +649,7 @@ cudaError_t move(const Dispatch& p, Scratch& sc, cudaStream_t st) {
 }
 
 JoinRows join_of(const Combine& p) {
-  return JoinRows{p.ys, p.ldys, p.rows, p.tokens, p.d, static_cast<int>(p.k), p.place, p.weights, p.y, p.dy, p.lddy, nullptr, p.dys, p.dweights};
+  return JoinRows{p.ys, p.ldys, p.rows, p.tokens, p.d, static_cast<int>(p.k), p.place, p.weights, p.y, p.dy, p.lddy, nullptr, nullptr, nullptr, nullptr, p.dys, p.dweights};
 }
 
 template <typename T, int VEC>
@@ -599,10 +667,13 @@ cudaError_t backward(const Combine& p, Scratch& sc, cudaStream_t st) {
   if (p.rows == 0) q.dys = nullptr;
   if (q.dys) {
     q.listed = sc.take<unsigned>(p.rows);
+    q.first = sc.take<int>(p.rows);
+    q.last = sc.take<int>(p.rows);
+    q.next = sc.take<int>(total);
     row_blocks = (p.rows + kRowsBlock - 1) / kRowsBlock;
     cudaError_t e = launch_after(clear_listed_kernel, static_cast<unsigned>((p.rows + kThreads - 1) / kThreads), kThreads, 0, st, q.listed, p.rows);
     const unsigned blocks = static_cast<unsigned>((total + kThreads - 1) / kThreads);
-    if (e == cudaSuccess && blocks) e = launch_after(count_listed_kernel, blocks, kThreads, 0, st, p.place, total, q.listed, p.rows);
+    if (e == cudaSuccess && blocks) e = launch_after(count_listed_kernel, blocks, kThreads, 0, st, p.place, total, q.listed, q.first, q.last, q.next, p.rows);
     if (e != cudaSuccess) return e;
   }
   if (token_blocks + row_blocks > INT32_MAX) return cudaErrorNotSupported;
@@ -644,7 +715,12 @@ cudaError_t launch_combine(const Combine& p, cudaStream_t st) {
 
 size_t combine_backward_scratch_bytes(const Combine& p) {
   Scratch sc;
-  if (p.dys) sc.take<unsigned>(p.rows);
+  if (p.dys) {
+    sc.take<unsigned>(p.rows);
+    sc.take<int>(p.rows);
+    sc.take<int>(p.rows);
+    sc.take<int>(p.tokens * p.k);
+  }
   return sc.used();
 }
 
