@@ -96,7 +96,7 @@ struct Sum2Pair {
     lo = plus(lo, plus(minus(hi, minus(s, b)), minus(v, b)));
     hi = s;
   }
-  // (an infinity becomes NaN, and its sum is made anew)
+  // (an infinity may become NaN, and its sum is made anew)
   __device__ __forceinline__ void settle() {
     const Pair s = plus(hi, lo);
     lo = minus(lo, minus(s, hi));
@@ -168,8 +168,10 @@ __global__ void __launch_bounds__(kSumThreads, 4) weight_sums_kernel(const Weigh
 #pragma unroll
       for (int e = 0; e < kWide / 2; ++e) sum[e].add(v[a].pair(e));
     }
+    if (i0 + kGroups * kAhead < n) {  // (the last ones' are joined, and settled, by the block)
 #pragma unroll
-    for (int e = 0; e < kWide / 2; ++e) sum[e].settle();
+      for (int e = 0; e < kWide / 2; ++e) sum[e].settle();
+    }
   }
 #pragma unroll
   for (int e = 0; e < kWide / 2; ++e) {
@@ -515,8 +517,10 @@ __global__ void __launch_bounds__(kReplaceThreads, 4) replace_kernel(const Repla
           for (int e = 0; e < WIDE; ++e) sum[q + e].add(counted(x.v[e]));
         }
       }
+      if (r0 + kAhead < n) {
 #pragma unroll
-      for (int e = 0; e < kHeld; ++e) sum[e].settle();
+        for (int e = 0; e < kHeld; ++e) sum[e].settle();
+      }
     }
     float value[kHeld];
 #pragma unroll
