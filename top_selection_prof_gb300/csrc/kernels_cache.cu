@@ -18,11 +18,12 @@
 // least score and writes the new row over it.
 //
 // One GB300, inputs changing between calls: 8 heads x 32768 positions x 128 queries bf16,
-// 4096 kept of 128 + 128 values (102 MB): 36.5 us, of which the sums take 17 (67 MB), the
+// 4096 kept of 128 + 128 values (102 MB): 36 us, of which the sums take 17 (67 MB), the
 // choice 11 (eight barriers of a cluster and the scans between them), the rows 6 (34 MB); 48 heads x 5001 f32, up to 1021
-// rows of 72 + 72 kept: 26.5 us, of which the rows 9 (56 MB).  Replacing one of 4096 slots in 512 heads, four bf16 weights a
-// slot (51 MB): 16 us; in 8 heads of 2048: 4.5 us, launch and barriers.  (Blocks of
-// 256 threads, four an SM, so that 512 heads run at once: with 512, two an SM, 19 us instead of 16.)
+// rows of 72 + 72 kept: 27 us, of which the rows 9 (56 MB).  Replacing one of 4096 slots in 512 heads, four bf16 weights a
+// slot (51 MB): 16.7 us, and 13.3 where three inputs in turn are still in the L2 in part; in 8 heads of 2048: 4.8 us
+// in a graph, launch and barriers.  (Blocks of 256 threads, four an SM, so that 512 heads run at once: with 512, two an SM,
+// 19 us instead of 16.5.)
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>

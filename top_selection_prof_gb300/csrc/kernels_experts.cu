@@ -4,15 +4,16 @@
 // t k + j goes behind all places of smaller experts and the earlier ones of its
 // own.  Places without an expert stand behind all, so that every row of the
 // result has one place, and those rows are zeros.  All of it is bound by the
-// rows moved: tokens are walked in order, each row of x (or of y, dy) is read or
-// written once, and the rows by expert once.
+// rows moved: tokens are walked in order, each row of x is read and each of y
+// written once (dy once for each four of a token's places), and the rows by expert once.
 //
 // One GB300, inputs changing between calls: dispatch of 8192 x 8 rows of 2048
-// bf16 (302 MB) 51.5 us, 5.9 TB/s: the rows 44 us, counts and ranks before them
-// the rest; combine of them 49 us, 6.2 TB/s; their gradients (604 MB less the
-// rows read twice) 104 us; the gradients of 4093 x 6 rows of 1001 f32, none on a
-// 16-byte boundary, 47 us (a 213 MB case whose scalar loads and stores bound it).
-// 16 x 4 rows of 4096 bf16 are dispatched in 4.2 us by one launch.
+// bf16 (302 MB) 52.6 us, 5.7 TB/s: the rows 44 us, counts and ranks before them
+// the rest (68 us with 384 experts, 69.5 with 512, whose ranks go a warp after another);
+// combine of them 48.7 us, 6.2 TB/s; their gradients (571 MB, dy once more than that) 100.6 us; the
+// gradients of 4093 x 6 rows of 1001 f32, none on a
+// 16-byte boundary, 46.5 us (a 213 MB case whose scalar loads and stores bound it).
+// 16 x 4 rows of 4096 bf16 are dispatched in 2.4 us of a graph by one launch.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -335,7 +336,7 @@ struct Listed {
 };
 
 // (Blocks that take several tokens in turn, the next one's places loaded ahead, have 97 registers instead of 72: 58 us instead
-// of 54 for 8192 x 8 rows of 2048 bf16.)
+// of 54, before a thread took two pieces, for 8192 x 8 rows of 2048 bf16.)
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const JoinRows p, int share) {
   using P = Piece<T, VEC>;
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const JoinRo
   const T* weights = static_cast<const T*>(p.weights);
   T* dys = static_cast<T*>(p.dys);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  using P = Piece<T, VEC, 4>;  // (eight bf16 values: 84 us instead of 74 for 4093 x 6 rows of 2001)
+  using P = Piece<T, VEC, 4>;  // (eight bf16 values: 84 us instead of 74, before a thread took four pieces, for 4093 x 6 rows of 2001)
   const int d = static_cast<int>(p.d);
   if (blockIdx.x < token_blocks) {
     // (in turn, a token's places loaded while the one before is worked on)
@@ -656,7 +657,8 @@ template <typename T, int VEC>
 cudaError_t backward(const Combine& p, Scratch& sc, cudaStream_t st) {
   JoinRows q = join_of(p);
   // (four pieces a thread: what a token costs beside them, its places and the sums over its threads, counts less.  With one piece
-  // 120 us instead of 104 for 8192 x 8 rows of 2048 bf16 and 75 instead of 68 for 4093 x 6 of 2001; with eight 111 and 72.)
+  // 120 us instead of 104 for 8192 x 8 rows of 2048 bf16 and 75 instead of 68 for 4093 x 6 of 2001; with eight 111 and 72.  With the
+  // rows' blocks as they are now 100.6 and 65.)
   const int share = share_of(p.d, 4 * (VEC > 1 ? VEC : 4));
   int64_t token_blocks = blocks_of(p.tokens, share);
   const int64_t total = p.tokens * p.k;

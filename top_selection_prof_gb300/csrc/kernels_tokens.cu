@@ -24,11 +24,16 @@
 // digits first, and a head that it cannot hold (a row of equal values) is searched
 // like a tail.
 //
-// One GB300, inputs changing between calls: 256 x 131072 f32 with a top_k of 200
-// 38 us (134 MB: the pass over the rows takes 23 of them, 5.8 TB/s, what a plain read of them takes too; what is before
-// and after it is latency: the sample 4, the searches 10); 96 x 131072 bf16, nucleus of 0.9, 50 us (the pass
-// 14, of which the values' weights 6, the search of the nucleus's end 13, of the token 4); 37 x 100003 f32
-// without filters 33 us; 1 x 65536 12 us.
+// One GB300, inputs changing between calls; the parts by the clock of each row's first block, median row:
+//   256 x 131072 f32, top_k 200, top_p, min_p  38 us (134 MB; a plain read of them takes 23): sample 6, pass 17, the blocks'
+//     lists joined 1, the head's sums 2, three searches 3.5: 30, in the slowest row 35
+//   96 x 131072 bf16, nucleus of 0.9  50 us: sample 4, read and counts by value 7, the values' weights 5.5, the head's
+//     vectors 2, lists and bins joined 5, the head's sums 2.5, the nucleus's end 13.5, the token 1.5: 42, in the slowest row
+//     51 (pass 4 more, the nucleus's end 20, the token 4)
+//   37 x 100003 f32, no filter  33.5 us: sample 2.5, pass with weights 9.5, joined 5, the head's sums 2, the token 10: 30, slowest 35
+//   1 x 65536 f32  12 us: sample 3, pass 2, joined 2, the head's sums 1.5, three searches 3
+// A second pass over the row takes 6 of a search's 10 us in the tail.  Above kPartMost tokens each row takes two blocks or more: 96
+// x 262144 bf16 with top_p 75 us in a graph, f32 121, 4 x 262144 bf16 39.
 // What is once over a row is bound by instructions that are run once and fetched for it: short loops took
 // less than unrolled ones all through the searches (62 -> 50 us for the nucleus).
 // 256 threads of 128 registers, two blocks an SM: with 512 of 64 the searches' state went through
