@@ -470,7 +470,8 @@ int topk_clip_grad_norm(const void* const* grads, void* const* out, const int64_
  * 2^45 (what is less than 1 is dropped, from each of the up to some thousand
  * largest tokens and from the others' sum), so the token is that of 64-bit
  * arithmetic unless u[r] (or a filter's border) is within about 2^-29 of the edge
- * between two; weights below 2^-48 of the largest count as 0.
+ * between two; weights below 2^-48 of the largest count as 0.  logprobs are off by
+ * at most 2^-22 of themselves and 2^-28.
  *   Each of temperature, top_k, top_p and min_p is a number, or one a row
  * (device, `rows` values) where its pointer is not null, the number then
  * being ignored; numbers are rounded to f32.  A row's temperature that is not

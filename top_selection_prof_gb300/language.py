@@ -113,7 +113,7 @@ def replace_(keys, values, score, positions, lengths, key, value, recent: int = 
 
     lengths (batch,): tokens before it.  While there are fewer than slots it takes the next one; then the one whose
     score is least, of those whose position is below lengths - recent (equal ones: the lowest slot; none: slot -1, and
-    nothing is stored).  key, value (batch, heads, dim); positions (batch, heads, capacity), int64: the position in each slot; weights as in evict, by slot,
-    added to the scores first.  The slot's score becomes 0.  lengths is not changed.  As after torch's in-place operators, a
-    backward pass that saved one of the four tensors before raises an error."""
+    nothing is stored).  key, value (batch, heads, dim); positions (batch, heads, capacity), int64: the position in each
+    slot; weights as in evict, by slot, added to the scores first.  The slot's score becomes 0.  lengths is not changed.
+    As after torch's in-place operators, a backward pass that saved one of the four tensors before raises an error."""
     return _call("replace", stream, keys, values, score, positions, lengths, key, value, recent, weights)
